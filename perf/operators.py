@@ -288,7 +288,8 @@ def _padding(past, new):
 def _plain_codes(fmt, x):
     x = x.float()
     if fmt == "int8":
-        a = x.abs().amax(-1, keepdim=True) / 127
+        a = x.abs().amax(-1, keepdim=True)
+        a = a / torch.full_like(a, 127)  # a division (by a plain number torch multiplies by its reciprocal)
         q = torch.where(a > 0, torch.clamp(torch.round(x / a), -127, 127), torch.zeros_like(x))
         return q.to(torch.int8), a
     b = x.unflatten(-1, (-1, 32))
@@ -398,7 +399,8 @@ def _exact_values(fmt, x):
         return x.to(torch.float16).double()
     x = x.to(torch.float32)
     if fmt == "int8":
-        a = torch.max(x, -1, keepdim=True).values.maximum(-torch.min(x, -1, keepdim=True).values) / 127
+        a = torch.max(x, -1, keepdim=True).values.maximum(-torch.min(x, -1, keepdim=True).values)
+        a = a / torch.tensor([127.0], device=x.device)
         q = torch.where(a == 0, 0.0, (x / a)).round().clamp(-127, 127)
         return q.double() * a.double()
     got = torch.empty(x.shape, dtype=torch.float64, device=x.device)
