@@ -20,7 +20,20 @@ FORMATS = {"q4_0": Q4_0, "cbk4": CBK4, "cbk8": CBK8, "pq2_0": PQ2_0, "aqlm_2x8":
            "aqlm_1x16": AQLM_1X16, "cbk4_row": CBK4_ROW, "cbk8_row": CBK8_ROW}
 QGEMV_OK, QGEMV_ERR_ARG, QGEMV_ERR_ALIGN, QGEMV_ERR_CUDA, QGEMV_ERR_TIMEOUT, QGEMV_ERR_NOMEM = range(6)
 
+KV_F16, KV_INT8, KV_Q4_0 = 1, 2, 3
+KV_FORMATS = {"f16": KV_F16, "int8": KV_INT8, "q4_0": KV_Q4_0}
+DT_F32, DT_F16, DT_BF16 = 0, 1, 2
+
+
+class KvCacheDesc(ctypes.Structure):
+    """``qgemv_kv_cache`` of include/qgemv.h."""
+    _fields_ = [("pages", ctypes.c_void_p), ("format", ctypes.c_int), ("head_dim", ctypes.c_int),
+                ("kv_heads", ctypes.c_int), ("page_tokens", ctypes.c_int), ("n_pages", ctypes.c_int64)]
+
+
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "_build", "libqgemv.so")
+
+_P, _I, _L, _F = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_float
 
 # Every exported symbol of include/qgemv.h with its ctypes signature.
 _SIGNATURES = {
@@ -55,6 +68,15 @@ _SIGNATURES = {
     "qgemv_stream_k_plan": (ctypes.c_int, [ctypes.c_int64, ctypes.c_int, ctypes.c_int64, ctypes.c_int,
                                            ctypes.c_int, ctypes.POINTER(ctypes.c_int64)]),
     "qgemv_destroy": (None, [ctypes.c_void_p]),
+    "qgemv_kv_bytes": (_L, [_I, _L, _I, _I, _I]),
+    "qgemv_kv_write": (_I, [_P, _I, _P, _L, _L, _P, _L, _L, _P, _L, _P]),
+    "qgemv_kv_read": (_I, [_P, _P, _L, _L, _P, _P, _L, _I, _P, _L, _L, _P, _L, _L, _P]),
+    "qgemv_attn_ws_bytes": (_L, [_L, _I, _I]),
+    "qgemv_attn_ws_init": (_I, [_P, _L, _P]),
+    "qgemv_attn_status": (_I, [_P]),
+    "qgemv_attn_tree": (_I, [_P, _P, _L, _L, _P, _P, _L, _L, _I, _P, _L, _P, _L, _L, _F, _P, _L, _L, _P, _P, _L, _P]),
+    "qgemv_attn_prompt": (_I, [_I, _I, _I, _I, _P, _L, _L, _P, _L, _L, _P, _L, _L, _L, _P, _P, _L, _L, _L, _F,
+                               _P, _L, _L, _P, _P, _L, _P]),
     "qgemv_last_error": (ctypes.c_char_p, []),
     "qgemv_last_error_code": (ctypes.c_int, []),
 }
@@ -87,6 +109,10 @@ def load(path: str | None = None) -> ctypes.CDLL:
 
 def _fmt(fmt) -> int:
     return FORMATS[fmt] if isinstance(fmt, str) else int(fmt)
+
+
+def _kv_fmt(fmt) -> int:
+    return KV_FORMATS[fmt] if isinstance(fmt, str) else int(fmt)
 
 
 def _check(rc: int):
@@ -214,6 +240,56 @@ def qgemv_last_error() -> str:
 
 def qgemv_last_error_code() -> int:
     return int(load().qgemv_last_error_code())
+
+
+def qgemv_kv_bytes(fmt, n_pages: int, page_tokens: int, kv_heads: int, head_dim: int) -> int:
+    return int(load().qgemv_kv_bytes(_kv_fmt(fmt), n_pages, page_tokens, kv_heads, head_dim))
+
+
+def qgemv_kv_write(cache: KvCacheDesc, dtype: int, k: int, k_token_stride: int, k_head_stride: int, v: int,
+                   v_token_stride: int, v_head_stride: int, slots: int, n_tokens: int, stream=None) -> int:
+    return _check(load().qgemv_kv_write(ctypes.byref(cache), dtype, k, k_token_stride, k_head_stride, v, v_token_stride,
+                                        v_head_stride, slots, n_tokens, _stream_ptr(stream)))
+
+
+def qgemv_kv_read(cache: KvCacheDesc, table: int, table_stride: int, n_seqs: int, starts: int | None, cu: int,
+                  n_tokens: int, dtype: int, k: int, k_token_stride: int, k_head_stride: int, v: int,
+                  v_token_stride: int, v_head_stride: int, stream=None) -> int:
+    return _check(load().qgemv_kv_read(ctypes.byref(cache), table, table_stride, n_seqs, starts, cu, n_tokens, dtype,
+                                       k, k_token_stride, k_head_stride, v, v_token_stride, v_head_stride,
+                                       _stream_ptr(stream)))
+
+
+def qgemv_attn_ws_bytes(n_seqs: int, q_heads: int, head_dim: int) -> int:
+    return int(load().qgemv_attn_ws_bytes(n_seqs, q_heads, head_dim))
+
+
+def qgemv_attn_ws_init(ws: int, ws_bytes: int, stream=None) -> int:
+    return _check(load().qgemv_attn_ws_init(ws, ws_bytes, _stream_ptr(stream)))
+
+
+def qgemv_attn_status(ws: int) -> int:
+    return _check(load().qgemv_attn_status(ws))
+
+
+def qgemv_attn_tree(cache: KvCacheDesc, table: int, table_stride: int, n_seqs: int, ctx_lens: int, q: int,
+                    q_token_stride: int, q_head_stride: int, q_heads: int, cu_q: int, n_q: int, masks: int | None,
+                    max_ctx: int, max_new: int, scale: float, out: int, out_token_stride: int, out_head_stride: int,
+                    lse: int | None, ws: int, ws_bytes: int, stream=None) -> int:
+    return _check(load().qgemv_attn_tree(ctypes.byref(cache), table, table_stride, n_seqs, ctx_lens, q, q_token_stride,
+                                         q_head_stride, q_heads, cu_q, n_q, masks, max_ctx, max_new, scale, out,
+                                         out_token_stride, out_head_stride, lse, ws, ws_bytes, _stream_ptr(stream)))
+
+
+def qgemv_attn_prompt(dtype: int, head_dim: int, q_heads: int, kv_heads: int, q: int, q_token_stride: int,
+                      q_head_stride: int, k: int, k_token_stride: int, k_head_stride: int, v: int,
+                      v_token_stride: int, v_head_stride: int, n_seqs: int, cu_q: int, cu_k: int, n_q: int, n_k: int,
+                      max_q: int, scale: float, out: int, out_token_stride: int, out_head_stride: int,
+                      lse: int | None, ws: int, ws_bytes: int, stream=None) -> int:
+    return _check(load().qgemv_attn_prompt(dtype, head_dim, q_heads, kv_heads, q, q_token_stride, q_head_stride, k,
+                                           k_token_stride, k_head_stride, v, v_token_stride, v_head_stride, n_seqs,
+                                           cu_q, cu_k, n_q, n_k, max_q, scale, out, out_token_stride, out_head_stride,
+                                           lse, ws, ws_bytes, _stream_ptr(stream)))
 
 
 # ----------------------------------------------------------- torch helper --
@@ -368,3 +444,160 @@ def prepare_x_int8(x, hadamard_block: int = 0, signs=None, stream=None):
                          hadamard_block, xq.data_ptr(), _current(stream))
     return xq
 
+
+# --------------------------------------------------- cache and attention --
+
+def _dtype_code(dtype) -> int:
+    import torch
+    code = {torch.float32: DT_F32, torch.float16: DT_F16, torch.bfloat16: DT_BF16}.get(dtype)
+    if code is None:
+        raise ValueError(f"rows are fp32, fp16 or bf16, not {dtype}")
+    return code
+
+
+def _rows(name, t, heads: int, head_dim: int):
+    """(address, token stride, head stride) of a CUDA tensor [n, heads, head_dim], its values contiguous."""
+    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != head_dim or t.stride(2) != 1 or not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor [n, {heads}, {head_dim}] with contiguous values, got "
+                         f"{tuple(t.shape)} with strides {t.stride()} on {t.device}")
+    # the stride of a dimension of one element means nothing to torch
+    return (t.data_ptr(), t.stride(0) if t.shape[0] > 1 else heads * head_dim,
+            t.stride(1) if heads > 1 else head_dim)
+
+
+def _index(name, t, dtype, shape):
+    if t.dtype != dtype or tuple(t.shape) != shape or not t.is_contiguous() or not t.is_cuda:
+        raise ValueError(f"{name} must be a contiguous CUDA {dtype} tensor of shape {shape}, got {t.dtype} "
+                         f"{tuple(t.shape)} on {t.device}")
+    return t.data_ptr()
+
+
+class AttnWorkspace:
+    """Workspace of ``KVCache.attend`` and ``attn_prompt`` for up to
+    ``n_seqs`` sequences, reused by any number of calls, one at a time (calls
+    that overlap on several streams need one each)."""
+
+    def __init__(self, n_seqs: int, q_heads: int, head_dim: int, device="cuda"):
+        import torch
+        self.nbytes = qgemv_attn_ws_bytes(n_seqs, q_heads, head_dim)
+        if self.nbytes == 0:
+            raise QgemvError(QGEMV_ERR_ARG, f"no workspace for {n_seqs} sequences of {q_heads} heads of {head_dim}")
+        self.buffer = torch.empty(self.nbytes, dtype=torch.uint8, device=device)
+        self.ptr = self.buffer.data_ptr()
+        self.reset()
+
+    def reset(self, stream=None):
+        """Set the workspace up again (needed only after ``status`` raised)."""
+        qgemv_attn_ws_init(self.ptr, self.nbytes, _current(stream))
+
+    def status(self):
+        """Synchronise; raises if a kernel of this workspace gave up a wait."""
+        return qgemv_attn_status(self.ptr)
+
+
+class KVCache:
+    """A paged key/value cache of one layer on the GPU.
+
+    ``KVCache(fmt, n_pages, page_tokens, kv_heads, head_dim)`` with fmt "f16",
+    "int8" or "q4_0" allocates (uninitialised) pages; ``write`` quantises new
+    rows into slots, ``read`` gives rows back, ``attend`` is the attention of
+    one or several drafted tokens of each sequence over the cached ones.
+    Runs are ordered on ``stream`` when one is given, else on torch's current
+    stream."""
+
+    def __init__(self, fmt, n_pages: int, page_tokens: int, kv_heads: int, head_dim: int, device="cuda"):
+        import torch
+        self.fmt = _kv_fmt(fmt)
+        self.kv_heads, self.head_dim, self.page_tokens, self.n_pages = kv_heads, head_dim, page_tokens, n_pages
+        nbytes = qgemv_kv_bytes(self.fmt, n_pages, page_tokens, kv_heads, head_dim)
+        if nbytes == 0:
+            raise QgemvError(QGEMV_ERR_ARG, f"invalid cache: {fmt}, {n_pages} pages of {page_tokens} tokens, "
+                                            f"{kv_heads} heads of {head_dim}")
+        self.pages = torch.empty(nbytes, dtype=torch.uint8, device=device)
+        self.desc = KvCacheDesc(self.pages.data_ptr(), self.fmt, head_dim, kv_heads, page_tokens, n_pages)
+
+    def write(self, k, v, slots, stream=None):
+        """Quantise the rows k and v [n, kv_heads, head_dim] (fp32, fp16 or
+        bf16, any token and head strides) into slots (int64 [n]; a slot is
+        page * page_tokens + place, negative ones are skipped)."""
+        import torch
+        if k.dtype != v.dtype or k.shape[0] != v.shape[0]:
+            raise ValueError("k and v must have the same type and number of tokens")
+        n = k.shape[0]
+        s = _index("slots", slots, torch.int64, (n,))
+        qgemv_kv_write(self.desc, _dtype_code(k.dtype), *_rows("k", k, self.kv_heads, self.head_dim),
+                       *_rows("v", v, self.kv_heads, self.head_dim), s, n, _current(stream))
+
+    def read(self, table, starts, cu, n_tokens: int, dtype=None, out=None, stream=None):
+        """The cached rows of positions starts[b] .. of each sequence, packed
+        by cu (int32 [n_seqs + 1]): (k, v) [n_tokens, kv_heads, head_dim] of
+        dtype (fp16 unless given).  table: int32 [n_seqs, most pages]."""
+        import torch
+        if out is None:
+            shape = (n_tokens, self.kv_heads, self.head_dim)
+            out = tuple(torch.empty(shape, dtype=dtype or torch.float16, device=self.pages.device) for _ in range(2))
+        k, v = out
+        if k.dtype != v.dtype or k.shape[0] != n_tokens or v.shape[0] != n_tokens:
+            raise ValueError(f"the outputs must have {n_tokens} tokens of one type")
+        n_seqs, stride = table.shape
+        qgemv_kv_read(self.desc, _index("table", table, torch.int32, (n_seqs, stride)), stride, n_seqs,
+                      None if starts is None else _index("starts", starts, torch.int32, (n_seqs,)),
+                      _index("cu", cu, torch.int32, (n_seqs + 1,)), n_tokens, _dtype_code(k.dtype),
+                      *_rows("k", k, self.kv_heads, self.head_dim), *_rows("v", v, self.kv_heads, self.head_dim),
+                      _current(stream))
+        return out
+
+    def attend(self, q, table, ctx_lens, cu_q, masks=None, *, max_ctx: int, max_new: int, workspace, scale=None,
+               out=None, lse=None, stream=None):
+        """Attention of the drafted tokens q [n, q_heads, head_dim] (fp16),
+        which are in the cache at positions ctx_lens[b] + i of their
+        sequences, over the first ctx_lens[b] positions and, by masks (int64
+        or uint64 [n]: bit j for drafted token j; None: a chain), over one
+        another.  Returns (out like q, lse fp32 [n, q_heads]).  scale is
+        1 / sqrt(head_dim) unless given; max_ctx and max_new bound the
+        lengths (they guide the split only)."""
+        import torch
+        n, heads, d = q.shape
+        if q.dtype != torch.float16:
+            raise ValueError("q must be fp16")
+        if out is None:
+            out = torch.empty((n, heads, d), dtype=torch.float16, device=q.device)
+        elif out.dtype != torch.float16 or out.shape != q.shape:
+            raise ValueError("out must be fp16, shaped like q")
+        if lse is None:
+            lse = torch.empty((n, heads), dtype=torch.float32, device=q.device)
+        if masks is not None and masks.dtype != torch.uint64:
+            _index("masks", masks, torch.int64, (n,))
+        n_seqs, stride = table.shape
+        qgemv_attn_tree(self.desc, _index("table", table, torch.int32, (n_seqs, stride)), stride, n_seqs,
+                        _index("ctx_lens", ctx_lens, torch.int32, (n_seqs,)), *_rows("q", q, heads, self.head_dim),
+                        heads, _index("cu_q", cu_q, torch.int32, (n_seqs + 1,)), n,
+                        None if masks is None else masks.data_ptr(), max_ctx, max_new,
+                        d ** -0.5 if scale is None else scale, *_rows("out", out, heads, d),
+                        _index("lse", lse, torch.float32, (n, heads)), workspace.ptr, workspace.nbytes,
+                        _current(stream))
+        return out, lse
+
+
+def attn_prompt(q, k, v, cu_q, cu_k, *, max_q: int, workspace, scale=None, out=None, lse=None, stream=None):
+    """Causal attention over packed prompts: q [n_q, q_heads, d], k and v
+    [n_k, kv_heads, d] (all fp16 or all bf16), sequence b the rows cu_q[b] ..
+    of q and cu_k[b] .. of k and v (int32 [n_seqs + 1]); its last query sees
+    all of its keys.  Returns (out like q, lse fp32 [n_q, q_heads])."""
+    import torch
+    n, heads, d = q.shape
+    if k.shape[0] != v.shape[0] or not (q.dtype == k.dtype == v.dtype):
+        raise ValueError("q, k and v must have one type, k and v the same number of tokens")
+    if out is None:
+        out = torch.empty((n, heads, d), dtype=q.dtype, device=q.device)
+    elif out.dtype != q.dtype or out.shape != q.shape:
+        raise ValueError("out must have q's type and shape")
+    if lse is None:
+        lse = torch.empty((n, heads), dtype=torch.float32, device=q.device)
+    n_seqs, kv_heads = cu_q.shape[0] - 1, k.shape[1]
+    qgemv_attn_prompt(_dtype_code(q.dtype), d, heads, kv_heads, *_rows("q", q, heads, d), *_rows("k", k, kv_heads, d),
+                      *_rows("v", v, kv_heads, d), n_seqs, _index("cu_q", cu_q, torch.int32, (n_seqs + 1,)),
+                      _index("cu_k", cu_k, torch.int32, (n_seqs + 1,)), n, k.shape[0], max_q,
+                      d ** -0.5 if scale is None else scale, *_rows("out", out, heads, d),
+                      _index("lse", lse, torch.float32, (n, heads)), workspace.ptr, workspace.nbytes, _current(stream))
+    return out, lse

@@ -355,6 +355,139 @@ int qgemv_run_q4_0_noalloc(const void* packed, int64_t N, int64_t K, const void*
 int qgemv_stream_k_plan(int64_t units, int grid, int64_t units_per_row_tile, int rows, int split_unit,
                         int64_t* out);
 
+/* ------------------------------------------------- cache and attention ----
+ *
+ * The attention of a decoder layer between its q|k|v and o projections: a
+ * paged key/value cache (fp16 or quantised), attention of one or several
+ * drafted tokens of each sequence over it, and causal attention over packed
+ * prompts.  No counterpart in the source pages, whose runtimes keep their
+ * own; formulas:
+ *
+ *   out_i = sum_j p_ij v_j / sum_j p_ij,  p_ij = exp(scale * q_i . k_j),
+ *   lse_i = log sum_j p_ij,  over the keys j that row i sees.
+ *
+ * A row that sees no key gives out = 0 and lse = -infinity.  Key/value head
+ * h serves the query heads h * g .. h * g + g - 1, g = q_heads / kv_heads.
+ * Scores, softmax statistics and sums are held in fp32; the probabilities
+ * are rounded to the values' 16-bit type for the tensor cores.  A value or
+ * key that a row does not see never reaches it, infinities and NaN included.
+ *
+ * Rows of heads are given as a device pointer and two element strides,
+ * between tokens and between heads; the head_dim values of a row are
+ * contiguous.  Inputs and outputs need 16-byte aligned pointers and strides
+ * that are multiples of 16 bytes (QGEMV_ERR_ALIGN), so that slices of a
+ * stacked projection's output can be passed as they are.  head_dim is 64 or
+ * 128.  Empty calls (no tokens) return QGEMV_OK.  Index arrays (slots, page
+ * table, lengths, offsets) live on the device and are not checked on the
+ * host; the kernels never read or write outside the buffers that the sizes
+ * describe, whatever they hold.                                             */
+
+/* Element types of rows. */
+typedef enum { QGEMV_DT_F32 = 0, QGEMV_DT_F16 = 1, QGEMV_DT_BF16 = 2 } qgemv_dtype;
+
+/* Cache formats; per token and head, a vector x of head_dim values. */
+typedef enum {
+  /* x rounded to fp16. */
+  QGEMV_KV_F16 = 1,
+  /* a = fl32(max|x| / 127) (fp32, kept), code = clamp(rint(fl32(x / a)),
+   * -127, 127), all 0 if a = 0; the value is code * a.                      */
+  QGEMV_KV_INT8 = 2,
+  /* The Q4_0 quantiser of qgemv_quantize_q4_0 on each 32 values: a =
+   * (signed value of largest magnitude) / -8, kept as fp16, code =
+   * clamp(round(x / a) + 8, 0, 15); the value is (code - 8) * fp16(a).      */
+  QGEMV_KV_Q4_0 = 3
+} qgemv_kv_format;
+/* A vector (Q4_0: a group of 32) with an infinity or NaN is kept as all NaN
+ * in the quantised formats.                                                 */
+
+/* A cache: n_pages pages of page_tokens tokens for each of kv_heads heads,
+ * in the caller's device memory (qgemv_kv_bytes bytes, 128-byte aligned).
+ * page_tokens is 16, 32, 64, 128 or 256.  A slot is page * page_tokens +
+ * token of the page.  The byte layout inside a page is the library's; pages
+ * are independent and may be copied whole (all bytes / n_pages each).       */
+typedef struct {
+  void* pages;
+  int format; /* qgemv_kv_format */
+  int head_dim;
+  int kv_heads;
+  int page_tokens;
+  int64_t n_pages;
+} qgemv_kv_cache;
+
+/* Bytes of a cache, or 0 for invalid sizes. */
+int64_t qgemv_kv_bytes(int format, int64_t n_pages, int page_tokens, int kv_heads, int head_dim);
+
+/* Quantise n_tokens tokens' k and v rows ([n_tokens][kv_heads][head_dim] of
+ * dtype, any qgemv_dtype) into the slots slots[i] (device int64).  A negative
+ * slot, or one past the cache, skips its token.  No two tokens of a call may
+ * share a slot.  Asynchronous on `stream`.                                  */
+int qgemv_kv_write(const qgemv_kv_cache* cache, int dtype, const void* k, int64_t k_token_stride,
+                   int64_t k_head_stride, const void* v, int64_t v_token_stride, int64_t v_head_stride,
+                   const int64_t* slots, int64_t n_tokens, void* stream);
+
+/* Read cached tokens back as rows of dtype (rounded once from fp32):
+ * sequence b's positions starts[b] .. (0 .. if starts is NULL) go to the rows
+ * cu[b] .. cu[b + 1] - 1 of k and v ([n_tokens][kv_heads][head_dim]); cu is
+ * device int32 [n_seqs + 1], not decreasing.  table: device int32 [n_seqs]
+ * [table_stride], the page of each page_tokens positions of a sequence.  A
+ * position whose page is missing (an entry outside the cache, or past the
+ * table) gives zeros.  Rows that belong to no sequence are left as they are.  */
+int qgemv_kv_read(const qgemv_kv_cache* cache, const int32_t* table, int64_t table_stride, int64_t n_seqs,
+                  const int32_t* starts, const int32_t* cu, int64_t n_tokens, int dtype, void* k,
+                  int64_t k_token_stride, int64_t k_head_stride, void* v, int64_t v_token_stride,
+                  int64_t v_head_stride, void* stream);
+
+/* Workspace of the attention calls for up to n_seqs sequences: device memory,
+ * 256-byte aligned, set up once by qgemv_attn_ws_init (asynchronous on
+ * stream) and then reused by any number of calls of both kinds, one at a
+ * time (calls that overlap on the GPU need a workspace each).               */
+int64_t qgemv_attn_ws_bytes(int64_t n_seqs, int q_heads, int head_dim);
+int qgemv_attn_ws_init(void* ws, int64_t ws_bytes, void* stream);
+
+/* Synchronise the device and return QGEMV_ERR_TIMEOUT if an attention kernel
+ * gave up a bounded wait since the last call (the workspace then needs
+ * qgemv_attn_ws_init), else QGEMV_OK.                                       */
+int qgemv_attn_status(void* ws);
+
+/* Attention of drafted tokens over the cache.  The tokens are in it already:
+ * token i of sequence b (row cu_q[b] + i of q and out, fp16 [n_q][q_heads]
+ * [head_dim]) is at position ctx_lens[b] + i.  It sees the positions before
+ * ctx_lens[b] and, of the drafted ones, ctx_lens[b] + j where bit j of
+ * masks[row] is set (masks: device uint64 [n_q], or NULL for bits 0 .. i: a
+ * chain, which for one token is plain decoding).  A sequence has at most 64
+ * drafted tokens; further rows are left as they are.  Positions whose page is
+ * missing are not seen.
+ *   ctx_lens, cu_q: device int32 [n_seqs], [n_seqs + 1].
+ *   max_ctx, max_new: upper bounds on the lengths, for the host's choice of
+ *     kernel and split only: results are right whatever they are.
+ *   lse: device fp32 [n_q][q_heads], or NULL.
+ * Asynchronous on `stream`, no allocation, can be captured in a CUDA graph;
+ * bitwise reproducible for given sizes and lengths.                         */
+int qgemv_attn_tree(const qgemv_kv_cache* cache, const int32_t* table, int64_t table_stride, int64_t n_seqs,
+                    const int32_t* ctx_lens, const void* q, int64_t q_token_stride, int64_t q_head_stride,
+                    int q_heads, const int32_t* cu_q, int64_t n_q, const uint64_t* masks, int64_t max_ctx,
+                    int64_t max_new, float scale, void* out, int64_t out_token_stride, int64_t out_head_stride,
+                    float* lse, void* ws, int64_t ws_bytes, void* stream);
+
+/* Causal attention over packed prompts: sequence b has the queries cu_q[b] ..
+ * cu_q[b + 1] - 1 of q [n_q][q_heads][head_dim] and the keys cu_k[b] ..
+ * cu_k[b + 1] - 1 of k and v [n_k][kv_heads][head_dim]; the last query sees
+ * all of the keys, the one before it all but the last, and so on (query i of
+ * nq sees the keys j <= i + nk - nq of nk: chunks after a past, or rows that
+ * see nothing where nk < nq).  dtype: QGEMV_DT_F16 or QGEMV_DT_BF16, of q, k,
+ * v and out.
+ *   cu_q, cu_k: device int32 [n_seqs + 1], not decreasing.
+ *   max_q: the most queries of a sequence (rows past it may be left out).
+ *   lse: device fp32 [n_q][q_heads], or NULL.
+ * Asynchronous on `stream`, no allocation, can be captured in a CUDA graph;
+ * bitwise reproducible.                                                     */
+int qgemv_attn_prompt(int dtype, int head_dim, int q_heads, int kv_heads, const void* q, int64_t q_token_stride,
+                      int64_t q_head_stride, const void* k, int64_t k_token_stride, int64_t k_head_stride,
+                      const void* v, int64_t v_token_stride, int64_t v_head_stride, int64_t n_seqs,
+                      const int32_t* cu_q, const int32_t* cu_k, int64_t n_q, int64_t n_k, int64_t max_q,
+                      float scale, void* out, int64_t out_token_stride, int64_t out_head_stride, float* lse,
+                      void* ws, int64_t ws_bytes, void* stream);
+
 /* Message and code of the last error on the calling thread ("" / 0 if none). */
 const char* qgemv_last_error(void);
 int qgemv_last_error_code(void);
