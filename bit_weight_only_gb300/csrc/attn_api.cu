@@ -46,8 +46,8 @@ int dtype_size(int dtype) {
 // such that rows overlap.
 int check_rows(const char* name, const void* ptr, int64_t ts, int64_t hs, int size, int heads, int head_dim, bool out) {
   if (!ptr) return fail(QGEMV_ERR_ARG, "%s is NULL", name);
-  const int64_t lim = int64_t(1) << 40;
-  if (ts < 0 || hs < 0 || ts > lim || hs > lim) return fail(QGEMV_ERR_ARG, "%s: strides outside [0, 2^40]", name);
+  const int64_t lim = int64_t(1) << 38;
+  if (ts < 0 || hs < 0 || ts > lim || hs > lim) return fail(QGEMV_ERR_ARG, "%s: strides outside [0, 2^38]", name);
   if (out && (ts < head_dim || (heads > 1 && hs < head_dim)))
     return fail(QGEMV_ERR_ARG, "%s: output rows overlap (strides %lld, %lld)", name, (long long)ts, (long long)hs);
   if ((reinterpret_cast<uintptr_t>(ptr) & 15) || (ts * size & 15) || (hs * size & 15))
@@ -180,6 +180,8 @@ int qgemv_attn_prompt(int dtype, int head_dim, int q_heads, int kv_heads, const 
   if (n_seqs < 0 || n_seqs > (1 << 20) || n_q < 0 || n_q > kMaxTokens || n_k < 0 || n_k > kMaxTokens || max_q < 0)
     return fail(QGEMV_ERR_ARG, "n_seqs outside [0, 2^20], or a token count outside [0, 2^30]");
   if (n_q == 0 || n_seqs == 0 || max_q == 0) return qgemv::report_error(QGEMV_OK, "");
+  if (n_q * (q_heads / 256.0) + static_cast<double>(n_seqs) * kv_heads > 2e9)
+    return fail(QGEMV_ERR_ARG, "too many rows for one call: %lld tokens of %d heads", (long long)n_q, q_heads);
   if (!cu_q || !cu_k) return fail(QGEMV_ERR_ARG, "cu_q or cu_k is NULL");
   if ((reinterpret_cast<uintptr_t>(cu_q) | reinterpret_cast<uintptr_t>(cu_k) | reinterpret_cast<uintptr_t>(lse)) & 3)
     return fail(QGEMV_ERR_ALIGN, "index arrays and lse must be 4-byte aligned");

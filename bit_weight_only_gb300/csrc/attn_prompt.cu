@@ -1,60 +1,498 @@
 // attn_prompt.cu -- causal attention over packed prompts with grouped heads
-// (qgemv_attn_prompt): one warp per (query, head) row.
+// (qgemv_attn_prompt), on the fifth-generation tensor cores.
+//
+//   S = Q K^T,  P = exp2(S * scale * log2 e - m),  O = P V,  out = O / sum P
+//
+// Rows: the queries of a sequence and the G query heads of a key/value head,
+// row = token * G + head, so that short prompts fill tiles and every K and V
+// tile serves all of the heads that share it.  A block takes 256 rows (two
+// tiles of 128) of one key/value head and walks the keys in tiles of 128 up
+// to the last one that its rows see.
+//
+// Warps (12): two softmax warpgroups, one for each row tile, a thread for
+// each row; one warp issues the TMA loads of K and V (two stages each), one
+// the MMAs; two mend V tiles that hold masked positions.  Tensor memory, 512
+// columns: S0 S1 (128 each; P, 16-bit, replaces the first half of S), O0 O1.
+//   * QK of row tile i for key tile j + 1 follows PV of tile j in issue order,
+//     so P may lie over S, and a softmax warpgroup that sees S of tile j knows
+//     that its PV of tile j - 1 is done: it rescales O itself, and only when
+//     a row's maximum has grown by more than 2^8 since the reference m was
+//     taken (P stays below 2^8, in range of fp16).  While one warpgroup takes
+//     its exponentials the tensor cores work on the other row tile.
+//   * A row's statistics live in its thread in fp32; no shuffles.
+//   * Masked scores are replaced by -inf.  V rows that some row of the block
+//     must not see cannot be masked so (0 * NaN): in key tiles with masked
+//     positions the mending warps zero what lies past the sequence and every
+//     infinity and NaN, and note the first position of each per column; the
+//     epilogue gives it to the rows that see it.
+// Every wait is bounded; on a timeout the block records the error, waits for
+// its own copies and MMAs, frees tensor memory and returns.
 #include "attn_row.cuh"
+#include "tc_common.cuh"
 
 namespace qgemv {
 namespace {
 
-constexpr int kThreads = 128;
+constexpr int kThreads = 384;
+constexpr int kRowsPerBlock = 256;
+constexpr int kKeys = 128;         // keys of a tile
+constexpr int kChunk = 128 * 128;  // bytes of 128 rows of 64 values
+constexpr int kErrPrompt = 16;
+constexpr float kLazy = 8.f;  // log2 of the growth that makes O be rescaled
 
-template <int D, typename T>
-__global__ void __launch_bounds__(kThreads) prompt_row_kernel(const PromptParams p) {
-  __shared__ float qs[kThreads / 32][D];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int64_t row = static_cast<int64_t>(blockIdx.x) * (kThreads / 32) + warp;
-  const int64_t token = row / p.q_heads;
-  if (token >= p.n_q) return;
-  const int head = static_cast<int>(row - token * p.q_heads);
-  const int kvh = head / (p.q_heads / p.kv_heads);
-  int seq = 0;
-  while (seq < p.n_seqs && p.cu_q[seq + 1] <= token) ++seq;
-  if (seq >= p.n_seqs || p.cu_q[seq] > token) return;
-  const int64_t i = token - p.cu_q[seq];
-  const int64_t k0 = max(0, p.cu_k[seq]), k1 = min(static_cast<int64_t>(p.cu_k[seq + 1]), p.n_k);
-  const int64_t n = max(static_cast<int64_t>(0), min(k1 - k0, i + 1 + (k1 - k0) - (p.cu_q[seq + 1] - p.cu_q[seq])));
-  const T* q = static_cast<const T*>(p.q.ptr) + token * p.q.token_stride + head * p.q.head_stride;
-  const T* kb = static_cast<const T*>(p.k.ptr) + k0 * p.k.token_stride + kvh * p.k.head_stride;
-  const T* vb = static_cast<const T*>(p.v.ptr) + k0 * p.v.token_stride + kvh * p.v.head_stride;
+template <int D>
+struct Smem {
+  static constexpr int kTile = D / 64 * kChunk;  // 128 rows
+  static constexpr int kQ = 0, kK = 2 * kTile, kV = 4 * kTile, kBars = 6 * kTile;
+  static constexpr int kBad = kBars + 256;  // int[3][D]
+  static constexpr int kBytes = kBad + 3 * D * 4 + 1024;  // + alignment
+};
+
+struct PromptArgs {
+  PromptParams p;
+  int G, n_slots;
+};
+
+// Barriers.
+// kBVm: a V tile with masked positions has landed (kBVf: one without); kBFix: it
+// is mended.  Their phases count the masked tiles of a stage.
+enum { kBQ = 0, kBKf = 2, kBVf = 4, kBVm = 6, kBKe = 8, kBVe = 10, kBFix = 12, kBS = 14, kBP = 16, kBO = 18, kBBad = 20,
+       kBDone = 21, kNBars = 22 };
+
+template <int D, bool BF16>
+__global__ void __launch_bounds__(kThreads, 1)
+prompt_kernel(const PromptArgs a, const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap) {
+  using T = typename std::conditional<BF16, __nv_bfloat16, __half>::type;
+  using S = Smem<D>;
+  const PromptParams& p = a.p;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + S::kBars);
+  volatile int* s_abort = reinterpret_cast<volatile int*>(bars + kNBars);
+  uint32_t* s_tmem = reinterpret_cast<uint32_t*>(bars + kNBars) + 1;
+  int* s_anybad = reinterpret_cast<int*>(bars + kNBars) + 2;
+  int* s_bad = reinterpret_cast<int*>(smem + S::kBad);
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int G = a.G;
+  const int slot = a.n_slots - 1 - static_cast<int>(blockIdx.x / p.kv_heads);
+  const int head = static_cast<int>(blockIdx.x % p.kv_heads);
+
+  // The sequence of this slot: its tiles start at slot floor(cu * G / 256) + b,
+  // which leaves each sequence at least as many slots as it has tiles.
+  int seq;
+  {
+    int lo = 0, hi = p.n_seqs - 1;
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (static_cast<int64_t>(p.cu_q[mid]) * G / kRowsPerBlock + mid <= slot) lo = mid;
+      else hi = mid - 1;
+    }
+    seq = lo;
+  }
+  const int64_t q0 = max(p.cu_q[seq], 0);
+  const int64_t nq = min(static_cast<int64_t>(p.cu_q[seq + 1]), p.n_q) - q0;
+  const int64_t row0 = (slot - (q0 * G / kRowsPerBlock + seq)) * kRowsPerBlock;
+  if (row0 < 0 || nq <= 0 || row0 >= nq * G) return;
+  const int64_t k0 = min(static_cast<int64_t>(max(p.cu_k[seq], 0)), p.n_k);
+  const int nk = static_cast<int>(max(static_cast<int64_t>(0), min(static_cast<int64_t>(p.cu_k[seq + 1]), p.n_k) - k0));
+  const int64_t tok0 = row0 / G;  // first token of the block, and the head of its first row
+  const int rem0 = static_cast<int>(row0 - tok0 * G);
+  const int64_t off = nk - nq;  // query i sees keys j <= i + off
+  const int64_t R = nq * G;
+  auto sees = [&](int64_t row) {  // keys that a row sees: 0 .. sees - 1
+    const int64_t v = row / G + off + 1;
+    return static_cast<int>(v < 0 ? 0 : v < nk ? v : nk);
+  };
+  int n_tiles[2];
 #pragma unroll
-  for (int e = 0; e < D / 32; ++e) qs[warp][32 * e + lane] = to_f32<T>(q[32 * e + lane]);
-  __syncwarp();
-  float acc[D / 32], m, l;
-  attend_row<D>(
-      n, [&](int64_t) { return true; },
-      [&](int64_t j) {
-        const T* k = kb + j * p.k.token_stride;
-        float s = 0.f;
-        for (int d = 0; d < D; ++d) s = fmaf(qs[warp][d], to_f32<T>(k[d]), s);
-        return s * p.scale * kLog2e;
-      },
-      [&](int64_t j, int d) { return to_f32<T>(vb[j * p.v.token_stride + d]); }, acc, m, l);
-  store_row<D>(static_cast<T*>(p.out.ptr) + token * p.out.token_stride + head * p.out.head_stride,
-               p.lse ? p.lse + token * p.q_heads + head : nullptr, acc, m, l);
+  for (int i = 0; i < 2; ++i) {
+    const int64_t r0 = row0 + 128 * i;
+    n_tiles[i] = r0 >= R ? 0 : (sees(min(r0 + 127, R - 1)) + kKeys - 1) / kKeys;
+  }
+  const int n_max = max(n_tiles[0], n_tiles[1]);
+  // the first key tile with positions that some row of the block does not see
+  const int first_masked = sees(row0) / kKeys;
+
+  if (tid == 0) {
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&bars[kBQ + i], 128);
+      mbar_init(&bars[kBKf + i], 1);
+      mbar_init(&bars[kBVf + i], 1);
+      mbar_init(&bars[kBVm + i], 1);
+      mbar_init(&bars[kBKe + i], 1);
+      mbar_init(&bars[kBVe + i], 1);
+      mbar_init(&bars[kBFix + i], 64);
+      mbar_init(&bars[kBS + i], 1);
+      mbar_init(&bars[kBP + i], 128);
+      mbar_init(&bars[kBO + i], 1);
+    }
+    mbar_init(&bars[kBBad], 64);
+    mbar_init(&bars[kBDone], 1);
+    fence_mbarrier_init();
+    *s_abort = 0;
+    *s_anybad = 0;
+  }
+  for (int i = tid; i < 3 * D; i += kThreads) s_bad[i] = 0x7fffffff;
+  if (warp == 8) tmem_alloc_all(s_tmem);
+  tcgen_before_sync();
+  __syncthreads();
+  tcgen_after_sync();
+  const uint32_t tbase = *s_tmem;
+
+  auto wait = [&](int bar, uint32_t parity) -> bool {
+    if (mbar_try_wait(&bars[bar], parity)) return true;
+    const unsigned long long t0 = global_timer_ns();
+    while (!mbar_try_wait(&bars[bar], parity)) {
+      if (*s_abort) return false;
+      if (global_timer_ns() - t0 > kWaitLimitNs) {
+        atomicOr(reinterpret_cast<int*>(p.ws), kErrPrompt);
+        *s_abort = 1;
+        return false;
+      }
+    }
+    return true;
+  };
+
+  // V tile j: the barrier of its landing, and the parity of it and of kBFix
+  auto v_bar = [&](int j) { return (j >= first_masked ? kBVm : kBVf) + (j & 1); };
+  auto v_parity = [&](int j) { return static_cast<uint32_t>(((j >= first_masked ? j - first_masked : j) >> 1) & 1); };
+
+  if (warp >= 8) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+    if (warp == 8) {
+      // ---- TMA: K and V tiles
+      if (lane == 0) {
+        int issued_k = 0, issued_v = 0;
+        auto load = [&](const CUtensorMap* map, int full, int empty, int base, int j) -> bool {
+          const int st = j & 1;
+          if (j >= 2 && !wait(empty + st, ((j >> 1) - 1) & 1)) return false;
+          mbar_arrive_expect_tx(&bars[full], S::kTile);
+#pragma unroll
+          for (int c = 0; c < D / 64; ++c)
+            tma_load_3d(smem + base + st * S::kTile + c * kChunk, map, 64 * c, head, static_cast<int>(k0) + j * kKeys,
+                        &bars[full]);
+          return true;
+        };
+        for (int j = 0; j < n_max; ++j) {
+          if (!load(&kmap, kBKf + (j & 1), kBKe, S::kK, j)) break;
+          ++issued_k;
+          if (!load(&vmap, v_bar(j), kBVe, S::kV, j)) break;
+          ++issued_v;
+        }
+        // Copies still in flight (after an abort) must land before the block ends.
+        for (int j = max(0, issued_k - 2); j < issued_k; ++j) mbar_wait_bounded(&bars[kBKf + (j & 1)], (j >> 1) & 1);
+        for (int j = max(0, issued_v - 2); j < issued_v; ++j) mbar_wait_bounded(&bars[v_bar(j)], v_parity(j));
+      }
+    } else if (warp == 9) {
+      // ---- MMAs
+      if (lane == 0 && n_max > 0) {
+        constexpr uint32_t id_qk = mma_idesc(BF16, false, kKeys), id_pv = mma_idesc(BF16, true, D);
+        const uint32_t sq = smem_u32(smem + S::kQ), sk = smem_u32(smem + S::kK), sv = smem_u32(smem + S::kV);
+        auto qk = [&](int i, int j) {
+          const uint64_t da = sw128_desc(sq + i * S::kTile, 0, 1024);
+          const uint64_t db = sw128_desc(sk + (j & 1) * S::kTile, 0, 1024);
+#pragma unroll
+          for (int k = 0; k < D / 16; ++k) {
+            const uint32_t o = ((k >> 2) * kChunk + (k & 3) * 32) >> 4;
+            mma_ss(tbase + 128 * i, da + o, db + o, id_qk, k > 0);
+          }
+          mma_commit(&bars[kBS + i]);
+        };
+        auto pv = [&](int i, int j) {
+          const uint64_t db = sw128_desc(sv + (j & 1) * S::kTile, kChunk, 1024);
+#pragma unroll
+          for (int k = 0; k < kKeys / 16; ++k)
+            mma_ts(tbase + 256 + 128 * i, tbase + 128 * i + 8 * k, db + ((k * 2048) >> 4), id_pv, j > 0 || k > 0);
+        };
+        bool ok = wait(kBKf, 0);
+        for (int i = 0; i < 2; ++i)
+          if (ok && n_tiles[i] > 0) {
+            ok = wait(kBQ + i, 0);
+            tcgen_after_sync();
+            if (ok) qk(i, 0);
+          }
+        if (ok) mma_commit(&bars[kBKe]);
+        for (int j = 0; ok && j < n_max; ++j) {
+          bool have_v = false, have_k = false;
+          for (int i = 0; ok && i < 2; ++i) {
+            if (j >= n_tiles[i]) continue;
+            if (!have_v) ok = wait((j >= first_masked ? kBFix : kBVf) + (j & 1), v_parity(j));
+            have_v = true;
+            if (ok) ok = wait(kBP + i, j & 1);
+            if (!ok) break;
+            tcgen_after_sync();
+            pv(i, j);
+            if (j + 1 < n_tiles[i]) {
+              if (!have_k) ok = wait(kBKf + ((j + 1) & 1), ((j + 1) >> 1) & 1);
+              have_k = true;
+              if (ok) qk(i, j + 1);
+            } else {
+              mma_commit(&bars[kBO + i]);
+            }
+          }
+          if (ok) {
+            mma_commit(&bars[kBVe + (j & 1)]);
+            if (have_k) mma_commit(&bars[kBKe + ((j + 1) & 1)]);
+          }
+        }
+        if (!ok) {  // MMAs in flight: let them finish before tensor memory is freed
+          mma_commit(&bars[kBDone]);
+          mbar_wait_bounded(&bars[kBDone], 0);
+        }
+      }
+    } else {
+      // ---- mending of V tiles with masked positions
+      const int t = tid - 320;
+      for (int j = first_masked; j < n_max; ++j) {
+        if (!wait(v_bar(j), v_parity(j))) break;
+        uint8_t* v = smem + S::kV + (j & 1) * S::kTile;
+        const int live = min(kKeys, nk - j * kKeys);  // positions of the tile inside the sequence
+        constexpr uint32_t kExp = BF16 ? 0x7F807F80u : 0x7C007C00u, kOne = BF16 ? 0x00800080u : 0x04000400u;
+        bool wrote = false;
+        for (int u = t; u < S::kTile / 16; u += 64) {
+          uint4* at = reinterpret_cast<uint4*>(v + u * 16);
+          const int r = (u >> 3) & 127;
+          if (r >= live) {
+            *at = make_uint4(0u, 0u, 0u, 0u);
+            wrote = true;
+            continue;
+          }
+          const uint4 w = *at;
+          const uint32_t bad = (((w.x & kExp) + kOne) | ((w.y & kExp) + kOne) | ((w.z & kExp) + kOne) | ((w.w & kExp) + kOne)) &
+                               0x80008000u;
+          if (bad) {
+            uint16_t* h = reinterpret_cast<uint16_t*>(at);
+            const int d0 = (u >> 10) * 64 + (((u & 7) ^ (r & 7)) << 3);
+            for (int e = 0; e < 8; ++e) {
+              const uint16_t x = h[e];
+              if ((x & (kExp & 0xffffu)) != (kExp & 0xffffu)) continue;
+              const int kind = (x & 0x7fff & ~(kExp & 0xffffu)) ? 0 : x >> 15 ? 2 : 1;
+              atomicMin(&s_bad[kind * D + d0 + e], j * kKeys + r);
+              h[e] = 0;
+            }
+            *s_anybad = 1;
+            wrote = true;
+          }
+        }
+        if (wrote) fence_async_smem();
+        mbar_arrive(&bars[kBFix + (j & 1)]);
+      }
+      mbar_arrive(&bars[kBBad]);
+    }
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
+    // ---- softmax warpgroup i: Q rows in, then a thread for each row
+    const int i = warp >> 2, wt = tid & 127;
+    const int64_t r0 = row0 + 128 * i;
+    const bool active = r0 < R;
+    if (active) {
+      uint8_t* q = smem + S::kQ + i * S::kTile;
+      constexpr int U = D / 8;  // 16-byte units of a row
+      const uint32_t flip = p.scale < 0.f ? 0x80008000u : 0u;  // a negative scale goes to Q
+      const T* qb = static_cast<const T*>(p.q.ptr);
+#pragma unroll 4
+      for (int it = 0; it < U; ++it) {
+        const int idx = it * 128 + wt;
+        const int r = idx / U, u = idx % U;
+        uint4 w = make_uint4(0u, 0u, 0u, 0u);
+        if (r0 + r < R) {
+          const int x = rem0 + 128 * i + r, tok = x / G;
+          w = __ldg(reinterpret_cast<const uint4*>(qb + (q0 + tok0 + tok) * p.q.token_stride +
+                                                   (head * G + x - tok * G) * p.q.head_stride + 8 * u));
+          w.x ^= flip, w.y ^= flip, w.z ^= flip, w.w ^= flip;
+        }
+        *reinterpret_cast<uint4*>(q + (u >> 3) * kChunk + r * 128 + (((u & 7) ^ (r & 7)) << 4)) = w;
+      }
+      fence_async_smem();
+      mbar_arrive(&bars[kBQ + i]);
+
+      const int64_t row = r0 + wt;
+      const int my_sees = sees(min(row, R - 1));
+      const int all_see = sees(r0);  // what every row of the tile sees
+      const int n = i == 0 ? n_tiles[0] : n_tiles[1];
+      const uint32_t t_lane = static_cast<uint32_t>(32 * (warp & 3)) << 16;
+      const uint32_t t_s = tbase + t_lane + 128 * i, t_o = tbase + t_lane + 256 + 128 * i;
+      const float sl = fmaxf(fabsf(p.scale) * kLog2e, 1.2e-38f);  // not 0: -inf * sl stays -inf
+      float m = -INFINITY, l = 0.f;
+      bool ok = true;
+      for (int j = 0; j < n; ++j) {
+        ok = wait(kBS + i, j & 1);
+        if (!__all_sync(0xffffffffu, ok)) {
+          ok = false;
+          break;
+        }
+        tcgen_after_sync();
+        uint32_t s[128];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) tmem_ld32(t_s + 32 * c, s + 32 * c);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) tmem_wait_ld32(s + 32 * c);
+        if ((j + 1) * kKeys > all_see) {
+          const int lim = my_sees - j * kKeys;
+#pragma unroll
+          for (int c = 0; c < 128; ++c)
+            if (c >= lim) s[c] = 0xff800000u;  // -inf
+        }
+        float top[4];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) top[c] = __uint_as_float(s[c]);
+#pragma unroll
+        for (int c = 4; c < 128; c += 8)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            top[e] = c + e + 4 < 128 ? fmaxf(top[e], fmaxf(__uint_as_float(s[c + e]), __uint_as_float(s[c + e + 4])))
+                                     : fmaxf(top[e], __uint_as_float(s[c + e]));
+        const float mt = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * sl;
+        const bool grow = mt > m + kLazy || (m == -INFINITY && mt > -INFINITY);
+        if (__any_sync(0xffffffffu, grow)) {
+          const float mn = fmaxf(m, mt);
+          const float f = m == -INFINITY ? 0.f : ex2(m - mn);
+          l *= f;
+          m = mn;
+          if (j > 0) {
+            const uint64_t f2 = pack2(f, f);
+#pragma unroll
+            for (int c = 0; c < D; c += 32) {
+              uint32_t o[32];
+              tmem_ld32(t_o + c, o);
+              tmem_wait_ld32(o);
+#pragma unroll
+              for (int e = 0; e < 32; e += 2) {
+                float x, y;
+                unpack2(mul2(pack2(__uint_as_float(o[e]), __uint_as_float(o[e + 1])), f2), x, y);
+                o[e] = __float_as_uint(x), o[e + 1] = __float_as_uint(y);
+              }
+              tmem_st32(t_o + c, o);
+            }
+          }
+        }
+        const float ref = m == -INFINITY ? 0.f : m;
+        const uint64_t sl2 = pack2(sl, sl), nm2 = pack2(-ref, -ref);
+        uint64_t sum[2] = {pack2(0.f, 0.f), pack2(0.f, 0.f)};
+#pragma unroll
+        for (int c = 0; c < 128; c += 2) {
+          float x, y;
+          unpack2(fma2(pack2(__uint_as_float(s[c]), __uint_as_float(s[c + 1])), sl2, nm2), x, y);
+          x = ex2(x), y = ex2(y);
+          sum[(c >> 1) & 1] = add2(sum[(c >> 1) & 1], pack2(x, y));
+          s[c >> 1] = cvt_pair<BF16>(x, y);
+        }
+        {
+          float x, y;
+          unpack2(add2(sum[0], sum[1]), x, y);
+          l += x + y;
+        }
+        tmem_st32(t_s, s);
+        tmem_st32(t_s + 32, s + 32);
+        tmem_wait_store();
+        tcgen_before_sync();
+        mbar_arrive(&bars[kBP + i]);
+      }
+      // ---- epilogue
+      ok = ok && (n == 0 || wait(kBO + i, 0)) && wait(kBBad, 0);
+      if (__all_sync(0xffffffffu, ok)) {
+        tcgen_after_sync();
+        const int64_t tok = row / G;
+        const int h = head * G + static_cast<int>(row - tok * G);
+        const bool store = row < R;
+        T* out = static_cast<T*>(p.out.ptr) + (q0 + tok) * p.out.token_stride + h * p.out.head_stride;
+        const float inv = l == 0.f ? 0.f : 1.f / l;
+        const bool bad = *s_anybad != 0;
+#pragma unroll
+        for (int c = 0; c < D; c += 32) {
+          uint32_t o[32];
+          if (n > 0) {
+            tmem_ld32(t_o + c, o);
+            tmem_wait_ld32(o);
+          }
+#pragma unroll
+          for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(l == 0.f ? 0.f : __uint_as_float(o[e]) * inv);
+          if (bad) {
+#pragma unroll
+            for (int e = 0; e < 32; ++e) {
+              const bool nan = s_bad[c + e] < my_sees, up = s_bad[D + c + e] < my_sees, down = s_bad[2 * D + c + e] < my_sees;
+              if (nan || (up && down)) o[e] = 0x7fffffffu;
+              else if (up) o[e] = 0x7f800000u;
+              else if (down) o[e] = 0xff800000u;
+            }
+          }
+          if (store) {
+#pragma unroll
+            for (int e = 0; e < 32; e += 8) {
+              uint4 w;
+              w.x = cvt_pair<BF16>(__uint_as_float(o[e]), __uint_as_float(o[e + 1]));
+              w.y = cvt_pair<BF16>(__uint_as_float(o[e + 2]), __uint_as_float(o[e + 3]));
+              w.z = cvt_pair<BF16>(__uint_as_float(o[e + 4]), __uint_as_float(o[e + 5]));
+              w.w = cvt_pair<BF16>(__uint_as_float(o[e + 6]), __uint_as_float(o[e + 7]));
+              *reinterpret_cast<uint4*>(out + c + e) = w;
+            }
+          }
+        }
+        if (store && p.lse) p.lse[(q0 + tok) * p.q_heads + h] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+        tcgen_before_sync();
+      }
+    }
+  }
+  __syncthreads();
+  if (warp == 8) tmem_free_all(tbase);
+}
+
+using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
+                              const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                              CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeFn encode_fn() {
+  static EncodeFn fn = [] {
+    void* f = nullptr;
+    cudaDriverEntryPointQueryResult r;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &r) != cudaSuccess ||
+        r != cudaDriverEntryPointSuccess)
+      f = nullptr;
+    return reinterpret_cast<EncodeFn>(f);
+  }();
+  return fn;
+}
+
+// Map of rows [tokens][heads][D]: boxes of 64 values x 1 head x 128 tokens.
+cudaError_t make_map(CUtensorMap* map, const RowsIn& r, int D, int heads, int64_t tokens, bool bf16) {
+  EncodeFn fn = encode_fn();
+  if (!fn) return cudaErrorNotSupported;
+  // the stride of a dimension of one element is free; zero strides have no map
+  const int64_t hs = heads > 1 ? r.head_stride : D, ts = tokens > 1 ? r.token_stride : static_cast<int64_t>(heads) * D;
+  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(heads), static_cast<cuuint64_t>(tokens)};
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(hs) * 2, static_cast<cuuint64_t>(ts) * 2};
+  const cuuint32_t box[3] = {64, 1, kKeys}, ones[3] = {1, 1, 1};
+  const CUresult rc = fn(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3,
+                         const_cast<void*>(r.ptr), dims, strides, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                         CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return rc == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+template <int D, bool BF16>
+cudaError_t launch(const PromptParams& p, cudaStream_t s) {
+  PromptArgs a;
+  a.p = p;
+  a.G = p.q_heads / p.kv_heads;
+  a.n_slots = static_cast<int>(p.n_q * a.G / kRowsPerBlock) + p.n_seqs;
+  CUtensorMap km = {}, vm = {};
+  if (p.n_k > 0) {
+    cudaError_t e = make_map(&km, p.k, D, p.kv_heads, p.n_k, BF16);
+    if (e == cudaSuccess) e = make_map(&vm, p.v, D, p.kv_heads, p.n_k, BF16);
+    if (e != cudaSuccess) return e;
+  }
+  static const cudaError_t attr =
+      cudaFuncSetAttribute(prompt_kernel<D, BF16>, cudaFuncAttributeMaxDynamicSharedMemorySize, Smem<D>::kBytes);
+  if (attr != cudaSuccess) return attr;
+  prompt_kernel<D, BF16><<<static_cast<unsigned>(a.n_slots) * p.kv_heads, kThreads, Smem<D>::kBytes, s>>>(a, km, vm);
+  return cudaGetLastError();
 }
 
 }  // namespace
 
 cudaError_t launch_attn_prompt(const PromptParams& p, cudaStream_t s) {
-  const int64_t rows = p.n_q * p.q_heads;
-  const unsigned grid = static_cast<unsigned>((rows + kThreads / 32 - 1) / (kThreads / 32));
-  if (p.dtype == QGEMV_DT_F16) {
-    if (p.head_dim == 64) prompt_row_kernel<64, __half><<<grid, kThreads, 0, s>>>(p);
-    else prompt_row_kernel<128, __half><<<grid, kThreads, 0, s>>>(p);
-  } else {
-    if (p.head_dim == 64) prompt_row_kernel<64, __nv_bfloat16><<<grid, kThreads, 0, s>>>(p);
-    else prompt_row_kernel<128, __nv_bfloat16><<<grid, kThreads, 0, s>>>(p);
-  }
-  return cudaGetLastError();
+  if (p.dtype == QGEMV_DT_F16) return p.head_dim == 64 ? launch<64, false>(p, s) : launch<128, false>(p, s);
+  return p.head_dim == 64 ? launch<64, true>(p, s) : launch<128, true>(p, s);
 }
 
 }  // namespace qgemv
