@@ -1,74 +1,824 @@
 // attn_tree.cu -- attention of drafted tokens over the paged key/value cache
-// (qgemv_attn_tree): one warp per (token, head) row.
+// (qgemv_attn_tree).
+//
+// Rows of a sequence and key/value head: row = token * G + head of the group,
+// in tiles of 16 or 32.  The work is a list of units, one block of 16 cached
+// tokens for one row tile, ordered (sequence, head, row tile, block); every
+// thread block takes an equal run of it, so that sequences of any lengths
+// share the GPU evenly.  Within its run a warp takes every W-th unit:
+//
+//   copy      one bulk copy into the warp's own ring of shared-memory stages
+//   S = Q K^T mma.m16n8k16 on the codes as fp16 (INT8 and Q4_0 codes are
+//             exact), K straight from the block's layout; the scales of the
+//             tokens (Q4_0: of each group, on partial sums) go to S in fp32
+//   softmax   base 2, an own reference m for each warp and row that moves only
+//             when a score passes it by 2^8: without a move no shuffle is
+//             needed.  m is taken over s + log2(scale of v), because what is
+//             rounded to fp16 is p * scale(v), the factor of v's codes: it
+//             stays in [0, 2^8] whatever the scales are
+//   O += P V  the same instruction on V's codes
+//
+// A warp's O, m and l live in its registers.  At the end of a run's part of a
+// row tile the warps' results are added in warp order through shared memory;
+// row tiles that several thread blocks share go to the workspace, and the last
+// of them to arrive adds all of them in order (so the result does not depend
+// on who is last) and clears the counter.
 #include "attn_row.cuh"
+#include "tc_common.cuh"
 
 namespace qgemv {
-
-int64_t tree_ws_bytes(int64_t, int, int) { return 0; }
-
 namespace {
 
-constexpr int kThreads = 128;
+constexpr int kErrTree = 32;
+constexpr float kLazyT = 8.f;
+constexpr int kMaxBlocks = 512;       // thread blocks of a call, at most
+constexpr int kMaxRows = 32;
+constexpr int kRingBytes = 200 * 1024;
 
+__host__ __device__ constexpr int64_t slot_floats(int D) { return static_cast<int64_t>(kMaxRows) * (D + 2); }
+
+__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(smem_u32(dst)),
+               "l"(src), "r"(bytes), "r"(smem_u32(bar))
+               : "memory");
+}
+
+// c += a . b: 16 x 16 . 16 x 8, fp16 in, fp32 sums.
+__device__ __forceinline__ void mma16816(float (&c)[4], const uint4& a, uint32_t b0, uint32_t b1) {
+  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+               : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+               : "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t s) { return __byte_perm(a, b, s); }
+__device__ __forceinline__ uint32_t hsub2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ uint32_t hfma2(uint32_t a, uint32_t b, uint32_t c) {
+  uint32_t r;
+  asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
+  return r;
+}
+__device__ __forceinline__ uint32_t half_pair(float lo, float hi) { return cvt_pair<false>(lo, hi); }
+__device__ __forceinline__ float lg2(float x) {
+  float y;
+  asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// Codes to fp16 pairs.  INT8: bytes b0, b1 of w, stored + 128: 0x64 in the
+// high byte makes 1024 + code.
+template <int SEL>
+__device__ __forceinline__ uint32_t i8_pair(uint32_t w) {
+  return hsub2(prmt(w, 0x64646464u, SEL), 0x64806480u);  // - 1152
+}
+// Q4_0: nibbles N and N + 4 of w, minus 8.
+template <int N>
+__device__ __forceinline__ uint32_t q4_pair(uint32_t w) {
+  const uint32_t v = N >= 2 ? w >> 8 : w;
+  if (N & 1) return hfma2((v & 0x00F000F0u) | 0x64006400u, 0x2C002C00u, 0xD480D480u);  // (1024 + 16 q) / 16 - 72
+  return hsub2((v & 0x000F000Fu) | 0x64006400u, 0x64086408u);                          // 1024 + q - 1032
+}
+
+// Per format: words of K and V of a lane, and the fp16 pairs in them.
 template <int FMT, int D>
-__global__ void __launch_bounds__(kThreads) tree_row_kernel(const TreeParams p) {
-  __shared__ float qs[kThreads / 32][D];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int64_t row = static_cast<int64_t>(blockIdx.x) * (kThreads / 32) + warp;
-  const int64_t token = row / p.q_heads;
-  if (token >= p.n_q) return;
-  const int head = static_cast<int>(row - token * p.q_heads);
-  const int kvh = head / (p.q_heads / p.cache.kv_heads);
-  int seq = 0;
-  while (seq < p.n_seqs && p.cu_q[seq + 1] <= token) ++seq;
-  if (seq >= p.n_seqs || p.cu_q[seq] > token) return;
-  const int i = static_cast<int>(token - p.cu_q[seq]);
-  const int T = min(p.cu_q[seq + 1] - p.cu_q[seq], kMaxDrafts);
-  if (i >= T) return;
-  const int ctx = max(0, p.ctx_lens[seq]);
-  const uint64_t mask = p.masks ? p.masks[token] : (i == 63 ? ~0ull : (1ull << (i + 1)) - 1);
-  const __half* q = static_cast<const __half*>(p.q.ptr) + token * p.q.token_stride + head * p.q.head_stride;
+struct Codes;
+
+template <int D>
+struct Codes<QGEMV_KV_F16, D> {
+  using L = KvLayout<QGEMV_KV_F16, D>;
+  static constexpr int kKw = D / 8;
+  __device__ static int q_at(int ks, int t) { return 32 * (ks >> 1) + 8 * t + 4 * (ks & 1); }
+  __device__ static int out_at(int nb, int n) { return 64 * (nb >> 3) + 8 * n + (nb & 7); }
+  __device__ static void load_k(const uint8_t* b, int tok, int t, uint32_t (&w)[kKw]) {
 #pragma unroll
-  for (int e = 0; e < D / 32; ++e) qs[warp][32 * e + lane] = __half2float(q[32 * e + lane]);
+    for (int i = 0; i < D / 32; ++i) *reinterpret_cast<uint4*>(&w[4 * i]) = lds128(b + L::k_off(tok, 64 * i + 16 * t));
+  }
+  __device__ static void k_frag(const uint32_t (&w)[kKw], int ks, uint32_t& b0, uint32_t& b1) {
+    b0 = w[2 * ks], b1 = w[2 * ks + 1];
+  }
+  // V: [unit][token pair 0, 1][token][word]
+  __device__ static void load_v(const uint8_t* b, int g, int t, uint32_t (&w)[4 * (D / 16)]) {
+#pragma unroll
+    for (int u = 0; u < D / 64; ++u)
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        *reinterpret_cast<uint4*>(&w[16 * u + 4 * k]) = lds128(b + L::v_off(2 * t + (k & 1) + 8 * (k >> 1), 128 * u + 16 * g));
+  }
+  __device__ static void v_frag(const uint32_t (&w)[4 * (D / 16)], int nb, uint32_t& b0, uint32_t& b1) {
+    const int at = 16 * (nb >> 3) + ((nb & 7) >> 1);
+    const uint32_t sel = nb & 1 ? 0x7632u : 0x5410u;
+    b0 = prmt(w[at], w[at + 4], sel);
+    b1 = prmt(w[at + 8], w[at + 12], sel);
+  }
+};
+
+template <int D>
+struct Codes<QGEMV_KV_INT8, D> {
+  using L = KvLayout<QGEMV_KV_INT8, D>;
+  static constexpr int kKw = D / 16;
+  __device__ static int q_at(int ks, int t) { return 64 * (ks >> 2) + 16 * t + 4 * (ks & 3); }
+  __device__ static int out_at(int nb, int n) { return D / 8 * n + nb; }
+  __device__ static void load_k(const uint8_t* b, int tok, int t, uint32_t (&w)[kKw]) {
+#pragma unroll
+    for (int h = 0; h < D / 64; ++h) *reinterpret_cast<uint4*>(&w[4 * h]) = lds128(b + L::k_off(tok, 64 * h + 16 * t));
+  }
+  __device__ static void k_frag(const uint32_t (&w)[kKw], int ks, uint32_t& b0, uint32_t& b1) {
+    b0 = i8_pair<0x4140>(w[ks]), b1 = i8_pair<0x4342>(w[ks]);
+  }
+  // V: [token][word]
+  __device__ static void load_v(const uint8_t* b, int g, int t, uint32_t (&w)[4 * (D / 32)]) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const uint8_t* at = b + L::v_off(2 * t + (k & 1) + 8 * (k >> 1), D / 8 * g);
+      if constexpr (D == 128) *reinterpret_cast<uint4*>(&w[4 * k]) = lds128(at);
+      else *reinterpret_cast<uint2*>(&w[2 * k]) = *reinterpret_cast<const uint2*>(at);
+    }
+  }
+  __device__ static void v_frag(const uint32_t (&w)[4 * (D / 32)], int nb, uint32_t& b0, uint32_t& b1) {
+    constexpr int P = D / 32;
+    const int e = nb >> 2, c = nb & 3;
+    const uint32_t x = prmt(w[e], w[P + e], c & 2 ? 0x7362u : 0x5140u);
+    const uint32_t y = prmt(w[2 * P + e], w[3 * P + e], c & 2 ? 0x7362u : 0x5140u);
+    b0 = c & 1 ? i8_pair<0x4342>(x) : i8_pair<0x4140>(x);
+    b1 = c & 1 ? i8_pair<0x4342>(y) : i8_pair<0x4140>(y);
+  }
+};
+
+template <int D>
+struct Codes<QGEMV_KV_Q4_0, D> {
+  using L = KvLayout<QGEMV_KV_Q4_0, D>;
+  static constexpr int kKw = D / 32;
+  __device__ static int q_at(int ks, int t) { return 32 * (ks >> 1) + 8 * t + 4 * (ks & 1); }
+  __device__ static int out_at(int nb, int n) { return 32 * (nb >> 2) + 4 * n + (nb & 3); }
+  __device__ static void load_k(const uint8_t* b, int tok, int t, uint32_t (&w)[kKw]) {
+    const uint8_t* at = b + L::k_off(tok, D / 8 * t);
+    if constexpr (D == 128) *reinterpret_cast<uint4*>(w) = lds128(at);
+    else *reinterpret_cast<uint2*>(w) = *reinterpret_cast<const uint2*>(at);
+  }
+  __device__ static void k_frag(const uint32_t (&w)[kKw], int ks, uint32_t& b0, uint32_t& b1) {
+    const uint32_t x = w[ks >> 1];
+    if (ks & 1) b0 = q4_pair<2>(x), b1 = q4_pair<3>(x);
+    else b0 = q4_pair<0>(x), b1 = q4_pair<1>(x);
+  }
+  // V: [token][group pair]
+  __device__ static void load_v(const uint8_t* b, int g, int t, uint32_t (&w)[4 * (D / 64)]) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const uint8_t* at = b + L::v_off(2 * t + (k & 1) + 8 * (k >> 1), D / 16 * g);
+      if constexpr (D == 128) *reinterpret_cast<uint2*>(&w[2 * k]) = *reinterpret_cast<const uint2*>(at);
+      else w[k] = *reinterpret_cast<const uint32_t*>(at);
+    }
+  }
+  __device__ static void v_frag(const uint32_t (&w)[4 * (D / 64)], int nb, uint32_t& b0, uint32_t& b1) {
+    constexpr int P = D / 64;
+    const int grp = nb >> 2, e = grp >> 1;
+    const uint32_t sel = grp & 1 ? 0x7632u : 0x5410u;
+    const uint32_t x = prmt(w[e], w[P + e], sel), y = prmt(w[2 * P + e], w[3 * P + e], sel);
+    switch (nb & 3) {
+      case 0: b0 = q4_pair<0>(x), b1 = q4_pair<0>(y); break;
+      case 1: b0 = q4_pair<1>(x), b1 = q4_pair<1>(y); break;
+      case 2: b0 = q4_pair<2>(x), b1 = q4_pair<2>(y); break;
+      default: b0 = q4_pair<3>(x), b1 = q4_pair<3>(y);
+    }
+  }
+};
+
+// Shape of a kernel: W warps, MT tiles of 16 rows.
+template <int FMT, int D, int MT>
+struct TreeShape {
+  using L = KvLayout<FMT, D>;
+  static constexpr int kWarps = MT == 2 || FMT == QGEMV_KV_F16 || D == 64 ? 8 : 16;
+  static constexpr int kThreads = 32 * kWarps;
+  static constexpr int kRows = 16 * MT;
+  static constexpr int kFitting = kRingBytes / (kWarps * L::kBlock);
+  static constexpr int kStages = kFitting > 6 ? 6 : kFitting;
+  static constexpr int kRing = kWarps * kStages * L::kBlock;
+  static constexpr int kMerge = kWarps * kRows * D * 4 + kRows * D * 2;  // the warps' O, then the rows as fp16
+  static constexpr int kRegion = kRing > kMerge ? kRing : kMerge;
+  static constexpr int kQ = kRegion;                            // Q fragments
+  static constexpr int kMl = kQ + MT * (D / 16) * 512;          // m, l of each warp and row
+  static constexpr int kMask = kMl + kWarps * kRows * 8;        // mask words of the rows
+  static constexpr int kBars = kMask + kRows * 8;
+  static constexpr int kBytes = kBars + kWarps * kStages * 8 + 16;
+};
+
+struct TreeArgs {
+  TreeParams p;
+  int G, page_shift, min_units;
+};
+
+struct SeqWork {
+  int64_t units;  // of one row tile
+  int tiles;      // row tiles of a head
+  int ctx, T;
+};
+
+template <int ROWS>
+__device__ __forceinline__ SeqWork seq_work(const TreeArgs& a, int b) {
+  const TreeParams& p = a.p;
+  SeqWork s;
+  const int64_t q0 = p.cu_q[b];
+  int64_t T = p.cu_q[b + 1] - q0;
+  if (q0 < 0 || T < 0) T = 0;
+  T = min(T, min(static_cast<int64_t>(kMaxDrafts), p.n_q - q0));
+  s.T = static_cast<int>(max(T, static_cast<int64_t>(0)));
+  s.ctx = max(0, p.ctx_lens[b]);
+  const int64_t n = min(static_cast<int64_t>(s.ctx) + s.T, p.table_stride << a.page_shift);
+  s.units = max(static_cast<int64_t>(1), (n + kKvBlockTokens - 1) / kKvBlockTokens);
+  s.tiles = (s.T * a.G + ROWS - 1) / ROWS;
+  return s;
+}
+
+template <int FMT, int D, int MT>
+__global__ void __launch_bounds__(TreeShape<FMT, D, MT>::kThreads, 1) tree_kernel(const TreeArgs a) {
+  using Sh = TreeShape<FMT, D, MT>;
+  using L = KvLayout<FMT, D>;
+  using C = Codes<FMT, D>;
+  constexpr int W = Sh::kWarps, NS = Sh::kStages, KS = D / 16, NB = D / 8;
+  const TreeParams& p = a.p;
+  extern __shared__ __align__(128) uint8_t smem[];
+  uint4* s_q = reinterpret_cast<uint4*>(smem + Sh::kQ);
+  float2* s_ml = reinterpret_cast<float2*>(smem + Sh::kMl);
+  uint64_t* s_mask = reinterpret_cast<uint64_t*>(smem + Sh::kMask);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + Sh::kBars);
+  int* s_last = reinterpret_cast<int*>(bars + W * NS);
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int g = lane >> 2, t = lane & 3;
+  const int H = p.cache.kv_heads;
+  const unsigned full = 0xffffffffu;
+
+  // This block's run of units, and the sequence it starts in (every warp for itself).
+  int64_t total = 0;
+  for (int b = lane; b < p.n_seqs; b += 32) {
+    const SeqWork s = seq_work<Sh::kRows>(a, b);
+    total += s.units * s.tiles * H;
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(full, total, o);
+  const int64_t quota = max(static_cast<int64_t>(a.min_units), (total + gridDim.x - 1) / gridDim.x);
+  int64_t cur = quota * blockIdx.x;
+  const int64_t end = min(cur + quota, total);
+  if (cur >= end) return;
+  int seq = 0;
+  int64_t base = 0;  // first unit of seq
+  for (int b0 = 0;; b0 += 32) {
+    int64_t mine = 0;
+    if (b0 + lane < p.n_seqs) {
+      const SeqWork s = seq_work<Sh::kRows>(a, b0 + lane);
+      mine = s.units * s.tiles * H;
+    }
+    int64_t sum = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t x = __shfl_up_sync(full, sum, o);
+      if (lane >= o) sum += x;
+    }
+    const unsigned past = __ballot_sync(full, base + sum > cur);
+    if (past) {
+      const int k = __ffs(past) - 1;
+      seq = b0 + k;
+      base += __shfl_sync(full, sum - mine, k);
+      break;
+    }
+    base += __shfl_sync(full, sum, 31);
+  }
+
+  uint64_t* my_bars = bars + warp * NS;
+  uint8_t* my_ring = smem + warp * NS * L::kBlock;
+  if (lane < NS) mbar_init(&my_bars[lane], 1);
+  fence_mbarrier_init();
   __syncwarp();
-  auto block = [&](int64_t j) -> const uint8_t* {
-    const int64_t pi = j / p.cache.page_tokens;
-    if (pi >= p.table_stride) return nullptr;
-    const int64_t page = p.table[seq * p.table_stride + pi];
-    if (page < 0 || page >= p.cache.n_pages) return nullptr;
-    return kv_block<FMT, D>(p.cache, page, kvh, static_cast<int>(j % p.cache.page_tokens) / kKvBlockTokens);
-  };
-  float acc[D / 32], m, l;
-  attend_row<D>(
-      static_cast<int64_t>(ctx) + T,
-      [&](int64_t j) { return (j < ctx || ((mask >> (j - ctx)) & 1)) && block(j) != nullptr; },
-      [&](int64_t j) {
-        const uint8_t* b = block(j);
-        float s = 0.f;
-        for (int d = 0; d < D; ++d) s = fmaf(qs[warp][d], kv_value<FMT, D>(b, false, j % kKvBlockTokens, d), s);
-        return s * p.scale * kLog2e;
-      },
-      [&](int64_t j, int d) { return kv_value<FMT, D>(block(j), true, j % kKvBlockTokens, d); }, acc, m, l);
-  store_row<D>(static_cast<__half*>(p.out.ptr) + token * p.out.token_stride + head * p.out.head_stride,
-               p.lse ? p.lse + token * p.q_heads + head : nullptr, acc, m, l);
+  int n_done = 0;  // units that this warp's ring has taken
+  bool dead = false;
+  float* slots = reinterpret_cast<float*>(p.ws + kWsHeaderBytes + 4 * kMaxBlocks);
+  int* counters = reinterpret_cast<int*>(p.ws + kWsHeaderBytes);
+
+  while (cur < end) {
+    const SeqWork sw = seq_work<Sh::kRows>(a, seq);
+    const int64_t in_seq = cur - base, per_seq = sw.units * sw.tiles * H;
+    if (in_seq >= per_seq) {
+      base += per_seq;
+      ++seq;
+      continue;
+    }
+    const int64_t item = in_seq / sw.units;
+    const int64_t u0 = in_seq - item * sw.units, u1 = min(sw.units, u0 + (end - cur));
+    const int head = static_cast<int>(item / sw.tiles), tile = static_cast<int>(item - static_cast<int64_t>(head) * sw.tiles);
+    const int R = sw.T * a.G, row0 = tile * Sh::kRows;
+    const int64_t q0 = p.cu_q[seq];
+    const int ctx = sw.ctx, all = ctx + sw.T;
+
+    // ---- this warp's units: u0 + warp + W * k
+    const int n_mine = static_cast<int>((u1 - u0 - warp + W - 1) / W);
+    int page_of = -1;  // lane l: the page of unit 32 * floor(k / 32) + l
+    uint32_t have = 0;  // stages with a unit whose page exists
+    auto prefetch = [&](int k) {
+      if ((k & 31) == 0) {
+        const int64_t u = u0 + warp + static_cast<int64_t>(W) * (k + lane);
+        const int64_t pi = (u * kKvBlockTokens) >> a.page_shift;
+        page_of = -1;
+        if (k + lane < n_mine && pi < p.table_stride) page_of = __ldg(p.table + seq * p.table_stride + pi);
+        if (page_of >= p.cache.n_pages) page_of = -1;
+      }
+      const int page = __shfl_sync(full, page_of, k & 31);
+      const int st = (n_done + k) % NS;
+      have = page >= 0 ? have | 1u << st : have & ~(1u << st);
+      if (page >= 0 && lane == 0) {
+        const int64_t u = u0 + warp + static_cast<int64_t>(W) * k;
+        const int blk = static_cast<int>(u & ((p.cache.page_tokens >> 4) - 1));
+        mbar_arrive_expect_tx(&my_bars[st], L::kBlock);
+        bulk_load(my_ring + st * L::kBlock, kv_block<FMT, D>(p.cache, page, head, blk), L::kBlock, &my_bars[st]);
+      } else if (page < 0 && lane == 0) {
+        mbar_arrive(&my_bars[st]);
+      }
+    };
+    for (int k = 0; k < NS && k < n_mine; ++k) prefetch(k);
+
+    // ---- Q fragments and masks of the row tile
+    for (int i = tid; i < MT * KS * 32; i += Sh::kThreads) {
+      const int ln = i & 31, ks = (i >> 5) % KS, mt = i / (32 * KS);
+      const int d = C::q_at(ks, ln & 3);
+      uint2 lo = make_uint2(0u, 0u), hi = make_uint2(0u, 0u);
+      auto row_q = [&](int r) -> uint2 {
+        if (r >= R) return make_uint2(0u, 0u);
+        const int tok = r / a.G;
+        const __half* q = static_cast<const __half*>(p.q.ptr) + (q0 + tok) * p.q.token_stride +
+                          (head * a.G + r - tok * a.G) * p.q.head_stride;
+        return __ldg(reinterpret_cast<const uint2*>(q + d));
+      };
+      lo = row_q(row0 + 16 * mt + (ln >> 2));
+      hi = row_q(row0 + 16 * mt + (ln >> 2) + 8);
+      s_q[i] = make_uint4(lo.x, hi.x, lo.y, hi.y);
+    }
+    for (int i = tid; i < Sh::kRows; i += Sh::kThreads) {
+      const int tok = (row0 + i) / a.G;
+      uint64_t m = 0;
+      if (row0 + i < R) m = p.masks ? p.masks[q0 + tok] : (~0ull >> (63 - tok));
+      s_mask[i] = m;
+    }
+    __syncthreads();
+
+    const float sl = p.scale * kLog2e;
+    float o[MT][NB][4], m[MT][2], l[MT][2];
+#pragma unroll
+    for (int i = 0; i < MT; ++i) {
+#pragma unroll
+      for (int n = 0; n < NB; ++n)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) o[i][n][c] = 0.f;
+      m[i][0] = m[i][1] = -INFINITY;
+      l[i][0] = l[i][1] = 0.f;
+    }
+
+    for (int k = 0; k < n_mine; ++k) {
+      const int st = (n_done + k) % NS;
+      if (!dead && !mbar_wait_bounded(&my_bars[st], ((n_done + k) / NS) & 1)) {
+        if (lane == 0) atomicOr(reinterpret_cast<int*>(p.ws), kErrTree);
+        dead = true;
+      }
+      dead = __any_sync(full, dead);
+      if (!dead && ((have >> st) & 1)) {
+        const uint8_t* blk = my_ring + st * L::kBlock;
+        const int64_t pos0 = (u0 + warp + static_cast<int64_t>(W) * k) * kKvBlockTokens;
+        const bool edge = pos0 + kKvBlockTokens > ctx;  // some positions are drafted, or past the end
+        // ---- S
+        float s[MT][2][4];
+#pragma unroll
+        for (int i = 0; i < MT; ++i)
+#pragma unroll
+          for (int nb = 0; nb < 2; ++nb)
+#pragma unroll
+            for (int c = 0; c < 4; ++c) s[i][nb][c] = 0.f;
+        {
+          uint32_t kw[2][C::kKw];
+          C::load_k(blk, g, t, kw[0]);
+          C::load_k(blk, 8 + g, t, kw[1]);
+          if constexpr (FMT == QGEMV_KV_Q4_0) {
+#pragma unroll
+            for (int grp = 0; grp < D / 32; ++grp) {
+              float part[MT][2][4];
+#pragma unroll
+              for (int i = 0; i < MT; ++i)
+#pragma unroll
+                for (int nb = 0; nb < 2; ++nb)
+#pragma unroll
+                  for (int c = 0; c < 4; ++c) part[i][nb][c] = 0.f;
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                const int ks = 2 * grp + h;
+                uint32_t b[2][2];
+                C::k_frag(kw[0], ks, b[0][0], b[0][1]);
+                C::k_frag(kw[1], ks, b[1][0], b[1][1]);
+#pragma unroll
+                for (int i = 0; i < MT; ++i) {
+                  const uint4 qa = s_q[(i * KS + ks) * 32 + lane];
+                  mma16816(part[i][0], qa, b[0][0], b[0][1]);
+                  mma16816(part[i][1], qa, b[1][0], b[1][1]);
+                }
+              }
+#pragma unroll
+              for (int nb = 0; nb < 2; ++nb) {
+                const __half* ksc = reinterpret_cast<const __half*>(blk + L::kKs) + (8 * nb + 2 * t) * (D / 32) + grp;
+                const float a0 = __half2float(ksc[0]) * sl, a1 = __half2float(ksc[D / 32]) * sl;
+#pragma unroll
+                for (int i = 0; i < MT; ++i) {
+                  s[i][nb][0] = fmaf(part[i][nb][0], a0, s[i][nb][0]);
+                  s[i][nb][1] = fmaf(part[i][nb][1], a1, s[i][nb][1]);
+                  s[i][nb][2] = fmaf(part[i][nb][2], a0, s[i][nb][2]);
+                  s[i][nb][3] = fmaf(part[i][nb][3], a1, s[i][nb][3]);
+                }
+              }
+            }
+          } else {
+#pragma unroll
+            for (int ks = 0; ks < KS; ++ks) {
+              uint32_t b[2][2];
+              C::k_frag(kw[0], ks, b[0][0], b[0][1]);
+              C::k_frag(kw[1], ks, b[1][0], b[1][1]);
+#pragma unroll
+              for (int i = 0; i < MT; ++i) {
+                const uint4 qa = s_q[(i * KS + ks) * 32 + lane];
+                mma16816(s[i][0], qa, b[0][0], b[0][1]);
+                mma16816(s[i][1], qa, b[1][0], b[1][1]);
+              }
+            }
+#pragma unroll
+            for (int nb = 0; nb < 2; ++nb) {
+              float2 ksc = make_float2(1.f, 1.f);
+              if constexpr (FMT == QGEMV_KV_INT8) ksc = *reinterpret_cast<const float2*>(blk + L::kKs + 4 * (8 * nb + 2 * t));
+              ksc.x *= sl, ksc.y *= sl;
+#pragma unroll
+              for (int i = 0; i < MT; ++i) s[i][nb][0] *= ksc.x, s[i][nb][1] *= ksc.y, s[i][nb][2] *= ksc.x, s[i][nb][3] *= ksc.y;
+            }
+          }
+        }
+        if (edge) {
+#pragma unroll
+          for (int i = 0; i < MT; ++i)
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              const uint64_t mask = s_mask[16 * i + g + 8 * (c >> 1)];
+#pragma unroll
+              for (int nb = 0; nb < 2; ++nb) {
+                const int64_t pos = pos0 + 8 * nb + 2 * t + (c & 1);
+                const bool on = pos < ctx || (pos < all && ((mask >> (pos - ctx)) & 1));
+                if (!on) s[i][nb][c] = -INFINITY;
+              }
+            }
+        }
+        // ---- scales of V and the reference
+        float vs[2][2][FMT == QGEMV_KV_Q4_0 ? D / 32 : 1], lv[2][2];
+#pragma unroll
+        for (int nb = 0; nb < 2; ++nb)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const int tok = 8 * nb + 2 * t + e;
+            if constexpr (FMT == QGEMV_KV_F16) {
+              vs[nb][e][0] = 1.f, lv[nb][e] = 0.f;
+            } else if constexpr (FMT == QGEMV_KV_INT8) {
+              vs[nb][e][0] = *reinterpret_cast<const float*>(blk + L::kVs + 4 * tok);
+              lv[nb][e] = lg2(fmaxf(vs[nb][e][0], 7.9e-31f));  // 2^-100
+            } else {
+              const __half* v = reinterpret_cast<const __half*>(blk + L::kVs) + tok * (D / 32);
+              float top = 7.9e-31f;
+#pragma unroll
+              for (int x = 0; x < D / 32; ++x) {
+                vs[nb][e][x] = __half2float(v[x]);
+                top = fmaxf(top, fabsf(vs[nb][e][x]));
+              }
+              lv[nb][e] = lg2(top);
+            }
+          }
+        bool grow = false;
+#pragma unroll
+        for (int i = 0; i < MT; ++i)
+#pragma unroll
+          for (int nb = 0; nb < 2; ++nb)
+#pragma unroll
+            for (int c = 0; c < 4; ++c) grow |= s[i][nb][c] + lv[nb][c & 1] > m[i][c >> 1] + kLazyT;
+        if (__any_sync(full, grow)) {
+#pragma unroll
+          for (int i = 0; i < MT; ++i)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              float top = fmaxf(fmaxf(s[i][0][2 * h] + lv[0][0], s[i][0][2 * h + 1] + lv[0][1]),
+                                fmaxf(s[i][1][2 * h] + lv[1][0], s[i][1][2 * h + 1] + lv[1][1]));
+              top = fmaxf(top, __shfl_xor_sync(full, top, 1));
+              top = fmaxf(top, __shfl_xor_sync(full, top, 2));
+              const float mn = fmaxf(m[i][h], top);
+              const float f = m[i][h] == -INFINITY ? 0.f : ex2(m[i][h] - mn);
+              m[i][h] = mn;
+              l[i][h] *= f;
+#pragma unroll
+              for (int n = 0; n < NB; ++n) o[i][n][2 * h] *= f, o[i][n][2 * h + 1] *= f;
+            }
+        }
+        // ---- P (in place of S); l takes p itself
+#pragma unroll
+        for (int i = 0; i < MT; ++i)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const float ref = m[i][h] == -INFINITY ? 0.f : m[i][h];
+#pragma unroll
+            for (int nb = 0; nb < 2; ++nb)
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                const float x = ex2(s[i][nb][2 * h + e] - ref);
+                l[i][h] += x;
+                s[i][nb][2 * h + e] = x;
+              }
+          }
+        // p * scale(v), 0 where p is masked whatever the scale holds
+        auto weights = [&](int i, int x) -> uint4 {
+          float w[2][4];
+#pragma unroll
+          for (int nb = 0; nb < 2; ++nb)
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              w[nb][c] = FMT == QGEMV_KV_F16 ? s[i][nb][c] : s[i][nb][c] * vs[nb][c & 1][x];
+              if (FMT != QGEMV_KV_F16 && edge && s[i][nb][c] == 0.f) w[nb][c] = 0.f;
+            }
+          return make_uint4(half_pair(w[0][0], w[0][1]), half_pair(w[0][2], w[0][3]), half_pair(w[1][0], w[1][1]),
+                            half_pair(w[1][2], w[1][3]));
+        };
+        // ---- O
+        uint32_t vw[4 * L::kRow / 32];
+        C::load_v(blk, g, t, vw);
+        if constexpr (FMT == QGEMV_KV_Q4_0) {
+#pragma unroll
+          for (int grp = 0; grp < D / 32; ++grp) {
+            uint4 pa[MT];
+#pragma unroll
+            for (int i = 0; i < MT; ++i) pa[i] = weights(i, grp);
+#pragma unroll
+            for (int n = 0; n < 4; ++n) {
+              uint32_t b0, b1;
+              C::v_frag(vw, 4 * grp + n, b0, b1);
+#pragma unroll
+              for (int i = 0; i < MT; ++i) mma16816(o[i][4 * grp + n], pa[i], b0, b1);
+            }
+          }
+        } else {
+          uint4 pa[MT];
+#pragma unroll
+          for (int i = 0; i < MT; ++i) pa[i] = weights(i, 0);
+          if (FMT == QGEMV_KV_F16 && edge) {
+            // fp16 values of positions past the end are whatever the page
+            // holds: zero.  Infinities and NaN of drafted tokens reach the rows
+            // that see them through a product of 0s and 1s instead.
+            const uint32_t k01 = (pos0 + 2 * t < all ? 0xffffu : 0u) | (pos0 + 2 * t + 1 < all ? 0xffff0000u : 0u);
+            const uint32_t k23 = (pos0 + 2 * t + 8 < all ? 0xffffu : 0u) | (pos0 + 2 * t + 9 < all ? 0xffff0000u : 0u);
+#pragma unroll
+            for (int n = 0; n < NB; ++n) {
+              uint32_t b0, b1;
+              C::v_frag(vw, n, b0, b1);
+              b0 &= k01, b1 &= k23;
+              const uint32_t bad0 = ((b0 & 0x7C007C00u) + 0x04000400u) & 0x80008000u;
+              const uint32_t bad1 = ((b1 & 0x7C007C00u) + 0x04000400u) & 0x80008000u;
+              if (__any_sync(full, (bad0 | bad1) != 0)) {
+                for (int kind = 0; kind < 3; ++kind) {  // NaN, +inf, -inf
+                  auto is = [&](uint32_t b) {
+                    uint32_t r = 0;
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                      const uint32_t x = (b >> (16 * h)) & 0xffffu;
+                      const bool on = kind == 0 ? (x & 0x7fffu) > 0x7C00u : x == (kind == 1 ? 0x7C00u : 0xFC00u);
+                      if (on) r |= 0x3C00u << (16 * h);
+                    }
+                    return r;
+                  };
+                  const uint32_t c0 = is(b0), c1 = is(b1);
+#pragma unroll
+                  for (int i = 0; i < MT; ++i) {
+                    auto sees = [&](int nb, int h) {
+                      uint32_t r = 0;
+#pragma unroll
+                      for (int e = 0; e < 2; ++e) {
+                        const int64_t pos = pos0 + 8 * nb + 2 * t + e;
+                        const uint64_t mask = s_mask[16 * i + g + 8 * h];
+                        if (pos < ctx || (pos < all && ((mask >> (pos - ctx)) & 1))) r |= 0x3C00u << (16 * e);
+                      }
+                      return r;
+                    };
+                    const uint4 va = make_uint4(sees(0, 0), sees(0, 1), sees(1, 0), sees(1, 1));
+                    float cnt[4] = {0.f, 0.f, 0.f, 0.f};
+                    mma16816(cnt, va, c0, c1);
+                    const float val = __int_as_float(kind == 0 ? 0x7fffffff : kind == 1 ? 0x7f800000 : 0xff800000);
+#pragma unroll
+                    for (int c = 0; c < 4; ++c)
+                      if (cnt[c] > 0.f) o[i][n][c] += val;
+                  }
+                }
+                if (bad0 & 0x8000u) b0 &= 0xffff0000u;
+                if (bad0 & 0x80000000u) b0 &= 0xffffu;
+                if (bad1 & 0x8000u) b1 &= 0xffff0000u;
+                if (bad1 & 0x80000000u) b1 &= 0xffffu;
+              }
+#pragma unroll
+              for (int i = 0; i < MT; ++i) mma16816(o[i][n], pa[i], b0, b1);
+            }
+          } else {
+#pragma unroll
+            for (int n = 0; n < NB; ++n) {
+              uint32_t b0, b1;
+              C::v_frag(vw, n, b0, b1);
+#pragma unroll
+              for (int i = 0; i < MT; ++i) mma16816(o[i][n], pa[i], b0, b1);
+            }
+          }
+        }
+      }
+      __syncwarp();
+      if (!dead && k + NS < n_mine) prefetch(k + NS);
+    }
+    // Copies of a warp that gave up must land before its ring is used again.
+    if (dead)
+      for (int s = 0; s < NS; ++s) __nanosleep(1000);
+    n_done += n_mine;
+
+    // ---- the warps' results, in warp order
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        l[i][h] += __shfl_xor_sync(full, l[i][h], 1);
+        l[i][h] += __shfl_xor_sync(full, l[i][h], 2);
+      }
+    __syncthreads();  // every ring is empty
+    float* s_o = reinterpret_cast<float*>(smem);
+#pragma unroll
+    for (int i = 0; i < MT; ++i) {
+#pragma unroll
+      for (int n = 0; n < NB; ++n)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) s_o[((warp * MT + i) * NB * 4 + n * 4 + c) * 32 + lane] = o[i][n][c];
+      if (t == 0) {
+        s_ml[warp * Sh::kRows + 16 * i + g] = make_float2(m[i][0], l[i][0]);
+        s_ml[warp * Sh::kRows + 16 * i + 8 + g] = make_float2(m[i][1], l[i][1]);
+      }
+    }
+    __syncthreads();
+
+    constexpr int kVec = Sh::kRows * D / 4;  // four lanes of a register: one row
+    constexpr int kPer = kVec / Sh::kThreads;
+    static_assert(kVec % Sh::kThreads == 0, "vectors per thread");
+    float4 acc[kPer];
+    float mm[kPer], ll[kPer];
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+      acc[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+      ll[j] = 0.f;
+    }
+    auto row_of = [&](int v) {  // v = (mt * NB * 4 + n * 4 + c) * 8 + g
+      return 16 * (v / (NB * 32)) + (v & 7) + 8 * ((v >> 4) & 1);
+    };
+    auto add = [&](int j, float pm, float pl, const float4& x, float top) {
+      const float f = pm == -INFINITY ? 0.f : ex2(pm - top);
+      ll[j] += pl * f;
+      // a part with nothing adds nothing (its O is 0, and f too)
+      acc[j].x += x.x * f, acc[j].y += x.y * f, acc[j].z += x.z * f, acc[j].w += x.w * f;
+    };
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+      const int v = tid + j * Sh::kThreads, row = row_of(v);
+      float top = -INFINITY;
+#pragma unroll
+      for (int w = 0; w < W; ++w) top = fmaxf(top, s_ml[w * Sh::kRows + row].x);
+      mm[j] = top;
+      const float ref = top == -INFINITY ? 0.f : top;
+#pragma unroll
+      for (int w = 0; w < W; ++w) {
+        const float2 ml = s_ml[w * Sh::kRows + row];
+        add(j, ml.x, ml.y, *reinterpret_cast<const float4*>(s_o + (w * kVec + v) * 4), ref);
+      }
+    }
+
+    bool mine_to_store = true;
+    if (u0 > 0 || u1 < sw.units) {  // shared with other blocks
+      const int64_t first_unit = cur - u0;
+      const int cf = static_cast<int>(first_unit / quota), cl = static_cast<int>((first_unit + sw.units - 1) / quota);
+      float* mine = slots + (2 * blockIdx.x + (u0 == 0 ? 1 : 0)) * slot_floats(D);
+#pragma unroll
+      for (int j = 0; j < kPer; ++j) {
+        const int v = tid + j * Sh::kThreads;
+        *reinterpret_cast<float4*>(mine + 4 * v) = acc[j];
+        if ((v & ~7) % (NB * 32) == 0 || (v & ~7) % (NB * 32) == 16)  // one vector of each row
+          *reinterpret_cast<float2*>(mine + Sh::kRows * D + 2 * row_of(v)) = make_float2(mm[j], ll[j]);
+      }
+      __threadfence();
+      __syncthreads();
+      if (tid == 0) {
+        const int old = atomicAdd(&counters[cf], 1);
+        *s_last = old == cl - cf;
+        if (old == cl - cf) counters[cf] = 0;
+      }
+      __syncthreads();
+      mine_to_store = *s_last != 0;
+      if (mine_to_store) {
+        __threadfence();
+#pragma unroll
+        for (int j = 0; j < kPer; ++j) {
+          const int v = tid + j * Sh::kThreads, row = row_of(v);
+          auto part = [&](int b) { return slots + (2 * b + (b == cf ? 1 : 0)) * slot_floats(D); };
+          float top = -INFINITY;
+#pragma unroll 8
+          for (int b = cf; b <= cl; ++b) top = fmaxf(top, __ldcg(part(b) + Sh::kRows * D + 2 * row));
+          mm[j] = top;
+          ll[j] = 0.f;
+          acc[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+          const float ref = top == -INFINITY ? 0.f : top;
+#pragma unroll 8
+          for (int b = cf; b <= cl; ++b) {
+            const float2 ml = __ldcg(reinterpret_cast<const float2*>(part(b) + Sh::kRows * D + 2 * row));
+            add(j, ml.x, ml.y, __ldcg(reinterpret_cast<const float4*>(part(b) + 4 * v)), ref);
+          }
+        }
+      }
+    }
+    if (mine_to_store) {  // uniform
+      __half* s_out = reinterpret_cast<__half*>(smem + W * Sh::kRows * D * 4);
+#pragma unroll
+      for (int j = 0; j < kPer; ++j) {
+        const int v = tid + j * Sh::kThreads, row = row_of(v);
+        const int n = (v >> 5) % NB, c = (v >> 3) & 3;
+        const float inv = ll[j] == 0.f ? 0.f : 1.f / ll[j];
+        __half* dst = s_out + row * D;
+        dst[C::out_at(n, (c & 1) + 0)] = __float2half_rn(acc[j].x * inv);
+        dst[C::out_at(n, (c & 1) + 2)] = __float2half_rn(acc[j].y * inv);
+        dst[C::out_at(n, (c & 1) + 4)] = __float2half_rn(acc[j].z * inv);
+        dst[C::out_at(n, (c & 1) + 6)] = __float2half_rn(acc[j].w * inv);
+        const int64_t r = row0 + row;
+        if (p.lse && r < R && ((v & ~7) % (NB * 32) == 0 || (v & ~7) % (NB * 32) == 16)) {
+          const int tok = static_cast<int>(r) / a.G;
+          p.lse[(q0 + tok) * p.q_heads + head * a.G + r - tok * a.G] = ll[j] == 0.f ? -INFINITY : (mm[j] + log2f(ll[j])) * kLn2;
+        }
+      }
+      __syncthreads();
+      for (int i = tid; i < Sh::kRows * D / 8; i += Sh::kThreads) {
+        const int row = i / (D / 8), u = i % (D / 8), r = row0 + row;
+        if (r < R) {
+          const int tok = r / a.G;
+          __half* out = static_cast<__half*>(p.out.ptr) + (q0 + tok) * p.out.token_stride +
+                        (head * a.G + r - tok * a.G) * p.out.head_stride;
+          *reinterpret_cast<uint4*>(out + 8 * u) = *reinterpret_cast<const uint4*>(s_out + row * D + 8 * u);
+        }
+      }
+    }
+    fence_async_smem();  // the ring is written by copies again
+    __syncthreads();
+    cur += u1 - u0;
+  }
+}
+
+template <int FMT, int D, int MT>
+cudaError_t launch(const TreeArgs& a, cudaStream_t s) {
+  using Sh = TreeShape<FMT, D, MT>;
+  static_assert(Sh::kStages >= 2 && Sh::kBytes <= 227 * 1024, "shared memory");
+  static const cudaError_t attr =
+      cudaFuncSetAttribute(tree_kernel<FMT, D, MT>, cudaFuncAttributeMaxDynamicSharedMemorySize, Sh::kBytes);
+  if (attr != cudaSuccess) return attr;
+  static const int sms = [] {
+    int dev = 0, n = 0;
+    cudaGetDevice(&dev);
+    cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
+    return n;
+  }();
+  if (sms <= 0) return cudaErrorInvalidDevice;
+  tree_kernel<FMT, D, MT><<<sms < kMaxBlocks ? sms : kMaxBlocks, Sh::kThreads, Sh::kBytes, s>>>(a);
+  return cudaGetLastError();
 }
 
 }  // namespace
 
+int64_t tree_ws_bytes(int64_t, int, int head_dim) {
+  return 4 * kMaxBlocks + 2 * kMaxBlocks * slot_floats(head_dim) * static_cast<int64_t>(sizeof(float));
+}
+
 cudaError_t launch_attn_tree(const TreeParams& p, cudaStream_t s) {
-  const int64_t rows = p.n_q * p.q_heads;
-  const unsigned grid = static_cast<unsigned>((rows + kThreads / 32 - 1) / (kThreads / 32));
+  TreeArgs a;
+  a.p = p;
+  a.G = p.q_heads / p.cache.kv_heads;
+  a.page_shift = 0;
+  while ((1 << a.page_shift) < p.cache.page_tokens) ++a.page_shift;
+  a.min_units = 16;
+  const bool wide = static_cast<int64_t>(p.max_new) * a.G > 16;  // 32-row tiles
+  auto by_rows = [&](auto fmt, auto d) {
+    constexpr int F = decltype(fmt)::value, D = decltype(d)::value;
+    return wide ? launch<F, D, 2>(a, s) : launch<F, D, 1>(a, s);
+  };
   auto by_dim = [&](auto fmt) {
-    constexpr int F = decltype(fmt)::value;
-    if (p.cache.head_dim == 64) tree_row_kernel<F, 64><<<grid, kThreads, 0, s>>>(p);
-    else tree_row_kernel<F, 128><<<grid, kThreads, 0, s>>>(p);
+    return p.cache.head_dim == 64 ? by_rows(fmt, std::integral_constant<int, 64>())
+                                  : by_rows(fmt, std::integral_constant<int, 128>());
   };
   switch (p.cache.format) {
-    case QGEMV_KV_F16: by_dim(std::integral_constant<int, QGEMV_KV_F16>()); break;
-    case QGEMV_KV_INT8: by_dim(std::integral_constant<int, QGEMV_KV_INT8>()); break;
-    default: by_dim(std::integral_constant<int, QGEMV_KV_Q4_0>());
+    case QGEMV_KV_F16: return by_dim(std::integral_constant<int, QGEMV_KV_F16>());
+    case QGEMV_KV_INT8: return by_dim(std::integral_constant<int, QGEMV_KV_INT8>());
+    default: return by_dim(std::integral_constant<int, QGEMV_KV_Q4_0>());
   }
-  return cudaGetLastError();
 }
 
 }  // namespace qgemv
