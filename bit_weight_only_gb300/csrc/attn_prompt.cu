@@ -27,7 +27,7 @@
 //     epilogue gives it to the rows that see it.
 // Every wait is bounded; on a timeout the block records the error, waits for
 // its own copies and MMAs, frees tensor memory and returns.
-#include "attn_row.cuh"
+#include "kv_layout.cuh"
 #include "tc_common.cuh"
 
 namespace qgemv {

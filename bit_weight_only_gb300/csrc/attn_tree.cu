@@ -23,7 +23,7 @@
 // row tiles that several thread blocks share go to the workspace, and the last
 // of them to arrive adds all of them in order (so the result does not depend
 // on who is last) and clears the counter.
-#include "attn_row.cuh"
+#include "kv_layout.cuh"
 #include "tc_common.cuh"
 
 namespace qgemv {
@@ -90,28 +90,31 @@ template <int D>
 struct Codes<QGEMV_KV_F16, D> {
   using L = KvLayout<QGEMV_KV_F16, D>;
   static constexpr int kKw = D / 8;
-  __device__ static int q_at(int ks, int t) { return 32 * (ks >> 1) + 8 * t + 4 * (ks & 1); }
-  __device__ static int out_at(int nb, int n) { return 64 * (nb >> 3) + 8 * n + (nb & 7); }
-  __device__ static void load_k(const uint8_t* b, int tok, int t, uint32_t (&w)[kKw]) {
+  static constexpr int kQ2 = 8;  // from the first pair of an operand's k to the second
+  __device__ static int q_at(int ks, int t) { return 16 * ks + 2 * t; }
+  __device__ static int out_at(int nb, int n) { return 8 * nb + n; }
+  // ldmatrix: lane l gives the address of row l & 7 of matrix l >> 3
+  __device__ static void load_k(const uint8_t* b, int tok, int lane, uint32_t (&w)[kKw]) {
+    tok += (lane & 7) - (lane >> 2);  // of the eight tokens, this lane's row
 #pragma unroll
-    for (int i = 0; i < D / 32; ++i) *reinterpret_cast<uint4*>(&w[4 * i]) = lds128(b + L::k_off(tok, 64 * i + 16 * t));
+    for (int i = 0; i < D / 32; ++i)
+      asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+                   : "=r"(w[4 * i]), "=r"(w[4 * i + 1]), "=r"(w[4 * i + 2]), "=r"(w[4 * i + 3])
+                   : "r"(smem_u32(b + L::k_off(tok, 64 * i + 16 * (lane >> 3)))));
   }
   __device__ static void k_frag(const uint32_t (&w)[kKw], int ks, uint32_t& b0, uint32_t& b1) {
     b0 = w[2 * ks], b1 = w[2 * ks + 1];
   }
-  // V: [unit][token pair 0, 1][token][word]
-  __device__ static void load_v(const uint8_t* b, int g, int t, uint32_t (&w)[4 * (D / 16)]) {
+  // matrices: tokens 0-7 and 8-15 of columns 16i .., then of 16i + 8 ..
+  __device__ static void load_v(const uint8_t* b, int, int lane, uint32_t (&w)[4 * (D / 16)]) {
 #pragma unroll
-    for (int u = 0; u < D / 64; ++u)
-#pragma unroll
-      for (int k = 0; k < 4; ++k)
-        *reinterpret_cast<uint4*>(&w[16 * u + 4 * k]) = lds128(b + L::v_off(2 * t + (k & 1) + 8 * (k >> 1), 128 * u + 16 * g));
+    for (int i = 0; i < D / 16; ++i)
+      asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                   : "=r"(w[4 * i]), "=r"(w[4 * i + 1]), "=r"(w[4 * i + 2]), "=r"(w[4 * i + 3])
+                   : "r"(smem_u32(b + L::v_off(lane & 15, 32 * i + 16 * (lane >> 4)))));
   }
   __device__ static void v_frag(const uint32_t (&w)[4 * (D / 16)], int nb, uint32_t& b0, uint32_t& b1) {
-    const int at = 16 * (nb >> 3) + ((nb & 7) >> 1);
-    const uint32_t sel = nb & 1 ? 0x7632u : 0x5410u;
-    b0 = prmt(w[at], w[at + 4], sel);
-    b1 = prmt(w[at + 8], w[at + 12], sel);
+    b0 = w[2 * nb], b1 = w[2 * nb + 1];
   }
 };
 
@@ -119,9 +122,11 @@ template <int D>
 struct Codes<QGEMV_KV_INT8, D> {
   using L = KvLayout<QGEMV_KV_INT8, D>;
   static constexpr int kKw = D / 16;
+  static constexpr int kQ2 = 2;
   __device__ static int q_at(int ks, int t) { return 64 * (ks >> 2) + 16 * t + 4 * (ks & 3); }
   __device__ static int out_at(int nb, int n) { return D / 8 * n + nb; }
-  __device__ static void load_k(const uint8_t* b, int tok, int t, uint32_t (&w)[kKw]) {
+  __device__ static void load_k(const uint8_t* b, int tok, int lane, uint32_t (&w)[kKw]) {
+    const int t = lane & 3;
 #pragma unroll
     for (int h = 0; h < D / 64; ++h) *reinterpret_cast<uint4*>(&w[4 * h]) = lds128(b + L::k_off(tok, 64 * h + 16 * t));
   }
@@ -129,7 +134,8 @@ struct Codes<QGEMV_KV_INT8, D> {
     b0 = i8_pair<0x4140>(w[ks]), b1 = i8_pair<0x4342>(w[ks]);
   }
   // V: [token][word]
-  __device__ static void load_v(const uint8_t* b, int g, int t, uint32_t (&w)[4 * (D / 32)]) {
+  __device__ static void load_v(const uint8_t* b, int g, int lane, uint32_t (&w)[4 * (D / 32)]) {
+    const int t = lane & 3;
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       const uint8_t* at = b + L::v_off(2 * t + (k & 1) + 8 * (k >> 1), D / 8 * g);
@@ -151,10 +157,11 @@ template <int D>
 struct Codes<QGEMV_KV_Q4_0, D> {
   using L = KvLayout<QGEMV_KV_Q4_0, D>;
   static constexpr int kKw = D / 32;
+  static constexpr int kQ2 = 2;
   __device__ static int q_at(int ks, int t) { return 32 * (ks >> 1) + 8 * t + 4 * (ks & 1); }
   __device__ static int out_at(int nb, int n) { return 32 * (nb >> 2) + 4 * n + (nb & 3); }
-  __device__ static void load_k(const uint8_t* b, int tok, int t, uint32_t (&w)[kKw]) {
-    const uint8_t* at = b + L::k_off(tok, D / 8 * t);
+  __device__ static void load_k(const uint8_t* b, int tok, int lane, uint32_t (&w)[kKw]) {
+    const uint8_t* at = b + L::k_off(tok, D / 8 * (lane & 3));
     if constexpr (D == 128) *reinterpret_cast<uint4*>(w) = lds128(at);
     else *reinterpret_cast<uint2*>(w) = *reinterpret_cast<const uint2*>(at);
   }
@@ -164,7 +171,8 @@ struct Codes<QGEMV_KV_Q4_0, D> {
     else b0 = q4_pair<0>(x), b1 = q4_pair<1>(x);
   }
   // V: [token][group pair]
-  __device__ static void load_v(const uint8_t* b, int g, int t, uint32_t (&w)[4 * (D / 64)]) {
+  __device__ static void load_v(const uint8_t* b, int g, int lane, uint32_t (&w)[4 * (D / 64)]) {
+    const int t = lane & 3;
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       const uint8_t* at = b + L::v_off(2 * t + (k & 1) + 8 * (k >> 1), D / 16 * g);
@@ -348,7 +356,7 @@ __global__ void __launch_bounds__(TreeShape<FMT, D, MT>::kThreads, 1) tree_kerne
         const int tok = r / a.G;
         const __half* q = static_cast<const __half*>(p.q.ptr) + (q0 + tok) * p.q.token_stride +
                           (head * a.G + r - tok * a.G) * p.q.head_stride;
-        return __ldg(reinterpret_cast<const uint2*>(q + d));
+        return make_uint2(__ldg(reinterpret_cast<const unsigned*>(q + d)), __ldg(reinterpret_cast<const unsigned*>(q + d + C::kQ2)));
       };
       lo = row_q(row0 + 16 * mt + (ln >> 2));
       hi = row_q(row0 + 16 * mt + (ln >> 2) + 8);
@@ -395,8 +403,8 @@ __global__ void __launch_bounds__(TreeShape<FMT, D, MT>::kThreads, 1) tree_kerne
             for (int c = 0; c < 4; ++c) s[i][nb][c] = 0.f;
         {
           uint32_t kw[2][C::kKw];
-          C::load_k(blk, g, t, kw[0]);
-          C::load_k(blk, 8 + g, t, kw[1]);
+          C::load_k(blk, g, lane, kw[0]);
+          C::load_k(blk, 8 + g, lane, kw[1]);
           if constexpr (FMT == QGEMV_KV_Q4_0) {
 #pragma unroll
             for (int grp = 0; grp < D / 32; ++grp) {
@@ -547,7 +555,7 @@ __global__ void __launch_bounds__(TreeShape<FMT, D, MT>::kThreads, 1) tree_kerne
         };
         // ---- O
         uint32_t vw[4 * L::kRow / 32];
-        C::load_v(blk, g, t, vw);
+        C::load_v(blk, g, lane, vw);
         if constexpr (FMT == QGEMV_KV_Q4_0) {
 #pragma unroll
           for (int grp = 0; grp < D / 32; ++grp) {

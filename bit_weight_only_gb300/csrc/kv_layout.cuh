@@ -11,16 +11,18 @@
 // matrix operands are read from shared memory by the widest loads without
 // bank conflicts (lane = 4g + t; one MMA step takes 4 values of k from each
 // of the four t and column n from each of the eight g):
-//   * K: lane (g, t) reads token g.  fp16: 16-byte units t, 4 + t, ..
-//     (values 32i + 8t ..); INT8: units t (values 64h + 16t ..), codes + 128;
-//     Q4_0: one cell of d/32 words, word i the 8 values 32i + 8t .., in
-//     nibble order 0 2 4 6 1 3 5 7 (so that masking a word yields the
-//     neighbouring pairs).  Rows of 128 bytes and more swap their 64-byte
-//     halves for odd tokens.
+//   * fp16, K and V: chunks of 64 values, each 16 rows of 128 bytes in the
+//     128-byte swizzle (16-byte unit u of token r at u ^ (r & 7)): what the
+//     tensor cores read, as a descriptor operand or by ldmatrix.
+//   * K: lane (g, t) reads token g.  INT8: 16-byte units t (values 64h + 16t
+//     ..), codes + 128; Q4_0: one cell of d/32 words, word i the 8 values 32i
+//     + 8t .., in nibble order 0 2 4 6 1 3 5 7 (so that masking a word yields
+//     neighbouring pairs).  Rows of 128 bytes swap their 64-byte halves for
+//     odd tokens.
 //   * V: lane (g, t) reads tokens 2t, 2t + 1, 2t + 8, 2t + 9 at column cell
-//     g.  fp16: units g, 8 + g; INT8: values (d/8) g ..; Q4_0: one halfword
-//     of each group i, the values 32i + 4g ...  Byte bits 5, 6 of a region
-//     are xored with the token's bits 1, 2.
+//     g.  INT8: values (d/8) g ..; Q4_0: one halfword of each group i, the
+//     values 32i + 4g ...  Byte bits 5, 6 of a region are xored with the
+//     token's bits 1, 2.
 // Scales: INT8 fp32 [16]; Q4_0 fp16 [16][d/32].
 #pragma once
 
@@ -43,10 +45,16 @@ struct KvLayout {
   static constexpr int kBlock = kVs + kKvBlockTokens * kScaleRow;
   static_assert(kBlock % 128 == 0 && kV % 128 == 0, "blocks and regions start on bank lines");
 
+  // Byte c of a token's row, K and V.
+  __host__ __device__ static constexpr int f16_off(int tok, int c) {
+    return (c >> 7) * 2048 + tok * 128 + ((c & 127) ^ ((tok & 7) << 4));
+  }
   __host__ __device__ static constexpr int k_off(int tok, int c) {
+    if (FMT == QGEMV_KV_F16) return f16_off(tok, c);
     return kRow >= 128 ? (tok * kRow + c) ^ ((tok & 1) << 6) : tok * kRow + c;
   }
   __host__ __device__ static constexpr int v_off(int tok, int c) {
+    if (FMT == QGEMV_KV_F16) return kV + f16_off(tok, c);
     return kV + ((tok * kRow + c) ^ (((tok >> 1) & 3) << 5));
   }
 };
@@ -62,50 +70,5 @@ __device__ __forceinline__ uint8_t* kv_block(const qgemv_kv_cache& c, int64_t pa
   const int per = c.page_tokens / kKvBlockTokens;
   return static_cast<uint8_t*>(c.pages) + ((page * c.kv_heads + head) * per + blk) * KvLayout<FMT, D>::kBlock;
 }
-
-// The value that a block's codes stand for: (token of the block, element d
-// of the head), element by element.
-template <int FMT, int D>
-__device__ __forceinline__ float kv_value(const uint8_t* b, bool v, int tok, int d) {
-  using L = KvLayout<FMT, D>;
-  if constexpr (FMT == QGEMV_KV_F16) {
-    return __half2float(*reinterpret_cast<const __half*>(b + (v ? L::v_off(tok, 2 * d) : L::k_off(tok, 2 * d))));
-  } else if constexpr (FMT == QGEMV_KV_INT8) {
-    const int u = b[v ? L::v_off(tok, d) : L::k_off(tok, d)];
-    return static_cast<float>(u - 128) * reinterpret_cast<const float*>(b + (v ? L::kVs : L::kKs))[tok];
-  } else {
-    const int grp = d >> 5, e = d & 31;
-    int byte, nib;
-    if (v) {
-      byte = L::v_off(tok, (e >> 2) * (D / 16) + 2 * grp + ((e & 3) >> 1));
-      nib = e & 1;
-    } else {
-      const int j = ((e & 7) >> 1) + 4 * (e & 1);  // nibble of value e & 7
-      byte = L::k_off(tok, (e >> 3) * (D / 8) + 4 * grp + (j >> 1));
-      nib = j & 1;
-    }
-    const int q = (b[byte] >> (4 * nib)) & 15;
-    const __half s = reinterpret_cast<const __half*>(b + (v ? L::kVs : L::kKs))[tok * (D / 32) + grp];
-    return static_cast<float>(q - 8) * __half2float(s);
-  }
-}
-
-template <typename T>
-__device__ __forceinline__ float to_f32(T v);
-template <>
-__device__ __forceinline__ float to_f32<float>(float v) { return v; }
-template <>
-__device__ __forceinline__ float to_f32<__half>(__half v) { return __half2float(v); }
-template <>
-__device__ __forceinline__ float to_f32<__nv_bfloat16>(__nv_bfloat16 v) { return __bfloat162float(v); }
-
-template <typename T>
-__device__ __forceinline__ T from_f32(float v);
-template <>
-__device__ __forceinline__ float from_f32<float>(float v) { return v; }
-template <>
-__device__ __forceinline__ __half from_f32<__half>(float v) { return __float2half_rn(v); }
-template <>
-__device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
 
 }  // namespace qgemv

@@ -312,7 +312,7 @@ def _current(stream):
     if stream is not None:
         return stream
     import torch
-    return torch.cuda.current_stream().cuda_stream
+    return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
 
 
 class QGemv:
@@ -447,9 +447,15 @@ def prepare_x_int8(x, hadamard_block: int = 0, signs=None, stream=None):
 
 # --------------------------------------------------- cache and attention --
 
+_DTYPES = None  # torch dtype -> DT_*, filled on first use (torch is imported only where it is used)
+
+
 def _dtype_code(dtype) -> int:
-    import torch
-    code = {torch.float32: DT_F32, torch.float16: DT_F16, torch.bfloat16: DT_BF16}.get(dtype)
+    global _DTYPES
+    if _DTYPES is None:
+        import torch
+        _DTYPES = {torch.float32: DT_F32, torch.float16: DT_F16, torch.bfloat16: DT_BF16}
+    code = _DTYPES.get(dtype)
     if code is None:
         raise ValueError(f"rows are fp32, fp16 or bf16, not {dtype}")
     return code
@@ -457,16 +463,16 @@ def _dtype_code(dtype) -> int:
 
 def _rows(name, t, heads: int, head_dim: int):
     """(address, token stride, head stride) of a CUDA tensor [n, heads, head_dim], its values contiguous."""
-    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != head_dim or t.stride(2) != 1 or not t.is_cuda:
+    if t.shape[1:] != (heads, head_dim) or not t.is_cuda or t.stride(2) != 1:
         raise ValueError(f"{name} must be a CUDA tensor [n, {heads}, {head_dim}] with contiguous values, got "
                          f"{tuple(t.shape)} with strides {t.stride()} on {t.device}")
+    token, head, _ = t.stride()
     # the stride of a dimension of one element means nothing to torch
-    return (t.data_ptr(), t.stride(0) if t.shape[0] > 1 else heads * head_dim,
-            t.stride(1) if heads > 1 else head_dim)
+    return t.data_ptr(), token if t.shape[0] > 1 else heads * head_dim, head if heads > 1 else head_dim
 
 
 def _index(name, t, dtype, shape):
-    if t.dtype != dtype or tuple(t.shape) != shape or not t.is_contiguous() or not t.is_cuda:
+    if t.dtype != dtype or t.shape != shape or not t.is_cuda or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous CUDA {dtype} tensor of shape {shape}, got {t.dtype} "
                          f"{tuple(t.shape)} on {t.device}")
     return t.data_ptr()
