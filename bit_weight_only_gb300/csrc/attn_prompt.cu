@@ -187,7 +187,7 @@ prompt_kernel(const PromptArgs a, const __grid_constant__ CUtensorMap kmap, cons
     } else if (warp == 9) {
       // ---- MMAs
       if (lane == 0 && n_max > 0) {
-        constexpr uint32_t id_qk = mma_idesc(BF16, false, kKeys), id_pv = mma_idesc(BF16, true, D);
+        constexpr uint32_t id_qk = mma_idesc(BF16, false, false, kKeys), id_pv = mma_idesc(BF16, false, true, D);
         const uint32_t sq = smem_u32(smem + S::kQ), sk = smem_u32(smem + S::kK), sv = smem_u32(smem + S::kV);
         auto qk = [&](int i, int j) {
           const uint64_t da = sw128_desc(sq + i * S::kTile, 0, 1024);

@@ -1,11 +1,11 @@
 // attn_tree.cu -- attention of drafted tokens over the paged key/value cache
 // (qgemv_attn_tree).
 //
-// Rows of a sequence and key/value head: row = token * G + head of the group,
-// in tiles of 16 or 32.  The work is a list of units, one block of 16 cached
-// tokens for one row tile, ordered (sequence, head, row tile, block); every
-// thread block takes an equal run of it, so that sequences of any lengths
-// share the GPU evenly.  Within its run a warp takes every W-th unit:
+// Rows of a sequence and key/value head: row = token * G + head of the group.
+// tree_kernel takes up to 32 of them at a time, in tiles of 16 or 32, by
+// mma.sync; more go to attn_tree_wide.cu.  A unit is a block of 16 cached
+// tokens (tree_work.cuh); within a thread block's segment a warp takes every
+// W-th unit:
 //
 //   copy      one bulk copy into the warp's own ring of shared-memory stages
 //   S = Q K^T mma.m16n8k16 on the codes as fp16 (INT8 and Q4_0 codes are
@@ -18,68 +18,23 @@
 //             stays in [0, 2^8] whatever the scales are
 //   O += P V  the same instruction on V's codes
 //
-// A warp's O, m and l live in its registers.  At the end of a run's part of a
-// row tile the warps' results are added in warp order through shared memory;
-// row tiles that several thread blocks share go to the workspace, and the last
-// of them to arrive adds all of them in order (so the result does not depend
-// on who is last) and clears the counter.
-#include "kv_layout.cuh"
+// A warp's O, m and l live in its registers.  At the end of a segment the
+// warps' results are added in warp order through shared memory.
 #include "tc_common.cuh"
+#include "tree_work.cuh"
 
 namespace qgemv {
 namespace {
 
 constexpr int kErrTree = 32;
 constexpr float kLazyT = 8.f;
-constexpr int kMaxBlocks = 512;       // thread blocks of a call, at most
-constexpr int kMaxRows = 32;
 constexpr int kRingBytes = 200 * 1024;
-
-__host__ __device__ constexpr int64_t slot_floats(int D) { return static_cast<int64_t>(kMaxRows) * (D + 2); }
-
-__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
-  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(smem_u32(dst)),
-               "l"(src), "r"(bytes), "r"(smem_u32(bar))
-               : "memory");
-}
 
 // c += a . b: 16 x 16 . 16 x 8, fp16 in, fp32 sums.
 __device__ __forceinline__ void mma16816(float (&c)[4], const uint4& a, uint32_t b0, uint32_t b1) {
   asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
                : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
                : "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b0), "r"(b1));
-}
-
-__device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t s) { return __byte_perm(a, b, s); }
-__device__ __forceinline__ uint32_t hsub2(uint32_t a, uint32_t b) {
-  uint32_t r;
-  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-  return r;
-}
-__device__ __forceinline__ uint32_t hfma2(uint32_t a, uint32_t b, uint32_t c) {
-  uint32_t r;
-  asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
-  return r;
-}
-__device__ __forceinline__ uint32_t half_pair(float lo, float hi) { return cvt_pair<false>(lo, hi); }
-__device__ __forceinline__ float lg2(float x) {
-  float y;
-  asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
-// Codes to fp16 pairs.  INT8: bytes b0, b1 of w, stored + 128: 0x64 in the
-// high byte makes 1024 + code.
-template <int SEL>
-__device__ __forceinline__ uint32_t i8_pair(uint32_t w) {
-  return hsub2(prmt(w, 0x64646464u, SEL), 0x64806480u);  // - 1152
-}
-// Q4_0: nibbles N and N + 4 of w, minus 8.
-template <int N>
-__device__ __forceinline__ uint32_t q4_pair(uint32_t w) {
-  const uint32_t v = N >= 2 ? w >> 8 : w;
-  if (N & 1) return hfma2((v & 0x00F000F0u) | 0x64006400u, 0x2C002C00u, 0xD480D480u);  // (1024 + 16 q) / 16 - 72
-  return hsub2((v & 0x000F000Fu) | 0x64006400u, 0x64086408u);                          // 1024 + q - 1032
 }
 
 // Per format: words of K and V of a lane, and the fp16 pairs in them.
@@ -213,33 +168,6 @@ struct TreeShape {
   static constexpr int kBytes = kBars + kWarps * kStages * 8 + 16;
 };
 
-struct TreeArgs {
-  TreeParams p;
-  int G, page_shift, min_units;
-};
-
-struct SeqWork {
-  int64_t units;  // of one row tile
-  int tiles;      // row tiles of a head
-  int ctx, T;
-};
-
-template <int ROWS>
-__device__ __forceinline__ SeqWork seq_work(const TreeArgs& a, int b) {
-  const TreeParams& p = a.p;
-  SeqWork s;
-  const int64_t q0 = p.cu_q[b];
-  int64_t T = p.cu_q[b + 1] - q0;
-  if (q0 < 0 || T < 0) T = 0;
-  T = min(T, min(static_cast<int64_t>(kMaxDrafts), p.n_q - q0));
-  s.T = static_cast<int>(max(T, static_cast<int64_t>(0)));
-  s.ctx = max(0, p.ctx_lens[b]);
-  const int64_t n = min(static_cast<int64_t>(s.ctx) + s.T, p.table_stride << a.page_shift);
-  s.units = max(static_cast<int64_t>(1), (n + kKvBlockTokens - 1) / kKvBlockTokens);
-  s.tiles = (s.T * a.G + ROWS - 1) / ROWS;
-  return s;
-}
-
 template <int FMT, int D, int MT>
 __global__ void __launch_bounds__(TreeShape<FMT, D, MT>::kThreads, 1) tree_kernel(const TreeArgs a) {
   using Sh = TreeShape<FMT, D, MT>;
@@ -252,49 +180,12 @@ __global__ void __launch_bounds__(TreeShape<FMT, D, MT>::kThreads, 1) tree_kerne
   float2* s_ml = reinterpret_cast<float2*>(smem + Sh::kMl);
   uint64_t* s_mask = reinterpret_cast<uint64_t*>(smem + Sh::kMask);
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + Sh::kBars);
-  int* s_last = reinterpret_cast<int*>(bars + W * NS);
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int g = lane >> 2, t = lane & 3;
-  const int H = p.cache.kv_heads;
   const unsigned full = 0xffffffffu;
 
-  // This block's run of units, and the sequence it starts in (every warp for itself).
-  int64_t total = 0;
-  for (int b = lane; b < p.n_seqs; b += 32) {
-    const SeqWork s = seq_work<Sh::kRows>(a, b);
-    total += s.units * s.tiles * H;
-  }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(full, total, o);
-  const int64_t quota = max(static_cast<int64_t>(a.min_units), (total + gridDim.x - 1) / gridDim.x);
-  int64_t cur = quota * blockIdx.x;
-  const int64_t end = min(cur + quota, total);
-  if (cur >= end) return;
-  int seq = 0;
-  int64_t base = 0;  // first unit of seq
-  for (int b0 = 0;; b0 += 32) {
-    int64_t mine = 0;
-    if (b0 + lane < p.n_seqs) {
-      const SeqWork s = seq_work<Sh::kRows>(a, b0 + lane);
-      mine = s.units * s.tiles * H;
-    }
-    int64_t sum = mine;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int64_t x = __shfl_up_sync(full, sum, o);
-      if (lane >= o) sum += x;
-    }
-    const unsigned past = __ballot_sync(full, base + sum > cur);
-    if (past) {
-      const int k = __ffs(past) - 1;
-      seq = b0 + k;
-      base += __shfl_sync(full, sum - mine, k);
-      break;
-    }
-    base += __shfl_sync(full, sum, 31);
-  }
-
+  Cursor<Sh::kRows, kKvBlockTokens> work(a);
   uint64_t* my_bars = bars + warp * NS;
   uint8_t* my_ring = smem + warp * NS * L::kBlock;
   if (lane < NS) mbar_init(&my_bars[lane], 1);
@@ -302,23 +193,14 @@ __global__ void __launch_bounds__(TreeShape<FMT, D, MT>::kThreads, 1) tree_kerne
   __syncwarp();
   int n_done = 0;  // units that this warp's ring has taken
   bool dead = false;
-  float* slots = reinterpret_cast<float*>(p.ws + kWsHeaderBytes + 4 * kMaxBlocks);
-  int* counters = reinterpret_cast<int*>(p.ws + kWsHeaderBytes);
 
-  while (cur < end) {
-    const SeqWork sw = seq_work<Sh::kRows>(a, seq);
-    const int64_t in_seq = cur - base, per_seq = sw.units * sw.tiles * H;
-    if (in_seq >= per_seq) {
-      base += per_seq;
-      ++seq;
-      continue;
-    }
-    const int64_t item = in_seq / sw.units;
-    const int64_t u0 = in_seq - item * sw.units, u1 = min(sw.units, u0 + (end - cur));
-    const int head = static_cast<int>(item / sw.tiles), tile = static_cast<int>(item - static_cast<int64_t>(head) * sw.tiles);
-    const int R = sw.T * a.G, row0 = tile * Sh::kRows;
+  Segment sg;
+  while (work.next(a, sg)) {
+    const int64_t u0 = sg.u0, u1 = sg.u1;
+    const int seq = sg.seq, head = sg.head;
+    const int R = sg.T * a.G, row0 = sg.tile * Sh::kRows;
     const int64_t q0 = p.cu_q[seq];
-    const int ctx = sw.ctx, all = ctx + sw.T;
+    const int ctx = sg.ctx, all = ctx + sg.T;
 
     // ---- this warp's units: u0 + warp + W * k
     const int n_mine = static_cast<int>((u1 - u0 - warp + W - 1) / W);
@@ -705,49 +587,21 @@ __global__ void __launch_bounds__(TreeShape<FMT, D, MT>::kThreads, 1) tree_kerne
       }
     }
 
-    bool mine_to_store = true;
-    if (u0 > 0 || u1 < sw.units) {  // shared with other blocks
-      const int64_t first_unit = cur - u0;
-      const int cf = static_cast<int>(first_unit / quota), cl = static_cast<int>((first_unit + sw.units - 1) / quota);
-      float* mine = slots + (2 * blockIdx.x + (u0 == 0 ? 1 : 0)) * slot_floats(D);
+    if (sg.shared) {
+      float* mine = tree_slot(p, blockIdx.x, u0 == 0, D);
 #pragma unroll
       for (int j = 0; j < kPer; ++j) {
-        const int v = tid + j * Sh::kThreads;
-        *reinterpret_cast<float4*>(mine + 4 * v) = acc[j];
+        const int v = tid + j * Sh::kThreads, row = row_of(v);
+        const int n = (v >> 5) % NB, c = (v >> 3) & 3;
+        float* dst = mine + row * D;
+        dst[C::out_at(n, (c & 1) + 0)] = acc[j].x;
+        dst[C::out_at(n, (c & 1) + 2)] = acc[j].y;
+        dst[C::out_at(n, (c & 1) + 4)] = acc[j].z;
+        dst[C::out_at(n, (c & 1) + 6)] = acc[j].w;
         if ((v & ~7) % (NB * 32) == 0 || (v & ~7) % (NB * 32) == 16)  // one vector of each row
-          *reinterpret_cast<float2*>(mine + Sh::kRows * D + 2 * row_of(v)) = make_float2(mm[j], ll[j]);
+          *reinterpret_cast<float2*>(mine + kSlotRows * D + 2 * row) = make_float2(mm[j], ll[j]);
       }
-      __threadfence();
-      __syncthreads();
-      if (tid == 0) {
-        const int old = atomicAdd(&counters[cf], 1);
-        *s_last = old == cl - cf;
-        if (old == cl - cf) counters[cf] = 0;
-      }
-      __syncthreads();
-      mine_to_store = *s_last != 0;
-      if (mine_to_store) {
-        __threadfence();
-#pragma unroll
-        for (int j = 0; j < kPer; ++j) {
-          const int v = tid + j * Sh::kThreads, row = row_of(v);
-          auto part = [&](int b) { return slots + (2 * b + (b == cf ? 1 : 0)) * slot_floats(D); };
-          float top = -INFINITY;
-#pragma unroll 8
-          for (int b = cf; b <= cl; ++b) top = fmaxf(top, __ldcg(part(b) + Sh::kRows * D + 2 * row));
-          mm[j] = top;
-          ll[j] = 0.f;
-          acc[j] = make_float4(0.f, 0.f, 0.f, 0.f);
-          const float ref = top == -INFINITY ? 0.f : top;
-#pragma unroll 8
-          for (int b = cf; b <= cl; ++b) {
-            const float2 ml = __ldcg(reinterpret_cast<const float2*>(part(b) + Sh::kRows * D + 2 * row));
-            add(j, ml.x, ml.y, __ldcg(reinterpret_cast<const float4*>(part(b) + 4 * v)), ref);
-          }
-        }
-      }
-    }
-    if (mine_to_store) {  // uniform
+    } else {
       __half* s_out = reinterpret_cast<__half*>(smem + W * Sh::kRows * D * 4);
 #pragma unroll
       for (int j = 0; j < kPer; ++j) {
@@ -778,8 +632,77 @@ __global__ void __launch_bounds__(TreeShape<FMT, D, MT>::kThreads, 1) tree_kerne
     }
     fence_async_smem();  // the ring is written by copies again
     __syncthreads();
-    cur += u1 - u0;
   }
+}
+
+// Adds the parts of the rows that several blocks share: a warp for each row.
+template <int ROWS, int UNIT, int D>
+__global__ void __launch_bounds__(128) tree_join_kernel(const TreeArgs a) {
+  const TreeParams& p = a.p;
+  const int lane = threadIdx.x & 31, H = p.cache.kv_heads;
+  const unsigned full = 0xffffffffu;
+  const int64_t row = (static_cast<int64_t>(blockIdx.x) * 128 + threadIdx.x) >> 5;
+  if (row >= p.n_q * p.q_heads) return;
+  const int64_t token = row / p.q_heads;
+  const int qh = static_cast<int>(row - token * p.q_heads), head = qh / a.G;
+  // its sequence, and the units before it
+  int64_t total = 0, base = 0;
+  int seq = 0;
+  for (int b = lane; b < p.n_seqs; b += 32) {
+    const SeqWork s = seq_work<ROWS, UNIT>(a, b);
+    const int64_t w = s.units * s.tiles * H;
+    total += w;
+    if (__ldg(p.cu_q + b + 1) <= token) base += w, ++seq;
+  }
+  total = warp_total(total);
+  base = warp_total(base);
+  seq = static_cast<int>(warp_total(seq));
+  if (seq >= p.n_seqs) return;
+  const SeqWork s = seq_work<ROWS, UNIT>(a, seq);
+  const int64_t i = token - __ldg(p.cu_q + seq);
+  if (i < 0 || i >= s.T) return;
+  const int64_t quota = run_quota(a, total);
+  const int r = static_cast<int>(i) * a.G + qh - head * a.G;
+  const int64_t first = base + (static_cast<int64_t>(head) * s.tiles + r / ROWS) * s.units;
+  const int b0 = static_cast<int>(div_small(first, quota)), b1 = static_cast<int>(div_small(first + s.units - 1, quota));
+  if (b0 == b1) return;  // one block had it all
+  float m = -INFINITY, l = 0.f, acc[D / 32];
+#pragma unroll
+  for (int c = 0; c < D / 32; ++c) acc[c] = 0.f;
+  for (int c0 = b0; c0 <= b1; c0 += 32) {
+    float2 ml = make_float2(-INFINITY, 0.f);
+    const int mine = c0 + lane;
+    if (mine <= b1)
+      ml = *reinterpret_cast<const float2*>(tree_slot(p, mine, mine == b0, D) + kSlotRows * D + 2 * (r % ROWS));
+    float top = ml.x;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(full, top, o));
+    const float mn = fmaxf(m, top), ref = mn == -INFINITY ? 0.f : mn;
+    const float g = m == -INFINITY ? 0.f : ex2(m - ref);
+    const float f = ml.x == -INFINITY ? 0.f : ex2(ml.x - ref);
+    m = mn;
+    l *= g;
+#pragma unroll
+    for (int c = 0; c < D / 32; ++c) acc[c] *= g;
+    const int n = min(32, b1 - c0 + 1);
+#pragma unroll 8
+    for (int k = 0; k < n; ++k) {
+      const float fk = __shfl_sync(full, f, k);
+      l += __shfl_sync(full, ml.y, k) * fk;
+      const float* part = tree_slot(p, c0 + k, c0 + k == b0, D) + (r % ROWS) * D + lane * (D / 32);
+      float x[D / 32];
+      if constexpr (D == 128) *reinterpret_cast<float4*>(x) = *reinterpret_cast<const float4*>(part);
+      else *reinterpret_cast<float2*>(x) = *reinterpret_cast<const float2*>(part);
+#pragma unroll
+      for (int c = 0; c < D / 32; ++c) acc[c] += x[c] * fk;
+    }
+  }
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+  __half* out = static_cast<__half*>(p.out.ptr) + token * p.out.token_stride + qh * p.out.head_stride + lane * (D / 32);
+#pragma unroll
+  for (int c = 0; c < D / 32; c += 2)
+    *reinterpret_cast<uint32_t*>(out + c) = half_pair(acc[c] * inv, acc[c + 1] * inv);
+  if (p.lse && lane == 0) p.lse[row] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
 }
 
 template <int FMT, int D, int MT>
@@ -789,6 +712,28 @@ cudaError_t launch(const TreeArgs& a, cudaStream_t s) {
   static const cudaError_t attr =
       cudaFuncSetAttribute(tree_kernel<FMT, D, MT>, cudaFuncAttributeMaxDynamicSharedMemorySize, Sh::kBytes);
   if (attr != cudaSuccess) return attr;
+  tree_kernel<FMT, D, MT><<<a.grid, Sh::kThreads, Sh::kBytes, s>>>(a);
+  return cudaGetLastError();
+}
+
+template <int ROWS, int UNIT>
+cudaError_t launch_join(const TreeArgs& a, cudaStream_t s) {
+  const int64_t rows = a.p.n_q * a.p.q_heads;
+  const unsigned grid = static_cast<unsigned>((rows + 3) / 4);
+  if (a.p.cache.head_dim == 64) tree_join_kernel<ROWS, UNIT, 64><<<grid, 128, 0, s>>>(a);
+  else tree_join_kernel<ROWS, UNIT, 128><<<grid, 128, 0, s>>>(a);
+  return cudaGetLastError();
+}
+
+int env_int(const char* n, int d) { const char* v = getenv(n); return v && *v ? atoi(v) : d; }
+
+}  // namespace
+
+int64_t tree_ws_bytes(int64_t, int, int head_dim) {
+  return 2 * kMaxBlocks * slot_floats(head_dim) * static_cast<int64_t>(sizeof(float));
+}
+
+cudaError_t launch_attn_tree(const TreeParams& p, cudaStream_t s) {
   static const int sms = [] {
     int dev = 0, n = 0;
     cudaGetDevice(&dev);
@@ -796,27 +741,28 @@ cudaError_t launch(const TreeArgs& a, cudaStream_t s) {
     return n;
   }();
   if (sms <= 0) return cudaErrorInvalidDevice;
-  tree_kernel<FMT, D, MT><<<sms < kMaxBlocks ? sms : kMaxBlocks, Sh::kThreads, Sh::kBytes, s>>>(a);
-  return cudaGetLastError();
-}
-
-}  // namespace
-
-int64_t tree_ws_bytes(int64_t, int, int head_dim) {
-  return 4 * kMaxBlocks + 2 * kMaxBlocks * slot_floats(head_dim) * static_cast<int64_t>(sizeof(float));
-}
-
-cudaError_t launch_attn_tree(const TreeParams& p, cudaStream_t s) {
   TreeArgs a;
   a.p = p;
   a.G = p.q_heads / p.cache.kv_heads;
   a.page_shift = 0;
   while ((1 << a.page_shift) < p.cache.page_tokens) ++a.page_shift;
+  a.grid = sms < kMaxBlocks ? sms : kMaxBlocks;
+  const int64_t rows = static_cast<int64_t>(p.max_new) * a.G;
+  static const int wide_from = env_int("QG_WIDE", 17);
+  if (rows >= wide_from) {
+    a.min_units = 2;
+    const cudaError_t e = launch_tree_wide(a, s);
+    return e != cudaSuccess ? e : launch_join<64, 128>(a, s);
+  }
   a.min_units = 16;
-  const bool wide = static_cast<int64_t>(p.max_new) * a.G > 16;  // 32-row tiles
   auto by_rows = [&](auto fmt, auto d) {
     constexpr int F = decltype(fmt)::value, D = decltype(d)::value;
-    return wide ? launch<F, D, 2>(a, s) : launch<F, D, 1>(a, s);
+    if (rows > 16) {
+      const cudaError_t e = launch<F, D, 2>(a, s);
+      return e != cudaSuccess ? e : launch_join<32, kKvBlockTokens>(a, s);
+    }
+    const cudaError_t e = launch<F, D, 1>(a, s);
+    return e != cudaSuccess ? e : launch_join<16, kKvBlockTokens>(a, s);
   };
   auto by_dim = [&](auto fmt) {
     return p.cache.head_dim == 64 ? by_rows(fmt, std::integral_constant<int, 64>())

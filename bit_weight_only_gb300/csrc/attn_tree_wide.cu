@@ -1,0 +1,795 @@
+// attn_tree_wide.cu -- the attention of drafted tokens over the cache for row
+// tiles of up to 64 rows (drafted tokens x heads of a group), on the
+// fifth-generation tensor cores.
+//
+//   S^T = K Q^T   (128 keys x N rows)      O^T += V^T P^T   (d x N rows)
+//
+// Keys, not rows, lie along M = 128, so that few rows cost little (N is the
+// number of rows, rounded up to 16) and a thread's key has its scales as two
+// scalars.  A unit is 128 cached tokens (tree_work.cuh).
+//
+// Warps (16):
+//   0-3    softmax, a thread for each key: S^T from tensor memory, times the
+//          key's scale; p = exp2(s - m_r) with a reference m_r for each row
+//          that all keys share, moved (and O^T with it) only when some score
+//          passes it by 2^8 -- the four warps agree on that by one reducing
+//          barrier; p * scale(v), rounded to fp16, to shared memory
+//   4-7    K codes to fp16 in the operands' swizzle, a thread for each token
+//          (fp16 pages need none: their blocks are copied into place)
+//   8-11   V codes likewise; in units that hold drafted tokens or end inside,
+//          whatever must not meet a masked row's 0 is taken out of V (below)
+//   12     the copies (bulk, from the pages), ahead of all
+//   13     the MMAs
+// INT8 codes are exact in fp16.  Q4_0: K's codes are exact too; a product for
+// each group of 32 goes to columns of its own and the key's thread adds them
+// with its four scales in fp32.  V's codes are multiplied by their group's
+// scale (over a power of two that goes to p) and rounded to fp16 once: here a
+// group's scale cannot be applied after the product, whose rows are d.
+// fp16 values and Q4_0 scales of drafted tokens may be infinite or NaN, and
+// what lies past the sequence's end is whatever the page holds: both are
+// zeroed in V, and the former noted by (drafted token, d) for the rows that
+// see them.
+//
+// Every wait is bounded; on a timeout the block records the error, waits for
+// its own copies and MMAs, frees tensor memory and returns.
+#include <type_traits>
+
+#include "tc_common.cuh"
+#include "tree_work.cuh"
+
+namespace qgemv {
+namespace {
+
+constexpr int kThreads = 512;
+constexpr int kRows = 64;
+constexpr int kKeys = 128;
+constexpr int kBlocks = kKeys / kKvBlockTokens;  // cache blocks of a unit
+constexpr int kErrWide = 64;
+constexpr float kLazyW = 8.f;
+constexpr float kNone = 1e30f;  // -m of a row that has seen nothing
+
+template <int FMT, int D>
+struct Wide {
+  using L = KvLayout<FMT, D>;
+  static constexpr bool kF16 = FMT == QGEMV_KV_F16, kQ4 = FMT == QGEMV_KV_Q4_0;
+  static constexpr int kTile = kKeys * D * 2;  // a K or V operand
+  static constexpr int kKs = kF16 ? 3 : 2, kVs = 2;
+  static constexpr int kHalf = kBlocks / 2 * L::kBlock;  // raw stage: half a unit
+  static constexpr int kRs = kF16 ? 0 : kQ4 ? 4 : 3;
+  static constexpr int kGroups = kQ4 ? D / 32 : 1;  // products of S
+  static constexpr int kSBufs = kQ4 ? 1 : 2;
+  static constexpr int kScales = kF16 ? 0 : kQ4 ? 4 : 1;  // floats of K's scales of a key
+  // shared memory
+  static constexpr int kK = 0;
+  static constexpr int kV = kK + kKs * kTile;
+  static constexpr int kQ = kV + kVs * kTile;
+  static constexpr int kP = kQ + kRows * D * 2;
+  static constexpr int kRaw = kP + kKeys * 128;
+  static constexpr int kKsc = kRaw + kRs * kHalf;          // [kKs][128][kScales]
+  static constexpr int kVsc = kKsc + kKs * kKeys * 4 * kScales;
+  static constexpr int kM = kVsc + (kF16 ? 0 : kKs * kKeys * 4);  // float[64] -m, float[64] factors, float[4][64] x 2
+  static constexpr int kRowOff = kM + 64 * 4 * 10;         // int64[64][2]: q and out offsets
+  static constexpr int kRowMask = kRowOff + 64 * 16;       // uint64[64]
+  static constexpr int kKeyMask = kRowMask + 64 * 8;       // uint64[64]: the rows that see a drafted token
+  static constexpr int kBad = kKeyMask + 64 * 8;           // uint64[4][3][D]
+  static constexpr int kInts = kBad + (FMT == QGEMV_KV_INT8 ? 0 : 4 * 3 * D * 8);
+  static constexpr int kBars = kInts + 128;
+  static constexpr int kBytes = kBars + 48 * 8 + 1024;  // + alignment
+  static_assert(kBytes <= 227 * 1024, "shared memory");
+  // tensor memory columns
+  static constexpr int kOCol = kSBufs * kGroups * kRows;
+  static_assert(kOCol + kRows <= 512, "tensor memory");
+};
+
+// Barriers: index of the first of each kind.
+struct Bars {
+  static constexpr int kRf = 0, kRe = kRf + 5, kKf = kRe + 5, kKe = kKf + 3, kVl = kKe + 3, kVf = kVl + 2, kVe = kVf + 2,
+                       kSf = kVe + 2, kSe = kSf + 2, kPf = kSe + 2, kPv = kPf + 1, kQf = kPv + 1, kDone = kQf + 1;
+};
+
+__device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+
+// OR of `pred` over the softmax warpgroup's 128 threads.
+__device__ __forceinline__ bool any_of_128(bool pred) {
+  __syncwarp();
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
+               "bar.red.or.pred q, 1, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+               : "=r"(r)
+               : "r"(pred ? 1u : 0u)
+               : "memory");
+  return r != 0;
+}
+
+__device__ __forceinline__ float warp_max(float x) {
+  int k = __float_as_int(x);
+  k ^= (k >> 31) & 0x7fffffff;
+  k = __reduce_max_sync(0xffffffffu, k);
+  k ^= (k >> 31) & 0x7fffffff;
+  return __int_as_float(k);
+}
+
+template <int FMT, int D>
+__global__ void __launch_bounds__(kThreads, 1) tree_wide_kernel(const TreeArgs a) {
+  using S = Wide<FMT, D>;
+  using L = typename S::L;
+  using B = Bars;
+  const TreeParams& p = a.p;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + S::kBars);
+  float* s_nm = reinterpret_cast<float*>(smem + S::kM);
+  float* s_f = s_nm + 64;
+  float* s_red = s_f + 64;  // [4][64]
+  float* s_l = s_red + 256;
+  int64_t* s_off = reinterpret_cast<int64_t*>(smem + S::kRowOff);
+  uint64_t* s_rowmask = reinterpret_cast<uint64_t*>(smem + S::kRowMask);
+  uint64_t* s_keymask = reinterpret_cast<uint64_t*>(smem + S::kKeyMask);
+  unsigned long long* s_bad = reinterpret_cast<unsigned long long*>(smem + S::kBad);
+  volatile int* s_int = reinterpret_cast<volatile int*>(smem + S::kInts);
+  volatile int* s_abort = s_int;
+  uint32_t* s_tmem = reinterpret_cast<uint32_t*>(smem + S::kInts) + 1;
+  volatile int* s_anybad = s_int + 2;   // [4]
+  // blocks (bits) whose pages exist, of each half of a unit
+  volatile int* s_valid = s_int + 6;    // [kKs][2]
+  volatile int* s_vvalid = s_int + 12;  // [kVs], whole units (fp16)
+  volatile int* s_rvalid = s_int + 14;  // [kRs]
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const unsigned full = 0xffffffffu;
+
+  if (tid == 0) {
+    for (int i = 0; i < 5; ++i) {
+      mbar_init(&bars[B::kRf + i], 1);
+      mbar_init(&bars[B::kRe + i], 128);
+    }
+    for (int i = 0; i < 3; ++i) {
+      mbar_init(&bars[B::kKf + i], S::kF16 ? 1 : 128);
+      mbar_init(&bars[B::kKe + i], 5);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&bars[B::kVl + i], 1);
+      mbar_init(&bars[B::kVf + i], 128);
+      mbar_init(&bars[B::kVe + i], 1);
+      mbar_init(&bars[B::kSf + i], 1);
+      mbar_init(&bars[B::kSe + i], 128);
+    }
+    mbar_init(&bars[B::kPf], 128);
+    mbar_init(&bars[B::kPv], 1);
+    mbar_init(&bars[B::kQf], 128);
+    mbar_init(&bars[B::kDone], 1);
+    fence_mbarrier_init();
+    *s_abort = 0;
+    for (int i = 0; i < 4; ++i) s_anybad[i] = 0;
+  }
+  if constexpr (FMT != QGEMV_KV_INT8)
+    for (int i = tid; i < 12 * D; i += kThreads) s_bad[i] = 0;
+  if (warp == 13) tmem_alloc_all(s_tmem);
+  tcgen_before_sync();
+  __syncthreads();
+  tcgen_after_sync();
+  const uint32_t tbase = *s_tmem;
+
+  auto wait = [&](int bar, uint32_t parity) -> bool {
+    if (mbar_try_wait(&bars[bar], parity)) return true;
+    const unsigned long long t0 = global_timer_ns();
+    while (!mbar_try_wait(&bars[bar], parity)) {
+      if (*s_abort) return false;
+      if (global_timer_ns() - t0 > kWaitLimitNs) {
+        atomicOr(reinterpret_cast<int*>(p.ws), kErrWide);
+        *s_abort = 1;
+        return false;
+      }
+    }
+    return true;
+  };
+  // stage and parity of use n of a ring of `k` stages: the wait for what
+  // fills it, and for its being free again
+  auto used = [](int64_t n, int k) { return static_cast<uint32_t>((n / k) & 1); };
+  auto freed = [](int64_t n, int k) { return static_cast<uint32_t>(((n / k) - 1) & 1); };
+
+  int jt = 0;  // units so far: the same count in every warp
+  Cursor<kRows, kKeys> work(a);
+  Segment sg;
+
+  if (warp < 4) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+    // ------------------------------------------------------------ softmax --
+    const int key = tid;
+    const uint32_t t_lane = static_cast<uint32_t>(32 * warp) << 16;
+    const float sl = p.scale * kLog2e;
+    int n_seg = 0;
+    // A wait that ran out sets `dead`; the four warps go on, and leave together
+    // where they agree on it (a warp that left alone would hold up the others'
+    // barriers).
+    bool dead = false, left = false;
+    while (!left && work.next(a, sg)) {
+      const int R = sg.T * a.G, row0 = sg.tile * kRows, live = min(kRows, R - row0);
+      const int ctx = sg.ctx, all = ctx + sg.T;
+      const int64_t q0 = __ldg(p.cu_q + sg.seq);
+      // ---- rows of the tile, Q
+      if (tid < kRows) {
+        const int r = row0 + min(tid, live - 1), tok = r / a.G, h = sg.head * a.G + r - tok * a.G;
+        s_off[2 * tid] = (q0 + tok) * p.q.token_stride + h * p.q.head_stride;
+        s_off[2 * tid + 1] = (q0 + tok) * p.out.token_stride + h * p.out.head_stride;
+        s_rowmask[tid] = tid >= live ? 0 : p.masks ? p.masks[q0 + tok] : (~0ull >> (63 - tok));
+        s_nm[tid] = kNone;
+      }
+      named_bar_sync(1, 128);
+      {
+        constexpr int U = D / 8;
+        const __half* qb = static_cast<const __half*>(p.q.ptr);
+#pragma unroll 4
+        for (int it = 0; it < kRows * U / 128; ++it) {
+          const int idx = it * 128 + tid, r = idx / U, u = idx % U;
+          uint4 w = make_uint4(0u, 0u, 0u, 0u);
+          if (r < live) w = __ldg(reinterpret_cast<const uint4*>(qb + s_off[2 * r] + 8 * u));
+          *reinterpret_cast<uint4*>(smem + S::kQ + (u >> 3) * (kRows * 128) + r * 128 + (((u & 7) ^ (r & 7)) << 4)) = w;
+        }
+        fence_async_smem();
+        mbar_arrive(&bars[B::kQf]);
+      }
+      if (sg.u1 * kKeys > ctx && tid < kMaxDrafts) {  // drafted tokens among the keys
+        uint64_t m = 0;
+        for (int r = 0; r < live; ++r) m |= ((s_rowmask[r] >> tid) & 1ull) << r;
+        s_keymask[tid] = m;
+      }
+      named_bar_sync(1, 128);
+
+      uint64_t l2[kRows / 2];
+#pragma unroll
+      for (int i = 0; i < kRows / 2; ++i) l2[i] = 0;
+      const int n = static_cast<int>(sg.u1 - sg.u0);
+      const int groups16 = (live + 15) >> 4;
+      for (int j = 0; j < n; ++j, ++jt) {
+        const int ks = jt % S::kKs, sb = jt % S::kSBufs;
+        dead |= !wait(B::kKf + ks, used(jt, S::kKs)) || !wait(B::kSf + sb, used(jt, S::kSBufs));
+        __syncwarp();
+        tcgen_after_sync();
+        // ---- S of this key
+        float ksc[4] = {1.f, 1.f, 1.f, 1.f};
+        float vs = 1.f, lv = 0.f;
+        if constexpr (FMT == QGEMV_KV_INT8) {
+          ksc[0] = reinterpret_cast<const float*>(smem + S::kKsc)[ks * kKeys + key];
+        } else if constexpr (S::kQ4) {
+          const float4 k4 = reinterpret_cast<const float4*>(smem + S::kKsc)[ks * kKeys + key];
+          ksc[0] = k4.x, ksc[1] = k4.y, ksc[2] = k4.z, ksc[3] = k4.w;
+        }
+        if constexpr (!S::kF16) {
+          vs = reinterpret_cast<const float*>(smem + S::kVsc)[ks * kKeys + key];
+          lv = __log2f(fmaxf(vs, 7.9e-31f));  // 2^-100
+        }
+        const bool there = (s_valid[2 * ks + (key >> 6)] >> ((key >> 4) & 3)) & 1;
+        uint64_t x2[kRows / 2];
+        uint32_t raw[32];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+#pragma unroll
+          for (int g = 0; g < S::kGroups; ++g) {
+            tmem_ld32(tbase + t_lane + (sb * S::kGroups + g) * kRows + 32 * h, raw);
+            tmem_wait_ld32(raw);
+            const float f = ksc[g] * sl;
+            const uint64_t f2 = pack2(f, f);
+#pragma unroll
+            for (int c = 0; c < 16; ++c) {
+              const uint64_t v = pack2(__uint_as_float(raw[2 * c]), __uint_as_float(raw[2 * c + 1]));
+              x2[16 * h + c] = g == 0 ? mul2(v, f2) : fma2(v, f2, x2[16 * h + c]);
+            }
+          }
+        }
+        tcgen_before_sync();
+        mbar_arrive(&bars[B::kSe + sb]);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars[B::kKe + ks]);
+        // ---- what sees this key
+        const int64_t pos = (sg.u0 + j) * kKeys + key;
+        uint64_t vis = 0;
+        if (there) vis = pos < ctx ? ~0ull : pos < all ? s_keymask[pos - ctx] : 0ull;
+        const bool some_masked = __any_sync(full, vis != ~0ull);
+        if (some_masked) {
+#pragma unroll
+          for (int i = 0; i < kRows / 2; ++i) {
+            float x, y;
+            unpack2(x2[i], x, y);
+            if (!((vis >> (2 * i)) & 1)) x = -INFINITY;
+            if (!((vis >> (2 * i + 1)) & 1)) y = -INFINITY;
+            x2[i] = pack2(x, y);
+          }
+          if (vis == 0) vs = 0.f, lv = -100.f;
+        }
+        // ---- the rows' references
+        float top = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < kRows / 4; ++i) {
+          if ((i >> 2) >= groups16) break;
+          const ulonglong2 nm = *reinterpret_cast<const ulonglong2*>(s_nm + 4 * i);
+          float x, y, z, w;
+          unpack2(add2(x2[2 * i], nm.x), x, y);
+          unpack2(add2(x2[2 * i + 1], nm.y), z, w);
+          top = fmaxf(top, fmaxf(fmaxf(x, y), fmaxf(z, w)));
+        }
+        if (any_of_128(dead || top + lv > kLazyW)) {
+          if (any_of_128(dead)) {
+            left = true;
+            break;
+          }
+#pragma unroll
+          for (int i = 0; i < kRows / 2; ++i) {
+            if ((i >> 3) >= groups16) break;
+            float x, y;
+            unpack2(x2[i], x, y);
+            x = warp_max(x + lv);
+            y = warp_max(y + lv);
+            if (lane == (i & 31)) *reinterpret_cast<float2*>(s_red + 64 * warp + 2 * i) = make_float2(x, y);
+          }
+          named_bar_sync(1, 128);
+          if (tid < kRows) {
+            const float m = -s_nm[tid];
+            const float mx = fmaxf(fmaxf(s_red[tid], s_red[64 + tid]), fmaxf(s_red[128 + tid], s_red[192 + tid]));
+            const float mn = fmaxf(m, mx);
+            s_f[tid] = m == -kNone ? 0.f : ex2(m - mn);
+            s_nm[tid] = -mn;
+          }
+          named_bar_sync(1, 128);
+#pragma unroll
+          for (int i = 0; i < kRows / 4; ++i) {
+            const ulonglong2 f = *reinterpret_cast<const ulonglong2*>(s_f + 4 * i);
+            l2[2 * i] = mul2(l2[2 * i], f.x);
+            l2[2 * i + 1] = mul2(l2[2 * i + 1], f.y);
+          }
+          if (j > 0) {  // O^T of the units before: this thread's d
+            dead |= !wait(B::kPv, (jt - 1) & 1);
+            __syncwarp();
+            tcgen_after_sync();
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              tmem_ld32(tbase + t_lane + S::kOCol + 32 * h, raw);
+              tmem_wait_ld32(raw);
+#pragma unroll
+              for (int c = 0; c < 16; ++c) {
+                float x, y;
+                unpack2(mul2(pack2(__uint_as_float(raw[2 * c]), __uint_as_float(raw[2 * c + 1])),
+                             reinterpret_cast<const uint64_t*>(s_f)[16 * h + c]),
+                        x, y);
+                raw[2 * c] = __float_as_uint(x), raw[2 * c + 1] = __float_as_uint(y);
+              }
+              tmem_st32(tbase + t_lane + S::kOCol + 32 * h, raw);
+            }
+            tmem_wait_store();
+          }
+        }
+        // ---- P
+        uint32_t w2[kRows / 2];
+        const uint64_t vs2 = pack2(vs, vs);
+#pragma unroll
+        for (int i = 0; i < kRows / 4; ++i) {
+          if ((i >> 2) >= groups16) break;
+          const ulonglong2 nm = *reinterpret_cast<const ulonglong2*>(s_nm + 4 * i);
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            float x, y;
+            unpack2(add2(x2[2 * i + e], e ? nm.y : nm.x), x, y);
+            x = ex2(x), y = ex2(y);
+            uint64_t pp = pack2(x, y);
+            l2[2 * i + e] = add2(l2[2 * i + e], pp);
+            if constexpr (!S::kF16) {
+              unpack2(mul2(pp, vs2), x, y);
+              if (some_masked) {  // 0 where masked, whatever the scale holds
+                if (!((vis >> (4 * i + 2 * e)) & 1)) x = 0.f;
+                if (!((vis >> (4 * i + 2 * e + 1)) & 1)) y = 0.f;
+              }
+            }
+            w2[2 * i + e] = cvt_pair<false>(x, y);
+          }
+        }
+        if (jt > 0) dead |= !wait(B::kPv, (jt - 1) & 1);  // the product before has read P
+#pragma unroll
+        for (int u = 0; u < kRows / 8; ++u) {
+          if ((u >> 1) >= groups16) break;
+          *reinterpret_cast<uint4*>(smem + S::kP + key * 128 + ((u ^ (key & 7)) << 4)) =
+              make_uint4(w2[4 * u], w2[4 * u + 1], w2[4 * u + 2], w2[4 * u + 3]);
+        }
+        fence_async_smem();
+        tcgen_before_sync();
+        mbar_arrive(&bars[B::kPf]);
+      }
+      if (left) break;
+      // ---- the segment's end: l over the keys, O^T
+      dead |= !wait(B::kPv, (jt - 1) & 1);
+      if (any_of_128(dead)) break;
+      tcgen_after_sync();
+      {
+        // Each step halves the rows a lane holds: lane i ends with rows 2i, 2i + 1.
+        float l[kRows];
+#pragma unroll
+        for (int i = 0; i < kRows / 2; ++i) unpack2(l2[i], l[2 * i], l[2 * i + 1]);
+#pragma unroll
+        for (int o = 16, h = kRows / 2; o > 0; o >>= 1, h >>= 1) {
+#pragma unroll
+          for (int i = 0; i < h; ++i) {
+            const bool up = lane & o;
+            const float give = up ? l[i] : l[i + h], keep = up ? l[i + h] : l[i];
+            l[i] = keep + __shfl_xor_sync(full, give, o);
+          }
+        }
+        s_l[64 * warp + 2 * lane] = l[0];
+        s_l[64 * warp + 2 * lane + 1] = l[1];
+      }
+      named_bar_sync(1, 128);
+      float* slot = tree_slot(p, blockIdx.x, sg.u0 == 0, D);
+      if (tid < kRows) {
+        const float l = (s_l[tid] + s_l[64 + tid]) + (s_l[128 + tid] + s_l[192 + tid]);
+        const float nm = s_nm[tid], m = nm == kNone ? -INFINITY : -nm;
+        s_f[tid] = sg.shared ? 1.f : l == 0.f ? 0.f : 1.f / l;
+        if (sg.shared) {
+          *reinterpret_cast<float2*>(slot + kSlotRows * D + 2 * tid) = make_float2(m, l);
+        } else if (p.lse && tid < live) {
+          const int r = row0 + tid, tok = r / a.G;
+          p.lse[(q0 + tok) * p.q_heads + sg.head * a.G + r - tok * a.G] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+        }
+      }
+      named_bar_sync(1, 128);
+      const int bb = n_seg & 3;
+      const bool bad = FMT != QGEMV_KV_INT8 && s_anybad[bb] != 0;
+      __half* outb = static_cast<__half*>(p.out.ptr);
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        uint32_t raw[32];
+        tmem_ld32(tbase + t_lane + S::kOCol + 32 * h, raw);
+        tmem_wait_ld32(raw);
+        if (tid < D) {
+#pragma unroll
+          for (int c = 0; c < 32; ++c) {
+            const int r = 32 * h + c;
+            if (r < live) {
+              float x = __uint_as_float(raw[c]) * s_f[r];
+              if (FMT != QGEMV_KV_INT8 && bad) {
+                const unsigned long long* bd = s_bad + bb * 3 * D + tid;
+                const uint64_t rm = s_rowmask[r];
+                const bool nan = bd[0] & rm, up = bd[D] & rm, down = bd[2 * D] & rm;
+                if (nan || (up && down)) x = __int_as_float(0x7fffffff);
+                else if (up) x += INFINITY;
+                else if (down) x -= INFINITY;
+              }
+              if (sg.shared) slot[r * D + tid] = x;
+              else outb[s_off[2 * r + 1] + tid] = __float2half_rn(x);
+            }
+          }
+        }
+      }
+      tcgen_before_sync();
+      named_bar_sync(1, 128);
+      if (FMT != QGEMV_KV_INT8 && bad) {
+        for (int i = tid; i < 3 * D; i += 128) s_bad[bb * 3 * D + i] = 0;
+        if (tid == 0) s_anybad[bb] = 0;
+      }
+      ++n_seg;
+    }
+  } else if (warp < 12) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
+    // ----------------------------------------------- codes to operands ----
+    const int key = tid & 127, half = key >> 6;
+    const bool is_v = warp >= 8;
+    int n_seg = 0;
+    bool ok = !(S::kF16 && !is_v);
+    while (ok && work.next(a, sg)) {
+      const int n = static_cast<int>(sg.u1 - sg.u0), ctx = sg.ctx, all = ctx + sg.T;
+      const int bb = n_seg & 3;
+      for (int j = 0; j < n; ++j, ++jt) {
+        const int64_t pos = (sg.u0 + j) * kKeys + key;
+        const int ks = jt % S::kKs, vst = jt % S::kVs;
+        uint8_t* dst = smem + (is_v ? S::kV + vst * S::kTile : S::kK + ks * S::kTile) + key * 128;
+        auto note = [&](int d, int kind) {  // a drafted token's value that is infinite or NaN
+          atomicOr(&s_bad[(bb * 3 + kind) * D + d], 1ull << (pos - ctx));
+          s_anybad[bb] = 1;
+        };
+        if constexpr (S::kF16) {
+          ok = wait(B::kVl + vst, used(jt, S::kVs));
+          if (!__all_sync(full, ok)) {
+            ok = false;
+            break;
+          }
+          const int valid = s_vvalid[vst];
+          if ((sg.u0 + j + 1) * kKeys > ctx || valid != (1 << kBlocks) - 1) {
+            const bool on = ((valid >> (key >> 4)) & 1) && pos < all;
+#pragma unroll 2
+            for (int u = 0; u < D / 8; ++u) {
+              uint4* at = reinterpret_cast<uint4*>(dst + (u >> 3) * (kKeys * 128) + (((u & 7) ^ (key & 7)) << 4));
+              if (!on) {
+                *at = make_uint4(0u, 0u, 0u, 0u);
+              } else if (pos >= ctx) {
+                const uint4 w = *at;
+                const uint32_t e = (((w.x & 0x7C007C00u) + 0x04000400u) | ((w.y & 0x7C007C00u) + 0x04000400u) |
+                                    ((w.z & 0x7C007C00u) + 0x04000400u) | ((w.w & 0x7C007C00u) + 0x04000400u)) & 0x80008000u;
+                if (e) {
+                  uint16_t* hw = reinterpret_cast<uint16_t*>(at);
+                  for (int i = 0; i < 8; ++i) {
+                    const uint32_t x = hw[i];
+                    if ((x & 0x7C00u) != 0x7C00u) continue;
+                    note(8 * u + i, (x & 0x3FFu) ? 0 : x >> 15 ? 2 : 1);
+                    hw[i] = 0;
+                  }
+                }
+              }
+            }
+            fence_async_smem();
+          }
+          mbar_arrive(&bars[B::kVf + vst]);
+        } else {
+          const int64_t rt = 2ll * jt + half;
+          const int rs = static_cast<int>(rt % S::kRs);
+          ok = wait(B::kRf + rs, used(rt, S::kRs));
+          if (ok && is_v && jt >= S::kVs) ok = wait(B::kVe + vst, freed(jt, S::kVs));
+          if (ok && !is_v && jt >= S::kKs) ok = wait(B::kKe + ks, freed(jt, S::kKs));
+          if (!__all_sync(full, ok)) {
+            ok = false;
+            break;
+          }
+          const int tok = key & 15;
+          const uint8_t* blk = smem + S::kRaw + rs * S::kHalf + ((key >> 4) & 3) * L::kBlock;
+          const int valid = s_rvalid[rs];
+          const bool there = (valid >> ((key >> 4) & 3)) & 1;
+          // 16-byte unit U of the row: chunk U >> 3, swizzled
+          auto put = [&](int U, uint32_t w0, uint32_t w1, uint32_t w2, uint32_t w3) {
+            *reinterpret_cast<uint4*>(dst + (U >> 3) * (kKeys * 128) + (((U & 7) ^ (key & 7)) << 4)) = make_uint4(w0, w1, w2, w3);
+          };
+          if constexpr (FMT == QGEMV_KV_INT8) {
+            constexpr int N = D / 16;
+            // which unit first: eight neighbouring lanes read eight (d = 64:
+            // four) different ones
+            const int turn = is_v ? (lane & (N - 1)) ^ ((D == 128 ? 2 * ((lane >> 1) & 3) : 0)) : lane & (N - 1);
+#pragma unroll
+            for (int u = 0; u < N; ++u) {
+              const int unit = is_v ? u ^ turn : (u + turn) & (N - 1);
+              const uint4 c = lds128(blk + (is_v ? L::v_off(tok, 16 * unit) : L::k_off(tok, 16 * unit)));
+              put(2 * unit, i8_pair<0x4140>(c.x), i8_pair<0x4342>(c.x), i8_pair<0x4140>(c.y), i8_pair<0x4342>(c.y));
+              put(2 * unit + 1, i8_pair<0x4140>(c.z), i8_pair<0x4342>(c.z), i8_pair<0x4140>(c.w), i8_pair<0x4342>(c.w));
+            }
+            if (!is_v) {
+              reinterpret_cast<float*>(smem + S::kKsc)[ks * kKeys + key] = reinterpret_cast<const float*>(blk + L::kKs)[tok];
+              reinterpret_cast<float*>(smem + S::kVsc)[ks * kKeys + key] = reinterpret_cast<const float*>(blk + L::kVs)[tok];
+            }
+          } else {
+            constexpr int NG = D / 32;
+            const __half* vsc = reinterpret_cast<const __half*>(blk + L::kVs) + tok * NG;
+            // V's scales over a power of two of the token, which goes to p
+            float vg[NG], top = 0.f;
+#pragma unroll
+            for (int g = 0; g < NG; ++g) {
+              vg[g] = __half2float(vsc[g]);
+              if (fabsf(vg[g]) < INFINITY) top = fmaxf(top, fabsf(vg[g]));
+            }
+            const int ex = top > 0.f ? (__float_as_int(top) >> 23) - 127 : 0;  // fp16 scales: -24 .. 15
+            if (!is_v) {
+              constexpr int CW = D / 32;  // words of a cell
+              const __half* ksc = reinterpret_cast<const __half*>(blk + L::kKs) + tok * NG;
+#pragma unroll
+              for (int u = 0; u < 4; ++u) {
+                const int c = (u + (lane >> 1)) & 3;
+                const uint8_t* at = blk + L::k_off(tok, c * (D / 8));
+                uint32_t w[CW];
+                if constexpr (D == 128) *reinterpret_cast<uint4*>(w) = lds128(at);
+                else *reinterpret_cast<uint2*>(w) = *reinterpret_cast<const uint2*>(at);
+#pragma unroll
+                for (int g = 0; g < CW; ++g) put(4 * g + c, q4_pair<0>(w[g]), q4_pair<1>(w[g]), q4_pair<2>(w[g]), q4_pair<3>(w[g]));
+              }
+              float k4[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+              for (int g = 0; g < NG; ++g) k4[g] = __half2float(ksc[g]);
+              reinterpret_cast<float4*>(smem + S::kKsc)[ks * kKeys + key] = make_float4(k4[0], k4[1], k4[2], k4[3]);
+              reinterpret_cast<float*>(smem + S::kVsc)[ks * kKeys + key] =
+                  top > 0.f ? __int_as_float((ex + 127) << 23) : 0.f;  // no values: no say in the references
+            } else {
+              const bool on = there && pos < all;
+              uint32_t s2[NG];
+#pragma unroll
+              for (int g = 0; g < NG; ++g) {
+                float f = vg[g] * __int_as_float((127 - ex) << 23);
+                if (!on) f = 0.f;
+                if (on && pos >= ctx && !(fabsf(f) < INFINITY)) {
+                  for (int d = 0; d < 32; ++d) note(32 * g + d, 0);
+                  f = 0.f;
+                }
+                s2[g] = cvt_pair<false>(f, f);
+              }
+              // two cells: eight values of each group
+              auto four = [&](uint32_t hw, uint32_t s, uint32_t& lo, uint32_t& hi) {
+                const uint32_t x = hw | hw << 12;
+                lo = hmul2(hsub2((x & 0x000F000Fu) | 0x64006400u, 0x64086408u), s);
+                hi = hmul2(hsub2(((x >> 8) & 0x000F000Fu) | 0x64006400u, 0x64086408u), s);
+              };
+#pragma unroll
+              for (int u = 0; u < 4; ++u) {
+                const int c = (u + (lane >> 1)) & 3;
+                uint32_t w[NG];  // [cell][halfword pair]
+                const uint8_t* at = blk + L::v_off(tok, c * (D / 8));
+                if constexpr (D == 128) *reinterpret_cast<uint4*>(w) = lds128(at);
+                else *reinterpret_cast<uint2*>(w) = *reinterpret_cast<const uint2*>(at);
+#pragma unroll
+                for (int g = 0; g < NG; ++g) {
+                  uint32_t o0, o1, o2, o3;
+                  four((w[g >> 1] >> (16 * (g & 1))) & 0xffffu, s2[g], o0, o1);
+                  four((w[NG / 2 + (g >> 1)] >> (16 * (g & 1))) & 0xffffu, s2[g], o2, o3);
+                  put(4 * g + c, o0, o1, o2, o3);
+                }
+              }
+            }
+          }
+          if (!is_v && (key & 63) == 0) s_valid[2 * ks + half] = valid;
+          fence_async_smem();
+          mbar_arrive(&bars[is_v ? B::kVf + vst : B::kKf + ks]);
+          mbar_arrive(&bars[B::kRe + rs]);
+        }
+      }
+      ++n_seg;
+    }
+  } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+    if (warp == 12) {
+      // -------------------------------------------------------- copies ----
+      int64_t n_raw = 0;
+      int issued_k = 0, issued_v = 0;
+      bool ok = true;
+      while (ok && work.next(a, sg)) {
+        const int n = static_cast<int>(sg.u1 - sg.u0);
+        const int64_t n_pos = static_cast<int64_t>(sg.ctx) + sg.T;
+        // lane b < 8: the page of block b of a unit, looked up a unit ahead
+        auto page_of = [&](int j) -> int64_t {
+          const int64_t pos = (sg.u0 + j) * kKeys + kKvBlockTokens * (lane & 7);
+          const int64_t pi = pos >> a.page_shift;
+          if (j >= n || pos >= n_pos || pi >= p.table_stride) return -1;
+          const int64_t pg = __ldg(p.table + sg.seq * p.table_stride + pi);
+          return pg < p.cache.n_pages ? pg : -1;
+        };
+        int64_t ahead = page_of(0);
+        for (int j = 0; j < n; ++j, ++jt) {
+          const int64_t page = ahead;
+          ahead = page_of(j + 1);
+          const int64_t pos = (sg.u0 + j) * kKeys + kKvBlockTokens * (lane & 7);
+          const unsigned valid = __ballot_sync(full, page >= 0) & 0xffu;
+          const uint8_t* src = page >= 0 ? kv_block<FMT, D>(p.cache, page, sg.head,
+                                                            static_cast<int>(pos & (p.cache.page_tokens - 1)) / kKvBlockTokens)
+                                         : nullptr;
+          if constexpr (S::kF16) {
+            const int ks = jt % S::kKs, vst = jt % S::kVs;
+            const uint32_t bytes = static_cast<uint32_t>(__popc(valid)) * L::kV;
+            ok = jt < S::kKs || wait(B::kKe + ks, freed(jt, S::kKs));
+            if (!__all_sync(full, ok)) { ok = false; break; }
+            if (lane == 0) {
+              s_valid[2 * ks] = static_cast<int>(valid & 15u);
+              s_valid[2 * ks + 1] = static_cast<int>(valid >> 4);
+              mbar_arrive_expect_tx(&bars[B::kKf + ks], bytes);
+            }
+            __syncwarp();
+            if (lane < 8 && src) {
+#pragma unroll
+              for (int c = 0; c < D / 64; ++c)
+                bulk_load(smem + S::kK + ks * S::kTile + c * (kKeys * 128) + lane * 2048, src + c * 2048, 2048, &bars[B::kKf + ks]);
+            }
+            ++issued_k;
+            ok = jt < S::kVs || wait(B::kVe + vst, freed(jt, S::kVs));
+            if (!__all_sync(full, ok)) { ok = false; break; }
+            if (lane == 0) {
+              s_vvalid[vst] = static_cast<int>(valid);
+              mbar_arrive_expect_tx(&bars[B::kVl + vst], bytes);
+            }
+            __syncwarp();
+            if (lane < 8 && src) {
+#pragma unroll
+              for (int c = 0; c < D / 64; ++c)
+                bulk_load(smem + S::kV + vst * S::kTile + c * (kKeys * 128) + lane * 2048, src + L::kV + c * 2048, 2048,
+                          &bars[B::kVl + vst]);
+            }
+            ++issued_v;
+          } else {
+            for (int h = 0; h < 2; ++h, ++n_raw) {
+              const int rs = static_cast<int>(n_raw % S::kRs);
+              ok = n_raw < S::kRs || wait(B::kRe + rs, freed(n_raw, S::kRs));
+              if (!__all_sync(full, ok)) { ok = false; break; }
+              const unsigned here = (valid >> (4 * h)) & 15u;
+              if (lane == 0) {
+                s_rvalid[rs] = static_cast<int>(here);
+                mbar_arrive_expect_tx(&bars[B::kRf + rs], __popc(here) * L::kBlock);
+              }
+              __syncwarp();
+              if ((lane >> 2) == h && src)
+                bulk_load(smem + S::kRaw + rs * S::kHalf + (lane & 3) * L::kBlock, src, L::kBlock, &bars[B::kRf + rs]);
+            }
+            if (!ok) break;
+          }
+        }
+      }
+      // copies in flight (after an abort) must land before the block ends
+      if constexpr (S::kF16) {
+        for (int n = max(0, issued_k - S::kKs); n < issued_k; ++n) mbar_wait_bounded(&bars[B::kKf + n % S::kKs], used(n, S::kKs));
+        for (int n = max(0, issued_v - S::kVs); n < issued_v; ++n) mbar_wait_bounded(&bars[B::kVl + n % S::kVs], used(n, S::kVs));
+      } else {
+        for (int64_t n = max(static_cast<int64_t>(0), n_raw - S::kRs); n < n_raw; ++n)
+          mbar_wait_bounded(&bars[B::kRf + static_cast<int>(n % S::kRs)], used(n, S::kRs));
+      }
+    } else if (warp == 13) {
+      // ---------------------------------------------------------- MMAs ----
+      int n_seg = 0;
+      bool ok = true;
+      const uint32_t sk = smem_u32(smem + S::kK), sv = smem_u32(smem + S::kV), sq = smem_u32(smem + S::kQ),
+                     sp = smem_u32(smem + S::kP);
+      while (ok && work.next(a, sg)) {
+        const int n = static_cast<int>(sg.u1 - sg.u0);
+        if (lane == 0) {
+          const int live = min(kRows, sg.T * a.G - sg.tile * kRows), N = (live + 15) & ~15;
+          const uint32_t id_qk = mma_idesc(false, false, false, N), id_pv = mma_idesc(false, true, true, N);
+          auto qk = [&](int x) -> bool {
+            const int ks = x % S::kKs, sb = x % S::kSBufs;
+            if (!wait(B::kKf + ks, used(x, S::kKs))) return false;
+            if (x >= S::kSBufs && !wait(B::kSe + sb, freed(x, S::kSBufs))) return false;
+            tcgen_after_sync();
+            const uint64_t da = sw128_desc(sk + ks * S::kTile, 0, 1024), db = sw128_desc(sq, 0, 1024);
+#pragma unroll
+            for (int k = 0; k < D / 16; ++k) {
+              const int g = S::kGroups == 1 ? 0 : k >> 1;
+              const uint32_t oa = ((k >> 2) * (kKeys * 128) + (k & 3) * 32) >> 4;
+              const uint32_t ob = ((k >> 2) * (kRows * 128) + (k & 3) * 32) >> 4;
+              mma_ss(tbase + (sb * S::kGroups + g) * kRows, da + oa, db + ob, id_qk, S::kGroups == 1 ? k > 0 : (k & 1) != 0);
+            }
+            mma_commit(&bars[B::kSf + sb]);
+            mma_commit(&bars[B::kKe + ks]);
+            return true;
+          };
+          ok = wait(B::kQf, n_seg & 1) && qk(jt);
+          for (int j = 0; ok && j < n; ++j) {
+            const int x = jt + j, vst = x % S::kVs;
+            if (j + 1 < n) ok = qk(x + 1);
+            ok = ok && wait(B::kVf + vst, used(x, S::kVs)) && wait(B::kPf, x & 1);
+            if (!ok) break;
+            tcgen_after_sync();
+            const uint64_t da = sw128_desc(sv + vst * S::kTile, kKeys * 128, 1024), db = sw128_desc(sp, 0, 1024);
+#pragma unroll
+            for (int k = 0; k < kKeys / 16; ++k)
+              mma_ss(tbase + S::kOCol, da + ((k * 2048) >> 4), db + ((k * 2048) >> 4), id_pv, j > 0 || k > 0);
+            mma_commit(&bars[B::kPv]);
+            mma_commit(&bars[B::kVe + vst]);
+          }
+          if (!ok) {  // MMAs in flight: let them finish before tensor memory is freed
+            mma_commit(&bars[B::kDone]);
+            mbar_wait_bounded(&bars[B::kDone], 0);
+          }
+        }
+        ok = __shfl_sync(full, ok ? 1 : 0, 0) != 0;
+        jt += n;
+        ++n_seg;
+      }
+    }
+  }
+  __syncthreads();
+  if (warp == 13) tmem_free_all(tbase);
+}
+
+template <int FMT, int D>
+cudaError_t launch(const TreeArgs& a, cudaStream_t s) {
+  using S = Wide<FMT, D>;
+  static const cudaError_t attr =
+      cudaFuncSetAttribute(tree_wide_kernel<FMT, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kBytes);
+  if (attr != cudaSuccess) return attr;
+  tree_wide_kernel<FMT, D><<<a.grid, kThreads, S::kBytes, s>>>(a);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_tree_wide(const TreeArgs& a, cudaStream_t s) {
+  auto by_dim = [&](auto fmt) {
+    constexpr int F = decltype(fmt)::value;
+    return a.p.cache.head_dim == 64 ? launch<F, 64>(a, s) : launch<F, 128>(a, s);
+  };
+  switch (a.p.cache.format) {
+    case QGEMV_KV_F16: return by_dim(std::integral_constant<int, QGEMV_KV_F16>());
+    case QGEMV_KV_INT8: return by_dim(std::integral_constant<int, QGEMV_KV_INT8>());
+    default: return by_dim(std::integral_constant<int, QGEMV_KV_Q4_0>());
+  }
+}
+
+}  // namespace qgemv

@@ -94,10 +94,18 @@ __device__ __forceinline__ uint64_t sw128_desc(uint32_t addr, uint32_t lbo, uint
 }
 
 // Instruction descriptor: fp32 accumulator, A and B fp16 (0) or bf16 (1),
-// A K-major, B K-major or MN-major, M = 128.
-__host__ __device__ constexpr uint32_t mma_idesc(bool bf16, bool b_mn_major, int n) {
-  return (1u << 4) | ((bf16 ? 1u : 0u) << 7) | ((bf16 ? 1u : 0u) << 10) | ((b_mn_major ? 1u : 0u) << 16) |
+// each K-major or MN-major, M = 128.
+__host__ __device__ constexpr uint32_t mma_idesc(bool bf16, bool a_mn_major, bool b_mn_major, int n) {
+  return (1u << 4) | ((bf16 ? 1u : 0u) << 7) | ((bf16 ? 1u : 0u) << 10) | ((a_mn_major ? 1u : 0u) << 15) |
+         ((b_mn_major ? 1u : 0u) << 16) |
          (static_cast<uint32_t>(n >> 3) << 17) | ((128u >> 4) << 24);
+}
+
+// Untiled copy of `bytes` bytes, completion on `bar`.
+__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(smem_u32(dst)),
+               "l"(src), "r"(bytes), "r"(smem_u32(bar))
+               : "memory");
 }
 
 // Tiled TMA load of a 3-D box at (x, y, z).
@@ -149,6 +157,38 @@ __device__ __forceinline__ uint32_t cvt_pair(float lo, float hi) {
   if constexpr (BF16) asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   else asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
+}
+
+__device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t s) { return __byte_perm(a, b, s); }
+__device__ __forceinline__ uint32_t hsub2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ uint32_t hfma2(uint32_t a, uint32_t b, uint32_t c) {
+  uint32_t r;
+  asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
+  return r;
+}
+__device__ __forceinline__ uint32_t half_pair(float lo, float hi) { return cvt_pair<false>(lo, hi); }
+__device__ __forceinline__ float lg2(float x) {
+  float y;
+  asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// Codes to fp16 pairs.  INT8: bytes b0, b1 of w, stored + 128: 0x64 in the
+// high byte makes 1024 + code.
+template <int SEL>
+__device__ __forceinline__ uint32_t i8_pair(uint32_t w) {
+  return hsub2(prmt(w, 0x64646464u, SEL), 0x64806480u);  // - 1152
+}
+// Q4_0: nibbles N and N + 4 of w, minus 8.
+template <int N>
+__device__ __forceinline__ uint32_t q4_pair(uint32_t w) {
+  const uint32_t v = N >= 2 ? w >> 8 : w;
+  if (N & 1) return hfma2((v & 0x00F000F0u) | 0x64006400u, 0x2C002C00u, 0xD480D480u);  // (1024 + 16 q) / 16 - 72
+  return hsub2((v & 0x000F000Fu) | 0x64006400u, 0x64086408u);                          // 1024 + q - 1032
 }
 
 }  // namespace qgemv

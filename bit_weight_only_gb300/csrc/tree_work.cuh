@@ -1,0 +1,146 @@
+// tree_work.cuh -- how the attention of drafted tokens is split over thread
+// blocks, shared by its kernels.
+//
+// The work is a list of units -- UNIT cached tokens for one tile of ROWS rows
+// -- ordered (sequence, head, row tile, position).  Each thread block takes an
+// equal run of it; a run's part of one row tile is a segment.  A row tile that
+// one block covers is stored by it; the parts of a shared one go to the
+// block's two workspace slots (0: it continues what an earlier block began,
+// 1: it begins), and the join kernel adds them in order.
+#pragma once
+
+#include "kv_layout.cuh"
+
+namespace qgemv {
+
+constexpr int kMaxBlocks = 256;  // thread blocks of a call, at most
+constexpr int kSlotRows = 64;    // rows of a workspace slot, at most
+__host__ __device__ constexpr int64_t slot_floats(int D) { return static_cast<int64_t>(kSlotRows) * (D + 2); }
+
+struct TreeArgs {
+  TreeParams p;
+  int G, page_shift, min_units, grid;
+};
+
+struct SeqWork {
+  int64_t units;  // of one row tile
+  int tiles;      // row tiles of a head
+  int ctx, T;
+};
+
+// a / b of values that nearly always fit 32 bits
+__device__ __forceinline__ int64_t div_small(int64_t a, int64_t b) {
+  if (((a | b) >> 32) == 0) return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
+  return a / b;
+}
+
+template <int ROWS, int UNIT>
+__device__ __forceinline__ SeqWork seq_work(const TreeArgs& a, int b) {
+  const TreeParams& p = a.p;
+  SeqWork s;
+  const int64_t q0 = __ldg(p.cu_q + b);
+  int64_t T = __ldg(p.cu_q + b + 1) - q0;
+  if (q0 < 0 || T < 0) T = 0;
+  T = min(T, min(static_cast<int64_t>(kMaxDrafts), p.n_q - q0));
+  s.T = static_cast<int>(max(T, static_cast<int64_t>(0)));
+  s.ctx = max(0, __ldg(p.ctx_lens + b));
+  const int64_t n = min(static_cast<int64_t>(s.ctx) + s.T, p.table_stride << a.page_shift);
+  s.units = max(static_cast<int64_t>(1), (n + UNIT - 1) / UNIT);
+  s.tiles = (s.T * a.G + ROWS - 1) / ROWS;
+  return s;
+}
+
+__device__ __forceinline__ int64_t warp_total(int64_t x) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+  return x;
+}
+
+__device__ __forceinline__ int64_t run_quota(const TreeArgs& a, int64_t total) {
+  return max(static_cast<int64_t>(a.min_units), div_small(total + a.grid - 1, a.grid));
+}
+
+// A block's part of one row tile.
+struct Segment {
+  int seq, head, tile, ctx, T;
+  int64_t u0, u1, units;  // units [u0, u1) of the row tile's `units`
+  bool shared;
+};
+
+// The segments of this block, one after the other (a whole warp calls it).
+template <int ROWS, int UNIT>
+struct Cursor {
+  int64_t cur, end, base;
+  int seq;
+
+  __device__ Cursor(const TreeArgs& a) {
+    const int lane = threadIdx.x & 31, H = a.p.cache.kv_heads;
+    int64_t total = 0;
+    for (int b = lane; b < a.p.n_seqs; b += 32) {
+      const SeqWork s = seq_work<ROWS, UNIT>(a, b);
+      total += s.units * s.tiles * H;
+    }
+    total = warp_total(total);
+    const int64_t quota = run_quota(a, total);
+    cur = quota * blockIdx.x;
+    end = min(cur + quota, total);
+    seq = 0;
+    base = 0;
+    if (cur >= end) return;
+    for (int b0 = 0;; b0 += 32) {
+      int64_t mine = 0;
+      if (b0 + lane < a.p.n_seqs) {
+        const SeqWork s = seq_work<ROWS, UNIT>(a, b0 + lane);
+        mine = s.units * s.tiles * H;
+      }
+      int64_t sum = mine;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int64_t x = __shfl_up_sync(0xffffffffu, sum, o);
+        if (lane >= o) sum += x;
+      }
+      const unsigned past = __ballot_sync(0xffffffffu, base + sum > cur);
+      if (past) {
+        const int k = __ffs(past) - 1;
+        seq = b0 + k;
+        base += __shfl_sync(0xffffffffu, sum - mine, k);
+        return;
+      }
+      base += __shfl_sync(0xffffffffu, sum, 31);
+    }
+  }
+
+  __device__ bool next(const TreeArgs& a, Segment& s) {
+    const int H = a.p.cache.kv_heads;
+    while (cur < end) {
+      const SeqWork w = seq_work<ROWS, UNIT>(a, seq);
+      const int64_t in_seq = cur - base, per_seq = w.units * w.tiles * H;
+      if (in_seq >= per_seq) {
+        base += per_seq;
+        ++seq;
+        continue;
+      }
+      const int64_t item = div_small(in_seq, w.units);
+      s.seq = seq;
+      s.ctx = w.ctx;
+      s.T = w.T;
+      s.units = w.units;
+      s.u0 = in_seq - item * w.units;
+      s.u1 = min(w.units, s.u0 + (end - cur));
+      s.head = static_cast<int>(div_small(item, w.tiles));
+      s.tile = static_cast<int>(item - static_cast<int64_t>(s.head) * w.tiles);
+      s.shared = s.u0 > 0 || s.u1 < w.units;
+      cur += s.u1 - s.u0;
+      return true;
+    }
+    return false;
+  }
+};
+
+__device__ __forceinline__ float* tree_slot(const TreeParams& p, int block, bool begins, int D) {
+  return reinterpret_cast<float*>(p.ws + kWsHeaderBytes) + (2 * block + (begins ? 1 : 0)) * slot_floats(D);
+}
+
+cudaError_t launch_tree_wide(const TreeArgs& a, cudaStream_t s);
+
+}  // namespace qgemv
