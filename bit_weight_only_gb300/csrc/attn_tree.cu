@@ -650,7 +650,7 @@ __global__ void __launch_bounds__(128) tree_join_kernel(const TreeArgs a) {
   int seq = 0;
   for (int b = lane; b < p.n_seqs; b += 32) {
     const SeqWork s = seq_work<ROWS, UNIT>(a, b);
-    const int64_t w = s.units * s.tiles * H;
+    const int64_t w = (s.units + a.extra) * s.tiles * H;
     total += w;
     if (__ldg(p.cu_q + b + 1) <= token) base += w, ++seq;
   }
@@ -663,7 +663,7 @@ __global__ void __launch_bounds__(128) tree_join_kernel(const TreeArgs a) {
   if (i < 0 || i >= s.T) return;
   const int64_t quota = run_quota(a, total);
   const int r = static_cast<int>(i) * a.G + qh - head * a.G;
-  const int64_t first = base + (static_cast<int64_t>(head) * s.tiles + r / ROWS) * s.units;
+  const int64_t first = base + (static_cast<int64_t>(head) * s.tiles + r / ROWS) * (s.units + a.extra) + a.extra;
   const int b0 = static_cast<int>(div_small(first, quota)), b1 = static_cast<int>(div_small(first + s.units - 1, quota));
   if (b0 == b1) return;  // one block had it all
   float m = -INFINITY, l = 0.f, acc[D / 32];
@@ -750,11 +750,15 @@ cudaError_t launch_attn_tree(const TreeParams& p, cudaStream_t s) {
   const int64_t rows = static_cast<int64_t>(p.max_new) * a.G;
   static const int wide_from = env_int("QG_WIDE", 17);
   if (rows >= wide_from) {
-    a.min_units = 2;
+    static const int ex = env_int("QG_EXW", 3), mu = env_int("QG_MUW", 2);
+    a.extra = ex;
+    a.min_units = mu + a.extra;
     const cudaError_t e = launch_tree_wide(a, s);
     return e != cudaSuccess ? e : launch_join<64, 128>(a, s);
   }
-  a.min_units = 16;
+  static const int ex = env_int("QG_EX", 32), mu = env_int("QG_MU", 16);
+  a.extra = ex;
+  a.min_units = mu + a.extra;
   auto by_rows = [&](auto fmt, auto d) {
     constexpr int F = decltype(fmt)::value, D = decltype(d)::value;
     if (rows > 16) {

@@ -8,18 +8,18 @@
 // number of rows, rounded up to 16) and a thread's key has its scales as two
 // scalars.  A unit is 128 cached tokens (tree_work.cuh).
 //
-// Warps (16):
-//   0-3    softmax, a thread for each key: S^T from tensor memory, times the
-//          key's scale; p = exp2(s - m_r) with a reference m_r for each row
-//          that all keys share, moved (and O^T with it) only when some score
-//          passes it by 2^8 -- the four warps agree on that by one reducing
-//          barrier; p * scale(v), rounded to fp16, to shared memory
-//   4-7    K codes to fp16 in the operands' swizzle, a thread for each token
+// Warps (20):
+//   softmax (8)  two warpgroups, each for half of the rows, a thread for each
+//          key: S^T from tensor memory, times the key's scale; p = exp2(s -
+//          m_r) with a reference m_r for each row that all keys share, moved
+//          (and O^T with it) only when some score passes it by 2^8 -- the four
+//          warps agree on that by one reducing barrier; p * scale(v), rounded
+//          to fp16, to shared memory
+//   K (4)  codes to fp16 in the operands' swizzle, a thread for each token
 //          (fp16 pages need none: their blocks are copied into place)
-//   8-11   V codes likewise; in units that hold drafted tokens or end inside,
-//          whatever must not meet a masked row's 0 is taken out of V (below)
-//   12     the copies (bulk, from the pages), ahead of all
-//   13     the MMAs
+//   V (4)  likewise; in units that hold drafted tokens or end inside, whatever
+//          must not meet a masked row's 0 is taken out of V (below)
+//   copies (bulk, from the pages), ahead of all; MMAs; two that do nothing
 // INT8 codes are exact in fp16.  Q4_0: K's codes are exact too; a product for
 // each group of 32 goes to columns of its own and the key's thread adds them
 // with its four scales in fp32.  V's codes are multiplied by their group's
@@ -40,13 +40,23 @@
 namespace qgemv {
 namespace {
 
-constexpr int kThreads = 512;
+constexpr int kSoft = 2;                            // softmax warpgroups, each of kCols rows of the tile
+constexpr int kConvWarp = 4 * kSoft;                // first of the decoding warps
+constexpr int kLoadWarp = kConvWarp + 8, kMmaWarp = kLoadWarp + 1;
+constexpr int kThreads = 32 * (kConvWarp + 12);
 constexpr int kRows = 64;
+constexpr int kCols = kRows / kSoft;
 constexpr int kKeys = 128;
 constexpr int kBlocks = kKeys / kKvBlockTokens;  // cache blocks of a unit
 constexpr int kErrWide = 64;
 constexpr float kLazyW = 8.f;
 constexpr float kNone = 1e30f;  // -m of a row that has seen nothing
+
+// Notes of infinite and NaN values, of three segments in turn: when V of
+// segment s is decoded, the product of two units before is done, so the
+// softmax warpgroups have ended segment s - 3 at least.  Each warpgroup has its
+// own copy, which it clears.
+constexpr int kNotes = 3;
 
 template <int FMT, int D>
 struct Wide {
@@ -70,9 +80,9 @@ struct Wide {
   static constexpr int kM = kVsc + (kF16 ? 0 : kKs * kKeys * 4);  // float[64] -m, float[64] factors, float[4][64] x 2
   static constexpr int kRowOff = kM + 64 * 4 * 10;         // int64[64][2]: q and out offsets
   static constexpr int kRowMask = kRowOff + 64 * 16;       // uint64[64]
-  static constexpr int kKeyMask = kRowMask + 64 * 8;       // uint64[64]: the rows that see a drafted token
-  static constexpr int kBad = kKeyMask + 64 * 8;           // uint64[4][3][D]
-  static constexpr int kInts = kBad + (FMT == QGEMV_KV_INT8 ? 0 : 4 * 3 * D * 8);
+  static constexpr int kKeyMask = kRowMask + 64 * 8;       // uint32[kSoft][64]: a warpgroup's rows that see a drafted token
+  static constexpr int kBad = kKeyMask + kSoft * 64 * 4;   // uint64[kSoft][kNotes][3][D]
+  static constexpr int kInts = kBad + (FMT == QGEMV_KV_INT8 ? 0 : kSoft * kNotes * 3 * D * 8);
   static constexpr int kBars = kInts + 128;
   static constexpr int kBytes = kBars + 48 * 8 + 1024;  // + alignment
   static_assert(kBytes <= 227 * 1024, "shared memory");
@@ -93,14 +103,14 @@ __device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
   return r;
 }
 
-// OR of `pred` over the softmax warpgroup's 128 threads.
-__device__ __forceinline__ bool any_of_128(bool pred) {
+// OR of `pred` over the 128 threads of softmax warpgroup w.
+__device__ __forceinline__ bool any_of_128(int w, bool pred) {
   __syncwarp();
   uint32_t r;
   asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
-               "bar.red.or.pred q, 1, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+               "bar.red.or.pred q, %2, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
                : "=r"(r)
-               : "r"(pred ? 1u : 0u)
+               : "r"(pred ? 1u : 0u), "r"(1 + w)
                : "memory");
   return r != 0;
 }
@@ -128,16 +138,16 @@ __global__ void __launch_bounds__(kThreads, 1) tree_wide_kernel(const TreeArgs a
   float* s_l = s_red + 256;
   int64_t* s_off = reinterpret_cast<int64_t*>(smem + S::kRowOff);
   uint64_t* s_rowmask = reinterpret_cast<uint64_t*>(smem + S::kRowMask);
-  uint64_t* s_keymask = reinterpret_cast<uint64_t*>(smem + S::kKeyMask);
+  uint32_t* s_keymask = reinterpret_cast<uint32_t*>(smem + S::kKeyMask);
   unsigned long long* s_bad = reinterpret_cast<unsigned long long*>(smem + S::kBad);
   volatile int* s_int = reinterpret_cast<volatile int*>(smem + S::kInts);
   volatile int* s_abort = s_int;
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(smem + S::kInts) + 1;
-  volatile int* s_anybad = s_int + 2;   // [4]
+  volatile int* s_anybad = s_int + 2;   // [kSoft][kNotes]
   // blocks (bits) whose pages exist, of each half of a unit
-  volatile int* s_valid = s_int + 6;    // [kKs][2]
-  volatile int* s_vvalid = s_int + 12;  // [kVs], whole units (fp16)
-  volatile int* s_rvalid = s_int + 14;  // [kRs]
+  volatile int* s_valid = s_int + 8;    // [kKs][2]
+  volatile int* s_vvalid = s_int + 14;  // [kVs], whole units (fp16)
+  volatile int* s_rvalid = s_int + 16;  // [kRs]
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const unsigned full = 0xffffffffu;
@@ -149,26 +159,26 @@ __global__ void __launch_bounds__(kThreads, 1) tree_wide_kernel(const TreeArgs a
     }
     for (int i = 0; i < 3; ++i) {
       mbar_init(&bars[B::kKf + i], S::kF16 ? 1 : 128);
-      mbar_init(&bars[B::kKe + i], 5);
+      mbar_init(&bars[B::kKe + i], 1 + 4 * kSoft);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&bars[B::kVl + i], 1);
       mbar_init(&bars[B::kVf + i], 128);
       mbar_init(&bars[B::kVe + i], 1);
       mbar_init(&bars[B::kSf + i], 1);
-      mbar_init(&bars[B::kSe + i], 128);
+      mbar_init(&bars[B::kSe + i], 128 * kSoft);
     }
-    mbar_init(&bars[B::kPf], 128);
+    mbar_init(&bars[B::kPf], 128 * kSoft);
     mbar_init(&bars[B::kPv], 1);
-    mbar_init(&bars[B::kQf], 128);
+    mbar_init(&bars[B::kQf], 128 * kSoft);
     mbar_init(&bars[B::kDone], 1);
     fence_mbarrier_init();
     *s_abort = 0;
-    for (int i = 0; i < 4; ++i) s_anybad[i] = 0;
+    for (int i = 0; i < kSoft * kNotes; ++i) s_anybad[i] = 0;
   }
   if constexpr (FMT != QGEMV_KV_INT8)
-    for (int i = tid; i < 12 * D; i += kThreads) s_bad[i] = 0;
-  if (warp == 13) tmem_alloc_all(s_tmem);
+    for (int i = tid; i < kSoft * kNotes * 3 * D; i += kThreads) s_bad[i] = 0;
+  if (warp == kMmaWarp) tmem_alloc_all(s_tmem);
   tcgen_before_sync();
   __syncthreads();
   tcgen_after_sync();
@@ -196,11 +206,12 @@ __global__ void __launch_bounds__(kThreads, 1) tree_wide_kernel(const TreeArgs a
   Cursor<kRows, kKeys> work(a);
   Segment sg;
 
-  if (warp < 4) {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+  if (warp < kConvWarp) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 136;");
     // ------------------------------------------------------------ softmax --
-    const int key = tid;
-    const uint32_t t_lane = static_cast<uint32_t>(32 * warp) << 16;
+    const int wg = warp >> 2, key = tid & 127, quarter = warp & 3;
+    const int c0 = wg * kCols;  // first of this warpgroup's rows
+    const uint32_t t_lane = static_cast<uint32_t>(32 * quarter) << 16;
     const float sl = p.scale * kLog2e;
     int n_seg = 0;
     // A wait that ran out sets `dead`; the four warps go on, and leave together
@@ -211,21 +222,31 @@ __global__ void __launch_bounds__(kThreads, 1) tree_wide_kernel(const TreeArgs a
       const int R = sg.T * a.G, row0 = sg.tile * kRows, live = min(kRows, R - row0);
       const int ctx = sg.ctx, all = ctx + sg.T;
       const int64_t q0 = __ldg(p.cu_q + sg.seq);
-      // ---- rows of the tile, Q
-      if (tid < kRows) {
-        const int r = row0 + min(tid, live - 1), tok = r / a.G, h = sg.head * a.G + r - tok * a.G;
-        s_off[2 * tid] = (q0 + tok) * p.q.token_stride + h * p.q.head_stride;
-        s_off[2 * tid + 1] = (q0 + tok) * p.out.token_stride + h * p.out.head_stride;
-        s_rowmask[tid] = tid >= live ? 0 : p.masks ? p.masks[q0 + tok] : (~0ull >> (63 - tok));
-        s_nm[tid] = kNone;
+      const bool drafts = sg.u1 * kKeys > ctx;  // drafted tokens among the keys
+      // ---- this warpgroup's rows: Q, masks, references
+      if (quarter == 0) {
+        const int r = row0 + min(c0 + (lane & (kCols - 1)), live - 1), tok = r / a.G, h = sg.head * a.G + r - tok * a.G;
+        const bool on = c0 + lane < live && lane < kCols;
+        const uint64_t m = !on ? 0 : p.masks ? __ldg(reinterpret_cast<const unsigned long long*>(p.masks) + q0 + tok) : (~0ull >> (63 - tok));
+        if (lane < kCols) {
+          s_off[2 * (c0 + lane)] = (q0 + tok) * p.q.token_stride + h * p.q.head_stride;
+          s_off[2 * (c0 + lane) + 1] = (q0 + tok) * p.out.token_stride + h * p.out.head_stride;
+          s_rowmask[c0 + lane] = m;
+          s_nm[c0 + lane] = kNone;
+        }
+        if (drafts)
+          for (int i = 0; i < sg.T; ++i) {
+            const unsigned bits = __ballot_sync(full, (m >> i) & 1);
+            if (lane == 0) s_keymask[wg * kMaxDrafts + i] = bits;
+          }
       }
-      named_bar_sync(1, 128);
+      named_bar_sync(1 + wg, 128);
       {
         constexpr int U = D / 8;
         const __half* qb = static_cast<const __half*>(p.q.ptr);
-#pragma unroll 4
-        for (int it = 0; it < kRows * U / 128; ++it) {
-          const int idx = it * 128 + tid, r = idx / U, u = idx % U;
+#pragma unroll
+        for (int it = 0; it < kCols * U / 128; ++it) {
+          const int idx = it * 128 + key, r = c0 + idx / U, u = idx % U;
           uint4 w = make_uint4(0u, 0u, 0u, 0u);
           if (r < live) w = __ldg(reinterpret_cast<const uint4*>(qb + s_off[2 * r] + 8 * u));
           *reinterpret_cast<uint4*>(smem + S::kQ + (u >> 3) * (kRows * 128) + r * 128 + (((u & 7) ^ (r & 7)) << 4)) = w;
@@ -233,24 +254,36 @@ __global__ void __launch_bounds__(kThreads, 1) tree_wide_kernel(const TreeArgs a
         fence_async_smem();
         mbar_arrive(&bars[B::kQf]);
       }
-      if (sg.u1 * kKeys > ctx && tid < kMaxDrafts) {  // drafted tokens among the keys
-        uint64_t m = 0;
-        for (int r = 0; r < live; ++r) m |= ((s_rowmask[r] >> tid) & 1ull) << r;
-        s_keymask[tid] = m;
-      }
-      named_bar_sync(1, 128);
+      const bool busy = c0 < live;  // this warpgroup has rows
 
-      uint64_t l2[kRows / 2];
+      uint64_t l2[kCols / 2];
 #pragma unroll
-      for (int i = 0; i < kRows / 2; ++i) l2[i] = 0;
+      for (int i = 0; i < kCols / 2; ++i) l2[i] = 0;
       const int n = static_cast<int>(sg.u1 - sg.u0);
-      const int groups16 = (live + 15) >> 4;
       for (int j = 0; j < n; ++j, ++jt) {
         const int ks = jt % S::kKs, sb = jt % S::kSBufs;
         dead |= !wait(B::kKf + ks, used(jt, S::kKs)) || !wait(B::kSf + sb, used(jt, S::kSBufs));
         __syncwarp();
         tcgen_after_sync();
+        if (!busy) {
+          mbar_arrive(&bars[B::kSe + sb]);
+          if (lane == 0) mbar_arrive(&bars[B::kKe + ks]);
+          // not before the product of the unit before: S may be a unit ahead of
+          // the other warpgroup's P, and this would count for that one
+          if (jt > 0) dead |= !wait(B::kPv, (jt - 1) & 1);
+          mbar_arrive(&bars[B::kPf]);
+          if (any_of_128(wg, dead)) {
+            left = true;
+            break;
+          }
+          continue;
+        }
         // ---- S of this key
+        const uint32_t t_s = tbase + t_lane + sb * S::kGroups * kRows + c0;
+        constexpr int LC = S::kGroups > 1 ? 16 : kCols;  // columns loaded at a time
+        uint32_t raw[S::kGroups][LC];
+#pragma unroll
+        for (int g = 0; g < S::kGroups; ++g) tmem_ld<LC>(t_s + g * kRows, raw[g]);
         float ksc[4] = {1.f, 1.f, 1.f, 1.f};
         float vs = 1.f, lv = 0.f;
         if constexpr (FMT == QGEMV_KV_INT8) {
@@ -264,20 +297,26 @@ __global__ void __launch_bounds__(kThreads, 1) tree_wide_kernel(const TreeArgs a
           lv = __log2f(fmaxf(vs, 7.9e-31f));  // 2^-100
         }
         const bool there = (s_valid[2 * ks + (key >> 6)] >> ((key >> 4) & 3)) & 1;
-        uint64_t x2[kRows / 2];
-        uint32_t raw[32];
+        const int64_t pos = (sg.u0 + j) * kKeys + key;
+        uint32_t vis = 0;  // the rows that see this key
+        if (there) vis = pos < ctx ? ~0u : pos < all ? s_keymask[wg * kMaxDrafts + (pos - ctx)] : 0u;
+        uint64_t x2[kCols / 2];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
+        for (int h = 0; h < kCols / LC; ++h) {
+          if (h > 0) {
+#pragma unroll
+            for (int g = 0; g < S::kGroups; ++g) tmem_ld<LC>(t_s + g * kRows + h * LC, raw[g]);
+          }
 #pragma unroll
           for (int g = 0; g < S::kGroups; ++g) {
-            tmem_ld32(tbase + t_lane + (sb * S::kGroups + g) * kRows + 32 * h, raw);
-            tmem_wait_ld32(raw);
+            tmem_wait_ld<LC>(raw[g]);
             const float f = ksc[g] * sl;
             const uint64_t f2 = pack2(f, f);
 #pragma unroll
-            for (int c = 0; c < 16; ++c) {
-              const uint64_t v = pack2(__uint_as_float(raw[2 * c]), __uint_as_float(raw[2 * c + 1]));
-              x2[16 * h + c] = g == 0 ? mul2(v, f2) : fma2(v, f2, x2[16 * h + c]);
+            for (int c = 0; c < LC / 2; ++c) {
+              const uint64_t v = pack2(__uint_as_float(raw[g][2 * c]), __uint_as_float(raw[g][2 * c + 1]));
+              uint64_t& x = x2[h * (LC / 2) + c];
+              x = g == 0 ? mul2(v, f2) : fma2(v, f2, x);
             }
           }
         }
@@ -285,14 +324,10 @@ __global__ void __launch_bounds__(kThreads, 1) tree_wide_kernel(const TreeArgs a
         mbar_arrive(&bars[B::kSe + sb]);
         __syncwarp();
         if (lane == 0) mbar_arrive(&bars[B::kKe + ks]);
-        // ---- what sees this key
-        const int64_t pos = (sg.u0 + j) * kKeys + key;
-        uint64_t vis = 0;
-        if (there) vis = pos < ctx ? ~0ull : pos < all ? s_keymask[pos - ctx] : 0ull;
-        const bool some_masked = __any_sync(full, vis != ~0ull);
+        const bool some_masked = __any_sync(full, vis != ~0u);
         if (some_masked) {
 #pragma unroll
-          for (int i = 0; i < kRows / 2; ++i) {
+          for (int i = 0; i < kCols / 2; ++i) {
             float x, y;
             unpack2(x2[i], x, y);
             if (!((vis >> (2 * i)) & 1)) x = -INFINITY;
@@ -302,42 +337,42 @@ __global__ void __launch_bounds__(kThreads, 1) tree_wide_kernel(const TreeArgs a
           if (vis == 0) vs = 0.f, lv = -100.f;
         }
         // ---- the rows' references
-        float top = -INFINITY;
+        float top[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-        for (int i = 0; i < kRows / 4; ++i) {
-          if ((i >> 2) >= groups16) break;
-          const ulonglong2 nm = *reinterpret_cast<const ulonglong2*>(s_nm + 4 * i);
+        for (int i = 0; i < kCols / 4; ++i) {
+          const ulonglong2 nm = *reinterpret_cast<const ulonglong2*>(s_nm + c0 + 4 * i);
           float x, y, z, w;
           unpack2(add2(x2[2 * i], nm.x), x, y);
           unpack2(add2(x2[2 * i + 1], nm.y), z, w);
-          top = fmaxf(top, fmaxf(fmaxf(x, y), fmaxf(z, w)));
+          top[0] = fmaxf(top[0], fmaxf(x, y));
+          top[1] = fmaxf(top[1], fmaxf(z, w));
         }
-        if (any_of_128(dead || top + lv > kLazyW)) {
-          if (any_of_128(dead)) {
+        if (any_of_128(wg, dead || fmaxf(top[0], top[1]) + lv > kLazyW)) {
+          if (any_of_128(wg, dead)) {
             left = true;
             break;
           }
 #pragma unroll
-          for (int i = 0; i < kRows / 2; ++i) {
-            if ((i >> 3) >= groups16) break;
+          for (int i = 0; i < kCols / 2; ++i) {
             float x, y;
             unpack2(x2[i], x, y);
             x = warp_max(x + lv);
             y = warp_max(y + lv);
-            if (lane == (i & 31)) *reinterpret_cast<float2*>(s_red + 64 * warp + 2 * i) = make_float2(x, y);
+            if (lane == i) *reinterpret_cast<float2*>(s_red + 64 * quarter + c0 + 2 * i) = make_float2(x, y);
           }
-          named_bar_sync(1, 128);
-          if (tid < kRows) {
-            const float m = -s_nm[tid];
-            const float mx = fmaxf(fmaxf(s_red[tid], s_red[64 + tid]), fmaxf(s_red[128 + tid], s_red[192 + tid]));
+          named_bar_sync(1 + wg, 128);
+          if (key < kCols) {
+            const int r = c0 + key;
+            const float m = -s_nm[r];
+            const float mx = fmaxf(fmaxf(s_red[r], s_red[64 + r]), fmaxf(s_red[128 + r], s_red[192 + r]));
             const float mn = fmaxf(m, mx);
-            s_f[tid] = m == -kNone ? 0.f : ex2(m - mn);
-            s_nm[tid] = -mn;
+            s_f[r] = m == -kNone ? 0.f : ex2(m - mn);
+            s_nm[r] = -mn;
           }
-          named_bar_sync(1, 128);
+          named_bar_sync(1 + wg, 128);
 #pragma unroll
-          for (int i = 0; i < kRows / 4; ++i) {
-            const ulonglong2 f = *reinterpret_cast<const ulonglong2*>(s_f + 4 * i);
+          for (int i = 0; i < kCols / 4; ++i) {
+            const ulonglong2 f = *reinterpret_cast<const ulonglong2*>(s_f + c0 + 4 * i);
             l2[2 * i] = mul2(l2[2 * i], f.x);
             l2[2 * i + 1] = mul2(l2[2 * i + 1], f.y);
           }
@@ -345,36 +380,33 @@ __global__ void __launch_bounds__(kThreads, 1) tree_wide_kernel(const TreeArgs a
             dead |= !wait(B::kPv, (jt - 1) & 1);
             __syncwarp();
             tcgen_after_sync();
+            uint32_t o[kCols];
+            tmem_ld<kCols>(tbase + t_lane + S::kOCol + c0, o);
+            tmem_wait_ld<kCols>(o);
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              tmem_ld32(tbase + t_lane + S::kOCol + 32 * h, raw);
-              tmem_wait_ld32(raw);
-#pragma unroll
-              for (int c = 0; c < 16; ++c) {
-                float x, y;
-                unpack2(mul2(pack2(__uint_as_float(raw[2 * c]), __uint_as_float(raw[2 * c + 1])),
-                             reinterpret_cast<const uint64_t*>(s_f)[16 * h + c]),
-                        x, y);
-                raw[2 * c] = __float_as_uint(x), raw[2 * c + 1] = __float_as_uint(y);
-              }
-              tmem_st32(tbase + t_lane + S::kOCol + 32 * h, raw);
+            for (int c = 0; c < kCols / 2; ++c) {
+              float x, y;
+              unpack2(mul2(pack2(__uint_as_float(o[2 * c]), __uint_as_float(o[2 * c + 1])),
+                           reinterpret_cast<const uint64_t*>(s_f + c0)[c]),
+                      x, y);
+              o[2 * c] = __float_as_uint(x), o[2 * c + 1] = __float_as_uint(y);
             }
+            tmem_st<kCols>(tbase + t_lane + S::kOCol + c0, o);
             tmem_wait_store();
           }
         }
         // ---- P
-        uint32_t w2[kRows / 2];
+        uint32_t w2[kCols / 2];
         const uint64_t vs2 = pack2(vs, vs);
 #pragma unroll
-        for (int i = 0; i < kRows / 4; ++i) {
-          if ((i >> 2) >= groups16) break;
-          const ulonglong2 nm = *reinterpret_cast<const ulonglong2*>(s_nm + 4 * i);
+        for (int i = 0; i < kCols / 4; ++i) {
+          const ulonglong2 nm = *reinterpret_cast<const ulonglong2*>(s_nm + c0 + 4 * i);
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
             float x, y;
             unpack2(add2(x2[2 * i + e], e ? nm.y : nm.x), x, y);
             x = ex2(x), y = ex2(y);
-            uint64_t pp = pack2(x, y);
+            const uint64_t pp = pack2(x, y);
             l2[2 * i + e] = add2(l2[2 * i + e], pp);
             if constexpr (!S::kF16) {
               unpack2(mul2(pp, vs2), x, y);
@@ -388,11 +420,9 @@ __global__ void __launch_bounds__(kThreads, 1) tree_wide_kernel(const TreeArgs a
         }
         if (jt > 0) dead |= !wait(B::kPv, (jt - 1) & 1);  // the product before has read P
 #pragma unroll
-        for (int u = 0; u < kRows / 8; ++u) {
-          if ((u >> 1) >= groups16) break;
-          *reinterpret_cast<uint4*>(smem + S::kP + key * 128 + ((u ^ (key & 7)) << 4)) =
+        for (int u = 0; u < kCols / 8; ++u)
+          *reinterpret_cast<uint4*>(smem + S::kP + key * 128 + (((c0 / 8 + u) ^ (key & 7)) << 4)) =
               make_uint4(w2[4 * u], w2[4 * u + 1], w2[4 * u + 2], w2[4 * u + 3]);
-        }
         fence_async_smem();
         tcgen_before_sync();
         mbar_arrive(&bars[B::kPf]);
@@ -400,92 +430,95 @@ __global__ void __launch_bounds__(kThreads, 1) tree_wide_kernel(const TreeArgs a
       if (left) break;
       // ---- the segment's end: l over the keys, O^T
       dead |= !wait(B::kPv, (jt - 1) & 1);
-      if (any_of_128(dead)) break;
+      if (any_of_128(wg, dead)) break;
       tcgen_after_sync();
-      {
-        // Each step halves the rows a lane holds: lane i ends with rows 2i, 2i + 1.
-        float l[kRows];
+      float* slot = tree_slot(p, blockIdx.x, sg.u0 == 0, D);
+      const int bb = wg * kNotes + n_seg % kNotes;
+      const bool bad = FMT != QGEMV_KV_INT8 && s_anybad[bb] != 0;
+      if (busy) {
+        {
+          // Each step halves the rows a lane holds: lane i ends with row i
+          // (of 16 rows: lanes 2i and 2i + 1, half of the keys each).
+          float l[kCols];
 #pragma unroll
-        for (int i = 0; i < kRows / 2; ++i) unpack2(l2[i], l[2 * i], l[2 * i + 1]);
+          for (int i = 0; i < kCols / 2; ++i) unpack2(l2[i], l[2 * i], l[2 * i + 1]);
 #pragma unroll
-        for (int o = 16, h = kRows / 2; o > 0; o >>= 1, h >>= 1) {
+          for (int o = 16, h = kCols / 2; h > 0; o >>= 1, h >>= 1) {
 #pragma unroll
-          for (int i = 0; i < h; ++i) {
-            const bool up = lane & o;
-            const float give = up ? l[i] : l[i + h], keep = up ? l[i + h] : l[i];
-            l[i] = keep + __shfl_xor_sync(full, give, o);
+            for (int i = 0; i < h; ++i) {
+              const bool up = lane & o;
+              const float give = up ? l[i] : l[i + h], keep = up ? l[i + h] : l[i];
+              l[i] = keep + __shfl_xor_sync(full, give, o);
+            }
+          }
+          if (kCols == 16) l[0] += __shfl_xor_sync(full, l[0], 1);
+          if (kCols == 32 || !(lane & 1)) s_l[64 * quarter + c0 + (kCols == 32 ? lane : lane >> 1)] = l[0];
+        }
+        named_bar_sync(1 + wg, 128);
+        if (key < kCols) {
+          const int r = c0 + key;
+          const float l = (s_l[r] + s_l[64 + r]) + (s_l[128 + r] + s_l[192 + r]);
+          const float nm = s_nm[r], m = nm == kNone ? -INFINITY : -nm;
+          s_f[r] = sg.shared ? 1.f : l == 0.f ? 0.f : 1.f / l;
+          if (sg.shared) {
+            *reinterpret_cast<float2*>(slot + kSlotRows * D + 2 * r) = make_float2(m, l);
+          } else if (p.lse && r < live) {
+            const int rr = row0 + r, tok = rr / a.G;
+            p.lse[(q0 + tok) * p.q_heads + sg.head * a.G + rr - tok * a.G] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
           }
         }
-        s_l[64 * warp + 2 * lane] = l[0];
-        s_l[64 * warp + 2 * lane + 1] = l[1];
-      }
-      named_bar_sync(1, 128);
-      float* slot = tree_slot(p, blockIdx.x, sg.u0 == 0, D);
-      if (tid < kRows) {
-        const float l = (s_l[tid] + s_l[64 + tid]) + (s_l[128 + tid] + s_l[192 + tid]);
-        const float nm = s_nm[tid], m = nm == kNone ? -INFINITY : -nm;
-        s_f[tid] = sg.shared ? 1.f : l == 0.f ? 0.f : 1.f / l;
-        if (sg.shared) {
-          *reinterpret_cast<float2*>(slot + kSlotRows * D + 2 * tid) = make_float2(m, l);
-        } else if (p.lse && tid < live) {
-          const int r = row0 + tid, tok = r / a.G;
-          p.lse[(q0 + tok) * p.q_heads + sg.head * a.G + r - tok * a.G] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
-        }
-      }
-      named_bar_sync(1, 128);
-      const int bb = n_seg & 3;
-      const bool bad = FMT != QGEMV_KV_INT8 && s_anybad[bb] != 0;
-      __half* outb = static_cast<__half*>(p.out.ptr);
+        named_bar_sync(1 + wg, 128);
+        uint32_t o[kCols];
+        tmem_ld<kCols>(tbase + t_lane + S::kOCol + c0, o);
+        tmem_wait_ld<kCols>(o);
+        __half* outb = static_cast<__half*>(p.out.ptr);
+        if (key < D) {
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        uint32_t raw[32];
-        tmem_ld32(tbase + t_lane + S::kOCol + 32 * h, raw);
-        tmem_wait_ld32(raw);
-        if (tid < D) {
-#pragma unroll
-          for (int c = 0; c < 32; ++c) {
-            const int r = 32 * h + c;
+          for (int c = 0; c < kCols; ++c) {
+            const int r = c0 + c;
             if (r < live) {
-              float x = __uint_as_float(raw[c]) * s_f[r];
+              float x = __uint_as_float(o[c]) * s_f[r];
               if (FMT != QGEMV_KV_INT8 && bad) {
-                const unsigned long long* bd = s_bad + bb * 3 * D + tid;
+                const unsigned long long* bd = s_bad + bb * 3 * D + key;
                 const uint64_t rm = s_rowmask[r];
                 const bool nan = bd[0] & rm, up = bd[D] & rm, down = bd[2 * D] & rm;
                 if (nan || (up && down)) x = __int_as_float(0x7fffffff);
                 else if (up) x += INFINITY;
                 else if (down) x -= INFINITY;
               }
-              if (sg.shared) slot[r * D + tid] = x;
-              else outb[s_off[2 * r + 1] + tid] = __float2half_rn(x);
+              if (sg.shared) slot[r * D + key] = x;
+              else outb[s_off[2 * r + 1] + key] = __float2half_rn(x);
             }
           }
         }
+        tcgen_before_sync();
       }
-      tcgen_before_sync();
-      named_bar_sync(1, 128);
+      named_bar_sync(1 + wg, 128);
       if (FMT != QGEMV_KV_INT8 && bad) {
-        for (int i = tid; i < 3 * D; i += 128) s_bad[bb * 3 * D + i] = 0;
-        if (tid == 0) s_anybad[bb] = 0;
+        for (int i = key; i < 3 * D; i += 128) s_bad[bb * 3 * D + i] = 0;
+        if (key == 0) s_anybad[bb] = 0;
       }
       ++n_seg;
     }
-  } else if (warp < 12) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
+  } else if (warp < kLoadWarp) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
     // ----------------------------------------------- codes to operands ----
     const int key = tid & 127, half = key >> 6;
-    const bool is_v = warp >= 8;
+    const bool is_v = warp >= kConvWarp + 4;
     int n_seg = 0;
     bool ok = !(S::kF16 && !is_v);
     while (ok && work.next(a, sg)) {
       const int n = static_cast<int>(sg.u1 - sg.u0), ctx = sg.ctx, all = ctx + sg.T;
-      const int bb = n_seg & 3;
+      const int bb = n_seg % kNotes;
       for (int j = 0; j < n; ++j, ++jt) {
         const int64_t pos = (sg.u0 + j) * kKeys + key;
         const int ks = jt % S::kKs, vst = jt % S::kVs;
         uint8_t* dst = smem + (is_v ? S::kV + vst * S::kTile : S::kK + ks * S::kTile) + key * 128;
         auto note = [&](int d, int kind) {  // a drafted token's value that is infinite or NaN
-          atomicOr(&s_bad[(bb * 3 + kind) * D + d], 1ull << (pos - ctx));
-          s_anybad[bb] = 1;
+          for (int w = 0; w < kSoft; ++w) {
+            atomicOr(&s_bad[((w * kNotes + bb) * 3 + kind) * D + d], 1ull << (pos - ctx));
+            s_anybad[w * kNotes + bb] = 1;
+          }
         };
         if constexpr (S::kF16) {
           ok = wait(B::kVl + vst, used(jt, S::kVs));
@@ -628,8 +661,8 @@ __global__ void __launch_bounds__(kThreads, 1) tree_wide_kernel(const TreeArgs a
       ++n_seg;
     }
   } else {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
-    if (warp == 12) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+    if (warp == kLoadWarp) {
       // -------------------------------------------------------- copies ----
       int64_t n_raw = 0;
       int issued_k = 0, issued_v = 0;
@@ -711,7 +744,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_wide_kernel(const TreeArgs a
         for (int64_t n = max(static_cast<int64_t>(0), n_raw - S::kRs); n < n_raw; ++n)
           mbar_wait_bounded(&bars[B::kRf + static_cast<int>(n % S::kRs)], used(n, S::kRs));
       }
-    } else if (warp == 13) {
+    } else if (warp == kMmaWarp) {
       // ---------------------------------------------------------- MMAs ----
       int n_seg = 0;
       bool ok = true;
@@ -765,7 +798,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_wide_kernel(const TreeArgs a
     }
   }
   __syncthreads();
-  if (warp == 13) tmem_free_all(tbase);
+  if (warp == kMmaWarp) tmem_free_all(tbase);
 }
 
 template <int FMT, int D>

@@ -3,7 +3,10 @@
 //
 // The work is a list of units -- UNIT cached tokens for one tile of ROWS rows
 // -- ordered (sequence, head, row tile, position).  Each thread block takes an
-// equal run of it; a run's part of one row tile is a segment.  A row tile that
+// equal run of it; a run's part of one row tile is a segment.  A row tile
+// costs more than its units (Q, the start and end of the softmax): it counts
+// as `extra` units more, which come first and stand for no tokens, so that
+// blocks whose sequences are short get fewer of them.  A row tile that
 // one block covers is stored by it; the parts of a shared one go to the
 // block's two workspace slots (0: it continues what an earlier block began,
 // 1: it begins), and the join kernel adds them in order.
@@ -19,7 +22,7 @@ __host__ __device__ constexpr int64_t slot_floats(int D) { return static_cast<in
 
 struct TreeArgs {
   TreeParams p;
-  int G, page_shift, min_units, grid;
+  int G, page_shift, min_units, extra, grid;
 };
 
 struct SeqWork {
@@ -78,7 +81,7 @@ struct Cursor {
     int64_t total = 0;
     for (int b = lane; b < a.p.n_seqs; b += 32) {
       const SeqWork s = seq_work<ROWS, UNIT>(a, b);
-      total += s.units * s.tiles * H;
+      total += (s.units + a.extra) * s.tiles * H;
     }
     total = warp_total(total);
     const int64_t quota = run_quota(a, total);
@@ -91,7 +94,7 @@ struct Cursor {
       int64_t mine = 0;
       if (b0 + lane < a.p.n_seqs) {
         const SeqWork s = seq_work<ROWS, UNIT>(a, b0 + lane);
-        mine = s.units * s.tiles * H;
+        mine = (s.units + a.extra) * s.tiles * H;
       }
       int64_t sum = mine;
 #pragma unroll
@@ -114,23 +117,25 @@ struct Cursor {
     const int H = a.p.cache.kv_heads;
     while (cur < end) {
       const SeqWork w = seq_work<ROWS, UNIT>(a, seq);
-      const int64_t in_seq = cur - base, per_seq = w.units * w.tiles * H;
+      const int64_t in_seq = cur - base, cost = w.units + a.extra, per_seq = cost * w.tiles * H;
       if (in_seq >= per_seq) {
         base += per_seq;
         ++seq;
         continue;
       }
-      const int64_t item = div_small(in_seq, w.units);
+      const int64_t item = div_small(in_seq, cost);
+      const int64_t v0 = in_seq - item * cost, v1 = min(cost, v0 + (end - cur));
+      cur += v1 - v0;
+      s.u0 = max(static_cast<int64_t>(0), v0 - a.extra);
+      s.u1 = v1 - a.extra;
+      if (s.u1 <= s.u0) continue;
       s.seq = seq;
       s.ctx = w.ctx;
       s.T = w.T;
       s.units = w.units;
-      s.u0 = in_seq - item * w.units;
-      s.u1 = min(w.units, s.u0 + (end - cur));
       s.head = static_cast<int>(div_small(item, w.tiles));
       s.tile = static_cast<int>(item - static_cast<int64_t>(s.head) * w.tiles);
       s.shared = s.u0 > 0 || s.u1 < w.units;
-      cur += s.u1 - s.u0;
       return true;
     }
     return false;
