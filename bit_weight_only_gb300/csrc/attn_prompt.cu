@@ -186,7 +186,8 @@ prompt_kernel(const PromptArgs a, const __grid_constant__ CUtensorMap kmap, cons
       }
     } else if (warp == 9) {
       // ---- MMAs
-      if (lane == 0 && n_max > 0) {
+      const bool leader = elect_one();
+      if (n_max > 0) {
         constexpr uint32_t id_qk = mma_idesc(BF16, false, false, kKeys), id_pv = mma_idesc(BF16, false, true, D);
         const uint32_t sq = smem_u32(smem + S::kQ), sk = smem_u32(smem + S::kK), sv = smem_u32(smem + S::kV);
         auto qk = [&](int i, int j) {
@@ -195,49 +196,51 @@ prompt_kernel(const PromptArgs a, const __grid_constant__ CUtensorMap kmap, cons
 #pragma unroll
           for (int k = 0; k < D / 16; ++k) {
             const uint32_t o = ((k >> 2) * kChunk + (k & 3) * 32) >> 4;
-            mma_ss(tbase + 128 * i, da + o, db + o, id_qk, k > 0);
+            mma_ss(tbase + 128 * i, da + o, db + o, id_qk, k > 0, leader);
           }
-          mma_commit(&bars[kBS + i]);
+          mma_commit(&bars[kBS + i], leader);
         };
         auto pv = [&](int i, int j) {
           const uint64_t db = sw128_desc(sv + (j & 1) * S::kTile, kChunk, 1024);
 #pragma unroll
           for (int k = 0; k < kKeys / 16; ++k)
-            mma_ts(tbase + 256 + 128 * i, tbase + 128 * i + 8 * k, db + ((k * 2048) >> 4), id_pv, j > 0 || k > 0);
+            mma_ts(tbase + 256 + 128 * i, tbase + 128 * i + 8 * k, db + ((k * 2048) >> 4), id_pv, j > 0 || k > 0, leader);
         };
-        bool ok = wait(kBKf, 0);
+        // every lane waits; a lane whose wait ran out stops them all
+        auto wait_all = [&](int bar, uint32_t parity) { return __all_sync(0xffffffffu, wait(bar, parity)) != 0; };
+        bool ok = wait_all(kBKf, 0);
         for (int i = 0; i < 2; ++i)
           if (ok && n_tiles[i] > 0) {
-            ok = wait(kBQ + i, 0);
+            ok = wait_all(kBQ + i, 0);
             tcgen_after_sync();
             if (ok) qk(i, 0);
           }
-        if (ok) mma_commit(&bars[kBKe]);
+        if (ok) mma_commit(&bars[kBKe], leader);
         for (int j = 0; ok && j < n_max; ++j) {
           bool have_v = false, have_k = false;
           for (int i = 0; ok && i < 2; ++i) {
             if (j >= n_tiles[i]) continue;
-            if (!have_v) ok = wait((j >= first_masked ? kBFix : kBVf) + (j & 1), v_parity(j));
+            if (!have_v) ok = wait_all((j >= first_masked ? kBFix : kBVf) + (j & 1), v_parity(j));
             have_v = true;
-            if (ok) ok = wait(kBP + i, j & 1);
+            if (ok) ok = wait_all(kBP + i, j & 1);
             if (!ok) break;
             tcgen_after_sync();
             pv(i, j);
             if (j + 1 < n_tiles[i]) {
-              if (!have_k) ok = wait(kBKf + ((j + 1) & 1), ((j + 1) >> 1) & 1);
+              if (!have_k) ok = wait_all(kBKf + ((j + 1) & 1), ((j + 1) >> 1) & 1);
               have_k = true;
               if (ok) qk(i, j + 1);
             } else {
-              mma_commit(&bars[kBO + i]);
+              mma_commit(&bars[kBO + i], leader);
             }
           }
           if (ok) {
-            mma_commit(&bars[kBVe + (j & 1)]);
-            if (have_k) mma_commit(&bars[kBKe + ((j + 1) & 1)]);
+            mma_commit(&bars[kBVe + (j & 1)], leader);
+            if (have_k) mma_commit(&bars[kBKe + ((j + 1) & 1)], leader);
           }
         }
         if (!ok) {  // MMAs in flight: let them finish before tensor memory is freed
-          mma_commit(&bars[kBDone]);
+          mma_commit(&bars[kBDone], leader);
           mbar_wait_bounded(&bars[kBDone], 0);
         }
       }

@@ -746,54 +746,54 @@ __global__ void __launch_bounds__(kThreads, 1) tree_wide_kernel(const TreeArgs a
       }
     } else if (warp == kMmaWarp) {
       // ---------------------------------------------------------- MMAs ----
+      const bool leader = elect_one();
       int n_seg = 0;
       bool ok = true;
       const uint32_t sk = smem_u32(smem + S::kK), sv = smem_u32(smem + S::kV), sq = smem_u32(smem + S::kQ),
                      sp = smem_u32(smem + S::kP);
+      // every lane waits; a lane whose wait ran out stops them all
+      auto wait_all = [&](int bar, uint32_t parity) { return __all_sync(full, wait(bar, parity)) != 0; };
       while (ok && work.next(a, sg)) {
         const int n = static_cast<int>(sg.u1 - sg.u0);
-        if (lane == 0) {
-          const int live = min(kRows, sg.T * a.G - sg.tile * kRows), N = (live + 15) & ~15;
-          const uint32_t id_qk = mma_idesc(false, false, false, N), id_pv = mma_idesc(false, true, true, N);
-          auto qk = [&](int x) -> bool {
-            const int ks = x % S::kKs, sb = x % S::kSBufs;
-            if (!wait(B::kKf + ks, used(x, S::kKs))) return false;
-            if (x >= S::kSBufs && !wait(B::kSe + sb, freed(x, S::kSBufs))) return false;
-            tcgen_after_sync();
-            const uint64_t da = sw128_desc(sk + ks * S::kTile, 0, 1024), db = sw128_desc(sq, 0, 1024);
+        const int live = min(kRows, sg.T * a.G - sg.tile * kRows), N = (live + 15) & ~15;
+        const uint32_t id_qk = mma_idesc(false, false, false, N), id_pv = mma_idesc(false, true, true, N);
+        auto qk = [&](int x) -> bool {
+          const int ks = x % S::kKs, sb = x % S::kSBufs;
+          if (!wait_all(B::kKf + ks, used(x, S::kKs))) return false;
+          if (x >= S::kSBufs && !wait_all(B::kSe + sb, freed(x, S::kSBufs))) return false;
+          tcgen_after_sync();
+          const uint64_t da = sw128_desc(sk + ks * S::kTile, 0, 1024), db = sw128_desc(sq, 0, 1024);
 #pragma unroll
-            for (int k = 0; k < D / 16; ++k) {
-              const int g = S::kGroups == 1 ? 0 : k >> 1;
-              const uint32_t oa = ((k >> 2) * (kKeys * 128) + (k & 3) * 32) >> 4;
-              const uint32_t ob = ((k >> 2) * (kRows * 128) + (k & 3) * 32) >> 4;
-              mma_ss(tbase + (sb * S::kGroups + g) * kRows, da + oa, db + ob, id_qk, S::kGroups == 1 ? k > 0 : (k & 1) != 0);
-            }
-            mma_commit(&bars[B::kSf + sb]);
-            mma_commit(&bars[B::kKe + ks]);
-            return true;
-          };
-          ok = wait(B::kQf, n_seg & 1) && qk(jt);
-          for (int j = 0; ok && j < n; ++j) {
-            const int x = jt + j, vst = x % S::kVs;
-            if (j + 1 < n) ok = qk(x + 1);
-            ok = ok && wait(B::kVf + vst, used(x, S::kVs)) && wait(B::kPf, x & 1);
-            if (!ok) break;
-            tcgen_after_sync();
-            const uint64_t da = sw128_desc(sv + vst * S::kTile, kKeys * 128, 1024), db = sw128_desc(sp, 0, 1024);
+          for (int k = 0; k < D / 16; ++k) {
+            const int g = S::kGroups == 1 ? 0 : k >> 1;
+            const uint32_t oa = ((k >> 2) * (kKeys * 128) + (k & 3) * 32) >> 4;
+            const uint32_t ob = ((k >> 2) * (kRows * 128) + (k & 3) * 32) >> 4;
+            mma_ss(tbase + (sb * S::kGroups + g) * kRows, da + oa, db + ob, id_qk, S::kGroups == 1 ? k > 0 : (k & 1) != 0, leader);
+          }
+          mma_commit(&bars[B::kSf + sb], leader);
+          mma_commit(&bars[B::kKe + ks], leader);
+          return true;
+        };
+        ok = wait_all(B::kQf, n_seg & 1) && qk(jt);
+        for (int j = 0; ok && j < n; ++j) {
+          const int x = jt + j, vst = x % S::kVs;
+          if (j + 1 < n) ok = qk(x + 1);
+          ok = ok && wait_all(B::kVf + vst, used(x, S::kVs)) && wait_all(B::kPf, x & 1);
+          if (!ok) break;
+          tcgen_after_sync();
+          const uint64_t da = sw128_desc(sv + vst * S::kTile, kKeys * 128, 1024), db = sw128_desc(sp, 0, 1024);
 #pragma unroll
-            for (int k = 0; k < kKeys / 16; ++k)
-              mma_ss(tbase + S::kOCol, da + ((k * 2048) >> 4), db + ((k * 2048) >> 4), id_pv, j > 0 || k > 0);
-            mma_commit(&bars[B::kPv]);
-            mma_commit(&bars[B::kVe + vst]);
-          }
-          if (!ok) {  // MMAs in flight: let them finish before tensor memory is freed
-            mma_commit(&bars[B::kDone]);
-            mbar_wait_bounded(&bars[B::kDone], 0);
-          }
+          for (int k = 0; k < kKeys / 16; ++k)
+            mma_ss(tbase + S::kOCol, da + ((k * 2048) >> 4), db + ((k * 2048) >> 4), id_pv, j > 0 || k > 0, leader);
+          mma_commit(&bars[B::kPv], leader);
+          mma_commit(&bars[B::kVe + vst], leader);
         }
-        ok = __shfl_sync(full, ok ? 1 : 0, 0) != 0;
         jt += n;
         ++n_seg;
+      }
+      if (!ok) {  // MMAs in flight: let them finish before tensor memory is freed
+        mma_commit(&bars[B::kDone], leader);
+        mbar_wait_bounded(&bars[B::kDone], 0);
       }
     }
   }
