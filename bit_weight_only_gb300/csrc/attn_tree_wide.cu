@@ -8,8 +8,8 @@
 // number of rows, rounded up to 16) and a thread's key has its scales as two
 // scalars.  A unit is 128 cached tokens (tree_work.cuh).
 //
-// Warps (20):
-//   softmax (8)  two warpgroups, each for half of the rows, a thread for each
+// Warps (28):
+//   softmax (16)  four warpgroups, each for 16 of the rows, a thread for each
 //          key: S^T from tensor memory, times the key's scale; p = exp2(s -
 //          m_r) with a reference m_r for each row that all keys share, moved
 //          (and O^T with it) only when some score passes it by 2^8 -- the four
@@ -40,7 +40,7 @@
 namespace qgemv {
 namespace {
 
-constexpr int kSoft = 2;                            // softmax warpgroups, each of kCols rows of the tile
+constexpr int kSoft = 4;                            // softmax warpgroups, each of kCols rows of the tile
 constexpr int kConvWarp = 4 * kSoft;                // first of the decoding warps
 constexpr int kLoadWarp = kConvWarp + 8, kMmaWarp = kLoadWarp + 1;
 constexpr int kThreads = 32 * (kConvWarp + 12);
@@ -52,10 +52,10 @@ constexpr int kErrWide = 64;
 constexpr float kLazyW = 8.f;
 constexpr float kNone = 1e30f;  // -m of a row that has seen nothing
 
-// Notes of infinite and NaN values, of three segments in turn: when V of
-// segment s is decoded, the product of two units before is done, so the
-// softmax warpgroups have ended segment s - 3 at least.  Each warpgroup has its
-// own copy, which it clears.
+// Notes of infinite and NaN values, of three segments in turn: when the first V
+// of segment s is decoded, the product of two units before is done, so the
+// softmax warpgroups have ended segment s - 3 at least, and the V warps clear
+// its notes.
 constexpr int kNotes = 3;
 
 template <int FMT, int D>
@@ -81,8 +81,8 @@ struct Wide {
   static constexpr int kRowOff = kM + 64 * 4 * 10;         // int64[64][2]: q and out offsets
   static constexpr int kRowMask = kRowOff + 64 * 16;       // uint64[64]
   static constexpr int kKeyMask = kRowMask + 64 * 8;       // uint32[kSoft][64]: a warpgroup's rows that see a drafted token
-  static constexpr int kBad = kKeyMask + kSoft * 64 * 4;   // uint64[kSoft][kNotes][3][D]
-  static constexpr int kInts = kBad + (FMT == QGEMV_KV_INT8 ? 0 : kSoft * kNotes * 3 * D * 8);
+  static constexpr int kBad = kKeyMask + kSoft * 64 * 4;   // uint64[kNotes][3][D]
+  static constexpr int kInts = kBad + (FMT == QGEMV_KV_INT8 ? 0 : kNotes * 3 * D * 8);
   static constexpr int kBars = kInts + 128;
   static constexpr int kBytes = kBars + 48 * 8 + 1024;  // + alignment
   static_assert(kBytes <= 227 * 1024, "shared memory");
@@ -143,11 +143,11 @@ __global__ void __launch_bounds__(kThreads, 1) tree_wide_kernel(const TreeArgs a
   volatile int* s_int = reinterpret_cast<volatile int*>(smem + S::kInts);
   volatile int* s_abort = s_int;
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(smem + S::kInts) + 1;
-  volatile int* s_anybad = s_int + 2;   // [kSoft][kNotes]
+  volatile int* s_anybad = s_int + 2;   // [kNotes]
   // blocks (bits) whose pages exist, of each half of a unit
-  volatile int* s_valid = s_int + 8;    // [kKs][2]
-  volatile int* s_vvalid = s_int + 14;  // [kVs], whole units (fp16)
-  volatile int* s_rvalid = s_int + 16;  // [kRs]
+  volatile int* s_valid = s_int + 6;    // [kKs][2]
+  volatile int* s_vvalid = s_int + 12;  // [kVs], whole units (fp16)
+  volatile int* s_rvalid = s_int + 14;  // [kRs]
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const unsigned full = 0xffffffffu;
@@ -174,10 +174,8 @@ __global__ void __launch_bounds__(kThreads, 1) tree_wide_kernel(const TreeArgs a
     mbar_init(&bars[B::kDone], 1);
     fence_mbarrier_init();
     *s_abort = 0;
-    for (int i = 0; i < kSoft * kNotes; ++i) s_anybad[i] = 0;
+    for (int i = 0; i < kNotes; ++i) s_anybad[i] = 0;
   }
-  if constexpr (FMT != QGEMV_KV_INT8)
-    for (int i = tid; i < kSoft * kNotes * 3 * D; i += kThreads) s_bad[i] = 0;
   if (warp == kMmaWarp) tmem_alloc_all(s_tmem);
   tcgen_before_sync();
   __syncthreads();
@@ -207,7 +205,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_wide_kernel(const TreeArgs a
   Segment sg;
 
   if (warp < kConvWarp) {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 136;");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 80;");
     // ------------------------------------------------------------ softmax --
     const int wg = warp >> 2, key = tid & 127, quarter = warp & 3;
     const int c0 = wg * kCols;  // first of this warpgroup's rows
@@ -433,7 +431,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_wide_kernel(const TreeArgs a
       if (any_of_128(wg, dead)) break;
       tcgen_after_sync();
       float* slot = tree_slot(p, blockIdx.x, sg.u0 == 0, D);
-      const int bb = wg * kNotes + n_seg % kNotes;
+      const int bb = n_seg % kNotes;
       const bool bad = FMT != QGEMV_KV_INT8 && s_anybad[bb] != 0;
       if (busy) {
         {
@@ -494,10 +492,6 @@ __global__ void __launch_bounds__(kThreads, 1) tree_wide_kernel(const TreeArgs a
         tcgen_before_sync();
       }
       named_bar_sync(1 + wg, 128);
-      if (FMT != QGEMV_KV_INT8 && bad) {
-        for (int i = key; i < 3 * D; i += 128) s_bad[bb * 3 * D + i] = 0;
-        if (key == 0) s_anybad[bb] = 0;
-      }
       ++n_seg;
     }
   } else if (warp < kLoadWarp) {
@@ -506,26 +500,33 @@ __global__ void __launch_bounds__(kThreads, 1) tree_wide_kernel(const TreeArgs a
     const int key = tid & 127, half = key >> 6;
     const bool is_v = warp >= kConvWarp + 4;
     int n_seg = 0;
-    bool ok = !(S::kF16 && !is_v);
-    while (ok && work.next(a, sg)) {
+    // As for the softmax: a wait that ran out sets `dead`, the warps of V leave
+    // together, at a segment's start.
+    bool dead = false;
+    while (!(S::kF16 && !is_v) && !(dead && !is_v) && work.next(a, sg)) {
       const int n = static_cast<int>(sg.u1 - sg.u0), ctx = sg.ctx, all = ctx + sg.T;
       const int bb = n_seg % kNotes;
+      bool left = false;
+      auto start_notes = [&]() {
+        left = any_of_128(kSoft, dead);
+        if (FMT == QGEMV_KV_INT8 || left) return;
+        for (int i = key; i < 3 * D; i += 128) s_bad[bb * 3 * D + i] = 0;
+        if (key == 0) s_anybad[bb] = 0;
+        named_bar_sync(1 + kSoft, 128);
+      };
       for (int j = 0; j < n; ++j, ++jt) {
         const int64_t pos = (sg.u0 + j) * kKeys + key;
         const int ks = jt % S::kKs, vst = jt % S::kVs;
         uint8_t* dst = smem + (is_v ? S::kV + vst * S::kTile : S::kK + ks * S::kTile) + key * 128;
         auto note = [&](int d, int kind) {  // a drafted token's value that is infinite or NaN
-          for (int w = 0; w < kSoft; ++w) {
-            atomicOr(&s_bad[((w * kNotes + bb) * 3 + kind) * D + d], 1ull << (pos - ctx));
-            s_anybad[w * kNotes + bb] = 1;
-          }
+          atomicOr(&s_bad[(bb * 3 + kind) * D + d], 1ull << (pos - ctx));
+          s_anybad[bb] = 1;
         };
         if constexpr (S::kF16) {
-          ok = wait(B::kVl + vst, used(jt, S::kVs));
-          if (!__all_sync(full, ok)) {
-            ok = false;
-            break;
-          }
+          dead |= !wait(B::kVl + vst, used(jt, S::kVs));
+          __syncwarp();
+          if (j == 0) start_notes();
+          if (left) break;
           const int valid = s_vvalid[vst];
           if ((sg.u0 + j + 1) * kKeys > ctx || valid != (1 << kBlocks) - 1) {
             const bool on = ((valid >> (key >> 4)) & 1) && pos < all;
@@ -555,13 +556,12 @@ __global__ void __launch_bounds__(kThreads, 1) tree_wide_kernel(const TreeArgs a
         } else {
           const int64_t rt = 2ll * jt + half;
           const int rs = static_cast<int>(rt % S::kRs);
-          ok = wait(B::kRf + rs, used(rt, S::kRs));
-          if (ok && is_v && jt >= S::kVs) ok = wait(B::kVe + vst, freed(jt, S::kVs));
-          if (ok && !is_v && jt >= S::kKs) ok = wait(B::kKe + ks, freed(jt, S::kKs));
-          if (!__all_sync(full, ok)) {
-            ok = false;
-            break;
-          }
+          dead |= !wait(B::kRf + rs, used(rt, S::kRs));
+          if (is_v && jt >= S::kVs) dead |= !wait(B::kVe + vst, freed(jt, S::kVs));
+          if (!is_v && jt >= S::kKs) dead |= !wait(B::kKe + ks, freed(jt, S::kKs));
+          __syncwarp();
+          if (is_v && j == 0) start_notes();
+          if (left) break;
           const int tok = key & 15;
           const uint8_t* blk = smem + S::kRaw + rs * S::kHalf + ((key >> 4) & 3) * L::kBlock;
           const int valid = s_rvalid[rs];
@@ -658,10 +658,11 @@ __global__ void __launch_bounds__(kThreads, 1) tree_wide_kernel(const TreeArgs a
           mbar_arrive(&bars[B::kRe + rs]);
         }
       }
+      if (left) break;
       ++n_seg;
     }
   } else {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
     if (warp == kLoadWarp) {
       // -------------------------------------------------------- copies ----
       int64_t n_raw = 0;
@@ -757,10 +758,8 @@ __global__ void __launch_bounds__(kThreads, 1) tree_wide_kernel(const TreeArgs a
         const int n = static_cast<int>(sg.u1 - sg.u0);
         const int live = min(kRows, sg.T * a.G - sg.tile * kRows), N = (live + 15) & ~15;
         const uint32_t id_qk = mma_idesc(false, false, false, N), id_pv = mma_idesc(false, true, true, N);
-        auto qk = [&](int x) -> bool {
+        auto qk = [&](int x) {
           const int ks = x % S::kKs, sb = x % S::kSBufs;
-          if (!wait_all(B::kKf + ks, used(x, S::kKs))) return false;
-          if (x >= S::kSBufs && !wait_all(B::kSe + sb, freed(x, S::kSBufs))) return false;
           tcgen_after_sync();
           const uint64_t da = sw128_desc(sk + ks * S::kTile, 0, 1024), db = sw128_desc(sq, 0, 1024);
 #pragma unroll
@@ -772,21 +771,40 @@ __global__ void __launch_bounds__(kThreads, 1) tree_wide_kernel(const TreeArgs a
           }
           mma_commit(&bars[B::kSf + sb], leader);
           mma_commit(&bars[B::kKe + ks], leader);
-          return true;
         };
-        ok = wait_all(B::kQf, n_seg & 1) && qk(jt);
-        for (int j = 0; ok && j < n; ++j) {
-          const int x = jt + j, vst = x % S::kVs;
-          if (j + 1 < n) ok = qk(x + 1);
-          ok = ok && wait_all(B::kVf + vst, used(x, S::kVs)) && wait_all(B::kPf, x & 1);
-          if (!ok) break;
+        auto pv = [&](int x) {
+          const int vst = x % S::kVs;
           tcgen_after_sync();
           const uint64_t da = sw128_desc(sv + vst * S::kTile, kKeys * 128, 1024), db = sw128_desc(sp, 0, 1024);
 #pragma unroll
           for (int k = 0; k < kKeys / 16; ++k)
-            mma_ss(tbase + S::kOCol, da + ((k * 2048) >> 4), db + ((k * 2048) >> 4), id_pv, j > 0 || k > 0, leader);
+            mma_ss(tbase + S::kOCol, da + ((k * 2048) >> 4), db + ((k * 2048) >> 4), id_pv, x > jt || k > 0, leader);
           mma_commit(&bars[B::kPv], leader);
           mma_commit(&bars[B::kVe + vst], leader);
+        };
+        auto now = [&](int bar, uint32_t parity) { return __all_sync(full, mbar_test(&bars[bar], parity)) != 0; };
+        ok = wait_all(B::kQf, n_seg & 1);
+        // S runs ahead of P V by one unit (two buffers) or none; whichever is
+        // ready goes first, so that a late K does not hold up a V that waits.
+        unsigned long long t0 = global_timer_ns();
+        for (int x = jt, y = jt; ok && y < jt + n;) {
+          bool went = false;
+          if (x < jt + n && x <= y + 1 && now(B::kKf + x % S::kKs, used(x, S::kKs)) &&
+              (x < S::kSBufs || now(B::kSe + x % S::kSBufs, freed(x, S::kSBufs)))) {
+            qk(x++);
+            went = true;
+          }
+          if (y < x && now(B::kPf, y & 1) && now(B::kVf + y % S::kVs, used(y, S::kVs))) {
+            pv(y++);
+            went = true;
+          }
+          if (went) {
+            t0 = global_timer_ns();
+          } else if (__any_sync(full, *s_abort != 0 || global_timer_ns() - t0 > kWaitLimitNs)) {
+            if (leader && *s_abort == 0) atomicOr(reinterpret_cast<int*>(p.ws), kErrWide);
+            *s_abort = 1;
+            ok = false;
+          }
         }
         jt += n;
         ++n_seg;
