@@ -26,6 +26,7 @@
 namespace qgemv {
 namespace {
 
+constexpr int kNarrowRows = 32;  // more rows than this go to the wide kernel
 constexpr int kErrTree = 32;
 constexpr float kLazyT = 8.f;
 constexpr int kRingBytes = 200 * 1024;
@@ -185,6 +186,7 @@ __global__ void __launch_bounds__(TreeShape<FMT, D, MT>::kThreads, 1) tree_kerne
   const int g = lane >> 2, t = lane & 3;
   const unsigned full = 0xffffffffu;
 
+  allow_next_kernel();
   Cursor<Sh::kRows, kKvBlockTokens> work(a);
   uint64_t* my_bars = bars + warp * NS;
   uint8_t* my_ring = smem + warp * NS * L::kBlock;
@@ -226,30 +228,35 @@ __global__ void __launch_bounds__(TreeShape<FMT, D, MT>::kThreads, 1) tree_kerne
         mbar_arrive(&my_bars[st]);
       }
     };
-    for (int k = 0; k < NS && k < n_mine; ++k) prefetch(k);
-
-    // ---- Q fragments and masks of the row tile
-    for (int i = tid; i < MT * KS * 32; i += Sh::kThreads) {
+    // ---- Q fragments and masks of the row tile: loaded ahead of the first
+    // copies' page lookups, stored after
+    constexpr int kQPer = (MT * KS * 32 + Sh::kThreads - 1) / Sh::kThreads;
+    uint4 qf[kQPer];
+#pragma unroll
+    for (int x = 0; x < kQPer; ++x) {
+      const int i = tid + x * Sh::kThreads;
       const int ln = i & 31, ks = (i >> 5) % KS, mt = i / (32 * KS);
       const int d = C::q_at(ks, ln & 3);
-      uint2 lo = make_uint2(0u, 0u), hi = make_uint2(0u, 0u);
       auto row_q = [&](int r) -> uint2 {
-        if (r >= R) return make_uint2(0u, 0u);
+        if (r >= R || mt >= MT) return make_uint2(0u, 0u);
         const int tok = r / a.G;
         const __half* q = static_cast<const __half*>(p.q.ptr) + (q0 + tok) * p.q.token_stride +
                           (head * a.G + r - tok * a.G) * p.q.head_stride;
         return make_uint2(__ldg(reinterpret_cast<const unsigned*>(q + d)), __ldg(reinterpret_cast<const unsigned*>(q + d + C::kQ2)));
       };
-      lo = row_q(row0 + 16 * mt + (ln >> 2));
-      hi = row_q(row0 + 16 * mt + (ln >> 2) + 8);
-      s_q[i] = make_uint4(lo.x, hi.x, lo.y, hi.y);
+      const uint2 lo = row_q(row0 + 16 * mt + (ln >> 2)), hi = row_q(row0 + 16 * mt + (ln >> 2) + 8);
+      qf[x] = make_uint4(lo.x, hi.x, lo.y, hi.y);
     }
-    for (int i = tid; i < Sh::kRows; i += Sh::kThreads) {
-      const int tok = (row0 + i) / a.G;
-      uint64_t m = 0;
-      if (row0 + i < R) m = p.masks ? p.masks[q0 + tok] : (~0ull >> (63 - tok));
-      s_mask[i] = m;
+    uint64_t row_mask = 0;
+    if (tid < Sh::kRows && row0 + tid < R) {
+      const int tok = (row0 + tid) / a.G;
+      row_mask = p.masks ? p.masks[q0 + tok] : (~0ull >> (63 - tok));
     }
+    for (int k = 0; k < NS && k < n_mine; ++k) prefetch(k);
+#pragma unroll
+    for (int x = 0; x < kQPer; ++x)
+      if (tid + x * Sh::kThreads < MT * KS * 32) s_q[tid + x * Sh::kThreads] = qf[x];
+    if (tid < Sh::kRows) s_mask[tid] = row_mask;
     __syncthreads();
 
     const float sl = p.scale * kLog2e;
@@ -540,12 +547,18 @@ __global__ void __launch_bounds__(TreeShape<FMT, D, MT>::kThreads, 1) tree_kerne
       }
     __syncthreads();  // every ring is empty
     float* s_o = reinterpret_cast<float*>(smem);
+    const bool few = MT == 1 && R - row0 <= 8;  // rows 8 .. 15 are nothing: half of the traffic
 #pragma unroll
     for (int i = 0; i < MT; ++i) {
 #pragma unroll
-      for (int n = 0; n < NB; ++n)
-#pragma unroll
-        for (int c = 0; c < 4; ++c) s_o[((warp * MT + i) * NB * 4 + n * 4 + c) * 32 + lane] = o[i][n][c];
+      for (int n = 0; n < NB; ++n) {
+        s_o[((warp * MT + i) * NB * 4 + n * 4) * 32 + lane] = o[i][n][0];
+        s_o[((warp * MT + i) * NB * 4 + n * 4 + 1) * 32 + lane] = o[i][n][1];
+        if (!few) {
+          s_o[((warp * MT + i) * NB * 4 + n * 4 + 2) * 32 + lane] = o[i][n][2];
+          s_o[((warp * MT + i) * NB * 4 + n * 4 + 3) * 32 + lane] = o[i][n][3];
+        }
+      }
       if (t == 0) {
         s_ml[warp * Sh::kRows + 16 * i + g] = make_float2(m[i][0], l[i][0]);
         s_ml[warp * Sh::kRows + 16 * i + 8 + g] = make_float2(m[i][1], l[i][1]);
@@ -575,6 +588,7 @@ __global__ void __launch_bounds__(TreeShape<FMT, D, MT>::kThreads, 1) tree_kerne
 #pragma unroll
     for (int j = 0; j < kPer; ++j) {
       const int v = tid + j * Sh::kThreads, row = row_of(v);
+      if (few && row >= 8) continue;
       float top = -INFINITY;
 #pragma unroll
       for (int w = 0; w < W; ++w) top = fmaxf(top, s_ml[w * Sh::kRows + row].x);
@@ -593,6 +607,7 @@ __global__ void __launch_bounds__(TreeShape<FMT, D, MT>::kThreads, 1) tree_kerne
       for (int j = 0; j < kPer; ++j) {
         const int v = tid + j * Sh::kThreads, row = row_of(v);
         const int n = (v >> 5) % NB, c = (v >> 3) & 3;
+        if (row0 + row >= R) continue;
         float* dst = mine + row * D;
         dst[C::out_at(n, (c & 1) + 0)] = acc[j].x;
         dst[C::out_at(n, (c & 1) + 2)] = acc[j].y;
@@ -642,7 +657,10 @@ __global__ void __launch_bounds__(128) tree_join_kernel(const TreeArgs a) {
   const int lane = threadIdx.x & 31, H = p.cache.kv_heads;
   const unsigned full = 0xffffffffu;
   const int64_t row = (static_cast<int64_t>(blockIdx.x) * 128 + threadIdx.x) >> 5;
-  if (row >= p.n_q * p.q_heads) return;
+  // Every thread waits for the main kernel, those with nothing to do too: what
+  // follows this kernel on the stream may rely on both.
+  auto leave = [] { wait_for_last_kernel(); };
+  if (row >= p.n_q * p.q_heads) return leave();
   const int64_t token = row / p.q_heads;
   const int qh = static_cast<int>(row - token * p.q_heads), head = qh / a.G;
   // its sequence, and the units before it
@@ -657,13 +675,14 @@ __global__ void __launch_bounds__(128) tree_join_kernel(const TreeArgs a) {
   total = warp_total(total);
   base = warp_total(base);
   seq = static_cast<int>(warp_total(seq));
-  if (seq >= p.n_seqs) return;
+  if (seq >= p.n_seqs) return leave();
   const SeqWork s = seq_work<ROWS, UNIT>(a, seq);
   const int64_t i = token - __ldg(p.cu_q + seq);
-  if (i < 0 || i >= s.T) return;
+  if (i < 0 || i >= s.T) return leave();
   const int64_t quota = run_quota(a, total);
   const int r = static_cast<int>(i) * a.G + qh - head * a.G;
   const int64_t first = base + (static_cast<int64_t>(head) * s.tiles + r / ROWS) * (s.units + a.extra) + a.extra;
+  wait_for_last_kernel();
   const int b0 = static_cast<int>(div_small(first, quota)), b1 = static_cast<int>(div_small(first + s.units - 1, quota));
   if (b0 == b1) return;  // one block had it all
   float m = -INFINITY, l = 0.f, acc[D / 32];
@@ -719,13 +738,18 @@ cudaError_t launch(const TreeArgs& a, cudaStream_t s) {
 template <int ROWS, int UNIT>
 cudaError_t launch_join(const TreeArgs& a, cudaStream_t s) {
   const int64_t rows = a.p.n_q * a.p.q_heads;
-  const unsigned grid = static_cast<unsigned>((rows + 3) / 4);
-  if (a.p.cache.head_dim == 64) tree_join_kernel<ROWS, UNIT, 64><<<grid, 128, 0, s>>>(a);
-  else tree_join_kernel<ROWS, UNIT, 128><<<grid, 128, 0, s>>>(a);
-  return cudaGetLastError();
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>((rows + 3) / 4));
+  cfg.blockDim = dim3(128);
+  cfg.stream = s;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return a.p.cache.head_dim == 64 ? cudaLaunchKernelEx(&cfg, tree_join_kernel<ROWS, UNIT, 64>, a)
+                                  : cudaLaunchKernelEx(&cfg, tree_join_kernel<ROWS, UNIT, 128>, a);
 }
-
-int env_int(const char* n, int d) { const char* v = getenv(n); return v && *v ? atoi(v) : d; }
 
 }  // namespace
 
@@ -748,17 +772,18 @@ cudaError_t launch_attn_tree(const TreeParams& p, cudaStream_t s) {
   while ((1 << a.page_shift) < p.cache.page_tokens) ++a.page_shift;
   a.grid = sms < kMaxBlocks ? sms : kMaxBlocks;
   const int64_t rows = static_cast<int64_t>(p.max_new) * a.G;
-  static const int wide_from = env_int("QG_WIDE", 17);
-  if (rows >= wide_from) {
-    static const int ex = env_int("QG_EXW", 3), mu = env_int("QG_MUW", 2);
-    a.extra = ex;
-    a.min_units = mu + a.extra;
+  // Up to 32 rows this kernel is faster (two sequences of up to 131000 tokens,
+  // INT8: 8 rows 87 us against 177, 32 rows 133 against 161), beyond it needs
+  // several tiles and passes over the cache, and the wide kernel is (16
+  // sequences of up to 16000 tokens, INT8, 64 rows: 96 us against 188).
+  if (rows > kNarrowRows) {
+    a.extra = 4;  // a row tile's start and end: about four units of 128 tokens
+    a.min_units = 2 + a.extra;
     const cudaError_t e = launch_tree_wide(a, s);
     return e != cudaSuccess ? e : launch_join<64, 128>(a, s);
   }
-  static const int ex = env_int("QG_EX", 32), mu = env_int("QG_MU", 16);
-  a.extra = ex;
-  a.min_units = mu + a.extra;
+  a.extra = 48;  // about 48 units of 16 tokens (64 ragged INT8 sequences: 148 us at 0, 84 at 32, 68 at 48 and 64)
+  a.min_units = 16 + a.extra;
   auto by_rows = [&](auto fmt, auto d) {
     constexpr int F = decltype(fmt)::value, D = decltype(d)::value;
     if (rows > 16) {

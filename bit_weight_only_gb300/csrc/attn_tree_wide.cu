@@ -151,6 +151,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_wide_kernel(const TreeArgs a
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const unsigned full = 0xffffffffu;
+  allow_next_kernel();
 
   if (tid == 0) {
     for (int i = 0; i < 5; ++i) {

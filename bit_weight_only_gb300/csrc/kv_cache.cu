@@ -41,6 +41,18 @@ __device__ __forceinline__ uint32_t half_bits(float lo, float hi) {
   return __half_as_ushort(__float2half_rn(lo)) | static_cast<uint32_t>(__half_as_ushort(__float2half_rn(hi))) << 16;
 }
 
+// round(fl32(x / a)) by a product with 1 / a: that is off by a few units in the
+// last place, so only a result close to a tie can round otherwise, and those
+// are worked out by the division (as are NaN).  |x / a| is at most 128.
+template <bool HALF_AWAY>
+__device__ __forceinline__ float round_quotient(float x, float a, float inv) {
+  constexpr float kShift = 12582912.f;  // 1.5 * 2^23
+  const float r = x * inv, q = (r + kShift) - kShift;
+  if (fabsf(r - q) < 0.4999f) return q;
+  const float e = __fdiv_rn(x, a);
+  return HALF_AWAY ? roundf(e) : rintf(e);
+}
+
 // The codes of lane values x[V] (values d0 .. of a row) into token tok of
 // block b.  Lanes of a row call it together.
 template <int FMT, int D, int V>
@@ -68,15 +80,17 @@ __device__ __forceinline__ void encode(uint8_t* b, bool v, int tok, int d0, cons
     for (int o = 1; o < D / V; o <<= 1) m = fmaxf(m, __shfl_xor_sync(full, m, o));
     const float a = m == INFINITY ? __int_as_float(0x7fffffff) : __fdiv_rn(m, 127.f);
     uint32_t w[V / 4];
+    const float inv = 1.f / a;
 #pragma unroll
     for (int j = 0; j < V / 4; ++j) {
-      w[j] = 0;
+      uint32_t c[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        int q = 0;
-        if (a > 0.f) q = max(-127, min(127, __float2int_rn(__fdiv_rn(x[4 * j + i], a))));
-        w[j] |= static_cast<uint32_t>(q + 128) << (8 * i);
+        float q = 0.f;
+        if (a > 0.f) q = fminf(fmaxf(round_quotient<false>(x[4 * j + i], a, inv), -127.f), 127.f);
+        c[i] = __float_as_uint(q + 8388736.f);  // 2^23 + 128: the code + 128 in the low byte
       }
+      w[j] = __byte_perm(__byte_perm(c[0], c[1], 0x0040), __byte_perm(c[2], c[3], 0x0040), 0x5410);
     }
     if (!on) return;
     uint8_t* at = b + (v ? L::v_off(tok, d0) : L::k_off(tok, d0));
@@ -103,10 +117,12 @@ __device__ __forceinline__ void encode(uint8_t* b, bool v, int tok, int d0, cons
     bad = fabsf(peak) == INFINITY;
     const float a = bad ? __int_as_float(0x7fffffff) : __fdiv_rn(peak, -8.f);
     uint32_t q[V];
+    const float inv = 1.f / a;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      q[i] = 8;
-      if (!bad && a != 0.f) q[i] = static_cast<uint32_t>(fminf(fmaxf(roundf(__fdiv_rn(x[i], a)) + 8.f, 0.f), 15.f));
+      float c = 8.f;
+      if (!bad && a != 0.f) c = fminf(fmaxf(round_quotient<true>(x[i], a, inv) + 8.f, 0.f), 15.f);
+      q[i] = __float_as_uint(c + 8388608.f) & 15u;
     }
     const int grp = d0 >> 5, e = d0 & 31;
     // K: word (group, e / 8), values 0 2 4 6 1 3 5 7 from the low nibble.  The

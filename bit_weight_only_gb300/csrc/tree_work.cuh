@@ -78,38 +78,45 @@ struct Cursor {
 
   __device__ Cursor(const TreeArgs& a) {
     const int lane = threadIdx.x & 31, H = a.p.cache.kv_heads;
-    int64_t total = 0;
-    for (int b = lane; b < a.p.n_seqs; b += 32) {
+    const unsigned full = 0xffffffffu;
+    auto cost_of = [&](int b) -> int64_t {
+      if (b >= a.p.n_seqs) return 0;
       const SeqWork s = seq_work<ROWS, UNIT>(a, b);
-      total += (s.units + a.extra) * s.tiles * H;
-    }
-    total = warp_total(total);
+      return (s.units + a.extra) * s.tiles * H;
+    };
+    auto scan = [&](int64_t x) {  // inclusive
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int64_t y = __shfl_up_sync(full, x, o);
+        if (lane >= o) x += y;
+      }
+      return x;
+    };
+    const int64_t mine0 = cost_of(lane), sum0 = scan(mine0);  // the first 32 sequences
+    int64_t rest = 0;
+    for (int b = 32 + lane; b < a.p.n_seqs; b += 32) rest += cost_of(b);
+    int64_t total = __shfl_sync(full, sum0, 31);
+    if (a.p.n_seqs > 32) total += warp_total(rest);
     const int64_t quota = run_quota(a, total);
     cur = quota * blockIdx.x;
     end = min(cur + quota, total);
     seq = 0;
     base = 0;
     if (cur >= end) return;
+    int64_t mine = mine0, sum = sum0;
     for (int b0 = 0;; b0 += 32) {
-      int64_t mine = 0;
-      if (b0 + lane < a.p.n_seqs) {
-        const SeqWork s = seq_work<ROWS, UNIT>(a, b0 + lane);
-        mine = (s.units + a.extra) * s.tiles * H;
+      if (b0 > 0) {
+        mine = cost_of(b0 + lane);
+        sum = scan(mine);
       }
-      int64_t sum = mine;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int64_t x = __shfl_up_sync(0xffffffffu, sum, o);
-        if (lane >= o) sum += x;
-      }
-      const unsigned past = __ballot_sync(0xffffffffu, base + sum > cur);
+      const unsigned past = __ballot_sync(full, base + sum > cur);
       if (past) {
         const int k = __ffs(past) - 1;
         seq = b0 + k;
-        base += __shfl_sync(0xffffffffu, sum - mine, k);
+        base += __shfl_sync(full, sum - mine, k);
         return;
       }
-      base += __shfl_sync(0xffffffffu, sum, 31);
+      base += __shfl_sync(full, sum, 31);
     }
   }
 
@@ -145,6 +152,12 @@ struct Cursor {
 __device__ __forceinline__ float* tree_slot(const TreeParams& p, int block, bool begins, int D) {
   return reinterpret_cast<float*>(p.ws + kWsHeaderBytes) + (2 * block + (begins ? 1 : 0)) * slot_floats(D);
 }
+
+// The join kernel may be launched before the main one has ended
+// (programmatic dependent launch): the main kernels allow it at their start,
+// the join waits for their end before it reads what they wrote.
+__device__ __forceinline__ void allow_next_kernel() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void wait_for_last_kernel() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 cudaError_t launch_tree_wide(const TreeArgs& a, cudaStream_t s);
 

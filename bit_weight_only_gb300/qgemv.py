@@ -568,20 +568,25 @@ class KVCache:
             raise ValueError("q must be fp16")
         if out is None:
             out = torch.empty((n, heads, d), dtype=torch.float16, device=q.device)
+            out_rows = out.data_ptr(), heads * d, d
         elif out.dtype != torch.float16 or out.shape != q.shape:
             raise ValueError("out must be fp16, shaped like q")
+        else:
+            out_rows = _rows("out", out, heads, d)
         if lse is None:
             lse = torch.empty((n, heads), dtype=torch.float32, device=q.device)
-        if masks is not None and masks.dtype != torch.uint64:
-            _index("masks", masks, torch.int64, (n,))
+        else:
+            _index("lse", lse, torch.float32, (n, heads))
+        if masks is not None:
+            if masks.dtype != torch.uint64:
+                _index("masks", masks, torch.int64, (n,))
+            masks = masks.data_ptr()
         n_seqs, stride = table.shape
         qgemv_attn_tree(self.desc, _index("table", table, torch.int32, (n_seqs, stride)), stride, n_seqs,
                         _index("ctx_lens", ctx_lens, torch.int32, (n_seqs,)), *_rows("q", q, heads, self.head_dim),
-                        heads, _index("cu_q", cu_q, torch.int32, (n_seqs + 1,)), n,
-                        None if masks is None else masks.data_ptr(), max_ctx, max_new,
-                        d ** -0.5 if scale is None else scale, *_rows("out", out, heads, d),
-                        _index("lse", lse, torch.float32, (n, heads)), workspace.ptr, workspace.nbytes,
-                        _current(stream))
+                        heads, _index("cu_q", cu_q, torch.int32, (n_seqs + 1,)), n, masks, max_ctx, max_new,
+                        d ** -0.5 if scale is None else scale, *out_rows, lse.data_ptr(), workspace.ptr,
+                        workspace.nbytes, _current(stream))
         return out, lse
 
 
@@ -596,14 +601,19 @@ def attn_prompt(q, k, v, cu_q, cu_k, *, max_q: int, workspace, scale=None, out=N
         raise ValueError("q, k and v must have one type, k and v the same number of tokens")
     if out is None:
         out = torch.empty((n, heads, d), dtype=q.dtype, device=q.device)
+        out_rows = out.data_ptr(), heads * d, d
     elif out.dtype != q.dtype or out.shape != q.shape:
         raise ValueError("out must have q's type and shape")
+    else:
+        out_rows = _rows("out", out, heads, d)
     if lse is None:
         lse = torch.empty((n, heads), dtype=torch.float32, device=q.device)
+    else:
+        _index("lse", lse, torch.float32, (n, heads))
     n_seqs, kv_heads = cu_q.shape[0] - 1, k.shape[1]
     qgemv_attn_prompt(_dtype_code(q.dtype), d, heads, kv_heads, *_rows("q", q, heads, d), *_rows("k", k, kv_heads, d),
                       *_rows("v", v, kv_heads, d), n_seqs, _index("cu_q", cu_q, torch.int32, (n_seqs + 1,)),
                       _index("cu_k", cu_k, torch.int32, (n_seqs + 1,)), n, k.shape[0], max_q,
-                      d ** -0.5 if scale is None else scale, *_rows("out", out, heads, d),
-                      _index("lse", lse, torch.float32, (n, heads)), workspace.ptr, workspace.nbytes, _current(stream))
+                      d ** -0.5 if scale is None else scale, *out_rows, lse.data_ptr(), workspace.ptr,
+                      workspace.nbytes, _current(stream))
     return out, lse
