@@ -1,14 +1,12 @@
 // kv_cache.cu -- writing rows into the quantised key/value cache and reading
 // them back (qgemv_kv_write, qgemv_kv_read).
 //
-// Memory-bound: rows are read once and codes written once.  A warp takes
-// eight (head, K or V) rows of one token, so that the slot, the sequence and
-// the divisions are worked out once for them, and has all of their loads in
-// flight together.
-//
-// Write: a lane holds 16 bytes of the input, V = 4 or 8 neighbouring values;
-// d / V lanes make a row.  A Q4_0 group is 8 or 4 lanes.
-// Read: a lane takes 8 neighbouring values.
+// Memory-bound in bytes, but the codes cost instructions enough to matter
+// (issue slots 65-80% busy at half of the bandwidth in the first form): a lane
+// takes eight neighbouring values, so that a row's reductions, scale and
+// address are shared by few lanes, d / 8; quantisers work without divisions or
+// conversions per value.  A warp takes eight (head, K or V) rows of one token
+// and has all of their loads in flight together.
 #include <type_traits>
 
 #include "kv_layout.cuh"
@@ -19,130 +17,127 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kWarpRows = 8;
 
+// Eight values as they lie in memory, and in fp32.
 template <typename T>
-__device__ __forceinline__ void load_values(const T* src, float (&x)[16 / sizeof(T)]) {
-  const uint4 w = __ldg(reinterpret_cast<const uint4*>(src));
-  const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+struct Raw {
+  uint4 w[sizeof(T) / 2];
+  __device__ void load(const T* src) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    if constexpr (std::is_same<T, float>::value) {
-      x[i] = __uint_as_float(u[i]);
-    } else if constexpr (std::is_same<T, __half>::value) {
-      x[2 * i] = __half2float(__ushort_as_half(static_cast<unsigned short>(u[i] & 0xffffu)));
-      x[2 * i + 1] = __half2float(__ushort_as_half(static_cast<unsigned short>(u[i] >> 16)));
-    } else {
-      x[2 * i] = __uint_as_float(u[i] << 16);
-      x[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
+    for (int i = 0; i < static_cast<int>(sizeof(T) / 2); ++i) w[i] = __ldg(reinterpret_cast<const uint4*>(src) + i);
+  }
+  __device__ void values(float (&x)[8]) const {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      if constexpr (std::is_same<T, float>::value) {
+        x[i] = __uint_as_float((&w[i >> 2].x)[i & 3]);
+      } else {
+        const uint32_t u = (&w[0].x)[i >> 1];
+        if constexpr (std::is_same<T, __half>::value)
+          x[i] = __half2float(__ushort_as_half(static_cast<unsigned short>(i & 1 ? u >> 16 : u & 0xffffu)));
+        else
+          x[i] = __uint_as_float(i & 1 ? u & 0xffff0000u : u << 16);
+      }
     }
   }
-}
+};
 
 __device__ __forceinline__ uint32_t half_bits(float lo, float hi) {
   return __half_as_ushort(__float2half_rn(lo)) | static_cast<uint32_t>(__half_as_ushort(__float2half_rn(hi))) << 16;
 }
 
-// round(fl32(x / a)) by a product with 1 / a: that is off by a few units in the
-// last place, so only a result close to a tie can round otherwise, and those
-// are worked out by the division (as are NaN).  |x / a| is at most 128.
+// round(fl32(x / a)) of eight values, by products with about 1 / a: those are
+// off by some units in the last place of at most 128, below 1e-4, so that only
+// a result within 1e-4 of a tie could round otherwise; then (and where NaN or
+// a = 0 come up) all eight are worked out by the division.  q in the low byte of
+// each word, as a signed number.
 template <bool HALF_AWAY>
-__device__ __forceinline__ float round_quotient(float x, float a, float inv) {
+__device__ __forceinline__ void round_quotients(const float (&x)[8], float a, uint32_t (&q)[8]) {
   constexpr float kShift = 12582912.f;  // 1.5 * 2^23
-  const float r = x * inv, q = (r + kShift) - kShift;
-  if (fabsf(r - q) < 0.4999f) return q;
-  const float e = __fdiv_rn(x, a);
-  return HALF_AWAY ? roundf(e) : rintf(e);
+  float inv;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(a));
+  bool sure = true;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float r = x[i] * inv, t = r + kShift;
+    q[i] = __float_as_uint(t);
+    const float d = fabsf(r - (t - kShift));
+    sure = sure && d < 0.4999f;
+  }
+  if (!sure) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float e = __fdiv_rn(x[i], a);
+      // (a subnormal a is coarse: the quotient can pass 127)
+      const float c = fminf(fmaxf(HALF_AWAY ? roundf(e) : rintf(e), -127.f), 127.f);
+      q[i] = a != 0.f && e == e ? static_cast<uint32_t>(static_cast<int>(c)) : 0u;
+    }
+  }
 }
 
-// The codes of lane values x[V] (values d0 .. of a row) into token tok of
-// block b.  Lanes of a row call it together.
-template <int FMT, int D, int V>
-__device__ __forceinline__ void encode(uint8_t* b, bool v, int tok, int d0, const float (&x)[V], bool on) {
+__device__ __forceinline__ uint32_t abs_bits(float x) { return __float_as_uint(x) & 0x7fffffffu; }
+constexpr uint32_t kInfBits = 0x7f800000u;
+
+// The codes of a lane's values x (d0 .. of a row) into token tok of block b.
+// The lanes of a warp call it together; a row is D / 8 of them.
+template <int FMT, int D>
+__device__ __forceinline__ void encode(uint8_t* b, bool v, int tok, int d0, const float (&x)[8], bool on) {
   using L = KvLayout<FMT, D>;
   const unsigned full = 0xffffffffu;
   if constexpr (FMT == QGEMV_KV_F16) {
-    uint32_t w[V / 2];
-#pragma unroll
-    for (int i = 0; i < V / 2; ++i) w[i] = half_bits(x[2 * i], x[2 * i + 1]);
-    if (!on) return;
-    uint8_t* at = b + (v ? L::v_off(tok, 2 * d0) : L::k_off(tok, 2 * d0));
-    if constexpr (V == 8) *reinterpret_cast<uint4*>(at) = make_uint4(w[0], w[1], w[2], w[3]);
-    else *reinterpret_cast<uint2*>(at) = make_uint2(w[0], w[1]);
+    if (on)
+      *reinterpret_cast<uint4*>(b + (v ? L::v_off(tok, 2 * d0) : L::k_off(tok, 2 * d0))) =
+          make_uint4(half_bits(x[0], x[1]), half_bits(x[2], x[3]), half_bits(x[4], x[5]), half_bits(x[6], x[7]));
   } else if constexpr (FMT == QGEMV_KV_INT8) {
-    float m = 0.f;
-    bool bad = false;
+    // magnitudes compare as integers, infinities and NaN above all numbers
+    uint32_t m = 0;
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-      m = fmaxf(m, fabsf(x[i]));
-      bad |= !(fabsf(x[i]) < INFINITY);
-    }
-    if (bad) m = INFINITY;
+    for (int i = 0; i < 8; ++i) m = max(m, abs_bits(x[i]));
 #pragma unroll
-    for (int o = 1; o < D / V; o <<= 1) m = fmaxf(m, __shfl_xor_sync(full, m, o));
-    const float a = m == INFINITY ? __int_as_float(0x7fffffff) : __fdiv_rn(m, 127.f);
-    uint32_t w[V / 4];
-    const float inv = 1.f / a;
-#pragma unroll
-    for (int j = 0; j < V / 4; ++j) {
-      uint32_t c[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        float q = 0.f;
-        if (a > 0.f) q = fminf(fmaxf(round_quotient<false>(x[4 * j + i], a, inv), -127.f), 127.f);
-        c[i] = __float_as_uint(q + 8388736.f);  // 2^23 + 128: the code + 128 in the low byte
-      }
-      w[j] = __byte_perm(__byte_perm(c[0], c[1], 0x0040), __byte_perm(c[2], c[3], 0x0040), 0x5410);
-    }
+    for (int o = 1; o < D / 8; o <<= 1) m = max(m, __shfl_xor_sync(full, m, o));
+    const bool bad = m >= kInfBits;
+    const float a = bad ? __int_as_float(0x7fffffff) : __fdiv_rn(__uint_as_float(m), 127.f);
+    uint32_t q[8];
+    round_quotients<false>(x, a, q);  // at most 127: no clamp
+    // code + 128 in a byte
+    const uint32_t lo = __byte_perm(__byte_perm(q[0], q[1], 0x0040), __byte_perm(q[2], q[3], 0x0040), 0x5410) ^ 0x80808080u;
+    const uint32_t hi = __byte_perm(__byte_perm(q[4], q[5], 0x0040), __byte_perm(q[6], q[7], 0x0040), 0x5410) ^ 0x80808080u;
     if (!on) return;
-    uint8_t* at = b + (v ? L::v_off(tok, d0) : L::k_off(tok, d0));
-    if constexpr (V == 8) *reinterpret_cast<uint2*>(at) = make_uint2(w[0], w[1]);
-    else *reinterpret_cast<uint32_t*>(at) = w[0];
+    *reinterpret_cast<uint2*>(b + (v ? L::v_off(tok, d0) : L::k_off(tok, d0))) = make_uint2(lo, hi);
     if (d0 == 0) reinterpret_cast<float*>(b + (v ? L::kVs : L::kKs))[tok] = a;
   } else {
-    // the value of largest magnitude of the group, the first one on ties
+    // the value of largest magnitude of the group's 32, the first one on ties
     float peak = x[0];
     int where = d0;
-    bool bad = false;
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-      bad |= !(fabsf(x[i]) < INFINITY);
-      if (fabsf(x[i]) > fabsf(peak)) peak = x[i], where = d0 + i;
-    }
-    if (bad) peak = INFINITY;
+    for (int i = 1; i < 8; ++i)
+      if (abs_bits(x[i]) > abs_bits(peak)) peak = x[i], where = d0 + i;
 #pragma unroll
-    for (int o = 1; o < 32 / V; o <<= 1) {
+    for (int o = 1; o < 4; o <<= 1) {
       const float op = __shfl_xor_sync(full, peak, o);
       const int ow = __shfl_xor_sync(full, where, o);
-      if (fabsf(op) > fabsf(peak) || (fabsf(op) == fabsf(peak) && ow < where)) peak = op, where = ow;
+      if (abs_bits(op) > abs_bits(peak) || (abs_bits(op) == abs_bits(peak) && ow < where)) peak = op, where = ow;
     }
-    bad = fabsf(peak) == INFINITY;
+    const bool bad = abs_bits(peak) >= kInfBits;
     const float a = bad ? __int_as_float(0x7fffffff) : __fdiv_rn(peak, -8.f);
-    uint32_t q[V];
-    const float inv = 1.f / a;
+    uint32_t q[8];
+    round_quotients<true>(x, a, q);
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-      float c = 8.f;
-      if (!bad && a != 0.f) c = fminf(fmaxf(round_quotient<true>(x[i], a, inv) + 8.f, 0.f), 15.f);
-      q[i] = __float_as_uint(c + 8388608.f) & 15u;
+    for (int i = 0; i < 8; ++i) {  // -8 .. 8 to 0 .. 15
+      const int c = (static_cast<int>(q[i] << 24) >> 24) + 8;
+      q[i] = static_cast<uint32_t>(min(max(c, 0), 15));
     }
+    if (!on) return;
     const int grp = d0 >> 5, e = d0 & 31;
-    // K: word (group, e / 8), values 0 2 4 6 1 3 5 7 from the low nibble.  The
-    // shuffle stands outside of the branch: a warp can hold rows of both kinds.
-    uint32_t w;
-    if constexpr (V == 8) {
-      w = q[0] | q[2] << 4 | q[4] << 8 | q[6] << 12 | q[1] << 16 | q[3] << 20 | q[5] << 24 | q[7] << 28;
-    } else {
-      w = q[0] | q[2] << 4 | q[1] << 16 | q[3] << 20;
-      w |= __shfl_down_sync(full, w, 1) << 8;  // values 4 .. 7
-    }
-    if (on && v) {  // V: halfword (group, e / 4), four neighbouring values
+    if (v) {  // halfword (group, e / 4): four neighbouring values
 #pragma unroll
-      for (int j = 0; j < V / 4; ++j)
+      for (int j = 0; j < 2; ++j)
         *reinterpret_cast<uint16_t*>(b + L::v_off(tok, ((e >> 2) + j) * (D / 16) + 2 * grp)) =
             static_cast<uint16_t>(q[4 * j] | q[4 * j + 1] << 4 | q[4 * j + 2] << 8 | q[4 * j + 3] << 12);
-    } else if (on && (e & 7) == 0) {
-      *reinterpret_cast<uint32_t*>(b + L::k_off(tok, (e >> 3) * (D / 8) + 4 * grp)) = w;
+    } else {  // word (group, e / 8): values 0 2 4 6 1 3 5 7 from the low nibble
+      *reinterpret_cast<uint32_t*>(b + L::k_off(tok, (e >> 3) * (D / 8) + 4 * grp)) =
+          q[0] | q[2] << 4 | q[4] << 8 | q[6] << 12 | q[1] << 16 | q[3] << 20 | q[5] << 24 | q[7] << 28;
     }
-    if (on && e == 0) reinterpret_cast<__half*>(b + (v ? L::kVs : L::kKs))[tok * (D / 32) + grp] = __float2half_rn(a);
+    if (e == 0) reinterpret_cast<__half*>(b + (v ? L::kVs : L::kKs))[tok * (D / 32) + grp] = __float2half_rn(a);
   }
 }
 
@@ -155,35 +150,45 @@ __device__ __forceinline__ WarpRows warp_rows(int H) {
   const int64_t w = (static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x) >> 5;
   const int per = (2 * H + kWarpRows - 1) / kWarpRows;
   WarpRows r;
-  r.token = w / per;
+  r.token = div_small(w, per);
   r.row0 = static_cast<int>(w - r.token * per) * kWarpRows;
   return r;
 }
 
+// Start of the block of (page, head 0, block in page); a head further is
+// `step` bytes.
+template <int FMT, int D>
+__device__ __forceinline__ uint8_t* block_of_token(const qgemv_kv_cache& c, int64_t page, int at, int& step) {
+  step = (c.page_tokens / kKvBlockTokens) * KvLayout<FMT, D>::kBlock;
+  return kv_block<FMT, D>(c, page, 0, at / kKvBlockTokens);
+}
+
 template <int FMT, int D, typename T>
 __global__ void __launch_bounds__(kThreads) kv_write_kernel(const KvWriteParams p) {
-  constexpr int V = 16 / sizeof(T), kLanes = D / V, kAt = 32 / kLanes;  // kAt rows at a time
+  constexpr int kLanes = D / 8, kAt = 32 / kLanes;  // kAt rows at a time
   const int lane = threadIdx.x & 31, H = p.cache.kv_heads;
   const WarpRows wr = warp_rows(H);
   if (wr.token >= p.n_tokens) return;
   const int64_t slot = __ldg(p.slots + wr.token);
   if (slot < 0 || slot >= p.cache.n_pages * p.cache.page_tokens) return;
   const int shift = 31 - __clz(p.cache.page_tokens);
-  const int64_t page = slot >> shift;
   const int at = static_cast<int>(slot) & (p.cache.page_tokens - 1);
-  const int d0 = (lane % kLanes) * V;
-  float x[kWarpRows / kAt][V];
+  const int d0 = (lane % kLanes) * 8;
+  int step;
+  uint8_t* b0 = block_of_token<FMT, D>(p.cache, slot >> shift, at, step);
+  Raw<T> raw[kWarpRows / kAt];
 #pragma unroll
   for (int i = 0; i < kWarpRows / kAt; ++i) {
     const int row = min(wr.row0 + i * kAt + lane / kLanes, 2 * H - 1);
     const RowsIn& in = row & 1 ? p.v : p.k;
-    load_values<T>(static_cast<const T*>(in.ptr) + wr.token * in.token_stride + (row >> 1) * in.head_stride + d0, x[i]);
+    raw[i].load(static_cast<const T*>(in.ptr) + wr.token * in.token_stride + (row >> 1) * in.head_stride + d0);
   }
 #pragma unroll
   for (int i = 0; i < kWarpRows / kAt; ++i) {
     const int row = wr.row0 + i * kAt + lane / kLanes;
-    uint8_t* b = kv_block<FMT, D>(p.cache, page, min(row, 2 * H - 1) >> 1, at / kKvBlockTokens);
-    encode<FMT, D, V>(b, row & 1, at % kKvBlockTokens, d0, x[i], row < 2 * H);
+    float x[8];
+    raw[i].values(x);
+    encode<FMT, D>(b0 + static_cast<int64_t>(row >> 1) * step, row & 1, at % kKvBlockTokens, d0, x, row < 2 * H);
   }
 }
 
@@ -225,9 +230,10 @@ struct Eight {
         const uint32_t u = (&w.x)[i >> 1];
         x[i] = __half2float(__ushort_as_half(static_cast<unsigned short>(i & 1 ? u >> 16 : u & 0xffffu)));
       } else if constexpr (FMT == QGEMV_KV_INT8) {
-        x[i] = static_cast<float>(static_cast<int>(((i < 4 ? w.x : w.y) >> (8 * (i & 3))) & 255u) - 128) * s;
+        // 2^23 + code + 128 as a pattern, no conversion
+        x[i] = (__uint_as_float(__byte_perm(i < 4 ? w.x : w.y, 0x4B000000u, 0x7540 + (i & 3))) - 8388736.f) * s;
       } else {
-        x[i] = static_cast<float>(static_cast<int>((w.x >> (4 * i)) & 15u) - 8) * s;
+        x[i] = (__uint_as_float(((w.x >> (4 * i)) & 15u) | 0x4B000000u) - 8388616.f) * s;
       }
     }
   }
@@ -278,10 +284,12 @@ __global__ void __launch_bounds__(kThreads) kv_read_kernel(const KvReadParams p)
   const int d0 = (lane % kLanes) * 8;
   Eight<FMT, D> e[kWarpRows / kAt];
   if (there) {
+    int step;
+    const uint8_t* b0 = block_of_token<FMT, D>(p.cache, page, at, step);
 #pragma unroll
     for (int i = 0; i < kWarpRows / kAt; ++i) {
       const int row = min(wr.row0 + i * kAt + lane / kLanes, 2 * H - 1);
-      e[i].load(kv_block<FMT, D>(p.cache, page, row >> 1, at / kKvBlockTokens), row & 1, at % kKvBlockTokens, d0);
+      e[i].load(b0 + static_cast<int64_t>(row >> 1) * step, row & 1, at % kKvBlockTokens, d0);
     }
   }
 #pragma unroll

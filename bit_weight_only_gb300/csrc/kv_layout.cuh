@@ -64,6 +64,12 @@ inline int64_t kv_block_bytes(int format, int head_dim) {
   return int64_t(kKvBlockTokens) * 2 * row;
 }
 
+// a / b of values that nearly always fit 32 bits
+__device__ __forceinline__ int64_t div_small(int64_t a, int64_t b) {
+  if (((a | b) >> 32) == 0) return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
+  return a / b;
+}
+
 // Start of the block of (page, head, block in page).
 template <int FMT, int D>
 __device__ __forceinline__ uint8_t* kv_block(const qgemv_kv_cache& c, int64_t page, int head, int blk) {

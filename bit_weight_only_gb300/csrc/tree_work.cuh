@@ -31,12 +31,6 @@ struct SeqWork {
   int ctx, T;
 };
 
-// a / b of values that nearly always fit 32 bits
-__device__ __forceinline__ int64_t div_small(int64_t a, int64_t b) {
-  if (((a | b) >> 32) == 0) return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
-  return a / b;
-}
-
 template <int ROWS, int UNIT>
 __device__ __forceinline__ SeqWork seq_work(const TreeArgs& a, int b) {
   const TreeParams& p = a.p;
