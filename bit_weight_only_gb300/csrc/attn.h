@@ -79,8 +79,9 @@ cudaError_t launch_kv_read(const KvReadParams& p, int dtype, cudaStream_t s);
 cudaError_t launch_attn_tree(const TreeParams& p, cudaStream_t s);
 cudaError_t launch_attn_prompt(const PromptParams& p, cudaStream_t s);
 
-// Workspace of the attention calls: a header (the error word), then what the
-// tree kernel keeps (attn_tree.cu).
+// Workspace of the attention calls: a header -- the error word, and the prompt
+// kernel's counters (next piece, blocks that are done), 0 between calls -- then
+// the tree kernels' slots, which need no setting up (tree_work.cuh).
 constexpr int64_t kWsHeaderBytes = 256;
 int64_t tree_ws_bytes(int64_t n_seqs, int q_heads, int head_dim);
 

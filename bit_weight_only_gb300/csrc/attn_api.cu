@@ -125,7 +125,7 @@ int64_t qgemv_attn_ws_bytes(int64_t n_seqs, int q_heads, int head_dim) {
 
 int qgemv_attn_ws_init(void* ws, int64_t ws_bytes, void* stream) {
   if (!ws || ws_bytes < qgemv::kWsHeaderBytes) return fail(QGEMV_ERR_ARG, "the workspace is NULL or too small");
-  return done(cudaMemsetAsync(ws, 0, static_cast<size_t>(ws_bytes), static_cast<cudaStream_t>(stream)),
+  return done(cudaMemsetAsync(ws, 0, static_cast<size_t>(qgemv::kWsHeaderBytes), static_cast<cudaStream_t>(stream)),
               "clearing the workspace");
 }
 

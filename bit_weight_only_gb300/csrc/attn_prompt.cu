@@ -9,10 +9,17 @@
 // tiles of 128) of one key/value head and walks the keys in tiles of 128 up
 // to the last one that its rows see.
 //
-// Warps (12): two softmax warpgroups, one for each row tile, a thread for
-// each row; one warp issues the TMA loads of K and V (two stages each), one
-// the MMAs; two mend V tiles that hold masked positions.  Tensor memory, 512
-// columns: S0 S1 (128 each; P, 16-bit, replaces the first half of S), O0 O1.
+// One block per SM takes such pieces one after the other from a counter, those
+// with the most keys first within a sequence.  Its warps (12) run through the
+// pieces on their own, held together by mbarriers only, so that one piece's
+// start overlaps the end of the one before:
+//   0-7    two softmax warpgroups, one for each row tile, a thread for each row
+//   8      takes the pieces; issues the TMA loads of K and V (two stages each)
+//   9      the MMAs
+//   10-11  load Q into the operands' swizzle (as soon as the last product with
+//          the one before is done), and mend V tiles that hold masked positions
+// Tensor memory, 512 columns: S0 S1 (128 each; P, 16-bit, replaces the first
+// half of S), O0 O1.
 //   * QK of row tile i for key tile j + 1 follows PV of tile j in issue order,
 //     so P may lie over S, and a softmax warpgroup that sees S of tile j knows
 //     that its PV of tile j - 1 is done: it rescales O itself, and only when
@@ -20,7 +27,7 @@
 //     taken (P stays below 2^8, in range of fp16).  While one warpgroup takes
 //     its exponentials the tensor cores work on the other row tile.
 //   * A row's statistics live in its thread in fp32; no shuffles.
-//   * Masked scores are replaced by -inf.  V rows that some row of the block
+//   * Masked scores are replaced by -inf.  V rows that some row of the piece
 //     must not see cannot be masked so (0 * NaN): in key tiles with masked
 //     positions the mending warps zero what lies past the sequence and every
 //     infinity and NaN, and note the first position of each per column; the
@@ -33,19 +40,25 @@
 namespace qgemv {
 namespace {
 
-constexpr int kThreads = 384;
+constexpr int kThreads = 384;  // 12 warps
 constexpr int kRowsPerBlock = 256;
 constexpr int kKeys = 128;         // keys of a tile
 constexpr int kChunk = 128 * 128;  // bytes of 128 rows of 64 values
 constexpr int kErrPrompt = 16;
 constexpr float kLazy = 8.f;  // log2 of the growth that makes O be rescaled
 
+// Notes of infinite and NaN values: a copy for each of the two mending warps,
+// which clears it before it uses it, of three pieces in turn.
+constexpr int kNotes = 3;
+constexpr int kItems = 4;  // ring of pieces
+
 template <int D>
 struct Smem {
   static constexpr int kTile = D / 64 * kChunk;  // 128 rows
   static constexpr int kQ = 0, kK = 2 * kTile, kV = 4 * kTile, kBars = 6 * kTile;
-  static constexpr int kBad = kBars + 256;  // int[3][D]
-  static constexpr int kBytes = kBad + 3 * D * 4 + 1024;  // + alignment
+  static constexpr int kInts = kBars + 320;
+  static constexpr int kBad = kInts + 64;  // int[2][kNotes][3][D]
+  static constexpr int kBytes = kBad + 2 * kNotes * 3 * D * 4 + 1024;  // + alignment
 };
 
 struct PromptArgs {
@@ -53,11 +66,60 @@ struct PromptArgs {
   int G, n_slots;
 };
 
-// Barriers.
-// kBVm: a V tile with masked positions has landed (kBVf: one without); kBFix: it
-// is mended.  Their phases count the masked tiles of a stage.
-enum { kBQ = 0, kBKf = 2, kBVf = 4, kBVm = 6, kBKe = 8, kBVe = 10, kBFix = 12, kBS = 14, kBP = 16, kBO = 18, kBBad = 20,
-       kBDone = 21, kNBars = 22 };
+// Barriers: full / empty pairs of the rings.  kBVf: a V tile has landed; kBFix:
+// it is mended (or need not be).
+enum { kBQ = 0, kBQe = 2, kBKf = 4, kBKe = 6, kBVf = 8, kBVe = 10, kBFix = 12, kBS = 14, kBP = 16, kBO = 18, kBNf = 20,
+       kBNe = 23, kBIf = 26, kBIe = 30, kBDone = 34, kNBars = 35 };
+
+// A piece: 256 rows of a sequence and head.
+struct Piece {
+  int64_t q0, k0, R;   // first query and key, rows of the sequence (queries * G)
+  int64_t tok0, off;   // first token of the piece; query i sees keys j <= i + off
+  int64_t row0;
+  int nk, rem0, head;  // keys; head of the first row
+  int n_tiles[2], n_max, first_masked;
+
+  // keys that a row sees: 0 .. sees - 1
+  __device__ int sees(int64_t row, int G) const {
+    const int64_t v = div_small(row, G) + off + 1;
+    return static_cast<int>(v < 0 ? 0 : v < nk ? v : nk);
+  }
+
+  // False: a slot without rows.
+  __device__ bool decode(const PromptArgs& a, int id) {
+    const PromptParams& p = a.p;
+    const int G = a.G;
+    const int slot = a.n_slots - 1 - id / p.kv_heads;
+    head = id % p.kv_heads;
+    // The sequence of this slot: its tiles start at slot floor(cu * G / 256) + b,
+    // which leaves each sequence at least as many slots as it has tiles.
+    int lo = 0, hi = p.n_seqs - 1;
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (static_cast<int64_t>(__ldg(p.cu_q + mid)) * G / kRowsPerBlock + mid <= slot) lo = mid;
+      else hi = mid - 1;
+    }
+    q0 = max(__ldg(p.cu_q + lo), 0);
+    const int64_t nq = min(static_cast<int64_t>(__ldg(p.cu_q + lo + 1)), p.n_q) - q0;
+    row0 = (slot - (q0 * G / kRowsPerBlock + lo)) * kRowsPerBlock;
+    if (row0 < 0 || nq <= 0 || row0 >= nq * G) return false;
+    k0 = min(static_cast<int64_t>(max(__ldg(p.cu_k + lo), 0)), p.n_k);
+    nk = static_cast<int>(max(static_cast<int64_t>(0), min(static_cast<int64_t>(__ldg(p.cu_k + lo + 1)), p.n_k) - k0));
+    R = nq * G;
+    tok0 = div_small(row0, G);
+    rem0 = static_cast<int>(row0 - tok0 * G);
+    off = nk - nq;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int64_t r0 = row0 + 128 * i;
+      n_tiles[i] = r0 >= R ? 0 : (sees(min(r0 + 127, R - 1), G) + kKeys - 1) / kKeys;
+    }
+    n_max = max(n_tiles[0], n_tiles[1]);
+    // the first key tile with positions that some row of the piece does not see
+    first_masked = sees(row0, G) / kKeys;
+    return true;
+  }
+};
 
 template <int D, bool BF16>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -68,73 +130,43 @@ prompt_kernel(const PromptArgs a, const __grid_constant__ CUtensorMap kmap, cons
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + S::kBars);
-  volatile int* s_abort = reinterpret_cast<volatile int*>(bars + kNBars);
-  uint32_t* s_tmem = reinterpret_cast<uint32_t*>(bars + kNBars) + 1;
-  int* s_anybad = reinterpret_cast<int*>(bars + kNBars) + 2;
+  volatile int* s_int = reinterpret_cast<volatile int*>(smem + S::kInts);
+  volatile int* s_abort = s_int;
+  uint32_t* s_tmem = reinterpret_cast<uint32_t*>(smem + S::kInts) + 1;
+  volatile int* s_items = s_int + 2;            // [kItems]
+  volatile int* s_anybad = s_int + 2 + kItems;  // [2][kNotes]
   int* s_bad = reinterpret_cast<int*>(smem + S::kBad);
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const unsigned full = 0xffffffffu;
   const int G = a.G;
-  const int slot = a.n_slots - 1 - static_cast<int>(blockIdx.x / p.kv_heads);
-  const int head = static_cast<int>(blockIdx.x % p.kv_heads);
-
-  // The sequence of this slot: its tiles start at slot floor(cu * G / 256) + b,
-  // which leaves each sequence at least as many slots as it has tiles.
-  int seq;
-  {
-    int lo = 0, hi = p.n_seqs - 1;
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) >> 1;
-      if (static_cast<int64_t>(p.cu_q[mid]) * G / kRowsPerBlock + mid <= slot) lo = mid;
-      else hi = mid - 1;
-    }
-    seq = lo;
-  }
-  const int64_t q0 = max(p.cu_q[seq], 0);
-  const int64_t nq = min(static_cast<int64_t>(p.cu_q[seq + 1]), p.n_q) - q0;
-  const int64_t row0 = (slot - (q0 * G / kRowsPerBlock + seq)) * kRowsPerBlock;
-  if (row0 < 0 || nq <= 0 || row0 >= nq * G) return;
-  const int64_t k0 = min(static_cast<int64_t>(max(p.cu_k[seq], 0)), p.n_k);
-  const int nk = static_cast<int>(max(static_cast<int64_t>(0), min(static_cast<int64_t>(p.cu_k[seq + 1]), p.n_k) - k0));
-  const int64_t tok0 = row0 / G;  // first token of the block, and the head of its first row
-  const int rem0 = static_cast<int>(row0 - tok0 * G);
-  const int64_t off = nk - nq;  // query i sees keys j <= i + off
-  const int64_t R = nq * G;
-  auto sees = [&](int64_t row) {  // keys that a row sees: 0 .. sees - 1
-    const int64_t v = row / G + off + 1;
-    return static_cast<int>(v < 0 ? 0 : v < nk ? v : nk);
-  };
-  int n_tiles[2];
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const int64_t r0 = row0 + 128 * i;
-    n_tiles[i] = r0 >= R ? 0 : (sees(min(r0 + 127, R - 1)) + kKeys - 1) / kKeys;
-  }
-  const int n_max = max(n_tiles[0], n_tiles[1]);
-  // the first key tile with positions that some row of the block does not see
-  const int first_masked = sees(row0) / kKeys;
 
   if (tid == 0) {
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&bars[kBQ + i], 128);
+      mbar_init(&bars[kBQ + i], 64);
+      mbar_init(&bars[kBQe + i], 1);
       mbar_init(&bars[kBKf + i], 1);
-      mbar_init(&bars[kBVf + i], 1);
-      mbar_init(&bars[kBVm + i], 1);
       mbar_init(&bars[kBKe + i], 1);
+      mbar_init(&bars[kBVf + i], 1);
       mbar_init(&bars[kBVe + i], 1);
       mbar_init(&bars[kBFix + i], 64);
       mbar_init(&bars[kBS + i], 1);
       mbar_init(&bars[kBP + i], 128);
       mbar_init(&bars[kBO + i], 1);
     }
-    mbar_init(&bars[kBBad], 64);
+    for (int i = 0; i < kNotes; ++i) {
+      mbar_init(&bars[kBNf + i], 64);
+      mbar_init(&bars[kBNe + i], 256);
+    }
+    for (int i = 0; i < kItems; ++i) {
+      mbar_init(&bars[kBIf + i], 1);
+      mbar_init(&bars[kBIe + i], 11);  // the other warps
+    }
     mbar_init(&bars[kBDone], 1);
     fence_mbarrier_init();
     *s_abort = 0;
-    *s_anybad = 0;
   }
-  for (int i = tid; i < 3 * D; i += kThreads) s_bad[i] = 0x7fffffff;
-  if (warp == 8) tmem_alloc_all(s_tmem);
+  if (warp == 9) tmem_alloc_all(s_tmem);
   tcgen_before_sync();
   __syncthreads();
   tcgen_after_sync();
@@ -153,81 +185,147 @@ prompt_kernel(const PromptArgs a, const __grid_constant__ CUtensorMap kmap, cons
     }
     return true;
   };
+  // every lane waits; a lane whose wait ran out stops the warp
+  auto wait_all = [&](int bar, uint32_t parity) { return __all_sync(full, wait(bar, parity)) != 0; };
+  // parity of use n of a ring of k stages: of what fills it, of its being free again
+  auto used = [](int n, int k) { return static_cast<uint32_t>((n / k) & 1); };
+  auto freed = [](int n, int k) { return static_cast<uint32_t>(((n / k) - 1) & 1); };
 
-  // V tile j: the barrier of its landing, and the parity of it and of kBFix
-  auto v_bar = [&](int j) { return (j >= first_masked ? kBVm : kBVf) + (j & 1); };
-  auto v_parity = [&](int j) { return static_cast<uint32_t>(((j >= first_masked ? j - first_masked : j) >> 1) & 1); };
+  // The next piece, for the warps that are told (a whole warp calls it); -1: no
+  // more, or a wait ran out.
+  int n_item = 0;
+  auto next_piece = [&](Piece& pc) -> bool {
+    const int st = n_item % kItems;
+    if (!wait_all(kBIf + st, used(n_item, kItems))) return false;
+    const int id = s_items[st];
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&bars[kBIe + st]);
+    ++n_item;
+    if (id < 0) return false;
+    pc.decode(a, id);
+    return true;
+  };
 
+  Piece pc;
   if (warp >= 8) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
     if (warp == 8) {
-      // ---- TMA: K and V tiles
-      if (lane == 0) {
-        int issued_k = 0, issued_v = 0;
-        auto load = [&](const CUtensorMap* map, int full, int empty, int base, int j) -> bool {
-          const int st = j & 1;
-          if (j >= 2 && !wait(empty + st, ((j >> 1) - 1) & 1)) return false;
-          mbar_arrive_expect_tx(&bars[full], S::kTile);
-#pragma unroll
-          for (int c = 0; c < D / 64; ++c)
-            tma_load_3d(smem + base + st * S::kTile + c * kChunk, map, 64 * c, head, static_cast<int>(k0) + j * kKeys,
-                        &bars[full]);
-          return true;
-        };
-        for (int j = 0; j < n_max; ++j) {
-          if (!load(&kmap, kBKf + (j & 1), kBKe, S::kK, j)) break;
-          ++issued_k;
-          if (!load(&vmap, v_bar(j), kBVe, S::kV, j)) break;
-          ++issued_v;
+      // ---- pieces; K and V tiles
+      int* counters = reinterpret_cast<int*>(p.ws) + 1;  // next piece, blocks that are done
+      const int total = a.n_slots * p.kv_heads;
+      const bool leader = elect_one();
+      auto take = [&]() {
+        int id = 0;
+        if (lane == 0) id = atomicAdd(counters, 1);
+        return __shfl_sync(full, id, 0);
+      };
+      int jt = 0;
+      bool ok = true;
+      int ahead = take();
+      while (ok) {
+        const int id = ahead;
+        const bool more = id < total;
+        if (more) {
+          ahead = take();
+          if (!pc.decode(a, id)) continue;
         }
-        // Copies still in flight (after an abort) must land before the block ends.
-        for (int j = max(0, issued_k - 2); j < issued_k; ++j) mbar_wait_bounded(&bars[kBKf + (j & 1)], (j >> 1) & 1);
-        for (int j = max(0, issued_v - 2); j < issued_v; ++j) mbar_wait_bounded(&bars[v_bar(j)], v_parity(j));
+        const int st = n_item % kItems;
+        if (n_item >= kItems) ok = wait_all(kBIe + st, freed(n_item, kItems));
+        if (!ok) break;
+        if (lane == 0) {
+          s_items[st] = more ? id : -1;
+          mbar_arrive(&bars[kBIf + st]);
+        }
+        __syncwarp();
+        ++n_item;
+        if (!more) break;
+        for (int j = 0; ok && j < pc.n_max; ++j, ++jt) {
+          const int ks = jt & 1;
+          auto load = [&](const CUtensorMap* map, int fullb, int empty, int base) -> bool {
+            if (jt >= 2 && !wait_all(empty + ks, freed(jt, 2))) return false;
+            if (leader) {
+              mbar_arrive_expect_tx(&bars[fullb + ks], S::kTile);
+#pragma unroll
+              for (int c = 0; c < D / 64; ++c)
+                tma_load_3d(smem + base + ks * S::kTile + c * kChunk, map, 64 * c, pc.head,
+                            static_cast<int>(pc.k0) + j * kKeys, &bars[fullb + ks]);
+            }
+            __syncwarp();
+            return true;
+          };
+          ok = load(&kmap, kBKf, kBKe, S::kK);
+          if (!ok) break;
+          ok = load(&vmap, kBVf, kBVe, S::kV);
+          if (!ok) {  // the K tile is on its way: it must land before the block ends
+            mbar_wait_bounded(&bars[kBKf + ks], used(jt, 2));
+            break;
+          }
+        }
+      }
+      // copies in flight (after an abort) must land before the block ends
+      for (int n = max(0, jt - 2); n < jt; ++n) {
+        mbar_wait_bounded(&bars[kBKf + (n & 1)], used(n, 2));
+        mbar_wait_bounded(&bars[kBVf + (n & 1)], used(n, 2));
+      }
+      if (lane == 0) {  // the last block leaves the counters as it found them
+        __threadfence();
+        if (atomicAdd(counters + 1, 1) == static_cast<int>(gridDim.x) - 1) {
+          counters[0] = 0;
+          counters[1] = 0;
+        }
       }
     } else if (warp == 9) {
       // ---- MMAs
       const bool leader = elect_one();
-      if (n_max > 0) {
-        constexpr uint32_t id_qk = mma_idesc(BF16, false, false, kKeys), id_pv = mma_idesc(BF16, false, true, D);
-        const uint32_t sq = smem_u32(smem + S::kQ), sk = smem_u32(smem + S::kK), sv = smem_u32(smem + S::kV);
+      constexpr uint32_t id_qk = mma_idesc(BF16, false, false, kKeys), id_pv = mma_idesc(BF16, false, true, D);
+      const uint32_t sq = smem_u32(smem + S::kQ), sk = smem_u32(smem + S::kK), sv = smem_u32(smem + S::kV);
+      int jt = 0, n_qi[2] = {0, 0}, n_s[2] = {0, 0};
+      bool ok = true;
+      while (ok && next_piece(pc)) {
         auto qk = [&](int i, int j) {
           const uint64_t da = sw128_desc(sq + i * S::kTile, 0, 1024);
-          const uint64_t db = sw128_desc(sk + (j & 1) * S::kTile, 0, 1024);
+          const uint64_t db = sw128_desc(sk + ((jt + j) & 1) * S::kTile, 0, 1024);
 #pragma unroll
           for (int k = 0; k < D / 16; ++k) {
             const uint32_t o = ((k >> 2) * kChunk + (k & 3) * 32) >> 4;
             mma_ss(tbase + 128 * i, da + o, db + o, id_qk, k > 0, leader);
           }
           mma_commit(&bars[kBS + i], leader);
+          if (j + 1 == pc.n_tiles[i]) mma_commit(&bars[kBQe + i], leader);
         };
         auto pv = [&](int i, int j) {
-          const uint64_t db = sw128_desc(sv + (j & 1) * S::kTile, kChunk, 1024);
+          const uint64_t db = sw128_desc(sv + ((jt + j) & 1) * S::kTile, kChunk, 1024);
 #pragma unroll
           for (int k = 0; k < kKeys / 16; ++k)
             mma_ts(tbase + 256 + 128 * i, tbase + 128 * i + 8 * k, db + ((k * 2048) >> 4), id_pv, j > 0 || k > 0, leader);
         };
-        // every lane waits; a lane whose wait ran out stops them all
-        auto wait_all = [&](int bar, uint32_t parity) { return __all_sync(0xffffffffu, wait(bar, parity)) != 0; };
-        bool ok = wait_all(kBKf, 0);
-        for (int i = 0; i < 2; ++i)
-          if (ok && n_tiles[i] > 0) {
-            ok = wait_all(kBQ + i, 0);
-            tcgen_after_sync();
-            if (ok) qk(i, 0);
-          }
-        if (ok) mma_commit(&bars[kBKe], leader);
-        for (int j = 0; ok && j < n_max; ++j) {
+        if (pc.n_max > 0) {
+          ok = wait_all(kBKf + (jt & 1), used(jt, 2));
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+            if (ok && pc.n_tiles[i] > 0) {
+              ok = wait_all(kBQ + i, n_qi[i] & 1);
+              ++n_qi[i];
+              tcgen_after_sync();
+              if (ok) qk(i, 0);
+            }
+          if (ok) mma_commit(&bars[kBKe + (jt & 1)], leader);
+        }
+        for (int j = 0; ok && j < pc.n_max; ++j) {
+          const int x = jt + j;
           bool have_v = false, have_k = false;
-          for (int i = 0; ok && i < 2; ++i) {
-            if (j >= n_tiles[i]) continue;
-            if (!have_v) ok = wait_all((j >= first_masked ? kBFix : kBVf) + (j & 1), v_parity(j));
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            if (!ok) break;
+            if (j >= pc.n_tiles[i]) continue;
+            if (!have_v) ok = wait_all(kBFix + (x & 1), used(x, 2));
             have_v = true;
-            if (ok) ok = wait_all(kBP + i, j & 1);
+            if (ok) ok = wait_all(kBP + i, (n_s[i] + j) & 1);
             if (!ok) break;
             tcgen_after_sync();
             pv(i, j);
-            if (j + 1 < n_tiles[i]) {
-              if (!have_k) ok = wait_all(kBKf + ((j + 1) & 1), ((j + 1) >> 1) & 1);
+            if (j + 1 < pc.n_tiles[i]) {
+              if (!have_k) ok = wait_all(kBKf + ((x + 1) & 1), used(x + 1, 2));
               have_k = true;
               if (ok) qk(i, j + 1);
             } else {
@@ -235,96 +333,139 @@ prompt_kernel(const PromptArgs a, const __grid_constant__ CUtensorMap kmap, cons
             }
           }
           if (ok) {
-            mma_commit(&bars[kBVe + (j & 1)], leader);
-            if (have_k) mma_commit(&bars[kBKe + ((j + 1) & 1)], leader);
+            mma_commit(&bars[kBVe + (x & 1)], leader);
+            if (have_k) mma_commit(&bars[kBKe + ((x + 1) & 1)], leader);
           }
         }
-        if (!ok) {  // MMAs in flight: let them finish before tensor memory is freed
-          mma_commit(&bars[kBDone], leader);
-          mbar_wait_bounded(&bars[kBDone], 0);
-        }
+        jt += pc.n_max;
+        n_s[0] += pc.n_tiles[0];
+        n_s[1] += pc.n_tiles[1];
+      }
+      if (!ok) {  // MMAs in flight: let them finish before tensor memory is freed
+        mma_commit(&bars[kBDone], leader);
+        mbar_wait_bounded(&bars[kBDone], 0);
       }
     } else {
-      // ---- mending of V tiles with masked positions
+      // ---- Q tiles; V tiles with masked positions
       const int t = tid - 320;
-      for (int j = first_masked; j < n_max; ++j) {
-        if (!wait(v_bar(j), v_parity(j))) break;
-        uint8_t* v = smem + S::kV + (j & 1) * S::kTile;
-        const int live = min(kKeys, nk - j * kKeys);  // positions of the tile inside the sequence
-        constexpr uint32_t kExp = BF16 ? 0x7F807F80u : 0x7C007C00u, kOne = BF16 ? 0x00800080u : 0x04000400u;
-        bool wrote = false;
-        for (int u = t; u < S::kTile / 16; u += 64) {
-          uint4* at = reinterpret_cast<uint4*>(v + u * 16);
-          const int r = (u >> 3) & 127;
-          if (r >= live) {
-            *at = make_uint4(0u, 0u, 0u, 0u);
-            wrote = true;
-            continue;
-          }
-          const uint4 w = *at;
-          const uint32_t bad = (((w.x & kExp) + kOne) | ((w.y & kExp) + kOne) | ((w.z & kExp) + kOne) | ((w.w & kExp) + kOne)) &
-                               0x80008000u;
-          if (bad) {
-            uint16_t* h = reinterpret_cast<uint16_t*>(at);
-            const int d0 = (u >> 10) * 64 + (((u & 7) ^ (r & 7)) << 3);
-            for (int e = 0; e < 8; ++e) {
-              const uint16_t x = h[e];
-              if ((x & (kExp & 0xffffu)) != (kExp & 0xffffu)) continue;
-              const int kind = (x & 0x7fff & ~(kExp & 0xffffu)) ? 0 : x >> 15 ? 2 : 1;
-              atomicMin(&s_bad[kind * D + d0 + e], j * kKeys + r);
-              h[e] = 0;
-            }
-            *s_anybad = 1;
-            wrote = true;
-          }
-        }
-        if (wrote) fence_async_smem();
-        mbar_arrive(&bars[kBFix + (j & 1)]);
-      }
-      mbar_arrive(&bars[kBBad]);
-    }
-  } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
-    // ---- softmax warpgroup i: Q rows in, then a thread for each row
-    const int i = warp >> 2, wt = tid & 127;
-    const int64_t r0 = row0 + 128 * i;
-    const bool active = r0 < R;
-    if (active) {
-      uint8_t* q = smem + S::kQ + i * S::kTile;
-      constexpr int U = D / 8;  // 16-byte units of a row
       const uint32_t flip = p.scale < 0.f ? 0x80008000u : 0u;  // a negative scale goes to Q
       const T* qb = static_cast<const T*>(p.q.ptr);
-#pragma unroll 4
-      for (int it = 0; it < U; ++it) {
-        const int idx = it * 128 + wt;
-        const int r = idx / U, u = idx % U;
-        uint4 w = make_uint4(0u, 0u, 0u, 0u);
-        if (r0 + r < R) {
-          const int x = rem0 + 128 * i + r, tok = x / G;
-          w = __ldg(reinterpret_cast<const uint4*>(qb + (q0 + tok0 + tok) * p.q.token_stride +
-                                                   (head * G + x - tok * G) * p.q.head_stride + 8 * u));
-          w.x ^= flip, w.y ^= flip, w.z ^= flip, w.w ^= flip;
-        }
-        *reinterpret_cast<uint4*>(q + (u >> 3) * kChunk + r * 128 + (((u & 7) ^ (r & 7)) << 4)) = w;
-      }
-      fence_async_smem();
-      mbar_arrive(&bars[kBQ + i]);
-
-      const int64_t row = r0 + wt;
-      const int my_sees = sees(min(row, R - 1));
-      const int all_see = sees(r0);  // what every row of the tile sees
-      const int n = i == 0 ? n_tiles[0] : n_tiles[1];
-      const uint32_t t_lane = static_cast<uint32_t>(32 * (warp & 3)) << 16;
-      const uint32_t t_s = tbase + t_lane + 128 * i, t_o = tbase + t_lane + 256 + 128 * i;
-      const float sl = fmaxf(fabsf(p.scale) * kLog2e, 1.2e-38f);  // not 0: -inf * sl stays -inf
-      float m = -INFINITY, l = 0.f;
+      // x / G by the high word of a product: exact for x * G below 2^32
+      const uint32_t g_inv = G == 1 ? 0u : 0xffffffffu / G + 1u;
+      int jt = 0, n_qi[2] = {0, 0};
       bool ok = true;
-      for (int j = 0; j < n; ++j) {
-        ok = wait(kBS + i, j & 1);
-        if (!__all_sync(0xffffffffu, ok)) {
-          ok = false;
-          break;
+      while (ok && next_piece(pc)) {
+        const int note = (n_item - 1) % kNotes;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          if (!ok) break;
+          if (pc.n_tiles[i] == 0) continue;
+          if (n_qi[i] > 0) ok = wait_all(kBQe + i, (n_qi[i] - 1) & 1);
+          if (!ok) break;
+          ++n_qi[i];
+          uint8_t* q = smem + S::kQ + i * S::kTile;
+          constexpr int U = D / 8;  // 16-byte units of a row
+          const int64_t r0 = pc.row0 + 128 * i;
+          // all copies in flight at once; rows past the sequence are zeros
+          auto place = [&](int it) {
+            const int idx = it * 64 + t, r = idx / U, u = idx % U;
+            return q + (u >> 3) * kChunk + r * 128 + (((u & 7) ^ (r & 7)) << 4);
+          };
+#pragma unroll 8
+          for (int it = 0; it < 2 * U; ++it) {
+            const int idx = it * 64 + t, r = idx / U, u = idx % U;
+            const uint32_t x = pc.rem0 + 128 * i + r, tok = G == 1 ? x : __umulhi(x, g_inv);
+            const bool on = r0 + r < pc.R;
+            const T* src = on ? qb + (pc.q0 + pc.tok0 + tok) * p.q.token_stride + (pc.head * G + x - tok * G) * p.q.head_stride + 8 * u
+                              : qb;
+            cp_async_16(place(it), src, on);
+          }
+          cp_async_wait();
+          if (flip)
+            for (int it = 0; it < 2 * U; ++it) {
+              uint4* at = reinterpret_cast<uint4*>(place(it));
+              uint4 w = *at;
+              w.x ^= flip, w.y ^= flip, w.z ^= flip, w.w ^= flip;
+              *at = w;
+            }
+          fence_async_smem();
+          mbar_arrive(&bars[kBQ + i]);
         }
+        if (ok && n_item > kNotes) ok = wait_all(kBNe + note, freed(n_item - 1, kNotes));
+        int* notes = s_bad + ((warp - 10) * kNotes + note) * 3 * D;
+        if (pc.first_masked < pc.n_max)
+          for (int x = lane; x < 3 * D; x += 32) notes[x] = 0x7fffffff;
+        if (lane == 0) s_anybad[(warp - 10) * kNotes + note] = 0;
+        __syncwarp();
+        for (int j = 0; ok && j < pc.n_max; ++j, ++jt) {
+          ok = wait_all(kBVf + (jt & 1), used(jt, 2));
+          if (!ok) break;
+          if (j >= pc.first_masked) {
+            uint8_t* v = smem + S::kV + (jt & 1) * S::kTile;
+            const int live = min(kKeys, pc.nk - j * kKeys);  // positions of the tile inside the sequence
+            constexpr uint32_t kExp = BF16 ? 0x7F807F80u : 0x7C007C00u, kOne = BF16 ? 0x00800080u : 0x04000400u;
+            bool wrote = false;
+#pragma unroll 4
+            for (int u = t; u < S::kTile / 16; u += 64) {
+              uint4* at = reinterpret_cast<uint4*>(v + u * 16);
+              const int r = (u >> 3) & 127;
+              if (r >= live) {
+                *at = make_uint4(0u, 0u, 0u, 0u);
+                wrote = true;
+                continue;
+              }
+              const uint4 w = *at;
+              const uint32_t bad = (((w.x & kExp) + kOne) | ((w.y & kExp) + kOne) | ((w.z & kExp) + kOne) | ((w.w & kExp) + kOne)) &
+                                   0x80008000u;
+              if (bad) {
+                uint16_t* h = reinterpret_cast<uint16_t*>(at);
+                const int d0 = (u >> 10) * 64 + (((u & 7) ^ (r & 7)) << 3);
+                for (int e = 0; e < 8; ++e) {
+                  const uint16_t x = h[e];
+                  if ((x & (kExp & 0xffffu)) != (kExp & 0xffffu)) continue;
+                  const int kind = (x & 0x7fff & ~(kExp & 0xffffu)) ? 0 : x >> 15 ? 2 : 1;
+                  atomicMin(&notes[kind * D + d0 + e], j * kKeys + r);
+                  s_anybad[(warp - 10) * kNotes + note] = 1;
+                  h[e] = 0;
+                }
+                wrote = true;
+              }
+            }
+            if (wrote) fence_async_smem();
+          }
+          mbar_arrive(&bars[kBFix + (jt & 1)]);
+        }
+        mbar_arrive(&bars[kBNf + note]);
+      }
+    }
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+    // ---- softmax warpgroup i, a thread for each row
+    const int i = warp >> 2, wt = tid & 127;
+    const uint32_t t_lane = static_cast<uint32_t>(32 * (warp & 3)) << 16;
+    const uint32_t t_s = tbase + t_lane + 128 * i, t_o = tbase + t_lane + 256 + 128 * i;
+    const float sl = fmaxf(fabsf(p.scale) * kLog2e, 1.2e-38f);  // not 0: -inf * sl stays -inf
+    int n_s = 0, n_o = 0;  // scores and results so far
+    bool ok = true;
+    while (ok && next_piece(pc)) {
+      const int note = (n_item - 1) % kNotes;
+      const int64_t row = pc.row0 + 128 * i + wt;
+      const bool store = row < pc.R;
+      const int n = i == 0 ? pc.n_tiles[0] : pc.n_tiles[1];
+      const int my_sees = pc.sees(min(row, pc.R - 1), G);
+      const int all_see = pc.sees(pc.row0 + 128 * i, G);  // what every row of the tile sees
+      T* out;
+      float* lse;
+      {
+        const int x = pc.rem0 + 128 * i + wt, tok = x / G;
+        const int h = pc.head * G + x - tok * G;
+        out = static_cast<T*>(p.out.ptr) + (pc.q0 + pc.tok0 + tok) * p.out.token_stride + h * p.out.head_stride;
+        lse = p.lse ? p.lse + (pc.q0 + pc.tok0 + tok) * p.q_heads + h : nullptr;
+      }
+      float m = -INFINITY, l = 0.f;
+      for (int j = 0; j < n; ++j, ++n_s) {
+        ok = wait_all(kBS + i, n_s & 1);
+        if (!ok) break;
         tcgen_after_sync();
         uint32_t s[128];
 #pragma unroll
@@ -347,15 +488,14 @@ prompt_kernel(const PromptArgs a, const __grid_constant__ CUtensorMap kmap, cons
             top[e] = c + e + 4 < 128 ? fmaxf(top[e], fmaxf(__uint_as_float(s[c + e]), __uint_as_float(s[c + e + 4])))
                                      : fmaxf(top[e], __uint_as_float(s[c + e]));
         const float mt = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * sl;
-        const bool grow = mt > m + kLazy || (m == -INFINITY && mt > -INFINITY);
-        if (__any_sync(0xffffffffu, grow)) {
+        if (__any_sync(full, mt > m + kLazy)) {
           const float mn = fmaxf(m, mt);
           const float f = m == -INFINITY ? 0.f : ex2(m - mn);
           l *= f;
           m = mn;
           if (j > 0) {
             const uint64_t f2 = pack2(f, f);
-#pragma unroll
+#pragma unroll 1
             for (int c = 0; c < D; c += 32) {
               uint32_t o[32];
               tmem_ld32(t_o + c, o);
@@ -393,16 +533,21 @@ prompt_kernel(const PromptArgs a, const __grid_constant__ CUtensorMap kmap, cons
         mbar_arrive(&bars[kBP + i]);
       }
       // ---- epilogue
-      ok = ok && (n == 0 || wait(kBO + i, 0)) && wait(kBBad, 0);
-      if (__all_sync(0xffffffffu, ok)) {
-        tcgen_after_sync();
-        const int64_t tok = row / G;
-        const int h = head * G + static_cast<int>(row - tok * G);
-        const bool store = row < R;
-        T* out = static_cast<T*>(p.out.ptr) + (q0 + tok) * p.out.token_stride + h * p.out.head_stride;
+      if (!ok) break;
+      if (n > 0) {
+        ok = wait_all(kBO + i, n_o & 1);
+        ++n_o;
+      }
+      ok = ok && wait_all(kBNf + note, used(n_item - 1, kNotes));
+      if (!ok) break;
+      tcgen_after_sync();
+      const bool bad = s_anybad[note] != 0 || s_anybad[kNotes + note] != 0;
+      const int* bad0 = s_bad + note * 3 * D;
+      const int* bad1 = s_bad + (kNotes + note) * 3 * D;
+      const bool use0 = s_anybad[note] != 0, use1 = s_anybad[kNotes + note] != 0;
+      {
         const float inv = l == 0.f ? 0.f : 1.f / l;
-        const bool bad = *s_anybad != 0;
-#pragma unroll
+#pragma unroll 1
         for (int c = 0; c < D; c += 32) {
           uint32_t o[32];
           if (n > 0) {
@@ -414,7 +559,8 @@ prompt_kernel(const PromptArgs a, const __grid_constant__ CUtensorMap kmap, cons
           if (bad) {
 #pragma unroll
             for (int e = 0; e < 32; ++e) {
-              const bool nan = s_bad[c + e] < my_sees, up = s_bad[D + c + e] < my_sees, down = s_bad[2 * D + c + e] < my_sees;
+              auto seen = [&](int x) { return (use0 && bad0[x] < my_sees) || (use1 && bad1[x] < my_sees); };
+              const bool nan = seen(c + e), up = seen(D + c + e), down = seen(2 * D + c + e);
               if (nan || (up && down)) o[e] = 0x7fffffffu;
               else if (up) o[e] = 0x7f800000u;
               else if (down) o[e] = 0xff800000u;
@@ -432,13 +578,14 @@ prompt_kernel(const PromptArgs a, const __grid_constant__ CUtensorMap kmap, cons
             }
           }
         }
-        if (store && p.lse) p.lse[(q0 + tok) * p.q_heads + h] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+        if (store && lse) *lse = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
         tcgen_before_sync();
       }
+      mbar_arrive(&bars[kBNe + note]);
     }
   }
   __syncthreads();
-  if (warp == 8) tmem_free_all(tbase);
+  if (warp == 9) tmem_free_all(tbase);
 }
 
 using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
@@ -487,7 +634,14 @@ cudaError_t launch(const PromptParams& p, cudaStream_t s) {
   static const cudaError_t attr =
       cudaFuncSetAttribute(prompt_kernel<D, BF16>, cudaFuncAttributeMaxDynamicSharedMemorySize, Smem<D>::kBytes);
   if (attr != cudaSuccess) return attr;
-  prompt_kernel<D, BF16><<<static_cast<unsigned>(a.n_slots) * p.kv_heads, kThreads, Smem<D>::kBytes, s>>>(a, km, vm);
+  static const int sms = [] {
+    int dev = 0, n = 0;
+    cudaGetDevice(&dev);
+    cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
+    return n;
+  }();
+  const int64_t pieces = static_cast<int64_t>(a.n_slots) * p.kv_heads;
+  prompt_kernel<D, BF16><<<static_cast<unsigned>(pieces < sms ? pieces : sms), kThreads, Smem<D>::kBytes, s>>>(a, km, vm);
   return cudaGetLastError();
 }
 
