@@ -81,8 +81,9 @@ cudaError_t launch_attn_prompt(const PromptParams& p, cudaStream_t s);
 
 // Workspace of the attention calls: a header -- the error word, and the prompt
 // kernel's counters (next piece, blocks that are done), 0 between calls -- then
-// the tree kernels' slots, which need no setting up (tree_work.cuh).
+// the slots of whichever kernel runs, which need no setting up.
 constexpr int64_t kWsHeaderBytes = 256;
-int64_t tree_ws_bytes(int64_t n_seqs, int q_heads, int head_dim);
+int64_t tree_ws_bytes(int head_dim);
+int64_t prompt_ws_bytes(int head_dim);
 
 }  // namespace qgemv

@@ -120,7 +120,8 @@ int qgemv_kv_read(const qgemv_kv_cache* cache, const int32_t* table, int64_t tab
 
 int64_t qgemv_attn_ws_bytes(int64_t n_seqs, int q_heads, int head_dim) {
   if (n_seqs < 0 || n_seqs > kMaxTokens || q_heads <= 0 || q_heads > 1024 || (head_dim != 64 && head_dim != 128)) return 0;
-  return qgemv::kWsHeaderBytes + qgemv::tree_ws_bytes(n_seqs, q_heads, head_dim);
+  const int64_t tree = qgemv::tree_ws_bytes(head_dim), prompt = qgemv::prompt_ws_bytes(head_dim);
+  return qgemv::kWsHeaderBytes + (tree > prompt ? tree : prompt);
 }
 
 int qgemv_attn_ws_init(void* ws, int64_t ws_bytes, void* stream) {

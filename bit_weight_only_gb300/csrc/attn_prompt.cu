@@ -9,7 +9,10 @@
 // tiles of 128) of one key/value head and walks the keys in tiles of 128 up
 // to the last one that its rows see.
 //
-// One block per SM takes such pieces one after the other from a counter, those
+// Where there are too few such pieces to fill the GPU, a piece is cut into parts
+// of its keys; their unnormalised results go to the workspace, and a second
+// kernel joins them in order.
+// One block per SM takes the pieces one after the other from a counter, those
 // with the most keys first within a sequence.  Its warps (12) run through the
 // pieces on their own, held together by mbarriers only, so that one piece's
 // start overlaps the end of the one before:
@@ -34,6 +37,10 @@
 //     epilogue gives it to the rows that see it.
 // Every wait is bounded; on a timeout the block records the error, waits for
 // its own copies and MMAs, frees tensor memory and returns.
+#include <algorithm>
+#include <cmath>
+#include <type_traits>
+
 #include "kv_layout.cuh"
 #include "tc_common.cuh"
 
@@ -51,19 +58,18 @@ constexpr float kLazy = 8.f;  // log2 of the growth that makes O be rescaled
 // which clears it before it uses it, of three pieces in turn.
 constexpr int kNotes = 3;
 constexpr int kItems = 4;  // ring of pieces
+constexpr int kMaxParts = 8;
 
-template <int D>
-struct Smem {
-  static constexpr int kTile = D / 64 * kChunk;  // 128 rows
-  static constexpr int kQ = 0, kK = 2 * kTile, kV = 4 * kTile, kBars = 6 * kTile;
-  static constexpr int kInts = kBars + 320;
-  static constexpr int kBad = kInts + 64;  // int[2][kNotes][3][D]
-  static constexpr int kBytes = kBad + 2 * kNotes * 3 * D * 4 + 1024;  // + alignment
-};
+// Workspace slot of a part: O [256][D], then m and l [256][2].
+constexpr int kPartSlots = 304;
+__host__ __device__ constexpr int64_t part_floats(int D) { return static_cast<int64_t>(kRowsPerBlock) * (D + 2); }
+__device__ __forceinline__ float* part_slot(const PromptParams& p, int id, int D) {
+  return reinterpret_cast<float*>(p.ws + kWsHeaderBytes) + id * part_floats(D);
+}
 
 struct PromptArgs {
   PromptParams p;
-  int G, n_slots;
+  int G, n_slots, parts;
 };
 
 // Barriers: full / empty pairs of the rings.  kBVf: a V tile has landed; kBFix:
@@ -71,13 +77,17 @@ struct PromptArgs {
 enum { kBQ = 0, kBQe = 2, kBKf = 4, kBKe = 6, kBVf = 8, kBVe = 10, kBFix = 12, kBS = 14, kBP = 16, kBO = 18, kBNf = 20,
        kBNe = 23, kBIf = 26, kBIe = 30, kBDone = 34, kNBars = 35 };
 
-// A piece: 256 rows of a sequence and head.
+// A piece: 256 rows of a sequence and head, and the key tiles t0 .. of them
+// that this part takes.
 struct Piece {
   int64_t q0, k0, R;   // first query and key, rows of the sequence (queries * G)
   int64_t tok0, off;   // first token of the piece; query i sees keys j <= i + off
   int64_t row0;
   int nk, rem0, head;  // keys; head of the first row
-  int n_tiles[2], n_max, first_masked;
+  int id;              // of the part; -1: no more
+  int t0, n[2], n_max; // key tiles: of each row tile, and the more of the two
+  int first_masked;    // of those, the first with positions that some row of the piece does not see
+  int pad[2];
 
   // keys that a row sees: 0 .. sees - 1
   __device__ int sees(int64_t row, int G) const {
@@ -86,11 +96,12 @@ struct Piece {
   }
 
   // False: a slot without rows.
-  __device__ bool decode(const PromptArgs& a, int id) {
+  __device__ bool decode(const PromptArgs& a, int part_id) {
     const PromptParams& p = a.p;
-    const int G = a.G;
-    const int slot = a.n_slots - 1 - id / p.kv_heads;
-    head = id % p.kv_heads;
+    const int G = a.G, part = part_id % a.parts, pid = part_id / a.parts;
+    const int slot = a.n_slots - 1 - pid / p.kv_heads;
+    id = part_id;
+    head = pid % p.kv_heads;
     // The sequence of this slot: its tiles start at slot floor(cu * G / 256) + b,
     // which leaves each sequence at least as many slots as it has tiles.
     int lo = 0, hi = p.n_seqs - 1;
@@ -109,16 +120,29 @@ struct Piece {
     tok0 = div_small(row0, G);
     rem0 = static_cast<int>(row0 - tok0 * G);
     off = nk - nq;
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int64_t r0 = row0 + 128 * i;
-      n_tiles[i] = r0 >= R ? 0 : (sees(min(r0 + 127, R - 1), G) + kKeys - 1) / kKeys;
-    }
-    n_max = max(n_tiles[0], n_tiles[1]);
-    // the first key tile with positions that some row of the piece does not see
-    first_masked = sees(row0, G) / kKeys;
+    const int64_t r1 = row0 + 128;
+    const int all0 = (sees(min(r1 - 1, R - 1), G) + kKeys - 1) / kKeys;
+    const int all1 = r1 >= R ? 0 : (sees(min(r1 + 127, R - 1), G) + kKeys - 1) / kKeys;
+    const int tiles = max(all0, all1);
+    t0 = static_cast<int>(static_cast<int64_t>(tiles) * part / a.parts);
+    const int t1 = static_cast<int>(static_cast<int64_t>(tiles) * (part + 1) / a.parts);
+    n[0] = max(0, min(t1, all0) - t0);
+    n[1] = max(0, min(t1, all1) - t0);
+    n_max = max(n[0], n[1]);
+    first_masked = max(0, sees(row0, G) / kKeys - t0);
     return true;
   }
+};
+static_assert(sizeof(Piece) * kItems <= 512, "room for the pieces");
+
+template <int D>
+struct Smem {
+  static constexpr int kTile = D / 64 * kChunk;  // 128 rows
+  static constexpr int kQ = 0, kK = 2 * kTile, kV = 4 * kTile, kBars = 6 * kTile;
+  static constexpr int kInts = kBars + 320;
+  static constexpr int kPieces = kInts + 64;  // Piece[kItems]
+  static constexpr int kBad = kPieces + 512;  // int[2][kNotes][3][D]
+  static constexpr int kBytes = kBad + 2 * kNotes * 3 * D * 4 + 1024;  // + alignment
 };
 
 template <int D, bool BF16>
@@ -133,13 +157,14 @@ prompt_kernel(const PromptArgs a, const __grid_constant__ CUtensorMap kmap, cons
   volatile int* s_int = reinterpret_cast<volatile int*>(smem + S::kInts);
   volatile int* s_abort = s_int;
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(smem + S::kInts) + 1;
-  volatile int* s_items = s_int + 2;            // [kItems]
-  volatile int* s_anybad = s_int + 2 + kItems;  // [2][kNotes]
+  volatile int* s_anybad = s_int + 2;  // [2][kNotes]
+  Piece* s_pieces = reinterpret_cast<Piece*>(smem + S::kPieces);
   int* s_bad = reinterpret_cast<int*>(smem + S::kBad);
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const unsigned full = 0xffffffffu;
   const int G = a.G;
+  allow_next_kernel();
 
   if (tid == 0) {
     for (int i = 0; i < 2; ++i) {
@@ -191,19 +216,17 @@ prompt_kernel(const PromptArgs a, const __grid_constant__ CUtensorMap kmap, cons
   auto used = [](int n, int k) { return static_cast<uint32_t>((n / k) & 1); };
   auto freed = [](int n, int k) { return static_cast<uint32_t>(((n / k) - 1) & 1); };
 
-  // The next piece, for the warps that are told (a whole warp calls it); -1: no
-  // more, or a wait ran out.
+  // The next piece, for the warps that are told (a whole warp calls it); false:
+  // no more, or a wait ran out.
   int n_item = 0;
   auto next_piece = [&](Piece& pc) -> bool {
     const int st = n_item % kItems;
     if (!wait_all(kBIf + st, used(n_item, kItems))) return false;
-    const int id = s_items[st];
+    pc = s_pieces[st];
     __syncwarp();
     if (lane == 0) mbar_arrive(&bars[kBIe + st]);
     ++n_item;
-    if (id < 0) return false;
-    pc.decode(a, id);
-    return true;
+    return pc.id >= 0;
   };
 
   Piece pc;
@@ -212,33 +235,34 @@ prompt_kernel(const PromptArgs a, const __grid_constant__ CUtensorMap kmap, cons
     if (warp == 8) {
       // ---- pieces; K and V tiles
       int* counters = reinterpret_cast<int*>(p.ws) + 1;  // next piece, blocks that are done
-      const int total = a.n_slots * p.kv_heads;
+      const int total = a.n_slots * p.kv_heads * a.parts;
       const bool leader = elect_one();
+      // the first piece is the block's number, the others come from the counter
       auto take = [&]() {
         int id = 0;
-        if (lane == 0) id = atomicAdd(counters, 1);
+        if (lane == 0) id = static_cast<int>(gridDim.x) + atomicAdd(counters, 1);
         return __shfl_sync(full, id, 0);
       };
-      int jt = 0;
-      bool ok = true;
-      int ahead = take();
-      while (ok) {
-        const int id = ahead;
-        const bool more = id < total;
-        if (more) {
-          ahead = take();
-          if (!pc.decode(a, id)) continue;
+      int jt = 0, id = blockIdx.x;
+      bool ok = true, more = true;
+      while (ok && more) {
+        more = id < total;
+        if (more && !pc.decode(a, id)) {
+          id = take();
+          continue;
         }
         const int st = n_item % kItems;
         if (n_item >= kItems) ok = wait_all(kBIe + st, freed(n_item, kItems));
         if (!ok) break;
         if (lane == 0) {
-          s_items[st] = more ? id : -1;
+          if (more) s_pieces[st] = pc;
+          else s_pieces[st].id = -1;
           mbar_arrive(&bars[kBIf + st]);
         }
         __syncwarp();
         ++n_item;
         if (!more) break;
+        const int ahead = take();
         for (int j = 0; ok && j < pc.n_max; ++j, ++jt) {
           const int ks = jt & 1;
           auto load = [&](const CUtensorMap* map, int fullb, int empty, int base) -> bool {
@@ -248,7 +272,7 @@ prompt_kernel(const PromptArgs a, const __grid_constant__ CUtensorMap kmap, cons
 #pragma unroll
               for (int c = 0; c < D / 64; ++c)
                 tma_load_3d(smem + base + ks * S::kTile + c * kChunk, map, 64 * c, pc.head,
-                            static_cast<int>(pc.k0) + j * kKeys, &bars[fullb + ks]);
+                            static_cast<int>(pc.k0) + (pc.t0 + j) * kKeys, &bars[fullb + ks]);
             }
             __syncwarp();
             return true;
@@ -261,6 +285,7 @@ prompt_kernel(const PromptArgs a, const __grid_constant__ CUtensorMap kmap, cons
             break;
           }
         }
+        id = ahead;
       }
       // copies in flight (after an abort) must land before the block ends
       for (int n = max(0, jt - 2); n < jt; ++n) {
@@ -291,7 +316,7 @@ prompt_kernel(const PromptArgs a, const __grid_constant__ CUtensorMap kmap, cons
             mma_ss(tbase + 128 * i, da + o, db + o, id_qk, k > 0, leader);
           }
           mma_commit(&bars[kBS + i], leader);
-          if (j + 1 == pc.n_tiles[i]) mma_commit(&bars[kBQe + i], leader);
+          if (j + 1 == pc.n[i]) mma_commit(&bars[kBQe + i], leader);
         };
         auto pv = [&](int i, int j) {
           const uint64_t db = sw128_desc(sv + ((jt + j) & 1) * S::kTile, kChunk, 1024);
@@ -303,7 +328,7 @@ prompt_kernel(const PromptArgs a, const __grid_constant__ CUtensorMap kmap, cons
           ok = wait_all(kBKf + (jt & 1), used(jt, 2));
 #pragma unroll
           for (int i = 0; i < 2; ++i)
-            if (ok && pc.n_tiles[i] > 0) {
+            if (ok && pc.n[i] > 0) {
               ok = wait_all(kBQ + i, n_qi[i] & 1);
               ++n_qi[i];
               tcgen_after_sync();
@@ -317,14 +342,14 @@ prompt_kernel(const PromptArgs a, const __grid_constant__ CUtensorMap kmap, cons
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
             if (!ok) break;
-            if (j >= pc.n_tiles[i]) continue;
+            if (j >= pc.n[i]) continue;
             if (!have_v) ok = wait_all(kBFix + (x & 1), used(x, 2));
             have_v = true;
             if (ok) ok = wait_all(kBP + i, (n_s[i] + j) & 1);
             if (!ok) break;
             tcgen_after_sync();
             pv(i, j);
-            if (j + 1 < pc.n_tiles[i]) {
+            if (j + 1 < pc.n[i]) {
               if (!have_k) ok = wait_all(kBKf + ((x + 1) & 1), used(x + 1, 2));
               have_k = true;
               if (ok) qk(i, j + 1);
@@ -338,8 +363,8 @@ prompt_kernel(const PromptArgs a, const __grid_constant__ CUtensorMap kmap, cons
           }
         }
         jt += pc.n_max;
-        n_s[0] += pc.n_tiles[0];
-        n_s[1] += pc.n_tiles[1];
+        n_s[0] += pc.n[0];
+        n_s[1] += pc.n[1];
       }
       if (!ok) {  // MMAs in flight: let them finish before tensor memory is freed
         mma_commit(&bars[kBDone], leader);
@@ -359,7 +384,7 @@ prompt_kernel(const PromptArgs a, const __grid_constant__ CUtensorMap kmap, cons
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           if (!ok) break;
-          if (pc.n_tiles[i] == 0) continue;
+          if (pc.n[i] == 0) continue;
           if (n_qi[i] > 0) ok = wait_all(kBQe + i, (n_qi[i] - 1) & 1);
           if (!ok) break;
           ++n_qi[i];
@@ -402,7 +427,7 @@ prompt_kernel(const PromptArgs a, const __grid_constant__ CUtensorMap kmap, cons
           if (!ok) break;
           if (j >= pc.first_masked) {
             uint8_t* v = smem + S::kV + (jt & 1) * S::kTile;
-            const int live = min(kKeys, pc.nk - j * kKeys);  // positions of the tile inside the sequence
+            const int live = min(kKeys, pc.nk - (pc.t0 + j) * kKeys);  // positions of the tile inside the sequence
             constexpr uint32_t kExp = BF16 ? 0x7F807F80u : 0x7C007C00u, kOne = BF16 ? 0x00800080u : 0x04000400u;
             bool wrote = false;
 #pragma unroll 4
@@ -424,7 +449,7 @@ prompt_kernel(const PromptArgs a, const __grid_constant__ CUtensorMap kmap, cons
                   const uint16_t x = h[e];
                   if ((x & (kExp & 0xffffu)) != (kExp & 0xffffu)) continue;
                   const int kind = (x & 0x7fff & ~(kExp & 0xffffu)) ? 0 : x >> 15 ? 2 : 1;
-                  atomicMin(&notes[kind * D + d0 + e], j * kKeys + r);
+                  atomicMin(&notes[kind * D + d0 + e], (pc.t0 + j) * kKeys + r);
                   s_anybad[(warp - 10) * kNotes + note] = 1;
                   h[e] = 0;
                 }
@@ -448,10 +473,11 @@ prompt_kernel(const PromptArgs a, const __grid_constant__ CUtensorMap kmap, cons
     int n_s = 0, n_o = 0;  // scores and results so far
     bool ok = true;
     while (ok && next_piece(pc)) {
-      const int note = (n_item - 1) % kNotes;
+      const int note = (n_item - 1) % kNotes, part_id = pc.id;
       const int64_t row = pc.row0 + 128 * i + wt;
       const bool store = row < pc.R;
-      const int n = i == 0 ? pc.n_tiles[0] : pc.n_tiles[1];
+      const int n = i == 0 ? pc.n[0] : pc.n[1], t0 = pc.t0;
+      float* part = a.parts > 1 ? part_slot(p, pc.id, D) + (128 * i + wt) * static_cast<int64_t>(D) : nullptr;
       const int my_sees = pc.sees(min(row, pc.R - 1), G);
       const int all_see = pc.sees(pc.row0 + 128 * i, G);  // what every row of the tile sees
       T* out;
@@ -472,8 +498,8 @@ prompt_kernel(const PromptArgs a, const __grid_constant__ CUtensorMap kmap, cons
         for (int c = 0; c < 4; ++c) tmem_ld32(t_s + 32 * c, s + 32 * c);
 #pragma unroll
         for (int c = 0; c < 4; ++c) tmem_wait_ld32(s + 32 * c);
-        if ((j + 1) * kKeys > all_see) {
-          const int lim = my_sees - j * kKeys;
+        if ((t0 + j + 1) * kKeys > all_see) {
+          const int lim = my_sees - (t0 + j) * kKeys;
 #pragma unroll
           for (int c = 0; c < 128; ++c)
             if (c >= lim) s[c] = 0xff800000u;  // -inf
@@ -546,7 +572,7 @@ prompt_kernel(const PromptArgs a, const __grid_constant__ CUtensorMap kmap, cons
       const int* bad1 = s_bad + (kNotes + note) * 3 * D;
       const bool use0 = s_anybad[note] != 0, use1 = s_anybad[kNotes + note] != 0;
       {
-        const float inv = l == 0.f ? 0.f : 1.f / l;
+        const float inv = part ? 1.f : l == 0.f ? 0.f : 1.f / l;
 #pragma unroll 1
         for (int c = 0; c < D; c += 32) {
           uint32_t o[32];
@@ -566,7 +592,11 @@ prompt_kernel(const PromptArgs a, const __grid_constant__ CUtensorMap kmap, cons
               else if (down) o[e] = 0xff800000u;
             }
           }
-          if (store) {
+          if (store && part) {
+#pragma unroll
+            for (int e = 0; e < 32; e += 4)
+              *reinterpret_cast<uint4*>(part + c + e) = make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+          } else if (store) {
 #pragma unroll
             for (int e = 0; e < 32; e += 8) {
               uint4 w;
@@ -578,7 +608,10 @@ prompt_kernel(const PromptArgs a, const __grid_constant__ CUtensorMap kmap, cons
             }
           }
         }
-        if (store && lse) *lse = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+        if (store && part)
+          *reinterpret_cast<float2*>(part_slot(p, part_id, D) + kRowsPerBlock * D + 2 * (128 * i + wt)) = make_float2(m, l);
+        else if (store && lse)
+          *lse = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
         tcgen_before_sync();
       }
       mbar_arrive(&bars[kBNe + note]);
@@ -586,6 +619,64 @@ prompt_kernel(const PromptArgs a, const __grid_constant__ CUtensorMap kmap, cons
   }
   __syncthreads();
   if (warp == 9) tmem_free_all(tbase);
+}
+
+// Adds the parts of a row: a warp for each.
+template <int D, bool BF16>
+__global__ void __launch_bounds__(128) prompt_join_kernel(const PromptArgs a) {
+  using T = typename std::conditional<BF16, __nv_bfloat16, __half>::type;
+  const PromptParams& p = a.p;
+  const int lane = threadIdx.x & 31;
+  const int64_t row = (static_cast<int64_t>(blockIdx.x) * 128 + threadIdx.x) >> 5;
+  const int64_t token = div_small(row, p.q_heads);
+  const int qh = static_cast<int>(row - token * p.q_heads), head = qh / a.G;
+  int lo = 0, hi = p.n_seqs;  // the sequence: the first with cu[seq + 1] > token
+  while (token < p.n_q && lo < hi) {
+    const int mid = (lo + hi) >> 1;
+    if (__ldg(p.cu_q + mid + 1) <= token) lo = mid + 1;
+    else hi = mid;
+  }
+  const bool on = token < p.n_q && lo < p.n_seqs && __ldg(p.cu_q + lo) <= token;
+  wait_for_last_kernel();  // every thread: what follows on the stream may rely on both kernels
+  if (!on) return;
+  const int64_t q0 = max(__ldg(p.cu_q + lo), 0);
+  const int64_t r = (token - q0) * a.G + qh - head * a.G;
+  const int64_t slot = q0 * a.G / kRowsPerBlock + lo + r / kRowsPerBlock;
+  const int rr = static_cast<int>(r % kRowsPerBlock);
+  const int first = static_cast<int>(((a.n_slots - 1 - slot) * p.kv_heads + head) * a.parts);
+  float m = -INFINITY, l = 0.f, ml[kMaxParts], ll[kMaxParts];
+#pragma unroll
+  for (int k = 0; k < kMaxParts; ++k) {
+    ml[k] = -INFINITY, ll[k] = 0.f;
+    if (k < a.parts) {
+      const float2 v = *reinterpret_cast<const float2*>(part_slot(p, first + k, D) + kRowsPerBlock * D + 2 * rr);
+      ml[k] = v.x, ll[k] = v.y;
+    }
+  }
+#pragma unroll
+  for (int k = 0; k < kMaxParts; ++k) m = fmaxf(m, ml[k]);
+  const float ref = m == -INFINITY ? 0.f : m;
+  float acc[D / 32];
+#pragma unroll
+  for (int c = 0; c < D / 32; ++c) acc[c] = 0.f;
+#pragma unroll
+  for (int k = 0; k < kMaxParts; ++k) {
+    if (k >= a.parts) break;
+    const float f = ml[k] == -INFINITY ? 0.f : ex2(ml[k] - ref);
+    l += ll[k] * f;
+    const float* src = part_slot(p, first + k, D) + rr * D + lane * (D / 32);
+    float x[D / 32];
+    if constexpr (D == 128) *reinterpret_cast<float4*>(x) = *reinterpret_cast<const float4*>(src);
+    else *reinterpret_cast<float2*>(x) = *reinterpret_cast<const float2*>(src);
+#pragma unroll
+    for (int c = 0; c < D / 32; ++c) acc[c] += x[c] * f;
+  }
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+  T* out = static_cast<T*>(p.out.ptr) + token * p.out.token_stride + qh * p.out.head_stride + lane * (D / 32);
+#pragma unroll
+  for (int c = 0; c < D / 32; c += 2)
+    *reinterpret_cast<uint32_t*>(out + c) = cvt_pair<BF16>(acc[c] * inv, acc[c + 1] * inv);
+  if (p.lse && lane == 0) p.lse[row] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
 }
 
 using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
@@ -641,11 +732,30 @@ cudaError_t launch(const PromptParams& p, cudaStream_t s) {
     return n;
   }();
   const int64_t pieces = static_cast<int64_t>(a.n_slots) * p.kv_heads;
-  prompt_kernel<D, BF16><<<static_cast<unsigned>(pieces < sms ? pieces : sms), kThreads, Smem<D>::kBytes, s>>>(a, km, vm);
-  return cudaGetLastError();
+  a.parts = 1;
+  {
+    // Parts: the number that makes the busiest block's share of the keys least.
+    // A part costs about kPartTiles key tiles more (its start and end, the join).
+    // The lengths are known as averages only; any choice is right.
+    const double kPartTiles = 6;
+    const double busy = std::ceil(static_cast<double>(p.n_q) * a.G / kRowsPerBlock / p.n_seqs) * p.n_seqs * p.kv_heads;
+    const double tiles = static_cast<double>(p.n_k) / p.n_seqs / kKeys;
+    double best = 0;
+    for (int n = 1; n <= kMaxParts && pieces * n <= kPartSlots; ++n) {
+      const double cost = std::ceil(busy * n / sms) * (tiles / n + (n > 1 ? kPartTiles : 0));
+      if (n == 1 || cost < best) best = cost, a.parts = n;
+    }
+  }
+  const int64_t total = pieces * a.parts;
+  prompt_kernel<D, BF16><<<static_cast<unsigned>(total < sms ? total : sms), kThreads, Smem<D>::kBytes, s>>>(a, km, vm);
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess || a.parts == 1) return e;
+  return launch_after(prompt_join_kernel<D, BF16>, static_cast<unsigned>((p.n_q * p.q_heads + 3) / 4), a, s);
 }
 
 }  // namespace
+
+int64_t prompt_ws_bytes(int head_dim) { return kPartSlots * part_floats(head_dim) * static_cast<int64_t>(sizeof(float)); }
 
 cudaError_t launch_attn_prompt(const PromptParams& p, cudaStream_t s) {
   if (p.dtype == QGEMV_DT_F16) return p.head_dim == 64 ? launch<64, false>(p, s) : launch<128, false>(p, s);

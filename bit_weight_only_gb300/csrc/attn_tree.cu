@@ -738,22 +738,14 @@ cudaError_t launch(const TreeArgs& a, cudaStream_t s) {
 template <int ROWS, int UNIT>
 cudaError_t launch_join(const TreeArgs& a, cudaStream_t s) {
   const int64_t rows = a.p.n_q * a.p.q_heads;
-  cudaLaunchAttribute attr;
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>((rows + 3) / 4));
-  cfg.blockDim = dim3(128);
-  cfg.stream = s;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  return a.p.cache.head_dim == 64 ? cudaLaunchKernelEx(&cfg, tree_join_kernel<ROWS, UNIT, 64>, a)
-                                  : cudaLaunchKernelEx(&cfg, tree_join_kernel<ROWS, UNIT, 128>, a);
+  const unsigned grid = static_cast<unsigned>((rows + 3) / 4);
+  return a.p.cache.head_dim == 64 ? launch_after(tree_join_kernel<ROWS, UNIT, 64>, grid, a, s)
+                                  : launch_after(tree_join_kernel<ROWS, UNIT, 128>, grid, a, s);
 }
 
 }  // namespace
 
-int64_t tree_ws_bytes(int64_t, int, int head_dim) {
+int64_t tree_ws_bytes(int head_dim) {
   return 2 * kMaxBlocks * slot_floats(head_dim) * static_cast<int64_t>(sizeof(float));
 }
 

@@ -252,4 +252,24 @@ __device__ __forceinline__ uint32_t q4_pair(uint32_t w) {
   return hsub2((v & 0x000F000Fu) | 0x64006400u, 0x64086408u);                          // 1024 + q - 1032
 }
 
+// A join kernel may be launched before the main one has ended
+// (programmatic dependent launch): the main kernels allow it at their start,
+// the join waits for their end before it reads what they wrote.
+__device__ __forceinline__ void allow_next_kernel() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void wait_for_last_kernel() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+template <typename A>
+cudaError_t launch_after(void (*kernel)(const A), unsigned grid, const A& a, cudaStream_t s) {
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(128);
+  cfg.stream = s;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, a);
+}
+
 }  // namespace qgemv

@@ -147,12 +147,6 @@ __device__ __forceinline__ float* tree_slot(const TreeParams& p, int block, bool
   return reinterpret_cast<float*>(p.ws + kWsHeaderBytes) + (2 * block + (begins ? 1 : 0)) * slot_floats(D);
 }
 
-// The join kernel may be launched before the main one has ended
-// (programmatic dependent launch): the main kernels allow it at their start,
-// the join waits for their end before it reads what they wrote.
-__device__ __forceinline__ void allow_next_kernel() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
-__device__ __forceinline__ void wait_for_last_kernel() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-
 cudaError_t launch_tree_wide(const TreeArgs& a, cudaStream_t s);
 
 }  // namespace qgemv

@@ -91,6 +91,26 @@ def test_matches_the_definition(kind, hq, hkv, d, nq, nk):
     c.check(f"{kind} {nq} {nk}", out, lse)
 
 
+@pytest.mark.parametrize("kind", list(KINDS))
+@pytest.mark.parametrize("hq, hkv, d, nq, nk", [
+    (4, 2, 128, [40, 7], [5000, 3333]),              # few rows, many keys: cut along the keys
+    (1, 1, 64, [2500], None),
+    (5, 1, 128, [300, 2, 30], [4100, 1, 9000]),      # parts that have no keys
+    (2, 1, 128, [1300, 900], [1300, 0]),
+])
+def test_few_rows_many_keys(kind, hq, hkv, d, nq, nk):
+    c = Case(kind, hq, hkv, d, nq, nk)
+    out, lse = c.run()
+    c.check(f"{kind} {nq} {nk}", out, lse)
+    again, lse2 = c.run()
+    assert torch.equal(out, again) and torch.equal(lse, lse2)
+    # an infinite value among many keys, seen by the rows from its position on
+    c.v[c.nk[0] - 3, 0, 5] = float("inf")
+    out, _ = c.run()
+    got = torch.isinf(out[:c.nq[0], 0, 5]).cpu()
+    assert torch.equal(got, torch.arange(c.nq[0]) >= c.nq[0] - 3)
+
+
 def test_rows_that_see_nothing():
     c = Case("float16", 4, 2, 64, [40, 300], [17, 0])
     out, lse = c.run()
