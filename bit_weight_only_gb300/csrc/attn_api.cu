@@ -190,6 +190,8 @@ int qgemv_attn_prompt(int dtype, int head_dim, int q_heads, int kv_heads, const 
   if (n_k > 0) {
     QG_TRY(check_rows("k", k, k_token_stride, k_head_stride, 2, kv_heads, head_dim, false));
     QG_TRY(check_rows("v", v, v_token_stride, v_head_stride, 2, kv_heads, head_dim, false));
+    if ((n_k > 1 && (k_token_stride == 0 || v_token_stride == 0)) || (kv_heads > 1 && (k_head_stride == 0 || v_head_stride == 0)))
+      return fail(QGEMV_ERR_ARG, "k and v of a prompt have no strides of zero");
   }
   QG_TRY(check_rows("out", out, out_token_stride, out_head_stride, 2, q_heads, head_dim, true));
   QG_TRY(check_ws(ws, ws_bytes, n_seqs, q_heads, head_dim));

@@ -27,6 +27,7 @@ namespace qgemv {
 namespace {
 
 constexpr int kNarrowRows = 32;  // more rows than this go to the wide kernel
+constexpr int64_t kWholeTokens = 1024;
 constexpr int kErrTree = 32;
 constexpr float kLazyT = 8.f;
 constexpr int kRingBytes = 200 * 1024;
@@ -194,7 +195,6 @@ __global__ void __launch_bounds__(TreeShape<FMT, D, MT>::kThreads, 1) tree_kerne
   fence_mbarrier_init();
   __syncwarp();
   int n_done = 0;  // units that this warp's ring has taken
-  bool dead = false;
 
   Segment sg;
   while (work.next(a, sg)) {
@@ -273,12 +273,15 @@ __global__ void __launch_bounds__(TreeShape<FMT, D, MT>::kThreads, 1) tree_kerne
 
     for (int k = 0; k < n_mine; ++k) {
       const int st = (n_done + k) % NS;
-      if (!dead && !mbar_wait_bounded(&my_bars[st], ((n_done + k) / NS) & 1)) {
+      const bool landed = mbar_wait_bounded(&my_bars[st], ((n_done + k) / NS) & 1);
+      if (!__all_sync(full, landed)) {
+        // Give up: record it, and let the copies in flight land (or their waits
+        // run out too) before the ring is used for anything else.
         if (lane == 0) atomicOr(reinterpret_cast<int*>(p.ws), kErrTree);
-        dead = true;
+        for (int x = k; x < n_mine && x < k + NS; ++x) mbar_wait_bounded(&my_bars[(n_done + x) % NS], ((n_done + x) / NS) & 1);
+        break;
       }
-      dead = __any_sync(full, dead);
-      if (!dead && ((have >> st) & 1)) {
+      if ((have >> st) & 1) {
         const uint8_t* blk = my_ring + st * L::kBlock;
         const int64_t pos0 = (u0 + warp + static_cast<int64_t>(W) * k) * kKvBlockTokens;
         const bool edge = pos0 + kKvBlockTokens > ctx;  // some positions are drafted, or past the end
@@ -530,11 +533,8 @@ __global__ void __launch_bounds__(TreeShape<FMT, D, MT>::kThreads, 1) tree_kerne
         }
       }
       __syncwarp();
-      if (!dead && k + NS < n_mine) prefetch(k + NS);
+      if (k + NS < n_mine) prefetch(k + NS);
     }
-    // Copies of a warp that gave up must land before its ring is used again.
-    if (dead)
-      for (int s = 0; s < NS; ++s) __nanosleep(1000);
     n_done += n_mine;
 
     // ---- the warps' results, in warp order
@@ -768,11 +768,14 @@ cudaError_t launch_attn_tree(const TreeParams& p, cudaStream_t s) {
   // INT8: 8 rows 87 us against 177, 32 rows 133 against 161), beyond it needs
   // several tiles and passes over the cache, and the wide kernel is (16
   // sequences of up to 16000 tokens, INT8, 64 rows: 96 us against 188).
+  // Contexts of up to kWholeTokens positions (as the caller bounds them) are
+  // not split: a second kernel would take longer than the split saves.
+  a.whole = p.max_ctx + p.max_new <= kWholeTokens;
   if (rows > kNarrowRows) {
     a.extra = 4;  // a row tile's start and end: about four units of 128 tokens
     a.min_units = 2 + a.extra;
     const cudaError_t e = launch_tree_wide(a, s);
-    return e != cudaSuccess ? e : launch_join<64, 128>(a, s);
+    return e != cudaSuccess || a.whole ? e : launch_join<64, 128>(a, s);
   }
   a.extra = 48;  // about 48 units of 16 tokens (64 ragged INT8 sequences: 148 us at 0, 84 at 32, 68 at 48 and 64)
   a.min_units = 16 + a.extra;
@@ -780,10 +783,10 @@ cudaError_t launch_attn_tree(const TreeParams& p, cudaStream_t s) {
     constexpr int F = decltype(fmt)::value, D = decltype(d)::value;
     if (rows > 16) {
       const cudaError_t e = launch<F, D, 2>(a, s);
-      return e != cudaSuccess ? e : launch_join<32, kKvBlockTokens>(a, s);
+      return e != cudaSuccess || a.whole ? e : launch_join<32, kKvBlockTokens>(a, s);
     }
     const cudaError_t e = launch<F, D, 1>(a, s);
-    return e != cudaSuccess ? e : launch_join<16, kKvBlockTokens>(a, s);
+    return e != cudaSuccess || a.whole ? e : launch_join<16, kKvBlockTokens>(a, s);
   };
   auto by_dim = [&](auto fmt) {
     return p.cache.head_dim == 64 ? by_rows(fmt, std::integral_constant<int, 64>())

@@ -20,9 +20,11 @@ constexpr int kMaxBlocks = 256;  // thread blocks of a call, at most
 constexpr int kSlotRows = 64;    // rows of a workspace slot, at most
 __host__ __device__ constexpr int64_t slot_floats(int D) { return static_cast<int64_t>(kSlotRows) * (D + 2); }
 
+// `whole`: short contexts are not split; block b takes the row tiles b, b +
+// grid, .. of the list whole, and there is nothing to join.
 struct TreeArgs {
   TreeParams p;
-  int G, page_shift, min_units, extra, grid;
+  int G, page_shift, min_units, extra, grid, whole;
 };
 
 struct SeqWork {
@@ -76,7 +78,7 @@ struct Cursor {
     auto cost_of = [&](int b) -> int64_t {
       if (b >= a.p.n_seqs) return 0;
       const SeqWork s = seq_work<ROWS, UNIT>(a, b);
-      return (s.units + a.extra) * s.tiles * H;
+      return (a.whole ? 1 : s.units + a.extra) * s.tiles * H;
     };
     auto scan = [&](int64_t x) {  // inclusive
 #pragma unroll
@@ -91,9 +93,14 @@ struct Cursor {
     for (int b = 32 + lane; b < a.p.n_seqs; b += 32) rest += cost_of(b);
     int64_t total = __shfl_sync(full, sum0, 31);
     if (a.p.n_seqs > 32) total += warp_total(rest);
-    const int64_t quota = run_quota(a, total);
-    cur = quota * blockIdx.x;
-    end = min(cur + quota, total);
+    if (a.whole) {
+      cur = blockIdx.x;
+      end = total;
+    } else {
+      const int64_t quota = run_quota(a, total);
+      cur = quota * blockIdx.x;
+      end = min(cur + quota, total);
+    }
     seq = 0;
     base = 0;
     if (cur >= end) return;
@@ -118,18 +125,24 @@ struct Cursor {
     const int H = a.p.cache.kv_heads;
     while (cur < end) {
       const SeqWork w = seq_work<ROWS, UNIT>(a, seq);
-      const int64_t in_seq = cur - base, cost = w.units + a.extra, per_seq = cost * w.tiles * H;
+      const int64_t in_seq = cur - base, cost = a.whole ? 1 : w.units + a.extra, per_seq = cost * w.tiles * H;
       if (in_seq >= per_seq) {
         base += per_seq;
         ++seq;
         continue;
       }
       const int64_t item = div_small(in_seq, cost);
-      const int64_t v0 = in_seq - item * cost, v1 = min(cost, v0 + (end - cur));
-      cur += v1 - v0;
-      s.u0 = max(static_cast<int64_t>(0), v0 - a.extra);
-      s.u1 = v1 - a.extra;
-      if (s.u1 <= s.u0) continue;
+      if (a.whole) {
+        cur += a.grid;
+        s.u0 = 0;
+        s.u1 = w.units;
+      } else {
+        const int64_t v0 = in_seq - item * cost, v1 = min(cost, v0 + (end - cur));
+        cur += v1 - v0;
+        s.u0 = max(static_cast<int64_t>(0), v0 - a.extra);
+        s.u1 = v1 - a.extra;
+        if (s.u1 <= s.u0) continue;
+      }
       s.seq = seq;
       s.ctx = w.ctx;
       s.T = w.T;

@@ -311,8 +311,8 @@ def _current(stream):
     stream)."""
     if stream is not None:
         return stream
-    import torch
-    return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+    c = _torch()._C
+    return c._cuda_getCurrentRawStream(c._cuda_getDevice())
 
 
 class QGemv:
@@ -447,7 +447,30 @@ def prepare_x_int8(x, hadamard_block: int = 0, signs=None, stream=None):
 
 # --------------------------------------------------- cache and attention --
 
+# These calls run once a layer and token, so the host's time counts: what can be
+# looked up once is (an import statement or an attribute chain each cost as much
+# as a check).
+_TORCH = None
 _DTYPES = None  # torch dtype -> DT_*, filled on first use (torch is imported only where it is used)
+
+
+def _torch():
+    global _TORCH
+    if _TORCH is None:
+        import torch
+        _TORCH = torch
+    return _TORCH
+
+
+def _on(stream):
+    """The address of the stream given, or of torch's current one."""
+    return _current(None) if stream is None else _stream_ptr(stream)
+
+
+def _call(fn, *args):
+    rc = fn(*args)
+    if rc:
+        _check(rc)
 
 
 def _dtype_code(dtype) -> int:
@@ -521,36 +544,40 @@ class KVCache:
                                             f"{kv_heads} heads of {head_dim}")
         self.pages = torch.empty(nbytes, dtype=torch.uint8, device=device)
         self.desc = KvCacheDesc(self.pages.data_ptr(), self.fmt, head_dim, kv_heads, page_tokens, n_pages)
+        self._ref, self.device = ctypes.byref(self.desc), self.pages.device
 
     def write(self, k, v, slots, stream=None):
         """Quantise the rows k and v [n, kv_heads, head_dim] (fp32, fp16 or
         bf16, any token and head strides) into slots (int64 [n]; a slot is
         page * page_tokens + place, negative ones are skipped)."""
-        import torch
         if k.dtype != v.dtype or k.shape[0] != v.shape[0]:
             raise ValueError("k and v must have the same type and number of tokens")
         n = k.shape[0]
-        s = _index("slots", slots, torch.int64, (n,))
-        qgemv_kv_write(self.desc, _dtype_code(k.dtype), *_rows("k", k, self.kv_heads, self.head_dim),
-                       *_rows("v", v, self.kv_heads, self.head_dim), s, n, _current(stream))
+        s = _index("slots", slots, _torch().int64, (n,))
+        _call(_lib.qgemv_kv_write, self._ref, _dtype_code(k.dtype), *_rows("k", k, self.kv_heads, self.head_dim),
+                       *_rows("v", v, self.kv_heads, self.head_dim), s, n, _on(stream))
 
     def read(self, table, starts, cu, n_tokens: int, dtype=None, out=None, stream=None):
         """The cached rows of positions starts[b] .. of each sequence, packed
         by cu (int32 [n_seqs + 1]): (k, v) [n_tokens, kv_heads, head_dim] of
         dtype (fp16 unless given).  table: int32 [n_seqs, most pages]."""
-        import torch
-        if out is None:
-            shape = (n_tokens, self.kv_heads, self.head_dim)
-            out = tuple(torch.empty(shape, dtype=dtype or torch.float16, device=self.pages.device) for _ in range(2))
-        k, v = out
-        if k.dtype != v.dtype or k.shape[0] != n_tokens or v.shape[0] != n_tokens:
-            raise ValueError(f"the outputs must have {n_tokens} tokens of one type")
+        torch = _torch()
         n_seqs, stride = table.shape
-        qgemv_kv_read(self.desc, _index("table", table, torch.int32, (n_seqs, stride)), stride, n_seqs,
-                      None if starts is None else _index("starts", starts, torch.int32, (n_seqs,)),
-                      _index("cu", cu, torch.int32, (n_seqs + 1,)), n_tokens, _dtype_code(k.dtype),
-                      *_rows("k", k, self.kv_heads, self.head_dim), *_rows("v", v, self.kv_heads, self.head_dim),
-                      _current(stream))
+        if out is None:
+            shape = n_tokens, self.kv_heads, self.head_dim
+            dtype = torch.float16 if dtype is None else dtype
+            out = (torch.empty(shape, dtype=dtype, device=self.device), torch.empty(shape, dtype=dtype, device=self.device))
+            row = self.kv_heads * self.head_dim, self.head_dim
+            rows = (out[0].data_ptr(), *row, out[1].data_ptr(), *row)
+        else:
+            k, v = out
+            if k.dtype != v.dtype or k.shape[0] != n_tokens or v.shape[0] != n_tokens:
+                raise ValueError(f"the outputs must have {n_tokens} tokens of one type")
+            dtype = k.dtype
+            rows = *_rows("k", k, self.kv_heads, self.head_dim), *_rows("v", v, self.kv_heads, self.head_dim)
+        _call(_lib.qgemv_kv_read, self._ref, _index("table", table, torch.int32, (n_seqs, stride)), stride, n_seqs,
+              None if starts is None else _index("starts", starts, torch.int32, (n_seqs,)),
+              _index("cu", cu, torch.int32, (n_seqs + 1,)), n_tokens, _dtype_code(dtype), *rows, _on(stream))
         return out
 
     def attend(self, q, table, ctx_lens, cu_q, masks=None, *, max_ctx: int, max_new: int, workspace, scale=None,
@@ -562,7 +589,7 @@ class KVCache:
         another.  Returns (out like q, lse fp32 [n, q_heads]).  scale is
         1 / sqrt(head_dim) unless given; max_ctx and max_new bound the
         lengths (they guide the split only)."""
-        import torch
+        torch = _torch()
         n, heads, d = q.shape
         if q.dtype != torch.float16:
             raise ValueError("q must be fp16")
@@ -582,11 +609,11 @@ class KVCache:
                 _index("masks", masks, torch.int64, (n,))
             masks = masks.data_ptr()
         n_seqs, stride = table.shape
-        qgemv_attn_tree(self.desc, _index("table", table, torch.int32, (n_seqs, stride)), stride, n_seqs,
-                        _index("ctx_lens", ctx_lens, torch.int32, (n_seqs,)), *_rows("q", q, heads, self.head_dim),
-                        heads, _index("cu_q", cu_q, torch.int32, (n_seqs + 1,)), n, masks, max_ctx, max_new,
-                        d ** -0.5 if scale is None else scale, *out_rows, lse.data_ptr(), workspace.ptr,
-                        workspace.nbytes, _current(stream))
+        _call(_lib.qgemv_attn_tree, self._ref, _index("table", table, torch.int32, (n_seqs, stride)), stride, n_seqs,
+              _index("ctx_lens", ctx_lens, torch.int32, (n_seqs,)), *_rows("q", q, heads, self.head_dim), heads,
+              _index("cu_q", cu_q, torch.int32, (n_seqs + 1,)), n, masks, max_ctx, max_new,
+              d ** -0.5 if scale is None else scale, *out_rows, lse.data_ptr(), workspace.ptr, workspace.nbytes,
+              _on(stream))
         return out, lse
 
 
@@ -595,7 +622,7 @@ def attn_prompt(q, k, v, cu_q, cu_k, *, max_q: int, workspace, scale=None, out=N
     [n_k, kv_heads, d] (all fp16 or all bf16), sequence b the rows cu_q[b] ..
     of q and cu_k[b] .. of k and v (int32 [n_seqs + 1]); its last query sees
     all of its keys.  Returns (out like q, lse fp32 [n_q, q_heads])."""
-    import torch
+    torch = _torch()
     n, heads, d = q.shape
     if k.shape[0] != v.shape[0] or not (q.dtype == k.dtype == v.dtype):
         raise ValueError("q, k and v must have one type, k and v the same number of tokens")
@@ -611,9 +638,9 @@ def attn_prompt(q, k, v, cu_q, cu_k, *, max_q: int, workspace, scale=None, out=N
     else:
         _index("lse", lse, torch.float32, (n, heads))
     n_seqs, kv_heads = cu_q.shape[0] - 1, k.shape[1]
-    qgemv_attn_prompt(_dtype_code(q.dtype), d, heads, kv_heads, *_rows("q", q, heads, d), *_rows("k", k, kv_heads, d),
-                      *_rows("v", v, kv_heads, d), n_seqs, _index("cu_q", cu_q, torch.int32, (n_seqs + 1,)),
-                      _index("cu_k", cu_k, torch.int32, (n_seqs + 1,)), n, k.shape[0], max_q,
-                      d ** -0.5 if scale is None else scale, *out_rows, lse.data_ptr(), workspace.ptr,
-                      workspace.nbytes, _current(stream))
+    _call(_lib.qgemv_attn_prompt, _dtype_code(q.dtype), d, heads, kv_heads, *_rows("q", q, heads, d),
+          *_rows("k", k, kv_heads, d), *_rows("v", v, kv_heads, d), n_seqs,
+          _index("cu_q", cu_q, torch.int32, (n_seqs + 1,)), _index("cu_k", cu_k, torch.int32, (n_seqs + 1,)), n,
+          k.shape[0], max_q, d ** -0.5 if scale is None else scale, *out_rows, lse.data_ptr(), workspace.ptr,
+          workspace.nbytes, _on(stream))
     return out, lse

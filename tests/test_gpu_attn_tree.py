@@ -231,6 +231,10 @@ def test_strides_hints_streams_and_bits():
         got, _ = c.run()
     s.synchronize()
     assert torch.equal(got, want)
+    for given in (s, s.cuda_stream):
+        got, _ = c.run(stream=given)
+        s.synchronize()
+        assert torch.equal(got, want)
 
 
 def test_in_a_graph_with_other_lengths():
@@ -285,3 +289,16 @@ def test_offsets_past_32_bits():
                             workspace=qgemv.AttnWorkspace(1, hkv, d))
     r = ref.attention(q.astype(np.float64), k.astype(np.float64), v.astype(np.float64), np.ones((1, 300), bool), d ** -0.5)
     ref.check("far pages", out.float().cpu().numpy(), lse.cpu().numpy(), r)
+
+
+def test_status_reports_a_wait_that_ran_out():
+    """The kernels record such a wait in the workspace's first word (here the test does); it is reported once."""
+    ws = qgemv.AttnWorkspace(2, 8, 128)
+    ws.status()
+    ws.buffer[:4].copy_(torch.tensor([32, 0, 0, 0], dtype=torch.uint8))
+    with pytest.raises(qgemv.QgemvError, match="bounded wait") as e:
+        ws.status()
+    assert e.value.code == qgemv.QGEMV_ERR_TIMEOUT
+    ws.status()
+    ws.reset()
+    ws.status()
