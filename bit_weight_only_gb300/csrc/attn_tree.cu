@@ -20,6 +20,8 @@
 //
 // A warp's O, m and l live in its registers.  At the end of a segment the
 // warps' results are added in warp order through shared memory.
+#include <algorithm>
+
 #include "tc_common.cuh"
 #include "tree_work.cuh"
 
@@ -30,7 +32,8 @@ constexpr int kNarrowRows = 32;  // more rows than this go to the wide kernel
 constexpr int64_t kWholeTokens = 1024;
 constexpr int kErrTree = 32;
 constexpr float kLazyT = 8.f;
-constexpr int kRingBytes = 200 * 1024;
+constexpr int kRingBytes = 100 * 1024;
+constexpr int kBlocksPerSm = 2;  // one's start and end of a row tile beside the other's stream
 
 // c += a . b: 16 x 16 . 16 x 8, fp16 in, fp32 sums.
 __device__ __forceinline__ void mma16816(float (&c)[4], const uint4& a, uint32_t b0, uint32_t b1) {
@@ -155,7 +158,7 @@ struct Codes<QGEMV_KV_Q4_0, D> {
 template <int FMT, int D, int MT>
 struct TreeShape {
   using L = KvLayout<FMT, D>;
-  static constexpr int kWarps = MT == 2 || FMT == QGEMV_KV_F16 || D == 64 ? 8 : 16;
+  static constexpr int kWarps = MT == 2 || FMT == QGEMV_KV_F16 ? 4 : 8;
   static constexpr int kThreads = 32 * kWarps;
   static constexpr int kRows = 16 * MT;
   static constexpr int kFitting = kRingBytes / (kWarps * L::kBlock);
@@ -171,7 +174,7 @@ struct TreeShape {
 };
 
 template <int FMT, int D, int MT>
-__global__ void __launch_bounds__(TreeShape<FMT, D, MT>::kThreads, 1) tree_kernel(const TreeArgs a) {
+__global__ void __launch_bounds__(TreeShape<FMT, D, MT>::kThreads, kBlocksPerSm) tree_kernel(const TreeArgs a) {
   using Sh = TreeShape<FMT, D, MT>;
   using L = KvLayout<FMT, D>;
   using C = Codes<FMT, D>;
@@ -727,7 +730,7 @@ __global__ void __launch_bounds__(128) tree_join_kernel(const TreeArgs a) {
 template <int FMT, int D, int MT>
 cudaError_t launch(const TreeArgs& a, cudaStream_t s) {
   using Sh = TreeShape<FMT, D, MT>;
-  static_assert(Sh::kStages >= 2 && Sh::kBytes <= 227 * 1024, "shared memory");
+  static_assert(Sh::kStages >= 2 && Sh::kBytes <= 113 * 1024, "shared memory of a block");
   static const cudaError_t attr =
       cudaFuncSetAttribute(tree_kernel<FMT, D, MT>, cudaFuncAttributeMaxDynamicSharedMemorySize, Sh::kBytes);
   if (attr != cudaSuccess) return attr;
@@ -764,10 +767,10 @@ cudaError_t launch_attn_tree(const TreeParams& p, cudaStream_t s) {
   while ((1 << a.page_shift) < p.cache.page_tokens) ++a.page_shift;
   a.grid = sms < kMaxBlocks ? sms : kMaxBlocks;
   const int64_t rows = static_cast<int64_t>(p.max_new) * a.G;
-  // Up to 32 rows this kernel is faster (two sequences of up to 131000 tokens,
-  // INT8: 8 rows 87 us against 177, 32 rows 133 against 161), beyond it needs
-  // several tiles and passes over the cache, and the wide kernel is (16
-  // sequences of up to 16000 tokens, INT8, 64 rows: 96 us against 188).
+  // Up to 32 rows this file's kernel is faster (two sequences of up to 131000
+  // tokens, INT8: 8 rows 89 us against 177, 32 rows 135 against 161); beyond,
+  // it would need several tiles and passes over the cache, and the wide one is
+  // (16 sequences of up to 16000 tokens, INT8, 64 rows: 96 us against 188).
   // Contexts of up to kWholeTokens positions (as the caller bounds them) are
   // not split: a second kernel would take longer than the split saves.
   a.whole = p.max_ctx + p.max_new <= kWholeTokens;
@@ -777,7 +780,11 @@ cudaError_t launch_attn_tree(const TreeParams& p, cudaStream_t s) {
     const cudaError_t e = launch_tree_wide(a, s);
     return e != cudaSuccess || a.whole ? e : launch_join<64, 128>(a, s);
   }
-  a.extra = 48;  // about 48 units of 16 tokens (64 ragged INT8 sequences: 148 us at 0, 84 at 32, 68 at 48 and 64)
+  // Two blocks per SM, so that one's starts and ends of row tiles run beside
+  // the other's stream: 64 ragged INT8 sequences 54 us against 68 with one of
+  // twice the warps (many row tiles); a few long sequences lose 2-4%.
+  a.grid = std::min(kBlocksPerSm * sms, kMaxBlocks);
+  a.extra = 32;  // a row tile's start and end: about 32 units of 16 tokens (those 64 sequences: 71 us at 16, 54 at 32)
   a.min_units = 16 + a.extra;
   auto by_rows = [&](auto fmt, auto d) {
     constexpr int F = decltype(fmt)::value, D = decltype(d)::value;

@@ -16,7 +16,7 @@
 
 namespace qgemv {
 
-constexpr int kMaxBlocks = 256;  // thread blocks of a call, at most
+constexpr int kMaxBlocks = 320;  // thread blocks of a call, at most
 constexpr int kSlotRows = 64;    // rows of a workspace slot, at most
 __host__ __device__ constexpr int64_t slot_floats(int D) { return static_cast<int64_t>(kSlotRows) * (D + 2); }
 
