@@ -181,7 +181,9 @@ int qgemv_attn_prompt(int dtype, int head_dim, int q_heads, int kv_heads, const 
   if (n_seqs < 0 || n_seqs > (1 << 20) || n_q < 0 || n_q > kMaxTokens || n_k < 0 || n_k > kMaxTokens || max_q < 0)
     return fail(QGEMV_ERR_ARG, "n_seqs outside [0, 2^20], or a token count outside [0, 2^30]");
   if (n_q == 0 || n_seqs == 0 || max_q == 0) return qgemv::report_error(QGEMV_OK, "");
-  if (n_q * (q_heads / 256.0) + static_cast<double>(n_seqs) * kv_heads > 2e9)
+  if (q_heads / kv_heads > 128)
+    return fail(QGEMV_ERR_ARG, "%d query heads of a key/value head: at most 128", q_heads / kv_heads);
+  if (n_q * (q_heads / 128.0) + static_cast<double>(n_seqs) * kv_heads > 2e9)
     return fail(QGEMV_ERR_ARG, "too many rows for one call: %lld tokens of %d heads", (long long)n_q, q_heads);
   if (!cu_q || !cu_k) return fail(QGEMV_ERR_ARG, "cu_q or cu_k is NULL");
   if ((reinterpret_cast<uintptr_t>(cu_q) | reinterpret_cast<uintptr_t>(cu_k) | reinterpret_cast<uintptr_t>(lse)) & 3)
@@ -190,8 +192,9 @@ int qgemv_attn_prompt(int dtype, int head_dim, int q_heads, int kv_heads, const 
   if (n_k > 0) {
     QG_TRY(check_rows("k", k, k_token_stride, k_head_stride, 2, kv_heads, head_dim, false));
     QG_TRY(check_rows("v", v, v_token_stride, v_head_stride, 2, kv_heads, head_dim, false));
-    if ((n_k > 1 && (k_token_stride == 0 || v_token_stride == 0)) || (kv_heads > 1 && (k_head_stride == 0 || v_head_stride == 0)))
-      return fail(QGEMV_ERR_ARG, "k and v of a prompt have no strides of zero");
+    if ((n_q > 1 && q_token_stride == 0) || (q_heads > 1 && q_head_stride == 0) ||
+        (n_k > 1 && (k_token_stride == 0 || v_token_stride == 0)) || (kv_heads > 1 && (k_head_stride == 0 || v_head_stride == 0)))
+      return fail(QGEMV_ERR_ARG, "q, k and v of a prompt have no strides of zero");
   }
   QG_TRY(check_rows("out", out, out_token_stride, out_head_stride, 2, q_heads, head_dim, true));
   QG_TRY(check_ws(ws, ws_bytes, n_seqs, q_heads, head_dim));

@@ -5,9 +5,9 @@
 //
 // Rows: the queries of a sequence and the G query heads of a key/value head,
 // row = token * G + head, so that short prompts fill tiles and every K and V
-// tile serves all of the heads that share it.  A block takes 256 rows (two
-// tiles of 128) of one key/value head and walks the keys in tiles of 128 up
-// to the last one that its rows see.
+// tile serves all of the heads that share it.  A piece is two row tiles of
+// floor(128 / G) tokens of one key/value head; a block walks the keys in tiles
+// of 128 up to the last one that the rows see.
 //
 // Where there are too few such pieces to fill the GPU, a piece is cut into parts
 // of its keys; their unnormalised results go to the workspace, and a second
@@ -17,10 +17,10 @@
 // pieces on their own, held together by mbarriers only, so that one piece's
 // start overlaps the end of the one before:
 //   0-7    two softmax warpgroups, one for each row tile, a thread for each row
-//   8      takes the pieces; issues the TMA loads of K and V (two stages each)
+//   8      takes the pieces; issues the TMA loads of Q (as soon as the last
+//          product with the one before is done), K and V (two stages each)
 //   9      the MMAs
-//   10-11  load Q into the operands' swizzle (as soon as the last product with
-//          the one before is done), and mend V tiles that hold masked positions
+//   10-11  mend V tiles that hold masked positions
 // Tensor memory, 512 columns: S0 S1 (128 each; P, 16-bit, replaces the first
 // half of S), O0 O1.
 //   * QK of row tile i for key tile j + 1 follows PV of tile j in issue order,
@@ -48,7 +48,7 @@ namespace qgemv {
 namespace {
 
 constexpr int kThreads = 384;  // 12 warps
-constexpr int kRowsPerBlock = 256;
+constexpr int kRowsPerBlock = 256;  // of a piece: two tiles of 128
 constexpr int kKeys = 128;         // keys of a tile
 constexpr int kChunk = 128 * 128;  // bytes of 128 rows of 64 values
 constexpr int kErrPrompt = 16;
@@ -69,7 +69,7 @@ __device__ __forceinline__ float* part_slot(const PromptParams& p, int id, int D
 
 struct PromptArgs {
   PromptParams p;
-  int G, n_slots, parts;
+  int G, tokens, n_slots, parts;  // tokens of a row tile
 };
 
 // Barriers: full / empty pairs of the rings.  kBVf: a V tile has landed; kBFix:
@@ -77,59 +77,54 @@ struct PromptArgs {
 enum { kBQ = 0, kBQe = 2, kBKf = 4, kBKe = 6, kBVf = 8, kBVe = 10, kBFix = 12, kBS = 14, kBP = 16, kBO = 18, kBNf = 20,
        kBNe = 23, kBIf = 26, kBIe = 30, kBDone = 34, kNBars = 35 };
 
-// A piece: 256 rows of a sequence and head, and the key tiles t0 .. of them
-// that this part takes.
+// A piece: two row tiles of a sequence and head, and the key tiles t0 .. of
+// them that this part takes.
 struct Piece {
-  int64_t q0, k0, R;   // first query and key, rows of the sequence (queries * G)
-  int64_t tok0, off;   // first token of the piece; query i sees keys j <= i + off
-  int64_t row0;
-  int nk, rem0, head;  // keys; head of the first row
-  int id;              // of the part; -1: no more
+  int64_t q0, k0;      // first query and key of the sequence
+  int tok0, nq;        // first token of the piece, tokens of the sequence
+  int off, nk;         // query i sees the keys j <= i + off; keys
+  int id, head;        // of the part (-1: no more); key/value head
   int t0, n[2], n_max; // key tiles: of each row tile, and the more of the two
   int first_masked;    // of those, the first with positions that some row of the piece does not see
-  int pad[2];
+  int mask_from;       // the first such position
 
-  // keys that a row sees: 0 .. sees - 1
-  __device__ int sees(int64_t row, int G) const {
-    const int64_t v = div_small(row, G) + off + 1;
-    return static_cast<int>(v < 0 ? 0 : v < nk ? v : nk);
-  }
+  // keys that a token sees: 0 .. sees - 1
+  __device__ int sees(int token) const { return max(0, min(nk, token + off + 1)); }
 
-  // False: a slot without rows.
+  // False: a slot without tokens.
   __device__ bool decode(const PromptArgs& a, int part_id) {
     const PromptParams& p = a.p;
-    const int G = a.G, part = part_id % a.parts, pid = part_id / a.parts;
+    const int part = part_id % a.parts, pid = part_id / a.parts, step = 2 * a.tokens;
     const int slot = a.n_slots - 1 - pid / p.kv_heads;
     id = part_id;
     head = pid % p.kv_heads;
-    // The sequence of this slot: its tiles start at slot floor(cu * G / 256) + b,
-    // which leaves each sequence at least as many slots as it has tiles.
+    // The sequence of this slot: its pieces start at slot floor(cu / step) + b,
+    // which leaves each sequence at least as many slots as it has pieces.
     int lo = 0, hi = p.n_seqs - 1;
     while (lo < hi) {
       const int mid = (lo + hi + 1) >> 1;
-      if (static_cast<int64_t>(__ldg(p.cu_q + mid)) * G / kRowsPerBlock + mid <= slot) lo = mid;
+      if (__ldg(p.cu_q + mid) / step + mid <= slot) lo = mid;
       else hi = mid - 1;
     }
     q0 = max(__ldg(p.cu_q + lo), 0);
-    const int64_t nq = min(static_cast<int64_t>(__ldg(p.cu_q + lo + 1)), p.n_q) - q0;
-    row0 = (slot - (q0 * G / kRowsPerBlock + lo)) * kRowsPerBlock;
-    if (row0 < 0 || nq <= 0 || row0 >= nq * G) return false;
+    nq = static_cast<int>(min(static_cast<int64_t>(__ldg(p.cu_q + lo + 1)), p.n_q) - q0);
+    const int64_t first = (slot - (q0 / step + lo)) * step;
+    if (first < 0 || first >= nq) return false;
+    tok0 = static_cast<int>(first);
     k0 = min(static_cast<int64_t>(max(__ldg(p.cu_k + lo), 0)), p.n_k);
     nk = static_cast<int>(max(static_cast<int64_t>(0), min(static_cast<int64_t>(__ldg(p.cu_k + lo + 1)), p.n_k) - k0));
-    R = nq * G;
-    tok0 = div_small(row0, G);
-    rem0 = static_cast<int>(row0 - tok0 * G);
     off = nk - nq;
-    const int64_t r1 = row0 + 128;
-    const int all0 = (sees(min(r1 - 1, R - 1), G) + kKeys - 1) / kKeys;
-    const int all1 = r1 >= R ? 0 : (sees(min(r1 + 127, R - 1), G) + kKeys - 1) / kKeys;
+    const int tok1 = tok0 + a.tokens;
+    const int all0 = (sees(min(tok1, nq) - 1) + kKeys - 1) / kKeys;
+    const int all1 = tok1 >= nq ? 0 : (sees(min(tok1 + a.tokens, nq) - 1) + kKeys - 1) / kKeys;
     const int tiles = max(all0, all1);
     t0 = static_cast<int>(static_cast<int64_t>(tiles) * part / a.parts);
     const int t1 = static_cast<int>(static_cast<int64_t>(tiles) * (part + 1) / a.parts);
     n[0] = max(0, min(t1, all0) - t0);
     n[1] = max(0, min(t1, all1) - t0);
     n_max = max(n[0], n[1]);
-    first_masked = max(0, sees(row0, G) / kKeys - t0);
+    mask_from = sees(tok0);
+    first_masked = max(0, mask_from / kKeys - t0);
     return true;
   }
 };
@@ -142,12 +137,15 @@ struct Smem {
   static constexpr int kInts = kBars + 320;
   static constexpr int kPieces = kInts + 64;  // Piece[kItems]
   static constexpr int kBad = kPieces + 512;  // int[2][kNotes][3][D]
-  static constexpr int kBytes = kBad + 2 * kNotes * 3 * D * 4 + 1024;  // + alignment
+  static constexpr int kStage = kBad + 2 * kNotes * 3 * D * 4;  // of the epilogue: 32 rows x 64 bytes for each of 8 warps
+  static constexpr int kBytes = kStage + 8 * 2048 + 1024;        // + alignment
+  static_assert(kBytes <= 227 * 1024, "shared memory");
 };
 
 template <int D, bool BF16>
 __global__ void __launch_bounds__(kThreads, 1)
-prompt_kernel(const PromptArgs a, const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap) {
+prompt_kernel(const PromptArgs a, const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
+              const __grid_constant__ CUtensorMap vmap) {
   using T = typename std::conditional<BF16, __nv_bfloat16, __half>::type;
   using S = Smem<D>;
   const PromptParams& p = a.p;
@@ -168,7 +166,7 @@ prompt_kernel(const PromptArgs a, const __grid_constant__ CUtensorMap kmap, cons
 
   if (tid == 0) {
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&bars[kBQ + i], 64);
+      mbar_init(&bars[kBQ + i], 1);
       mbar_init(&bars[kBQe + i], 1);
       mbar_init(&bars[kBKf + i], 1);
       mbar_init(&bars[kBKe + i], 1);
@@ -243,7 +241,7 @@ prompt_kernel(const PromptArgs a, const __grid_constant__ CUtensorMap kmap, cons
         if (lane == 0) id = static_cast<int>(gridDim.x) + atomicAdd(counters, 1);
         return __shfl_sync(full, id, 0);
       };
-      int jt = 0, id = blockIdx.x;
+      int jt = 0, id = blockIdx.x, n_qi[2] = {0, 0};
       bool ok = true, more = true;
       while (ok && more) {
         more = id < total;
@@ -279,8 +277,26 @@ prompt_kernel(const PromptArgs a, const __grid_constant__ CUtensorMap kmap, cons
           };
           ok = load(&kmap, kBKf, kBKe, S::kK);
           if (!ok) break;
-          ok = load(&vmap, kBVf, kBVe, S::kV);
-          if (!ok) {  // the K tile is on its way: it must land before the block ends
+          if (j == 0) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              if (pc.n[i] == 0) continue;
+              if (n_qi[i] > 0) ok = ok && wait_all(kBQe + i, (n_qi[i] - 1) & 1);
+              if (!ok) continue;
+              ++n_qi[i];
+              if (leader) {
+                // tokens past the sequence's end give rows that are not stored
+                mbar_arrive_expect_tx(&bars[kBQ + i], D / 64 * a.tokens * G * 128);
+#pragma unroll
+                for (int c = 0; c < D / 64; ++c)
+                  tma_load_3d(smem + S::kQ + i * S::kTile + c * kChunk, &qmap, 64 * c, pc.head * G,
+                              static_cast<int>(pc.q0) + pc.tok0 + i * a.tokens, &bars[kBQ + i]);
+              }
+              __syncwarp();
+            }
+          }
+          if (ok) ok = load(&vmap, kBVf, kBVe, S::kV);
+          if (!ok) {  // this K tile is on its way: it must land before the block ends
             mbar_wait_bounded(&bars[kBKf + ks], used(jt, 2));
             break;
           }
@@ -292,6 +308,8 @@ prompt_kernel(const PromptArgs a, const __grid_constant__ CUtensorMap kmap, cons
         mbar_wait_bounded(&bars[kBKf + (n & 1)], used(n, 2));
         mbar_wait_bounded(&bars[kBVf + (n & 1)], used(n, 2));
       }
+      for (int i = 0; i < 2; ++i)
+        if (n_qi[i] > 0) mbar_wait_bounded(&bars[kBQ + i], (n_qi[i] - 1) & 1);
       if (lane == 0) {  // the last block leaves the counters as it found them
         __threadfence();
         if (atomicAdd(counters + 1, 1) == static_cast<int>(gridDim.x) - 1) {
@@ -371,51 +389,12 @@ prompt_kernel(const PromptArgs a, const __grid_constant__ CUtensorMap kmap, cons
         mbar_wait_bounded(&bars[kBDone], 0);
       }
     } else {
-      // ---- Q tiles; V tiles with masked positions
+      // ---- V tiles with masked positions
       const int t = tid - 320;
-      const uint32_t flip = p.scale < 0.f ? 0x80008000u : 0u;  // a negative scale goes to Q
-      const T* qb = static_cast<const T*>(p.q.ptr);
-      // x / G by the high word of a product: exact for x * G below 2^32
-      const uint32_t g_inv = G == 1 ? 0u : 0xffffffffu / G + 1u;
-      int jt = 0, n_qi[2] = {0, 0};
+      int jt = 0;
       bool ok = true;
       while (ok && next_piece(pc)) {
         const int note = (n_item - 1) % kNotes;
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          if (!ok) break;
-          if (pc.n[i] == 0) continue;
-          if (n_qi[i] > 0) ok = wait_all(kBQe + i, (n_qi[i] - 1) & 1);
-          if (!ok) break;
-          ++n_qi[i];
-          uint8_t* q = smem + S::kQ + i * S::kTile;
-          constexpr int U = D / 8;  // 16-byte units of a row
-          const int64_t r0 = pc.row0 + 128 * i;
-          // all copies in flight at once; rows past the sequence are zeros
-          auto place = [&](int it) {
-            const int idx = it * 64 + t, r = idx / U, u = idx % U;
-            return q + (u >> 3) * kChunk + r * 128 + (((u & 7) ^ (r & 7)) << 4);
-          };
-#pragma unroll 8
-          for (int it = 0; it < 2 * U; ++it) {
-            const int idx = it * 64 + t, r = idx / U, u = idx % U;
-            const uint32_t x = pc.rem0 + 128 * i + r, tok = G == 1 ? x : __umulhi(x, g_inv);
-            const bool on = r0 + r < pc.R;
-            const T* src = on ? qb + (pc.q0 + pc.tok0 + tok) * p.q.token_stride + (pc.head * G + x - tok * G) * p.q.head_stride + 8 * u
-                              : qb;
-            cp_async_16(place(it), src, on);
-          }
-          cp_async_wait();
-          if (flip)
-            for (int it = 0; it < 2 * U; ++it) {
-              uint4* at = reinterpret_cast<uint4*>(place(it));
-              uint4 w = *at;
-              w.x ^= flip, w.y ^= flip, w.z ^= flip, w.w ^= flip;
-              *at = w;
-            }
-          fence_async_smem();
-          mbar_arrive(&bars[kBQ + i]);
-        }
         if (ok && n_item > kNotes) ok = wait_all(kBNe + note, freed(n_item - 1, kNotes));
         int* notes = s_bad + ((warp - 10) * kNotes + note) * 3 * D;
         if (pc.first_masked < pc.n_max)
@@ -430,30 +409,35 @@ prompt_kernel(const PromptArgs a, const __grid_constant__ CUtensorMap kmap, cons
             const int live = min(kKeys, pc.nk - (pc.t0 + j) * kKeys);  // positions of the tile inside the sequence
             constexpr uint32_t kExp = BF16 ? 0x7F807F80u : 0x7C007C00u, kOne = BF16 ? 0x00800080u : 0x04000400u;
             bool wrote = false;
+            // rows from the first position that some row does not see
+            const int r0 = max(0, pc.mask_from - (pc.t0 + j) * kKeys);
+#pragma unroll
+            for (int c = 0; c < D / 64; ++c) {
 #pragma unroll 4
-            for (int u = t; u < S::kTile / 16; u += 64) {
-              uint4* at = reinterpret_cast<uint4*>(v + u * 16);
-              const int r = (u >> 3) & 127;
-              if (r >= live) {
-                *at = make_uint4(0u, 0u, 0u, 0u);
-                wrote = true;
-                continue;
-              }
-              const uint4 w = *at;
-              const uint32_t bad = (((w.x & kExp) + kOne) | ((w.y & kExp) + kOne) | ((w.z & kExp) + kOne) | ((w.w & kExp) + kOne)) &
-                                   0x80008000u;
-              if (bad) {
-                uint16_t* h = reinterpret_cast<uint16_t*>(at);
-                const int d0 = (u >> 10) * 64 + (((u & 7) ^ (r & 7)) << 3);
-                for (int e = 0; e < 8; ++e) {
-                  const uint16_t x = h[e];
-                  if ((x & (kExp & 0xffffu)) != (kExp & 0xffffu)) continue;
-                  const int kind = (x & 0x7fff & ~(kExp & 0xffffu)) ? 0 : x >> 15 ? 2 : 1;
-                  atomicMin(&notes[kind * D + d0 + e], (pc.t0 + j) * kKeys + r);
-                  s_anybad[(warp - 10) * kNotes + note] = 1;
-                  h[e] = 0;
+              for (int x = t; x < (kKeys - r0) * 8; x += 64) {
+                const int r = r0 + (x >> 3), u = x & 7;
+                uint4* at = reinterpret_cast<uint4*>(v + c * kChunk + r * 128 + u * 16);
+                if (r >= live) {
+                  *at = make_uint4(0u, 0u, 0u, 0u);
+                  wrote = true;
+                  continue;
                 }
-                wrote = true;
+                const uint4 w = *at;
+                const uint32_t bad = (((w.x & kExp) + kOne) | ((w.y & kExp) + kOne) | ((w.z & kExp) + kOne) | ((w.w & kExp) + kOne)) &
+                                     0x80008000u;
+                if (bad) {
+                  uint16_t* h = reinterpret_cast<uint16_t*>(at);
+                  const int d0 = c * 64 + ((u ^ (r & 7)) << 3);
+                  for (int e = 0; e < 8; ++e) {
+                    const uint16_t y = h[e];
+                    if ((y & (kExp & 0xffffu)) != (kExp & 0xffffu)) continue;
+                    const int kind = (y & 0x7fff & ~(kExp & 0xffffu)) ? 0 : y >> 15 ? 2 : 1;
+                    atomicMin(&notes[kind * D + d0 + e], (pc.t0 + j) * kKeys + r);
+                    s_anybad[(warp - 10) * kNotes + note] = 1;
+                    h[e] = 0;
+                  }
+                  wrote = true;
+                }
               }
             }
             if (wrote) fence_async_smem();
@@ -470,24 +454,19 @@ prompt_kernel(const PromptArgs a, const __grid_constant__ CUtensorMap kmap, cons
     const uint32_t t_lane = static_cast<uint32_t>(32 * (warp & 3)) << 16;
     const uint32_t t_s = tbase + t_lane + 128 * i, t_o = tbase + t_lane + 256 + 128 * i;
     const float sl = fmaxf(fabsf(p.scale) * kLog2e, 1.2e-38f);  // not 0: -inf * sl stays -inf
+    const int tok_l = wt / G, head_l = wt - tok_l * G;  // this thread's row in its tile
+    uint8_t* stage = smem + S::kStage + warp * 2048;
     int n_s = 0, n_o = 0;  // scores and results so far
     bool ok = true;
     while (ok && next_piece(pc)) {
-      const int note = (n_item - 1) % kNotes, part_id = pc.id;
-      const int64_t row = pc.row0 + 128 * i + wt;
-      const bool store = row < pc.R;
+      const int note = (n_item - 1) % kNotes;
+      const int token = pc.tok0 + i * a.tokens + tok_l;
+      const bool store = wt < a.tokens * G && token < pc.nq;
       const int n = i == 0 ? pc.n[0] : pc.n[1], t0 = pc.t0;
-      float* part = a.parts > 1 ? part_slot(p, pc.id, D) + (128 * i + wt) * static_cast<int64_t>(D) : nullptr;
-      const int my_sees = pc.sees(min(row, pc.R - 1), G);
-      const int all_see = pc.sees(pc.row0 + 128 * i, G);  // what every row of the tile sees
-      T* out;
-      float* lse;
-      {
-        const int x = pc.rem0 + 128 * i + wt, tok = x / G;
-        const int h = pc.head * G + x - tok * G;
-        out = static_cast<T*>(p.out.ptr) + (pc.q0 + pc.tok0 + tok) * p.out.token_stride + h * p.out.head_stride;
-        lse = p.lse ? p.lse + (pc.q0 + pc.tok0 + tok) * p.q_heads + h : nullptr;
-      }
+      const int my_sees = pc.sees(min(token, pc.nq - 1));
+      const int all_see = pc.sees(pc.tok0 + i * a.tokens);  // what every row of the tile sees
+      const int64_t at = pc.q0 + token;                       // row of q and out
+      const int h = pc.head * G + head_l;
       float m = -INFINITY, l = 0.f;
       for (int j = 0; j < n; ++j, ++n_s) {
         ok = wait_all(kBS + i, n_s & 1);
@@ -498,6 +477,10 @@ prompt_kernel(const PromptArgs a, const __grid_constant__ CUtensorMap kmap, cons
         for (int c = 0; c < 4; ++c) tmem_ld32(t_s + 32 * c, s + 32 * c);
 #pragma unroll
         for (int c = 0; c < 4; ++c) tmem_wait_ld32(s + 32 * c);
+        if (p.scale < 0.f) {  // the sign goes to the scores
+#pragma unroll
+          for (int c = 0; c < 128; ++c) s[c] ^= 0x80000000u;
+        }
         if ((t0 + j + 1) * kKeys > all_see) {
           const int lim = my_sees - (t0 + j) * kKeys;
 #pragma unroll
@@ -572,7 +555,12 @@ prompt_kernel(const PromptArgs a, const __grid_constant__ CUtensorMap kmap, cons
       const int* bad1 = s_bad + (kNotes + note) * 3 * D;
       const bool use0 = s_anybad[note] != 0, use1 = s_anybad[kNotes + note] != 0;
       {
-        const float inv = part ? 1.f : l == 0.f ? 0.f : 1.f / l;
+        const float inv = a.parts > 1 ? 1.f : l == 0.f ? 0.f : 1.f / l;
+        T* out = static_cast<T*>(p.out.ptr);
+        int64_t off8[4];  // of the rows this lane stores; -1: none
+#pragma unroll
+        for (int x = 0; x < 4; ++x)
+          off8[x] = __shfl_sync(full, store ? at * p.out.token_stride + h * p.out.head_stride : -1, 8 * x + (lane >> 2));
 #pragma unroll 1
         for (int c = 0; c < D; c += 32) {
           uint32_t o[32];
@@ -592,26 +580,49 @@ prompt_kernel(const PromptArgs a, const __grid_constant__ CUtensorMap kmap, cons
               else if (down) o[e] = 0xff800000u;
             }
           }
-          if (store && part) {
+          // through shared memory, so that a store covers whole sectors: 32 rows of
+          // 64 bytes (parts, in fp32: two halves of the columns)
+          if (a.parts > 1) {
+            float* part = part_slot(p, pc.id, D) + (128 * i + 32 * (warp & 3)) * D + c;
 #pragma unroll
-            for (int e = 0; e < 32; e += 4)
-              *reinterpret_cast<uint4*>(part + c + e) = make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
-          } else if (store) {
+            for (int half = 0; half < 2; ++half) {
 #pragma unroll
-            for (int e = 0; e < 32; e += 8) {
-              uint4 w;
-              w.x = cvt_pair<BF16>(__uint_as_float(o[e]), __uint_as_float(o[e + 1]));
-              w.y = cvt_pair<BF16>(__uint_as_float(o[e + 2]), __uint_as_float(o[e + 3]));
-              w.z = cvt_pair<BF16>(__uint_as_float(o[e + 4]), __uint_as_float(o[e + 5]));
-              w.w = cvt_pair<BF16>(__uint_as_float(o[e + 6]), __uint_as_float(o[e + 7]));
-              *reinterpret_cast<uint4*>(out + c + e) = w;
+              for (int u = 0; u < 4; ++u)
+                *reinterpret_cast<uint4*>(stage + lane * 64 + ((u ^ ((lane >> 1) & 3)) << 4)) =
+                    make_uint4(o[16 * half + 4 * u], o[16 * half + 4 * u + 1], o[16 * half + 4 * u + 2], o[16 * half + 4 * u + 3]);
+              __syncwarp();
+#pragma unroll
+              for (int x = 0; x < 4; ++x) {
+                const int r = 8 * x + (lane >> 2), u = lane & 3;
+                *reinterpret_cast<uint4*>(part + r * D + 16 * half + 4 * u) =
+                    *reinterpret_cast<const uint4*>(stage + r * 64 + ((u ^ ((r >> 1) & 3)) << 4));
+              }
+              __syncwarp();
             }
+          } else {
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+              uint4 w;
+              w.x = cvt_pair<BF16>(__uint_as_float(o[8 * u]), __uint_as_float(o[8 * u + 1]));
+              w.y = cvt_pair<BF16>(__uint_as_float(o[8 * u + 2]), __uint_as_float(o[8 * u + 3]));
+              w.z = cvt_pair<BF16>(__uint_as_float(o[8 * u + 4]), __uint_as_float(o[8 * u + 5]));
+              w.w = cvt_pair<BF16>(__uint_as_float(o[8 * u + 6]), __uint_as_float(o[8 * u + 7]));
+              *reinterpret_cast<uint4*>(stage + lane * 64 + ((u ^ ((lane >> 1) & 3)) << 4)) = w;
+            }
+            __syncwarp();
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+              const int r = 8 * x + (lane >> 2), u = lane & 3;
+              const uint4 w = *reinterpret_cast<const uint4*>(stage + r * 64 + ((u ^ ((r >> 1) & 3)) << 4));
+              if (off8[x] >= 0) *reinterpret_cast<uint4*>(out + off8[x] + c + 8 * u) = w;
+            }
+            __syncwarp();
           }
         }
-        if (store && part)
-          *reinterpret_cast<float2*>(part_slot(p, part_id, D) + kRowsPerBlock * D + 2 * (128 * i + wt)) = make_float2(m, l);
-        else if (store && lse)
-          *lse = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+        if (a.parts > 1)
+          *reinterpret_cast<float2*>(part_slot(p, pc.id, D) + kRowsPerBlock * D + 2 * (128 * i + wt)) = make_float2(m, l);
+        else if (store && p.lse)
+          p.lse[at * p.q_heads + h] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
         tcgen_before_sync();
       }
       mbar_arrive(&bars[kBNe + note]);
@@ -640,9 +651,9 @@ __global__ void __launch_bounds__(128) prompt_join_kernel(const PromptArgs a) {
   wait_for_last_kernel();  // every thread: what follows on the stream may rely on both kernels
   if (!on) return;
   const int64_t q0 = max(__ldg(p.cu_q + lo), 0);
-  const int64_t r = (token - q0) * a.G + qh - head * a.G;
-  const int64_t slot = q0 * a.G / kRowsPerBlock + lo + r / kRowsPerBlock;
-  const int rr = static_cast<int>(r % kRowsPerBlock);
+  const int i = static_cast<int>(token - q0), in_piece = i % (2 * a.tokens);
+  const int64_t slot = q0 / (2 * a.tokens) + lo + i / (2 * a.tokens);
+  const int rr = 128 * (in_piece / a.tokens) + in_piece % a.tokens * a.G + qh - head * a.G;
   const int first = static_cast<int>(((a.n_slots - 1 - slot) * p.kv_heads + head) * a.parts);
   float m = -INFINITY, l = 0.f, ml[kMaxParts], ll[kMaxParts];
 #pragma unroll
@@ -695,15 +706,16 @@ EncodeFn encode_fn() {
   return fn;
 }
 
-// Map of rows [tokens][heads][D]: boxes of 64 values x 1 head x 128 tokens.
-cudaError_t make_map(CUtensorMap* map, const RowsIn& r, int D, int heads, int64_t tokens, bool bf16) {
+// Map of rows [tokens][heads][D]: boxes of 64 values x box_heads x box_tokens.
+cudaError_t make_map(CUtensorMap* map, const RowsIn& r, int D, int heads, int64_t tokens, bool bf16, int box_heads,
+                     int box_tokens) {
   EncodeFn fn = encode_fn();
   if (!fn) return cudaErrorNotSupported;
   // the stride of a dimension of one element is free; zero strides have no map
   const int64_t hs = heads > 1 ? r.head_stride : D, ts = tokens > 1 ? r.token_stride : static_cast<int64_t>(heads) * D;
   const cuuint64_t dims[3] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(heads), static_cast<cuuint64_t>(tokens)};
   const cuuint64_t strides[2] = {static_cast<cuuint64_t>(hs) * 2, static_cast<cuuint64_t>(ts) * 2};
-  const cuuint32_t box[3] = {64, 1, kKeys}, ones[3] = {1, 1, 1};
+  const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(box_heads), static_cast<cuuint32_t>(box_tokens)}, ones[3] = {1, 1, 1};
   const CUresult rc = fn(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3,
                          const_cast<void*>(r.ptr), dims, strides, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
                          CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
@@ -715,11 +727,13 @@ cudaError_t launch(const PromptParams& p, cudaStream_t s) {
   PromptArgs a;
   a.p = p;
   a.G = p.q_heads / p.kv_heads;
-  a.n_slots = static_cast<int>(p.n_q * a.G / kRowsPerBlock) + p.n_seqs;
-  CUtensorMap km = {}, vm = {};
-  if (p.n_k > 0) {
-    cudaError_t e = make_map(&km, p.k, D, p.kv_heads, p.n_k, BF16);
-    if (e == cudaSuccess) e = make_map(&vm, p.v, D, p.kv_heads, p.n_k, BF16);
+  a.tokens = 128 / a.G;
+  a.n_slots = static_cast<int>(p.n_q / (2 * a.tokens)) + p.n_seqs;
+  CUtensorMap qm = {}, km = {}, vm = {};
+  if (p.n_k > 0) {  // without keys nothing is loaded
+    cudaError_t e = make_map(&qm, p.q, D, p.q_heads, p.n_q, BF16, a.G, a.tokens);
+    if (e == cudaSuccess) e = make_map(&km, p.k, D, p.kv_heads, p.n_k, BF16, 1, kKeys);
+    if (e == cudaSuccess) e = make_map(&vm, p.v, D, p.kv_heads, p.n_k, BF16, 1, kKeys);
     if (e != cudaSuccess) return e;
   }
   static const cudaError_t attr =
@@ -738,7 +752,7 @@ cudaError_t launch(const PromptParams& p, cudaStream_t s) {
     // A part costs about kPartTiles key tiles more (its start and end, the join).
     // The lengths are known as averages only; any choice is right.
     const double kPartTiles = 6;
-    const double busy = std::ceil(static_cast<double>(p.n_q) * a.G / kRowsPerBlock / p.n_seqs) * p.n_seqs * p.kv_heads;
+    const double busy = std::ceil(static_cast<double>(p.n_q) / (2 * a.tokens) / p.n_seqs) * p.n_seqs * p.kv_heads;
     const double tiles = static_cast<double>(p.n_k) / p.n_seqs / kKeys;
     double best = 0;
     for (int n = 1; n <= kMaxParts && pieces * n <= kPartSlots; ++n) {
@@ -747,7 +761,7 @@ cudaError_t launch(const PromptParams& p, cudaStream_t s) {
     }
   }
   const int64_t total = pieces * a.parts;
-  prompt_kernel<D, BF16><<<static_cast<unsigned>(total < sms ? total : sms), kThreads, Smem<D>::kBytes, s>>>(a, km, vm);
+  prompt_kernel<D, BF16><<<static_cast<unsigned>(total < sms ? total : sms), kThreads, Smem<D>::kBytes, s>>>(a, qm, km, vm);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess || a.parts == 1) return e;
   return launch_after(prompt_join_kernel<D, BF16>, static_cast<unsigned>((p.n_q * p.q_heads + 3) / 4), a, s);

@@ -475,7 +475,8 @@ int qgemv_attn_tree(const qgemv_kv_cache* cache, const int32_t* table, int64_t t
  * all of the keys, the one before it all but the last, and so on (query i of
  * nq sees the keys j <= i + nk - nq of nk: chunks after a past, or rows that
  * see nothing where nk < nq).  dtype: QGEMV_DT_F16 or QGEMV_DT_BF16, of q, k,
- * v and out; k and v have no strides of zero.
+ * v and out; no strides of zero, and at most
+ * 128 query heads of a key/value head.
  *   cu_q, cu_k: device int32 [n_seqs + 1], not decreasing.
  *   max_q: the most queries of a sequence; 0 for a call with nothing to do.
  *   lse: device fp32 [n_q][q_heads], or NULL.

@@ -93,7 +93,8 @@ def test_tree_refusals(lib, kw, code):
                                       ({"q": None}, ARG), ({"k": None}, ARG), ({"out": None}, ARG), ({"cu_q": None}, ARG),
                                       ({"cu_k": None}, ARG), ({"n_q": -1}, ARG), ({"max_q": -1}, ARG), ({"k": 257}, ALIGN),
                                       ({"vt": 130}, ALIGN), ({"ot": 64}, ARG), ({"ws": None}, ARG), ({"ws_bytes": 1}, ARG),
-                                      ({"cu_k": 65}, ALIGN), ({"kt": 0}, ARG), ({"vh": 0}, ARG), ({"n_q": 0}, OK), ({"n_seqs": 0}, OK), ({"max_q": 0}, OK)])
+                                      ({"cu_k": 65}, ALIGN), ({"kt": 0}, ARG), ({"vh": 0}, ARG), ({"qt": 0}, ARG),
+                                      ({"heads": 258, "ot": 258 * 128}, ARG), ({"n_q": 0}, OK), ({"n_seqs": 0}, OK), ({"max_q": 0}, OK)])
 def test_prompt_refusals(lib, kw, code):
     assert call(lib.qgemv_attn_prompt, PROMPT, kw) == code
 

@@ -84,6 +84,8 @@ class Case:
     (8, 8, 128, [5, 130, 1, 200], [900, 131, 256, 777]),   # chunks after a past
     (4, 2, 128, [40, 300, 7], [17, 0, 3]),           # fewer keys than queries: rows that see nothing
     (40, 8, 128, [33, 257], [290, 257]),
+    (71, 1, 64, [5, 1], None),                       # one token's heads to a tile
+    (128, 1, 128, [3], [130]),
 ])
 def test_matches_the_definition(kind, hq, hkv, d, nq, nk):
     c = Case(kind, hq, hkv, d, nq, nk)
