@@ -411,22 +411,26 @@ prompt_kernel(const PromptArgs a, const __grid_constant__ CUtensorMap qmap, cons
             bool wrote = false;
             // rows from the first position that some row does not see
             const int r0 = max(0, pc.mask_from - (pc.t0 + j) * kKeys);
-#pragma unroll
+            constexpr int kAtOnce = 8;  // units of a thread in flight
+            const int r1 = max(r0, live), units = (r1 - r0) * 8;
             for (int c = 0; c < D / 64; ++c) {
-#pragma unroll 4
-              for (int x = t; x < (kKeys - r0) * 8; x += 64) {
-                const int r = r0 + (x >> 3), u = x & 7;
-                uint4* at = reinterpret_cast<uint4*>(v + c * kChunk + r * 128 + u * 16);
-                if (r >= live) {
-                  *at = make_uint4(0u, 0u, 0u, 0u);
-                  wrote = true;
-                  continue;
+              uint8_t* vc = v + c * kChunk;
+              for (int x0 = t; x0 < units; x0 += 64 * kAtOnce) {
+                uint4 w[kAtOnce];
+                uint32_t any = 0;
+#pragma unroll
+                for (int k = 0; k < kAtOnce; ++k) {
+                  // (past the end: the first unit again)
+                  const int x = x0 + 64 * k < units ? x0 + 64 * k : x0;
+                  w[k] = *reinterpret_cast<const uint4*>(vc + r0 * 128 + x * 16);
                 }
-                const uint4 w = *at;
-                const uint32_t bad = (((w.x & kExp) + kOne) | ((w.y & kExp) + kOne) | ((w.z & kExp) + kOne) | ((w.w & kExp) + kOne)) &
-                                     0x80008000u;
-                if (bad) {
-                  uint16_t* h = reinterpret_cast<uint16_t*>(at);
+#pragma unroll
+                for (int k = 0; k < kAtOnce; ++k)
+                  any |= ((w[k].x & kExp) + kOne) | ((w[k].y & kExp) + kOne) | ((w[k].z & kExp) + kOne) | ((w[k].w & kExp) + kOne);
+                if ((any & 0x80008000u) == 0) continue;
+                for (int x = x0; x < units && x < x0 + 64 * kAtOnce; x += 64) {
+                  const int r = r0 + (x >> 3), u = x & 7;
+                  uint16_t* h = reinterpret_cast<uint16_t*>(vc + r0 * 128 + x * 16);
                   const int d0 = c * 64 + ((u ^ (r & 7)) << 3);
                   for (int e = 0; e < 8; ++e) {
                     const uint16_t y = h[e];
@@ -435,9 +439,13 @@ prompt_kernel(const PromptArgs a, const __grid_constant__ CUtensorMap qmap, cons
                     atomicMin(&notes[kind * D + d0 + e], (pc.t0 + j) * kKeys + r);
                     s_anybad[(warp - 10) * kNotes + note] = 1;
                     h[e] = 0;
+                    wrote = true;
                   }
-                  wrote = true;
                 }
+              }
+              for (int x = max(live, 0) * 8 + t; x < kKeys * 8; x += 64) {  // past the sequence
+                *reinterpret_cast<uint4*>(vc + x * 16) = make_uint4(0u, 0u, 0u, 0u);
+                wrote = true;
               }
             }
             if (wrote) fence_async_smem();
