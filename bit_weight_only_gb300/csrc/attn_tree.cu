@@ -2,8 +2,8 @@
 // (qgemv_attn_tree).
 //
 // Rows of a sequence and key/value head: row = token * G + head of the group.
-// tree_kernel takes up to 32 of them at a time, in tiles of 16 or 32, by
-// mma.sync; more go to attn_tree_wide.cu.  A unit is a block of 16 cached
+// tree_kernel takes them in tiles of 16 or 32, by mma.sync; more than 32 rows
+// of the fp16 and INT8 formats go to attn_tree_wide.cu.  A unit is a block of 16 cached
 // tokens (tree_work.cuh); within a thread block's segment a warp takes every
 // W-th unit:
 //
@@ -28,7 +28,7 @@
 namespace qgemv {
 namespace {
 
-constexpr int kNarrowRows = 32;  // more rows than this go to the wide kernel
+constexpr int kNarrowRows = 32;  // more rows than this go to the wide kernel, but for Q4_0
 constexpr int64_t kWholeTokens = 1024;
 constexpr int kErrTree = 32;
 constexpr float kLazyT = 8.f;
@@ -40,6 +40,13 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint4& a, uint32_t
   asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
                : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
                : "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b0), "r"(b1));
+}
+
+// c = a . b
+__device__ __forceinline__ void mma16816_first(float (&c)[4], const uint4& a, uint32_t b0, uint32_t b1) {
+  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+               : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+               : "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b0), "r"(b1), "f"(0.f));
 }
 
 // Per format: words of K and V of a lane, and the fp16 pairs in them.
@@ -153,6 +160,17 @@ struct Codes<QGEMV_KV_Q4_0, D> {
     }
   }
 };
+
+// Q4_0 scales of a lane's tokens 8 nb + 2 t + e of a block, from `at`.
+template <int D>
+__device__ __forceinline__ void load_scales(const uint8_t* at, int t, __half (&sc)[2][2][D / 32]) {
+#pragma unroll
+  for (int nb = 0; nb < 2; ++nb) {
+    const uint8_t* src = at + (8 * nb + 2 * t) * (D / 16);
+    if constexpr (D == 128) *reinterpret_cast<uint4*>(&sc[nb][0][0]) = lds128(src);
+    else *reinterpret_cast<uint2*>(&sc[nb][0][0]) = *reinterpret_cast<const uint2*>(src);
+  }
+}
 
 // Shape of a kernel: W warps, MT tiles of 16 rows.
 template <int FMT, int D, int MT>
@@ -290,26 +308,17 @@ __global__ void __launch_bounds__(TreeShape<FMT, D, MT>::kThreads, kBlocksPerSm)
         const bool edge = pos0 + kKvBlockTokens > ctx;  // some positions are drafted, or past the end
         // ---- S
         float s[MT][2][4];
-#pragma unroll
-        for (int i = 0; i < MT; ++i)
-#pragma unroll
-          for (int nb = 0; nb < 2; ++nb)
-#pragma unroll
-            for (int c = 0; c < 4; ++c) s[i][nb][c] = 0.f;
         {
           uint32_t kw[2][C::kKw];
           C::load_k(blk, g, lane, kw[0]);
           C::load_k(blk, 8 + g, lane, kw[1]);
           if constexpr (FMT == QGEMV_KV_Q4_0) {
+            // sums of each group, times the tokens' scales of the group
+            alignas(16) __half ksc[2][2][D / 32];
+            load_scales<D>(blk + L::kKs, t, ksc);
 #pragma unroll
             for (int grp = 0; grp < D / 32; ++grp) {
               float part[MT][2][4];
-#pragma unroll
-              for (int i = 0; i < MT; ++i)
-#pragma unroll
-                for (int nb = 0; nb < 2; ++nb)
-#pragma unroll
-                  for (int c = 0; c < 4; ++c) part[i][nb][c] = 0.f;
 #pragma unroll
               for (int h = 0; h < 2; ++h) {
                 const int ks = 2 * grp + h;
@@ -319,23 +328,33 @@ __global__ void __launch_bounds__(TreeShape<FMT, D, MT>::kThreads, kBlocksPerSm)
 #pragma unroll
                 for (int i = 0; i < MT; ++i) {
                   const uint4 qa = s_q[(i * KS + ks) * 32 + lane];
-                  mma16816(part[i][0], qa, b[0][0], b[0][1]);
-                  mma16816(part[i][1], qa, b[1][0], b[1][1]);
+#pragma unroll
+                  for (int nb = 0; nb < 2; ++nb) {
+                    if (h == 0) mma16816_first(part[i][nb], qa, b[nb][0], b[nb][1]);
+                    else mma16816(part[i][nb], qa, b[nb][0], b[nb][1]);
+                  }
                 }
               }
 #pragma unroll
-              for (int nb = 0; nb < 2; ++nb) {
-                const __half* ksc = reinterpret_cast<const __half*>(blk + L::kKs) + (8 * nb + 2 * t) * (D / 32) + grp;
-                const float a0 = __half2float(ksc[0]) * sl, a1 = __half2float(ksc[D / 32]) * sl;
+              for (int nb = 0; nb < 2; ++nb)
 #pragma unroll
-                for (int i = 0; i < MT; ++i) {
-                  s[i][nb][0] = fmaf(part[i][nb][0], a0, s[i][nb][0]);
-                  s[i][nb][1] = fmaf(part[i][nb][1], a1, s[i][nb][1]);
-                  s[i][nb][2] = fmaf(part[i][nb][2], a0, s[i][nb][2]);
-                  s[i][nb][3] = fmaf(part[i][nb][3], a1, s[i][nb][3]);
+                for (int e = 0; e < 2; ++e) {
+                  const float f = __half2float(ksc[nb][e][grp]);
+#pragma unroll
+                  for (int i = 0; i < MT; ++i)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                      float& x = s[i][nb][2 * h + e];
+                      x = grp == 0 ? part[i][nb][2 * h + e] * f : fmaf(part[i][nb][2 * h + e], f, x);
+                    }
                 }
-              }
             }
+#pragma unroll
+            for (int i = 0; i < MT; ++i)
+#pragma unroll
+              for (int nb = 0; nb < 2; ++nb)
+#pragma unroll
+                for (int c = 0; c < 4; ++c) s[i][nb][c] *= sl;
           } else {
 #pragma unroll
             for (int ks = 0; ks < KS; ++ks) {
@@ -345,8 +364,11 @@ __global__ void __launch_bounds__(TreeShape<FMT, D, MT>::kThreads, kBlocksPerSm)
 #pragma unroll
               for (int i = 0; i < MT; ++i) {
                 const uint4 qa = s_q[(i * KS + ks) * 32 + lane];
-                mma16816(s[i][0], qa, b[0][0], b[0][1]);
-                mma16816(s[i][1], qa, b[1][0], b[1][1]);
+#pragma unroll
+                for (int nb = 0; nb < 2; ++nb) {
+                  if (ks == 0) mma16816_first(s[i][nb], qa, b[nb][0], b[nb][1]);
+                  else mma16816(s[i][nb], qa, b[nb][0], b[nb][1]);
+                }
               }
             }
 #pragma unroll
@@ -375,27 +397,31 @@ __global__ void __launch_bounds__(TreeShape<FMT, D, MT>::kThreads, kBlocksPerSm)
         }
         // ---- scales of V and the reference
         float vs[2][2][FMT == QGEMV_KV_Q4_0 ? D / 32 : 1], lv[2][2];
+        if constexpr (FMT == QGEMV_KV_Q4_0) {
+          alignas(16) __half vsc[2][2][D / 32];
+          load_scales<D>(blk + L::kVs, t, vsc);
 #pragma unroll
-        for (int nb = 0; nb < 2; ++nb)
+          for (int nb = 0; nb < 2; ++nb)
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const int tok = 8 * nb + 2 * t + e;
-            if constexpr (FMT == QGEMV_KV_F16) {
-              vs[nb][e][0] = 1.f, lv[nb][e] = 0.f;
-            } else if constexpr (FMT == QGEMV_KV_INT8) {
-              vs[nb][e][0] = *reinterpret_cast<const float*>(blk + L::kVs + 4 * tok);
-              lv[nb][e] = lg2(fmaxf(vs[nb][e][0], 7.9e-31f));  // 2^-100
-            } else {
-              const __half* v = reinterpret_cast<const __half*>(blk + L::kVs) + tok * (D / 32);
-              float top = 7.9e-31f;
+            for (int e = 0; e < 2; ++e) {
+              float top = 7.9e-31f;  // 2^-100
 #pragma unroll
               for (int x = 0; x < D / 32; ++x) {
-                vs[nb][e][x] = __half2float(v[x]);
+                vs[nb][e][x] = __half2float(vsc[nb][e][x]);
                 top = fmaxf(top, fabsf(vs[nb][e][x]));
               }
               lv[nb][e] = lg2(top);
             }
+        } else {
+#pragma unroll
+          for (int nb = 0; nb < 2; ++nb) {
+            float2 v = make_float2(1.f, 1.f);
+            if constexpr (FMT == QGEMV_KV_INT8) v = *reinterpret_cast<const float2*>(blk + L::kVs + 4 * (8 * nb + 2 * t));
+            vs[nb][0][0] = v.x, vs[nb][1][0] = v.y;
+            lv[nb][0] = FMT == QGEMV_KV_F16 ? 0.f : lg2(fmaxf(v.x, 7.9e-31f));
+            lv[nb][1] = FMT == QGEMV_KV_F16 ? 0.f : lg2(fmaxf(v.y, 7.9e-31f));
           }
+        }
         bool grow = false;
 #pragma unroll
         for (int i = 0; i < MT; ++i)
@@ -774,7 +800,7 @@ cudaError_t launch_attn_tree(const TreeParams& p, cudaStream_t s) {
   // Contexts of up to kWholeTokens positions (as the caller bounds them) are
   // not split: a second kernel would take longer than the split saves.
   a.whole = p.max_ctx + p.max_new <= kWholeTokens;
-  if (rows > kNarrowRows) {
+  if (rows > kNarrowRows && p.cache.format != QGEMV_KV_Q4_0) {
     a.extra = 4;  // a row tile's start and end: about four units of 128 tokens
     a.min_units = 2 + a.extra;
     const cudaError_t e = launch_tree_wide(a, s);

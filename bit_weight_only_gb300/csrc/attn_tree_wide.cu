@@ -20,15 +20,13 @@
 //   V (4)  likewise; in units that hold drafted tokens or end inside, whatever
 //          must not meet a masked row's 0 is taken out of V (below)
 //   copies (bulk, from the pages), ahead of all; MMAs; two that do nothing
-// INT8 codes are exact in fp16.  Q4_0: K's codes are exact too; a product for
-// each group of 32 goes to columns of its own and the key's thread adds them
-// with its four scales in fp32.  V's codes are multiplied by their group's
-// scale (over a power of two that goes to p) and rounded to fp16 once: here a
-// group's scale cannot be applied after the product, whose rows are d.
-// fp16 values and Q4_0 scales of drafted tokens may be infinite or NaN, and
-// what lies past the sequence's end is whatever the page holds: both are
-// zeroed in V, and the former noted by (drafted token, d) for the rows that
-// see them.
+// INT8 codes are exact in fp16.  fp16 values of drafted tokens may be infinite
+// or NaN, and what lies past the sequence's end is whatever the page holds:
+// both are zeroed in V, and the former noted by (drafted token, d) for the rows
+// that see them.  Q4_0 does not come here: its groups' scales would take a
+// product for each group of K and another rounding of V, and with them this
+// kernel was slower than tiles of 32 rows by attn_tree.cu's (12 ragged
+// sequences, 45 rows: 135 us against 110).
 //
 // Every wait is bounded; on a timeout the block records the error, waits for
 // its own copies and MMAs, frees tensor memory and returns.
@@ -61,33 +59,32 @@ constexpr int kNotes = 3;
 template <int FMT, int D>
 struct Wide {
   using L = KvLayout<FMT, D>;
-  static constexpr bool kF16 = FMT == QGEMV_KV_F16, kQ4 = FMT == QGEMV_KV_Q4_0;
+  static constexpr bool kF16 = FMT == QGEMV_KV_F16;
+  static_assert(kF16 || FMT == QGEMV_KV_INT8, "format");
   static constexpr int kTile = kKeys * D * 2;  // a K or V operand
   static constexpr int kKs = kF16 ? 3 : 2, kVs = 2;
   static constexpr int kHalf = kBlocks / 2 * L::kBlock;  // raw stage: half a unit
-  static constexpr int kRs = kF16 ? 0 : kQ4 ? 4 : 3;
-  static constexpr int kGroups = kQ4 ? D / 32 : 1;  // products of S
-  static constexpr int kSBufs = kQ4 ? 1 : 2;
-  static constexpr int kScales = kF16 ? 0 : kQ4 ? 4 : 1;  // floats of K's scales of a key
+  static constexpr int kRs = kF16 ? 0 : 3;
+  static constexpr int kSBufs = 2;
   // shared memory
   static constexpr int kK = 0;
   static constexpr int kV = kK + kKs * kTile;
   static constexpr int kQ = kV + kVs * kTile;
   static constexpr int kP = kQ + kRows * D * 2;
   static constexpr int kRaw = kP + kKeys * 128;
-  static constexpr int kKsc = kRaw + kRs * kHalf;          // [kKs][128][kScales]
-  static constexpr int kVsc = kKsc + kKs * kKeys * 4 * kScales;
+  static constexpr int kKsc = kRaw + kRs * kHalf;          // [kKs][128]
+  static constexpr int kVsc = kKsc + (kF16 ? 0 : kKs * kKeys * 4);
   static constexpr int kM = kVsc + (kF16 ? 0 : kKs * kKeys * 4);  // float[64] -m, float[64] factors, float[4][64] x 2
   static constexpr int kRowOff = kM + 64 * 4 * 10;         // int64[64][2]: q and out offsets
   static constexpr int kRowMask = kRowOff + 64 * 16;       // uint64[64]
   static constexpr int kKeyMask = kRowMask + 64 * 8;       // uint32[kSoft][64]: a warpgroup's rows that see a drafted token
   static constexpr int kBad = kKeyMask + kSoft * 64 * 4;   // uint64[kNotes][3][D]
-  static constexpr int kInts = kBad + (FMT == QGEMV_KV_INT8 ? 0 : kNotes * 3 * D * 8);
+  static constexpr int kInts = kBad + (!kF16 ? 0 : kNotes * 3 * D * 8);
   static constexpr int kBars = kInts + 128;
   static constexpr int kBytes = kBars + 48 * 8 + 1024;  // + alignment
   static_assert(kBytes <= 227 * 1024, "shared memory");
   // tensor memory columns
-  static constexpr int kOCol = kSBufs * kGroups * kRows;
+  static constexpr int kOCol = kSBufs * kRows;
   static_assert(kOCol + kRows <= 512, "tensor memory");
 };
 
@@ -96,12 +93,6 @@ struct Bars {
   static constexpr int kRf = 0, kRe = kRf + 5, kKf = kRe + 5, kKe = kKf + 3, kVl = kKe + 3, kVf = kVl + 2, kVe = kVf + 2,
                        kSf = kVe + 2, kSe = kSf + 2, kPf = kSe + 2, kPv = kPf + 1, kQf = kPv + 1, kDone = kQf + 1;
 };
-
-__device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
-  uint32_t r;
-  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-  return r;
-}
 
 // OR of `pred` over the 128 threads of softmax warpgroup w.
 __device__ __forceinline__ bool any_of_128(int w, bool pred) {
@@ -278,20 +269,11 @@ __global__ void __launch_bounds__(kThreads, 1) tree_wide_kernel(const TreeArgs a
           continue;
         }
         // ---- S of this key
-        const uint32_t t_s = tbase + t_lane + sb * S::kGroups * kRows + c0;
-        constexpr int LC = S::kGroups > 1 ? 16 : kCols;  // columns loaded at a time
-        uint32_t raw[S::kGroups][LC];
-#pragma unroll
-        for (int g = 0; g < S::kGroups; ++g) tmem_ld<LC>(t_s + g * kRows, raw[g]);
-        float ksc[4] = {1.f, 1.f, 1.f, 1.f};
-        float vs = 1.f, lv = 0.f;
-        if constexpr (FMT == QGEMV_KV_INT8) {
-          ksc[0] = reinterpret_cast<const float*>(smem + S::kKsc)[ks * kKeys + key];
-        } else if constexpr (S::kQ4) {
-          const float4 k4 = reinterpret_cast<const float4*>(smem + S::kKsc)[ks * kKeys + key];
-          ksc[0] = k4.x, ksc[1] = k4.y, ksc[2] = k4.z, ksc[3] = k4.w;
-        }
+        uint32_t raw[kCols];
+        tmem_ld<kCols>(tbase + t_lane + sb * kRows + c0, raw);
+        float f = sl, vs = 1.f, lv = 0.f;
         if constexpr (!S::kF16) {
+          f *= reinterpret_cast<const float*>(smem + S::kKsc)[ks * kKeys + key];
           vs = reinterpret_cast<const float*>(smem + S::kVsc)[ks * kKeys + key];
           lv = __log2f(fmaxf(vs, 7.9e-31f));  // 2^-100
         }
@@ -300,25 +282,11 @@ __global__ void __launch_bounds__(kThreads, 1) tree_wide_kernel(const TreeArgs a
         uint32_t vis = 0;  // the rows that see this key
         if (there) vis = pos < ctx ? ~0u : pos < all ? s_keymask[wg * kMaxDrafts + (pos - ctx)] : 0u;
         uint64_t x2[kCols / 2];
+        const uint64_t f2 = pack2(f, f);
+        tmem_wait_ld<kCols>(raw);
 #pragma unroll
-        for (int h = 0; h < kCols / LC; ++h) {
-          if (h > 0) {
-#pragma unroll
-            for (int g = 0; g < S::kGroups; ++g) tmem_ld<LC>(t_s + g * kRows + h * LC, raw[g]);
-          }
-#pragma unroll
-          for (int g = 0; g < S::kGroups; ++g) {
-            tmem_wait_ld<LC>(raw[g]);
-            const float f = ksc[g] * sl;
-            const uint64_t f2 = pack2(f, f);
-#pragma unroll
-            for (int c = 0; c < LC / 2; ++c) {
-              const uint64_t v = pack2(__uint_as_float(raw[g][2 * c]), __uint_as_float(raw[g][2 * c + 1]));
-              uint64_t& x = x2[h * (LC / 2) + c];
-              x = g == 0 ? mul2(v, f2) : fma2(v, f2, x);
-            }
-          }
-        }
+        for (int c = 0; c < kCols / 2; ++c)
+          x2[c] = mul2(pack2(__uint_as_float(raw[2 * c]), __uint_as_float(raw[2 * c + 1])), f2);
         tcgen_before_sync();
         mbar_arrive(&bars[B::kSe + sb]);
         __syncwarp();
@@ -433,7 +401,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_wide_kernel(const TreeArgs a
       tcgen_after_sync();
       float* slot = tree_slot(p, blockIdx.x, sg.u0 == 0, D);
       const int bb = n_seg % kNotes;
-      const bool bad = FMT != QGEMV_KV_INT8 && s_anybad[bb] != 0;
+      const bool bad = S::kF16 && s_anybad[bb] != 0;
       if (busy) {
         {
           // Each step halves the rows a lane holds: lane i ends with row i
@@ -477,7 +445,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_wide_kernel(const TreeArgs a
             const int r = c0 + c;
             if (r < live) {
               float x = __uint_as_float(o[c]) * s_f[r];
-              if (FMT != QGEMV_KV_INT8 && bad) {
+              if (S::kF16 && bad) {
                 const unsigned long long* bd = s_bad + bb * 3 * D + key;
                 const uint64_t rm = s_rowmask[r];
                 const bool nan = bd[0] & rm, up = bd[D] & rm, down = bd[2 * D] & rm;
@@ -510,10 +478,12 @@ __global__ void __launch_bounds__(kThreads, 1) tree_wide_kernel(const TreeArgs a
       bool left = false;
       auto start_notes = [&]() {
         left = any_of_128(kSoft, dead);
-        if (FMT == QGEMV_KV_INT8 || left) return;
-        for (int i = key; i < 3 * D; i += 128) s_bad[bb * 3 * D + i] = 0;
-        if (key == 0) s_anybad[bb] = 0;
-        named_bar_sync(1 + kSoft, 128);
+        if constexpr (S::kF16) {
+          if (left) return;
+          for (int i = key; i < 3 * D; i += 128) s_bad[bb * 3 * D + i] = 0;
+          if (key == 0) s_anybad[bb] = 0;
+          named_bar_sync(1 + kSoft, 128);
+        }
       };
       for (int j = 0; j < n; ++j, ++jt) {
         const int64_t pos = (sg.u0 + j) * kKeys + key;
@@ -566,92 +536,24 @@ __global__ void __launch_bounds__(kThreads, 1) tree_wide_kernel(const TreeArgs a
           const int tok = key & 15;
           const uint8_t* blk = smem + S::kRaw + rs * S::kHalf + ((key >> 4) & 3) * L::kBlock;
           const int valid = s_rvalid[rs];
-          const bool there = (valid >> ((key >> 4) & 3)) & 1;
           // 16-byte unit U of the row: chunk U >> 3, swizzled
           auto put = [&](int U, uint32_t w0, uint32_t w1, uint32_t w2, uint32_t w3) {
             *reinterpret_cast<uint4*>(dst + (U >> 3) * (kKeys * 128) + (((U & 7) ^ (key & 7)) << 4)) = make_uint4(w0, w1, w2, w3);
           };
-          if constexpr (FMT == QGEMV_KV_INT8) {
-            constexpr int N = D / 16;
-            // which unit first: eight neighbouring lanes read eight (d = 64:
-            // four) different ones
-            const int turn = is_v ? (lane & (N - 1)) ^ ((D == 128 ? 2 * ((lane >> 1) & 3) : 0)) : lane & (N - 1);
+          constexpr int N = D / 16;
+          // which unit first: eight neighbouring lanes read eight (d = 64:
+          // four) different ones
+          const int turn = is_v ? (lane & (N - 1)) ^ ((D == 128 ? 2 * ((lane >> 1) & 3) : 0)) : lane & (N - 1);
 #pragma unroll
-            for (int u = 0; u < N; ++u) {
-              const int unit = is_v ? u ^ turn : (u + turn) & (N - 1);
-              const uint4 c = lds128(blk + (is_v ? L::v_off(tok, 16 * unit) : L::k_off(tok, 16 * unit)));
-              put(2 * unit, i8_pair<0x4140>(c.x), i8_pair<0x4342>(c.x), i8_pair<0x4140>(c.y), i8_pair<0x4342>(c.y));
-              put(2 * unit + 1, i8_pair<0x4140>(c.z), i8_pair<0x4342>(c.z), i8_pair<0x4140>(c.w), i8_pair<0x4342>(c.w));
-            }
-            if (!is_v) {
-              reinterpret_cast<float*>(smem + S::kKsc)[ks * kKeys + key] = reinterpret_cast<const float*>(blk + L::kKs)[tok];
-              reinterpret_cast<float*>(smem + S::kVsc)[ks * kKeys + key] = reinterpret_cast<const float*>(blk + L::kVs)[tok];
-            }
-          } else {
-            constexpr int NG = D / 32;
-            const __half* vsc = reinterpret_cast<const __half*>(blk + L::kVs) + tok * NG;
-            // V's scales over a power of two of the token, which goes to p
-            float vg[NG], top = 0.f;
-#pragma unroll
-            for (int g = 0; g < NG; ++g) {
-              vg[g] = __half2float(vsc[g]);
-              if (fabsf(vg[g]) < INFINITY) top = fmaxf(top, fabsf(vg[g]));
-            }
-            const int ex = top > 0.f ? (__float_as_int(top) >> 23) - 127 : 0;  // fp16 scales: -24 .. 15
-            if (!is_v) {
-              constexpr int CW = D / 32;  // words of a cell
-              const __half* ksc = reinterpret_cast<const __half*>(blk + L::kKs) + tok * NG;
-#pragma unroll
-              for (int u = 0; u < 4; ++u) {
-                const int c = (u + (lane >> 1)) & 3;
-                const uint8_t* at = blk + L::k_off(tok, c * (D / 8));
-                uint32_t w[CW];
-                if constexpr (D == 128) *reinterpret_cast<uint4*>(w) = lds128(at);
-                else *reinterpret_cast<uint2*>(w) = *reinterpret_cast<const uint2*>(at);
-#pragma unroll
-                for (int g = 0; g < CW; ++g) put(4 * g + c, q4_pair<0>(w[g]), q4_pair<1>(w[g]), q4_pair<2>(w[g]), q4_pair<3>(w[g]));
-              }
-              float k4[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-              for (int g = 0; g < NG; ++g) k4[g] = __half2float(ksc[g]);
-              reinterpret_cast<float4*>(smem + S::kKsc)[ks * kKeys + key] = make_float4(k4[0], k4[1], k4[2], k4[3]);
-              reinterpret_cast<float*>(smem + S::kVsc)[ks * kKeys + key] =
-                  top > 0.f ? __int_as_float((ex + 127) << 23) : 0.f;  // no values: no say in the references
-            } else {
-              const bool on = there && pos < all;
-              uint32_t s2[NG];
-#pragma unroll
-              for (int g = 0; g < NG; ++g) {
-                float f = vg[g] * __int_as_float((127 - ex) << 23);
-                if (!on) f = 0.f;
-                if (on && pos >= ctx && !(fabsf(f) < INFINITY)) {
-                  for (int d = 0; d < 32; ++d) note(32 * g + d, 0);
-                  f = 0.f;
-                }
-                s2[g] = cvt_pair<false>(f, f);
-              }
-              // two cells: eight values of each group
-              auto four = [&](uint32_t hw, uint32_t s, uint32_t& lo, uint32_t& hi) {
-                const uint32_t x = hw | hw << 12;
-                lo = hmul2(hsub2((x & 0x000F000Fu) | 0x64006400u, 0x64086408u), s);
-                hi = hmul2(hsub2(((x >> 8) & 0x000F000Fu) | 0x64006400u, 0x64086408u), s);
-              };
-#pragma unroll
-              for (int u = 0; u < 4; ++u) {
-                const int c = (u + (lane >> 1)) & 3;
-                uint32_t w[NG];  // [cell][halfword pair]
-                const uint8_t* at = blk + L::v_off(tok, c * (D / 8));
-                if constexpr (D == 128) *reinterpret_cast<uint4*>(w) = lds128(at);
-                else *reinterpret_cast<uint2*>(w) = *reinterpret_cast<const uint2*>(at);
-#pragma unroll
-                for (int g = 0; g < NG; ++g) {
-                  uint32_t o0, o1, o2, o3;
-                  four((w[g >> 1] >> (16 * (g & 1))) & 0xffffu, s2[g], o0, o1);
-                  four((w[NG / 2 + (g >> 1)] >> (16 * (g & 1))) & 0xffffu, s2[g], o2, o3);
-                  put(4 * g + c, o0, o1, o2, o3);
-                }
-              }
-            }
+          for (int u = 0; u < N; ++u) {
+            const int unit = is_v ? u ^ turn : (u + turn) & (N - 1);
+            const uint4 c = lds128(blk + (is_v ? L::v_off(tok, 16 * unit) : L::k_off(tok, 16 * unit)));
+            put(2 * unit, i8_pair<0x4140>(c.x), i8_pair<0x4342>(c.x), i8_pair<0x4140>(c.y), i8_pair<0x4342>(c.y));
+            put(2 * unit + 1, i8_pair<0x4140>(c.z), i8_pair<0x4342>(c.z), i8_pair<0x4140>(c.w), i8_pair<0x4342>(c.w));
+          }
+          if (!is_v) {
+            reinterpret_cast<float*>(smem + S::kKsc)[ks * kKeys + key] = reinterpret_cast<const float*>(blk + L::kKs)[tok];
+            reinterpret_cast<float*>(smem + S::kVsc)[ks * kKeys + key] = reinterpret_cast<const float*>(blk + L::kVs)[tok];
           }
           if (!is_v && (key & 63) == 0) s_valid[2 * ks + half] = valid;
           fence_async_smem();
@@ -765,10 +667,9 @@ __global__ void __launch_bounds__(kThreads, 1) tree_wide_kernel(const TreeArgs a
           const uint64_t da = sw128_desc(sk + ks * S::kTile, 0, 1024), db = sw128_desc(sq, 0, 1024);
 #pragma unroll
           for (int k = 0; k < D / 16; ++k) {
-            const int g = S::kGroups == 1 ? 0 : k >> 1;
             const uint32_t oa = ((k >> 2) * (kKeys * 128) + (k & 3) * 32) >> 4;
             const uint32_t ob = ((k >> 2) * (kRows * 128) + (k & 3) * 32) >> 4;
-            mma_ss(tbase + (sb * S::kGroups + g) * kRows, da + oa, db + ob, id_qk, S::kGroups == 1 ? k > 0 : (k & 1) != 0, leader);
+            mma_ss(tbase + sb * kRows, da + oa, db + ob, id_qk, k > 0, leader);
           }
           mma_commit(&bars[B::kSf + sb], leader);
           mma_commit(&bars[B::kKe + ks], leader);
@@ -785,8 +686,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_wide_kernel(const TreeArgs a
         };
         auto now = [&](int bar, uint32_t parity) { return __all_sync(full, mbar_test(&bars[bar], parity)) != 0; };
         ok = wait_all(B::kQf, n_seg & 1);
-        // S runs ahead of P V by one unit (two buffers) or none; whichever is
-        // ready goes first, so that a late K does not hold up a V that waits.
+        // S runs ahead of P V by one unit; whichever is ready goes first, so that a late K does not hold up a V that waits.
         unsigned long long t0 = global_timer_ns();
         for (int x = jt, y = jt; ok && y < jt + n;) {
           bool went = false;
@@ -839,8 +739,7 @@ cudaError_t launch_tree_wide(const TreeArgs& a, cudaStream_t s) {
   };
   switch (a.p.cache.format) {
     case QGEMV_KV_F16: return by_dim(std::integral_constant<int, QGEMV_KV_F16>());
-    case QGEMV_KV_INT8: return by_dim(std::integral_constant<int, QGEMV_KV_INT8>());
-    default: return by_dim(std::integral_constant<int, QGEMV_KV_Q4_0>());
+    default: return by_dim(std::integral_constant<int, QGEMV_KV_INT8>());
   }
 }
 

@@ -15,8 +15,6 @@ of an output, from the roundings that the kernels may make:
     factor e^e, so out by at most 2 e A, with e = 2 * d * 2^-24 * scale *
     |q|.|k| (a sum's worst order, and as much again for the hardware's way of
     adding);
-  * values that a 4-bit cache's group scale multiplies may be rounded to fp16
-    too (`v_rounded`): u * A more;
   * exp2 and fp32 sums: 2^-20 * A, generously.
 """
 import numpy as np
@@ -54,7 +52,7 @@ def quantised(fmt, x):
     return out
 
 
-def attention(q, k, v, see, scale, kind="float16", v_rounded=False):
+def attention(q, k, v, see, scale, kind="float16"):
     """q [n, hq, d], k and v [m, hkv, d] float64, see [n, m] -> out, lse, and the bounds of both."""
     n, hq, d = q.shape
     g = hq // k.shape[1] if k.shape[1] else 1
@@ -75,7 +73,7 @@ def attention(q, k, v, see, scale, kind="float16", v_rounded=False):
             with np.errstate(invalid="ignore"):
                 out[i, h] = p @ vv / l
                 A = p @ np.abs(vv) / l
-                bound[i, h] = (u * 1.01 * np.abs(out[i, h]) + (2.03 if v_rounded else 1.01) * u * A + 2.0 ** -25 * np.abs(vv).sum(0) / l
+                bound[i, h] = (u * 1.01 * np.abs(out[i, h]) + 1.01 * u * A + 2.0 ** -25 * np.abs(vv).sum(0) / l
                                + 2 * e * A + 2.0 ** -20 * A + 2.0 ** -25)
             lse[i, h] = top + np.log(l)
             lse_bound[i, h] = e + 2.0 ** -20 * (1 + abs(lse[i, h]))

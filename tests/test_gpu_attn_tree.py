@@ -90,8 +90,7 @@ class Case:
             for i in range(n):
                 see[i, c:] = [(self.masks[self.cu[b] + i] >> j) & 1 for j in range(n)]
             lo, hi = self.start[b], self.start[b + 1]
-            parts.append(ref.attention(self.q[self.cu[b]:self.cu[b + 1]].astype(np.float64), k[lo:hi], v[lo:hi], see, self.scale,
-                                       v_rounded=self.fmt == "q4_0"))
+            parts.append(ref.attention(self.q[self.cu[b]:self.cu[b + 1]].astype(np.float64), k[lo:hi], v[lo:hi], see, self.scale))
         return [np.concatenate(x) for x in zip(*parts)]
 
     def check(self, name, out, lse):
@@ -201,11 +200,11 @@ def test_missing_pages_are_not_seen(fmt):
     for i in range(3):
         see[i, 100:] = [(c.masks[i] >> j) & 1 for j in range(3)]
     see[:, 32:48] = see[:, 64:80] = False
-    ref.check("missing", out.float().cpu().numpy(), lse.cpu().numpy(), ref.attention(c.q.astype(np.float64), k, v, see, c.scale, v_rounded=fmt == "q4_0"))
+    ref.check("missing", out.float().cpu().numpy(), lse.cpu().numpy(), ref.attention(c.q.astype(np.float64), k, v, see, c.scale))
     c.table = table[:, :2]  # a table that ends before the sequence does
     out, lse = c.run()
     see[:, 32:] = False
-    ref.check("short table", out.float().cpu().numpy(), lse.cpu().numpy(), ref.attention(c.q.astype(np.float64), k, v, see, c.scale, v_rounded=fmt == "q4_0"))
+    ref.check("short table", out.float().cpu().numpy(), lse.cpu().numpy(), ref.attention(c.q.astype(np.float64), k, v, see, c.scale))
 
 
 def test_strides_hints_streams_and_bits():
