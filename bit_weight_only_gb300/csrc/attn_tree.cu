@@ -8,15 +8,20 @@
 // W-th unit:
 //
 //   copy      one bulk copy into the warp's own ring of shared-memory stages
-//   S = Q K^T mma.m16n8k16 on the codes as fp16 (INT8 and Q4_0 codes are
-//             exact), K straight from the block's layout; the scales of the
-//             tokens (Q4_0: of each group, on partial sums) go to S in fp32
+//   S = Q K^T mma.m16n8k16 on the codes as fp16, K straight from the block's
+//             layout: stored bytes and nibbles are fp16 subnormals as they
+//             stand (code + offset, times 2^-24), and the sums start at
+//             -offset times the row's sum of q, so that a code pair costs one
+//             instruction; the scales of the tokens (Q4_0: of each group, on
+//             partial sums) go to S in fp32
 //   softmax   base 2, an own reference m for each warp and row that moves only
 //             when a score passes it by 2^8: without a move no shuffle is
 //             needed.  m is taken over s + log2(scale of v), because what is
 //             rounded to fp16 is p * scale(v), the factor of v's codes: it
 //             stays in [0, 2^8] whatever the scales are
-//   O += P V  the same instruction on V's codes
+//   O += P V  the same instruction on V's codes, exact in fp16 (their offsets are
+//             taken off first: here sums run over all keys, and would not
+//             stay small beside the offsets' share)
 //
 // A warp's O, m and l live in its registers.  At the end of a segment the
 // warps' results are added in warp order through shared memory.
@@ -42,6 +47,12 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint4& a, uint32_t
                : "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b0), "r"(b1));
 }
 
+// c = a . b + z, z for rows g and g + 8
+__device__ __forceinline__ void mma16816_from(float (&c)[4], const uint4& a, uint32_t b0, uint32_t b1, float z0, float z1) {
+  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%11,%11};"
+               : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+               : "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b0), "r"(b1), "f"(z0), "f"(z1));
+}
 // c = a . b
 __device__ __forceinline__ void mma16816_first(float (&c)[4], const uint4& a, uint32_t b0, uint32_t b1) {
   asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
@@ -90,6 +101,7 @@ struct Codes<QGEMV_KV_INT8, D> {
   using L = KvLayout<QGEMV_KV_INT8, D>;
   static constexpr int kKw = D / 16;
   static constexpr int kQ2 = 2;
+  static constexpr uint32_t kOff0 = 0x80808080u, kOff1 = 0x80808080u;  // -128 * 2^-24
   __device__ static int q_at(int ks, int t) { return 64 * (ks >> 2) + 16 * t + 4 * (ks & 3); }
   __device__ static int out_at(int nb, int n) { return D / 8 * n + nb; }
   __device__ static void load_k(const uint8_t* b, int tok, int lane, uint32_t (&w)[kKw]) {
@@ -98,7 +110,7 @@ struct Codes<QGEMV_KV_INT8, D> {
     for (int h = 0; h < D / 64; ++h) *reinterpret_cast<uint4*>(&w[4 * h]) = lds128(b + L::k_off(tok, 64 * h + 16 * t));
   }
   __device__ static void k_frag(const uint32_t (&w)[kKw], int ks, uint32_t& b0, uint32_t& b1) {
-    b0 = i8_pair<0x4140>(w[ks]), b1 = i8_pair<0x4342>(w[ks]);
+    b0 = prmt(w[ks], 0u, 0x4140), b1 = prmt(w[ks], 0u, 0x4342);
   }
   // V: [token][word]
   __device__ static void load_v(const uint8_t* b, int g, int lane, uint32_t (&w)[4 * (D / 32)]) {
@@ -125,6 +137,7 @@ struct Codes<QGEMV_KV_Q4_0, D> {
   using L = KvLayout<QGEMV_KV_Q4_0, D>;
   static constexpr int kKw = D / 32;
   static constexpr int kQ2 = 2;
+  static constexpr uint32_t kOff0 = 0x80088008u, kOff1 = 0x80808080u;  // -8 * 2^-24, and 16 times that
   __device__ static int q_at(int ks, int t) { return 32 * (ks >> 1) + 8 * t + 4 * (ks & 1); }
   __device__ static int out_at(int nb, int n) { return 32 * (nb >> 2) + 4 * n + (nb & 3); }
   __device__ static void load_k(const uint8_t* b, int tok, int lane, uint32_t (&w)[kKw]) {
@@ -133,9 +146,8 @@ struct Codes<QGEMV_KV_Q4_0, D> {
     else *reinterpret_cast<uint2*>(w) = *reinterpret_cast<const uint2*>(at);
   }
   __device__ static void k_frag(const uint32_t (&w)[kKw], int ks, uint32_t& b0, uint32_t& b1) {
-    const uint32_t x = w[ks >> 1];
-    if (ks & 1) b0 = q4_pair<2>(x), b1 = q4_pair<3>(x);
-    else b0 = q4_pair<0>(x), b1 = q4_pair<1>(x);
+    const uint32_t x = ks & 1 ? w[ks >> 1] >> 8 : w[ks >> 1];
+    b0 = x & 0x000F000Fu, b1 = x & 0x00F000F0u;  // the latter times 16: Q's share of it is over 16
   }
   // V: [token][group pair]
   __device__ static void load_v(const uint8_t* b, int g, int lane, uint32_t (&w)[4 * (D / 64)]) {
@@ -185,7 +197,8 @@ struct TreeShape {
   static constexpr int kMerge = kWarps * kRows * D * 4 + kRows * D * 2;  // the warps' O, then the rows as fp16
   static constexpr int kRegion = kRing > kMerge ? kRing : kMerge;
   static constexpr int kQ = kRegion;                            // Q fragments
-  static constexpr int kMl = kQ + MT * (D / 16) * 512;          // m, l of each warp and row
+  static constexpr int kOffs = kQ + MT * (D / 16) * 512;        // Q4_0: the sums' starts, [rows][4]
+  static constexpr int kMl = kOffs + (FMT == QGEMV_KV_Q4_0 ? kRows * 16 : 0);  // m, l of each warp and row
   static constexpr int kMask = kMl + kWarps * kRows * 8;        // mask words of the rows
   static constexpr int kBars = kMask + kRows * 8;
   static constexpr int kBytes = kBars + kWarps * kStages * 8 + 16;
@@ -200,6 +213,7 @@ __global__ void __launch_bounds__(TreeShape<FMT, D, MT>::kThreads, kBlocksPerSm)
   const TreeParams& p = a.p;
   extern __shared__ __align__(128) uint8_t smem[];
   uint4* s_q = reinterpret_cast<uint4*>(smem + Sh::kQ);
+  float* s_offs = reinterpret_cast<float*>(smem + Sh::kOffs);
   float2* s_ml = reinterpret_cast<float2*>(smem + Sh::kMl);
   uint64_t* s_mask = reinterpret_cast<uint64_t*>(smem + Sh::kMask);
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + Sh::kBars);
@@ -215,7 +229,8 @@ __global__ void __launch_bounds__(TreeShape<FMT, D, MT>::kThreads, kBlocksPerSm)
   if (lane < NS) mbar_init(&my_bars[lane], 1);
   fence_mbarrier_init();
   __syncwarp();
-  int n_done = 0;  // units that this warp's ring has taken
+  int ring_at = 0;           // stage of the next unit, and the
+  uint32_t ring_parity = 0;  // parity of its landing
 
   Segment sg;
   while (work.next(a, sg)) {
@@ -227,28 +242,33 @@ __global__ void __launch_bounds__(TreeShape<FMT, D, MT>::kThreads, kBlocksPerSm)
 
     // ---- this warp's units: u0 + warp + W * k
     const int n_mine = static_cast<int>((u1 - u0 - warp + W - 1) / W);
-    int page_of = -1;  // lane l: the page of unit 32 * floor(k / 32) + l
-    uint32_t have = 0;  // stages with a unit whose page exists
-    auto prefetch = [&](int k) {
+    unsigned long long src_of = 0;  // lane l: the block of unit 32 * floor(k / 32) + l, 0 if its page is missing
+    uint32_t have = 0;              // stages with a unit whose page exists
+    auto prefetch = [&](int k, int st) {
       if ((k & 31) == 0) {
         const int64_t u = u0 + warp + static_cast<int64_t>(W) * (k + lane);
         const int64_t pi = (u * kKvBlockTokens) >> a.page_shift;
-        page_of = -1;
-        if (k + lane < n_mine && pi < p.table_stride) page_of = __ldg(p.table + seq * p.table_stride + pi);
-        if (page_of >= p.cache.n_pages) page_of = -1;
+        src_of = 0;
+        if (k + lane < n_mine && pi < p.table_stride) {
+          const int page = __ldg(p.table + seq * p.table_stride + pi);
+          if (page >= 0 && page < p.cache.n_pages)
+            src_of = reinterpret_cast<unsigned long long>(
+                kv_block<FMT, D>(p.cache, page, head, static_cast<int>(u & ((p.cache.page_tokens >> 4) - 1))));
+        }
       }
-      const int page = __shfl_sync(full, page_of, k & 31);
-      const int st = (n_done + k) % NS;
-      have = page >= 0 ? have | 1u << st : have & ~(1u << st);
-      if (page >= 0 && lane == 0) {
-        const int64_t u = u0 + warp + static_cast<int64_t>(W) * k;
-        const int blk = static_cast<int>(u & ((p.cache.page_tokens >> 4) - 1));
-        mbar_arrive_expect_tx(&my_bars[st], L::kBlock);
-        bulk_load(my_ring + st * L::kBlock, kv_block<FMT, D>(p.cache, page, head, blk), L::kBlock, &my_bars[st]);
-      } else if (page < 0 && lane == 0) {
-        mbar_arrive(&my_bars[st]);
+      const unsigned long long src = __shfl_sync(full, src_of, k & 31);
+      have = src ? have | 1u << st : have & ~(1u << st);
+      if (lane == 0) {
+        if (src) {
+          mbar_arrive_expect_tx(&my_bars[st], L::kBlock);
+          bulk_load(my_ring + st * L::kBlock, reinterpret_cast<const void*>(src), L::kBlock, &my_bars[st]);
+        } else {
+          mbar_arrive(&my_bars[st]);
+        }
       }
     };
+    // the ring goes on where the segment before left it
+    auto stage_of = [&](int k) { return (ring_at + k) % NS; };
     // ---- Q fragments and masks of the row tile: loaded ahead of the first
     // copies' page lookups, stored after
     constexpr int kQPer = (MT * KS * 32 + Sh::kThreads - 1) / Sh::kThreads;
@@ -273,14 +293,49 @@ __global__ void __launch_bounds__(TreeShape<FMT, D, MT>::kThreads, kBlocksPerSm)
       const int tok = (row0 + tid) / a.G;
       row_mask = p.masks ? p.masks[q0 + tok] : (~0ull >> (63 - tok));
     }
-    for (int k = 0; k < NS && k < n_mine; ++k) prefetch(k);
+    for (int k = 0; k < NS && k < n_mine; ++k) prefetch(k, stage_of(k));
 #pragma unroll
     for (int x = 0; x < kQPer; ++x)
-      if (tid + x * Sh::kThreads < MT * KS * 32) s_q[tid + x * Sh::kThreads] = qf[x];
+      if (tid + x * Sh::kThreads < MT * KS * 32) {
+        if (FMT == QGEMV_KV_Q4_0) {  // see k_frag
+          qf[x].z = hfma2(qf[x].z, 0x2C002C00u, 0u);
+          qf[x].w = hfma2(qf[x].w, 0x2C002C00u, 0u);
+        }
+        s_q[tid + x * Sh::kThreads] = qf[x];
+      }
     if (tid < Sh::kRows) s_mask[tid] = row_mask;
     __syncthreads();
 
-    const float sl = p.scale * kLog2e;
+    // where the sums of S start: -offset * sum of q, by a product with constants
+    float c_row[MT][4];
+    if constexpr (FMT == QGEMV_KV_INT8) {
+#pragma unroll
+      for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks) {
+          if (ks == 0) mma16816_first(c_row[i], s_q[(i * KS + ks) * 32 + lane], C::kOff0, C::kOff1);
+          else mma16816(c_row[i], s_q[(i * KS + ks) * 32 + lane], C::kOff0, C::kOff1);
+        }
+    } else if constexpr (FMT == QGEMV_KV_Q4_0) {
+      if (warp == 0) {
+#pragma unroll
+        for (int i = 0; i < MT; ++i)
+#pragma unroll
+          for (int grp = 0; grp < D / 32; ++grp) {
+            float c[4];
+            mma16816_first(c, s_q[(i * KS + 2 * grp) * 32 + lane], C::kOff0, C::kOff1);
+            mma16816(c, s_q[(i * KS + 2 * grp + 1) * 32 + lane], C::kOff0, C::kOff1);
+            if (t == 0) {
+              s_offs[(16 * i + g) * 4 + grp] = c[0];
+              s_offs[(16 * i + 8 + g) * 4 + grp] = c[2];
+            }
+          }
+      }
+      __syncthreads();
+    }
+
+    // (codes as subnormals are 2^-24 of their values)
+    const float sl = p.scale * kLog2e * (FMT == QGEMV_KV_F16 ? 1.f : 16777216.f);
     float o[MT][NB][4], m[MT][2], l[MT][2];
 #pragma unroll
     for (int i = 0; i < MT; ++i) {
@@ -293,13 +348,14 @@ __global__ void __launch_bounds__(TreeShape<FMT, D, MT>::kThreads, kBlocksPerSm)
     }
 
     for (int k = 0; k < n_mine; ++k) {
-      const int st = (n_done + k) % NS;
-      const bool landed = mbar_wait_bounded(&my_bars[st], ((n_done + k) / NS) & 1);
+      const int st = ring_at;
+      const bool landed = mbar_wait_bounded(&my_bars[st], ring_parity);
       if (!__all_sync(full, landed)) {
         // Give up: record it, and let the copies in flight land (or their waits
         // run out too) before the ring is used for anything else.
         if (lane == 0) atomicOr(reinterpret_cast<int*>(p.ws), kErrTree);
-        for (int x = k; x < n_mine && x < k + NS; ++x) mbar_wait_bounded(&my_bars[(n_done + x) % NS], ((n_done + x) / NS) & 1);
+        for (int x = 1; x < NS && k + x < n_mine; ++x)
+          mbar_wait_bounded(&my_bars[(st + x) % NS], st + x < NS ? ring_parity : ring_parity ^ 1u);
         break;
       }
       if ((have >> st) & 1) {
@@ -316,6 +372,12 @@ __global__ void __launch_bounds__(TreeShape<FMT, D, MT>::kThreads, kBlocksPerSm)
             // sums of each group, times the tokens' scales of the group
             alignas(16) __half ksc[2][2][D / 32];
             load_scales<D>(blk + L::kKs, t, ksc);
+            float4 offs[MT][2];
+#pragma unroll
+            for (int i = 0; i < MT; ++i) {
+              offs[i][0] = *reinterpret_cast<const float4*>(s_offs + (16 * i + g) * 4);
+              offs[i][1] = *reinterpret_cast<const float4*>(s_offs + (16 * i + 8 + g) * 4);
+            }
 #pragma unroll
             for (int grp = 0; grp < D / 32; ++grp) {
               float part[MT][2][4];
@@ -330,7 +392,7 @@ __global__ void __launch_bounds__(TreeShape<FMT, D, MT>::kThreads, kBlocksPerSm)
                   const uint4 qa = s_q[(i * KS + ks) * 32 + lane];
 #pragma unroll
                   for (int nb = 0; nb < 2; ++nb) {
-                    if (h == 0) mma16816_first(part[i][nb], qa, b[nb][0], b[nb][1]);
+                    if (h == 0) mma16816_from(part[i][nb], qa, b[nb][0], b[nb][1], (&offs[i][0].x)[grp], (&offs[i][1].x)[grp]);
                     else mma16816(part[i][nb], qa, b[nb][0], b[nb][1]);
                   }
                 }
@@ -366,8 +428,9 @@ __global__ void __launch_bounds__(TreeShape<FMT, D, MT>::kThreads, kBlocksPerSm)
                 const uint4 qa = s_q[(i * KS + ks) * 32 + lane];
 #pragma unroll
                 for (int nb = 0; nb < 2; ++nb) {
-                  if (ks == 0) mma16816_first(s[i][nb], qa, b[nb][0], b[nb][1]);
-                  else mma16816(s[i][nb], qa, b[nb][0], b[nb][1]);
+                  if (ks > 0) mma16816(s[i][nb], qa, b[nb][0], b[nb][1]);
+                  else if (FMT == QGEMV_KV_INT8) mma16816_from(s[i][nb], qa, b[nb][0], b[nb][1], c_row[i][0], c_row[i][2]);
+                  else mma16816_first(s[i][nb], qa, b[nb][0], b[nb][1]);
                 }
               }
             }
@@ -461,16 +524,31 @@ __global__ void __launch_bounds__(TreeShape<FMT, D, MT>::kThreads, kBlocksPerSm)
                 s[i][nb][2 * h + e] = x;
               }
           }
-        // p * scale(v), 0 where p is masked whatever the scale holds
+        // p * scale(v).  Where a masked token's scale is infinite or NaN (past the
+        // end it may be anything) the product is 0 all the same.
+        bool odd = false;
+        if (FMT != QGEMV_KV_F16 && edge) {
+#pragma unroll
+          for (int nb = 0; nb < 2; ++nb)
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+#pragma unroll
+              for (int x = 0; x < (FMT == QGEMV_KV_Q4_0 ? D / 32 : 1); ++x) odd |= !(fabsf(vs[nb][e][x]) < INFINITY);
+          odd = __any_sync(full, odd);
+        }
         auto weights = [&](int i, int x) -> uint4 {
           float w[2][4];
 #pragma unroll
           for (int nb = 0; nb < 2; ++nb)
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
-              w[nb][c] = FMT == QGEMV_KV_F16 ? s[i][nb][c] : s[i][nb][c] * vs[nb][c & 1][x];
-              if (FMT != QGEMV_KV_F16 && edge && s[i][nb][c] == 0.f) w[nb][c] = 0.f;
-            }
+            for (int c = 0; c < 4; ++c) w[nb][c] = FMT == QGEMV_KV_F16 ? s[i][nb][c] : s[i][nb][c] * vs[nb][c & 1][x];
+          if (odd) {
+#pragma unroll
+            for (int nb = 0; nb < 2; ++nb)
+#pragma unroll
+              for (int c = 0; c < 4; ++c)
+                if (s[i][nb][c] == 0.f) w[nb][c] = 0.f;
+          }
           return make_uint4(half_pair(w[0][0], w[0][1]), half_pair(w[0][2], w[0][3]), half_pair(w[1][0], w[1][1]),
                             half_pair(w[1][2], w[1][3]));
         };
@@ -562,9 +640,10 @@ __global__ void __launch_bounds__(TreeShape<FMT, D, MT>::kThreads, kBlocksPerSm)
         }
       }
       __syncwarp();
-      if (k + NS < n_mine) prefetch(k + NS);
+      if (k + NS < n_mine) prefetch(k + NS, st);
+      ring_at = st + 1 == NS ? 0 : st + 1;
+      ring_parity ^= st + 1 == NS ? 1u : 0u;
     }
-    n_done += n_mine;
 
     // ---- the warps' results, in warp order
 #pragma unroll
