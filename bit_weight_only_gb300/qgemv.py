@@ -486,12 +486,12 @@ def _dtype_code(dtype) -> int:
 
 def _rows(name, t, heads: int, head_dim: int):
     """(address, token stride, head stride) of a CUDA tensor [n, heads, head_dim], its values contiguous."""
-    if t.shape[1:] != (heads, head_dim) or not t.is_cuda or t.stride(2) != 1:
+    shape, strides = t.shape, t.stride()
+    if len(shape) != 3 or shape[1] != heads or shape[2] != head_dim or strides[2] != 1 or not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor [n, {heads}, {head_dim}] with contiguous values, got "
-                         f"{tuple(t.shape)} with strides {t.stride()} on {t.device}")
-    token, head, _ = t.stride()
+                         f"{tuple(shape)} with strides {strides} on {t.device}")
     # the stride of a dimension of one element means nothing to torch
-    return t.data_ptr(), token if t.shape[0] > 1 else heads * head_dim, head if heads > 1 else head_dim
+    return (t.data_ptr(), strides[0] if shape[0] > 1 else heads * head_dim, strides[1] if heads > 1 else head_dim)
 
 
 def _index(name, t, dtype, shape):
