@@ -19,7 +19,8 @@
 //          (fp16 pages need none: their blocks are copied into place)
 //   V (4)  likewise; in units that hold drafted tokens or end inside, whatever
 //          must not meet a masked row's 0 is taken out of V (below)
-//   copies (bulk, from the pages), ahead of all; MMAs; two that do nothing
+//   copies of K and of V (bulk, from the pages), a warp for each, so that a V
+//          that waits for its product holds up no K; MMAs; one that does nothing
 // INT8 codes are exact in fp16.  fp16 values of drafted tokens may be infinite
 // or NaN, and what lies past the sequence's end is whatever the page holds:
 // both are zeroed in V, and the former noted by (drafted token, d) for the rows
@@ -40,7 +41,7 @@ namespace {
 
 constexpr int kSoft = 4;                            // softmax warpgroups, each of kCols rows of the tile
 constexpr int kConvWarp = 4 * kSoft;                // first of the decoding warps
-constexpr int kLoadWarp = kConvWarp + 8, kMmaWarp = kLoadWarp + 1;
+constexpr int kLoadWarp = kConvWarp + 8, kMmaWarp = kLoadWarp + 1, kLoadVWarp = kLoadWarp + 2;
 constexpr int kThreads = 32 * (kConvWarp + 12);
 constexpr int kRows = 64;
 constexpr int kCols = kRows / kSoft;
@@ -63,7 +64,10 @@ struct Wide {
   static_assert(kF16 || FMT == QGEMV_KV_INT8, "format");
   static constexpr int kTile = kKeys * D * 2;  // a K or V operand
   static constexpr int kKs = kF16 ? 3 : 2, kVs = 2;
-  static constexpr int kHalf = kBlocks / 2 * L::kBlock;  // raw stage: half a unit
+  // raw stages, half a unit of K or V codes each: the codes of a block as they
+  // lie in it, K's with the block's scales after them
+  static constexpr int kRawK = L::kV + L::kBlock - L::kKs, kRawV = L::kV;
+  static constexpr int kHalf = kBlocks / 2 * (kRawK + kRawV);
   static constexpr int kRs = kF16 ? 0 : 3;
   static constexpr int kSBufs = 2;
   // shared memory
@@ -71,7 +75,7 @@ struct Wide {
   static constexpr int kV = kK + kKs * kTile;
   static constexpr int kQ = kV + kVs * kTile;
   static constexpr int kP = kQ + kRows * D * 2;
-  static constexpr int kRaw = kP + kKeys * 128;
+  static constexpr int kRaw = kP + kKeys * 128;  // [kRs] stages of K, then of V
   static constexpr int kKsc = kRaw + kRs * kHalf;          // [kKs][128]
   static constexpr int kVsc = kKsc + (kF16 ? 0 : kKs * kKeys * 4);
   static constexpr int kM = kVsc + (kF16 ? 0 : kKs * kKeys * 4);  // float[64] -m, float[64] factors, float[4][64] x 2
@@ -88,9 +92,9 @@ struct Wide {
   static_assert(kOCol + kRows <= 512, "tensor memory");
 };
 
-// Barriers: index of the first of each kind.
+// Barriers: index of the first of each kind (kRf, kRe: three of K, three of V).
 struct Bars {
-  static constexpr int kRf = 0, kRe = kRf + 5, kKf = kRe + 5, kKe = kKf + 3, kVl = kKe + 3, kVf = kVl + 2, kVe = kVf + 2,
+  static constexpr int kRf = 0, kRe = kRf + 6, kKf = kRe + 6, kKe = kKf + 3, kVl = kKe + 3, kVf = kVl + 2, kVe = kVf + 2,
                        kSf = kVe + 2, kSe = kSf + 2, kPf = kSe + 2, kPv = kPf + 1, kQf = kPv + 1, kDone = kQf + 1;
 };
 
@@ -145,9 +149,9 @@ __global__ void __launch_bounds__(kThreads, 1) tree_wide_kernel(const TreeArgs a
   allow_next_kernel();
 
   if (tid == 0) {
-    for (int i = 0; i < 5; ++i) {
+    for (int i = 0; i < 6; ++i) {
       mbar_init(&bars[B::kRf + i], 1);
-      mbar_init(&bars[B::kRe + i], 128);
+      mbar_init(&bars[B::kRe + i], 64);
     }
     for (int i = 0; i < 3; ++i) {
       mbar_init(&bars[B::kKf + i], S::kF16 ? 1 : 128);
@@ -526,16 +530,16 @@ __global__ void __launch_bounds__(kThreads, 1) tree_wide_kernel(const TreeArgs a
           mbar_arrive(&bars[B::kVf + vst]);
         } else {
           const int64_t rt = 2ll * jt + half;
-          const int rs = static_cast<int>(rt % S::kRs);
-          dead |= !wait(B::kRf + rs, used(rt, S::kRs));
+          const int rs = static_cast<int>(rt % S::kRs), rb = rs + (is_v ? 3 : 0);
+          dead |= !wait(B::kRf + rb, used(rt, S::kRs));
           if (is_v && jt >= S::kVs) dead |= !wait(B::kVe + vst, freed(jt, S::kVs));
           if (!is_v && jt >= S::kKs) dead |= !wait(B::kKe + ks, freed(jt, S::kKs));
           __syncwarp();
           if (is_v && j == 0) start_notes();
           if (left) break;
           const int tok = key & 15;
-          const uint8_t* blk = smem + S::kRaw + rs * S::kHalf + ((key >> 4) & 3) * L::kBlock;
-          const int valid = s_rvalid[rs];
+          const int nb = rs * (kBlocks / 2) + ((key >> 4) & 3);  // block of the ring
+          const uint8_t* blk = is_v ? smem + S::kRaw + S::kRs * (kBlocks / 2) * S::kRawK + nb * S::kRawV : smem + S::kRaw + nb * S::kRawK;
           // 16-byte unit U of the row: chunk U >> 3, swizzled
           auto put = [&](int U, uint32_t w0, uint32_t w1, uint32_t w2, uint32_t w3) {
             *reinterpret_cast<uint4*>(dst + (U >> 3) * (kKeys * 128) + (((U & 7) ^ (key & 7)) << 4)) = make_uint4(w0, w1, w2, w3);
@@ -547,18 +551,18 @@ __global__ void __launch_bounds__(kThreads, 1) tree_wide_kernel(const TreeArgs a
 #pragma unroll
           for (int u = 0; u < N; ++u) {
             const int unit = is_v ? u ^ turn : (u + turn) & (N - 1);
-            const uint4 c = lds128(blk + (is_v ? L::v_off(tok, 16 * unit) : L::k_off(tok, 16 * unit)));
+            const uint4 c = lds128(blk + (is_v ? L::v_off(tok, 16 * unit) - L::kV : L::k_off(tok, 16 * unit)));
             put(2 * unit, i8_pair<0x4140>(c.x), i8_pair<0x4342>(c.x), i8_pair<0x4140>(c.y), i8_pair<0x4342>(c.y));
             put(2 * unit + 1, i8_pair<0x4140>(c.z), i8_pair<0x4342>(c.z), i8_pair<0x4140>(c.w), i8_pair<0x4342>(c.w));
           }
           if (!is_v) {
-            reinterpret_cast<float*>(smem + S::kKsc)[ks * kKeys + key] = reinterpret_cast<const float*>(blk + L::kKs)[tok];
-            reinterpret_cast<float*>(smem + S::kVsc)[ks * kKeys + key] = reinterpret_cast<const float*>(blk + L::kVs)[tok];
+            reinterpret_cast<float*>(smem + S::kKsc)[ks * kKeys + key] = reinterpret_cast<const float*>(blk + L::kV)[tok];
+            reinterpret_cast<float*>(smem + S::kVsc)[ks * kKeys + key] = reinterpret_cast<const float*>(blk + L::kV + L::kVs - L::kKs)[tok];
           }
-          if (!is_v && (key & 63) == 0) s_valid[2 * ks + half] = valid;
+          if (!is_v && (key & 63) == 0) s_valid[2 * ks + half] = s_rvalid[rs];
           fence_async_smem();
           mbar_arrive(&bars[is_v ? B::kVf + vst : B::kKf + ks]);
-          mbar_arrive(&bars[B::kRe + rs]);
+          mbar_arrive(&bars[B::kRe + rb]);
         }
       }
       if (left) break;
@@ -566,11 +570,11 @@ __global__ void __launch_bounds__(kThreads, 1) tree_wide_kernel(const TreeArgs a
     }
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
-    if (warp == kLoadWarp) {
+    if (warp == kLoadWarp || warp == kLoadVWarp) {
       // -------------------------------------------------------- copies ----
-      int64_t n_raw = 0;
-      int issued_k = 0, issued_v = 0;
+      const bool is_v = warp == kLoadVWarp;
       bool ok = true;
+      int n_raw = 0;  // stages filled (half units; fp16: units)
       while (ok && work.next(a, sg)) {
         const int n = static_cast<int>(sg.u1 - sg.u0);
         const int64_t n_pos = static_cast<int64_t>(sg.ctx) + sg.T;
@@ -583,7 +587,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_wide_kernel(const TreeArgs a
           return pg < p.cache.n_pages ? pg : -1;
         };
         int64_t ahead = page_of(0);
-        for (int j = 0; j < n; ++j, ++jt) {
+        for (int j = 0; ok && j < n; ++j) {
           const int64_t page = ahead;
           ahead = page_of(j + 1);
           const int64_t pos = (sg.u0 + j) * kKeys + kKvBlockTokens * (lane & 7);
@@ -591,62 +595,58 @@ __global__ void __launch_bounds__(kThreads, 1) tree_wide_kernel(const TreeArgs a
           const uint8_t* src = page >= 0 ? kv_block<FMT, D>(p.cache, page, sg.head,
                                                             static_cast<int>(pos & (p.cache.page_tokens - 1)) / kKvBlockTokens)
                                          : nullptr;
-          if constexpr (S::kF16) {
-            const int ks = jt % S::kKs, vst = jt % S::kVs;
-            const uint32_t bytes = static_cast<uint32_t>(__popc(valid)) * L::kV;
-            ok = jt < S::kKs || wait(B::kKe + ks, freed(jt, S::kKs));
-            if (!__all_sync(full, ok)) { ok = false; break; }
+          if constexpr (S::kF16) {  // into place
+            const int stages = is_v ? S::kVs : S::kKs, st = n_raw % stages;
+            const int filled = (is_v ? B::kVl : B::kKf) + st;
+            ok = __all_sync(full, n_raw < stages || wait((is_v ? B::kVe : B::kKe) + st, freed(n_raw, stages))) != 0;
+            if (!ok) break;
             if (lane == 0) {
-              s_valid[2 * ks] = static_cast<int>(valid & 15u);
-              s_valid[2 * ks + 1] = static_cast<int>(valid >> 4);
-              mbar_arrive_expect_tx(&bars[B::kKf + ks], bytes);
+              if (is_v) {
+                s_vvalid[st] = static_cast<int>(valid);
+              } else {
+                s_valid[2 * st] = static_cast<int>(valid & 15u);
+                s_valid[2 * st + 1] = static_cast<int>(valid >> 4);
+              }
+              mbar_arrive_expect_tx(&bars[filled], static_cast<uint32_t>(__popc(valid)) * L::kV);
             }
             __syncwarp();
             if (lane < 8 && src) {
+              uint8_t* dst = smem + (is_v ? S::kV : S::kK) + st * S::kTile + lane * 2048;
 #pragma unroll
               for (int c = 0; c < D / 64; ++c)
-                bulk_load(smem + S::kK + ks * S::kTile + c * (kKeys * 128) + lane * 2048, src + c * 2048, 2048, &bars[B::kKf + ks]);
+                bulk_load(dst + c * (kKeys * 128), src + (is_v ? L::kV : 0) + c * 2048, 2048, &bars[filled]);
             }
-            ++issued_k;
-            ok = jt < S::kVs || wait(B::kVe + vst, freed(jt, S::kVs));
-            if (!__all_sync(full, ok)) { ok = false; break; }
-            if (lane == 0) {
-              s_vvalid[vst] = static_cast<int>(valid);
-              mbar_arrive_expect_tx(&bars[B::kVl + vst], bytes);
-            }
-            __syncwarp();
-            if (lane < 8 && src) {
-#pragma unroll
-              for (int c = 0; c < D / 64; ++c)
-                bulk_load(smem + S::kV + vst * S::kTile + c * (kKeys * 128) + lane * 2048, src + L::kV + c * 2048, 2048,
-                          &bars[B::kVl + vst]);
-            }
-            ++issued_v;
+            ++n_raw;
           } else {
             for (int h = 0; h < 2; ++h, ++n_raw) {
-              const int rs = static_cast<int>(n_raw % S::kRs);
-              ok = n_raw < S::kRs || wait(B::kRe + rs, freed(n_raw, S::kRs));
-              if (!__all_sync(full, ok)) { ok = false; break; }
+              const int rs = n_raw % S::kRs, rb = rs + (is_v ? 3 : 0);
+              ok = __all_sync(full, n_raw < S::kRs || wait(B::kRe + rb, freed(n_raw, S::kRs))) != 0;
+              if (!ok) break;
               const unsigned here = (valid >> (4 * h)) & 15u;
               if (lane == 0) {
-                s_rvalid[rs] = static_cast<int>(here);
-                mbar_arrive_expect_tx(&bars[B::kRf + rs], __popc(here) * L::kBlock);
+                if (!is_v) s_rvalid[rs] = static_cast<int>(here);
+                mbar_arrive_expect_tx(&bars[B::kRf + rb], __popc(here) * (is_v ? S::kRawV : S::kRawK));
               }
               __syncwarp();
-              if ((lane >> 2) == h && src)
-                bulk_load(smem + S::kRaw + rs * S::kHalf + (lane & 3) * L::kBlock, src, L::kBlock, &bars[B::kRf + rs]);
+              if ((lane >> 2) == h && src) {
+                const int nb = rs * (kBlocks / 2) + (lane & 3);
+                if (is_v) {
+                  bulk_load(smem + S::kRaw + S::kRs * (kBlocks / 2) * S::kRawK + nb * S::kRawV, src + L::kV, S::kRawV, &bars[B::kRf + rb]);
+                } else {
+                  uint8_t* dst = smem + S::kRaw + nb * S::kRawK;
+                  bulk_load(dst, src, L::kV, &bars[B::kRf + rb]);
+                  bulk_load(dst + L::kV, src + L::kKs, L::kBlock - L::kKs, &bars[B::kRf + rb]);
+                }
+              }
             }
-            if (!ok) break;
           }
         }
       }
       // copies in flight (after an abort) must land before the block ends
-      if constexpr (S::kF16) {
-        for (int n = max(0, issued_k - S::kKs); n < issued_k; ++n) mbar_wait_bounded(&bars[B::kKf + n % S::kKs], used(n, S::kKs));
-        for (int n = max(0, issued_v - S::kVs); n < issued_v; ++n) mbar_wait_bounded(&bars[B::kVl + n % S::kVs], used(n, S::kVs));
-      } else {
-        for (int64_t n = max(static_cast<int64_t>(0), n_raw - S::kRs); n < n_raw; ++n)
-          mbar_wait_bounded(&bars[B::kRf + static_cast<int>(n % S::kRs)], used(n, S::kRs));
+      {
+        const int stages = !S::kF16 ? S::kRs : is_v ? S::kVs : S::kKs;
+        const int filled = !S::kF16 ? B::kRf + (is_v ? 3 : 0) : is_v ? B::kVl : B::kKf;
+        for (int x = max(0, n_raw - stages); x < n_raw; ++x) mbar_wait_bounded(&bars[filled + x % stages], used(x, stages));
       }
     } else if (warp == kMmaWarp) {
       // ---------------------------------------------------------- MMAs ----
