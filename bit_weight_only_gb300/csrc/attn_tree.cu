@@ -47,9 +47,9 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint4& a, uint32_t
                : "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b0), "r"(b1));
 }
 
-// c = a . b + z, z for rows g and g + 8
+// c = a . b + z, z for columns 2 t and 2 t + 1
 __device__ __forceinline__ void mma16816_from(float (&c)[4], const uint4& a, uint32_t b0, uint32_t b1, float z0, float z1) {
-  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%11,%11};"
+  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%11,%10,%11};"
                : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
                : "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b0), "r"(b1), "f"(z0), "f"(z1));
 }
@@ -58,6 +58,13 @@ __device__ __forceinline__ void mma16816_first(float (&c)[4], const uint4& a, ui
   asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
                : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
                : "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b0), "r"(b1), "f"(0.f));
+}
+
+// The transpose of an 8 x 8 matrix of 16-bit values, lane (g, t) holding row g, columns 2t and 2t + 1.
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+  uint32_t y;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
 }
 
 // Per format: words of K and V of a lane, and the fp16 pairs in them.
@@ -173,46 +180,43 @@ struct Codes<QGEMV_KV_Q4_0, D> {
   }
 };
 
-// Q4_0 scales of a lane's tokens 8 nb + 2 t + e of a block, from `at`.
+// Q4_0 scales of a token's groups, from `at`.
 template <int D>
-__device__ __forceinline__ void load_scales(const uint8_t* at, int t, __half (&sc)[2][2][D / 32]) {
-#pragma unroll
-  for (int nb = 0; nb < 2; ++nb) {
-    const uint8_t* src = at + (8 * nb + 2 * t) * (D / 16);
-    if constexpr (D == 128) *reinterpret_cast<uint4*>(&sc[nb][0][0]) = lds128(src);
-    else *reinterpret_cast<uint2*>(&sc[nb][0][0]) = *reinterpret_cast<const uint2*>(src);
-  }
+__device__ __forceinline__ void load_scales(const uint8_t* at, __half2 (&sc)[D / 64]) {
+  if constexpr (D == 128) *reinterpret_cast<uint2*>(sc) = *reinterpret_cast<const uint2*>(at);
+  else *reinterpret_cast<uint32_t*>(sc) = *reinterpret_cast<const uint32_t*>(at);
 }
 
-// Shape of a kernel: W warps, MT tiles of 16 rows.
-template <int FMT, int D, int MT>
+// Shape of a kernel: W warps, NT tiles of 8 rows.
+template <int FMT, int D, int NT>
 struct TreeShape {
   using L = KvLayout<FMT, D>;
-  static constexpr int kWarps = MT == 2 || FMT == QGEMV_KV_F16 ? 4 : 8;
+  static constexpr int kWarps = NT > 2 || FMT == QGEMV_KV_F16 ? 4 : 8;
   static constexpr int kThreads = 32 * kWarps;
-  static constexpr int kRows = 16 * MT;
+  static constexpr int kRows = 8 * NT;
   static constexpr int kFitting = kRingBytes / (kWarps * L::kBlock);
   static constexpr int kStages = kFitting > 6 ? 6 : kFitting;
   static constexpr int kRing = kWarps * kStages * L::kBlock;
-  static constexpr int kMerge = kWarps * kRows * D * 4 + kRows * D * 2;  // the warps' O, then the rows as fp16
+  static constexpr int kPitch = D + 4;  // of a row of the warps' O: four rows' stores meet no bank twice
+  static constexpr int kMerge = kWarps * kRows * kPitch * 4 + kRows * D * 2;  // the warps' O, then the rows as fp16
   static constexpr int kRegion = kRing > kMerge ? kRing : kMerge;
-  static constexpr int kQ = kRegion;                            // Q fragments
-  static constexpr int kOffs = kQ + MT * (D / 16) * 512;        // Q4_0: the sums' starts, [rows][4]
-  static constexpr int kMl = kOffs + (FMT == QGEMV_KV_Q4_0 ? kRows * 16 : 0);  // m, l of each warp and row
+  static constexpr int kQ = (kRegion + 127) / 128 * 128;        // Q fragments
+  static constexpr int kOffs = kQ + NT * (D / 16) * 256;        // the sums' starts, [group, INT8: all][row]
+  static constexpr int kMl = kOffs + kRows * (FMT == QGEMV_KV_Q4_0 ? 16 : FMT == QGEMV_KV_INT8 ? 4 : 0);  // m, l of each warp and row
   static constexpr int kMask = kMl + kWarps * kRows * 8;        // mask words of the rows
   static constexpr int kBars = kMask + kRows * 8;
   static constexpr int kBytes = kBars + kWarps * kStages * 8 + 16;
 };
 
-template <int FMT, int D, int MT>
-__global__ void __launch_bounds__(TreeShape<FMT, D, MT>::kThreads, kBlocksPerSm) tree_kernel(const TreeArgs a) {
-  using Sh = TreeShape<FMT, D, MT>;
+template <int FMT, int D, int NT>
+__global__ void __launch_bounds__(TreeShape<FMT, D, NT>::kThreads, kBlocksPerSm) tree_kernel(const TreeArgs a) {
+  using Sh = TreeShape<FMT, D, NT>;
   using L = KvLayout<FMT, D>;
   using C = Codes<FMT, D>;
-  constexpr int W = Sh::kWarps, NS = Sh::kStages, KS = D / 16, NB = D / 8;
+  constexpr int W = Sh::kWarps, NS = Sh::kStages, KS = D / 16, MB = D / 16;
   const TreeParams& p = a.p;
   extern __shared__ __align__(128) uint8_t smem[];
-  uint4* s_q = reinterpret_cast<uint4*>(smem + Sh::kQ);
+  uint4* s_q = reinterpret_cast<uint4*>(smem + Sh::kQ);  // [8 rows][two steps of k][lane]
   float* s_offs = reinterpret_cast<float*>(smem + Sh::kOffs);
   float2* s_ml = reinterpret_cast<float2*>(smem + Sh::kMl);
   uint64_t* s_mask = reinterpret_cast<uint64_t*>(smem + Sh::kMask);
@@ -271,22 +275,21 @@ __global__ void __launch_bounds__(TreeShape<FMT, D, MT>::kThreads, kBlocksPerSm)
     auto stage_of = [&](int k) { return (ring_at + k) % NS; };
     // ---- Q fragments and masks of the row tile: loaded ahead of the first
     // copies' page lookups, stored after
-    constexpr int kQPer = (MT * KS * 32 + Sh::kThreads - 1) / Sh::kThreads;
+    constexpr int kQAll = NT * KS / 2 * 32, kQPer = (kQAll + Sh::kThreads - 1) / Sh::kThreads;
     uint4 qf[kQPer];
 #pragma unroll
     for (int x = 0; x < kQPer; ++x) {
       const int i = tid + x * Sh::kThreads;
-      const int ln = i & 31, ks = (i >> 5) % KS, mt = i / (32 * KS);
-      const int d = C::q_at(ks, ln & 3);
-      auto row_q = [&](int r) -> uint2 {
-        if (r >= R || mt >= MT) return make_uint2(0u, 0u);
+      const int ln = i & 31, ks = 2 * ((i >> 5) % (KS / 2)), r = row0 + 8 * (i / (16 * KS)) + (ln >> 2);
+      qf[x] = make_uint4(0u, 0u, 0u, 0u);
+      if (r < R && i < kQAll) {
         const int tok = r / a.G;
         const __half* q = static_cast<const __half*>(p.q.ptr) + (q0 + tok) * p.q.token_stride +
                           (head * a.G + r - tok * a.G) * p.q.head_stride;
-        return make_uint2(__ldg(reinterpret_cast<const unsigned*>(q + d)), __ldg(reinterpret_cast<const unsigned*>(q + d + C::kQ2)));
-      };
-      const uint2 lo = row_q(row0 + 16 * mt + (ln >> 2)), hi = row_q(row0 + 16 * mt + (ln >> 2) + 8);
-      qf[x] = make_uint4(lo.x, hi.x, lo.y, hi.y);
+        auto at = [&](int d) { return __ldg(reinterpret_cast<const unsigned*>(q + d)); };
+        const int d0 = C::q_at(ks, ln & 3), d1 = C::q_at(ks + 1, ln & 3);
+        qf[x] = make_uint4(at(d0), at(d0 + C::kQ2), at(d1), at(d1 + C::kQ2));
+      }
     }
     uint64_t row_mask = 0;
     if (tid < Sh::kRows && row0 + tid < R) {
@@ -296,9 +299,9 @@ __global__ void __launch_bounds__(TreeShape<FMT, D, MT>::kThreads, kBlocksPerSm)
     for (int k = 0; k < NS && k < n_mine; ++k) prefetch(k, stage_of(k));
 #pragma unroll
     for (int x = 0; x < kQPer; ++x)
-      if (tid + x * Sh::kThreads < MT * KS * 32) {
+      if (tid + x * Sh::kThreads < kQAll) {
         if (FMT == QGEMV_KV_Q4_0) {  // see k_frag
-          qf[x].z = hfma2(qf[x].z, 0x2C002C00u, 0u);
+          qf[x].y = hfma2(qf[x].y, 0x2C002C00u, 0u);
           qf[x].w = hfma2(qf[x].w, 0x2C002C00u, 0u);
         }
         s_q[tid + x * Sh::kThreads] = qf[x];
@@ -307,40 +310,34 @@ __global__ void __launch_bounds__(TreeShape<FMT, D, MT>::kThreads, kBlocksPerSm)
     __syncthreads();
 
     // where the sums of S start: -offset * sum of q, by a product with constants
-    float c_row[MT][4];
-    if constexpr (FMT == QGEMV_KV_INT8) {
-#pragma unroll
-      for (int i = 0; i < MT; ++i)
-#pragma unroll
-        for (int ks = 0; ks < KS; ++ks) {
-          if (ks == 0) mma16816_first(c_row[i], s_q[(i * KS + ks) * 32 + lane], C::kOff0, C::kOff1);
-          else mma16816(c_row[i], s_q[(i * KS + ks) * 32 + lane], C::kOff0, C::kOff1);
-        }
-    } else if constexpr (FMT == QGEMV_KV_Q4_0) {
+    if constexpr (FMT != QGEMV_KV_F16) {
       if (warp == 0) {
+        const uint4 off = make_uint4(C::kOff0, C::kOff0, C::kOff1, C::kOff1);
 #pragma unroll
-        for (int i = 0; i < MT; ++i)
+        for (int i = 0; i < NT; ++i) {
+          float c[4];
 #pragma unroll
-          for (int grp = 0; grp < D / 32; ++grp) {
-            float c[4];
-            mma16816_first(c, s_q[(i * KS + 2 * grp) * 32 + lane], C::kOff0, C::kOff1);
-            mma16816(c, s_q[(i * KS + 2 * grp + 1) * 32 + lane], C::kOff0, C::kOff1);
-            if (t == 0) {
-              s_offs[(16 * i + g) * 4 + grp] = c[0];
-              s_offs[(16 * i + 8 + g) * 4 + grp] = c[2];
-            }
+          for (int kp = 0; kp < KS / 2; ++kp) {
+            const uint4 qb = s_q[(i * (KS / 2) + kp) * 32 + lane];
+            if (kp == 0 || FMT == QGEMV_KV_Q4_0) mma16816_first(c, off, qb.x, qb.y);
+            else mma16816(c, off, qb.x, qb.y);
+            mma16816(c, off, qb.z, qb.w);
+            const int grp = FMT == QGEMV_KV_Q4_0 ? kp : 0;
+            if (g == 0 && (FMT == QGEMV_KV_Q4_0 || kp == KS / 2 - 1))
+              *reinterpret_cast<float2*>(s_offs + grp * Sh::kRows + 8 * i + 2 * t) = make_float2(c[0], c[1]);
           }
+        }
       }
       __syncthreads();
     }
 
     // (codes as subnormals are 2^-24 of their values)
     const float sl = p.scale * kLog2e * (FMT == QGEMV_KV_F16 ? 1.f : 16777216.f);
-    float o[MT][NB][4], m[MT][2], l[MT][2];
+    float o[NT][MB][4], m[NT][2], l[NT][2];  // values 16 b + g, + 8; rows 2t and 2t + 1 of each tile
 #pragma unroll
-    for (int i = 0; i < MT; ++i) {
+    for (int i = 0; i < NT; ++i) {
 #pragma unroll
-      for (int n = 0; n < NB; ++n)
+      for (int n = 0; n < MB; ++n)
 #pragma unroll
         for (int c = 0; c < 4; ++c) o[i][n][c] = 0.f;
       m[i][0] = m[i][1] = -INFINITY;
@@ -362,217 +359,184 @@ __global__ void __launch_bounds__(TreeShape<FMT, D, MT>::kThreads, kBlocksPerSm)
         const uint8_t* blk = my_ring + st * L::kBlock;
         const int64_t pos0 = (u0 + warp + static_cast<int64_t>(W) * k) * kKvBlockTokens;
         const bool edge = pos0 + kKvBlockTokens > ctx;  // some positions are drafted, or past the end
-        // ---- S
-        float s[MT][2][4];
+        // ---- S: tokens g and g + 8 of the block, rows 2t and 2t + 1 of each tile
+        float s[NT][4];
         {
           uint32_t kw[2][C::kKw];
           C::load_k(blk, g, lane, kw[0]);
           C::load_k(blk, 8 + g, lane, kw[1]);
+          auto k_codes = [&](int ks) {
+            uint4 r;
+            C::k_frag(kw[0], ks, r.x, r.z);
+            C::k_frag(kw[1], ks, r.y, r.w);
+            return r;
+          };
           if constexpr (FMT == QGEMV_KV_Q4_0) {
             // sums of each group, times the tokens' scales of the group
-            alignas(16) __half ksc[2][2][D / 32];
-            load_scales<D>(blk + L::kKs, t, ksc);
-            float4 offs[MT][2];
-#pragma unroll
-            for (int i = 0; i < MT; ++i) {
-              offs[i][0] = *reinterpret_cast<const float4*>(s_offs + (16 * i + g) * 4);
-              offs[i][1] = *reinterpret_cast<const float4*>(s_offs + (16 * i + 8 + g) * 4);
-            }
+            alignas(8) __half2 ksc[2][D / 64];
+            load_scales<D>(blk + L::kKs + g * (D / 16), ksc[0]);
+            load_scales<D>(blk + L::kKs + (8 + g) * (D / 16), ksc[1]);
 #pragma unroll
             for (int grp = 0; grp < D / 32; ++grp) {
-              float part[MT][2][4];
+              const uint4 k0 = k_codes(2 * grp), k1 = k_codes(2 * grp + 1);
+              const float f0 = grp & 1 ? __high2float(ksc[0][grp >> 1]) : __low2float(ksc[0][grp >> 1]);
+              const float f1 = grp & 1 ? __high2float(ksc[1][grp >> 1]) : __low2float(ksc[1][grp >> 1]);
 #pragma unroll
-              for (int h = 0; h < 2; ++h) {
-                const int ks = 2 * grp + h;
-                uint32_t b[2][2];
-                C::k_frag(kw[0], ks, b[0][0], b[0][1]);
-                C::k_frag(kw[1], ks, b[1][0], b[1][1]);
+              for (int i = 0; i < NT; ++i) {
+                const uint4 qb = s_q[(i * (KS / 2) + grp) * 32 + lane];
+                float part[4];
+                const float2 from = *reinterpret_cast<const float2*>(s_offs + grp * Sh::kRows + 8 * i + 2 * t);
+                mma16816_from(part, k0, qb.x, qb.y, from.x, from.y);
+                mma16816(part, k1, qb.z, qb.w);
 #pragma unroll
-                for (int i = 0; i < MT; ++i) {
-                  const uint4 qa = s_q[(i * KS + ks) * 32 + lane];
-#pragma unroll
-                  for (int nb = 0; nb < 2; ++nb) {
-                    if (h == 0) mma16816_from(part[i][nb], qa, b[nb][0], b[nb][1], (&offs[i][0].x)[grp], (&offs[i][1].x)[grp]);
-                    else mma16816(part[i][nb], qa, b[nb][0], b[nb][1]);
-                  }
+                for (int h = 0; h < 2; ++h) {
+                  const uint64_t x = pack2(part[2 * h], part[2 * h + 1]), f = h ? pack2(f1, f1) : pack2(f0, f0);
+                  unpack2(grp == 0 ? mul2(x, f) : fma2(x, f, pack2(s[i][2 * h], s[i][2 * h + 1])), s[i][2 * h], s[i][2 * h + 1]);
                 }
               }
-#pragma unroll
-              for (int nb = 0; nb < 2; ++nb)
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                  const float f = __half2float(ksc[nb][e][grp]);
-#pragma unroll
-                  for (int i = 0; i < MT; ++i)
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                      float& x = s[i][nb][2 * h + e];
-                      x = grp == 0 ? part[i][nb][2 * h + e] * f : fmaf(part[i][nb][2 * h + e], f, x);
-                    }
-                }
             }
 #pragma unroll
-            for (int i = 0; i < MT; ++i)
+            for (int i = 0; i < NT; ++i)
 #pragma unroll
-              for (int nb = 0; nb < 2; ++nb)
-#pragma unroll
-                for (int c = 0; c < 4; ++c) s[i][nb][c] *= sl;
+              for (int c = 0; c < 4; ++c) s[i][c] *= sl;
           } else {
 #pragma unroll
-            for (int ks = 0; ks < KS; ++ks) {
-              uint32_t b[2][2];
-              C::k_frag(kw[0], ks, b[0][0], b[0][1]);
-              C::k_frag(kw[1], ks, b[1][0], b[1][1]);
+            for (int kp = 0; kp < KS / 2; ++kp) {
+              const uint4 k0 = k_codes(2 * kp), k1 = k_codes(2 * kp + 1);
 #pragma unroll
-              for (int i = 0; i < MT; ++i) {
-                const uint4 qa = s_q[(i * KS + ks) * 32 + lane];
-#pragma unroll
-                for (int nb = 0; nb < 2; ++nb) {
-                  if (ks > 0) mma16816(s[i][nb], qa, b[nb][0], b[nb][1]);
-                  else if (FMT == QGEMV_KV_INT8) mma16816_from(s[i][nb], qa, b[nb][0], b[nb][1], c_row[i][0], c_row[i][2]);
-                  else mma16816_first(s[i][nb], qa, b[nb][0], b[nb][1]);
+              for (int i = 0; i < NT; ++i) {
+                const uint4 qb = s_q[(i * (KS / 2) + kp) * 32 + lane];
+                if (kp > 0) {
+                  mma16816(s[i], k0, qb.x, qb.y);
+                } else if (FMT == QGEMV_KV_INT8) {
+                  const float2 from = *reinterpret_cast<const float2*>(s_offs + 8 * i + 2 * t);
+                  mma16816_from(s[i], k0, qb.x, qb.y, from.x, from.y);
+                } else {
+                  mma16816_first(s[i], k0, qb.x, qb.y);
                 }
+                mma16816(s[i], k1, qb.z, qb.w);
               }
             }
 #pragma unroll
-            for (int nb = 0; nb < 2; ++nb) {
-              float2 ksc = make_float2(1.f, 1.f);
-              if constexpr (FMT == QGEMV_KV_INT8) ksc = *reinterpret_cast<const float2*>(blk + L::kKs + 4 * (8 * nb + 2 * t));
-              ksc.x *= sl, ksc.y *= sl;
+            for (int h = 0; h < 2; ++h) {
+              float ksc = sl;
+              if constexpr (FMT == QGEMV_KV_INT8) ksc *= *reinterpret_cast<const float*>(blk + L::kKs + 4 * (8 * h + g));
 #pragma unroll
-              for (int i = 0; i < MT; ++i) s[i][nb][0] *= ksc.x, s[i][nb][1] *= ksc.y, s[i][nb][2] *= ksc.x, s[i][nb][3] *= ksc.y;
+              for (int i = 0; i < NT; ++i) s[i][2 * h] *= ksc, s[i][2 * h + 1] *= ksc;
             }
           }
         }
         if (edge) {
 #pragma unroll
-          for (int i = 0; i < MT; ++i)
+          for (int i = 0; i < NT; ++i)
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
-              const uint64_t mask = s_mask[16 * i + g + 8 * (c >> 1)];
-#pragma unroll
-              for (int nb = 0; nb < 2; ++nb) {
-                const int64_t pos = pos0 + 8 * nb + 2 * t + (c & 1);
-                const bool on = pos < ctx || (pos < all && ((mask >> (pos - ctx)) & 1));
-                if (!on) s[i][nb][c] = -INFINITY;
-              }
+              const int64_t pos = pos0 + g + 8 * (c >> 1);
+              const bool on = pos < ctx || (pos < all && ((s_mask[8 * i + 2 * t + (c & 1)] >> (pos - ctx)) & 1));
+              if (!on) s[i][c] = -INFINITY;
             }
         }
         // ---- scales of V and the reference
-        float vs[2][2][FMT == QGEMV_KV_Q4_0 ? D / 32 : 1], lv[2][2];
-        if constexpr (FMT == QGEMV_KV_Q4_0) {
-          alignas(16) __half vsc[2][2][D / 32];
-          load_scales<D>(blk + L::kVs, t, vsc);
+        float vs[2][FMT == QGEMV_KV_Q4_0 ? D / 32 : 1], lv[2];
 #pragma unroll
-          for (int nb = 0; nb < 2; ++nb)
+        for (int h = 0; h < 2; ++h) {
+          if constexpr (FMT == QGEMV_KV_Q4_0) {
+            alignas(8) __half2 vsc[D / 64];
+            load_scales<D>(blk + L::kVs + (8 * h + g) * (D / 16), vsc);
+            __half2 top = __habs2(vsc[0]);
+            if constexpr (D == 128) top = __hmax2(top, __habs2(vsc[1]));
+            lv[h] = lg2(fmaxf(fmaxf(__low2float(top), __high2float(top)), 7.9e-31f));  // 2^-100
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              float top = 7.9e-31f;  // 2^-100
-#pragma unroll
-              for (int x = 0; x < D / 32; ++x) {
-                vs[nb][e][x] = __half2float(vsc[nb][e][x]);
-                top = fmaxf(top, fabsf(vs[nb][e][x]));
-              }
-              lv[nb][e] = lg2(top);
-            }
-        } else {
-#pragma unroll
-          for (int nb = 0; nb < 2; ++nb) {
-            float2 v = make_float2(1.f, 1.f);
-            if constexpr (FMT == QGEMV_KV_INT8) v = *reinterpret_cast<const float2*>(blk + L::kVs + 4 * (8 * nb + 2 * t));
-            vs[nb][0][0] = v.x, vs[nb][1][0] = v.y;
-            lv[nb][0] = FMT == QGEMV_KV_F16 ? 0.f : lg2(fmaxf(v.x, 7.9e-31f));
-            lv[nb][1] = FMT == QGEMV_KV_F16 ? 0.f : lg2(fmaxf(v.y, 7.9e-31f));
+            for (int x = 0; x < D / 32; ++x) vs[h][x] = x & 1 ? __high2float(vsc[x >> 1]) : __low2float(vsc[x >> 1]);
+          } else if constexpr (FMT == QGEMV_KV_INT8) {
+            vs[h][0] = *reinterpret_cast<const float*>(blk + L::kVs + 4 * (8 * h + g));
+            lv[h] = lg2(fmaxf(vs[h][0], 7.9e-31f));
+          } else {
+            vs[h][0] = 1.f;
+            lv[h] = 0.f;
           }
         }
         bool grow = false;
 #pragma unroll
-        for (int i = 0; i < MT; ++i)
+        for (int i = 0; i < NT; ++i)
 #pragma unroll
-          for (int nb = 0; nb < 2; ++nb)
-#pragma unroll
-            for (int c = 0; c < 4; ++c) grow |= s[i][nb][c] + lv[nb][c & 1] > m[i][c >> 1] + kLazyT;
+          for (int c = 0; c < 4; ++c) grow |= s[i][c] + lv[c >> 1] > m[i][c & 1] + kLazyT;
         if (__any_sync(full, grow)) {
 #pragma unroll
-          for (int i = 0; i < MT; ++i)
+          for (int i = 0; i < NT; ++i)
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-              float top = fmaxf(fmaxf(s[i][0][2 * h] + lv[0][0], s[i][0][2 * h + 1] + lv[0][1]),
-                                fmaxf(s[i][1][2 * h] + lv[1][0], s[i][1][2 * h + 1] + lv[1][1]));
-              top = fmaxf(top, __shfl_xor_sync(full, top, 1));
-              top = fmaxf(top, __shfl_xor_sync(full, top, 2));
+              float top = fmaxf(s[i][h] + lv[0], s[i][2 + h] + lv[1]);
+#pragma unroll
+              for (int x = 4; x < 32; x *= 2) top = fmaxf(top, __shfl_xor_sync(full, top, x));
               const float mn = fmaxf(m[i][h], top);
               const float f = m[i][h] == -INFINITY ? 0.f : ex2(m[i][h] - mn);
               m[i][h] = mn;
               l[i][h] *= f;
 #pragma unroll
-              for (int n = 0; n < NB; ++n) o[i][n][2 * h] *= f, o[i][n][2 * h + 1] *= f;
+              for (int n = 0; n < MB; ++n) o[i][n][h] *= f, o[i][n][2 + h] *= f;
             }
         }
         // ---- P (in place of S); l takes p itself
 #pragma unroll
-        for (int i = 0; i < MT; ++i)
+        for (int i = 0; i < NT; ++i)
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const float ref = m[i][h] == -INFINITY ? 0.f : m[i][h];
-#pragma unroll
-            for (int nb = 0; nb < 2; ++nb)
-#pragma unroll
-              for (int e = 0; e < 2; ++e) {
-                const float x = ex2(s[i][nb][2 * h + e] - ref);
-                l[i][h] += x;
-                s[i][nb][2 * h + e] = x;
-              }
+          for (int c = 0; c < 4; ++c) {
+            const float ref = m[i][c & 1] == -INFINITY ? 0.f : m[i][c & 1];
+            s[i][c] = ex2(s[i][c] - ref);
+            l[i][c & 1] += s[i][c];
           }
         // p * scale(v).  Where a masked token's scale is infinite or NaN (past the
         // end it may be anything) the product is 0 all the same.
         bool odd = false;
         if (FMT != QGEMV_KV_F16 && edge) {
 #pragma unroll
-          for (int nb = 0; nb < 2; ++nb)
+          for (int h = 0; h < 2; ++h)
 #pragma unroll
-            for (int e = 0; e < 2; ++e)
-#pragma unroll
-              for (int x = 0; x < (FMT == QGEMV_KV_Q4_0 ? D / 32 : 1); ++x) odd |= !(fabsf(vs[nb][e][x]) < INFINITY);
+            for (int x = 0; x < (FMT == QGEMV_KV_Q4_0 ? D / 32 : 1); ++x) odd |= !(fabsf(vs[h][x]) < INFINITY);
           odd = __any_sync(full, odd);
         }
-        auto weights = [&](int i, int x) -> uint4 {
-          float w[2][4];
+        // as the second operand: lane (g, t) row g, tokens 2t, 2t + 1 and 8 more
+        auto weights = [&](int i, int x) -> uint2 {
+          float w[4];
 #pragma unroll
-          for (int nb = 0; nb < 2; ++nb)
-#pragma unroll
-            for (int c = 0; c < 4; ++c) w[nb][c] = FMT == QGEMV_KV_F16 ? s[i][nb][c] : s[i][nb][c] * vs[nb][c & 1][x];
+          for (int h = 0; h < 2; ++h) {
+            uint64_t pp = pack2(s[i][2 * h], s[i][2 * h + 1]);
+            if (FMT != QGEMV_KV_F16) pp = mul2(pp, pack2(vs[h][x], vs[h][x]));
+            unpack2(pp, w[2 * h], w[2 * h + 1]);
+          }
           if (odd) {
 #pragma unroll
-            for (int nb = 0; nb < 2; ++nb)
-#pragma unroll
-              for (int c = 0; c < 4; ++c)
-                if (s[i][nb][c] == 0.f) w[nb][c] = 0.f;
+            for (int c = 0; c < 4; ++c)
+              if (s[i][c] == 0.f) w[c] = 0.f;
           }
-          return make_uint4(half_pair(w[0][0], w[0][1]), half_pair(w[0][2], w[0][3]), half_pair(w[1][0], w[1][1]),
-                            half_pair(w[1][2], w[1][3]));
+          return make_uint2(transpose8(half_pair(w[0], w[1])), transpose8(half_pair(w[2], w[3])));
         };
-        // ---- O
+        // ---- O, its values the rows of the product
         uint32_t vw[4 * L::kRow / 32];
         C::load_v(blk, g, lane, vw);
+        auto v_codes = [&](int n) {
+          uint4 r;
+          C::v_frag(vw, 2 * n, r.x, r.z);
+          C::v_frag(vw, 2 * n + 1, r.y, r.w);
+          return r;
+        };
+        uint2 pb[NT];
         if constexpr (FMT == QGEMV_KV_Q4_0) {
 #pragma unroll
           for (int grp = 0; grp < D / 32; ++grp) {
-            uint4 pa[MT];
 #pragma unroll
-            for (int i = 0; i < MT; ++i) pa[i] = weights(i, grp);
+            for (int i = 0; i < NT; ++i) pb[i] = weights(i, grp);
 #pragma unroll
-            for (int n = 0; n < 4; ++n) {
-              uint32_t b0, b1;
-              C::v_frag(vw, 4 * grp + n, b0, b1);
+            for (int n = 0; n < 2; ++n) {
+              const uint4 v = v_codes(2 * grp + n);
 #pragma unroll
-              for (int i = 0; i < MT; ++i) mma16816(o[i][4 * grp + n], pa[i], b0, b1);
+              for (int i = 0; i < NT; ++i) mma16816(o[i][2 * grp + n], v, pb[i].x, pb[i].y);
             }
           }
         } else {
-          uint4 pa[MT];
 #pragma unroll
-          for (int i = 0; i < MT; ++i) pa[i] = weights(i, 0);
+          for (int i = 0; i < NT; ++i) pb[i] = weights(i, 0);
           if (FMT == QGEMV_KV_F16 && edge) {
             // fp16 values of positions past the end are whatever the page
             // holds: zero.  Infinities and NaN of drafted tokens reach the rows
@@ -580,13 +544,11 @@ __global__ void __launch_bounds__(TreeShape<FMT, D, MT>::kThreads, kBlocksPerSm)
             const uint32_t k01 = (pos0 + 2 * t < all ? 0xffffu : 0u) | (pos0 + 2 * t + 1 < all ? 0xffff0000u : 0u);
             const uint32_t k23 = (pos0 + 2 * t + 8 < all ? 0xffffu : 0u) | (pos0 + 2 * t + 9 < all ? 0xffff0000u : 0u);
 #pragma unroll
-            for (int n = 0; n < NB; ++n) {
-              uint32_t b0, b1;
-              C::v_frag(vw, n, b0, b1);
-              b0 &= k01, b1 &= k23;
-              const uint32_t bad0 = ((b0 & 0x7C007C00u) + 0x04000400u) & 0x80008000u;
-              const uint32_t bad1 = ((b1 & 0x7C007C00u) + 0x04000400u) & 0x80008000u;
-              if (__any_sync(full, (bad0 | bad1) != 0)) {
+            for (int n = 0; n < MB; ++n) {
+              uint4 v = v_codes(n);
+              v.x &= k01, v.y &= k01, v.z &= k23, v.w &= k23;
+              auto bad = [](uint32_t x) { return ((x & 0x7C007C00u) + 0x04000400u) & 0x80008000u; };
+              if (__any_sync(full, (bad(v.x) | bad(v.y) | bad(v.z) | bad(v.w)) != 0)) {
                 for (int kind = 0; kind < 3; ++kind) {  // NaN, +inf, -inf
                   auto is = [&](uint32_t b) {
                     uint32_t r = 0;
@@ -598,43 +560,42 @@ __global__ void __launch_bounds__(TreeShape<FMT, D, MT>::kThreads, kBlocksPerSm)
                     }
                     return r;
                   };
-                  const uint32_t c0 = is(b0), c1 = is(b1);
+                  const uint4 which = make_uint4(is(v.x), is(v.y), is(v.z), is(v.w));
 #pragma unroll
-                  for (int i = 0; i < MT; ++i) {
-                    auto sees = [&](int nb, int h) {
+                  for (int i = 0; i < NT; ++i) {
+                    auto sees = [&](int nb) {
                       uint32_t r = 0;
 #pragma unroll
                       for (int e = 0; e < 2; ++e) {
                         const int64_t pos = pos0 + 8 * nb + 2 * t + e;
-                        const uint64_t mask = s_mask[16 * i + g + 8 * h];
-                        if (pos < ctx || (pos < all && ((mask >> (pos - ctx)) & 1))) r |= 0x3C00u << (16 * e);
+                        if (pos < ctx || (pos < all && ((s_mask[8 * i + g] >> (pos - ctx)) & 1))) r |= 0x3C00u << (16 * e);
                       }
                       return r;
                     };
-                    const uint4 va = make_uint4(sees(0, 0), sees(0, 1), sees(1, 0), sees(1, 1));
-                    float cnt[4] = {0.f, 0.f, 0.f, 0.f};
-                    mma16816(cnt, va, c0, c1);
+                    float cnt[4];
+                    mma16816_first(cnt, which, sees(0), sees(1));
                     const float val = __int_as_float(kind == 0 ? 0x7fffffff : kind == 1 ? 0x7f800000 : 0xff800000);
 #pragma unroll
                     for (int c = 0; c < 4; ++c)
                       if (cnt[c] > 0.f) o[i][n][c] += val;
                   }
                 }
-                if (bad0 & 0x8000u) b0 &= 0xffff0000u;
-                if (bad0 & 0x80000000u) b0 &= 0xffffu;
-                if (bad1 & 0x8000u) b1 &= 0xffff0000u;
-                if (bad1 & 0x80000000u) b1 &= 0xffffu;
+                auto finite = [&](uint32_t x) {
+                  if (bad(x) & 0x8000u) x &= 0xffff0000u;
+                  if (bad(x) & 0x80000000u) x &= 0xffffu;
+                  return x;
+                };
+                v = make_uint4(finite(v.x), finite(v.y), finite(v.z), finite(v.w));
               }
 #pragma unroll
-              for (int i = 0; i < MT; ++i) mma16816(o[i][n], pa[i], b0, b1);
+              for (int i = 0; i < NT; ++i) mma16816(o[i][n], v, pb[i].x, pb[i].y);
             }
           } else {
 #pragma unroll
-            for (int n = 0; n < NB; ++n) {
-              uint32_t b0, b1;
-              C::v_frag(vw, n, b0, b1);
+            for (int n = 0; n < MB; ++n) {
+              const uint4 v = v_codes(n);
 #pragma unroll
-              for (int i = 0; i < MT; ++i) mma16816(o[i][n], pa[i], b0, b1);
+              for (int i = 0; i < NT; ++i) mma16816(o[i][n], v, pb[i].x, pb[i].y);
             }
           }
         }
@@ -647,36 +608,30 @@ __global__ void __launch_bounds__(TreeShape<FMT, D, MT>::kThreads, kBlocksPerSm)
 
     // ---- the warps' results, in warp order
 #pragma unroll
-    for (int i = 0; i < MT; ++i)
+    for (int i = 0; i < NT; ++i)
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        l[i][h] += __shfl_xor_sync(full, l[i][h], 1);
-        l[i][h] += __shfl_xor_sync(full, l[i][h], 2);
-      }
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int x = 4; x < 32; x *= 2) l[i][h] += __shfl_xor_sync(full, l[i][h], x);
     __syncthreads();  // every ring is empty
-    float* s_o = reinterpret_cast<float*>(smem);
-    const bool few = MT == 1 && R - row0 <= 8;  // rows 8 .. 15 are nothing: half of the traffic
+    float* s_o = reinterpret_cast<float*>(smem);  // [warp][row][value, as the products order them]
 #pragma unroll
-    for (int i = 0; i < MT; ++i) {
+    for (int i = 0; i < NT; ++i) {
 #pragma unroll
-      for (int n = 0; n < NB; ++n) {
-        s_o[((warp * MT + i) * NB * 4 + n * 4) * 32 + lane] = o[i][n][0];
-        s_o[((warp * MT + i) * NB * 4 + n * 4 + 1) * 32 + lane] = o[i][n][1];
-        if (!few) {
-          s_o[((warp * MT + i) * NB * 4 + n * 4 + 2) * 32 + lane] = o[i][n][2];
-          s_o[((warp * MT + i) * NB * 4 + n * 4 + 3) * 32 + lane] = o[i][n][3];
-        }
-      }
-      if (t == 0) {
-        s_ml[warp * Sh::kRows + 16 * i + g] = make_float2(m[i][0], l[i][0]);
-        s_ml[warp * Sh::kRows + 16 * i + 8 + g] = make_float2(m[i][1], l[i][1]);
+      for (int n = 0; n < MB; ++n)
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+          s_o[(warp * Sh::kRows + 8 * i + 2 * t + (c & 1)) * Sh::kPitch + 16 * n + 8 * (c >> 1) + g] = o[i][n][c];
+      if (g == 0) {
+        s_ml[warp * Sh::kRows + 8 * i + 2 * t] = make_float2(m[i][0], l[i][0]);
+        s_ml[warp * Sh::kRows + 8 * i + 2 * t + 1] = make_float2(m[i][1], l[i][1]);
       }
     }
     __syncthreads();
 
-    constexpr int kVec = Sh::kRows * D / 4;  // four lanes of a register: one row
-    constexpr int kPer = kVec / Sh::kThreads;
-    static_assert(kVec % Sh::kThreads == 0, "vectors per thread");
+    // four values of a row each
+    constexpr int kVec = Sh::kRows * D / 4;
+    constexpr int kPer = (kVec + Sh::kThreads - 1) / Sh::kThreads;
     float4 acc[kPer];
     float mm[kPer], ll[kPer];
 #pragma unroll
@@ -684,8 +639,14 @@ __global__ void __launch_bounds__(TreeShape<FMT, D, MT>::kThreads, kBlocksPerSm)
       acc[j] = make_float4(0.f, 0.f, 0.f, 0.f);
       ll[j] = 0.f;
     }
-    auto row_of = [&](int v) {  // v = (mt * NB * 4 + n * 4 + c) * 8 + g
-      return 16 * (v / (NB * 32)) + (v & 7) + 8 * ((v >> 4) & 1);
+    auto row_of = [&](int v) { return v / (D / 4); };
+    auto to = [&](auto* dst, int v, float x, float y, float z, float w) {
+      const int n = (v % (D / 4)) / 2, n0 = 4 * (v & 1);
+      using T = std::remove_reference_t<decltype(*dst)>;
+      dst[C::out_at(n, n0)] = static_cast<T>(x);
+      dst[C::out_at(n, n0 + 1)] = static_cast<T>(y);
+      dst[C::out_at(n, n0 + 2)] = static_cast<T>(z);
+      dst[C::out_at(n, n0 + 3)] = static_cast<T>(w);
     };
     auto add = [&](int j, float pm, float pl, const float4& x, float top) {
       const float f = pm == -INFINITY ? 0.f : ex2(pm - top);
@@ -696,7 +657,7 @@ __global__ void __launch_bounds__(TreeShape<FMT, D, MT>::kThreads, kBlocksPerSm)
 #pragma unroll
     for (int j = 0; j < kPer; ++j) {
       const int v = tid + j * Sh::kThreads, row = row_of(v);
-      if (few && row >= 8) continue;
+      if (v >= kVec) continue;
       float top = -INFINITY;
 #pragma unroll
       for (int w = 0; w < W; ++w) top = fmaxf(top, s_ml[w * Sh::kRows + row].x);
@@ -705,7 +666,7 @@ __global__ void __launch_bounds__(TreeShape<FMT, D, MT>::kThreads, kBlocksPerSm)
 #pragma unroll
       for (int w = 0; w < W; ++w) {
         const float2 ml = s_ml[w * Sh::kRows + row];
-        add(j, ml.x, ml.y, *reinterpret_cast<const float4*>(s_o + (w * kVec + v) * 4), ref);
+        add(j, ml.x, ml.y, *reinterpret_cast<const float4*>(s_o + (w * Sh::kRows + row) * Sh::kPitch + 4 * (v % (D / 4))), ref);
       }
     }
 
@@ -714,30 +675,20 @@ __global__ void __launch_bounds__(TreeShape<FMT, D, MT>::kThreads, kBlocksPerSm)
 #pragma unroll
       for (int j = 0; j < kPer; ++j) {
         const int v = tid + j * Sh::kThreads, row = row_of(v);
-        const int n = (v >> 5) % NB, c = (v >> 3) & 3;
-        if (row0 + row >= R) continue;
-        float* dst = mine + row * D;
-        dst[C::out_at(n, (c & 1) + 0)] = acc[j].x;
-        dst[C::out_at(n, (c & 1) + 2)] = acc[j].y;
-        dst[C::out_at(n, (c & 1) + 4)] = acc[j].z;
-        dst[C::out_at(n, (c & 1) + 6)] = acc[j].w;
-        if ((v & ~7) % (NB * 32) == 0 || (v & ~7) % (NB * 32) == 16)  // one vector of each row
-          *reinterpret_cast<float2*>(mine + kSlotRows * D + 2 * row) = make_float2(mm[j], ll[j]);
+        if (v >= kVec || row0 + row >= R) continue;
+        to(mine + row * D, v, acc[j].x, acc[j].y, acc[j].z, acc[j].w);
+        if (v % (D / 4) == 0) *reinterpret_cast<float2*>(mine + kSlotRows * D + 2 * row) = make_float2(mm[j], ll[j]);
       }
     } else {
-      __half* s_out = reinterpret_cast<__half*>(smem + W * Sh::kRows * D * 4);
+      __half* s_out = reinterpret_cast<__half*>(smem + W * Sh::kRows * Sh::kPitch * 4);
 #pragma unroll
       for (int j = 0; j < kPer; ++j) {
         const int v = tid + j * Sh::kThreads, row = row_of(v);
-        const int n = (v >> 5) % NB, c = (v >> 3) & 3;
+        if (v >= kVec) continue;
         const float inv = ll[j] == 0.f ? 0.f : 1.f / ll[j];
-        __half* dst = s_out + row * D;
-        dst[C::out_at(n, (c & 1) + 0)] = __float2half_rn(acc[j].x * inv);
-        dst[C::out_at(n, (c & 1) + 2)] = __float2half_rn(acc[j].y * inv);
-        dst[C::out_at(n, (c & 1) + 4)] = __float2half_rn(acc[j].z * inv);
-        dst[C::out_at(n, (c & 1) + 6)] = __float2half_rn(acc[j].w * inv);
+        to(s_out + row * D, v, acc[j].x * inv, acc[j].y * inv, acc[j].z * inv, acc[j].w * inv);
         const int64_t r = row0 + row;
-        if (p.lse && r < R && ((v & ~7) % (NB * 32) == 0 || (v & ~7) % (NB * 32) == 16)) {
+        if (p.lse && r < R && v % (D / 4) == 0) {
           const int tok = static_cast<int>(r) / a.G;
           p.lse[(q0 + tok) * p.q_heads + head * a.G + r - tok * a.G] = ll[j] == 0.f ? -INFINITY : (mm[j] + log2f(ll[j])) * kLn2;
         }
@@ -832,14 +783,14 @@ __global__ void __launch_bounds__(128) tree_join_kernel(const TreeArgs a) {
   if (p.lse && lane == 0) p.lse[row] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
 }
 
-template <int FMT, int D, int MT>
+template <int FMT, int D, int NT>
 cudaError_t launch(const TreeArgs& a, cudaStream_t s) {
-  using Sh = TreeShape<FMT, D, MT>;
+  using Sh = TreeShape<FMT, D, NT>;
   static_assert(Sh::kStages >= 2 && Sh::kBytes <= 113 * 1024, "shared memory of a block");
   static const cudaError_t attr =
-      cudaFuncSetAttribute(tree_kernel<FMT, D, MT>, cudaFuncAttributeMaxDynamicSharedMemorySize, Sh::kBytes);
+      cudaFuncSetAttribute(tree_kernel<FMT, D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, Sh::kBytes);
   if (attr != cudaSuccess) return attr;
-  tree_kernel<FMT, D, MT><<<a.grid, Sh::kThreads, Sh::kBytes, s>>>(a);
+  tree_kernel<FMT, D, NT><<<a.grid, Sh::kThreads, Sh::kBytes, s>>>(a);
   return cudaGetLastError();
 }
 
@@ -893,12 +844,17 @@ cudaError_t launch_attn_tree(const TreeParams& p, cudaStream_t s) {
   a.min_units = 16 + a.extra;
   auto by_rows = [&](auto fmt, auto d) {
     constexpr int F = decltype(fmt)::value, D = decltype(d)::value;
-    if (rows > 16) {
-      const cudaError_t e = launch<F, D, 2>(a, s);
-      return e != cudaSuccess || a.whole ? e : launch_join<32, kKvBlockTokens>(a, s);
-    }
-    const cudaError_t e = launch<F, D, 1>(a, s);
-    return e != cudaSuccess || a.whole ? e : launch_join<16, kKvBlockTokens>(a, s);
+    auto run = [&](auto nt) {
+      constexpr int NT = decltype(nt)::value;
+      const cudaError_t e = launch<F, D, NT>(a, s);
+      return e != cudaSuccess || a.whole ? e : launch_join<8 * NT, kKvBlockTokens>(a, s);
+    };
+    // the smallest tiles that take the rows in as few passes over the cache
+    const int64_t tiles = (rows + kNarrowRows - 1) / kNarrowRows, each = (rows + tiles - 1) / tiles;
+    if (each <= 8) return run(std::integral_constant<int, 1>());
+    if (each <= 16) return run(std::integral_constant<int, 2>());
+    if (each <= 24) return run(std::integral_constant<int, 3>());
+    return run(std::integral_constant<int, 4>());
   };
   auto by_dim = [&](auto fmt) {
     return p.cache.head_dim == 64 ? by_rows(fmt, std::integral_constant<int, 64>())
