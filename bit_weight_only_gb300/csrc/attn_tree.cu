@@ -398,7 +398,7 @@ __global__ void __launch_bounds__(TreeShape<FMT, D, NT>::kThreads, kBlocksPerSm)
 #pragma unroll
             for (int i = 0; i < NT; ++i)
 #pragma unroll
-              for (int c = 0; c < 4; ++c) s[i][c] *= sl;
+              for (int h = 0; h < 2; ++h) unpack2(mul2(pack2(s[i][2 * h], s[i][2 * h + 1]), pack2(sl, sl)), s[i][2 * h], s[i][2 * h + 1]);
           } else {
 #pragma unroll
             for (int kp = 0; kp < KS / 2; ++kp) {
@@ -422,7 +422,7 @@ __global__ void __launch_bounds__(TreeShape<FMT, D, NT>::kThreads, kBlocksPerSm)
               float ksc = sl;
               if constexpr (FMT == QGEMV_KV_INT8) ksc *= *reinterpret_cast<const float*>(blk + L::kKs + 4 * (8 * h + g));
 #pragma unroll
-              for (int i = 0; i < NT; ++i) s[i][2 * h] *= ksc, s[i][2 * h + 1] *= ksc;
+              for (int i = 0; i < NT; ++i) unpack2(mul2(pack2(s[i][2 * h], s[i][2 * h + 1]), pack2(ksc, ksc)), s[i][2 * h], s[i][2 * h + 1]);
             }
           }
         }
@@ -460,7 +460,11 @@ __global__ void __launch_bounds__(TreeShape<FMT, D, NT>::kThreads, kBlocksPerSm)
 #pragma unroll
         for (int i = 0; i < NT; ++i)
 #pragma unroll
-          for (int c = 0; c < 4; ++c) grow |= s[i][c] + lv[c >> 1] > m[i][c & 1] + kLazyT;
+          for (int h = 0; h < 2; ++h) {
+            float x, y;
+            unpack2(add2(pack2(s[i][2 * h], s[i][2 * h + 1]), pack2(lv[h], lv[h])), x, y);
+            grow |= x > m[i][0] + kLazyT || y > m[i][1] + kLazyT;
+          }
         if (__any_sync(full, grow)) {
 #pragma unroll
           for (int i = 0; i < NT; ++i)
@@ -481,10 +485,12 @@ __global__ void __launch_bounds__(TreeShape<FMT, D, NT>::kThreads, kBlocksPerSm)
 #pragma unroll
         for (int i = 0; i < NT; ++i)
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            const float ref = m[i][c & 1] == -INFINITY ? 0.f : m[i][c & 1];
-            s[i][c] = ex2(s[i][c] - ref);
-            l[i][c & 1] += s[i][c];
+          for (int h = 0; h < 2; ++h) {
+            const uint64_t less = pack2(m[i][0] == -INFINITY ? 0.f : -m[i][0], m[i][1] == -INFINITY ? 0.f : -m[i][1]);
+            float x, y;
+            unpack2(add2(pack2(s[i][2 * h], s[i][2 * h + 1]), less), x, y);
+            s[i][2 * h] = ex2(x), s[i][2 * h + 1] = ex2(y);
+            unpack2(add2(pack2(l[i][0], l[i][1]), pack2(s[i][2 * h], s[i][2 * h + 1])), l[i][0], l[i][1]);
           }
         // p * scale(v).  Where a masked token's scale is infinite or NaN (past the
         // end it may be anything) the product is 0 all the same.
