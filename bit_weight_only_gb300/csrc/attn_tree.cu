@@ -191,7 +191,7 @@ __device__ __forceinline__ void load_scales(const uint8_t* at, __half2 (&sc)[D /
 template <int FMT, int D, int NT>
 struct TreeShape {
   using L = KvLayout<FMT, D>;
-  static constexpr int kWarps = NT > 2 || FMT == QGEMV_KV_F16 ? 4 : 8;
+  static constexpr int kWarps = NT > 2 || FMT == QGEMV_KV_F16 ? 4 : NT == 2 && D == 128 ? 6 : 8;
   static constexpr int kThreads = 32 * kWarps;
   static constexpr int kRows = 8 * NT;
   static constexpr int kFitting = kRingBytes / (kWarps * L::kBlock);
