@@ -2,13 +2,15 @@
 // (qgemv_attn_tree).
 //
 // Rows of a sequence and key/value head: row = token * G + head of the group.
-// tree_kernel takes them in tiles of 16 or 32, by mma.sync; more than 32 rows
-// of the fp16 and INT8 formats go to attn_tree_wide.cu.  A unit is a block of 16 cached
-// tokens (tree_work.cuh); within a thread block's segment a warp takes every
-// W-th unit:
+// tree_kernel takes them in tiles of 8, 16, 24 or 32, by mma.sync; many rows
+// of the fp16 and INT8 formats go to attn_tree_wide.cu.  A unit is a block of
+// 16 cached tokens (tree_work.cuh); within a thread block's segment a warp
+// takes every W-th unit:
 //
 //   copy      one bulk copy into the warp's own ring of shared-memory stages
-//   S = Q K^T mma.m16n8k16 on the codes as fp16, K straight from the block's
+//   S' = K Q' mma.m16n8k16, the unit's tokens its 16 rows and 8 query rows its
+//             columns, so that the common eight rows (one token of a group of
+//             8 heads) fill an instruction.  K straight from the block's
 //             layout: stored bytes and nibbles are fp16 subnormals as they
 //             stand (code + offset, times 2^-24), and the sums start at
 //             -offset times the row's sum of q, so that a code pair costs one
@@ -19,9 +21,11 @@
 //             needed.  m is taken over s + log2(scale of v), because what is
 //             rounded to fp16 is p * scale(v), the factor of v's codes: it
 //             stays in [0, 2^8] whatever the scales are
-//   O += P V  the same instruction on V's codes, exact in fp16 (their offsets are
-//             taken off first: here sums run over all keys, and would not
-//             stay small beside the offsets' share)
+//   O' += V' P' the same instruction, 16 values of the head its rows.  P'
+//             is the scores' registers, transposed 8 x 8 between lanes.  V's
+//             codes are exact in fp16 (their offsets are taken off first: here
+//             sums run over all keys, and would not stay small beside the
+//             offsets' share)
 //
 // A warp's O, m and l live in its registers.  At the end of a segment the
 // warps' results are added in warp order through shared memory.
@@ -33,7 +37,7 @@
 namespace qgemv {
 namespace {
 
-constexpr int kNarrowRows = 32;  // more rows than this go to the wide kernel, but for Q4_0
+constexpr int kNarrowRows = 32;  // rows of a pass, at most
 constexpr int64_t kWholeTokens = 1024;
 constexpr int kErrTree = 32;
 constexpr float kLazyT = 8.f;
@@ -830,13 +834,18 @@ cudaError_t launch_attn_tree(const TreeParams& p, cudaStream_t s) {
   a.grid = sms < kMaxBlocks ? sms : kMaxBlocks;
   const int64_t rows = static_cast<int64_t>(p.max_new) * a.G;
   // Up to 32 rows this file's kernel is faster (two sequences of up to 131000
-  // tokens, INT8: 8 rows 89 us against 177, 32 rows 135 against 161); beyond,
-  // it would need several tiles and passes over the cache, and the wide one is
-  // (16 sequences of up to 16000 tokens, INT8, 64 rows: 96 us against 188).
+  // tokens, INT8: 8 rows 87 us against 177, 32 rows 124 against 161).  Beyond
+  // it needs several tiles and passes over the cache.  fp16: the wide kernel is
+  // faster from there (those sequences, 40 rows: 115 us against 135; 64 rows: 150
+  // against 229).  INT8, whose codes the wide kernel has to write out as fp16
+  // first: two passes are no slower on the whole (64 rows: 16 sequences of up to
+  // 16000 tokens 83 us against 93, two of 131000 179 against 167), but for
+  // contexts that are not split (16 of up to 1000: 27 against 22).
   // Contexts of up to kWholeTokens positions (as the caller bounds them) are
   // not split: a second kernel would take longer than the split saves.
   a.whole = p.max_ctx + p.max_new <= kWholeTokens;
-  if (rows > kNarrowRows && p.cache.format != QGEMV_KV_Q4_0) {
+  const int narrow = p.cache.format == QGEMV_KV_INT8 && !a.whole ? 2 * kNarrowRows : kNarrowRows;
+  if (rows > narrow && p.cache.format != QGEMV_KV_Q4_0) {
     a.extra = 4;  // a row tile's start and end: about four units of 128 tokens
     a.min_units = 2 + a.extra;
     const cudaError_t e = launch_tree_wide(a, s);

@@ -115,6 +115,15 @@ def test_matches_the_definition(fmt, hq, hkv, d, page, ctx, new):
 
 
 @pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("new", [1, 2, 3, 5, 6, 7, 8, 9, 11, 13, 16, 17, 25])
+def test_tiles_of_rows(fmt, d, new):
+    """Numbers of rows (four a token) at and around the ends of the kernels' tiles, in contexts that are split."""
+    c = Case(fmt, 4, 1, d, 32, [1500, 0, 333], [new, 1, max(1, new - 2)]).fill()
+    c.check(f"{fmt} {d} {new}", *c.run())
+
+
+@pytest.mark.parametrize("fmt", FMTS)
 @pytest.mark.parametrize("masks", ["chain", "random", "none"])
 def test_masks(fmt, masks):
     """Chains (also as no masks at all), any bits, and rows that see nothing but the past (with no past: nothing)."""
