@@ -9,11 +9,12 @@
 // floor(128 / G) tokens of one key/value head; a block walks the keys in tiles
 // of 128 up to the last one that the rows see.
 //
-// Where there are too few such pieces to fill the GPU, a piece is cut into parts
-// of its keys; their unnormalised results go to the workspace, and a second
-// kernel joins them in order.
 // One block per SM takes the pieces one after the other from a counter, those
-// with the most keys first within a sequence.  Its warps (12) run through the
+// with the most keys first within a sequence.  Where there are too few pieces
+// to fill the GPU evenly so, each block takes an equal run of the list of all
+// pieces' key tiles instead; the unnormalised results of pieces that runs
+// share go to the workspace, and a second kernel joins them in order.
+// A block's warps (12) run through the
 // pieces on their own, held together by mbarriers only, so that one piece's
 // start overlaps the end of the one before:
 //   0-7    two softmax warpgroups, one for each row tile, a thread for each row
@@ -58,18 +59,29 @@ constexpr float kLazy = 8.f;  // log2 of the growth that makes O be rescaled
 // which clears it before it uses it, of three pieces in turn.
 constexpr int kNotes = 3;
 constexpr int kItems = 4;  // ring of pieces
-constexpr int kMaxParts = 8;
 
-// Workspace slot of a part: O [256][D], then m and l [256][2].
-constexpr int kPartSlots = 304;
+// Runs: a piece counts as this many key tiles more (its start and end), which
+// come first; a run is that long at least.
+constexpr int kStartTiles = 3;
+constexpr int kMinRun = 4 + kStartTiles;
+constexpr int kMaxPieces = 1024;  // of a call whose blocks take runs
+constexpr double kJoinTiles = 10;  // what the second kernel takes, in key tiles
+
+// The workspace of runs: two slots a block (0: it goes on with a piece, 1: it
+// begins one that others go on with), each O [256][D], then m and l [256][2];
+// then the first and the last block of each piece.
+constexpr int kMaxBlocks = 152, kPartSlots = 2 * kMaxBlocks;
 __host__ __device__ constexpr int64_t part_floats(int D) { return static_cast<int64_t>(kRowsPerBlock) * (D + 2); }
 __device__ __forceinline__ float* part_slot(const PromptParams& p, int id, int D) {
   return reinterpret_cast<float*>(p.ws + kWsHeaderBytes) + id * part_floats(D);
 }
+__device__ __forceinline__ int* piece_blocks(const PromptParams& p, int piece, int D) {
+  return reinterpret_cast<int*>(part_slot(p, kPartSlots, D)) + 2 * piece;
+}
 
 struct PromptArgs {
   PromptParams p;
-  int G, tokens, n_slots, parts;  // tokens of a row tile
+  int G, tokens, n_slots;  // tokens of a row tile
 };
 
 // Barriers: full / empty pairs of the rings.  kBVf: a V tile has landed; kBFix:
@@ -78,12 +90,14 @@ enum { kBQ = 0, kBQe = 2, kBKf = 4, kBKe = 6, kBVf = 8, kBVe = 10, kBFix = 12, k
        kBNe = 23, kBIf = 26, kBIe = 30, kBDone = 34, kNBars = 35 };
 
 // A piece: two row tiles of a sequence and head, and the key tiles t0 .. of
-// them that this part takes.
+// them that this block takes.
 struct Piece {
   int64_t q0, k0;      // first query and key of the sequence
   int tok0, nq;        // first token of the piece, tokens of the sequence
   int off, nk;         // query i sees the keys j <= i + off; keys
-  int id, head;        // of the part (-1: no more); key/value head
+  int head;            // key/value head; -1: no more pieces
+  int part;            // workspace slot of the results, -1: they are the piece's
+  int all[2];          // key tiles that each row tile sees
   int t0, n[2], n_max; // key tiles: of each row tile, and the more of the two
   int first_masked;    // of those, the first with positions that some row of the piece does not see
   int mask_from;       // the first such position
@@ -91,13 +105,13 @@ struct Piece {
   // keys that a token sees: 0 .. sees - 1
   __device__ int sees(int token) const { return max(0, min(nk, token + off + 1)); }
 
+  __device__ int tiles() const { return max(all[0], all[1]); }
+
+  // Pieces are numbered by slots of tokens, the last first, and heads within.
   // False: a slot without tokens.
-  __device__ bool decode(const PromptArgs& a, int part_id) {
+  __device__ bool locate(const PromptArgs& a, int slot_from_last) {
     const PromptParams& p = a.p;
-    const int part = part_id % a.parts, pid = part_id / a.parts, step = 2 * a.tokens;
-    const int slot = a.n_slots - 1 - pid / p.kv_heads;
-    id = part_id;
-    head = pid % p.kv_heads;
+    const int step = 2 * a.tokens, slot = a.n_slots - 1 - slot_from_last;
     // The sequence of this slot: its pieces start at slot floor(cu / step) + b,
     // which leaves each sequence at least as many slots as it has pieces.
     int lo = 0, hi = p.n_seqs - 1;
@@ -115,20 +129,86 @@ struct Piece {
     nk = static_cast<int>(max(static_cast<int64_t>(0), min(static_cast<int64_t>(__ldg(p.cu_k + lo + 1)), p.n_k) - k0));
     off = nk - nq;
     const int tok1 = tok0 + a.tokens;
-    const int all0 = (sees(min(tok1, nq) - 1) + kKeys - 1) / kKeys;
-    const int all1 = tok1 >= nq ? 0 : (sees(min(tok1 + a.tokens, nq) - 1) + kKeys - 1) / kKeys;
-    const int tiles = max(all0, all1);
-    t0 = static_cast<int>(static_cast<int64_t>(tiles) * part / a.parts);
-    const int t1 = static_cast<int>(static_cast<int64_t>(tiles) * (part + 1) / a.parts);
-    n[0] = max(0, min(t1, all0) - t0);
-    n[1] = max(0, min(t1, all1) - t0);
-    n_max = max(n[0], n[1]);
+    all[0] = (sees(min(tok1, nq) - 1) + kKeys - 1) / kKeys;
+    all[1] = tok1 >= nq ? 0 : (sees(min(tok1 + a.tokens, nq) - 1) + kKeys - 1) / kKeys;
     mask_from = sees(tok0);
-    first_masked = max(0, mask_from / kKeys - t0);
     return true;
+  }
+
+  __device__ void take(int of_head, int from, int to, int to_part) {
+    head = of_head;
+    part = to_part;
+    t0 = from;
+    n[0] = max(0, min(to, all[0]) - from);
+    n[1] = max(0, min(to, all[1]) - from);
+    n_max = max(n[0], n[1]);
+    first_masked = max(0, mask_from / kKeys - from);
   }
 };
 static_assert(sizeof(Piece) * kItems <= 512, "room for the pieces");
+
+// A block's run (a whole warp calls it).  The costs of 32 slots at a time are
+// in the lanes.
+struct Run {
+  int64_t cur = 0, end = 0, base = 0;  // base: what comes before those slots
+  int64_t cost = 0, sum = 0;           // of the lane's slot, all heads; sums up to it
+  int s0 = 0;
+
+  __device__ void costs(const PromptArgs& a) {
+    const int lane = threadIdx.x & 31;
+    Piece x;
+    cost = s0 + lane < a.n_slots && x.locate(a, s0 + lane) ? static_cast<int64_t>(x.tiles() + kStartTiles) * a.p.kv_heads : 0;
+    sum = cost;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t y = __shfl_up_sync(0xffffffffu, sum, o);
+      if (lane >= o) sum += y;
+    }
+  }
+
+  __device__ void start(const PromptArgs& a) {
+    int64_t total = 0;
+    for (s0 = (a.n_slots - 1) / 32 * 32; s0 >= 0; s0 -= 32) {
+      costs(a);
+      total += __shfl_sync(0xffffffffu, sum, 31);
+    }
+    s0 = 0;  // the slots whose costs are there
+    const int64_t quota = max(static_cast<int64_t>(kMinRun), div_small(total + gridDim.x - 1, gridDim.x));
+    cur = quota * blockIdx.x;
+    end = min(cur + quota, total);
+  }
+
+  // The next piece; false: the run ends.
+  __device__ bool next(const PromptArgs& a, Piece& pc, int D) {
+    const int lane = threadIdx.x & 31;
+    while (cur < end) {
+      const unsigned past = __ballot_sync(0xffffffffu, base + sum > cur);
+      if (!past) {
+        base += __shfl_sync(0xffffffffu, sum, 31);
+        s0 += 32;
+        costs(a);
+        continue;
+      }
+      const int k = __ffs(past) - 1;
+      const int64_t in = cur - base - __shfl_sync(0xffffffffu, sum - cost, k);
+      pc.locate(a, s0 + k);
+      const int64_t each = pc.tiles() + kStartTiles;
+      const int head = static_cast<int>(div_small(in, each));
+      const int64_t v0 = in - head * each, v1 = min(each, v0 + end - cur);
+      cur += v1 - v0;
+      const int from = static_cast<int>(max(static_cast<int64_t>(0), v0 - kStartTiles)), to = static_cast<int>(v1) - kStartTiles;
+      // its first blocks may have nothing but a share of its start
+      if (to <= from && !(pc.tiles() == 0 && v0 == 0)) continue;
+      const bool first = from == 0, last = to >= pc.tiles() || pc.tiles() == 0;
+      pc.take(head, from, max(to, 0), first && last ? -1 : static_cast<int>(2 * blockIdx.x) + (first ? 1 : 0));
+      int* blocks = piece_blocks(a.p, (s0 + k) * a.p.kv_heads + head, D);
+      if (lane == 0 && first) blocks[0] = blockIdx.x;
+      if (lane == 0 && last) blocks[1] = blockIdx.x;
+      return true;
+    }
+    return false;
+  }
+};
 
 template <int D>
 struct Smem {
@@ -142,7 +222,7 @@ struct Smem {
   static_assert(kBytes <= 227 * 1024, "shared memory");
 };
 
-template <int D, bool BF16>
+template <int D, bool BF16, bool RUNS>
 __global__ void __launch_bounds__(kThreads, 1)
 prompt_kernel(const PromptArgs a, const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
               const __grid_constant__ CUtensorMap vmap) {
@@ -221,10 +301,13 @@ prompt_kernel(const PromptArgs a, const __grid_constant__ CUtensorMap qmap, cons
     const int st = n_item % kItems;
     if (!wait_all(kBIf + st, used(n_item, kItems))) return false;
     pc = s_pieces[st];
-    __syncwarp();
-    if (lane == 0) mbar_arrive(&bars[kBIe + st]);
     ++n_item;
-    return pc.id >= 0;
+    return pc.head >= 0;
+  };
+  // its place may be used again
+  auto release_piece = [&]() {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&bars[kBIe + (n_item - 1) % kItems]);
   };
 
   Piece pc;
@@ -233,7 +316,7 @@ prompt_kernel(const PromptArgs a, const __grid_constant__ CUtensorMap qmap, cons
     if (warp == 8) {
       // ---- pieces; K and V tiles
       int* counters = reinterpret_cast<int*>(p.ws) + 1;  // next piece, blocks that are done
-      const int total = a.n_slots * p.kv_heads * a.parts;
+      const int total = a.n_slots * p.kv_heads;
       const bool leader = elect_one();
       // the first piece is the block's number, the others come from the counter
       auto take = [&]() {
@@ -243,25 +326,35 @@ prompt_kernel(const PromptArgs a, const __grid_constant__ CUtensorMap qmap, cons
       };
       int jt = 0, id = blockIdx.x, n_qi[2] = {0, 0};
       bool ok = true, more = true;
+      Run run;
+      if (RUNS) run.start(a);
       while (ok && more) {
-        more = id < total;
-        if (more && !pc.decode(a, id)) {
-          id = take();
-          continue;
+        if (RUNS) {
+          more = run.next(a, pc, D);
+        } else {
+          more = id < total;
+          if (more && !pc.locate(a, id / p.kv_heads)) {
+            id = take();
+            continue;
+          }
+          if (more) pc.take(id % p.kv_heads, 0, pc.tiles(), -1);
         }
         const int st = n_item % kItems;
         if (n_item >= kItems) ok = wait_all(kBIe + st, freed(n_item, kItems));
         if (!ok) break;
         if (lane == 0) {
           if (more) s_pieces[st] = pc;
-          else s_pieces[st].id = -1;
+          else s_pieces[st].head = -1;
           mbar_arrive(&bars[kBIf + st]);
         }
         __syncwarp();
         ++n_item;
         if (!more) break;
-        const int ahead = take();
+        // the next piece is taken near this one's end: a block with a long one would
+        // keep it waiting
+        int ahead = !RUNS && pc.n_max == 0 ? take() : 0;
         for (int j = 0; ok && j < pc.n_max; ++j, ++jt) {
+          if (!RUNS && j == max(0, pc.n_max - 2)) ahead = take();
           const int ks = jt & 1;
           auto load = [&](const CUtensorMap* map, int fullb, int empty, int base) -> bool {
             if (jt >= 2 && !wait_all(empty + ks, freed(jt, 2))) return false;
@@ -310,7 +403,7 @@ prompt_kernel(const PromptArgs a, const __grid_constant__ CUtensorMap qmap, cons
       }
       for (int i = 0; i < 2; ++i)
         if (n_qi[i] > 0) mbar_wait_bounded(&bars[kBQ + i], (n_qi[i] - 1) & 1);
-      if (lane == 0) {  // the last block leaves the counters as it found them
+      if (!RUNS && lane == 0) {  // the last block leaves the counters as it found them
         __threadfence();
         if (atomicAdd(counters + 1, 1) == static_cast<int>(gridDim.x) - 1) {
           counters[0] = 0;
@@ -325,6 +418,7 @@ prompt_kernel(const PromptArgs a, const __grid_constant__ CUtensorMap qmap, cons
       int jt = 0, n_qi[2] = {0, 0}, n_s[2] = {0, 0};
       bool ok = true;
       while (ok && next_piece(pc)) {
+        release_piece();
         auto qk = [&](int i, int j) {
           const uint64_t da = sw128_desc(sq + i * S::kTile, 0, 1024);
           const uint64_t db = sw128_desc(sk + ((jt + j) & 1) * S::kTile, 0, 1024);
@@ -394,6 +488,7 @@ prompt_kernel(const PromptArgs a, const __grid_constant__ CUtensorMap qmap, cons
       int jt = 0;
       bool ok = true;
       while (ok && next_piece(pc)) {
+        release_piece();
         const int note = (n_item - 1) % kNotes;
         if (ok && n_item > kNotes) ok = wait_all(kBNe + note, freed(n_item - 1, kNotes));
         int* notes = s_bad + ((warp - 10) * kNotes + note) * 3 * D;
@@ -467,14 +562,9 @@ prompt_kernel(const PromptArgs a, const __grid_constant__ CUtensorMap qmap, cons
     int n_s = 0, n_o = 0;  // scores and results so far
     bool ok = true;
     while (ok && next_piece(pc)) {
-      const int note = (n_item - 1) % kNotes;
-      const int token = pc.tok0 + i * a.tokens + tok_l;
-      const bool store = wt < a.tokens * G && token < pc.nq;
-      const int n = i == 0 ? pc.n[0] : pc.n[1], t0 = pc.t0;
-      const int my_sees = pc.sees(min(token, pc.nq - 1));
+      const int n = i == 0 ? pc.n[0] : pc.n[1], t0 = RUNS ? pc.t0 : 0;
+      const int my_sees = pc.sees(min(pc.tok0 + i * a.tokens + tok_l, pc.nq - 1));
       const int all_see = pc.sees(pc.tok0 + i * a.tokens);  // what every row of the tile sees
-      const int64_t at = pc.q0 + token;                       // row of q and out
-      const int h = pc.head * G + head_l;
       float m = -INFINITY, l = 0.f;
       for (int j = 0; j < n; ++j, ++n_s) {
         ok = wait_all(kBS + i, n_s & 1);
@@ -555,15 +645,22 @@ prompt_kernel(const PromptArgs a, const __grid_constant__ CUtensorMap qmap, cons
         ok = wait_all(kBO + i, n_o & 1);
         ++n_o;
       }
+      const int note = (n_item - 1) % kNotes;
       ok = ok && wait_all(kBNf + note, used(n_item - 1, kNotes));
       if (!ok) break;
       tcgen_after_sync();
+      // the piece, read again: its registers are scarce in the loop above
+      const Piece& piece = s_pieces[(n_item - 1) % kItems];
+      const int token = piece.tok0 + i * a.tokens + tok_l, part = RUNS ? piece.part : -1;
+      const bool store = wt < a.tokens * G && token < piece.nq;
+      const int64_t at = piece.q0 + token;  // row of q and out
+      const int h = piece.head * G + head_l;
       const bool bad = s_anybad[note] != 0 || s_anybad[kNotes + note] != 0;
       const int* bad0 = s_bad + note * 3 * D;
       const int* bad1 = s_bad + (kNotes + note) * 3 * D;
       const bool use0 = s_anybad[note] != 0, use1 = s_anybad[kNotes + note] != 0;
       {
-        const float inv = a.parts > 1 ? 1.f : l == 0.f ? 0.f : 1.f / l;
+        const float inv = part >= 0 ? 1.f : l == 0.f ? 0.f : 1.f / l;
         T* out = static_cast<T*>(p.out.ptr);
         int64_t off8[4];  // of the rows this lane stores; -1: none
 #pragma unroll
@@ -590,8 +687,8 @@ prompt_kernel(const PromptArgs a, const __grid_constant__ CUtensorMap qmap, cons
           }
           // through shared memory, so that a store covers whole sectors: 32 rows of
           // 64 bytes (parts, in fp32: two halves of the columns)
-          if (a.parts > 1) {
-            float* part = part_slot(p, pc.id, D) + (128 * i + 32 * (warp & 3)) * D + c;
+          if (part >= 0) {
+            float* to = part_slot(p, part, D) + (128 * i + 32 * (warp & 3)) * D + c;
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
 #pragma unroll
@@ -602,7 +699,7 @@ prompt_kernel(const PromptArgs a, const __grid_constant__ CUtensorMap qmap, cons
 #pragma unroll
               for (int x = 0; x < 4; ++x) {
                 const int r = 8 * x + (lane >> 2), u = lane & 3;
-                *reinterpret_cast<uint4*>(part + r * D + 16 * half + 4 * u) =
+                *reinterpret_cast<uint4*>(to + r * D + 16 * half + 4 * u) =
                     *reinterpret_cast<const uint4*>(stage + r * 64 + ((u ^ ((r >> 1) & 3)) << 4));
               }
               __syncwarp();
@@ -627,12 +724,13 @@ prompt_kernel(const PromptArgs a, const __grid_constant__ CUtensorMap qmap, cons
             __syncwarp();
           }
         }
-        if (a.parts > 1)
-          *reinterpret_cast<float2*>(part_slot(p, pc.id, D) + kRowsPerBlock * D + 2 * (128 * i + wt)) = make_float2(m, l);
+        if (part >= 0)
+          *reinterpret_cast<float2*>(part_slot(p, part, D) + kRowsPerBlock * D + 2 * (128 * i + wt)) = make_float2(m, l);
         else if (store && p.lse)
           p.lse[at * p.q_heads + h] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
         tcgen_before_sync();
       }
+      release_piece();
       mbar_arrive(&bars[kBNe + note]);
     }
   }
@@ -662,33 +760,40 @@ __global__ void __launch_bounds__(128) prompt_join_kernel(const PromptArgs a) {
   const int i = static_cast<int>(token - q0), in_piece = i % (2 * a.tokens);
   const int64_t slot = q0 / (2 * a.tokens) + lo + i / (2 * a.tokens);
   const int rr = 128 * (in_piece / a.tokens) + in_piece % a.tokens * a.G + qh - head * a.G;
-  const int first = static_cast<int>(((a.n_slots - 1 - slot) * p.kv_heads + head) * a.parts);
-  float m = -INFINITY, l = 0.f, ml[kMaxParts], ll[kMaxParts];
-#pragma unroll
-  for (int k = 0; k < kMaxParts; ++k) {
-    ml[k] = -INFINITY, ll[k] = 0.f;
-    if (k < a.parts) {
-      const float2 v = *reinterpret_cast<const float2*>(part_slot(p, first + k, D) + kRowsPerBlock * D + 2 * rr);
-      ml[k] = v.x, ll[k] = v.y;
-    }
-  }
-#pragma unroll
-  for (int k = 0; k < kMaxParts; ++k) m = fmaxf(m, ml[k]);
-  const float ref = m == -INFINITY ? 0.f : m;
-  float acc[D / 32];
+  const int* blocks = piece_blocks(p, static_cast<int>((a.n_slots - 1 - slot) * p.kv_heads + head), D);
+  const int b0 = max(0, blocks[0]), b1 = min(blocks[1], kMaxBlocks - 1);
+  if (b0 >= b1) return;  // one block had it all
+  const unsigned full = 0xffffffffu;
+  float m = -INFINITY, l = 0.f, acc[D / 32];
 #pragma unroll
   for (int c = 0; c < D / 32; ++c) acc[c] = 0.f;
+  for (int c0 = b0; c0 <= b1; c0 += 32) {
+    float2 ml = make_float2(-INFINITY, 0.f);
+    const int mine = c0 + lane;
+    if (mine <= b1)
+      ml = *reinterpret_cast<const float2*>(part_slot(p, 2 * mine + (mine == b0 ? 1 : 0), D) + kRowsPerBlock * D + 2 * rr);
+    float top = ml.x;
 #pragma unroll
-  for (int k = 0; k < kMaxParts; ++k) {
-    if (k >= a.parts) break;
-    const float f = ml[k] == -INFINITY ? 0.f : ex2(ml[k] - ref);
-    l += ll[k] * f;
-    const float* src = part_slot(p, first + k, D) + rr * D + lane * (D / 32);
-    float x[D / 32];
-    if constexpr (D == 128) *reinterpret_cast<float4*>(x) = *reinterpret_cast<const float4*>(src);
-    else *reinterpret_cast<float2*>(x) = *reinterpret_cast<const float2*>(src);
+    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(full, top, o));
+    const float mn = fmaxf(m, top), ref = mn == -INFINITY ? 0.f : mn;
+    const float g = m == -INFINITY ? 0.f : ex2(m - ref);
+    const float f = ml.x == -INFINITY ? 0.f : ex2(ml.x - ref);
+    m = mn;
+    l *= g;
 #pragma unroll
-    for (int c = 0; c < D / 32; ++c) acc[c] += x[c] * f;
+    for (int c = 0; c < D / 32; ++c) acc[c] *= g;
+    const int n = min(32, b1 - c0 + 1);
+#pragma unroll 4
+    for (int k = 0; k < n; ++k) {
+      const float fk = __shfl_sync(full, f, k);
+      l += __shfl_sync(full, ml.y, k) * fk;
+      const float* src = part_slot(p, 2 * (c0 + k) + (c0 + k == b0 ? 1 : 0), D) + rr * D + lane * (D / 32);
+      float x[D / 32];
+      if constexpr (D == 128) *reinterpret_cast<float4*>(x) = *reinterpret_cast<const float4*>(src);
+      else *reinterpret_cast<float2*>(x) = *reinterpret_cast<const float2*>(src);
+#pragma unroll
+      for (int c = 0; c < D / 32; ++c) acc[c] += x[c] * fk;
+    }
   }
   const float inv = l == 0.f ? 0.f : 1.f / l;
   T* out = static_cast<T*>(p.out.ptr) + token * p.out.token_stride + qh * p.out.head_stride + lane * (D / 32);
@@ -744,9 +849,6 @@ cudaError_t launch(const PromptParams& p, cudaStream_t s) {
     if (e == cudaSuccess) e = make_map(&vm, p.v, D, p.kv_heads, p.n_k, BF16, 1, kKeys);
     if (e != cudaSuccess) return e;
   }
-  static const cudaError_t attr =
-      cudaFuncSetAttribute(prompt_kernel<D, BF16>, cudaFuncAttributeMaxDynamicSharedMemorySize, Smem<D>::kBytes);
-  if (attr != cudaSuccess) return attr;
   static const int sms = [] {
     int dev = 0, n = 0;
     cudaGetDevice(&dev);
@@ -754,30 +856,33 @@ cudaError_t launch(const PromptParams& p, cudaStream_t s) {
     return n;
   }();
   const int64_t pieces = static_cast<int64_t>(a.n_slots) * p.kv_heads;
-  a.parts = 1;
-  {
-    // Parts: the number that makes the busiest block's share of the keys least.
-    // A part costs about kPartTiles key tiles more (its start and end, the join).
-    // The lengths are known as averages only; any choice is right.
-    const double kPartTiles = 6;
-    const double busy = std::ceil(static_cast<double>(p.n_q) / (2 * a.tokens) / p.n_seqs) * p.n_seqs * p.kv_heads;
-    const double tiles = static_cast<double>(p.n_k) / p.n_seqs / kKeys;
-    double best = 0;
-    for (int n = 1; n <= kMaxParts && pieces * n <= kPartSlots; ++n) {
-      const double cost = std::ceil(busy * n / sms) * (tiles / n + (n > 1 ? kPartTiles : 0));
-      if (n == 1 || cost < best) best = cost, a.parts = n;
-    }
-  }
-  const int64_t total = pieces * a.parts;
-  prompt_kernel<D, BF16><<<static_cast<unsigned>(total < sms ? total : sms), kThreads, Smem<D>::kBytes, s>>>(a, qm, km, vm);
-  cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess || a.parts == 1) return e;
+  // Whole pieces, or runs: whichever makes the busiest block's share of the keys
+  // less.  The lengths are known as averages only; either is right.
+  const double busy = std::ceil(static_cast<double>(p.n_q) / (2 * a.tokens) / p.n_seqs) * p.n_seqs * p.kv_heads;
+  const double most = static_cast<double>(p.n_k) / p.n_seqs / kKeys;  // key tiles of a sequence's last piece
+  const double mean = std::max(1.0, (p.n_k - 0.5 * p.n_q) / p.n_seqs / kKeys) + kStartTiles;
+  const double whole = std::max(std::ceil(busy / sms) * mean, most + kStartTiles);
+  const double runs = busy * mean / sms + kStartTiles + kJoinTiles;
+  auto run = [&](auto by_runs, int64_t blocks) {
+    constexpr bool RUNS = decltype(by_runs)::value;
+    static const cudaError_t attr =
+        cudaFuncSetAttribute(prompt_kernel<D, BF16, RUNS>, cudaFuncAttributeMaxDynamicSharedMemorySize, Smem<D>::kBytes);
+    if (attr != cudaSuccess) return attr;
+    prompt_kernel<D, BF16, RUNS>
+        <<<static_cast<unsigned>(std::min<int64_t>(blocks, sms)), kThreads, Smem<D>::kBytes, s>>>(a, qm, km, vm);
+    return cudaGetLastError();
+  };
+  if (pieces > kMaxPieces || runs >= whole) return run(std::false_type(), pieces);
+  const cudaError_t e = run(std::true_type(), kMaxBlocks);
+  if (e != cudaSuccess) return e;
   return launch_after(prompt_join_kernel<D, BF16>, static_cast<unsigned>((p.n_q * p.q_heads + 3) / 4), a, s);
 }
 
 }  // namespace
 
-int64_t prompt_ws_bytes(int head_dim) { return kPartSlots * part_floats(head_dim) * static_cast<int64_t>(sizeof(float)); }
+int64_t prompt_ws_bytes(int head_dim) { 
+  return kPartSlots * part_floats(head_dim) * static_cast<int64_t>(sizeof(float)) + kMaxPieces * 2 * static_cast<int64_t>(sizeof(int));
+}
 
 cudaError_t launch_attn_prompt(const PromptParams& p, cudaStream_t s) {
   if (p.dtype == QGEMV_DT_F16) return p.head_dim == 64 ? launch<64, false>(p, s) : launch<128, false>(p, s);

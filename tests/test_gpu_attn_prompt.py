@@ -113,6 +113,22 @@ def test_few_rows_many_keys(kind, hq, hkv, d, nq, nk):
     assert torch.equal(got, torch.arange(c.nq[0]) >= c.nq[0] - 3)
 
 
+@pytest.mark.parametrize("kind", list(KINDS))
+@pytest.mark.parametrize("hq, hkv, d, nq, nk", [
+    (8, 1, 128, [3, 1, 0, 40] * 11, [4000, 3, 700, 6000] * 11),          # more sequences than lanes; one without queries
+    (5, 5, 64, [26, 130, 1, 51], [9000, 130, 20, 51]),
+    (64, 8, 128, [16], [9001]),
+    (16, 1, 64, [1, 700, 2], [12000, 700, 0]),                           # and one without keys
+])
+def test_uneven_pieces(kind, hq, hkv, d, nq, nk):
+    """Few pieces of very different lengths, which several blocks share."""
+    c = Case(kind, hq, hkv, d, nq, nk)
+    out, lse = c.run()
+    c.check(f"{kind} {nq} {nk}", out, lse)
+    again, lse2 = c.run()
+    assert torch.equal(out, again) and torch.equal(lse, lse2)
+
+
 def test_rows_that_see_nothing():
     c = Case("float16", 4, 2, 64, [40, 300], [17, 0])
     out, lse = c.run()
