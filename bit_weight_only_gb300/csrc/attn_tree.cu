@@ -758,10 +758,23 @@ __global__ void __launch_bounds__(128) tree_join_kernel(const TreeArgs a) {
 #pragma unroll
   for (int c = 0; c < D / 32; ++c) acc[c] = 0.f;
   for (int c0 = b0; c0 <= b1; c0 += 32) {
+    const int n = min(32, b1 - c0 + 1);
+    // sixteen parts in flight at a time, the first beside their m and l
+    float x[16][D / 32];
+    auto fetch = [&](int k0) {
+#pragma unroll
+      for (int k = 0; k < 16; ++k) {
+        if (k0 + k >= n) break;
+        const float* part = tree_slot(p, c0 + k0 + k, c0 + k0 + k == b0, D) + (r % ROWS) * D + lane * (D / 32);
+        if constexpr (D == 128) *reinterpret_cast<float4*>(x[k]) = *reinterpret_cast<const float4*>(part);
+        else *reinterpret_cast<float2*>(x[k]) = *reinterpret_cast<const float2*>(part);
+      }
+    };
     float2 ml = make_float2(-INFINITY, 0.f);
     const int mine = c0 + lane;
     if (mine <= b1)
       ml = *reinterpret_cast<const float2*>(tree_slot(p, mine, mine == b0, D) + kSlotRows * D + 2 * (r % ROWS));
+    fetch(0);
     float top = ml.x;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(full, top, o));
@@ -772,17 +785,16 @@ __global__ void __launch_bounds__(128) tree_join_kernel(const TreeArgs a) {
     l *= g;
 #pragma unroll
     for (int c = 0; c < D / 32; ++c) acc[c] *= g;
-    const int n = min(32, b1 - c0 + 1);
-#pragma unroll 8
-    for (int k = 0; k < n; ++k) {
-      const float fk = __shfl_sync(full, f, k);
-      l += __shfl_sync(full, ml.y, k) * fk;
-      const float* part = tree_slot(p, c0 + k, c0 + k == b0, D) + (r % ROWS) * D + lane * (D / 32);
-      float x[D / 32];
-      if constexpr (D == 128) *reinterpret_cast<float4*>(x) = *reinterpret_cast<const float4*>(part);
-      else *reinterpret_cast<float2*>(x) = *reinterpret_cast<const float2*>(part);
+    for (int k0 = 0; k0 < n; k0 += 16) {
+      if (k0 > 0) fetch(k0);
 #pragma unroll
-      for (int c = 0; c < D / 32; ++c) acc[c] += x[c] * fk;
+      for (int k = 0; k < 16; ++k) {
+        if (k0 + k >= n) break;
+        const float fk = __shfl_sync(full, f, k0 + k);
+        l += __shfl_sync(full, ml.y, k0 + k) * fk;
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c) acc[c] += x[k][c] * fk;
+      }
     }
   }
   const float inv = l == 0.f ? 0.f : 1.f / l;
