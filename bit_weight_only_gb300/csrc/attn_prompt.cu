@@ -768,10 +768,23 @@ __global__ void __launch_bounds__(128) prompt_join_kernel(const PromptArgs a) {
 #pragma unroll
   for (int c = 0; c < D / 32; ++c) acc[c] = 0.f;
   for (int c0 = b0; c0 <= b1; c0 += 32) {
+    const int n = min(32, b1 - c0 + 1);
+    // eight parts in flight at a time, the first beside their m and l
+    float x[8][D / 32];
+    auto fetch = [&](int k0) {
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        if (k0 + k >= n) break;
+        const float* part = part_slot(p, 2 * (c0 + k0 + k) + (c0 + k0 + k == b0 ? 1 : 0), D) + rr * D + lane * (D / 32);
+        if constexpr (D == 128) *reinterpret_cast<float4*>(x[k]) = *reinterpret_cast<const float4*>(part);
+        else *reinterpret_cast<float2*>(x[k]) = *reinterpret_cast<const float2*>(part);
+      }
+    };
     float2 ml = make_float2(-INFINITY, 0.f);
     const int mine = c0 + lane;
     if (mine <= b1)
       ml = *reinterpret_cast<const float2*>(part_slot(p, 2 * mine + (mine == b0 ? 1 : 0), D) + kRowsPerBlock * D + 2 * rr);
+    fetch(0);
     float top = ml.x;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(full, top, o));
@@ -782,17 +795,16 @@ __global__ void __launch_bounds__(128) prompt_join_kernel(const PromptArgs a) {
     l *= g;
 #pragma unroll
     for (int c = 0; c < D / 32; ++c) acc[c] *= g;
-    const int n = min(32, b1 - c0 + 1);
-#pragma unroll 4
-    for (int k = 0; k < n; ++k) {
-      const float fk = __shfl_sync(full, f, k);
-      l += __shfl_sync(full, ml.y, k) * fk;
-      const float* src = part_slot(p, 2 * (c0 + k) + (c0 + k == b0 ? 1 : 0), D) + rr * D + lane * (D / 32);
-      float x[D / 32];
-      if constexpr (D == 128) *reinterpret_cast<float4*>(x) = *reinterpret_cast<const float4*>(src);
-      else *reinterpret_cast<float2*>(x) = *reinterpret_cast<const float2*>(src);
+    for (int k0 = 0; k0 < n; k0 += 8) {
+      if (k0 > 0) fetch(k0);
 #pragma unroll
-      for (int c = 0; c < D / 32; ++c) acc[c] += x[c] * fk;
+      for (int k = 0; k < 8; ++k) {
+        if (k0 + k >= n) break;
+        const float fk = __shfl_sync(full, f, k0 + k);
+        l += __shfl_sync(full, ml.y, k0 + k) * fk;
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c) acc[c] += x[k][c] * fk;
+      }
     }
   }
   const float inv = l == 0.f ? 0.f : 1.f / l;

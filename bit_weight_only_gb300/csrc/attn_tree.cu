@@ -38,7 +38,7 @@ namespace qgemv {
 namespace {
 
 constexpr int kNarrowRows = 32;  // rows of a pass, at most
-constexpr int64_t kWholeTokens = 1024;
+constexpr int64_t kWholeTokens = 768;
 constexpr int kErrTree = 32;
 constexpr float kLazyT = 8.f;
 constexpr int kRingBytes = 100 * 1024;
@@ -854,7 +854,9 @@ cudaError_t launch_attn_tree(const TreeParams& p, cudaStream_t s) {
   // 16000 tokens 83 us against 93, two of 131000 179 against 167), but for
   // contexts that are not split (16 of up to 1000: 27 against 22).
   // Contexts of up to kWholeTokens positions (as the caller bounds them) are
-  // not split: a second kernel would take longer than the split saves.
+  // not split: a second kernel would take longer than the split saves (one
+  // sequence and token, INT8: 700 positions 9.3 us against 10.3 split, 1000
+  // positions 11.1 against 10.7).
   a.whole = p.max_ctx + p.max_new <= kWholeTokens;
   const int narrow = p.cache.format == QGEMV_KV_INT8 && !a.whole ? 2 * kNarrowRows : kNarrowRows;
   if (rows > narrow && p.cache.format != QGEMV_KV_Q4_0) {
@@ -868,7 +870,7 @@ cudaError_t launch_attn_tree(const TreeParams& p, cudaStream_t s) {
   // twice the warps (many row tiles); a few long sequences lose 2-4%.
   a.grid = std::min(kBlocksPerSm * sms, kMaxBlocks);
   a.extra = 32;  // a row tile's start and end: about 32 units of 16 tokens (those 64 sequences: 71 us at 16, 54 at 32)
-  a.min_units = 16 + a.extra;
+  a.min_units = 10 + a.extra;  // a block's share, at least (one sequence of 1500 tokens: 10.9 us, with 16 11.3)
   auto by_rows = [&](auto fmt, auto d) {
     constexpr int F = decltype(fmt)::value, D = decltype(d)::value;
     auto run = [&](auto nt) {
