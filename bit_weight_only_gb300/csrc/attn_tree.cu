@@ -29,6 +29,13 @@
 //
 // A warp's O, m and l live in its registers.  At the end of a segment the
 // warps' results are added in warp order through shared memory.
+//
+// Two sequences of up to 131000 tokens, one token of 64 heads over 8: fp16 140 us
+// (the bytes' floor 137), INT8 84 (71), Q4_0 76 (38).  fp16 and INT8 stream at
+// the copy bandwidth, with about 12 us of start, join and gap around it; Q4_0
+// is held up by instruction issue (decoding V, the products' scales).  With
+// the rows, not the tokens, along the products' 16 rows, half of an instruction
+// was empty at 8 rows: INT8 88 us, Q4_0 110.
 #include <algorithm>
 
 #include "tc_common.cuh"
@@ -845,14 +852,15 @@ cudaError_t launch_attn_tree(const TreeParams& p, cudaStream_t s) {
   while ((1 << a.page_shift) < p.cache.page_tokens) ++a.page_shift;
   a.grid = sms < kMaxBlocks ? sms : kMaxBlocks;
   const int64_t rows = static_cast<int64_t>(p.max_new) * a.G;
-  // Up to 32 rows this file's kernel is faster (two sequences of up to 131000
-  // tokens, INT8: 8 rows 87 us against 177, 32 rows 124 against 161).  Beyond
-  // it needs several tiles and passes over the cache.  fp16: the wide kernel is
-  // faster from there (those sequences, 40 rows: 115 us against 135; 64 rows: 150
-  // against 229).  INT8, whose codes the wide kernel has to write out as fp16
-  // first: two passes are no slower on the whole (64 rows: 16 sequences of up to
-  // 16000 tokens 83 us against 93, two of 131000 179 against 167), but for
-  // contexts that are not split (16 of up to 1000: 27 against 22).
+  // Up to 32 rows this file's kernel is faster on the whole (two sequences of up
+  // to 131000 tokens, INT8: 8 rows 84 us against 146, 32 rows 120 against 152;
+  // fp16 of 32 rows 152 against 149).  Beyond it needs several tiles and passes
+  // over the cache.  fp16: the wide kernel is faster from there (those
+  // sequences, 40 rows: 113 us against 133; 64 rows: 148 against 230).  INT8,
+  // whose codes the wide kernel has to write out as fp16 first: two passes are
+  // no slower on the whole (64 rows: 16 sequences of up to 16000 tokens 82 us
+  // against 92, two of 131000 176 against 164), but for contexts that are not
+  // split (one of up to 700: 20 against 18).
   // Contexts of up to kWholeTokens positions (as the caller bounds them) are
   // not split: a second kernel would take longer than the split saves (one
   // sequence and token, INT8: 700 positions 9.3 us against 10.3 split, 1000
@@ -866,10 +874,10 @@ cudaError_t launch_attn_tree(const TreeParams& p, cudaStream_t s) {
     return e != cudaSuccess || a.whole ? e : launch_join<64, 128>(a, s);
   }
   // Two blocks per SM, so that one's starts and ends of row tiles run beside
-  // the other's stream: 64 ragged INT8 sequences 54 us against 68 with one of
-  // twice the warps (many row tiles); a few long sequences lose 2-4%.
+  // the other's stream: 64 ragged INT8 sequences of up to 4000 tokens 49 us
+  // against 70 with one of twice the warps (many row tiles); a few long sequences lose up to 3%.
   a.grid = std::min(kBlocksPerSm * sms, kMaxBlocks);
-  a.extra = 32;  // a row tile's start and end: about 32 units of 16 tokens (those 64 sequences: 71 us at 16, 54 at 32)
+  a.extra = 32;  // a row tile's start and end: about 32 units of 16 tokens (those 64 sequences: 64 us at 16, 49 at 32)
   a.min_units = 10 + a.extra;  // a block's share, at least (one sequence of 1500 tokens: 10.9 us, with 16 11.3)
   auto by_rows = [&](auto fmt, auto d) {
     constexpr int F = decltype(fmt)::value, D = decltype(d)::value;
