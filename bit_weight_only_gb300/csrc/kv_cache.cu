@@ -7,11 +7,12 @@
 // address are shared by few lanes, d / 8; quantisers work without divisions or
 // conversions per value.  A warp takes eight (head, K or V) rows of one token
 // and has all of their loads in flight together.  20463 tokens of 32 heads of
-// 128, fp32 rows into an INT8 cache and back as fp16: 228 us, 0.89 of the copy
-// bandwidth (writing 140, with DRAM 75% busy, reading 89, with issue slots 80%);
+// 128, fp32 rows into an INT8 cache and back as fp16: 219 us, 0.92 of the copy
+// bandwidth;
 // a chunk into an fp16 cache and all of it back: 0.98.
 #include <type_traits>
 
+#include "tc_common.cuh"
 #include "kv_layout.cuh"
 
 namespace qgemv {
@@ -44,10 +45,6 @@ struct Raw {
   }
 };
 
-__device__ __forceinline__ uint32_t half_bits(float lo, float hi) {
-  return __half_as_ushort(__float2half_rn(lo)) | static_cast<uint32_t>(__half_as_ushort(__float2half_rn(hi))) << 16;
-}
-
 // round(fl32(x / a)) of eight values, by products with about 1 / a: those are
 // off by some units in the last place of at most 128, below 1e-4, so that only
 // a result within 1e-4 of a tie could round otherwise; then (and where NaN or
@@ -58,14 +55,19 @@ __device__ __forceinline__ void round_quotients(const float (&x)[8], float a, ui
   constexpr float kShift = 12582912.f;  // 1.5 * 2^23
   float inv;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(a));
-  bool sure = true;
+  const uint64_t inv2 = pack2(inv, inv), up = pack2(kShift, kShift), down = pack2(-kShift, -kShift), less = pack2(-1.f, -1.f);
+  float worst = 0.f;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const float r = x[i] * inv, t = r + kShift;
-    q[i] = __float_as_uint(t);
-    const float d = fabsf(r - (t - kShift));
-    sure = sure && d < 0.4999f;
+  for (int i = 0; i < 8; i += 2) {
+    const uint64_t r = mul2(pack2(x[i], x[i + 1]), inv2), t = add2(r, up);
+    float y, z;
+    unpack2(t, y, z);
+    q[i] = __float_as_uint(y), q[i + 1] = __float_as_uint(z);
+    unpack2(fma2(add2(t, down), less, r), y, z);
+    worst = fmaxf(worst, fmaxf(fabsf(y), fabsf(z)));
   }
+  // (where a result is NaN, 1 / a is infinite or NaN: x / a is at most 127)
+  const bool sure = worst < 0.4999f && fabsf(inv) < INFINITY;
   if (!sure) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
@@ -89,7 +91,7 @@ __device__ __forceinline__ void encode(uint8_t* b, bool v, int tok, int d0, cons
   if constexpr (FMT == QGEMV_KV_F16) {
     if (on)
       *reinterpret_cast<uint4*>(b + (v ? L::v_off(tok, 2 * d0) : L::k_off(tok, 2 * d0))) =
-          make_uint4(half_bits(x[0], x[1]), half_bits(x[2], x[3]), half_bits(x[4], x[5]), half_bits(x[6], x[7]));
+          make_uint4(half_pair(x[0], x[1]), half_pair(x[2], x[3]), half_pair(x[4], x[5]), half_pair(x[6], x[7]));
   } else if constexpr (FMT == QGEMV_KV_INT8) {
     // magnitudes compare as integers, infinities and NaN above all numbers
     uint32_t m = 0;
@@ -227,16 +229,22 @@ struct Eight {
     }
   }
   __device__ void values(float (&x)[8]) const {
+    if constexpr (FMT != QGEMV_KV_F16) {
+      // 2^23 + code + offset as a pattern, no conversion
+      const float off = FMT == QGEMV_KV_INT8 ? -8388736.f : -8388616.f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      if constexpr (FMT == QGEMV_KV_F16) {
+      for (int i = 0; i < 8; i += 2) {
+        auto bits = [&](int e) {
+          return __uint_as_float(FMT == QGEMV_KV_INT8 ? __byte_perm(e < 4 ? w.x : w.y, 0x4B000000u, 0x7540 + (e & 3))
+                                                      : ((w.x >> (4 * e)) & 15u) | 0x4B000000u);
+        };
+        unpack2(mul2(add2(pack2(bits(i), bits(i + 1)), pack2(off, off)), pack2(s, s)), x[i], x[i + 1]);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
         const uint32_t u = (&w.x)[i >> 1];
         x[i] = __half2float(__ushort_as_half(static_cast<unsigned short>(i & 1 ? u >> 16 : u & 0xffffu)));
-      } else if constexpr (FMT == QGEMV_KV_INT8) {
-        // 2^23 + code + 128 as a pattern, no conversion
-        x[i] = (__uint_as_float(__byte_perm(i < 4 ? w.x : w.y, 0x4B000000u, 0x7540 + (i & 3))) - 8388736.f) * s;
-      } else {
-        x[i] = (__uint_as_float(((w.x >> (4 * i)) & 15u) | 0x4B000000u) - 8388616.f) * s;
       }
     }
   }
@@ -252,10 +260,9 @@ __device__ __forceinline__ void store_values(T* dst, const float (&x)[8]) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       if constexpr (std::is_same<T, __half>::value) {
-        w[i] = half_bits(x[2 * i], x[2 * i + 1]);
+        w[i] = half_pair(x[2 * i], x[2 * i + 1]);
       } else {
-        w[i] = __bfloat16_as_ushort(__float2bfloat16_rn(x[2 * i])) |
-               static_cast<uint32_t>(__bfloat16_as_ushort(__float2bfloat16_rn(x[2 * i + 1]))) << 16;
+        w[i] = cvt_pair<true>(x[2 * i], x[2 * i + 1]);
       }
     }
     *reinterpret_cast<uint4*>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
