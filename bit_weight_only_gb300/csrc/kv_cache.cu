@@ -8,8 +8,7 @@
 // conversions per value.  A warp takes eight (head, K or V) rows of one token
 // and has all of their loads in flight together.  20463 tokens of 32 heads of
 // 128, fp32 rows into an INT8 cache and back as fp16: 219 us, 0.92 of the copy
-// bandwidth;
-// a chunk into an fp16 cache and all of it back: 0.98.
+// bandwidth; a chunk into an fp16 cache and all of it back: 0.98.
 #include <type_traits>
 
 #include "tc_common.cuh"
