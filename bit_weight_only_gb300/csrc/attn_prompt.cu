@@ -39,9 +39,9 @@
 // What bounds it: both operands of Q K^T come from shared memory, whose
 // bandwidth the products take whole, and the softmax warps need nearly as long
 // for their exponentials (heads of 64: longer).  fp16, 64 heads of 128 over 8:
-// one prompt of 16384 tokens 2.91 ms, 1513 TFLOP/s (0.81 of the library's dense
-// bf16 product); one of 8192 0.75 ms (0.78); four packed ones of up to 4000,
-// bf16, 0.30 ms (0.72).
+// one prompt of 16384 tokens 2.83 ms, 1553 TFLOP/s (0.83 of the library's dense
+// bf16 product); one of 8192 0.73 ms (0.81); four packed ones of up to 4000,
+// bf16, 0.29 ms (0.75).
 //
 // Every wait is bounded; on a timeout the block records the error, waits for
 // its own copies and MMAs, frees tensor memory and returns.
@@ -319,7 +319,9 @@ prompt_kernel(const PromptArgs a, const __grid_constant__ CUtensorMap qmap, cons
 
   Piece pc;
   if (warp >= 8) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+    // 128 x 72 + 256 x 216 registers: the 384 x 168 of the launch.  The softmax
+    // warps hold 128 scores each (88 and 208: packed prompts 302 us against 289)
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
     if (warp == 8) {
       // ---- pieces; K and V tiles
       int* counters = reinterpret_cast<int*>(p.ws) + 1;  // next piece, blocks that are done
@@ -558,7 +560,7 @@ prompt_kernel(const PromptArgs a, const __grid_constant__ CUtensorMap qmap, cons
       }
     }
   } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
     // ---- softmax warpgroup i, a thread for each row
     const int i = warp >> 2, wt = tid & 127;
     const uint32_t t_lane = static_cast<uint32_t>(32 * (warp & 3)) << 16;
@@ -878,7 +880,7 @@ cudaError_t launch(const PromptParams& p, cudaStream_t s) {
   // Whole pieces, or runs: whichever makes the busiest block's share of the keys
   // less.  The lengths are known as averages only; either is right.  (Two chunks
   // of up to 300 tokens after 6000, 96 pieces: 67 us by runs, 81 whole; one of
-  // 512 after 6000, 128 pieces: 93 by runs, 82 whole.)
+  // 512 after 6000, 128 pieces: 93 by runs, 80 whole.)
   const double busy = std::ceil(static_cast<double>(p.n_q) / (2 * a.tokens) / p.n_seqs) * p.n_seqs * p.kv_heads;
   const double most = static_cast<double>(p.n_k) / p.n_seqs / kKeys;  // key tiles of a sequence's last piece
   const double mean = std::max(1.0, (p.n_k - 0.5 * p.n_q) / p.n_seqs / kKeys) + kStartTiles;
