@@ -10,7 +10,7 @@
 // a block.  Inside the code regions the bytes lie so that the attention's
 // matrix operands are read from shared memory by the widest loads without
 // bank conflicts (lane = 4g + t; one MMA step takes 4 values of k from each
-// of the four t and column n from each of the eight g):
+// of the four t and a row from each of the eight g):
 //   * fp16, K and V: chunks of 64 values, each 16 rows of 128 bytes in the
 //     128-byte swizzle (16-byte unit u of token r at u ^ (r & 7)): what the
 //     tensor cores read, as a descriptor operand or by ldmatrix.
