@@ -851,7 +851,8 @@ cudaError_t launch_attn_tree(const TreeParams& p, cudaStream_t s) {
   a.page_shift = 0;
   while ((1 << a.page_shift) < p.cache.page_tokens) ++a.page_shift;
   a.grid = sms < kMaxBlocks ? sms : kMaxBlocks;
-  const int64_t rows = static_cast<int64_t>(p.max_new) * a.G;
+  // (hints may be 0: one token is the least that a call has)
+  const int64_t rows = std::max<int64_t>(1, p.max_new) * a.G;
   // Up to 32 rows this file's kernel is faster on the whole (two sequences of up
   // to 131000 tokens, INT8: 8 rows 84 us against 146, 32 rows 120 against 152;
   // fp16 of 32 rows 152 against 149).  Beyond it needs several tiles and passes
@@ -865,7 +866,7 @@ cudaError_t launch_attn_tree(const TreeParams& p, cudaStream_t s) {
   // not split: a second kernel would take longer than the split saves (one
   // sequence and token, INT8: 700 positions 9.3 us against 10.3 split, 1000
   // positions 11.1 against 10.7).
-  a.whole = p.max_ctx + p.max_new <= kWholeTokens;
+  a.whole = static_cast<int64_t>(p.max_ctx) + p.max_new <= kWholeTokens;
   const int narrow = p.cache.format == QGEMV_KV_INT8 && !a.whole ? 2 * kNarrowRows : kNarrowRows;
   if (rows > narrow && p.cache.format != QGEMV_KV_Q4_0) {
     a.extra = 4;  // a row tile's start and end: about four units of 128 tokens
