@@ -689,9 +689,10 @@ prompt_kernel(const PromptArgs a, const __grid_constant__ CUtensorMap qmap, cons
             for (int e = 0; e < 32; ++e) {
               auto seen = [&](int x) { return (use0 && bad0[x] < my_sees) || (use1 && bad1[x] < my_sees); };
               const bool nan = seen(c + e), up = seen(D + c + e), down = seen(2 * D + c + e);
+              // added: O may hold infinities and NaN of other tiles, or of the scores
               if (nan || (up && down)) o[e] = 0x7fffffffu;
-              else if (up) o[e] = 0x7f800000u;
-              else if (down) o[e] = 0xff800000u;
+              else if (up) o[e] = __float_as_uint(__uint_as_float(o[e]) + INFINITY);
+              else if (down) o[e] = __float_as_uint(__uint_as_float(o[e]) - INFINITY);
             }
           }
           // through shared memory, so that a store covers whole sectors: 32 rows of
