@@ -574,7 +574,11 @@ prompt_kernel(const PromptArgs a, const __grid_constant__ CUtensorMap qmap, cons
       const int n = i == 0 ? pc.n[0] : pc.n[1], t0 = RUNS ? pc.t0 : 0;
       const int my_sees = pc.sees(min(pc.tok0 + i * a.tokens + tok_l, pc.nq - 1));
       const int all_see = pc.sees(pc.tok0 + i * a.tokens);  // what every row of the tile sees
-      float m = -INFINITY, l = 0.f;
+      // A row that is no query of the piece (past the tile's tokens Q is what an
+      // earlier call left there, past the sequence's another's) takes no part in
+      // the warp's votes on the reference: no score passes +inf.  What it computes
+      // is not stored.
+      float m = wt < a.tokens * G && pc.tok0 + i * a.tokens + tok_l < pc.nq ? -INFINITY : INFINITY, l = 0.f;
       for (int j = 0; j < n; ++j, ++n_s) {
         ok = wait_all(kBS + i, n_s & 1);
         if (!ok) break;

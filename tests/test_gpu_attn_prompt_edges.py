@@ -91,3 +91,43 @@ def test_nan_scores_stay_beside_an_infinite_value(kind, d):
     out, lse = attend(q, k, v, [300], [300])
     assert torch.isnan(out[10:, :2]).all() and torch.isnan(lse[10:, :2]).all()
     assert torch.isfinite(out[:10]).all() and torch.isfinite(out[:, 2:]).all()
+
+
+@pytest.mark.parametrize("kind", list(KINDS))
+@pytest.mark.parametrize("hq, hkv, d, nq, nk", [
+    (40, 8, 128, [50] * 20, [1500] * 20),     # groups of 5: 125 rows of a tile of 128
+    (5, 1, 128, [50, 9], [3000, 700]),        # shared by several blocks
+    (21, 3, 64, [36] * 20, [1500] * 20),      # of 7: 126
+    (3, 1, 64, [300], [300]),
+])
+def test_the_same_bits_whatever_ran_before(kind, hq, hkv, d, nq, nk):
+    """Rows of a tile that belong to no query hold what an earlier call left there: here zeros, or values whose scores grow
+    along the keys, so that they would move the softmax reference of the rows beside them."""
+    dt = KINDS[kind]
+    q, k, v = rows(1, sum(nq), hq, d, dt), rows(2, sum(nk), hkv, d, dt), rows(3, sum(nk), hkv, d, dt)
+    at = torch.cat([torch.arange(n, device="cuda") for n in nk])
+    k[:, :, 0] = (0.02 * at).to(dt)[:, None]
+    q[:, :, 0] = 0
+    got = []
+    for left in (0.0, 64.0, -64.0):
+        before = torch.zeros(1024, 64, d, dtype=dt, device="cuda")
+        before[:, :, 0] = left
+        attend(before, before, before, [1024], [1024])   # 64 heads of their own: every tile of every block is full
+        got.append(attend(q, k, v, nq, nk))
+    for out, lse in got[1:]:
+        assert torch.equal(out, got[0][0]) and torch.equal(lse, got[0][1])
+
+
+def test_rows_of_other_sequences_do_not_reach_a_result():
+    """The rows past the packed queries, and a neighbour's, may hold anything."""
+    nq, nk = [30, 20], [700, 900]
+    q, k, v = rows(1, 60, 5, 128, torch.float16), rows(2, 1600, 1, 128, torch.float16), rows(3, 1600, 1, 128, torch.float16)
+    k[:, :, 0] = (0.02 * torch.arange(1600, device="cuda")).half()[:, None]
+    q[:, :, 0] = 0
+    want, lse = attend(q, k, v, nq, nk)
+    q[50:, :, 0] = 64.0
+    out, lse2 = attend(q, k, v, nq, nk)
+    assert torch.equal(out[:50], want[:50]) and torch.equal(lse[:50], lse2[:50])
+    q[30:50, :, 0] = 64.0
+    out, _ = attend(q, k, v, nq, nk)
+    assert torch.equal(out[:30], want[:30])
