@@ -605,9 +605,7 @@ class KVCache:
         else:
             _index("lse", lse, torch.float32, (n, heads))
         if masks is not None:
-            if masks.dtype != torch.uint64:
-                _index("masks", masks, torch.int64, (n,))
-            masks = masks.data_ptr()
+            masks = _index("masks", masks, torch.uint64 if masks.dtype == torch.uint64 else torch.int64, (n,))
         n_seqs, stride = table.shape
         _call(_lib.qgemv_attn_tree, self._ref, _index("table", table, torch.int32, (n_seqs, stride)), stride, n_seqs,
               _index("ctx_lens", ctx_lens, torch.int32, (n_seqs,)), *_rows("q", q, heads, self.head_dim), heads,
