@@ -50,6 +50,7 @@
 #include <type_traits>
 
 #include "kv_layout.cuh"
+#include "per_device.h"
 #include "tc_common.cuh"
 
 namespace qgemv {
@@ -834,14 +835,18 @@ using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, voi
                               CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
 
 EncodeFn encode_fn() {
-  static EncodeFn fn = [] {
-    void* f = nullptr;
-    cudaDriverEntryPointQueryResult r;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &r) != cudaSuccess ||
-        r != cudaDriverEntryPointSuccess)
-      f = nullptr;
-    return reinterpret_cast<EncodeFn>(f);
-  }();
+  static std::atomic<EncodeFn> known{nullptr};  // of the driver, the same for every device
+  EncodeFn fn = known.load(std::memory_order_relaxed);
+  if (fn) return fn;
+  void* f = nullptr;
+  cudaDriverEntryPointQueryResult r;
+  if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &r) != cudaSuccess ||
+      r != cudaDriverEntryPointSuccess) {
+    cudaGetLastError();
+    return nullptr;
+  }
+  fn = reinterpret_cast<EncodeFn>(f);
+  known.store(fn, std::memory_order_relaxed);
   return fn;
 }
 
@@ -875,12 +880,9 @@ cudaError_t launch(const PromptParams& p, cudaStream_t s) {
     if (e == cudaSuccess) e = make_map(&vm, p.v, D, p.kv_heads, p.n_k, BF16, 1, kKeys);
     if (e != cudaSuccess) return e;
   }
-  static const int sms = [] {
-    int dev = 0, n = 0;
-    cudaGetDevice(&dev);
-    cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
-    return n;
-  }();
+  int dev = 0, sms = 0;
+  const cudaError_t found = current_device(&dev, &sms);
+  if (found != cudaSuccess) return found;
   const int64_t pieces = static_cast<int64_t>(a.n_slots) * p.kv_heads;
   // Whole pieces, or runs: whichever makes the busiest block's share of the keys
   // less.  The lengths are known as averages only; either is right.  (Two chunks
@@ -893,9 +895,9 @@ cudaError_t launch(const PromptParams& p, cudaStream_t s) {
   const double runs = busy * mean / sms + kStartTiles + kJoinTiles;
   auto run = [&](auto by_runs, int64_t blocks) {
     constexpr bool RUNS = decltype(by_runs)::value;
-    static const cudaError_t attr =
-        cudaFuncSetAttribute(prompt_kernel<D, BF16, RUNS>, cudaFuncAttributeMaxDynamicSharedMemorySize, Smem<D>::kBytes);
-    if (attr != cudaSuccess) return attr;
+    static std::atomic<uint64_t> set;
+    const cudaError_t e = allow_shared_memory(set, dev, prompt_kernel<D, BF16, RUNS>, Smem<D>::kBytes);
+    if (e != cudaSuccess) return e;
     prompt_kernel<D, BF16, RUNS>
         <<<static_cast<unsigned>(std::min<int64_t>(blocks, sms)), kThreads, Smem<D>::kBytes, s>>>(a, qm, km, vm);
     return cudaGetLastError();

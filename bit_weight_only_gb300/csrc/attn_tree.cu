@@ -38,6 +38,7 @@
 // was empty at 8 rows: INT8 88 us, Q4_0 110.
 #include <algorithm>
 
+#include "per_device.h"
 #include "tc_common.cuh"
 #include "tree_work.cuh"
 
@@ -813,12 +814,12 @@ __global__ void __launch_bounds__(128) tree_join_kernel(const TreeArgs a) {
 }
 
 template <int FMT, int D, int NT>
-cudaError_t launch(const TreeArgs& a, cudaStream_t s) {
+cudaError_t launch(const TreeArgs& a, int dev, cudaStream_t s) {
   using Sh = TreeShape<FMT, D, NT>;
   static_assert(Sh::kStages >= 2 && Sh::kBytes <= 113 * 1024, "shared memory of a block");
-  static const cudaError_t attr =
-      cudaFuncSetAttribute(tree_kernel<FMT, D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, Sh::kBytes);
-  if (attr != cudaSuccess) return attr;
+  static std::atomic<uint64_t> set;
+  const cudaError_t e = allow_shared_memory(set, dev, tree_kernel<FMT, D, NT>, Sh::kBytes);
+  if (e != cudaSuccess) return e;
   tree_kernel<FMT, D, NT><<<a.grid, Sh::kThreads, Sh::kBytes, s>>>(a);
   return cudaGetLastError();
 }
@@ -838,13 +839,9 @@ int64_t tree_ws_bytes(int head_dim) {
 }
 
 cudaError_t launch_attn_tree(const TreeParams& p, cudaStream_t s) {
-  static const int sms = [] {
-    int dev = 0, n = 0;
-    cudaGetDevice(&dev);
-    cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
-    return n;
-  }();
-  if (sms <= 0) return cudaErrorInvalidDevice;
+  int dev = 0, sms = 0;
+  const cudaError_t found = current_device(&dev, &sms);
+  if (found != cudaSuccess) return found;
   TreeArgs a;
   a.p = p;
   a.G = p.q_heads / p.cache.kv_heads;
@@ -871,7 +868,7 @@ cudaError_t launch_attn_tree(const TreeParams& p, cudaStream_t s) {
   if (rows > narrow && p.cache.format != QGEMV_KV_Q4_0) {
     a.extra = 4;  // a row tile's start and end: about four units of 128 tokens
     a.min_units = 2 + a.extra;
-    const cudaError_t e = launch_tree_wide(a, s);
+    const cudaError_t e = launch_tree_wide(a, dev, s);
     return e != cudaSuccess || a.whole ? e : launch_join<64, 128>(a, s);
   }
   // Two blocks per SM, so that one's starts and ends of row tiles run beside
@@ -884,7 +881,7 @@ cudaError_t launch_attn_tree(const TreeParams& p, cudaStream_t s) {
     constexpr int F = decltype(fmt)::value, D = decltype(d)::value;
     auto run = [&](auto nt) {
       constexpr int NT = decltype(nt)::value;
-      const cudaError_t e = launch<F, D, NT>(a, s);
+      const cudaError_t e = launch<F, D, NT>(a, dev, s);
       return e != cudaSuccess || a.whole ? e : launch_join<8 * NT, kKvBlockTokens>(a, s);
     };
     // the smallest tiles that take the rows in as few passes over the cache

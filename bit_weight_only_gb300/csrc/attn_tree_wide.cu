@@ -38,6 +38,7 @@
 // its own copies and MMAs, frees tensor memory and returns.
 #include <type_traits>
 
+#include "per_device.h"
 #include "tc_common.cuh"
 #include "tree_work.cuh"
 
@@ -726,21 +727,21 @@ __global__ void __launch_bounds__(kThreads, 1) tree_wide_kernel(const TreeArgs a
 }
 
 template <int FMT, int D>
-cudaError_t launch(const TreeArgs& a, cudaStream_t s) {
+cudaError_t launch(const TreeArgs& a, int dev, cudaStream_t s) {
   using S = Wide<FMT, D>;
-  static const cudaError_t attr =
-      cudaFuncSetAttribute(tree_wide_kernel<FMT, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kBytes);
-  if (attr != cudaSuccess) return attr;
+  static std::atomic<uint64_t> set;
+  const cudaError_t e = allow_shared_memory(set, dev, tree_wide_kernel<FMT, D>, S::kBytes);
+  if (e != cudaSuccess) return e;
   tree_wide_kernel<FMT, D><<<a.grid, kThreads, S::kBytes, s>>>(a);
   return cudaGetLastError();
 }
 
 }  // namespace
 
-cudaError_t launch_tree_wide(const TreeArgs& a, cudaStream_t s) {
+cudaError_t launch_tree_wide(const TreeArgs& a, int dev, cudaStream_t s) {
   auto by_dim = [&](auto fmt) {
     constexpr int F = decltype(fmt)::value;
-    return a.p.cache.head_dim == 64 ? launch<F, 64>(a, s) : launch<F, 128>(a, s);
+    return a.p.cache.head_dim == 64 ? launch<F, 64>(a, dev, s) : launch<F, 128>(a, dev, s);
   };
   switch (a.p.cache.format) {
     case QGEMV_KV_F16: return by_dim(std::integral_constant<int, QGEMV_KV_F16>());

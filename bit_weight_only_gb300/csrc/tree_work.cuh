@@ -160,6 +160,6 @@ __device__ __forceinline__ float* tree_slot(const TreeParams& p, int block, bool
   return reinterpret_cast<float*>(p.ws + kWsHeaderBytes) + (2 * block + (begins ? 1 : 0)) * slot_floats(D);
 }
 
-cudaError_t launch_tree_wide(const TreeArgs& a, cudaStream_t s);
+cudaError_t launch_tree_wide(const TreeArgs& a, int dev, cudaStream_t s);
 
 }  // namespace qgemv

@@ -32,3 +32,46 @@ answer(out)
         assert ("join" in kernels[-1]) == (ctx + new > 768), (hint, kernels)
     for ctx in (0, 5000):
         assert got[f"{ctx} 0"] == got[f"{ctx} 1"]
+
+
+CALLS = {"tree narrow": ("tree('int8', max_new=2)", "tree_kernel"), "tree wide": ("tree('f16', max_new=60)", "tree_wide_kernel"),
+         "prompt": ("prompt(n_q=65536, n_k=65536)", "prompt_kernel"), "prompt by runs": ("prompt(n_seqs=2, n_q=600, n_k=12600)", "prompt_kernel")}
+
+
+@pytest.mark.parametrize("name", list(CALLS))
+def test_devices_are_set_up_each(host, name):
+    """The limit of shared memory is set on every device, once, and the grid is of the device's own SMs (152 and 100)."""
+    call, kernel = CALLS[name]
+    got = host(f"""
+out = []
+for dev in (0, 1, 0, 1):
+    fake.fake_set_device(dev)
+    out.append([{call}, notes()])
+answer(out)
+""")
+    for k, (rc, notes) in enumerate(got):
+        dev = k % 2
+        assert rc == 0
+        sets = [n for n in notes if n[0] == "attribute"]
+        assert [n[1] for n in sets] == [str(dev)] * (k < 2), "set on the device, the first time"
+        main = next(n for n in notes if n[0] == "launch" and kernel in n[-1])
+        sms = (152, 100)[dev]
+        assert main[1] == str(dev) and int(main[2]) in (sms, 2 * sms)
+        if k < 2:
+            assert int(main[4]) == int(sets[0][3]) > 48 * 1024
+
+
+@pytest.mark.parametrize("name", list(CALLS))
+def test_a_failed_set_up_is_tried_again(host, name):
+    call, kernel = CALLS[name]
+    fails = ["attributes"] if "tree" in name else ["entry_points", "attributes"]
+    got = host(f"""
+out = []
+for kind in {fails}:
+    getattr(fake, "fake_fail_" + kind)(1)
+    out.append({call})
+notes()
+answer([out, {call}, notes()])
+""")
+    assert got[0] == [3] * len(fails)  # QGEMV_ERR_CUDA
+    assert got[1] == 0 and any(n[0] == "launch" and kernel in n[-1] for n in got[2])
