@@ -462,15 +462,28 @@ def _torch():
     return _TORCH
 
 
-def _on(stream):
-    """The address of the stream given, or of torch's current one."""
-    return _current(None) if stream is None else _stream_ptr(stream)
+def _on(stream, dev: int):
+    """The address of the stream given, or of torch's current one of the device."""
+    return _torch()._C._cuda_getCurrentRawStream(dev) if stream is None else _stream_ptr(stream)
 
 
-def _call(fn, *args):
-    rc = fn(*args)
-    if rc:
-        _check(rc)
+def _device_now() -> int:
+    return _torch()._C._cuda_getDevice()
+
+
+def _call(dev: int, fn, *args):
+    """A library call with device `dev` current."""
+    if dev == _device_now():
+        rc = fn(*args)
+    else:
+        with _torch().cuda.device(dev):
+            rc = fn(*args)
+    return _check(rc) if rc else rc
+
+
+def _gpu(what, device) -> None:
+    if _torch().device(device).type != "cuda":
+        raise ValueError(f"{what} must be on a CUDA device, not {device}")
 
 
 def _dtype_code(dtype) -> int:
@@ -484,21 +497,34 @@ def _dtype_code(dtype) -> int:
     return code
 
 
-def _rows(name, t, heads: int, head_dim: int):
-    """(address, token stride, head stride) of a CUDA tensor [n, heads, head_dim], its values contiguous."""
+def _where(dev) -> str:
+    return "" if dev is None else f" on cuda:{dev}"
+
+
+def _rows(name, t, heads: int, head_dim: int, dev: int | None = None):
+    """(address, token stride, head stride) of a CUDA tensor [n, heads, head_dim], its values contiguous; on device `dev`
+    where one is given."""
     shape, strides = t.shape, t.stride()
-    if len(shape) != 3 or shape[1] != heads or shape[2] != head_dim or strides[2] != 1 or not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor [n, {heads}, {head_dim}] with contiguous values, got "
-                         f"{tuple(shape)} with strides {strides} on {t.device}")
+    if (len(shape) != 3 or shape[1] != heads or shape[2] != head_dim or strides[2] != 1
+            or (not t.is_cuda if dev is None else t.get_device() != dev)):
+        raise ValueError(f"{name} must be a CUDA tensor [n, {heads}, {head_dim}] with contiguous values"
+                         f"{_where(dev)}, got {tuple(shape)} with strides {strides} on {t.device}")
     # the stride of a dimension of one element means nothing to torch
     return (t.data_ptr(), strides[0] if shape[0] > 1 else heads * head_dim, strides[1] if heads > 1 else head_dim)
 
 
-def _index(name, t, dtype, shape):
-    if t.dtype != dtype or t.shape != shape or not t.is_cuda or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous CUDA {dtype} tensor of shape {shape}, got {t.dtype} "
+def _index(name, t, dtype, shape, dev: int | None = None):
+    if (t.dtype != dtype or t.shape != shape or not t.is_contiguous()
+            or (not t.is_cuda if dev is None else t.get_device() != dev)):
+        raise ValueError(f"{name} must be a contiguous CUDA {dtype} tensor of shape {shape}{_where(dev)}, got {t.dtype} "
                          f"{tuple(t.shape)} on {t.device}")
     return t.data_ptr()
+
+
+def _ws(workspace, dev: int):
+    if workspace._dev != dev:
+        raise ValueError(f"the workspace must be on cuda:{dev}, not cuda:{workspace._dev}")
+    return workspace.ptr, workspace.nbytes
 
 
 class AttnWorkspace:
@@ -511,17 +537,18 @@ class AttnWorkspace:
         self.nbytes = qgemv_attn_ws_bytes(n_seqs, q_heads, head_dim)
         if self.nbytes == 0:
             raise QgemvError(QGEMV_ERR_ARG, f"no workspace for {n_seqs} sequences of {q_heads} heads of {head_dim}")
+        _gpu("a workspace", device)
         self.buffer = torch.empty(self.nbytes, dtype=torch.uint8, device=device)
-        self.ptr = self.buffer.data_ptr()
+        self.ptr, self._dev = self.buffer.data_ptr(), self.buffer.get_device()
         self.reset()
 
     def reset(self, stream=None):
         """Set the workspace up again (needed only after ``status`` raised)."""
-        qgemv_attn_ws_init(self.ptr, self.nbytes, _current(stream))
+        _call(self._dev, _lib.qgemv_attn_ws_init, self.ptr, self.nbytes, _on(stream, self._dev))
 
     def status(self):
         """Synchronise; raises if a kernel of this workspace gave up a wait."""
-        return qgemv_attn_status(self.ptr)
+        return _call(self._dev, _lib.qgemv_attn_status, self.ptr)
 
 
 class KVCache:
@@ -532,7 +559,8 @@ class KVCache:
     rows into slots, ``read`` gives rows back, ``attend`` is the attention of
     one or several drafted tokens of each sequence over the cached ones.
     Runs are ordered on ``stream`` when one is given, else on torch's current
-    stream."""
+    stream.  Their tensors and the workspace are on the cache's device, which
+    need not be the current one."""
 
     def __init__(self, fmt, n_pages: int, page_tokens: int, kv_heads: int, head_dim: int, device="cuda"):
         import torch
@@ -542,9 +570,10 @@ class KVCache:
         if nbytes == 0:
             raise QgemvError(QGEMV_ERR_ARG, f"invalid cache: {fmt}, {n_pages} pages of {page_tokens} tokens, "
                                             f"{kv_heads} heads of {head_dim}")
+        _gpu("a cache", device)
         self.pages = torch.empty(nbytes, dtype=torch.uint8, device=device)
         self.desc = KvCacheDesc(self.pages.data_ptr(), self.fmt, head_dim, kv_heads, page_tokens, n_pages)
-        self._ref, self.device = ctypes.byref(self.desc), self.pages.device
+        self._ref, self.device, self._dev = ctypes.byref(self.desc), self.pages.device, self.pages.get_device()
 
     def write(self, k, v, slots, stream=None):
         """Quantise the rows k and v [n, kv_heads, head_dim] (fp32, fp16 or
@@ -552,16 +581,16 @@ class KVCache:
         page * page_tokens + place, negative ones are skipped)."""
         if k.dtype != v.dtype or k.shape[0] != v.shape[0]:
             raise ValueError("k and v must have the same type and number of tokens")
-        n = k.shape[0]
-        s = _index("slots", slots, _torch().int64, (n,))
-        _call(_lib.qgemv_kv_write, self._ref, _dtype_code(k.dtype), *_rows("k", k, self.kv_heads, self.head_dim),
-                       *_rows("v", v, self.kv_heads, self.head_dim), s, n, _on(stream))
+        n, dev = k.shape[0], self._dev
+        s = _index("slots", slots, _torch().int64, (n,), dev)
+        _call(dev, _lib.qgemv_kv_write, self._ref, _dtype_code(k.dtype), *_rows("k", k, self.kv_heads, self.head_dim, dev),
+              *_rows("v", v, self.kv_heads, self.head_dim, dev), s, n, _on(stream, dev))
 
     def read(self, table, starts, cu, n_tokens: int, dtype=None, out=None, stream=None):
         """The cached rows of positions starts[b] .. of each sequence, packed
         by cu (int32 [n_seqs + 1]): (k, v) [n_tokens, kv_heads, head_dim] of
         dtype (fp16 unless given).  table: int32 [n_seqs, most pages]."""
-        torch = _torch()
+        torch, dev = _torch(), self._dev
         n_seqs, stride = table.shape
         if out is None:
             shape = n_tokens, self.kv_heads, self.head_dim
@@ -574,10 +603,10 @@ class KVCache:
             if k.dtype != v.dtype or k.shape[0] != n_tokens or v.shape[0] != n_tokens:
                 raise ValueError(f"the outputs must have {n_tokens} tokens of one type")
             dtype = k.dtype
-            rows = *_rows("k", k, self.kv_heads, self.head_dim), *_rows("v", v, self.kv_heads, self.head_dim)
-        _call(_lib.qgemv_kv_read, self._ref, _index("table", table, torch.int32, (n_seqs, stride)), stride, n_seqs,
-              None if starts is None else _index("starts", starts, torch.int32, (n_seqs,)),
-              _index("cu", cu, torch.int32, (n_seqs + 1,)), n_tokens, _dtype_code(dtype), *rows, _on(stream))
+            rows = *_rows("k", k, self.kv_heads, self.head_dim, dev), *_rows("v", v, self.kv_heads, self.head_dim, dev)
+        _call(dev, _lib.qgemv_kv_read, self._ref, _index("table", table, torch.int32, (n_seqs, stride), dev), stride, n_seqs,
+              None if starts is None else _index("starts", starts, torch.int32, (n_seqs,), dev),
+              _index("cu", cu, torch.int32, (n_seqs + 1,), dev), n_tokens, _dtype_code(dtype), *rows, _on(stream, dev))
         return out
 
     def attend(self, q, table, ctx_lens, cu_q, masks=None, *, max_ctx: int, max_new: int, workspace, scale=None,
@@ -589,7 +618,7 @@ class KVCache:
         another.  Returns (out like q, lse fp32 [n, q_heads]).  scale is
         1 / sqrt(head_dim) unless given; max_ctx and max_new bound the
         lengths (they guide the split only)."""
-        torch = _torch()
+        torch, dev = _torch(), self._dev
         n, heads, d = q.shape
         if q.dtype != torch.float16:
             raise ValueError("q must be fp16")
@@ -599,19 +628,19 @@ class KVCache:
         elif out.dtype != torch.float16 or out.shape != q.shape:
             raise ValueError("out must be fp16, shaped like q")
         else:
-            out_rows = _rows("out", out, heads, d)
+            out_rows = _rows("out", out, heads, d, dev)
         if lse is None:
             lse = torch.empty((n, heads), dtype=torch.float32, device=q.device)
         else:
-            _index("lse", lse, torch.float32, (n, heads))
+            _index("lse", lse, torch.float32, (n, heads), dev)
         if masks is not None:
-            masks = _index("masks", masks, torch.uint64 if masks.dtype == torch.uint64 else torch.int64, (n,))
+            masks = _index("masks", masks, torch.uint64 if masks.dtype == torch.uint64 else torch.int64, (n,), dev)
         n_seqs, stride = table.shape
-        _call(_lib.qgemv_attn_tree, self._ref, _index("table", table, torch.int32, (n_seqs, stride)), stride, n_seqs,
-              _index("ctx_lens", ctx_lens, torch.int32, (n_seqs,)), *_rows("q", q, heads, self.head_dim), heads,
-              _index("cu_q", cu_q, torch.int32, (n_seqs + 1,)), n, masks, max_ctx, max_new,
-              d ** -0.5 if scale is None else scale, *out_rows, lse.data_ptr(), workspace.ptr, workspace.nbytes,
-              _on(stream))
+        _call(dev, _lib.qgemv_attn_tree, self._ref, _index("table", table, torch.int32, (n_seqs, stride), dev), stride,
+              n_seqs, _index("ctx_lens", ctx_lens, torch.int32, (n_seqs,), dev),
+              *_rows("q", q, heads, self.head_dim, dev), heads, _index("cu_q", cu_q, torch.int32, (n_seqs + 1,), dev), n,
+              masks, max_ctx, max_new, d ** -0.5 if scale is None else scale, *out_rows, lse.data_ptr(),
+              *_ws(workspace, dev), _on(stream, dev))
         return out, lse
 
 
@@ -619,9 +648,11 @@ def attn_prompt(q, k, v, cu_q, cu_k, *, max_q: int, workspace, scale=None, out=N
     """Causal attention over packed prompts: q [n_q, q_heads, d], k and v
     [n_k, kv_heads, d] (all fp16 or all bf16), sequence b the rows cu_q[b] ..
     of q and cu_k[b] .. of k and v (int32 [n_seqs + 1]); its last query sees
-    all of its keys.  Returns (out like q, lse fp32 [n_q, q_heads])."""
+    all of its keys.  Returns (out like q, lse fp32 [n_q, q_heads]).  All
+    tensors and the workspace are on q's device."""
     torch = _torch()
     n, heads, d = q.shape
+    q_rows, dev = _rows("q", q, heads, d), q.get_device()
     if k.shape[0] != v.shape[0] or not (q.dtype == k.dtype == v.dtype):
         raise ValueError("q, k and v must have one type, k and v the same number of tokens")
     if out is None:
@@ -630,15 +661,15 @@ def attn_prompt(q, k, v, cu_q, cu_k, *, max_q: int, workspace, scale=None, out=N
     elif out.dtype != q.dtype or out.shape != q.shape:
         raise ValueError("out must have q's type and shape")
     else:
-        out_rows = _rows("out", out, heads, d)
+        out_rows = _rows("out", out, heads, d, dev)
     if lse is None:
         lse = torch.empty((n, heads), dtype=torch.float32, device=q.device)
     else:
-        _index("lse", lse, torch.float32, (n, heads))
+        _index("lse", lse, torch.float32, (n, heads), dev)
     n_seqs, kv_heads = cu_q.shape[0] - 1, k.shape[1]
-    _call(_lib.qgemv_attn_prompt, _dtype_code(q.dtype), d, heads, kv_heads, *_rows("q", q, heads, d),
-          *_rows("k", k, kv_heads, d), *_rows("v", v, kv_heads, d), n_seqs,
-          _index("cu_q", cu_q, torch.int32, (n_seqs + 1,)), _index("cu_k", cu_k, torch.int32, (n_seqs + 1,)), n,
-          k.shape[0], max_q, d ** -0.5 if scale is None else scale, *out_rows, lse.data_ptr(), workspace.ptr,
-          workspace.nbytes, _on(stream))
+    _call(dev, _lib.qgemv_attn_prompt, _dtype_code(q.dtype), d, heads, kv_heads, *q_rows,
+          *_rows("k", k, kv_heads, d, dev), *_rows("v", v, kv_heads, d, dev), n_seqs,
+          _index("cu_q", cu_q, torch.int32, (n_seqs + 1,), dev), _index("cu_k", cu_k, torch.int32, (n_seqs + 1,), dev), n,
+          k.shape[0], max_q, d ** -0.5 if scale is None else scale, *out_rows, lse.data_ptr(), *_ws(workspace, dev),
+          _on(stream, dev))
     return out, lse
