@@ -315,6 +315,33 @@ def _current(stream):
     return c._cuda_getCurrentRawStream(c._cuda_getDevice())
 
 
+def _along(stream, dev: int, make):
+    """make() with `stream` as torch's current one, where one is given: what
+    it allocates is memory of that stream, free of other streams' unfinished
+    work, and the tensors that it returns (one, or a tuple) are not handed out
+    again while the stream that was current still uses them."""
+    torch = _torch()
+    if stream is None:
+        return make()
+    ptr = _stream_ptr(stream)
+    if ptr == torch._C._cuda_getCurrentRawStream(dev):
+        return make()
+    with torch.cuda.stream(torch.cuda.ExternalStream(ptr, device=dev) if ptr else torch.cuda.default_stream(dev)):
+        out = make()
+    before = torch.cuda.current_stream(dev)
+    for t in out if isinstance(out, tuple) else (out,):
+        t.record_stream(before)
+    return out
+
+
+def _empty(shape, dtype, dev: int, stream):
+    """A new tensor for a call on `stream`."""
+    empty = _torch().empty
+    if stream is None:
+        return empty(shape, dtype=dtype, device=dev)
+    return _along(stream, dev, lambda: empty(shape, dtype=dtype, device=dev))
+
+
 class QGemv:
     """One packed weight matrix on the GPU.
 
@@ -375,12 +402,16 @@ class QGemv:
 
     def gemv(self, x, stream=None):
         import torch
-        y = torch.empty((x.shape[0], self.N), dtype=torch.float32, device=x.device)
-        return self.run(x.contiguous(), y, stream)
+
+        def make():
+            y = torch.empty((x.shape[0], self.N), dtype=torch.float32, device=x.device)
+            return self.run(x.contiguous(), y)
+        return _along(stream, x.get_device(), make)
 
     def dequant(self, stream=None):
         import torch
-        w = torch.empty((self.N, self.K), dtype=torch.float32, device="cuda")
+        dev = _device_now()
+        w = _empty((self.N, self.K), torch.float32, dev, stream)
         qgemv_dequant(self.handle, w.data_ptr(), _current(stream))
         return w
 
@@ -415,9 +446,12 @@ def quantize_q4_0(w, stream=None):
     """Q4_0 quantizer on the GPU: fp32 CUDA tensor [N, K] -> uint8 CUDA tensor."""
     import torch
     N, K = w.shape
-    out = torch.empty(qgemv_packed_bytes(Q4_0, N, K), dtype=torch.uint8, device=w.device)
-    qgemv_quantize_q4_0(w.contiguous().data_ptr(), N, K, out.data_ptr(), _current(stream))
-    return out
+
+    def make():
+        out = torch.empty(qgemv_packed_bytes(Q4_0, N, K), dtype=torch.uint8, device=w.device)
+        qgemv_quantize_q4_0(w.contiguous().data_ptr(), N, K, out.data_ptr(), _current(None))
+        return out
+    return _along(stream, w.get_device(), make)
 
 
 def quantize_x_int8(x, stream=None):
@@ -425,10 +459,13 @@ def quantize_x_int8(x, stream=None):
     -> (int8 [M, K], fp32 scales [M, K/128]) CUDA tensors."""
     import torch
     M, K = x.shape
-    q = torch.empty((M, K), dtype=torch.int8, device=x.device)
-    a = torch.empty((M, K // 128), dtype=torch.float32, device=x.device)
-    qgemv_quantize_x_int8(x.contiguous().data_ptr(), M, K, q.data_ptr(), a.data_ptr(), _current(stream))
-    return q, a
+
+    def make():
+        q = torch.empty((M, K), dtype=torch.int8, device=x.device)
+        a = torch.empty((M, K // 128), dtype=torch.float32, device=x.device)
+        qgemv_quantize_x_int8(x.contiguous().data_ptr(), M, K, q.data_ptr(), a.data_ptr(), _current(None))
+        return q, a
+    return _along(stream, x.get_device(), make)
 
 
 def prepare_x_int8(x, hadamard_block: int = 0, signs=None, stream=None):
@@ -439,10 +476,13 @@ def prepare_x_int8(x, hadamard_block: int = 0, signs=None, stream=None):
     tensor [K] of +-1, or None)."""
     import torch
     M, K = x.shape
-    xq = torch.empty(qgemv_xq_bytes(M, K), dtype=torch.uint8, device=x.device)
-    qgemv_prepare_x_int8(x.contiguous().data_ptr(), M, K, None if signs is None else signs.data_ptr(),
-                         hadamard_block, xq.data_ptr(), _current(stream))
-    return xq
+
+    def make():
+        xq = torch.empty(qgemv_xq_bytes(M, K), dtype=torch.uint8, device=x.device)
+        qgemv_prepare_x_int8(x.contiguous().data_ptr(), M, K, None if signs is None else signs.data_ptr(),
+                             hadamard_block, xq.data_ptr(), _current(None))
+        return xq
+    return _along(stream, x.get_device(), make)
 
 
 # --------------------------------------------------- cache and attention --
@@ -559,8 +599,8 @@ class KVCache:
     rows into slots, ``read`` gives rows back, ``attend`` is the attention of
     one or several drafted tokens of each sequence over the cached ones.
     Runs are ordered on ``stream`` when one is given, else on torch's current
-    stream.  Their tensors and the workspace are on the cache's device, which
-    need not be the current one."""
+    stream; outputs that a call makes are memory of that stream.  Tensors and
+    workspace are on the cache's device, which need not be the current one."""
 
     def __init__(self, fmt, n_pages: int, page_tokens: int, kv_heads: int, head_dim: int, device="cuda"):
         import torch
@@ -595,7 +635,7 @@ class KVCache:
         if out is None:
             shape = n_tokens, self.kv_heads, self.head_dim
             dtype = torch.float16 if dtype is None else dtype
-            out = (torch.empty(shape, dtype=dtype, device=self.device), torch.empty(shape, dtype=dtype, device=self.device))
+            out = _empty(shape, dtype, dev, stream), _empty(shape, dtype, dev, stream)
             row = self.kv_heads * self.head_dim, self.head_dim
             rows = (out[0].data_ptr(), *row, out[1].data_ptr(), *row)
         else:
@@ -623,14 +663,14 @@ class KVCache:
         if q.dtype != torch.float16:
             raise ValueError("q must be fp16")
         if out is None:
-            out = torch.empty((n, heads, d), dtype=torch.float16, device=q.device)
+            out = _empty((n, heads, d), torch.float16, dev, stream)
             out_rows = out.data_ptr(), heads * d, d
         elif out.dtype != torch.float16 or out.shape != q.shape:
             raise ValueError("out must be fp16, shaped like q")
         else:
             out_rows = _rows("out", out, heads, d, dev)
         if lse is None:
-            lse = torch.empty((n, heads), dtype=torch.float32, device=q.device)
+            lse = _empty((n, heads), torch.float32, dev, stream)
         else:
             _index("lse", lse, torch.float32, (n, heads), dev)
         if masks is not None:
@@ -656,14 +696,14 @@ def attn_prompt(q, k, v, cu_q, cu_k, *, max_q: int, workspace, scale=None, out=N
     if k.shape[0] != v.shape[0] or not (q.dtype == k.dtype == v.dtype):
         raise ValueError("q, k and v must have one type, k and v the same number of tokens")
     if out is None:
-        out = torch.empty((n, heads, d), dtype=q.dtype, device=q.device)
+        out = _empty((n, heads, d), q.dtype, dev, stream)
         out_rows = out.data_ptr(), heads * d, d
     elif out.dtype != q.dtype or out.shape != q.shape:
         raise ValueError("out must have q's type and shape")
     else:
         out_rows = _rows("out", out, heads, d, dev)
     if lse is None:
-        lse = torch.empty((n, heads), dtype=torch.float32, device=q.device)
+        lse = _empty((n, heads), torch.float32, dev, stream)
     else:
         _index("lse", lse, torch.float32, (n, heads), dev)
     n_seqs, kv_heads = cu_q.shape[0] - 1, k.shape[1]
