@@ -166,7 +166,7 @@ struct Codes<QGEMV_KV_Q4_0, D> {
   }
   __device__ static void k_frag(const uint32_t (&w)[kKw], int ks, uint32_t& b0, uint32_t& b1) {
     const uint32_t x = ks & 1 ? w[ks >> 1] >> 8 : w[ks >> 1];
-    b0 = x & 0x000F000Fu, b1 = x & 0x00F000F0u;  // the latter times 16: Q's share of it is over 16
+    b0 = x & 0x000F000Fu, b1 = x & 0x00F000F0u;  // the latter times 16
   }
   // V: [token][group pair]
   __device__ static void load_v(const uint8_t* b, int g, int lane, uint32_t (&w)[4 * (D / 64)]) {
@@ -197,6 +197,13 @@ template <int D>
 __device__ __forceinline__ void load_scales(const uint8_t* at, __half2 (&sc)[D / 64]) {
   if constexpr (D == 128) *reinterpret_cast<uint2*>(sc) = *reinterpret_cast<const uint2*>(at);
   else *reinterpret_cast<uint32_t*>(sc) = *reinterpret_cast<const uint32_t*>(at);
+}
+
+// Magnitude bits of a pair of fp16, the larger.
+__device__ __forceinline__ uint32_t top_half(uint32_t w) { return max(w & 0x7fffu, (w >> 16) & 0x7fffu); }
+// A pair of fp16 times f, in fp32, rounded to fp16.
+__device__ __forceinline__ uint32_t scaled_pair(uint32_t w, float f) {
+  return half_pair(h2f(w & 0xffffu) * f, h2f(w >> 16) * f);
 }
 
 // Shape of a kernel: W warps, NT tiles of 8 rows.
@@ -309,15 +316,36 @@ __global__ void __launch_bounds__(TreeShape<FMT, D, NT>::kThreads, kBlocksPerSm)
       row_mask = p.masks ? p.masks[q0 + tok] : (~0ull >> (63 - tok));
     }
     for (int k = 0; k < NS && k < n_mine; ++k) prefetch(k, stage_of(k));
+    // (codes as subnormals are 2^-24 of their values)
+    float sl = p.scale * kLog2e * (FMT == QGEMV_KV_F16 ? 1.f : 16777216.f);
+    if constexpr (FMT == QGEMV_KV_Q4_0) {
+      // Half of the codes come times 16 (k_frag), so their q is divided by it.  The
+      // tile's q are brought to 2^15 .. 2^16 by a power of 2 first, which the
+      // scores' factor takes back: none loses bits but those below 2^-24 of the
+      // largest.
+      uint32_t* s_top = reinterpret_cast<uint32_t*>(s_offs);  // of each warp, until the sums' starts
+      uint32_t top = 0;
+#pragma unroll
+      for (int x = 0; x < kQPer; ++x)
+        top = max(top, max(max(top_half(qf[x].x), top_half(qf[x].y)), max(top_half(qf[x].z), top_half(qf[x].w))));
+      top = __reduce_max_sync(full, top);
+      if (lane == 0) s_top[warp] = top;
+      __syncthreads();
+#pragma unroll
+      for (int w = 0; w < W; ++w) top = max(top, s_top[w]);
+      // (zeros, infinities and NaN stay as they are)
+      const int e = top == 0 || top >= 0x7C00u ? 0 : 15 - (static_cast<int>(__float_as_uint(h2f(top)) >> 23) - 127);
+      const float f = __int_as_float((127 + e) << 23);
+#pragma unroll
+      for (int x = 0; x < kQPer; ++x) {
+        qf[x].x = scaled_pair(qf[x].x, f), qf[x].z = scaled_pair(qf[x].z, f);
+        qf[x].y = scaled_pair(qf[x].y, f * 0.0625f), qf[x].w = scaled_pair(qf[x].w, f * 0.0625f);
+      }
+      sl *= __int_as_float((127 - e) << 23);
+    }
 #pragma unroll
     for (int x = 0; x < kQPer; ++x)
-      if (tid + x * Sh::kThreads < kQAll) {
-        if (FMT == QGEMV_KV_Q4_0) {  // see k_frag
-          qf[x].y = hfma2(qf[x].y, 0x2C002C00u, 0u);
-          qf[x].w = hfma2(qf[x].w, 0x2C002C00u, 0u);
-        }
-        s_q[tid + x * Sh::kThreads] = qf[x];
-      }
+      if (tid + x * Sh::kThreads < kQAll) s_q[tid + x * Sh::kThreads] = qf[x];
     if (tid < Sh::kRows) s_mask[tid] = row_mask;
     __syncthreads();
 
@@ -343,8 +371,6 @@ __global__ void __launch_bounds__(TreeShape<FMT, D, NT>::kThreads, kBlocksPerSm)
       __syncthreads();
     }
 
-    // (codes as subnormals are 2^-24 of their values)
-    const float sl = p.scale * kLog2e * (FMT == QGEMV_KV_F16 ? 1.f : 16777216.f);
     float o[NT][MB][4], m[NT][2], l[NT][2];  // values 16 b + g, + 8; rows 2t and 2t + 1 of each tile
 #pragma unroll
     for (int i = 0; i < NT; ++i) {
