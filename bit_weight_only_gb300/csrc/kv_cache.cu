@@ -121,7 +121,10 @@ __device__ __forceinline__ void encode(uint8_t* b, bool v, int tok, int d0, cons
       const int ow = __shfl_xor_sync(full, where, o);
       if (abs_bits(op) > abs_bits(peak) || (abs_bits(op) == abs_bits(peak) && ow < where)) peak = op, where = ow;
     }
-    const bool bad = abs_bits(peak) >= kInfBits;
+    // a from 65520 on is past fp16: its group, too, is kept as NaN (an infinite
+    // scale would make infinities of some codes, and hide the row's other groups
+    // from the attention)
+    const bool bad = abs_bits(peak) >= __float_as_uint(8.f * 65520.f);
     const float a = bad ? __int_as_float(0x7fffffff) : __fdiv_rn(peak, -8.f);
     uint32_t q[8];
     round_quotients<true>(x, a, q);

@@ -399,7 +399,8 @@ typedef enum {
   QGEMV_KV_Q4_0 = 3
 } qgemv_kv_format;
 /* A vector (Q4_0: a group of 32) with an infinity or NaN is kept as all NaN
- * in the quantised formats.                                                 */
+ * in the quantised formats; so is a Q4_0 group whose a is past fp16's range
+ * (values from 524160 on).                                                  */
 
 /* A cache: n_pages pages of page_tokens tokens for each of kv_heads heads,
  * in the caller's device memory (qgemv_kv_bytes bytes, 128-byte aligned).

@@ -33,6 +33,45 @@ def test_small_queries(fmt, d, power):
     c.check(f"{fmt} 2^{power}", *c.run())
 
 
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
+@pytest.mark.parametrize("size", [5.25e5, 1e6, 3e38])
+def test_groups_beyond_the_range_of_their_scale(kind, size):
+    """Q4_0 keeps scales as fp16: a group of 32 whose scale is past them is all NaN, as one with an infinity; the groups beside
+    it, and the rows that do not see it, are what they were."""
+    dt = {"f32": torch.float32, "bf16": torch.bfloat16}[kind]
+    for at in (7, 40 + 2):                                        # a cached and a drafted token
+        c = Case("q4_0", 4, 1, 128, 32, [40], [9])
+        c.fill()
+        k, v = (torch.from_numpy(x).to(dt) for x in (c.k, c.v))
+        v[at, 0, 32:64] = size * torch.linspace(-1, 1, 32)
+        v[at, 0, 32] = -size
+        slots = i64([int(c.table[0, at // 32]) * 32 + at % 32])
+        c.cache.write(k[at:at + 1].cuda(), v[at:at + 1].cuda(), slots)
+        back = c.cache.read(i32(c.table), i32([at]), i32([0, 1]), 1, dtype=torch.float32)[1][0, 0].cpu()
+        assert torch.isnan(back[32:64]).all()
+        c.k, c.v = c.k.astype(np.float32), c.v.astype(np.float32)
+        c.k[at], c.v[at] = k[at].float().numpy(), v[at].float().numpy()
+        assert np.array_equal(back[:32].numpy(), ref.quantised("q4_0", c.v[at, 0, :32]).astype(np.float32))
+        c.v[at, 0, 32:64] = np.nan
+        c.check("values", *c.run())
+        # keys: every row that sees the token is NaN
+        c = Case("q4_0", 4, 1, 128, 32, [40], [9]).fill()
+        k = torch.from_numpy(c.k).to(dt)
+        k[at, 0, 32:64] = size * torch.linspace(-1, 1, 32)
+        k[at, 0, 32] = -size
+        c.cache.write(k[at:at + 1].cuda(), torch.from_numpy(c.v[at:at + 1]).to(dt).cuda(), slots)
+        out, lse = c.run()
+        sees = [at < 40 or (m >> (at - 40)) & 1 for m in c.masks]
+        for i, s in enumerate(sees):
+            assert torch.isnan(out[i]).all() == bool(s) and torch.isnan(lse[i]).all() == bool(s), i
+    # the largest group that the scale holds
+    cache = qgemv.KVCache("q4_0", 1, 16, 1, 64)
+    x = torch.full((1, 1, 64), 65504.0 * 8, device="cuda")
+    cache.write(x, -x, i64([0]))
+    k, v = cache.read(i32([[0]]), None, i32([0, 1]), 1, dtype=torch.float32)
+    assert (k == 65504.0 * 8).all() and (v == -65504.0 * 8).all()
+
+
 @pytest.mark.parametrize("fmt", FMTS)
 @pytest.mark.parametrize("d", [64, 128])
 def test_queries_of_different_sizes(fmt, d):
