@@ -531,14 +531,23 @@ __global__ void __launch_bounds__(TreeShape<FMT, D, NT>::kThreads, kBlocksPerSm)
             unpack2(add2(pack2(l[i][0], l[i][1]), pack2(s[i][2 * h], s[i][2 * h + 1])), l[i][0], l[i][1]);
           }
         // p * scale(v).  Where a masked token's scale is infinite or NaN (past the
-        // end it may be anything) the product is 0 all the same.
-        bool odd = false;
+        // end it may be anything) the product is 0 all the same; a seen token's is
+        // NaN, however small its p.
+        uint32_t hidden = 0;  // bits [tile][c]: masked for the row; bit 31 where some lane's token is such a one
         if (FMT != QGEMV_KV_F16 && edge) {
+          bool odd = false;
 #pragma unroll
           for (int h = 0; h < 2; ++h)
 #pragma unroll
             for (int x = 0; x < (FMT == QGEMV_KV_Q4_0 ? D / 32 : 1); ++x) odd |= !(fabsf(vs[h][x]) < INFINITY);
-          odd = __any_sync(full, odd);
+          if (__any_sync(full, odd)) {
+            hidden = 1u << 31;
+            for (int x = 0; x < 4 * NT; ++x) {
+              const int64_t pos = pos0 + g + 8 * ((x >> 1) & 1);
+              const bool on = pos < ctx || (pos < all && ((s_mask[8 * (x >> 2) + 2 * t + (x & 1)] >> (pos - ctx)) & 1));
+              if (!on) hidden |= 1u << x;
+            }
+          }
         }
         // as the second operand: lane (g, t) row g, tokens 2t, 2t + 1 and 8 more
         auto weights = [&](int i, int x) -> uint2 {
@@ -549,10 +558,10 @@ __global__ void __launch_bounds__(TreeShape<FMT, D, NT>::kThreads, kBlocksPerSm)
             if (FMT != QGEMV_KV_F16) pp = mul2(pp, pack2(vs[h][x], vs[h][x]));
             unpack2(pp, w[2 * h], w[2 * h + 1]);
           }
-          if (odd) {
+          if (hidden) {
 #pragma unroll
             for (int c = 0; c < 4; ++c)
-              if (s[i][c] == 0.f) w[c] = 0.f;
+              if ((hidden >> (4 * i + c)) & 1) w[c] = 0.f;
           }
           return make_uint2(transpose8(half_pair(w[0], w[1])), transpose8(half_pair(w[2], w[3])));
         };

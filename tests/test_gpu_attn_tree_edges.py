@@ -33,6 +33,22 @@ def test_small_queries(fmt, d, power):
     c.check(f"{fmt} 2^{power}", *c.run())
 
 
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("new", [4, 20])
+def test_a_seen_nan_counts_at_any_score(fmt, new):
+    """A drafted token whose values are NaN, far below the others in score: exp is small there, but not 0."""
+    c = Case(fmt, 4, 1, 128, 32, [40], [new], masks="tree")
+    c.q[:] = 1
+    c.k[:] = 1
+    hit = 40 + 1
+    c.k[hit] = -20
+    c.v[hit, 0, 37] = np.nan
+    c.fill()
+    c.check("far NaN", *c.run())
+    sees = [(m >> 1) & 1 for m in c.masks]
+    assert any(sees) and not all(sees)
+
+
 @pytest.mark.parametrize("kind", ["f32", "bf16"])
 @pytest.mark.parametrize("size", [5.25e5, 1e6, 3e38])
 def test_groups_beyond_the_range_of_their_scale(kind, size):
