@@ -42,13 +42,26 @@ int dtype_size(int dtype) {
   return dtype == QGEMV_DT_F32 ? 4 : dtype == QGEMV_DT_F16 || dtype == QGEMV_DT_BF16 ? 2 : 0;
 }
 
-// A row argument: not NULL, aligned, strides neither negative nor (outputs)
-// such that rows overlap.
-int check_rows(const char* name, const void* ptr, int64_t ts, int64_t hs, int size, int heads, int head_dim, bool out) {
+// Whether two of the rows (token i, head h) at i * ts + h * hs, of d elements
+// each, share one.
+bool rows_overlap(int64_t n, int heads, int64_t ts, int64_t hs, int d) {
+  if ((n > 1 && ts < d) || (heads > 1 && hs < d)) return true;
+  if (n <= 1 || heads <= 1 || ts >= (heads - 1) * hs + d || (hs - d) / ts >= n - 1) return false;
+  for (int h = 1; h < heads; ++h) {  // the tokens just below and above h heads further
+    const int64_t below = h * hs / ts, past = h * hs - below * ts;
+    if ((below < n && past < d) || (below + 1 < n && ts - past < d)) return true;
+  }
+  return false;
+}
+
+// A row argument: not NULL, aligned, strides not negative nor (outputs, `n` of
+// them) such that rows overlap.
+int check_rows(const char* name, const void* ptr, int64_t ts, int64_t hs, int size, int heads, int head_dim, int64_t n,
+               bool out) {
   if (!ptr) return fail(QGEMV_ERR_ARG, "%s is NULL", name);
   const int64_t lim = int64_t(1) << 38;
   if (ts < 0 || hs < 0 || ts > lim || hs > lim) return fail(QGEMV_ERR_ARG, "%s: strides outside [0, 2^38]", name);
-  if (out && (ts < head_dim || (heads > 1 && hs < head_dim)))
+  if (out && rows_overlap(n, heads, ts, hs, head_dim))
     return fail(QGEMV_ERR_ARG, "%s: output rows overlap (strides %lld, %lld)", name, (long long)ts, (long long)hs);
   if ((reinterpret_cast<uintptr_t>(ptr) & 15) || (ts * size & 15) || (hs * size & 15))
     return fail(QGEMV_ERR_ALIGN, "%s and its strides must be 16-byte aligned", name);
@@ -90,8 +103,8 @@ int qgemv_kv_write(const qgemv_kv_cache* cache, int dtype, const void* k, int64_
   if (size == 0) return fail(QGEMV_ERR_ARG, "unknown dtype %d", dtype);
   if (n_tokens < 0 || n_tokens > kMaxTokens) return fail(QGEMV_ERR_ARG, "n_tokens outside [0, 2^30]");
   if (n_tokens == 0) return qgemv::report_error(QGEMV_OK, "");
-  QG_TRY(check_rows("k", k, k_token_stride, k_head_stride, size, cache->kv_heads, cache->head_dim, false));
-  QG_TRY(check_rows("v", v, v_token_stride, v_head_stride, size, cache->kv_heads, cache->head_dim, false));
+  QG_TRY(check_rows("k", k, k_token_stride, k_head_stride, size, cache->kv_heads, cache->head_dim, n_tokens, false));
+  QG_TRY(check_rows("v", v, v_token_stride, v_head_stride, size, cache->kv_heads, cache->head_dim, n_tokens, false));
   if (!slots) return fail(QGEMV_ERR_ARG, "slots is NULL");
   if (reinterpret_cast<uintptr_t>(slots) & 7) return fail(QGEMV_ERR_ALIGN, "slots must be 8-byte aligned");
   qgemv::KvWriteParams p = {*cache, {k, k_token_stride, k_head_stride}, {v, v_token_stride, v_head_stride}, slots, n_tokens};
@@ -111,8 +124,8 @@ int qgemv_kv_read(const qgemv_kv_cache* cache, const int32_t* table, int64_t tab
   if ((!table && table_stride > 0) || !cu) return fail(QGEMV_ERR_ARG, "table or cu is NULL");
   if (((reinterpret_cast<uintptr_t>(table) | reinterpret_cast<uintptr_t>(cu) | reinterpret_cast<uintptr_t>(starts)) & 3))
     return fail(QGEMV_ERR_ALIGN, "table, starts and cu must be 4-byte aligned");
-  QG_TRY(check_rows("k", k, k_token_stride, k_head_stride, size, cache->kv_heads, cache->head_dim, true));
-  QG_TRY(check_rows("v", v, v_token_stride, v_head_stride, size, cache->kv_heads, cache->head_dim, true));
+  QG_TRY(check_rows("k", k, k_token_stride, k_head_stride, size, cache->kv_heads, cache->head_dim, n_tokens, true));
+  QG_TRY(check_rows("v", v, v_token_stride, v_head_stride, size, cache->kv_heads, cache->head_dim, n_tokens, true));
   qgemv::KvReadParams p = {*cache, table, table_stride, n_seqs, starts, cu, n_tokens,
                            {k, k_token_stride, k_head_stride}, {v, v_token_stride, v_head_stride}};
   return done(qgemv::launch_kv_read(p, dtype, static_cast<cudaStream_t>(stream)), "launching the cache read");
@@ -156,8 +169,8 @@ int qgemv_attn_tree(const qgemv_kv_cache* cache, const int32_t* table, int64_t t
   if (((reinterpret_cast<uintptr_t>(table) | reinterpret_cast<uintptr_t>(ctx_lens) | reinterpret_cast<uintptr_t>(cu_q) |
         reinterpret_cast<uintptr_t>(lse)) & 3) || (reinterpret_cast<uintptr_t>(masks) & 7))
     return fail(QGEMV_ERR_ALIGN, "index arrays and lse must be aligned to their elements");
-  QG_TRY(check_rows("q", q, q_token_stride, q_head_stride, 2, q_heads, cache->head_dim, false));
-  QG_TRY(check_rows("out", out, out_token_stride, out_head_stride, 2, q_heads, cache->head_dim, true));
+  QG_TRY(check_rows("q", q, q_token_stride, q_head_stride, 2, q_heads, cache->head_dim, n_q, false));
+  QG_TRY(check_rows("out", out, out_token_stride, out_head_stride, 2, q_heads, cache->head_dim, n_q, true));
   QG_TRY(check_ws(ws, ws_bytes, n_seqs, q_heads, cache->head_dim));
   const int64_t lim = int64_t(1) << 30;
   qgemv::TreeParams p = {*cache, table, table_stride, static_cast<int>(n_seqs), ctx_lens,
@@ -188,15 +201,15 @@ int qgemv_attn_prompt(int dtype, int head_dim, int q_heads, int kv_heads, const 
   if (!cu_q || !cu_k) return fail(QGEMV_ERR_ARG, "cu_q or cu_k is NULL");
   if ((reinterpret_cast<uintptr_t>(cu_q) | reinterpret_cast<uintptr_t>(cu_k) | reinterpret_cast<uintptr_t>(lse)) & 3)
     return fail(QGEMV_ERR_ALIGN, "index arrays and lse must be 4-byte aligned");
-  QG_TRY(check_rows("q", q, q_token_stride, q_head_stride, 2, q_heads, head_dim, false));
+  QG_TRY(check_rows("q", q, q_token_stride, q_head_stride, 2, q_heads, head_dim, n_q, false));
   if (n_k > 0) {
-    QG_TRY(check_rows("k", k, k_token_stride, k_head_stride, 2, kv_heads, head_dim, false));
-    QG_TRY(check_rows("v", v, v_token_stride, v_head_stride, 2, kv_heads, head_dim, false));
+    QG_TRY(check_rows("k", k, k_token_stride, k_head_stride, 2, kv_heads, head_dim, n_k, false));
+    QG_TRY(check_rows("v", v, v_token_stride, v_head_stride, 2, kv_heads, head_dim, n_k, false));
     if ((n_q > 1 && q_token_stride == 0) || (q_heads > 1 && q_head_stride == 0) ||
         (n_k > 1 && (k_token_stride == 0 || v_token_stride == 0)) || (kv_heads > 1 && (k_head_stride == 0 || v_head_stride == 0)))
       return fail(QGEMV_ERR_ARG, "q, k and v of a prompt have no strides of zero");
   }
-  QG_TRY(check_rows("out", out, out_token_stride, out_head_stride, 2, q_heads, head_dim, true));
+  QG_TRY(check_rows("out", out, out_token_stride, out_head_stride, 2, q_heads, head_dim, n_q, true));
   QG_TRY(check_ws(ws, ws_bytes, n_seqs, q_heads, head_dim));
   qgemv::PromptParams p = {dtype, head_dim, q_heads, kv_heads,
                            {q, q_token_stride, q_head_stride}, {k, k_token_stride, k_head_stride},

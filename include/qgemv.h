@@ -376,9 +376,9 @@ int qgemv_stream_k_plan(int64_t units, int grid, int64_t units_per_row_tile, int
  * between tokens and between heads; the head_dim values of a row are
  * contiguous.  Inputs and outputs need 16-byte aligned pointers and strides
  * that are multiples of 16 bytes (QGEMV_ERR_ALIGN), so that slices of a
- * stacked projection's output can be passed as they are.  head_dim is 64 or
- * 128.  Calls run on the current device, which all of their memory belongs
- * to.  Empty calls (no tokens) return QGEMV_OK.  Index arrays (slots, page
+ * stacked projection's output can be passed as they are; two rows of an
+ * output share no element (QGEMV_ERR_ARG).  head_dim is 64 or 128.  Calls
+ * run on the current device, which all of their memory belongs to.  Empty calls (no tokens) return QGEMV_OK.  Index arrays (slots, page
  * table, lengths, offsets) live on the device and are not checked on the
  * host; the kernels never read or write outside the buffers that the sizes
  * describe, whatever they hold.                                             */

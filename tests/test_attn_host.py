@@ -75,3 +75,32 @@ answer([out, {call}, notes()])
 """)
     assert got[0] == [3] * len(fails)  # QGEMV_ERR_CUDA
     assert got[1] == 0 and any(n[0] == "launch" and kernel in n[-1] for n in got[2])
+
+
+@pytest.mark.parametrize("n, heads, ts, hs, apart", [
+    (5, 8, 1024, 128, True),          # rows of one tensor
+    (5, 8, 128, 640, True),           # head-major
+    (5, 8, 128, 128, False),          # every row of a head but the first is the next head's
+    (5, 8, 512, 128, False),          # tokens closer than their heads
+    (5, 2, 256, 128, True),
+    (5, 2, 256, 384, True),           # heads between the tokens of others
+    (5, 2, 256, 512, False),
+    (2, 2, 256, 512, True),           # that token is not there
+    (5, 2, 256, 448, False),          # half of a row
+    (1, 8, 128, 128, True),           # one token: its stride means nothing
+    (5, 1, 128, 128, True),           # one head
+    (1 << 30, 2, 128, 1 << 37, True),
+    (1 << 30, 2, 128, (1 << 37) - 128, False),
+    (1 << 30, 2, 1 << 38, (1 << 38) - 1024, True),
+    (1 << 30, 3, 1 << 38, 1 << 37, False),
+])
+def test_overlapping_outputs_are_refused(host, n, heads, ts, hs, apart):
+    """Two rows of an output that share an element would be written by blocks that know nothing of one another."""
+    got = host(f"""
+out = [read(kv_heads={heads}, n={n}, kt={ts}, kh={hs})]
+if {n} < 1 << 20:
+    out += [tree("f16", kv_heads={heads}, q_heads={heads}, n={n}, ot={ts}, oh={hs}),
+            prompt(kv_heads={heads}, q_heads={heads}, n_q={n}, n_k={n}, ot={ts}, oh={hs})]
+answer(out)
+""")
+    assert got == [0 if apart else 1] * len(got)  # QGEMV_OK, QGEMV_ERR_ARG
