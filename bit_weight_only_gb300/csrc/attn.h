@@ -67,7 +67,6 @@ struct PromptParams {
   const int32_t* cu_q;
   const int32_t* cu_k;
   int64_t n_q, n_k;
-  int max_q;
   float scale;
   RowsOut out;
   float* lse;

@@ -213,8 +213,7 @@ int qgemv_attn_prompt(int dtype, int head_dim, int q_heads, int kv_heads, const 
   QG_TRY(check_ws(ws, ws_bytes, n_seqs, q_heads, head_dim));
   qgemv::PromptParams p = {dtype, head_dim, q_heads, kv_heads,
                            {q, q_token_stride, q_head_stride}, {k, k_token_stride, k_head_stride},
-                           {v, v_token_stride, v_head_stride}, static_cast<int>(n_seqs), cu_q, cu_k, n_q, n_k,
-                           static_cast<int>(max_q < n_q ? max_q : n_q), scale,
+                           {v, v_token_stride, v_head_stride}, static_cast<int>(n_seqs), cu_q, cu_k, n_q, n_k, scale,
                            {out, out_token_stride, out_head_stride}, lse, static_cast<uint8_t*>(ws)};
   return done(qgemv::launch_attn_prompt(p, static_cast<cudaStream_t>(stream)), "launching the prompt attention");
 }

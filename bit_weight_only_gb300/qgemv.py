@@ -688,7 +688,8 @@ def attn_prompt(q, k, v, cu_q, cu_k, *, max_q: int, workspace, scale=None, out=N
     """Causal attention over packed prompts: q [n_q, q_heads, d], k and v
     [n_k, kv_heads, d] (all fp16 or all bf16), sequence b the rows cu_q[b] ..
     of q and cu_k[b] .. of k and v (int32 [n_seqs + 1]); its last query sees
-    all of its keys.  Returns (out like q, lse fp32 [n_q, q_heads]).  All
+    all of its keys.  max_q bounds the queries of a sequence: results are right
+    whatever it is.  Returns (out like q, lse fp32 [n_q, q_heads]).  All
     tensors and the workspace are on q's device."""
     torch = _torch()
     n, heads, d = q.shape
@@ -710,6 +711,6 @@ def attn_prompt(q, k, v, cu_q, cu_k, *, max_q: int, workspace, scale=None, out=N
     _call(dev, _lib.qgemv_attn_prompt, _dtype_code(q.dtype), d, heads, kv_heads, *q_rows,
           *_rows("k", k, kv_heads, d, dev), *_rows("v", v, kv_heads, d, dev), n_seqs,
           _index("cu_q", cu_q, torch.int32, (n_seqs + 1,), dev), _index("cu_k", cu_k, torch.int32, (n_seqs + 1,), dev), n,
-          k.shape[0], max_q, d ** -0.5 if scale is None else scale, *out_rows, lse.data_ptr(), *_ws(workspace, dev),
+          k.shape[0], max_q or 1, d ** -0.5 if scale is None else scale, *out_rows, lse.data_ptr(), *_ws(workspace, dev),
           _on(stream, dev))
     return out, lse

@@ -378,10 +378,11 @@ int qgemv_stream_k_plan(int64_t units, int grid, int64_t units_per_row_tile, int
  * that are multiples of 16 bytes (QGEMV_ERR_ALIGN), so that slices of a
  * stacked projection's output can be passed as they are; two rows of an
  * output share no element (QGEMV_ERR_ARG).  head_dim is 64 or 128.  Calls
- * run on the current device, which all of their memory belongs to.  Empty calls (no tokens) return QGEMV_OK.  Index arrays (slots, page
- * table, lengths, offsets) live on the device and are not checked on the
- * host; the kernels never read or write outside the buffers that the sizes
- * describe, whatever they hold.                                             */
+ * run on the current device, which all of their memory belongs to.  Empty
+ * calls (no tokens) return QGEMV_OK.  Index arrays (slots, page table,
+ * lengths, offsets) live on the device and are not checked on the host; the
+ * kernels never read or write outside the buffers that the sizes describe,
+ * whatever they hold.                                                       */
 
 /* Element types of rows. */
 typedef enum { QGEMV_DT_F32 = 0, QGEMV_DT_F16 = 1, QGEMV_DT_BF16 = 2 } qgemv_dtype;
@@ -480,7 +481,8 @@ int qgemv_attn_tree(const qgemv_kv_cache* cache, const int32_t* table, int64_t t
  * v and out; no strides of zero, and at most
  * 128 query heads of a key/value head.
  *   cu_q, cu_k: device int32 [n_seqs + 1], not decreasing.
- *   max_q: the most queries of a sequence; 0 for a call with nothing to do.
+ *   max_q: the most queries of a sequence; 0 for a call with nothing to do,
+ *     which then does nothing.  Its other values change nothing at present.
  *   lse: device fp32 [n_q][q_heads], or NULL.
  * Asynchronous on `stream`, no allocation, can be captured in a CUDA graph;
  * bitwise reproducible.                                                     */

@@ -131,3 +131,14 @@ def test_rows_of_other_sequences_do_not_reach_a_result():
     q[30:50, :, 0] = 64.0
     out, _ = attend(q, k, v, nq, nk)
     assert torch.equal(out[:30], want[:30])
+
+
+@pytest.mark.parametrize("kind", list(KINDS))
+def test_a_bound_of_no_queries_changes_nothing(kind):
+    """max_q is a bound that a caller may get wrong: where there are queries, they are answered."""
+    q, k, v = (rows(i, 90, 2, 64, KINDS[kind]) for i in (1, 2, 3))
+    ws = qgemv.AttnWorkspace(2, 2, 64)
+    want, lse = qgemv.attn_prompt(q, k, v, cu([70, 20]), cu([70, 20]), max_q=70, workspace=ws)
+    out, lse2 = torch.full_like(want, 5.0), torch.full_like(lse, 5.0)
+    qgemv.attn_prompt(q, k, v, cu([70, 20]), cu([70, 20]), max_q=0, workspace=ws, out=out, lse=lse2)
+    assert torch.equal(out, want) and torch.equal(lse, lse2)
