@@ -342,7 +342,7 @@ prompt_kernel(const PromptArgs a, const __grid_constant__ CUtensorMap qmap, cons
         if (RUNS) {
           more = run.next(a, pc, D);
         } else {
-          more = id < total;
+          more = static_cast<unsigned>(id) < static_cast<unsigned>(total);  // (a workspace that was not set up ends here too)
           if (more && !pc.locate(a, id / p.kv_heads)) {
             id = take();
             continue;

@@ -570,7 +570,8 @@ def _ws(workspace, dev: int):
 class AttnWorkspace:
     """Workspace of ``KVCache.attend`` and ``attn_prompt`` for up to
     ``n_seqs`` sequences, reused by any number of calls, one at a time (calls
-    that overlap on several streams need one each)."""
+    that overlap on several streams need one each).  Making one waits for its
+    setting up on the current stream."""
 
     def __init__(self, n_seqs: int, q_heads: int, head_dim: int, device="cuda"):
         import torch
@@ -581,6 +582,12 @@ class AttnWorkspace:
         self.buffer = torch.empty(self.nbytes, dtype=torch.uint8, device=device)
         self.ptr, self._dev = self.buffer.data_ptr(), self.buffer.get_device()
         self.reset()
+        # The first call may be on another stream: what it counts on must be there.
+        # (While a graph is captured the setting up is part of it.)
+        stream = torch.cuda.current_stream(self._dev)
+        with torch.cuda.stream(stream):
+            if not torch.cuda.is_current_stream_capturing():
+                stream.synchronize()
 
     def reset(self, stream=None):
         """Set the workspace up again (needed only after ``status`` raised)."""

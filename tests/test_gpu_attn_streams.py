@@ -94,3 +94,27 @@ def test_outputs_stay_while_the_current_stream_uses_them(name):
     for g, w in zip(kept, want):
         assert torch.equal(g, w)
     del again
+
+
+@pytest.mark.parametrize("as_number", [False, True])
+def test_a_new_workspace_serves_any_stream(as_number):
+    """A workspace is set up when it is there, also for a stream that does not wait for the one it was made on."""
+    fn, a, _ = calls()["attn_prompt"]
+    want = [t.clone() for t in fn(a, None)]
+    g = torch.Generator(device="cuda").manual_seed(1)
+    q = torch.randn(3000, 8, 128, generator=g, device="cuda").half()
+    cu = i32([0, 3000])
+    ws = qgemv.AttnWorkspace(1, 8, 128)
+    whole, _ = qgemv.attn_prompt(q, q, q, cu, cu, max_q=3000, workspace=ws)
+    nbytes = ws.nbytes
+    torch.cuda.synchronize()
+    del ws
+    torch.full((nbytes,), 127, dtype=torch.uint8, device="cuda")  # what the next one is made of
+    s = torch.cuda.Stream()
+    busy()
+    ws = qgemv.AttnWorkspace(1, 8, 128)
+    out, _ = qgemv.attn_prompt(q, q, q, cu, cu, max_q=3000, workspace=ws, stream=s.cuda_stream if as_number else s)
+    torch.cuda.synchronize()
+    ws.status()
+    assert torch.equal(out, whole)
+    assert torch.equal(fn(a, None)[0], want[0])
