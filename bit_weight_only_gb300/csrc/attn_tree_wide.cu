@@ -51,6 +51,7 @@ constexpr int kLoadWarp = kConvWarp + 8, kMmaWarp = kLoadWarp + 1, kLoadVWarp = 
 constexpr int kThreads = 32 * (kConvWarp + 12);
 constexpr int kRows = 64;
 constexpr int kCols = kRows / kSoft;
+static_assert(kCols == 16, "half a warp's lanes a row, where l is summed");
 constexpr int kKeys = 128;
 constexpr int kBlocks = kKeys / kKvBlockTokens;  // cache blocks of a unit
 constexpr int kErrWide = 64;
@@ -414,8 +415,8 @@ __global__ void __launch_bounds__(kThreads, 1) tree_wide_kernel(const TreeArgs a
       const bool bad = S::kF16 && s_anybad[bb] != 0;
       if (busy) {
         {
-          // Each step halves the rows a lane holds: lane i ends with row i
-          // (of 16 rows: lanes 2i and 2i + 1, half of the keys each).
+          // Each step halves the rows a lane holds: lanes 2i and 2i + 1 end with
+          // half of the keys of row i each.
           float l[kCols];
 #pragma unroll
           for (int i = 0; i < kCols / 2; ++i) unpack2(l2[i], l[2 * i], l[2 * i + 1]);
@@ -428,8 +429,8 @@ __global__ void __launch_bounds__(kThreads, 1) tree_wide_kernel(const TreeArgs a
               l[i] = keep + __shfl_xor_sync(full, give, o);
             }
           }
-          if (kCols == 16) l[0] += __shfl_xor_sync(full, l[0], 1);
-          if (kCols == 32 || !(lane & 1)) s_l[64 * quarter + c0 + (kCols == 32 ? lane : lane >> 1)] = l[0];
+          l[0] += __shfl_xor_sync(full, l[0], 1);
+          if (!(lane & 1)) s_l[64 * quarter + c0 + (lane >> 1)] = l[0];
         }
         named_bar_sync(1 + wg, 128);
         if (key < kCols) {
