@@ -334,12 +334,10 @@ def _along(stream, dev: int, make):
     return out
 
 
-def _empty(shape, dtype, dev: int, stream):
-    """A new tensor for a call on `stream`."""
+def _empty_on(stream, dev: int):
+    """torch.empty for a call on `stream`."""
     empty = _torch().empty
-    if stream is None:
-        return empty(shape, dtype=dtype, device=dev)
-    return _along(stream, dev, lambda: empty(shape, dtype=dtype, device=dev))
+    return lambda *args, **kw: _along(stream, dev, lambda: empty(*args, **kw))
 
 
 class QGemv:
@@ -410,10 +408,12 @@ class QGemv:
 
     def dequant(self, stream=None):
         import torch
-        dev = _device_now()
-        w = _empty((self.N, self.K), torch.float32, dev, stream)
-        qgemv_dequant(self.handle, w.data_ptr(), _current(stream))
-        return w
+
+        def make():
+            w = torch.empty((self.N, self.K), dtype=torch.float32, device="cuda")
+            qgemv_dequant(self.handle, w.data_ptr(), _current(None))
+            return w
+        return _along(stream, _device_now(), make)
 
     def status(self):
         return qgemv_status(self.handle)
@@ -504,11 +504,19 @@ def _torch():
 
 def _on(stream, dev: int):
     """The address of the stream given, or of torch's current one of the device."""
-    return _torch()._C._cuda_getCurrentRawStream(dev) if stream is None else _stream_ptr(stream)
+    return _raw_stream(dev) if stream is None else _stream_ptr(stream)
+
+
+def _raw_stream(dev: int) -> int:
+    global _raw_stream  # torch's function itself, from the second call on
+    _raw_stream = _torch()._C._cuda_getCurrentRawStream
+    return _raw_stream(dev)
 
 
 def _device_now() -> int:
-    return _torch()._C._cuda_getDevice()
+    global _device_now
+    _device_now = _torch()._C._cuda_getDevice
+    return _device_now()
 
 
 def _call(dev: int, fn, *args):
@@ -561,10 +569,8 @@ def _index(name, t, dtype, shape, dev: int | None = None):
     return t.data_ptr()
 
 
-def _ws(workspace, dev: int):
-    if workspace._dev != dev:
-        raise ValueError(f"the workspace must be on cuda:{dev}, not cuda:{workspace._dev}")
-    return workspace.ptr, workspace.nbytes
+def _elsewhere(workspace, dev: int):
+    raise ValueError(f"the workspace must be on cuda:{dev}, not cuda:{workspace._dev}")
 
 
 class AttnWorkspace:
@@ -642,7 +648,8 @@ class KVCache:
         if out is None:
             shape = n_tokens, self.kv_heads, self.head_dim
             dtype = torch.float16 if dtype is None else dtype
-            out = _empty(shape, dtype, dev, stream), _empty(shape, dtype, dev, stream)
+            empty = torch.empty if stream is None else _empty_on(stream, dev)
+            out = empty(shape, dtype=dtype, device=self.device), empty(shape, dtype=dtype, device=self.device)
             row = self.kv_heads * self.head_dim, self.head_dim
             rows = (out[0].data_ptr(), *row, out[1].data_ptr(), *row)
         else:
@@ -669,15 +676,18 @@ class KVCache:
         n, heads, d = q.shape
         if q.dtype != torch.float16:
             raise ValueError("q must be fp16")
+        if workspace._dev != dev:
+            _elsewhere(workspace, dev)
+        empty = torch.empty if stream is None else _empty_on(stream, dev)
         if out is None:
-            out = _empty((n, heads, d), torch.float16, dev, stream)
+            out = empty((n, heads, d), dtype=torch.float16, device=self.device)
             out_rows = out.data_ptr(), heads * d, d
         elif out.dtype != torch.float16 or out.shape != q.shape:
             raise ValueError("out must be fp16, shaped like q")
         else:
             out_rows = _rows("out", out, heads, d, dev)
         if lse is None:
-            lse = _empty((n, heads), torch.float32, dev, stream)
+            lse = empty((n, heads), dtype=torch.float32, device=self.device)
         else:
             _index("lse", lse, torch.float32, (n, heads), dev)
         if masks is not None:
@@ -687,7 +697,7 @@ class KVCache:
               n_seqs, _index("ctx_lens", ctx_lens, torch.int32, (n_seqs,), dev),
               *_rows("q", q, heads, self.head_dim, dev), heads, _index("cu_q", cu_q, torch.int32, (n_seqs + 1,), dev), n,
               masks, max_ctx, max_new, d ** -0.5 if scale is None else scale, *out_rows, lse.data_ptr(),
-              *_ws(workspace, dev), _on(stream, dev))
+              workspace.ptr, workspace.nbytes, _on(stream, dev))
         return out, lse
 
 
@@ -703,21 +713,24 @@ def attn_prompt(q, k, v, cu_q, cu_k, *, max_q: int, workspace, scale=None, out=N
     q_rows, dev = _rows("q", q, heads, d), q.get_device()
     if k.shape[0] != v.shape[0] or not (q.dtype == k.dtype == v.dtype):
         raise ValueError("q, k and v must have one type, k and v the same number of tokens")
+    if workspace._dev != dev:
+        _elsewhere(workspace, dev)
+    empty = torch.empty if stream is None else _empty_on(stream, dev)
     if out is None:
-        out = _empty((n, heads, d), q.dtype, dev, stream)
+        out = empty((n, heads, d), dtype=q.dtype, device=q.device)
         out_rows = out.data_ptr(), heads * d, d
     elif out.dtype != q.dtype or out.shape != q.shape:
         raise ValueError("out must have q's type and shape")
     else:
         out_rows = _rows("out", out, heads, d, dev)
     if lse is None:
-        lse = _empty((n, heads), torch.float32, dev, stream)
+        lse = empty((n, heads), dtype=torch.float32, device=q.device)
     else:
         _index("lse", lse, torch.float32, (n, heads), dev)
     n_seqs, kv_heads = cu_q.shape[0] - 1, k.shape[1]
     _call(dev, _lib.qgemv_attn_prompt, _dtype_code(q.dtype), d, heads, kv_heads, *q_rows,
           *_rows("k", k, kv_heads, d, dev), *_rows("v", v, kv_heads, d, dev), n_seqs,
           _index("cu_q", cu_q, torch.int32, (n_seqs + 1,), dev), _index("cu_k", cu_k, torch.int32, (n_seqs + 1,), dev), n,
-          k.shape[0], max_q or 1, d ** -0.5 if scale is None else scale, *out_rows, lse.data_ptr(), *_ws(workspace, dev),
-          _on(stream, dev))
+          k.shape[0], max_q or 1, d ** -0.5 if scale is None else scale, *out_rows, lse.data_ptr(), workspace.ptr,
+          workspace.nbytes, _on(stream, dev))
     return out, lse
