@@ -15,7 +15,11 @@
 //             stand (code + offset, times 2^-24), and the sums start at
 //             -offset times the row's sum of q, so that a code pair costs one
 //             instruction; the scales of the tokens (Q4_0: of each group, on
-//             partial sums) go to S in fp32
+//             partial sums) go to S in fp32.  The sums are thus of the size of
+//             offset * |sum q|, and their fp32 error with them: at most about
+//             2^-23 max|k| sum|q| (measured on keys with one value that is not
+//             0: 2^-26, INT8, and 2^-24, Q4_0), which is more than that of the
+//             products alone where most of k is small
 //   softmax   base 2, an own reference m for each warp and row that moves only
 //             when a score passes it by 2^8: without a move no shuffle is
 //             needed.  m is taken over s + log2(scale of v), because what is
@@ -30,12 +34,13 @@
 // A warp's O, m and l live in its registers.  At the end of a segment the
 // warps' results are added in warp order through shared memory.
 //
-// Two sequences of up to 131000 tokens, one token of 64 heads over 8: fp16 140 us
-// (the bytes' floor 137), INT8 84 (71), Q4_0 76 (38).  fp16 and INT8 stream at
-// the copy bandwidth, with about 12 us of start, join and gap around it; Q4_0
-// is held up by instruction issue (decoding V, the products' scales).  With
-// the rows, not the tokens, along the products' 16 rows, half of an instruction
-// was empty at 8 rows: INT8 88 us, Q4_0 110.
+// Two sequences of 224000 tokens together, one token of 64 heads over 8: fp16
+// 139 us (the bytes' floor 137), INT8 84 (71), Q4_0 69 (39).  fp16 and INT8
+// stream at the copy bandwidth, with about 12 us of start, join and gap around
+// it; Q4_0 is held up by instruction issue (decoding V, the products' scales).
+// With the rows, not the tokens, along the products' 16 rows, half of an
+// instruction was empty at 8 rows: INT8 88 us (Q4_0 of 252000 tokens 110
+// against 76).
 #include <algorithm>
 
 #include "per_device.h"
@@ -322,7 +327,9 @@ __global__ void __launch_bounds__(TreeShape<FMT, D, NT>::kThreads, kBlocksPerSm)
       // Half of the codes come times 16 (k_frag), so their q is divided by it.  The
       // tile's q are brought to 2^15 .. 2^16 by a power of 2 first, which the
       // scores' factor takes back: none loses bits but those below 2^-24 of the
-      // largest.
+      // largest.  (Codes shifted into place instead: two sequences of 224000
+      // tokens, one row, 71.1 us against 69; a power for each row: 12 ragged ones
+      // of 45 rows 84.8 against 83.8.)
       uint32_t* s_top = reinterpret_cast<uint32_t*>(s_offs);  // of each warp, until the sums' starts
       uint32_t top = 0;
 #pragma unroll

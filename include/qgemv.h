@@ -368,9 +368,12 @@ int qgemv_stream_k_plan(int64_t units, int grid, int64_t units_per_row_tile, int
  *
  * A row that sees no key gives out = 0 and lse = -infinity.  Key/value head
  * h serves the query heads h * g .. h * g + g - 1, g = q_heads / kv_heads.
- * Scores, softmax statistics and sums are held in fp32; the probabilities
- * are rounded to the values' 16-bit type for the tensor cores.  A value or
- * key that a row does not see never reaches it, infinities and NaN included.
+ * Scores, softmax statistics and sums are held in fp32 (over INT8 and Q4_0
+ * keys a score's error is about 2^-24 max|k_j| sum|q_i| scale, the codes being
+ * summed with an offset); the probabilities, INT8 and Q4_0: times the values'
+ * scales, are rounded to the values' 16-bit type (fp16 over a cache) for the
+ * tensor cores.  A value or key that a row does not see never reaches it,
+ * infinities and NaN included.
  *
  * Rows of heads are given as a device pointer and two element strides,
  * between tokens and between heads; the head_dim values of a row are
