@@ -46,6 +46,8 @@ struct TreeParams {
   qgemv_kv_cache cache;
   const int32_t* table;
   int64_t table_stride;
+  // rows of the table of a sequence: 1, or one for each key/value head
+  int table_heads;
   int n_seqs;
   const int32_t* ctx_lens;
   RowsIn q;

@@ -1,72 +1,11 @@
 // attn_api.cu -- the C ABI of the key/value cache and the attention calls
 // (include/qgemv.h): argument checks on the host, then the launches.  No
 // exception crosses the ABI and no call allocates.
-#include <cstdarg>
-#include <cstdio>
-
-#include "attn.h"
-#include "formats.h"
+#include "api_checks.h"
 
 namespace {
 
-int fail(int code, const char* fmt, ...) {
-  char msg[256];
-  va_list ap;
-  va_start(ap, fmt);
-  vsnprintf(msg, sizeof(msg), fmt, ap);
-  va_end(ap);
-  return qgemv::report_error(code, msg);
-}
-
-int done(cudaError_t e, const char* what) {
-  if (e == cudaSuccess) return qgemv::report_error(QGEMV_OK, "");
-  return fail(QGEMV_ERR_CUDA, "%s: %s (%s)", what, cudaGetErrorString(e), cudaGetErrorName(e));
-}
-
-bool cache_sizes_ok(int format, int64_t n_pages, int page_tokens, int kv_heads, int head_dim) {
-  return format >= QGEMV_KV_F16 && format <= QGEMV_KV_Q4_0 && n_pages > 0 && n_pages < (int64_t(1) << 31) &&
-         page_tokens >= 16 && page_tokens <= 256 && (page_tokens & (page_tokens - 1)) == 0 && kv_heads > 0 &&
-         kv_heads <= 1024 && (head_dim == 64 || head_dim == 128);
-}
-
-int check_cache(const qgemv_kv_cache* c) {
-  if (!c || !c->pages) return fail(QGEMV_ERR_ARG, "the cache or its pages are NULL");
-  if (!cache_sizes_ok(c->format, c->n_pages, c->page_tokens, c->kv_heads, c->head_dim))
-    return fail(QGEMV_ERR_ARG, "invalid cache: format %d, %lld pages of %d tokens, %d heads of %d", c->format,
-                (long long)c->n_pages, c->page_tokens, c->kv_heads, c->head_dim);
-  if (reinterpret_cast<uintptr_t>(c->pages) & 127) return fail(QGEMV_ERR_ALIGN, "the cache must be 128-byte aligned");
-  return QGEMV_OK;
-}
-
-int dtype_size(int dtype) {
-  return dtype == QGEMV_DT_F32 ? 4 : dtype == QGEMV_DT_F16 || dtype == QGEMV_DT_BF16 ? 2 : 0;
-}
-
-// Whether two of the rows (token i, head h) at i * ts + h * hs, of d elements
-// each, share one.
-bool rows_overlap(int64_t n, int heads, int64_t ts, int64_t hs, int d) {
-  if ((n > 1 && ts < d) || (heads > 1 && hs < d)) return true;
-  if (n <= 1 || heads <= 1 || ts >= (heads - 1) * hs + d || (hs - d) / ts >= n - 1) return false;
-  for (int h = 1; h < heads; ++h) {  // the tokens just below and above h heads further
-    const int64_t below = h * hs / ts, past = h * hs - below * ts;
-    if ((below < n && past < d) || (below + 1 < n && ts - past < d)) return true;
-  }
-  return false;
-}
-
-// A row argument: not NULL, aligned, strides not negative nor (outputs, `n` of
-// them) such that rows overlap.
-int check_rows(const char* name, const void* ptr, int64_t ts, int64_t hs, int size, int heads, int head_dim, int64_t n,
-               bool out) {
-  if (!ptr) return fail(QGEMV_ERR_ARG, "%s is NULL", name);
-  const int64_t lim = int64_t(1) << 38;
-  if (ts < 0 || hs < 0 || ts > lim || hs > lim) return fail(QGEMV_ERR_ARG, "%s: strides outside [0, 2^38]", name);
-  if (out && rows_overlap(n, heads, ts, hs, head_dim))
-    return fail(QGEMV_ERR_ARG, "%s: output rows overlap (strides %lld, %lld)", name, (long long)ts, (long long)hs);
-  if ((reinterpret_cast<uintptr_t>(ptr) & 15) || (ts * size & 15) || (hs * size & 15))
-    return fail(QGEMV_ERR_ALIGN, "%s and its strides must be 16-byte aligned", name);
-  return QGEMV_OK;
-}
+using namespace qgemv;
 
 int check_ws(void* ws, int64_t ws_bytes, int64_t n_seqs, int q_heads, int head_dim) {
   if (!ws) return fail(QGEMV_ERR_ARG, "the workspace is NULL");
@@ -77,13 +16,31 @@ int check_ws(void* ws, int64_t ws_bytes, int64_t n_seqs, int q_heads, int head_d
   return QGEMV_OK;
 }
 
-#define QG_TRY(expr)                  \
-  do {                                \
-    const int rc_ = (expr);           \
-    if (rc_ != QGEMV_OK) return rc_;  \
-  } while (0)
-
-constexpr int64_t kMaxTokens = int64_t(1) << 30;
+// Attention over the cache by a page table for each sequence, or (table_heads =
+// kv_heads) for each key/value head of it.
+int attend(const qgemv_kv_cache* cache, const int32_t* table, int64_t table_stride, int table_heads, int64_t n_seqs,
+           const int32_t* ctx_lens, RowsIn q, int q_heads, const int32_t* cu_q, int64_t n_q, const uint64_t* masks,
+           int64_t max_ctx, int64_t max_new, float scale, RowsOut out, float* lse, void* ws, int64_t ws_bytes, void* stream) {
+  QG_TRY(check_cache(cache));
+  if (q_heads <= 0 || q_heads > 1024 || q_heads % cache->kv_heads)
+    return fail(QGEMV_ERR_ARG, "q_heads=%d must be a positive multiple of kv_heads=%d, at most 1024", q_heads, cache->kv_heads);
+  if (n_seqs < 0 || n_seqs > (1 << 20) || n_q < 0 || n_q > kMaxTokens || table_stride < 0 || max_ctx < 0 || max_new < 0)
+    return fail(QGEMV_ERR_ARG, "n_seqs outside [0, 2^20], n_q outside [0, 2^30], or a negative size");
+  if (n_q == 0 || n_seqs == 0) return report_error(QGEMV_OK, "");
+  if ((!table && table_stride > 0) || !ctx_lens || !cu_q) return fail(QGEMV_ERR_ARG, "table, ctx_lens or cu_q is NULL");
+  if (((reinterpret_cast<uintptr_t>(table) | reinterpret_cast<uintptr_t>(ctx_lens) | reinterpret_cast<uintptr_t>(cu_q) |
+        reinterpret_cast<uintptr_t>(lse)) & 3) || (reinterpret_cast<uintptr_t>(masks) & 7))
+    return fail(QGEMV_ERR_ALIGN, "index arrays and lse must be aligned to their elements");
+  QG_TRY(check_rows("q", q.ptr, q.token_stride, q.head_stride, 2, q_heads, cache->head_dim, n_q, false));
+  QG_TRY(check_rows("out", out.ptr, out.token_stride, out.head_stride, 2, q_heads, cache->head_dim, n_q, true));
+  QG_TRY(check_ws(ws, ws_bytes, n_seqs, q_heads, cache->head_dim));
+  const int64_t lim = int64_t(1) << 30;
+  TreeParams p = {*cache, table, table_stride, table_heads, static_cast<int>(n_seqs), ctx_lens,
+                         q, q_heads, cu_q, n_q, masks,
+                         static_cast<int>(max_ctx < lim ? max_ctx : lim), static_cast<int>(max_new < lim ? max_new : lim),
+                         scale, out, lse, static_cast<uint8_t*>(ws)};
+  return done(launch_attn_tree(p, static_cast<cudaStream_t>(stream)), "launching the attention");
+}
 
 }  // namespace
 
@@ -159,25 +116,18 @@ int qgemv_attn_tree(const qgemv_kv_cache* cache, const int32_t* table, int64_t t
                     int q_heads, const int32_t* cu_q, int64_t n_q, const uint64_t* masks, int64_t max_ctx,
                     int64_t max_new, float scale, void* out, int64_t out_token_stride, int64_t out_head_stride,
                     float* lse, void* ws, int64_t ws_bytes, void* stream) {
+  return attend(cache, table, table_stride, 1, n_seqs, ctx_lens, {q, q_token_stride, q_head_stride}, q_heads, cu_q, n_q, masks,
+                max_ctx, max_new, scale, {out, out_token_stride, out_head_stride}, lse, ws, ws_bytes, stream);
+}
+
+int qgemv_attn_pages(const qgemv_kv_cache* cache, const int32_t* pages, int64_t pages_stride, int64_t n_seqs,
+                     const int32_t* ctx_lens, const void* q, int64_t q_token_stride, int64_t q_head_stride,
+                     int q_heads, const int32_t* cu_q, int64_t n_q, const uint64_t* masks, int64_t max_ctx,
+                     int64_t max_new, float scale, void* out, int64_t out_token_stride, int64_t out_head_stride,
+                     float* lse, void* ws, int64_t ws_bytes, void* stream) {
   QG_TRY(check_cache(cache));
-  if (q_heads <= 0 || q_heads > 1024 || q_heads % cache->kv_heads)
-    return fail(QGEMV_ERR_ARG, "q_heads=%d must be a positive multiple of kv_heads=%d, at most 1024", q_heads, cache->kv_heads);
-  if (n_seqs < 0 || n_seqs > (1 << 20) || n_q < 0 || n_q > kMaxTokens || table_stride < 0 || max_ctx < 0 || max_new < 0)
-    return fail(QGEMV_ERR_ARG, "n_seqs outside [0, 2^20], n_q outside [0, 2^30], or a negative size");
-  if (n_q == 0 || n_seqs == 0) return qgemv::report_error(QGEMV_OK, "");
-  if ((!table && table_stride > 0) || !ctx_lens || !cu_q) return fail(QGEMV_ERR_ARG, "table, ctx_lens or cu_q is NULL");
-  if (((reinterpret_cast<uintptr_t>(table) | reinterpret_cast<uintptr_t>(ctx_lens) | reinterpret_cast<uintptr_t>(cu_q) |
-        reinterpret_cast<uintptr_t>(lse)) & 3) || (reinterpret_cast<uintptr_t>(masks) & 7))
-    return fail(QGEMV_ERR_ALIGN, "index arrays and lse must be aligned to their elements");
-  QG_TRY(check_rows("q", q, q_token_stride, q_head_stride, 2, q_heads, cache->head_dim, n_q, false));
-  QG_TRY(check_rows("out", out, out_token_stride, out_head_stride, 2, q_heads, cache->head_dim, n_q, true));
-  QG_TRY(check_ws(ws, ws_bytes, n_seqs, q_heads, cache->head_dim));
-  const int64_t lim = int64_t(1) << 30;
-  qgemv::TreeParams p = {*cache, table, table_stride, static_cast<int>(n_seqs), ctx_lens,
-                         {q, q_token_stride, q_head_stride}, q_heads, cu_q, n_q, masks,
-                         static_cast<int>(max_ctx < lim ? max_ctx : lim), static_cast<int>(max_new < lim ? max_new : lim),
-                         scale, {out, out_token_stride, out_head_stride}, lse, static_cast<uint8_t*>(ws)};
-  return done(qgemv::launch_attn_tree(p, static_cast<cudaStream_t>(stream)), "launching the attention");
+  return attend(cache, pages, pages_stride, cache->kv_heads, n_seqs, ctx_lens, {q, q_token_stride, q_head_stride}, q_heads, cu_q,
+                n_q, masks, max_ctx, max_new, scale, {out, out_token_stride, out_head_stride}, lse, ws, ws_bytes, stream);
 }
 
 int qgemv_attn_prompt(int dtype, int head_dim, int q_heads, int kv_heads, const void* q, int64_t q_token_stride,

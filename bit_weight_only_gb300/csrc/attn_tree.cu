@@ -278,7 +278,7 @@ __global__ void __launch_bounds__(TreeShape<FMT, D, NT>::kThreads, kBlocksPerSm)
         const int64_t pi = (u * kKvBlockTokens) >> a.page_shift;
         src_of = 0;
         if (k + lane < n_mine && pi < p.table_stride) {
-          const int page = __ldg(p.table + seq * p.table_stride + pi);
+          const int page = __ldg(table_row(p, seq, head) + pi);
           if (page >= 0 && page < p.cache.n_pages)
             src_of = reinterpret_cast<unsigned long long>(
                 kv_block<FMT, D>(p.cache, page, head, static_cast<int>(u & ((p.cache.page_tokens >> 4) - 1))));

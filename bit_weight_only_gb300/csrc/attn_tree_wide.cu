@@ -590,7 +590,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_wide_kernel(const TreeArgs a
           const int64_t pos = (sg.u0 + j) * kKeys + kKvBlockTokens * (lane & 7);
           const int64_t pi = pos >> a.page_shift;
           if (j >= n || pos >= n_pos || pi >= p.table_stride) return -1;
-          const int64_t pg = __ldg(p.table + sg.seq * p.table_stride + pi);
+          const int64_t pg = __ldg(table_row(p, sg.seq, sg.head) + pi);
           return pg < p.cache.n_pages ? pg : -1;
         };
         int64_t ahead = page_of(0);

@@ -1,0 +1,379 @@
+// beam.cu -- the selection of beam search (qgemv_beam_select): of a sequence's
+// candidates (beam b, token t) the `width` of largest
+//
+//   score[b] + x[b][t] - log sum_u exp x[b][u].
+//
+// One pass over the logits, which are its bytes' floor.  A block takes a part
+// of a row in tiles of 4096 values: each thread keeps a running maximum and sum
+// of exponentials, and whatever passes the part's threshold goes to a list in
+// shared memory.  Of one row the order of the candidates is that of its logits
+// (ties: the lower token first), so a candidate is a 64-bit key, value above
+// inverted token, and no two are equal.  The threshold is the `width`-th
+// largest of the threads' maxima when a tile would overflow the list (that
+// many keys at least reach it, and at most `width` threads' values do) and the
+// list's own `width`-th key once it was cut; after the first tile few values
+// pass.  A second kernel, a block a sequence and a warp a beam, merges the
+// parts' sorted lists, and then the beams by their scores in 64 bits: fp32
+// would make ties of scores that differ.
+//
+// Sums are fp32, of at most 2^12 values times the tiles of a thread; the log
+// sum and the scores are 64-bit.
+#include <type_traits>
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "beam.h"
+#include "per_device.h"
+#include "tc_common.cuh"
+
+namespace qgemv {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kPer = 16;                       // values of a thread in a tile
+constexpr int kTile = kThreads * kPer;         // values of a tile
+constexpr int kListMax = 2048;                 // keys of the list
+static_assert(kMaxWidth * kPer <= kListMax / 2, "a tile's candidates fit beside a list that was not cut yet");
+
+// Order of floats as unsigned numbers, +0 and -0 as one; 0 is below all.
+__device__ __forceinline__ uint32_t ordered(float x) {
+  const uint32_t b = __float_as_uint(x + 0.f);
+  return b & 0x80000000u ? ~b : b | 0x80000000u;
+}
+__device__ __forceinline__ float from_ordered(uint32_t o) {
+  return __uint_as_float(o & 0x80000000u ? o & 0x7fffffffu : ~o);
+}
+// Larger values first, then lower tokens; 0 for what is no candidate.
+__device__ __forceinline__ uint64_t key_of(float x, uint32_t token) {
+  return x > -INFINITY ? static_cast<uint64_t>(ordered(x)) << 32 | (0xffffffffu - token) : 0;
+}
+
+// 16-byte loads of a row that may start anywhere: the row's values are those of
+// 16-byte units from the unit that holds the first one.
+template <typename T>
+struct RowUnits {
+  static constexpr int kVec = 16 / sizeof(T);
+  const T* base;  // unit 0 (its first values may lie before the row)
+  int64_t lead, end;  // the row is values [lead, end) from base
+  __device__ RowUnits(const T* row, int64_t n) {
+    const uintptr_t a = reinterpret_cast<uintptr_t>(row);
+    lead = static_cast<int64_t>((a & 15) / sizeof(T));
+    base = row - lead;
+    end = lead + n;
+  }
+  // values of unit u; what is outside the row is -infinity
+  __device__ void load(int64_t u, float* x) const {
+    const int64_t i0 = u * kVec;
+    if (i0 >= lead && i0 + kVec <= end) {
+      const uint4 w = __ldg(reinterpret_cast<const uint4*>(base) + u);
+#pragma unroll
+      for (int i = 0; i < kVec; ++i) {
+        if constexpr (std::is_same<T, float>::value) {
+          x[i] = __uint_as_float((&w.x)[i]);
+        } else {
+          const uint32_t h = (&w.x)[i >> 1];
+          if constexpr (std::is_same<T, __half>::value)
+            x[i] = __half2float(__ushort_as_half(static_cast<unsigned short>(i & 1 ? h >> 16 : h & 0xffffu)));
+          else
+            x[i] = __uint_as_float(i & 1 ? h & 0xffff0000u : h << 16);
+        }
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < kVec; ++i) x[i] = i0 + i >= lead && i0 + i < end ? static_cast<float>(base[i0 + i]) : -INFINITY;
+    }
+  }
+};
+
+struct Lists {
+  uint64_t list[kListMax];
+  uint64_t sorted[kThreads];  // the warps' maxima, each warp's in order
+  uint64_t threshold;
+  int fill;
+};
+
+// The k-th largest (k <= 256) of the threads' keys, which differ or are 0; to
+// all threads.  Each warp sorts its own, then a key's rank is found by binary
+// searches in the others'.
+__device__ uint64_t kth_of_threads(uint64_t key, int k, Lists& s) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const unsigned full = 0xffffffffu;
+#pragma unroll
+  for (int size = 2; size <= 32; size <<= 1) {
+#pragma unroll
+    for (int o = size >> 1; o > 0; o >>= 1) {
+      const uint64_t other = __shfl_xor_sync(full, key, o);
+      const bool descending = (lane & size) == 0 || size == 32, low = (lane & o) == 0;
+      if ((key < other) == (descending == low)) key = other;
+    }
+  }
+  s.sorted[threadIdx.x] = key;
+  if (threadIdx.x == 0) s.threshold = 0;
+  __syncthreads();
+  int rank = lane;  // of equal keys (0 only) any order does
+#pragma unroll
+  for (int w = 0; w < kThreads / 32; ++w) {
+    if (w == warp) continue;
+    int n = 0;  // keys of warp w above this one
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+      if (s.sorted[w * 32 + n + o - 1] > key) n += o;
+    if (n == 31 && s.sorted[w * 32 + 31] > key) n = 32;
+    rank += n;
+  }
+  if (rank == k - 1 && key) s.threshold = key;
+  __syncthreads();
+  return s.threshold;
+}
+
+// Leaves the `width` largest keys of the list in it, in order, and the last of
+// them as the threshold (0 while there are fewer).
+__device__ uint64_t cut_list(int width, Lists& s) {
+  __syncthreads();
+  int n = min(s.fill, kListMax);
+  if (n > 2 * kThreads) {  // first by the threads' maxima: at most `width` threads' keys stay
+    uint64_t top = 0;
+    for (int i = threadIdx.x; i < n; i += kThreads) top = max(top, s.list[i]);
+    const uint64_t th = kth_of_threads(top, width, s);
+    uint64_t mine[kListMax / kThreads];
+#pragma unroll
+    for (int j = 0; j < kListMax / kThreads; ++j) {
+      const int i = threadIdx.x + j * kThreads;
+      mine[j] = i < n ? s.list[i] : 0;
+    }
+    __syncthreads();
+    if (threadIdx.x == 0) s.fill = 0;
+    __syncthreads();
+#pragma unroll
+    for (int j = 0; j < kListMax / kThreads; ++j)
+      if (mine[j] >= th && mine[j]) s.list[atomicAdd(&s.fill, 1)] = mine[j];
+    __syncthreads();
+    n = s.fill;
+  }
+  static_assert(kMaxWidth * (kListMax / kThreads) <= 2 * kThreads, "what stays is two keys a thread");
+  uint64_t mine[2];
+  int rank[2] = {0, 0};
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    const int i = threadIdx.x + j * kThreads;
+    mine[j] = i < n ? s.list[i] : 0;
+  }
+  for (int i = 0; i < n; ++i) {
+    const uint64_t o = s.list[i];
+    rank[0] += o > mine[0];
+    rank[1] += o > mine[1];
+  }
+  __syncthreads();
+  if (threadIdx.x == 0) s.fill = min(n, width), s.threshold = 0;
+  __syncthreads();
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    if (mine[j] && rank[j] < width) {
+      s.list[rank[j]] = mine[j];
+      if (rank[j] == width - 1) s.threshold = mine[j];
+    }
+  }
+  __syncthreads();
+  return s.threshold;
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kThreads) beam_row_kernel(const BeamParams p) {
+  __shared__ Lists s;
+  __shared__ float2 s_sum[kThreads / 32];
+  allow_next_kernel();
+  using Units = RowUnits<T>;
+  constexpr int kVec = Units::kVec, kUnits = kPer / kVec;
+  const int64_t row = blockIdx.x / p.parts;
+  const int part = static_cast<int>(blockIdx.x - row * p.parts);
+  const Units units(static_cast<const T*>(p.logits) + row * p.row_stride, p.vocab);
+  const int64_t first = static_cast<int64_t>(part) * p.tiles * kTile, last = min(units.end, first + static_cast<int64_t>(p.tiles) * kTile);
+  if (threadIdx.x == 0) s.fill = 0;
+  __syncthreads();
+
+  float m = -INFINITY, l = 0.f;
+  uint64_t threshold = 0;  // keys above it are candidates (and equal to it: it is in the list)
+  for (int64_t at = first; at < last; at += kTile) {
+    float x[kPer];
+#pragma unroll
+    for (int i = 0; i < kUnits; ++i) units.load(at / kVec + i * kThreads + threadIdx.x, x + i * kVec);
+    auto token = [&](int i) {
+      return static_cast<uint32_t>(at + (static_cast<int64_t>(i / kVec) * kThreads + threadIdx.x) * kVec + i % kVec - units.lead);
+    };
+    float top = x[0];
+#pragma unroll
+    for (int i = 1; i < kPer; ++i) top = fmaxf(top, x[i]);
+    const float mn = fmaxf(m, top), ref = mn == -INFINITY ? 0.f : mn;
+    float sum = 0.f;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) sum += ex2((x[i] - ref) * kLog2e);
+    l = l * ex2((m - ref) * kLog2e) + sum;
+    m = mn;
+
+    // candidates: values that the threshold's does not exceed
+    const float low = threshold ? from_ordered(static_cast<uint32_t>(threshold >> 32)) : -INFINITY;
+    int mine = 0;
+    if (top >= low) {
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) mine += key_of(x[i], token(i)) > threshold;
+    }
+    const int fill = s.fill;  // read before any thread of this tile adds to it: the branches below are the block's
+    const int total = __syncthreads_count(mine > 0);
+    if (total == 0) continue;
+    // (an upper bound: a thread has at most kPer)
+    if (fill + total * kPer > kListMax) {
+      uint64_t best = 0;
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) best = max(best, key_of(x[i], token(i)));
+      const uint64_t th = kth_of_threads(best, p.width, s);
+      // at least `width` of the tile reach it
+      if (th > threshold) threshold = th - 1;
+      if (fill + p.width * kPer > kListMax) threshold = max(threshold, cut_list(p.width, s));
+    }
+    if (mine) {
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) {
+        const uint64_t k = key_of(x[i], token(i));
+        if (k > threshold) {
+          const int to = atomicAdd(&s.fill, 1);
+          if (to < kListMax) s.list[to] = k;
+        }
+      }
+    }
+    __syncthreads();
+    if (s.fill > 2 * kThreads) threshold = max(threshold, cut_list(p.width, s));
+  }
+  cut_list(p.width, s);
+  uint64_t* keys = p.keys + (row * p.parts + part) * p.width;
+  for (int i = threadIdx.x; i < p.width; i += kThreads) keys[i] = i < s.fill ? s.list[i] : 0;
+
+  // the sums of the threads
+  auto join = [](float& m, float& l, float om, float ol) {
+    const float mn = fmaxf(m, om), ref = mn == -INFINITY ? 0.f : mn;
+    l = l * ex2((m - ref) * kLog2e) + ol * ex2((om - ref) * kLog2e);
+    m = mn;
+  };
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    const float om = __shfl_xor_sync(0xffffffffu, m, o), ol = __shfl_xor_sync(0xffffffffu, l, o);
+    join(m, l, om, ol);
+  }
+  if ((threadIdx.x & 31) == 0) s_sum[threadIdx.x >> 5] = make_float2(m, l);
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    for (int w = 1; w < kThreads / 32; ++w) join(m, l, s_sum[w].x, s_sum[w].y);
+    p.sums[row * p.parts + part] = make_float2(m, l);
+  }
+}
+
+// The largest key of the warp's lanes, and the lane that has it.
+__device__ __forceinline__ uint64_t warp_max(uint64_t key) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) key = max(key, __shfl_xor_sync(0xffffffffu, key, o));
+  return key;
+}
+__device__ __forceinline__ uint64_t ordered64(double x) {
+  const uint64_t b = static_cast<uint64_t>(__double_as_longlong(x + 0.0));
+  return b >> 63 ? ~b : b | 1ull << 63;
+}
+__device__ __forceinline__ double from_ordered64(uint64_t o) {
+  return __longlong_as_double(static_cast<long long>(o >> 63 ? o & ~(1ull << 63) : ~o));
+}
+
+__global__ void __launch_bounds__(1024) beam_merge_kernel(const BeamParams p) {
+  __shared__ uint64_t s_keys[kMaxBeams][kMaxWidth];  // scores of a beam's candidates, descending (0: none)
+  __shared__ uint32_t s_tokens[kMaxBeams][kMaxWidth];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+  const unsigned full = 0xffffffffu;
+  const int64_t seq = blockIdx.x;
+  wait_for_last_kernel();
+  for (int b = warp; b < p.beams; b += warps) {
+    const int64_t row = seq * p.beams + b;
+    // the log sum, and what the beam's candidates start from
+    float2 ml = make_float2(-INFINITY, 0.f);
+    const uint64_t* keys = p.keys + (row * p.parts + lane) * p.width;
+    uint64_t head = 0;
+    if (lane < p.parts) ml = p.sums[row * p.parts + lane], head = keys[0];
+    float top = ml.x;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(full, top, o));
+    double l = ml.x == -INFINITY && ml.y == 0.f ? 0.0 : static_cast<double>(ml.y) * exp(static_cast<double>(ml.x) - static_cast<double>(top));
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(full, l, o);
+    const double base = static_cast<double>(p.scores[row]) - (static_cast<double>(top) + log(l));
+    const bool fine = isfinite(base);
+    // the parts' lists, merged
+    int at = 0;
+    for (int i = 0; i < p.width; ++i) {
+      const uint64_t best = fine ? warp_max(head) : 0;
+      if (best && best == head) head = ++at < p.width ? keys[at] : 0;  // one lane: keys differ
+      if (lane == 0) {
+        s_keys[b][i] = best ? ordered64(base + static_cast<double>(from_ordered(static_cast<uint32_t>(best >> 32)))) : 0;
+        s_tokens[b][i] = 0xffffffffu - static_cast<uint32_t>(best);
+      }
+    }
+  }
+  __syncthreads();
+  if (warp != 0) return;
+  // the beams' lists, merged: ties go to the lower beam, whose token is lower
+  int at[2] = {0, 0};
+  uint64_t head[2];
+#pragma unroll
+  for (int j = 0; j < 2; ++j) head[j] = lane + 32 * j < p.beams ? s_keys[lane + 32 * j][0] : 0;
+  for (int i = 0; i < p.width; ++i) {
+    const uint64_t best = warp_max(max(head[0], head[1]));
+    const unsigned lo = __ballot_sync(full, best && head[0] == best), hi = __ballot_sync(full, best && head[1] == best);
+    const int b = lo ? __ffs(lo) - 1 : hi ? 31 + __ffs(hi) : -1;
+    const int64_t to = seq * p.width + i;
+    if (b < 0) {
+      if (lane == 0) p.out_scores[to] = -INFINITY, p.out_beams[to] = -1, p.out_tokens[to] = -1;
+      continue;
+    }
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      if (b == lane + 32 * j) {
+        p.out_scores[to] = static_cast<float>(from_ordered64(best));
+        p.out_beams[to] = b;
+        p.out_tokens[to] = static_cast<int32_t>(s_tokens[b][at[j]]);
+        head[j] = ++at[j] < p.width ? s_keys[b][at[j]] : 0;
+      }
+    }
+  }
+}
+
+}  // namespace
+
+// Parts of a row: enough blocks to fill the GPU, of a tile at least.
+int beam_parts(int64_t rows, int64_t vocab, int sms) {
+  const int64_t tiles = (vocab + 7 + kTile - 1) / kTile;  // (a row that starts inside a 16-byte unit is up to 7 longer)
+  const int64_t want = (4 * static_cast<int64_t>(sms) + rows - 1) / rows;
+  int64_t parts = want < tiles ? want : tiles;
+  if (parts > kMaxParts) parts = kMaxParts;
+  const int64_t per = (tiles + parts - 1) / parts;
+  return static_cast<int>((tiles + per - 1) / per);
+}
+
+cudaError_t launch_beam(const BeamParams& given, int dtype, cudaStream_t s) {
+  int dev = 0, sms = 0;
+  const cudaError_t found = current_device(&dev, &sms);
+  if (found != cudaSuccess) return found;
+  BeamParams p = given;
+  const int64_t rows = p.n_seqs * p.beams;
+  p.parts = beam_parts(rows, p.vocab, sms);
+  p.tiles = static_cast<int>(((p.vocab + 7 + kTile - 1) / kTile + p.parts - 1) / p.parts);
+  p.sums = reinterpret_cast<float2*>(p.keys + rows * p.parts * p.width);
+  const int64_t grid = rows * p.parts;
+  if (grid > 0x7fffffff) return cudaErrorInvalidConfiguration;
+  auto go = [&](auto kernel) {
+    kernel<<<static_cast<unsigned>(grid), kThreads, 0, s>>>(p);
+    return cudaGetLastError();
+  };
+  const cudaError_t e = dtype == QGEMV_DT_F32 ? go(beam_row_kernel<float>)
+                        : dtype == QGEMV_DT_F16 ? go(beam_row_kernel<__half>) : go(beam_row_kernel<__nv_bfloat16>);
+  if (e != cudaSuccess) return e;
+  const int warps = p.beams < 32 ? p.beams : 32;
+  return launch_after(beam_merge_kernel, static_cast<unsigned>(p.n_seqs), p, s, 32 * warps);
+}
+
+}  // namespace qgemv

@@ -1,0 +1,359 @@
+// pages.cu -- pages of a cache given out, shared, returned, packed and copied
+// (qgemv_pool_*, qgemv_kv_copy_pages).
+//
+// A pool is a count of rows for each page (0: free).  All of it is whole
+// numbers: counts change by atomic additions, whose order does not matter, and
+// free pages are given out lowest first in the rows' order, so a call's results
+// depend on its inputs alone.  Nothing returns to the host.
+//
+// Bookkeeping reads tables and counts of a few hundred kB at most: a chain of
+// latencies, of a launch and a scan, bounds it.  Free pages are found by one
+// block in steps of 16384 counts, as many as are needed, the lowest first; the
+// compacting scan, which needs all counts, is spread over blocks of 4096 each,
+// whose sums every block adds up for itself.  Copies are bytes: a block takes
+// 16 kB of a page with all of its loads in flight.
+#include "pages.h"
+#include "per_device.h"
+#include "kv_layout.cuh"
+#include "tc_common.cuh"
+
+namespace qgemv {
+namespace {
+
+constexpr int kGive = 1024;     // threads of the block that gives pages out
+constexpr int kGivePer = 16;    // counts of a thread in a step
+constexpr int kRowThreads = 256;
+
+// Inclusive sum over the block's threads; `total` to all of them.
+template <int THREADS>
+__device__ int block_sum(int x, int* s_warp, int& total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += y;
+  }
+  if (lane == 31) s_warp[warp] = x;
+  __syncthreads();
+  if (warp == 0) {
+    int w = lane < THREADS / 32 ? s_warp[lane] : 0;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, w, o);
+      if (lane >= o) w += y;
+    }
+    s_warp[lane] = w;
+  }
+  __syncthreads();
+  const int before = warp > 0 ? s_warp[warp - 1] : 0;
+  total = s_warp[THREADS / 32 - 1];
+  __syncthreads();
+  return before + x;
+}
+
+// The lowest free pages, `want` of them where there are as many: give(rank,
+// page), each by some thread of the block.  Returns how many there were.
+template <typename F>
+__device__ int free_pages(const int32_t* refs, int64_t n_pages, int want, int* s_warp, F give) {
+  int got = 0;
+  for (int64_t p0 = 0; p0 < n_pages && got < want; p0 += kGive * kGivePer) {
+    const int64_t mine = p0 + static_cast<int64_t>(threadIdx.x) * kGivePer;
+    int v[kGivePer];
+    if (mine + kGivePer <= n_pages && (reinterpret_cast<uintptr_t>(refs) & 15) == 0) {
+#pragma unroll
+      for (int i = 0; i < kGivePer; i += 4) *reinterpret_cast<int4*>(v + i) = *reinterpret_cast<const int4*>(refs + mine + i);
+    } else {
+#pragma unroll
+      for (int i = 0; i < kGivePer; ++i) v[i] = mine + i < n_pages ? refs[mine + i] : 1;
+    }
+    int n = 0, total;
+#pragma unroll
+    for (int i = 0; i < kGivePer; ++i) n += v[i] <= 0;
+    int rank = got + block_sum<kGive>(n, s_warp, total) - n;
+#pragma unroll
+    for (int i = 0; i < kGivePer; ++i) {
+      if (v[i] <= 0) {
+        if (rank < want) give(rank, static_cast<int32_t>(mine + i));
+        ++rank;
+      }
+    }
+    got += total;
+  }
+  return min(got, want);
+}
+
+__device__ __forceinline__ int64_t pages_for(int64_t tokens, int page) { return tokens <= 0 ? 0 : (tokens + page - 1) / page; }
+
+// ---- reserve: one block
+__global__ void __launch_bounds__(kGive) reserve_kernel(const PoolParams p) {
+  __shared__ int s_warp[32];
+  extern __shared__ int s_upto[];  // pages that the sequences up to and with this one need
+  const int n = static_cast<int>(p.n_seqs);
+  auto range = [&](int b, int64_t& e0, int64_t& e1) {
+    e0 = pages_for(p.from[b], p.page_tokens);
+    e1 = min(pages_for(p.to[b], p.page_tokens), p.table_stride);
+    if (e1 < e0) e1 = e0;
+  };
+  int64_t want = 0;
+  for (int b0 = 0; b0 < n; b0 += kGive) {
+    const int b = b0 + threadIdx.x;
+    int64_t e0 = 0, e1 = 0;
+    if (b < n) range(b, e0, e1);
+    int total;
+    const int mine = block_sum<kGive>(static_cast<int>(e1 - e0), s_warp, total);  // (a row has at most 2^20 entries)
+    if (b < n) s_upto[b] = static_cast<int>(min(want + mine, static_cast<int64_t>(0x7fffffff)));
+    want += total;
+  }
+  want = min(want, static_cast<int64_t>(0x7fffffff));
+  __syncthreads();
+  auto place = [&](int rank) -> int32_t* {  // the entry that gets the page of this rank
+    int lo = 0, hi = n - 1;
+    while (lo < hi) {
+      const int mid = (lo + hi) >> 1;
+      if (s_upto[mid] <= rank) lo = mid + 1;
+      else hi = mid;
+    }
+    return p.table + lo * p.table_stride + pages_for(p.from[lo], p.page_tokens) + rank - (lo > 0 ? s_upto[lo - 1] : 0);
+  };
+  const int got = free_pages(p.refs, p.n_pages, static_cast<int>(want), s_warp, [&](int rank, int32_t page) {
+    *place(rank) = page;
+    p.refs[page] = 1;
+  });
+  for (int64_t r = got + static_cast<int64_t>(threadIdx.x); r < want; r += kGive) *place(static_cast<int>(r)) = -1;
+  if (threadIdx.x == 0 && got < want) *p.missing += static_cast<int>(want - got);
+}
+
+// ---- fork: a block for each old row (its pages' counts, its children's
+// copies) and each new one (its entries)
+__global__ void __launch_bounds__(kRowThreads) fork_rows_kernel(const PoolParams p) {
+  __shared__ int s_kids, s_first;
+  allow_next_kernel();
+  if (blockIdx.x < p.n_old) {
+    const int64_t b = blockIdx.x;
+    if (threadIdx.x == 0) s_kids = 0, s_first = 0x7fffffff;
+    __syncthreads();
+    for (int64_t r = threadIdx.x; r < p.n_seqs; r += kRowThreads)
+      if (p.parents[r] == b) atomicAdd(&s_kids, 1), atomicMin(&s_first, static_cast<int>(r));
+    __syncthreads();
+    const int kids = s_kids, len = max(p.from[b], 0), rest = len % p.page_tokens;
+    const int64_t used = pages_for(len, p.page_tokens), here = min(used, p.old_stride);
+    const int32_t* row = p.old_table + b * p.old_stride;
+    for (int64_t e = threadIdx.x; e < here; e += kRowThreads) {
+      const int32_t page = row[e];
+      // the page that is filled in part stays with the first child alone
+      const int change = (rest && e == used - 1 ? min(kids, 1) : kids) - 1;
+      if (page >= 0 && page < p.n_pages && change) atomicAdd(p.refs + page, change);
+    }
+    const int32_t last = rest && used <= p.old_stride ? row[used - 1] : -1;
+    const bool copies = last >= 0 && last < p.n_pages;
+    for (int64_t r = threadIdx.x; r < p.n_seqs; r += kRowThreads) {
+      if (p.parents[r] != b) continue;
+      const bool copy = copies && r != s_first;
+      p.src[r] = copy ? last : -1;
+      p.tokens[r] = copy ? rest : 0;
+    }
+  } else {
+    const int64_t r = blockIdx.x - p.n_old;
+    const int64_t b = p.parents[r];
+    const bool there = b >= 0 && b < p.n_old;
+    if (!there && threadIdx.x == 0) p.src[r] = -1, p.tokens[r] = 0;
+    const int64_t used = there ? min(pages_for(p.from[b], p.page_tokens), p.old_stride) : 0;
+    for (int64_t e = threadIdx.x; e < p.table_stride; e += kRowThreads)
+      p.table[r * p.table_stride + e] = e < used ? p.old_table[b * p.old_stride + e] : -1;
+  }
+}
+
+// The copies' pages: one block.
+__global__ void __launch_bounds__(kGive) fork_copies_kernel(const PoolParams p) {
+  __shared__ int s_warp[32];
+  __shared__ int s_rows[kMaxPoolSeqs];  // the rows that get a copy
+  wait_for_last_kernel();
+  int want = 0;
+  for (int64_t r0 = 0; r0 < p.n_seqs; r0 += kGive) {
+    const int64_t r = r0 + threadIdx.x;
+    const bool need = r < p.n_seqs && p.src[r] >= 0;
+    int total;
+    const int at = want + block_sum<kGive>(need, s_warp, total) - 1;
+    if (need) s_rows[at] = static_cast<int>(r);
+    else if (r < p.n_seqs) p.dst[r] = -1;
+    want += total;
+  }
+  __syncthreads();
+  auto entry = [&](int r) -> int32_t& {
+    return p.table[r * p.table_stride + pages_for(p.from[p.parents[r]], p.page_tokens) - 1];
+  };
+  const int got = free_pages(p.refs, p.n_pages, want, s_warp, [&](int rank, int32_t page) {
+    const int r = s_rows[rank];
+    p.dst[r] = page;
+    entry(r) = page;
+    p.refs[page] = 1;
+  });
+  for (int i = got + threadIdx.x; i < want; i += kGive) {
+    const int r = s_rows[i];
+    p.dst[r] = -1;
+    entry(r) = -1;
+  }
+  if (threadIdx.x == 0 && got < want) *p.missing += want - got;
+}
+
+// ---- release: a block for each row
+__global__ void __launch_bounds__(kRowThreads) release_kernel(const PoolParams p) {
+  const int64_t b = blockIdx.x;
+  const int64_t e0 = p.from ? pages_for(p.from[b], p.page_tokens) : 0;
+  const int64_t e1 = min(pages_for(p.to[b], p.page_tokens), p.table_stride);
+  for (int64_t e = e0 + threadIdx.x; e < e1; e += kRowThreads) {
+    int32_t& page = p.table[b * p.table_stride + e];
+    if (page >= 0 && page < p.n_pages) atomicSub(p.refs + page, 1);
+    page = -1;
+  }
+}
+
+// ---- compact
+__device__ __forceinline__ int64_t pool_tiles(int64_t n_pages) { return (n_pages + kPoolTile - 1) / kPoolTile; }
+
+// Pages in use of a tile.
+__global__ void __launch_bounds__(kRowThreads) compact_count_kernel(const PoolParams p) {
+  __shared__ int s_warp[32];
+  allow_next_kernel();
+  const int64_t p0 = static_cast<int64_t>(blockIdx.x) * kPoolTile;
+  int n = 0, total;
+  for (int i = threadIdx.x; i < kPoolTile; i += kRowThreads) n += p0 + i < p.n_pages && p.refs[p0 + i] > 0;
+  block_sum<kRowThreads>(n, s_warp, total);
+  if (threadIdx.x == 0) p.scratch[blockIdx.x] = total;
+}
+
+// The moves: with U pages in use, the j-th one from number U on goes to the
+// j-th free one below.  map[page] = j for a page that moves, else -1.
+__global__ void __launch_bounds__(kRowThreads) compact_moves_kernel(const PoolParams p) {
+  __shared__ int s_warp[32];
+  allow_next_kernel();
+  wait_for_last_kernel();
+  const int64_t tiles = pool_tiles(p.n_pages), me = blockIdx.x;
+  int32_t* map = p.scratch + tiles;
+  // pages in use before this tile, and in all
+  int before = 0, all = 0, used, below;
+  for (int64_t t = threadIdx.x; t < tiles; t += kRowThreads) {
+    all += p.scratch[t];
+    if (t < me) before += p.scratch[t];
+  }
+  block_sum<kRowThreads>(before, s_warp, before);
+  block_sum<kRowThreads>(all, s_warp, used);
+  // pages in use below number `used`
+  int n = 0;
+  const int64_t edge = used / kPoolTile;
+  for (int64_t t = threadIdx.x; t < edge; t += kRowThreads) n += p.scratch[t];
+  for (int64_t q = edge * kPoolTile + threadIdx.x; q < used; q += kRowThreads) n += p.refs[q] > 0;
+  block_sum<kRowThreads>(n, s_warp, below);
+
+  for (int i0 = 0; i0 < kPoolTile; i0 += kRowThreads) {
+    const int64_t page = me * kPoolTile + i0 + threadIdx.x;
+    const bool on = page < p.n_pages && p.refs[page] > 0;
+    int total;
+    const int upto = before + block_sum<kRowThreads>(on, s_warp, total) - on;  // in use before this page
+    before += total;
+    if (page >= p.n_pages) continue;
+    const bool moves = on && page >= used;
+    const int64_t j = moves ? upto - below : page - upto;
+    map[page] = moves ? static_cast<int32_t>(j) : -1;
+    if (j >= p.n_moves) continue;
+    if (moves) p.src[j] = static_cast<int32_t>(page);
+    else if (!on && page < used) p.dst[j] = static_cast<int32_t>(page);
+  }
+  // behind the moves: as many as there are pages in use from number `used` on
+  for (int64_t j = used - below + me * kRowThreads + threadIdx.x; j < p.n_moves; j += tiles * kRowThreads) p.src[j] = p.dst[j] = -1;
+}
+
+// Tables and counts follow.
+__global__ void __launch_bounds__(kRowThreads) compact_apply_kernel(const PoolParams p) {
+  wait_for_last_kernel();
+  const int32_t* map = p.scratch + pool_tiles(p.n_pages);
+  const int64_t at = static_cast<int64_t>(blockIdx.x) * kRowThreads + threadIdx.x, all = static_cast<int64_t>(gridDim.x) * kRowThreads;
+  for (int64_t i = at; i < p.n_seqs * p.table_stride; i += all) {
+    const int64_t b = i / p.table_stride, e = i - b * p.table_stride;
+    const int32_t page = p.old_table[b * p.old_stride + e];
+    const int j = page >= 0 && page < p.n_pages ? map[page] : -1;
+    p.table[i] = j >= 0 ? p.dst[j] : page;
+  }
+  for (int64_t j = at; j < p.n_moves; j += all) {
+    const int32_t from = p.src[j], to = p.dst[j];
+    if (from < 0) break;
+    p.refs[to] = p.refs[from];
+    p.refs[from] = 0;
+  }
+}
+
+// ---- copies: a block takes kCopyBytes of a page at a time
+constexpr int kCopyThreads = 256;
+constexpr int kCopyUnits = 4;  // 16-byte units of a thread
+constexpr int kCopyBytes = kCopyThreads * kCopyUnits * 16;
+
+__global__ void __launch_bounds__(kCopyThreads) copy_pages_kernel(const CopyPagesParams p) {
+  const int64_t chunks = (p.page_bytes + kCopyBytes - 1) / kCopyBytes;
+  for (int64_t item = blockIdx.x; item < p.n * chunks; item += gridDim.x) {
+    const int64_t i = div_small(item, chunks), chunk = item - i * chunks;
+    const int64_t from = p.src[i], to = p.dst[i];
+    if (from < 0 || from >= p.n_pages || to < 0 || to >= p.n_pages) continue;
+    // the blocks of the first tokens of each head: `run` units at every `step`
+    const int blocks = p.tokens ? (min(max(p.tokens[i], 0), p.blocks * kKvBlockTokens) + kKvBlockTokens - 1) / kKvBlockTokens : p.blocks;
+    const uint32_t run = static_cast<uint32_t>(blocks) * p.block_bytes / 16, step = static_cast<uint32_t>(p.blocks) * p.block_bytes / 16;
+    const int64_t units = static_cast<int64_t>(run) * p.heads, u0 = chunk * (kCopyBytes / 16) + threadIdx.x;
+    const uint4* s = reinterpret_cast<const uint4*>(p.pages + from * p.page_bytes);
+    uint4* d = reinterpret_cast<uint4*>(p.pages + to * p.page_bytes);
+    uint4 x[kCopyUnits];
+    int64_t at[kCopyUnits];
+#pragma unroll
+    for (int k = 0; k < kCopyUnits; ++k) {
+      const int64_t u = u0 + k * kCopyThreads;
+      at[k] = -1;
+      if (u < units) {
+        const int64_t h = run == step ? 0 : div_small(u, run);
+        at[k] = u + h * (step - run);
+        x[k] = s[at[k]];
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < kCopyUnits; ++k)
+      if (at[k] >= 0) d[at[k]] = x[k];
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_pool_reserve(const PoolParams& p, cudaStream_t s) {
+  reserve_kernel<<<1, kGive, static_cast<unsigned>(p.n_seqs) * 4, s>>>(p);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_pool_fork(const PoolParams& p, cudaStream_t s) {
+  fork_rows_kernel<<<static_cast<unsigned>(p.n_old + p.n_seqs), kRowThreads, 0, s>>>(p);
+  const cudaError_t e = cudaGetLastError();
+  return e != cudaSuccess ? e : launch_after(fork_copies_kernel, 1, p, s, kGive);
+}
+
+cudaError_t launch_pool_release(const PoolParams& p, cudaStream_t s) {
+  release_kernel<<<static_cast<unsigned>(p.n_seqs), kRowThreads, 0, s>>>(p);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_pool_compact(const PoolParams& p, cudaStream_t s) {
+  const unsigned tiles = static_cast<unsigned>((p.n_pages + kPoolTile - 1) / kPoolTile);
+  compact_count_kernel<<<tiles, kRowThreads, 0, s>>>(p);
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  e = launch_after(compact_moves_kernel, tiles, p, s, kRowThreads);
+  if (e != cudaSuccess) return e;
+  const int64_t items = p.n_seqs * p.table_stride > p.n_moves ? p.n_seqs * p.table_stride : p.n_moves;
+  const int64_t blocks = (items + kRowThreads - 1) / kRowThreads;
+  return launch_after(compact_apply_kernel, static_cast<unsigned>(blocks < 1 ? 1 : blocks < 1024 ? blocks : 1024), p, s, kRowThreads);
+}
+
+cudaError_t launch_copy_pages(const CopyPagesParams& p, cudaStream_t s) {
+  int dev = 0, sms = 0;
+  const cudaError_t found = current_device(&dev, &sms);
+  if (found != cudaSuccess) return found;
+  const int64_t items = p.n * ((p.page_bytes + kCopyBytes - 1) / kCopyBytes), most = 8 * static_cast<int64_t>(sms);
+  copy_pages_kernel<<<static_cast<unsigned>(items < most ? items : most), kCopyThreads, 0, s>>>(p);
+  return cudaGetLastError();
+}
+
+}  // namespace qgemv

@@ -59,6 +59,11 @@ __device__ __forceinline__ int64_t run_quota(const TreeArgs& a, int64_t total) {
   return max(static_cast<int64_t>(a.min_units), div_small(total + a.grid - 1, a.grid));
 }
 
+// The page table of a head of a sequence.
+__device__ __forceinline__ const int32_t* table_row(const TreeParams& p, int seq, int head) {
+  return p.table + (p.table_heads == 1 ? seq : static_cast<int64_t>(seq) * p.table_heads + head) * p.table_stride;
+}
+
 // A block's part of one row tile.
 struct Segment {
   int seq, head, tile, ctx, T;

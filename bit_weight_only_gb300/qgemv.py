@@ -23,6 +23,8 @@ QGEMV_OK, QGEMV_ERR_ARG, QGEMV_ERR_ALIGN, QGEMV_ERR_CUDA, QGEMV_ERR_TIMEOUT, QGE
 KV_F16, KV_INT8, KV_Q4_0 = 1, 2, 3
 KV_FORMATS = {"f16": KV_F16, "int8": KV_INT8, "q4_0": KV_Q4_0}
 DT_F32, DT_F16, DT_BF16 = 0, 1, 2
+ROPE_HALVES, ROPE_NEIGHBOURS = 0, 1
+ROPE_PAIRINGS = {"halves": ROPE_HALVES, "neighbours": ROPE_NEIGHBOURS}
 
 
 class KvCacheDesc(ctypes.Structure):
@@ -77,6 +79,23 @@ _SIGNATURES = {
     "qgemv_attn_tree": (_I, [_P, _P, _L, _L, _P, _P, _L, _L, _I, _P, _L, _P, _L, _L, _F, _P, _L, _L, _P, _P, _L, _P]),
     "qgemv_attn_prompt": (_I, [_I, _I, _I, _I, _P, _L, _L, _P, _L, _L, _P, _L, _L, _L, _P, _P, _L, _L, _L, _F,
                                _P, _L, _L, _P, _P, _L, _P]),
+    "qgemv_rope_plan_bytes": (_L, [_I]),
+    "qgemv_rope_plan": (_I, [_P, _P, _I, _P]),
+    "qgemv_rope_rows": (_I, [_P, _I, _I, _I, _P, _I, _I, _I, _P, _L, _L, _L, _I, _P, _L, _L, _P]),
+    "qgemv_kv_write_rotated": (_I, [_P, _P, _I, _I, _I, _P, _I, _P, _L, _L, _I, _P, _L, _L, _P, _L, _L, _P, _L, _I,
+                                    _P, _L, _L, _P]),
+    "qgemv_beam_ws_bytes": (_L, [_L, _I, _L, _I]),
+    "qgemv_beam_select": (_I, [_I, _P, _L, _L, _P, _L, _I, _I, _P, _P, _P, _P, _L, _P]),
+    "qgemv_pool_reserve": (_I, [_P, _L, _I, _P, _L, _L, _P, _P, _P, _P]),
+    "qgemv_pool_fork": (_I, [_P, _L, _I, _P, _L, _L, _P, _L, _P, _P, _P, _P, _P, _P, _P]),
+    "qgemv_pool_release": (_I, [_P, _L, _I, _P, _L, _L, _P, _P, _P]),
+    "qgemv_pool_ws_bytes": (_L, [_L]),
+    "qgemv_pool_compact": (_I, [_P, _L, _P, _L, _L, _P, _P, _P, _L, _P, _L, _P]),
+    "qgemv_kv_copy_pages": (_I, [_P, _P, _P, _P, _L, _P]),
+    "qgemv_kv_summarize": (_I, [_P, _P, _L, _P, _P, _P]),
+    "qgemv_kv_select_width": (_L, [_I, _L]),
+    "qgemv_kv_select": (_I, [_P, _P, _P, _P, _L, _L, _P, _P, _L, _L, _I, _P, _L, _L, _P, _P, _P]),
+    "qgemv_attn_pages": (_I, [_P, _P, _L, _L, _P, _P, _L, _L, _I, _P, _L, _P, _L, _L, _F, _P, _L, _L, _P, _P, _L, _P]),
     "qgemv_last_error": (ctypes.c_char_p, []),
     "qgemv_last_error_code": (ctypes.c_int, []),
 }
@@ -290,6 +309,100 @@ def qgemv_attn_prompt(dtype: int, head_dim: int, q_heads: int, kv_heads: int, q:
                                            k_token_stride, k_head_stride, v, v_token_stride, v_head_stride, n_seqs,
                                            cu_q, cu_k, n_q, n_k, max_q, scale, out, out_token_stride, out_head_stride,
                                            lse, ws, ws_bytes, _stream_ptr(stream)))
+
+
+def qgemv_rope_plan_bytes(pairs: int) -> int:
+    return int(load().qgemv_rope_plan_bytes(pairs))
+
+
+def qgemv_rope_plan(freqs: int, axes: int, pairs: int, plan: int) -> int:
+    return _check(load().qgemv_rope_plan(freqs, axes, pairs, plan))
+
+
+def qgemv_rope_rows(plan: int, pairs: int, pairing: int, n_axes: int, positions: int, dtype: int, heads: int,
+                    head_dim: int, x: int, x_token_stride: int, x_head_stride: int, n_tokens: int, out_dtype: int,
+                    out: int, out_token_stride: int, out_head_stride: int, stream=None) -> int:
+    return _check(load().qgemv_rope_rows(plan, pairs, pairing, n_axes, positions, dtype, heads, head_dim, x,
+                                         x_token_stride, x_head_stride, n_tokens, out_dtype, out, out_token_stride,
+                                         out_head_stride, _stream_ptr(stream)))
+
+
+def qgemv_kv_write_rotated(cache: KvCacheDesc, plan: int, pairs: int, pairing: int, n_axes: int, positions: int,
+                           dtype: int, q: int, q_token_stride: int, q_head_stride: int, q_heads: int, k: int,
+                           k_token_stride: int, k_head_stride: int, v: int, v_token_stride: int, v_head_stride: int,
+                           slots: int, n_tokens: int, out_dtype: int, q_out: int, out_token_stride: int,
+                           out_head_stride: int, stream=None) -> int:
+    return _check(load().qgemv_kv_write_rotated(
+        ctypes.byref(cache), plan, pairs, pairing, n_axes, positions, dtype, q, q_token_stride, q_head_stride, q_heads, k,
+        k_token_stride, k_head_stride, v, v_token_stride, v_head_stride, slots, n_tokens, out_dtype, q_out,
+        out_token_stride, out_head_stride, _stream_ptr(stream)))
+
+
+def qgemv_beam_ws_bytes(n_seqs: int, beams: int, vocab: int, width: int) -> int:
+    return int(load().qgemv_beam_ws_bytes(n_seqs, beams, vocab, width))
+
+
+def qgemv_beam_select(dtype: int, logits: int, row_stride: int, vocab: int, scores: int, n_seqs: int, beams: int, width: int,
+                      out_scores: int, out_beams: int, out_tokens: int, ws: int, ws_bytes: int, stream=None) -> int:
+    return _check(load().qgemv_beam_select(dtype, logits, row_stride, vocab, scores, n_seqs, beams, width, out_scores,
+                                           out_beams, out_tokens, ws, ws_bytes, _stream_ptr(stream)))
+
+
+def qgemv_pool_reserve(refs: int, n_pages: int, page_tokens: int, table: int, table_stride: int, n_seqs: int, have: int,
+                       need: int, missing: int, stream=None) -> int:
+    return _check(load().qgemv_pool_reserve(refs, n_pages, page_tokens, table, table_stride, n_seqs, have, need, missing,
+                                            _stream_ptr(stream)))
+
+
+def qgemv_pool_fork(refs: int, n_pages: int, page_tokens: int, table: int, table_stride: int, n_rows: int, parents: int,
+                    n_new: int, lens: int, new_table: int, src: int, dst: int, tokens: int, missing: int, stream=None) -> int:
+    return _check(load().qgemv_pool_fork(refs, n_pages, page_tokens, table, table_stride, n_rows, parents, n_new, lens,
+                                         new_table, src, dst, tokens, missing, _stream_ptr(stream)))
+
+
+def qgemv_pool_release(refs: int, n_pages: int, page_tokens: int, table: int, table_stride: int, n_seqs: int, lens: int,
+                       keep: int | None, stream=None) -> int:
+    return _check(load().qgemv_pool_release(refs, n_pages, page_tokens, table, table_stride, n_seqs, lens, keep,
+                                            _stream_ptr(stream)))
+
+
+def qgemv_pool_ws_bytes(n_pages: int) -> int:
+    return int(load().qgemv_pool_ws_bytes(n_pages))
+
+
+def qgemv_pool_compact(refs: int, n_pages: int, table: int, table_stride: int, n_seqs: int, new_table: int, src: int, dst: int,
+                       n_moves: int, ws: int, ws_bytes: int, stream=None) -> int:
+    return _check(load().qgemv_pool_compact(refs, n_pages, table, table_stride, n_seqs, new_table, src, dst, n_moves, ws,
+                                            ws_bytes, _stream_ptr(stream)))
+
+
+def qgemv_kv_copy_pages(cache: KvCacheDesc, src: int, dst: int, tokens: int | None, n: int, stream=None) -> int:
+    return _check(load().qgemv_kv_copy_pages(ctypes.byref(cache), src, dst, tokens, n, _stream_ptr(stream)))
+
+
+def qgemv_kv_summarize(cache: KvCacheDesc, pages: int, n: int, codes: int, scales: int, stream=None) -> int:
+    return _check(load().qgemv_kv_summarize(ctypes.byref(cache), pages, n, codes, scales, _stream_ptr(stream)))
+
+
+def qgemv_kv_select_width(page_tokens: int, n_select: int) -> int:
+    return int(load().qgemv_kv_select_width(page_tokens, n_select))
+
+
+def qgemv_kv_select(cache: KvCacheDesc, codes: int, scales: int, table: int, table_stride: int, n_seqs: int, ctx_lens: int,
+                    q: int, q_token_stride: int, q_head_stride: int, q_heads: int, cu_q: int, n_q: int, n_select: int,
+                    pages: int, lens: int, stream=None) -> int:
+    return _check(load().qgemv_kv_select(ctypes.byref(cache), codes, scales, table, table_stride, n_seqs, ctx_lens, q,
+                                         q_token_stride, q_head_stride, q_heads, cu_q, n_q, n_select, pages, lens,
+                                         _stream_ptr(stream)))
+
+
+def qgemv_attn_pages(cache: KvCacheDesc, pages: int, pages_stride: int, n_seqs: int, ctx_lens: int, q: int,
+                     q_token_stride: int, q_head_stride: int, q_heads: int, cu_q: int, n_q: int, masks: int | None,
+                     max_ctx: int, max_new: int, scale: float, out: int, out_token_stride: int, out_head_stride: int,
+                     lse: int | None, ws: int, ws_bytes: int, stream=None) -> int:
+    return _check(load().qgemv_attn_pages(ctypes.byref(cache), pages, pages_stride, n_seqs, ctx_lens, q, q_token_stride,
+                                          q_head_stride, q_heads, cu_q, n_q, masks, max_ctx, max_new, scale, out,
+                                          out_token_stride, out_head_stride, lse, ws, ws_bytes, _stream_ptr(stream)))
 
 
 # ----------------------------------------------------------- torch helper --
@@ -553,7 +666,7 @@ def _rows(name, t, heads: int, head_dim: int, dev: int | None = None):
     """(address, token stride, head stride) of a CUDA tensor [n, heads, head_dim], its values contiguous; on device `dev`
     where one is given."""
     shape, strides = t.shape, t.stride()
-    if (len(shape) != 3 or shape[1] != heads or shape[2] != head_dim or strides[2] != 1
+    if (len(shape) != 3 or shape[1] != heads or shape[2] != head_dim or (strides[2] != 1 and shape[0] > 0)
             or (not t.is_cuda if dev is None else t.get_device() != dev)):
         raise ValueError(f"{name} must be a CUDA tensor [n, {heads}, {head_dim}] with contiguous values"
                          f"{_where(dev)}, got {tuple(shape)} with strides {strides} on {t.device}")
@@ -604,6 +717,60 @@ class AttnWorkspace:
         return _call(self._dev, _lib.qgemv_attn_status, self.ptr)
 
 
+class Rotary:
+    """Rotary positions for heads of head_dim values, on the GPU.
+
+    ``Rotary(head_dim, sections, base=10000.0)``: sections[a] pairs of each
+    head belong to axis a of a position (one to four axes; ``[head_dim // 2]``
+    for plain text); with n pairs in all, pair j turns by
+    ``position[axis(j)] * base ** (-j / n)``, or by ``freqs[j]`` a position
+    where those are given.  pairs: "halves" (values j and j + n are a pair) or
+    "neighbours" (2j and 2j + 1).  Values behind the pairs stay.  ``rotate``
+    turns rows, ``KVCache.write_rotated`` turns q and k on their way into a
+    cache; negative positions turn back."""
+
+    def __init__(self, head_dim: int, sections, base: float = 10000.0, freqs=None, pairs: str = "halves", device="cuda"):
+        import torch
+        sections = [int(s) for s in sections]
+        n = sum(sections)
+        if head_dim not in (64, 128) or not 1 <= len(sections) <= 4 or min(sections) < 0 or not 1 <= n <= head_dim // 2:
+            raise QgemvError(QGEMV_ERR_ARG, f"invalid plan: sections {sections} of a head of {head_dim}")
+        if pairs not in ROPE_PAIRINGS:
+            raise QgemvError(QGEMV_ERR_ARG, f"unknown pairing {pairs!r}")
+        freqs = [float(base) ** (-j / n) for j in range(n)] if freqs is None else [float(f) for f in freqs]
+        if len(freqs) != n:
+            raise QgemvError(QGEMV_ERR_ARG, f"{len(freqs)} frequencies for {n} pairs")
+        f = np.array(freqs, dtype=np.float64)
+        a = np.repeat(np.arange(len(sections), dtype=np.int32), sections)
+        plan = np.zeros(qgemv_rope_plan_bytes(n) // 8, dtype=np.int64)
+        qgemv_rope_plan(f.ctypes.data, a.ctypes.data, n, plan.ctypes.data)
+        _gpu("a rotary plan", device)
+        self.head_dim, self.pairs, self.axes, self.pairing = head_dim, n, len(sections), ROPE_PAIRINGS[pairs]
+        self.plan = torch.from_numpy(plan).to(device)
+        self.ptr, self._dev = self.plan.data_ptr(), self.plan.get_device()
+        torch.cuda.current_stream(self._dev).synchronize()  # any stream may use it first
+
+    def rotate(self, x, positions, dtype=None, out=None, stream=None):
+        """The rows x [n, heads, head_dim] turned to the positions (int32 [n,
+        axes]), of x's type unless dtype is given; out may be x itself."""
+        n, heads, d = x.shape
+        dev = self._dev
+        rows = _rows("x", x, heads, self.head_dim, dev)
+        if out is None:
+            torch = _torch()
+            empty = torch.empty if stream is None else _empty_on(stream, dev)
+            out = empty((n, heads, d), dtype=x.dtype if dtype is None else dtype, device=x.device)
+            out_rows = out.data_ptr(), heads * d, d
+        elif out.shape != x.shape or dtype not in (None, out.dtype):
+            raise ValueError("out must be shaped like x, of the dtype given")
+        else:
+            out_rows = _rows("out", out, heads, d, dev)
+        _call(dev, _lib.qgemv_rope_rows, self.ptr, self.pairs, self.pairing, self.axes,
+              _index("positions", positions, _torch().int32, (n, self.axes), dev), _dtype_code(x.dtype), heads, d, *rows, n,
+              _dtype_code(out.dtype), *out_rows, _on(stream, dev))
+        return out
+
+
 class KVCache:
     """A paged key/value cache of one layer on the GPU.
 
@@ -639,6 +806,32 @@ class KVCache:
         _call(dev, _lib.qgemv_kv_write, self._ref, _dtype_code(k.dtype), *_rows("k", k, self.kv_heads, self.head_dim, dev),
               *_rows("v", v, self.kv_heads, self.head_dim, dev), s, n, _on(stream, dev))
 
+    def write_rotated(self, rotary, q, k, v, positions, slots, out=None, stream=None):
+        """``write`` of k rotated to the positions (int32 [n, axes]) and v as
+        it is, and q [n, q_heads, head_dim] rotated, in one launch; q, k and v
+        have one type.  Returns the rotated q: fp16, or of the type of ``out``."""
+        torch, dev = _torch(), self._dev
+        n, heads, d = q.shape
+        if not q.dtype == k.dtype == v.dtype or k.shape[0] != n or v.shape[0] != n:
+            raise ValueError("q, k and v must have the same type and number of tokens")
+        if rotary._dev != dev or rotary.head_dim != self.head_dim:
+            raise ValueError(f"the rotary plan is for heads of {rotary.head_dim} on cuda:{rotary._dev}, the cache has "
+                             f"heads of {self.head_dim} on cuda:{dev}")
+        if out is None:
+            empty = torch.empty if stream is None else _empty_on(stream, dev)
+            out = empty((n, heads, d), dtype=torch.float16, device=self.device)
+            out_rows = out.data_ptr(), heads * d, d
+        elif out.shape != q.shape:
+            raise ValueError("out must be shaped like q")
+        else:
+            out_rows = _rows("out", out, heads, d, dev)
+        _call(dev, _lib.qgemv_kv_write_rotated, self._ref, rotary.ptr, rotary.pairs, rotary.pairing, rotary.axes,
+              _index("positions", positions, torch.int32, (n, rotary.axes), dev), _dtype_code(q.dtype),
+              *_rows("q", q, heads, self.head_dim, dev), heads, *_rows("k", k, self.kv_heads, self.head_dim, dev),
+              *_rows("v", v, self.kv_heads, self.head_dim, dev), _index("slots", slots, torch.int64, (n,), dev), n,
+              _dtype_code(out.dtype), *out_rows, _on(stream, dev))
+        return out
+
     def read(self, table, starts, cu, n_tokens: int, dtype=None, out=None, stream=None):
         """The cached rows of positions starts[b] .. of each sequence, packed
         by cu (int32 [n_seqs + 1]): (k, v) [n_tokens, kv_heads, head_dim] of
@@ -663,6 +856,16 @@ class KVCache:
               _index("cu", cu, torch.int32, (n_seqs + 1,), dev), n_tokens, _dtype_code(dtype), *rows, _on(stream, dev))
         return out
 
+    def copy_pages(self, src, dst, tokens=None, stream=None):
+        """Copy page src[i] to page dst[i] (int32 [n]), whole or the first
+        tokens[i] tokens (int32 [n]); pairs with a number that is no page are
+        passed over.  No page may be the destination of two copies, or of one
+        and the source of another."""
+        dev, i32 = self._dev, _torch().int32
+        n, = src.shape
+        _call(dev, _lib.qgemv_kv_copy_pages, self._ref, _index("src", src, i32, (n,), dev), _index("dst", dst, i32, (n,), dev),
+              None if tokens is None else _index("tokens", tokens, i32, (n,), dev), n, _on(stream, dev))
+
     def attend(self, q, table, ctx_lens, cu_q, masks=None, *, max_ctx: int, max_new: int, workspace, scale=None,
                out=None, lse=None, stream=None):
         """Attention of the drafted tokens q [n, q_heads, head_dim] (fp16),
@@ -672,6 +875,51 @@ class KVCache:
         another.  Returns (out like q, lse fp32 [n, q_heads]).  scale is
         1 / sqrt(head_dim) unless given; max_ctx and max_new bound the
         lengths (they guide the split only)."""
+        n_seqs, stride = table.shape
+        return self._attend(_lib.qgemv_attn_tree, _index("table", table, _torch().int32, (n_seqs, stride), self._dev), n_seqs,
+                            stride, q, ctx_lens, cu_q, masks, max_ctx, max_new, workspace, scale, out, lse, stream)
+
+    def select(self, q, table, ctx_lens, cu_q, *, summary, n_select: int, out=None, stream=None):
+        """For each sequence and key/value head the n_select whole pages of
+        highest score (``KeySummary``) before ctx_lens[b], in order, and the
+        pages behind them: (pages int32 [n_seqs, kv_heads, width], lens int32
+        [n_seqs]), a page table of each head's own and the context's length
+        over it, for ``attend_pages``.  q, table, ctx_lens and cu_q as for
+        ``attend``."""
+        torch, dev = _torch(), self._dev
+        n, heads, d = q.shape
+        if q.dtype != torch.float16:
+            raise ValueError("q must be fp16")
+        if summary.cache is not self:
+            raise ValueError("the summary is another cache's")
+        n_seqs, stride = table.shape
+        width = _lib.qgemv_kv_select_width(self.page_tokens, n_select)
+        if width == 0:
+            raise QgemvError(QGEMV_ERR_ARG, f"n_select={n_select} is not in [0, 2^20]")
+        if out is None:
+            empty = torch.empty if stream is None else _empty_on(stream, dev)
+            out = (empty((n_seqs, self.kv_heads, width), dtype=torch.int32, device=self.device),
+                   empty((n_seqs,), dtype=torch.int32, device=self.device))
+            to = out[0].data_ptr(), out[1].data_ptr()
+        else:
+            to = (_index("pages", out[0], torch.int32, (n_seqs, self.kv_heads, width), dev),
+                  _index("lens", out[1], torch.int32, (n_seqs,), dev))
+        _call(dev, _lib.qgemv_kv_select, self._ref, summary.codes.data_ptr(), summary.scales.data_ptr(),
+              _index("table", table, torch.int32, (n_seqs, stride), dev), stride, n_seqs,
+              _index("ctx_lens", ctx_lens, torch.int32, (n_seqs,), dev), *_rows("q", q, heads, self.head_dim, dev), heads,
+              _index("cu_q", cu_q, torch.int32, (n_seqs + 1,), dev), n, n_select, *to, _on(stream, dev))
+        return out
+
+    def attend_pages(self, q, pages, lens, cu_q, masks=None, *, max_ctx: int, max_new: int, workspace, scale=None, out=None,
+                     lse=None, stream=None):
+        """``attend`` with a page table for each key/value head: pages int32
+        [n_seqs, kv_heads, width] and the contexts' lengths over it, as
+        ``select`` gives them."""
+        n_seqs, heads, stride = pages.shape
+        return self._attend(_lib.qgemv_attn_pages, _index("pages", pages, _torch().int32, (n_seqs, self.kv_heads, stride), self._dev),
+                            n_seqs, stride, q, lens, cu_q, masks, max_ctx, max_new, workspace, scale, out, lse, stream)
+
+    def _attend(self, fn, table, n_seqs, stride, q, ctx_lens, cu_q, masks, max_ctx, max_new, workspace, scale, out, lse, stream):
         torch, dev = _torch(), self._dev
         n, heads, d = q.shape
         if q.dtype != torch.float16:
@@ -692,13 +940,126 @@ class KVCache:
             _index("lse", lse, torch.float32, (n, heads), dev)
         if masks is not None:
             masks = _index("masks", masks, torch.uint64 if masks.dtype == torch.uint64 else torch.int64, (n,), dev)
-        n_seqs, stride = table.shape
-        _call(dev, _lib.qgemv_attn_tree, self._ref, _index("table", table, torch.int32, (n_seqs, stride), dev), stride,
-              n_seqs, _index("ctx_lens", ctx_lens, torch.int32, (n_seqs,), dev),
+        _call(dev, fn, self._ref, table, stride, n_seqs, _index("ctx_lens", ctx_lens, torch.int32, (n_seqs,), dev),
               *_rows("q", q, heads, self.head_dim, dev), heads, _index("cu_q", cu_q, torch.int32, (n_seqs + 1,), dev), n,
               masks, max_ctx, max_new, d ** -0.5 if scale is None else scale, *out_rows, lse.data_ptr(),
               workspace.ptr, workspace.nbytes, _on(stream, dev))
         return out, lse
+
+
+class KeySummary:
+    """Summaries of a cache's pages, by which ``KVCache.select`` scores them:
+    per page and key/value head the largest and smallest key values of each
+    channel, as INT8 ``codes`` [n_pages, kv_heads, 2, head_dim] with a scale
+    (``scales`` [n_pages, kv_heads]).  ``update`` takes those of pages that have
+    become full; it has to be called again for pages that are written anew or
+    copied to."""
+
+    def __init__(self, cache: KVCache):
+        import torch
+        self.cache = cache
+        shape = cache.n_pages, cache.kv_heads
+        self.codes = torch.zeros(*shape, 2, cache.head_dim, dtype=torch.int8, device=cache.device)
+        self.scales = torch.zeros(shape, dtype=torch.float32, device=cache.device)
+        torch.cuda.current_stream(cache._dev).synchronize()  # any stream may use it first
+
+    def update(self, pages, stream=None):
+        """Take the summaries of the pages (int32 [n]; numbers that are no page
+        of the cache are passed over)."""
+        c = self.cache
+        n, = pages.shape
+        _call(c._dev, _lib.qgemv_kv_summarize, c._ref, _index("pages", pages, _torch().int32, (n,), c._dev), n,
+              self.codes.data_ptr(), self.scales.data_ptr(), _on(stream, c._dev))
+
+
+class PagePool:
+    """The pages of one or more caches of n_pages pages (say a cache a layer,
+    with one page table): ``refs`` (int32 [n_pages]) counts the rows of page
+    tables that hold a page, 0 for a free one.  A row of n tokens holds the
+    pages of its first ceil(n / page_tokens) entries.  ``reserve`` gives pages
+    out, lowest first; ``fork`` makes the new rows of a step of beam search;
+    ``release`` takes pages back; ``compact`` packs the pages in use.  Tables
+    are int32 [rows, entries], lengths int32 [rows].  Calls return at once, and
+    run one at a time; ``status`` tells whether pages ran out."""
+
+    def __init__(self, n_pages: int, page_tokens: int, device="cuda"):
+        import torch
+        nbytes = qgemv_pool_ws_bytes(n_pages)
+        if nbytes == 0 or page_tokens not in (16, 32, 64, 128, 256):
+            raise QgemvError(QGEMV_ERR_ARG, f"invalid pool: {n_pages} pages of {page_tokens} tokens")
+        _gpu("a pool", device)
+        self.n_pages, self.page_tokens, self._nbytes = n_pages, page_tokens, nbytes
+        self.refs = torch.zeros(n_pages, dtype=torch.int32, device=device)
+        self._missing = torch.zeros(1, dtype=torch.int32, device=device)
+        self._ws = torch.empty(nbytes // 4, dtype=torch.int32, device=device)
+        self._dev = self.refs.get_device()
+        torch.cuda.current_stream(self._dev).synchronize()  # any stream may use it first
+
+    def _table(self, table):
+        rows, stride = table.shape
+        return _index("table", table, _torch().int32, (rows, stride), self._dev), stride, rows
+
+    def _ints(self, name, t, n):
+        return _index(name, t, _torch().int32, (n,), self._dev)
+
+    def reserve(self, table, have, need, stream=None):
+        """Give row b, which holds have[b] tokens, the pages for need[b]; the
+        table's entries are filled in place."""
+        ptr, stride, rows = self._table(table)
+        _call(self._dev, _lib.qgemv_pool_reserve, self.refs.data_ptr(), self.n_pages, self.page_tokens, ptr, stride, rows,
+              self._ints("have", have, rows), self._ints("need", need, rows), self._missing.data_ptr(), _on(stream, self._dev))
+
+    def fork(self, table, parents, lens, stream=None):
+        """Replace the rows of table (lens tokens each) by new ones, row r what
+        row parents[r] (int32 [n]) was: whole pages are shared, rows without
+        children return theirs.  Returns (new table, src, dst, tokens): the page
+        that a row has filled in part stays with its first child, the others
+        get one each, and ``copy_pages(src, dst, tokens)`` of every cache
+        copies its tokens."""
+        ptr, stride, rows = self._table(table)
+        torch, dev = _torch(), self._dev
+        n, = parents.shape
+        empty = torch.empty if stream is None else _empty_on(stream, dev)
+        new = empty((n, stride), dtype=torch.int32, device=table.device)
+        src, dst, tokens = (empty((n,), dtype=torch.int32, device=table.device) for _ in range(3))
+        _call(dev, _lib.qgemv_pool_fork, self.refs.data_ptr(), self.n_pages, self.page_tokens, ptr, stride, rows,
+              self._ints("parents", parents, n), n, self._ints("lens", lens, rows), new.data_ptr(), src.data_ptr(),
+              dst.data_ptr(), tokens.data_ptr(), self._missing.data_ptr(), _on(stream, dev))
+        return new, src, dst, tokens
+
+    def release(self, table, lens, keep=None, stream=None):
+        """Take back the pages of row b's tokens keep[b] .. lens[b] (all of
+        them unless keep is given) that no kept token is in; their entries
+        become -1."""
+        ptr, stride, rows = self._table(table)
+        _call(self._dev, _lib.qgemv_pool_release, self.refs.data_ptr(), self.n_pages, self.page_tokens, ptr, stride, rows,
+              self._ints("lens", lens, rows), None if keep is None else self._ints("keep", keep, rows), _on(stream, self._dev))
+
+    def compact(self, table, out=None, stream=None):
+        """Move the pages in use to the lowest numbers.  Returns (new table,
+        src, dst): the moves, for ``copy_pages`` of every cache, end with -1.
+        The table holds every row that is in use; out may be table itself."""
+        ptr, stride, rows = self._table(table)
+        torch, dev = _torch(), self._dev
+        empty = torch.empty if stream is None else _empty_on(stream, dev)
+        n = self.n_pages // 2
+        if out is None:
+            out = empty((rows, stride), dtype=torch.int32, device=table.device)
+        src, dst = (empty((n,), dtype=torch.int32, device=table.device) for _ in range(2))
+        _call(dev, _lib.qgemv_pool_compact, self.refs.data_ptr(), self.n_pages, ptr, stride, rows,
+              _index("out", out, torch.int32, (rows, stride), dev), src.data_ptr(), dst.data_ptr(), n, self._ws.data_ptr(),
+              self._nbytes, _on(stream, dev))
+        return out, src, dst
+
+    def status(self):
+        """Synchronise; raises if pages ran out since the last call."""
+        torch = _torch()
+        torch.cuda.synchronize(self._dev)
+        n = int(self._missing.item())
+        if n:
+            self._missing.zero_()
+            torch.cuda.synchronize(self._dev)
+            raise QgemvError(QGEMV_ERR_NOMEM, f"{n} pages were not there to give")
 
 
 def attn_prompt(q, k, v, cu_q, cu_k, *, max_q: int, workspace, scale=None, out=None, lse=None, stream=None):
@@ -734,3 +1095,47 @@ def attn_prompt(q, k, v, cu_q, cu_k, *, max_q: int, workspace, scale=None, out=N
           k.shape[0], max_q or 1, d ** -0.5 if scale is None else scale, *out_rows, lse.data_ptr(), workspace.ptr,
           workspace.nbytes, _on(stream, dev))
     return out, lse
+
+
+class BeamWorkspace:
+    """Workspace of ``beam_select`` for up to n_seqs sequences of these sizes,
+    reused by any number of calls, one at a time."""
+
+    def __init__(self, n_seqs: int, beams: int, vocab: int, width: int, device="cuda"):
+        import torch
+        self.nbytes = qgemv_beam_ws_bytes(n_seqs, beams, vocab, width)
+        if self.nbytes == 0:
+            raise QgemvError(QGEMV_ERR_ARG, f"no workspace for {n_seqs} sequences of {beams} beams, {vocab} tokens, {width} kept")
+        _gpu("a workspace", device)
+        self.buffer = torch.empty(self.nbytes, dtype=torch.uint8, device=device)
+        self.ptr, self._dev = self.buffer.data_ptr(), self.buffer.get_device()
+
+
+def beam_select(logits, scores, width: int, *, workspace, out=None, stream=None):
+    """Beam search's choice: of each sequence's candidates (beam, token) the
+    width with the largest scores[s, b] + log_softmax(logits)[token], in
+    descending order, ties to the lower beam and token.  logits [n_seqs *
+    beams, vocab] (fp32, fp16 or bf16, any row stride), scores fp32 [n_seqs,
+    beams].  Returns (scores fp32, beams int32, tokens int32), each [n_seqs,
+    width]; (-inf, -1, -1) where there is no candidate.  All tensors and the
+    workspace are on the logits' device."""
+    torch, dev = _torch(), logits.get_device()
+    n_seqs, beams = scores.shape
+    shape, strides = logits.shape, logits.stride()
+    if len(shape) != 2 or shape[0] != n_seqs * beams or (strides[1] != 1 and shape[1] > 1) or not logits.is_cuda:
+        raise ValueError(f"logits must be a CUDA tensor [{n_seqs * beams}, vocab] with contiguous rows, got {tuple(shape)} with "
+                         f"strides {strides} on {logits.device}")
+    if workspace._dev != dev:
+        _elsewhere(workspace, dev)
+    got = n_seqs, width
+    if out is None:
+        empty = torch.empty if stream is None else _empty_on(stream, dev)
+        out = (empty(got, dtype=torch.float32, device=logits.device), empty(got, dtype=torch.int32, device=logits.device),
+               empty(got, dtype=torch.int32, device=logits.device))
+        to = out[0].data_ptr(), out[1].data_ptr(), out[2].data_ptr()
+    else:
+        to = tuple(_index(f"out[{i}]", t, kind, got, dev) for i, (t, kind) in enumerate(zip(out, (torch.float32, torch.int32, torch.int32))))
+    _call(dev, _lib.qgemv_beam_select, _dtype_code(logits.dtype), logits.data_ptr(), strides[0] if shape[0] > 1 else shape[1],
+          shape[1], _index("scores", scores, torch.float32, (n_seqs, beams), dev), n_seqs, beams, width, *to, workspace.ptr,
+          workspace.nbytes, _on(stream, dev))
+    return out

@@ -496,6 +496,187 @@ int qgemv_attn_prompt(int dtype, int head_dim, int q_heads, int kv_heads, const 
                       float scale, void* out, int64_t out_token_stride, int64_t out_head_stride, float* lse,
                       void* ws, int64_t ws_bytes, void* stream);
 
+/* ------------------------------------------------------ rotary positions ----
+ *
+ * Pair j of a head vector, (a, b), becomes (a cos - b sin, a sin + b cos) of
+ * the angle position[axes[j]] * freqs[j]: up to four axes, as for images and
+ * video (time, height, width).  Values behind the pairs stay as they are.
+ * The angle is taken in 64-bit fixed point, so that far positions lose
+ * nothing (it is off by at most |position| 2^-65 turns and then rounded once to
+ * fp32); the products are fp32, the results rounded once.  Negative positions
+ * turn backwards: rotating by -position undoes a rotation (and is its
+ * gradient), rotating kept keys by a difference moves them.                  */
+typedef enum {
+  QGEMV_ROPE_HALVES = 0,    /* pair j: values j and j + pairs */
+  QGEMV_ROPE_NEIGHBOURS = 1 /* pair j: values 2j and 2j + 1 */
+} qgemv_rope_pairing;
+
+/* A plan of `pairs` pairs (1 .. 64): 16 bytes each; 0 for invalid numbers.
+ * qgemv_rope_plan fills host memory, which the caller copies to the device
+ * (16-byte aligned there); freqs in radians a position, within [-1024, 1024],
+ * axes 0 .. 3.                                                               */
+int64_t qgemv_rope_plan_bytes(int pairs);
+int qgemv_rope_plan(const double* freqs, const int32_t* axes, int pairs, void* plan);
+
+/* Rotate the rows x [n_tokens][heads][head_dim] of dtype into out (of
+ * out_dtype; x itself, where pointer, strides and types are the same, but no
+ * other rows that overlap x).  positions: device int32 [n_tokens][n_axes];
+ * a pair of an axis past n_axes is not turned.  head_dim 64 or 128, at most
+ * head_dim / 2 pairs.  Asynchronous on `stream`.                             */
+int qgemv_rope_rows(const void* plan, int pairs, int pairing, int n_axes, const int32_t* positions, int dtype, int heads,
+                    int head_dim, const void* x, int64_t x_token_stride, int64_t x_head_stride, int64_t n_tokens,
+                    int out_dtype, void* out, int64_t out_token_stride, int64_t out_head_stride, void* stream);
+
+/* qgemv_kv_write of rotated keys, and the rotated queries beside it, in one
+ * launch: q [n_tokens][q_heads][head_dim] goes rotated to q_out (of
+ * out_dtype), k rotated and v as it is are quantised into the slots.  Rows
+ * and slots as for qgemv_kv_write (the keys' codes are of their rotated fp32
+ * values); a token whose slot is skipped still gets its q.                  */
+int qgemv_kv_write_rotated(const qgemv_kv_cache* cache, const void* plan, int pairs, int pairing, int n_axes,
+                           const int32_t* positions, int dtype, const void* q, int64_t q_token_stride,
+                           int64_t q_head_stride, int q_heads, const void* k, int64_t k_token_stride,
+                           int64_t k_head_stride, const void* v, int64_t v_token_stride, int64_t v_head_stride,
+                           const int64_t* slots, int64_t n_tokens, int out_dtype, void* q_out,
+                           int64_t out_token_stride, int64_t out_head_stride, void* stream);
+
+/* --------------------------------------------------- beam search's choice ----
+ *
+ * Of each sequence's candidates (beam b, token t) the `width` of largest
+ *
+ *   scores[b] + x[b][t] - log sum_u exp x[b][u],
+ *
+ * in descending order; ties go to the lower beam, then to the lower token.
+ *   logits: device rows of dtype (any qgemv_dtype), one for each beam of each
+ *     sequence ([n_seqs * beams], row_stride elements apart; any alignment of
+ *     elements), of vocab tokens: an LM head's output.
+ *   scores: device fp32 [n_seqs][beams], the beams' sums of log
+ *     probabilities so far.
+ *   out_scores, out_beams, out_tokens: device [n_seqs][width].
+ * A beam whose score is not finite (-infinity: not in use), or whose log sum
+ * is not (a NaN or +infinity among its logits, or nothing but -infinity), has
+ * no candidates, nor have tokens of -infinity; places for which there is no
+ * candidate hold (-infinity, -1, -1).  The sums of exponentials are fp32, log sums and scores
+ * are compared in 64 bits and rounded once.  beams and width are at most 64.
+ * ws: qgemv_beam_ws_bytes bytes, 16-byte aligned, no setting up; calls that
+ * overlap on the GPU need one each.  Asynchronous on `stream`, no allocation,
+ * can be captured in a CUDA graph; bitwise reproducible.                     */
+int64_t qgemv_beam_ws_bytes(int64_t n_seqs, int beams, int64_t vocab, int width);
+int qgemv_beam_select(int dtype, const void* logits, int64_t row_stride, int64_t vocab, const float* scores, int64_t n_seqs,
+                      int beams, int width, float* out_scores, int32_t* out_beams, int32_t* out_tokens, void* ws,
+                      int64_t ws_bytes, void* stream);
+
+/* --------------------------------------------------------- pages of a cache ----
+ *
+ * A pool's bookkeeping of pages, for any number of caches with the same
+ * numbers of pages and tokens (a cache a layer, one page table): refs, device int32
+ * [n_pages], counts the rows of page tables that hold a page; pages of count
+ * 0 (or less) are free.  The caller zeroes it once.  Tables are device int32
+ * [rows][table_stride], lengths device int32 in tokens; a row of length n
+ * holds the pages of its first ceil(n / page_tokens) entries.  Entries that
+ * are no page's number are passed over.  Free pages are given out lowest
+ * first, in the order of the rows, so results depend on the inputs alone.
+ * Where there are none left, the entry becomes -1 and *missing (device int32)
+ * counts it.  At most 8192 rows of 2^20 entries a call; calls of one pool
+ * one at a time.  All are asynchronous on `stream`, allocate nothing, can be
+ * captured in a CUDA graph, and leave refs the only state.
+ *
+ * reserve: row b, which holds have[b] tokens, gets the pages that need[b]
+ * tokens take beyond them.                                                   */
+int qgemv_pool_reserve(int32_t* refs, int64_t n_pages, int page_tokens, int32_t* table, int64_t table_stride, int64_t n_seqs,
+                       const int32_t* have, const int32_t* need, int32_t* missing, void* stream);
+
+/* fork (a step of beam search): the rows are replaced by n_new new ones, row
+ * r of new_table (same table_stride; no overlap with table) what row
+ * parents[r] was; lens has the old rows' lengths.  A parent outside the rows
+ * gives an empty row.  Whole pages are shared: their counts change by the
+ * children of each row that held them, less one, so that rows without
+ * children return theirs.  The page that a row has filled in part must be
+ * that row's alone; it stays with the row's first child, and each further
+ * child r gets a free page instead, to which tokens[r] tokens have to be
+ * copied: src[r] to dst[r], by qgemv_kv_copy_pages for each cache; -1 for rows
+ * without a copy (device int32 [n_new] each).  Entries behind a row's
+ * length become -1 and are not counted.                                      */
+int qgemv_pool_fork(int32_t* refs, int64_t n_pages, int page_tokens, const int32_t* table, int64_t table_stride, int64_t n_rows,
+                    const int32_t* parents, int64_t n_new, const int32_t* lens, int32_t* new_table, int32_t* src, int32_t* dst,
+                    int32_t* tokens, int32_t* missing, void* stream);
+
+/* release: row b, of lens[b] tokens, keeps the pages of its first keep[b]
+ * tokens (none where keep is NULL); the others' counts go down by one and
+ * their entries become -1.                                                   */
+int qgemv_pool_release(int32_t* refs, int64_t n_pages, int page_tokens, int32_t* table, int64_t table_stride, int64_t n_seqs,
+                       const int32_t* lens, const int32_t* keep, void* stream);
+
+/* compact: with U pages in use, those numbered U and more move, in order, to
+ * the free ones below U.  src and dst (device int32 [n_moves], n_moves at
+ * least n_pages / 2) are the moves for qgemv_kv_copy_pages, followed by -1;
+ * refs follows, and new_table is table with the new numbers (or table
+ * itself; every entry that is a page in use is renumbered).  ws:
+ * qgemv_pool_ws_bytes bytes, no setting up.                                  */
+int64_t qgemv_pool_ws_bytes(int64_t n_pages);
+int qgemv_pool_compact(int32_t* refs, int64_t n_pages, const int32_t* table, int64_t table_stride, int64_t n_seqs,
+                       int32_t* new_table, int32_t* src, int32_t* dst, int64_t n_moves, void* ws, int64_t ws_bytes, void* stream);
+
+/* Copy page src[i] of a cache to page dst[i] (device int32 [n]), whole, or the
+ * first tokens[i] tokens of every head, up to a multiple of 16.  Pairs with a
+ * number that is no page are passed over.  No page may be the destination of
+ * two copies, or of one and the source of another.  A page is kv_heads runs
+ * of page_tokens / 16 blocks of 16 tokens, all of the same size.
+ * Asynchronous on `stream`.                                                  */
+int qgemv_kv_copy_pages(const qgemv_kv_cache* cache, const int32_t* src, const int32_t* dst, const int32_t* tokens, int64_t n,
+                        void* stream);
+
+/* ------------------------------------------- attention over selected pages ----
+ *
+ * Long contexts without reading all of them: of a sequence's whole pages
+ * (those that end at or before ctx_lens[b]) each key/value head attends the
+ * n_select with the highest score, and all positions behind the last whole
+ * page.  Scores come from summaries of the pages' keys, which qgemv_kv_summarize
+ * takes once a page is full (and again when it was written anew):
+ *
+ *   hi_d, lo_d = the largest and smallest of the page's key values, as the
+ *   cache stands for them, of channel d; a = fl32(max_d max(|hi_d|, |lo_d|) /
+ *   127), codes clamp(rint(fl32(x / a)), -127, 127), 0 if a = 0;
+ *   up_d, down_d = sum of max(q_d, 0), min(q_d, 0) over the sequence's queries
+ *   (all drafted tokens, all heads of the group), exact, rounded once to
+ *   fp32; codes the same way, with the largest of both;
+ *   score = fl32(sum_d (up_d hi_d + down_d lo_d, of the codes) * a).
+ *
+ * Without the roundings to codes no key of a page has a product with the
+ * queries above its score.  Ties go to the earlier page.  A page whose keys
+ * hold an infinity or NaN (scale NaN) comes before all others; queries that
+ * do give codes of 0.  Pages whose entry in the table is missing are no
+ * candidates.
+ *
+ * codes: device int8 [n_pages][kv_heads][2][head_dim] (hi, lo), 16-byte
+ * aligned; scales: device fp32 [n_pages][kv_heads].  Both are the caller's.
+ * summarize: of the pages pages[i] (device int32 [n]; numbers that are no
+ * page's are passed over), all page_tokens tokens of each.                   */
+int qgemv_kv_summarize(const qgemv_kv_cache* cache, const int32_t* pages, int64_t n, int8_t* codes, float* scales, void* stream);
+
+/* Choose: pages (device int32 [n_seqs][kv_heads][width], width =
+ * qgemv_kv_select_width, n_select and the pages that a context's end and 64
+ * drafted tokens take; 0 for invalid sizes) gets, for each head, the chosen pages in
+ * the context's order, then the table's entries from the last whole page on,
+ * then -1; lens (device int32 [n_seqs]) the context's length over them: a page
+ * table for qgemv_attn_pages.  Sequences, q, cu_q and the table as for
+ * qgemv_attn_tree; cache's pages are not read; table_stride is at most
+ * 393216.  Asynchronous on `stream`, no allocation, can be captured in a CUDA
+ * graph; the same inputs give the same choice.                               */
+int64_t qgemv_kv_select_width(int page_tokens, int64_t n_select);
+int qgemv_kv_select(const qgemv_kv_cache* cache, const int8_t* codes, const float* scales, const int32_t* table,
+                    int64_t table_stride, int64_t n_seqs, const int32_t* ctx_lens, const void* q, int64_t q_token_stride,
+                    int64_t q_head_stride, int q_heads, const int32_t* cu_q, int64_t n_q, int64_t n_select, int32_t* pages,
+                    int32_t* lens, void* stream);
+
+/* qgemv_attn_tree with a page table for each key/value head: pages is device
+ * int32 [n_seqs][kv_heads][pages_stride], and ctx_lens are lengths over it (as
+ * qgemv_kv_select gives both).                                               */
+int qgemv_attn_pages(const qgemv_kv_cache* cache, const int32_t* pages, int64_t pages_stride, int64_t n_seqs,
+                     const int32_t* ctx_lens, const void* q, int64_t q_token_stride, int64_t q_head_stride,
+                     int q_heads, const int32_t* cu_q, int64_t n_q, const uint64_t* masks, int64_t max_ctx,
+                     int64_t max_new, float scale, void* out, int64_t out_token_stride, int64_t out_head_stride,
+                     float* lse, void* ws, int64_t ws_bytes, void* stream);
+
 /* Message and code of the last error on the calling thread ("" / 0 if none). */
 const char* qgemv_last_error(void);
 int qgemv_last_error_code(void);
