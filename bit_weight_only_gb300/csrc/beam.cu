@@ -12,12 +12,11 @@
 // largest of the threads' maxima when a tile would overflow the list (that
 // many keys at least reach it, and at most `width` threads' values do) and the
 // list's own `width`-th key once it was cut; after the first tile few values
-// pass.  A second kernel, a block a sequence and a warp a beam, merges the
-// parts' sorted lists, and then the beams by their scores in 64 bits: fp32
-// would make ties of scores that differ.
+// pass.  A second kernel, a block a sequence, merges the parts' sorted lists
+// with the beams' scores in 64 bits: fp32 would make ties of scores that differ.
 //
-// Sums are fp32, of at most 2^12 values times the tiles of a thread; the log
-// sum and the scores are 64-bit.
+// Sums of exponentials are fp32, 17 additions a tile in a thread; the log sum,
+// whose whole powers of two are taken apart, and the scores are 64-bit.
 #include <type_traits>
 
 #include <cuda_bf16.h>
@@ -62,26 +61,36 @@ struct RowUnits {
     base = row - lead;
     end = lead + n;
   }
-  // values of unit u; what is outside the row is -infinity
-  __device__ void load(int64_t u, float* x) const {
+  // unit u as it lies in memory; what is outside the row is -infinity
+  __device__ uint4 load(int64_t u) const {
     const int64_t i0 = u * kVec;
-    if (i0 >= lead && i0 + kVec <= end) {
-      const uint4 w = __ldg(reinterpret_cast<const uint4*>(base) + u);
+    if (i0 >= lead && i0 + kVec <= end) return __ldg(reinterpret_cast<const uint4*>(base) + u);
+    uint32_t w[4] = {0, 0, 0, 0};
+    constexpr uint32_t kNone = sizeof(T) == 4 ? 0xff800000u : std::is_same<T, __half>::value ? 0xfc00u : 0xff80u;
 #pragma unroll
-      for (int i = 0; i < kVec; ++i) {
-        if constexpr (std::is_same<T, float>::value) {
-          x[i] = __uint_as_float((&w.x)[i]);
-        } else {
-          const uint32_t h = (&w.x)[i >> 1];
-          if constexpr (std::is_same<T, __half>::value)
-            x[i] = __half2float(__ushort_as_half(static_cast<unsigned short>(i & 1 ? h >> 16 : h & 0xffffu)));
-          else
-            x[i] = __uint_as_float(i & 1 ? h & 0xffff0000u : h << 16);
-        }
+    for (int i = 0; i < kVec; ++i) {
+      uint32_t v = kNone;
+      if (i0 + i >= lead && i0 + i < end) {
+        if constexpr (sizeof(T) == 4) v = reinterpret_cast<const uint32_t*>(base)[i0 + i];
+        else v = reinterpret_cast<const unsigned short*>(base)[i0 + i];
       }
-    } else {
+      if constexpr (sizeof(T) == 4) w[i] = v;
+      else w[i >> 1] |= v << (16 * (i & 1));
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+  }
+  __device__ static void values(const uint4& w, float* x) {
 #pragma unroll
-      for (int i = 0; i < kVec; ++i) x[i] = i0 + i >= lead && i0 + i < end ? static_cast<float>(base[i0 + i]) : -INFINITY;
+    for (int i = 0; i < kVec; ++i) {
+      if constexpr (std::is_same<T, float>::value) {
+        x[i] = __uint_as_float((&w.x)[i]);
+      } else {
+        const uint32_t h = (&w.x)[i >> 1];
+        if constexpr (std::is_same<T, __half>::value)
+          x[i] = __half2float(__ushort_as_half(static_cast<unsigned short>(i & 1 ? h >> 16 : h & 0xffffu)));
+        else
+          x[i] = __uint_as_float(i & 1 ? h & 0xffff0000u : h << 16);
+      }
     }
   }
 };
@@ -194,10 +203,17 @@ __global__ void __launch_bounds__(kThreads) beam_row_kernel(const BeamParams p) 
 
   float m = -INFINITY, l = 0.f;
   uint64_t threshold = 0;  // keys above it are candidates (and equal to it: it is in the list)
+  uint4 ahead[kUnits];
+  auto fetch = [&](int64_t at) {
+#pragma unroll
+    for (int i = 0; i < kUnits; ++i) ahead[i] = units.load(at / kVec + i * kThreads + threadIdx.x);
+  };
+  if (first < last) fetch(first);
   for (int64_t at = first; at < last; at += kTile) {
     float x[kPer];
 #pragma unroll
-    for (int i = 0; i < kUnits; ++i) units.load(at / kVec + i * kThreads + threadIdx.x, x + i * kVec);
+    for (int i = 0; i < kUnits; ++i) Units::values(ahead[i], x + i * kVec);
+    if (at + kTile < last) fetch(at + kTile);
     auto token = [&](int i) {
       return static_cast<uint32_t>(at + (static_cast<int64_t>(i / kVec) * kThreads + threadIdx.x) * kVec + i % kVec - units.lead);
     };
@@ -267,12 +283,6 @@ __global__ void __launch_bounds__(kThreads) beam_row_kernel(const BeamParams p) 
   }
 }
 
-// The largest key of the warp's lanes, and the lane that has it.
-__device__ __forceinline__ uint64_t warp_max(uint64_t key) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) key = max(key, __shfl_xor_sync(0xffffffffu, key, o));
-  return key;
-}
 __device__ __forceinline__ uint64_t ordered64(double x) {
   const uint64_t b = static_cast<uint64_t>(__double_as_longlong(x + 0.0));
   return b >> 63 ? ~b : b | 1ull << 63;
@@ -281,64 +291,93 @@ __device__ __forceinline__ double from_ordered64(uint64_t o) {
   return __longlong_as_double(static_cast<long long>(o >> 63 ? o & ~(1ull << 63) : ~o));
 }
 
-__global__ void __launch_bounds__(1024) beam_merge_kernel(const BeamParams p) {
-  __shared__ uint64_t s_keys[kMaxBeams][kMaxWidth];  // scores of a beam's candidates, descending (0: none)
-  __shared__ uint32_t s_tokens[kMaxBeams][kMaxWidth];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+constexpr int kMergeThreads = 256;
+constexpr int kMergeKeys = 2048;                     // scores kept in shared memory
+constexpr int kMaxLists = kMaxBeams * kMaxParts;
+
+// A list is a part of a beam's row: list i is part i % parts of beam i / parts,
+// so that of equal scores the one from the lower list goes first.
+__global__ void __launch_bounds__(kMergeThreads) beam_merge_kernel(const BeamParams p) {
+  __shared__ double s_base[kMaxBeams];  // what a beam's candidates start from
+  __shared__ uint64_t s_score[kMergeKeys];
+  __shared__ uint32_t s_token[kMergeKeys];
+  __shared__ unsigned char s_at[kMaxLists];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const unsigned full = 0xffffffffu;
   const int64_t seq = blockIdx.x;
+  const int lists = p.beams * p.parts, first = min(p.width, kMergeKeys / lists);  // scores of a list that are kept
+  const uint64_t* keys = p.keys + seq * lists * p.width;
+  for (int i = tid; i < lists; i += kMergeThreads) s_at[i] = 0;
   wait_for_last_kernel();
-  for (int b = warp; b < p.beams; b += warps) {
+  for (int b = warp; b < p.beams; b += kMergeThreads / 32) {
     const int64_t row = seq * p.beams + b;
-    // the log sum, and what the beam's candidates start from
-    float2 ml = make_float2(-INFINITY, 0.f);
-    const uint64_t* keys = p.keys + (row * p.parts + lane) * p.width;
-    uint64_t head = 0;
-    if (lane < p.parts) ml = p.sums[row * p.parts + lane], head = keys[0];
+    const float2 ml = lane < p.parts ? p.sums[row * p.parts + lane] : make_float2(-INFINITY, 0.f);
+    const float score = __ldg(p.scores + row);
     float top = ml.x;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(full, top, o));
-    double l = ml.x == -INFINITY && ml.y == 0.f ? 0.0 : static_cast<double>(ml.y) * exp(static_cast<double>(ml.x) - static_cast<double>(top));
+    float l = ml.x == -INFINITY && ml.y == 0.f ? 0.f : ml.y * ex2((ml.x - top) * kLog2e);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(full, l, o);
-    const double base = static_cast<double>(p.scores[row]) - (static_cast<double>(top) + log(l));
-    const bool fine = isfinite(base);
-    // the parts' lists, merged
-    int at = 0;
-    for (int i = 0; i < p.width; ++i) {
-      const uint64_t best = fine ? warp_max(head) : 0;
-      if (best && best == head) head = ++at < p.width ? keys[at] : 0;  // one lane: keys differ
-      if (lane == 0) {
-        s_keys[b][i] = best ? ordered64(base + static_cast<double>(from_ordered(static_cast<uint32_t>(best >> 32)))) : 0;
-        s_tokens[b][i] = 0xffffffffu - static_cast<uint32_t>(best);
-      }
-    }
+    // log l = e log 2 + log m, 1 <= m < 2: the fp32 logarithm is small
+    const bool fine = l >= 0.5f && l < INFINITY && fabsf(top) < INFINITY && fabsf(score) < INFINITY;
+    const int e = static_cast<int>(__float_as_uint(l) >> 23) - 127;
+    const float m = __uint_as_float((__float_as_uint(l) & 0x007fffffu) | 0x3f800000u);
+    if (lane == 0)
+      s_base[b] = fine ? static_cast<double>(score) - static_cast<double>(top) - e * 0.69314718055994530942 - static_cast<double>(logf(m))
+                       : -INFINITY;
+  }
+  __syncthreads();
+  auto score_of = [&](int list, uint64_t key) -> uint64_t {
+    const double base = s_base[list / p.parts];
+    return key && base > -INFINITY ? ordered64(base + static_cast<double>(from_ordered(static_cast<uint32_t>(key >> 32)))) : 0;
+  };
+  for (int i = tid; i < lists * first; i += kMergeThreads) {
+    const int list = i / first;
+    const uint64_t key = keys[static_cast<int64_t>(list) * p.width + i - list * first];
+    s_score[i] = score_of(list, key);
+    s_token[i] = 0xffffffffu - static_cast<uint32_t>(key);
   }
   __syncthreads();
   if (warp != 0) return;
-  // the beams' lists, merged: ties go to the lower beam, whose token is lower
-  int at[2] = {0, 0};
-  uint64_t head[2];
-#pragma unroll
-  for (int j = 0; j < 2; ++j) head[j] = lane + 32 * j < p.beams ? s_keys[lane + 32 * j][0] : 0;
-  for (int i = 0; i < p.width; ++i) {
-    const uint64_t best = warp_max(max(head[0], head[1]));
-    const unsigned lo = __ballot_sync(full, best && head[0] == best), hi = __ballot_sync(full, best && head[1] == best);
-    const int b = lo ? __ffs(lo) - 1 : hi ? 31 + __ffs(hi) : -1;
-    const int64_t to = seq * p.width + i;
-    if (b < 0) {
-      if (lane == 0) p.out_scores[to] = -INFINITY, p.out_beams[to] = -1, p.out_tokens[to] = -1;
-      continue;
-    }
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      if (b == lane + 32 * j) {
-        p.out_scores[to] = static_cast<float>(from_ordered64(best));
-        p.out_beams[to] = b;
-        p.out_tokens[to] = static_cast<int32_t>(s_tokens[b][at[j]]);
-        head[j] = ++at[j] < p.width ? s_keys[b][at[j]] : 0;
+  // rounds: each lane has the best of its lists (score, list, token)
+  uint64_t best = 0;
+  uint32_t token = 0;
+  int mine = 0;
+  auto look = [&] {
+    best = 0;
+    mine = 0x7fffffff;
+    for (int i = lane; i < lists; i += 32) {
+      const int at = s_at[i];
+      if (at >= p.width) continue;
+      uint64_t sc;
+      uint32_t tk;
+      if (at < first) {
+        sc = s_score[i * first + at], tk = s_token[i * first + at];
+      } else {
+        const uint64_t key = keys[static_cast<int64_t>(i) * p.width + at];
+        sc = score_of(i, key), tk = 0xffffffffu - static_cast<uint32_t>(key);
       }
+      if (sc > best) best = sc, mine = i, token = tk;
     }
+  };
+  look();
+  for (int i = 0; i < p.width; ++i) {
+    const uint32_t hi = static_cast<uint32_t>(best >> 32), top = __reduce_max_sync(full, hi);
+    const uint32_t lo = hi == top ? static_cast<uint32_t>(best) : 0, low = __reduce_max_sync(full, lo);
+    const bool have = hi == top && static_cast<uint32_t>(best) == low;
+    const int list = __reduce_min_sync(full, have ? mine : 0x7fffffff);
+    const int64_t to = seq * p.width + i;
+    if (top == 0) {  // (a score's pattern has high bits) no candidate is left
+      if (lane == 0) p.out_scores[to] = -INFINITY, p.out_beams[to] = -1, p.out_tokens[to] = -1;
+    } else if (have && mine == list) {
+      p.out_scores[to] = static_cast<float>(from_ordered64(best));
+      p.out_beams[to] = list / p.parts;
+      p.out_tokens[to] = static_cast<int32_t>(token);
+      ++s_at[list];
+      look();
+    }
+    __syncwarp();
   }
 }
 
@@ -372,8 +411,7 @@ cudaError_t launch_beam(const BeamParams& given, int dtype, cudaStream_t s) {
   const cudaError_t e = dtype == QGEMV_DT_F32 ? go(beam_row_kernel<float>)
                         : dtype == QGEMV_DT_F16 ? go(beam_row_kernel<__half>) : go(beam_row_kernel<__nv_bfloat16>);
   if (e != cudaSuccess) return e;
-  const int warps = p.beams < 32 ? p.beams : 32;
-  return launch_after(beam_merge_kernel, static_cast<unsigned>(p.n_seqs), p, s, 32 * warps);
+  return launch_after(beam_merge_kernel, static_cast<unsigned>(p.n_seqs), p, s, kMergeThreads);
 }
 
 }  // namespace qgemv

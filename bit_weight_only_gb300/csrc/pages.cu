@@ -51,28 +51,37 @@ __device__ int block_sum(int x, int* s_warp, int& total) {
   return before + x;
 }
 
+// kPer neighbouring counts from refs[at]; past the end 1 (in use).
+template <int kPer>
+struct Counts {
+  int v[kPer];
+  __device__ void load(const int32_t* refs, int64_t n_pages, int64_t at) {
+    if (at + kPer <= n_pages && (reinterpret_cast<uintptr_t>(refs) & 15) == 0) {
+#pragma unroll
+      for (int i = 0; i < kPer; i += 4) *reinterpret_cast<int4*>(v + i) = *reinterpret_cast<const int4*>(refs + at + i);
+    } else {
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) v[i] = at + i < n_pages ? refs[at + i] : 1;
+    }
+  }
+};
+
 // The lowest free pages, `want` of them where there are as many: give(rank,
-// page), each by some thread of the block.  Returns how many there were.
+// page), each by some thread of the block; `c` has the first step's counts.
+// Returns how many there were.
 template <typename F>
-__device__ int free_pages(const int32_t* refs, int64_t n_pages, int want, int* s_warp, F give) {
+__device__ int free_pages(const int32_t* refs, int64_t n_pages, int want, Counts<kGivePer>& c, int* s_warp, F give) {
   int got = 0;
   for (int64_t p0 = 0; p0 < n_pages && got < want; p0 += kGive * kGivePer) {
     const int64_t mine = p0 + static_cast<int64_t>(threadIdx.x) * kGivePer;
-    int v[kGivePer];
-    if (mine + kGivePer <= n_pages && (reinterpret_cast<uintptr_t>(refs) & 15) == 0) {
-#pragma unroll
-      for (int i = 0; i < kGivePer; i += 4) *reinterpret_cast<int4*>(v + i) = *reinterpret_cast<const int4*>(refs + mine + i);
-    } else {
-#pragma unroll
-      for (int i = 0; i < kGivePer; ++i) v[i] = mine + i < n_pages ? refs[mine + i] : 1;
-    }
+    if (p0 > 0) c.load(refs, n_pages, mine);
     int n = 0, total;
 #pragma unroll
-    for (int i = 0; i < kGivePer; ++i) n += v[i] <= 0;
+    for (int i = 0; i < kGivePer; ++i) n += c.v[i] <= 0;
     int rank = got + block_sum<kGive>(n, s_warp, total) - n;
 #pragma unroll
     for (int i = 0; i < kGivePer; ++i) {
-      if (v[i] <= 0) {
+      if (c.v[i] <= 0) {
         if (rank < want) give(rank, static_cast<int32_t>(mine + i));
         ++rank;
       }
@@ -89,6 +98,8 @@ __global__ void __launch_bounds__(kGive) reserve_kernel(const PoolParams p) {
   __shared__ int s_warp[32];
   extern __shared__ int s_upto[];  // pages that the sequences up to and with this one need
   const int n = static_cast<int>(p.n_seqs);
+  Counts<kGivePer> counts;
+  counts.load(p.refs, p.n_pages, static_cast<int64_t>(threadIdx.x) * kGivePer);
   auto range = [&](int b, int64_t& e0, int64_t& e1) {
     e0 = pages_for(p.from[b], p.page_tokens);
     e1 = min(pages_for(p.to[b], p.page_tokens), p.table_stride);
@@ -115,7 +126,7 @@ __global__ void __launch_bounds__(kGive) reserve_kernel(const PoolParams p) {
     }
     return p.table + lo * p.table_stride + pages_for(p.from[lo], p.page_tokens) + rank - (lo > 0 ? s_upto[lo - 1] : 0);
   };
-  const int got = free_pages(p.refs, p.n_pages, static_cast<int>(want), s_warp, [&](int rank, int32_t page) {
+  const int got = free_pages(p.refs, p.n_pages, static_cast<int>(want), counts, s_warp, [&](int rank, int32_t page) {
     *place(rank) = page;
     p.refs[page] = 1;
   });
@@ -150,13 +161,14 @@ __global__ void __launch_bounds__(kRowThreads) fork_rows_kernel(const PoolParams
       if (p.parents[r] != b) continue;
       const bool copy = copies && r != s_first;
       p.src[r] = copy ? last : -1;
+      p.dst[r] = copy ? static_cast<int32_t>(used - 1) : -1;  // its entry, for the kernel that gives the page
       p.tokens[r] = copy ? rest : 0;
     }
   } else {
     const int64_t r = blockIdx.x - p.n_old;
     const int64_t b = p.parents[r];
     const bool there = b >= 0 && b < p.n_old;
-    if (!there && threadIdx.x == 0) p.src[r] = -1, p.tokens[r] = 0;
+    if (!there && threadIdx.x == 0) p.src[r] = p.dst[r] = -1, p.tokens[r] = 0;
     const int64_t used = there ? min(pages_for(p.from[b], p.page_tokens), p.old_stride) : 0;
     for (int64_t e = threadIdx.x; e < p.table_stride; e += kRowThreads)
       p.table[r * p.table_stride + e] = e < used ? p.old_table[b * p.old_stride + e] : -1;
@@ -166,33 +178,28 @@ __global__ void __launch_bounds__(kRowThreads) fork_rows_kernel(const PoolParams
 // The copies' pages: one block.
 __global__ void __launch_bounds__(kGive) fork_copies_kernel(const PoolParams p) {
   __shared__ int s_warp[32];
-  __shared__ int s_rows[kMaxPoolSeqs];  // the rows that get a copy
+  extern __shared__ int2 s_rows[];  // (row, entry) of the rows that get a copy
   wait_for_last_kernel();
+  Counts<kGivePer> counts;
+  counts.load(p.refs, p.n_pages, static_cast<int64_t>(threadIdx.x) * kGivePer);
   int want = 0;
   for (int64_t r0 = 0; r0 < p.n_seqs; r0 += kGive) {
     const int64_t r = r0 + threadIdx.x;
-    const bool need = r < p.n_seqs && p.src[r] >= 0;
+    const int entry = r < p.n_seqs ? p.dst[r] : -1;
     int total;
-    const int at = want + block_sum<kGive>(need, s_warp, total) - 1;
-    if (need) s_rows[at] = static_cast<int>(r);
-    else if (r < p.n_seqs) p.dst[r] = -1;
+    const int at = want + block_sum<kGive>(entry >= 0, s_warp, total) - 1;
+    if (entry >= 0) s_rows[at] = make_int2(static_cast<int>(r), entry);
     want += total;
   }
   __syncthreads();
-  auto entry = [&](int r) -> int32_t& {
-    return p.table[r * p.table_stride + pages_for(p.from[p.parents[r]], p.page_tokens) - 1];
+  auto give = [&](int rank, int32_t page) {
+    const int2 r = s_rows[rank];
+    p.dst[r.x] = page;
+    p.table[r.x * p.table_stride + r.y] = page;
+    if (page >= 0) p.refs[page] = 1;
   };
-  const int got = free_pages(p.refs, p.n_pages, want, s_warp, [&](int rank, int32_t page) {
-    const int r = s_rows[rank];
-    p.dst[r] = page;
-    entry(r) = page;
-    p.refs[page] = 1;
-  });
-  for (int i = got + threadIdx.x; i < want; i += kGive) {
-    const int r = s_rows[i];
-    p.dst[r] = -1;
-    entry(r) = -1;
-  }
+  const int got = free_pages(p.refs, p.n_pages, want, counts, s_warp, give);
+  for (int i = got + threadIdx.x; i < want; i += kGive) give(i, -1);
   if (threadIdx.x == 0 && got < want) *p.missing += want - got;
 }
 
@@ -211,13 +218,18 @@ __global__ void __launch_bounds__(kRowThreads) release_kernel(const PoolParams p
 // ---- compact
 __device__ __forceinline__ int64_t pool_tiles(int64_t n_pages) { return (n_pages + kPoolTile - 1) / kPoolTile; }
 
+constexpr int kTilePer = kPoolTile / kRowThreads;  // counts of a thread
+
 // Pages in use of a tile.
 __global__ void __launch_bounds__(kRowThreads) compact_count_kernel(const PoolParams p) {
   __shared__ int s_warp[32];
   allow_next_kernel();
-  const int64_t p0 = static_cast<int64_t>(blockIdx.x) * kPoolTile;
+  Counts<kTilePer> c;
+  c.load(p.refs, p.n_pages, static_cast<int64_t>(blockIdx.x) * kPoolTile + threadIdx.x * kTilePer);
   int n = 0, total;
-  for (int i = threadIdx.x; i < kPoolTile; i += kRowThreads) n += p0 + i < p.n_pages && p.refs[p0 + i] > 0;
+#pragma unroll
+  for (int i = 0; i < kTilePer; ++i)
+    n += static_cast<int64_t>(blockIdx.x) * kPoolTile + threadIdx.x * kTilePer + i < p.n_pages && c.v[i] > 0;
   block_sum<kRowThreads>(n, s_warp, total);
   if (threadIdx.x == 0) p.scratch[blockIdx.x] = total;
 }
@@ -227,9 +239,11 @@ __global__ void __launch_bounds__(kRowThreads) compact_count_kernel(const PoolPa
 __global__ void __launch_bounds__(kRowThreads) compact_moves_kernel(const PoolParams p) {
   __shared__ int s_warp[32];
   allow_next_kernel();
-  wait_for_last_kernel();
-  const int64_t tiles = pool_tiles(p.n_pages), me = blockIdx.x;
+  const int64_t tiles = pool_tiles(p.n_pages), me = blockIdx.x, page0 = me * kPoolTile + threadIdx.x * kTilePer;
   int32_t* map = p.scratch + tiles;
+  Counts<kTilePer> c;
+  c.load(p.refs, p.n_pages, page0);
+  wait_for_last_kernel();
   // pages in use before this tile, and in all
   int before = 0, all = 0, used, below;
   for (int64_t t = threadIdx.x; t < tiles; t += kRowThreads) {
@@ -242,18 +256,22 @@ __global__ void __launch_bounds__(kRowThreads) compact_moves_kernel(const PoolPa
   int n = 0;
   const int64_t edge = used / kPoolTile;
   for (int64_t t = threadIdx.x; t < edge; t += kRowThreads) n += p.scratch[t];
+#pragma unroll 4
   for (int64_t q = edge * kPoolTile + threadIdx.x; q < used; q += kRowThreads) n += p.refs[q] > 0;
   block_sum<kRowThreads>(n, s_warp, below);
 
-  for (int i0 = 0; i0 < kPoolTile; i0 += kRowThreads) {
-    const int64_t page = me * kPoolTile + i0 + threadIdx.x;
-    const bool on = page < p.n_pages && p.refs[page] > 0;
-    int total;
-    const int upto = before + block_sum<kRowThreads>(on, s_warp, total) - on;  // in use before this page
-    before += total;
-    if (page >= p.n_pages) continue;
-    const bool moves = on && page >= used;
+  n = 0;
+#pragma unroll
+  for (int i = 0; i < kTilePer; ++i) n += page0 + i < p.n_pages && c.v[i] > 0;
+  int total;
+  int upto = before + block_sum<kRowThreads>(n, s_warp, total) - n;  // pages in use before this one
+#pragma unroll
+  for (int i = 0; i < kTilePer; ++i) {
+    const int64_t page = page0 + i;
+    if (page >= p.n_pages) break;
+    const bool on = c.v[i] > 0, moves = on && page >= used;
     const int64_t j = moves ? upto - below : page - upto;
+    upto += on;
     map[page] = moves ? static_cast<int32_t>(j) : -1;
     if (j >= p.n_moves) continue;
     if (moves) p.src[j] = static_cast<int32_t>(page);
@@ -282,38 +300,101 @@ __global__ void __launch_bounds__(kRowThreads) compact_apply_kernel(const PoolPa
   }
 }
 
-// ---- copies: a block takes kCopyBytes of a page at a time
+// ---- copies: a block takes chunks of kCopyBytes of what is to be copied
 constexpr int kCopyThreads = 256;
 constexpr int kCopyUnits = 4;  // 16-byte units of a thread
 constexpr int kCopyBytes = kCopyThreads * kCopyUnits * 16;
+constexpr int kCopyWindow = 1024;  // pairs that are looked at together
 
-__global__ void __launch_bounds__(kCopyThreads) copy_pages_kernel(const CopyPagesParams p) {
-  const int64_t chunks = (p.page_bytes + kCopyBytes - 1) / kCopyBytes;
-  for (int64_t item = blockIdx.x; item < p.n * chunks; item += gridDim.x) {
-    const int64_t i = div_small(item, chunks), chunk = item - i * chunks;
-    const int64_t from = p.src[i], to = p.dst[i];
-    if (from < 0 || from >= p.n_pages || to < 0 || to >= p.n_pages) continue;
-    // the blocks of the first tokens of each head: `run` units at every `step`
-    const int blocks = p.tokens ? (min(max(p.tokens[i], 0), p.blocks * kKvBlockTokens) + kKvBlockTokens - 1) / kKvBlockTokens : p.blocks;
-    const uint32_t run = static_cast<uint32_t>(blocks) * p.block_bytes / 16, step = static_cast<uint32_t>(p.blocks) * p.block_bytes / 16;
-    const int64_t units = static_cast<int64_t>(run) * p.heads, u0 = chunk * (kCopyBytes / 16) + threadIdx.x;
-    const uint4* s = reinterpret_cast<const uint4*>(p.pages + from * p.page_bytes);
-    uint4* d = reinterpret_cast<uint4*>(p.pages + to * p.page_bytes);
-    uint4 x[kCopyUnits];
-    int64_t at[kCopyUnits];
+struct CopyPair {
+  int from, to;
+  uint32_t run;  // 16-byte units of each head
+};
+
+__device__ __forceinline__ CopyPair copy_pair(const CopyPagesParams& p, int64_t i) {
+  CopyPair c = {-1, -1, 0};
+  if (i >= p.n) return c;
+  c.from = p.src[i], c.to = p.dst[i];
+  // the blocks of the first tokens of each head
+  const int blocks = p.tokens ? (min(max(p.tokens[i], 0), p.blocks * kKvBlockTokens) + kKvBlockTokens - 1) / kKvBlockTokens : p.blocks;
+  if (c.from >= 0 && c.from < p.n_pages && c.to >= 0 && c.to < p.n_pages) c.run = static_cast<uint32_t>(blocks) * p.block_bytes / 16;
+  return c;
+}
+__device__ __forceinline__ int64_t copy_chunks(const CopyPagesParams& p, const CopyPair& c) {
+  return (static_cast<int64_t>(c.run) * p.heads + kCopyBytes / 16 - 1) / (kCopyBytes / 16);
+}
+
+__device__ __forceinline__ void copy_chunk(const CopyPagesParams& p, const CopyPair& c, int64_t chunk) {
+  const uint32_t step = static_cast<uint32_t>(p.blocks) * p.block_bytes / 16;
+  const int64_t units = static_cast<int64_t>(c.run) * p.heads, u0 = chunk * (kCopyBytes / 16) + threadIdx.x;
+  const uint4* s = reinterpret_cast<const uint4*>(p.pages + c.from * p.page_bytes);
+  uint4* d = reinterpret_cast<uint4*>(p.pages + c.to * p.page_bytes);
+  uint4 x[kCopyUnits];
+  int64_t at[kCopyUnits];
 #pragma unroll
-    for (int k = 0; k < kCopyUnits; ++k) {
-      const int64_t u = u0 + k * kCopyThreads;
-      at[k] = -1;
-      if (u < units) {
-        const int64_t h = run == step ? 0 : div_small(u, run);
-        at[k] = u + h * (step - run);
-        x[k] = s[at[k]];
-      }
+  for (int k = 0; k < kCopyUnits; ++k) {
+    const int64_t u = u0 + k * kCopyThreads;
+    at[k] = -1;
+    if (u < units) {
+      at[k] = c.run == step ? u : u + div_small(u, c.run) * (step - c.run);
+      x[k] = s[at[k]];
     }
+  }
 #pragma unroll
-    for (int k = 0; k < kCopyUnits; ++k)
-      if (at[k] >= 0) d[at[k]] = x[k];
+  for (int k = 0; k < kCopyUnits; ++k)
+    if (at[k] >= 0) d[at[k]] = x[k];
+}
+
+// A block for each chunk of each pair.
+__global__ void __launch_bounds__(kCopyThreads) copy_few_kernel(const CopyPagesParams p) {
+  const int64_t chunks = (p.page_bytes + kCopyBytes - 1) / kCopyBytes, i = div_small(blockIdx.x, chunks);
+  const CopyPair c = copy_pair(p, i);
+  if (c.run) copy_chunk(p, c, blockIdx.x - i * chunks);
+}
+
+// Blocks take the chunks of the pairs that are to be copied in turn: those pairs
+// are gathered first, kCopyWindow at a time, so that pairs without a page, or
+// with few tokens, leave no block without work.
+__global__ void __launch_bounds__(kCopyThreads) copy_pages_kernel(const CopyPagesParams p) {
+  __shared__ CopyPair s_pair[kCopyWindow];
+  __shared__ int64_t s_upto[kCopyWindow];  // chunks of the pairs up to and with this one
+  __shared__ int s_warp[32];
+  constexpr int kPer = kCopyWindow / kCopyThreads;
+  int64_t done = 0;  // chunks of earlier windows
+  for (int64_t w0 = 0; w0 < p.n; w0 += kCopyWindow) {
+    CopyPair mine[kPer];
+    int n = 0, pairs, total;
+    int64_t chunks = 0;
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) {
+      mine[k] = copy_pair(p, w0 + threadIdx.x * kPer + k);
+      if (mine[k].run) ++n, chunks += copy_chunks(p, mine[k]);
+    }
+    // (a page has less than 2^14 chunks)
+    int at = block_sum<kCopyThreads>(n, s_warp, pairs) - n;
+    int64_t upto = block_sum<kCopyThreads>(static_cast<int>(chunks), s_warp, total) - chunks;
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) {
+      if (!mine[k].run) continue;
+      upto += copy_chunks(p, mine[k]);
+      s_pair[at] = mine[k], s_upto[at] = upto;
+      ++at;
+    }
+    __syncthreads();
+    // this block's: those with (done + index) % gridDim == blockIdx
+    int64_t c = blockIdx.x - done % gridDim.x;
+    if (c < 0) c += gridDim.x;
+    for (; c < total; c += gridDim.x) {
+      int lo = 0, hi = pairs - 1;
+      while (lo < hi) {
+        const int mid = (lo + hi) >> 1;
+        if (s_upto[mid] <= c) lo = mid + 1;
+        else hi = mid;
+      }
+      copy_chunk(p, s_pair[lo], c - (lo > 0 ? s_upto[lo - 1] : 0));
+    }
+    done += total;
+    __syncthreads();
   }
 }
 
@@ -327,7 +408,7 @@ cudaError_t launch_pool_reserve(const PoolParams& p, cudaStream_t s) {
 cudaError_t launch_pool_fork(const PoolParams& p, cudaStream_t s) {
   fork_rows_kernel<<<static_cast<unsigned>(p.n_old + p.n_seqs), kRowThreads, 0, s>>>(p);
   const cudaError_t e = cudaGetLastError();
-  return e != cudaSuccess ? e : launch_after(fork_copies_kernel, 1, p, s, kGive);
+  return e != cudaSuccess ? e : launch_after(fork_copies_kernel, 1, p, s, kGive, static_cast<int>(p.n_seqs) * 8);
 }
 
 cudaError_t launch_pool_release(const PoolParams& p, cudaStream_t s) {
@@ -351,8 +432,10 @@ cudaError_t launch_copy_pages(const CopyPagesParams& p, cudaStream_t s) {
   int dev = 0, sms = 0;
   const cudaError_t found = current_device(&dev, &sms);
   if (found != cudaSuccess) return found;
+  // few chunks, at most those that run at once: no gathering
   const int64_t items = p.n * ((p.page_bytes + kCopyBytes - 1) / kCopyBytes), most = 8 * static_cast<int64_t>(sms);
-  copy_pages_kernel<<<static_cast<unsigned>(items < most ? items : most), kCopyThreads, 0, s>>>(p);
+  if (items <= most) copy_few_kernel<<<static_cast<unsigned>(items), kCopyThreads, 0, s>>>(p);
+  else copy_pages_kernel<<<static_cast<unsigned>(most), kCopyThreads, 0, s>>>(p);
   return cudaGetLastError();
 }
 

@@ -8,7 +8,7 @@ namespace qgemv {
 
 // Sequences of a bookkeeping call, at most (their needs are summed in shared
 // memory).
-constexpr int kMaxPoolSeqs = 8192;
+constexpr int kMaxPoolSeqs = 4096;
 // Pages of a tile of the compacting scan.
 constexpr int kPoolTile = 4096;
 

@@ -10,10 +10,14 @@
 // become a float of at most 1 and sincospif's argument.
 //
 // Bytes bound it, as the cache write (kv_cache.cu), whose layout it takes: a
-// lane for eight neighbouring values, a warp for eight rows of one token, so
-// that the angles are worked out once for eight rows.  The other value of a
-// pair comes by a shuffle where the pairs are a multiple of eight (any head
-// whose halves are rotated whole), else through shared memory.
+// lane for eight neighbouring values, a warp for eight rows of one token, all of
+// them queries, keys or values.  A block works out the angles of its eight
+// warps' tokens once, while their rows are on their way, and keeps cosines and
+// sines in shared memory; with an angle for each lane's values in every warp the
+// instructions were the bound (27003 tokens of 32 + 32 + 32 heads, bf16 into an
+// fp16 cache: 408 us).  The other value of a pair comes by a shuffle where the
+// pairs are a multiple of eight (any head whose halves are turned whole), else
+// through shared memory.
 #include <type_traits>
 
 #include "kv_codes.cuh"
@@ -23,106 +27,152 @@ namespace qgemv {
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int kWarps = kThreads / 32;  // and tokens of a block, at most
 constexpr int kWarpRows = 8;
+
+// Warps of a token: for its queries, keys and values.
+__host__ __device__ __forceinline__ int row_warps(int heads) { return (heads + kWarpRows - 1) / kWarpRows; }
 
 // FMT 0: rows only, no cache.
 template <int FMT, int D, typename T>
 __global__ void __launch_bounds__(kThreads) rope_kernel(const RopeParams p) {
   constexpr int kLanes = D / 8, kAt = 32 / kLanes;  // kAt rows at a time
   constexpr int kPasses = kWarpRows / kAt;
-  __shared__ float s_row[kThreads / 32][kAt][D];
+  // Cosines and sines of a token's D / 2 pairs, as quads of pairs 4 i .. 4 i + 3:
+  // the even quads first, so that neighbouring lanes, two quads each, read
+  // neighbouring ones.
+  __shared__ float4 s_cos[kWarps][D / 8], s_sin[kWarps][D / 8];
+  __shared__ float s_row[kWarps][kAt][D];
   const unsigned full = 0xffffffffu;
-  const int lane = threadIdx.x & 31, H = FMT ? p.cache.kv_heads : 0;
-  const int q_warps = (p.q_heads + kWarpRows - 1) / kWarpRows, per = q_warps + (2 * H + kWarpRows - 1) / kWarpRows;
-  const int64_t w = (static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x) >> 5;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, n = p.pairs;
+  const int H = FMT ? p.cache.kv_heads : 0, q_warps = row_warps(p.q_heads), k_warps = row_warps(H), per = q_warps + 2 * k_warps;
+  const int64_t w0 = static_cast<int64_t>(blockIdx.x) * kWarps, t0 = div_small(w0, per), w = w0 + warp;
   const int64_t token = div_small(w, per);
-  if (token >= p.n_tokens) return;
-  const int part = static_cast<int>(w - token * per);
-  const bool is_q = part < q_warps;
-  const int rows = is_q ? p.q_heads : 2 * H;  // cache rows: 2 * head + (V ? 1 : 0)
-  const int row0 = (is_q ? part : part - q_warps) * kWarpRows;
+  const int part = static_cast<int>(w - token * per), kind = part < q_warps ? 0 : part < q_warps + k_warps ? 1 : 2;  // q, k, v
+  const int heads = kind == 0 ? p.q_heads : H;
+  const int row0 = (kind == 0 ? part : kind == 1 ? part - q_warps : part - q_warps - k_warps) * kWarpRows;
   const int d0 = (lane % kLanes) * 8;
+  bool on = token < p.n_tokens;
 
   uint8_t* b0 = nullptr;
   int at = 0;
   int64_t step = 0;
   if constexpr (FMT != 0) {
-    if (!is_q) {
+    if (on && kind != 0) {
       const int64_t slot = __ldg(p.slots + token);
-      if (slot < 0 || slot >= p.cache.n_pages * p.cache.page_tokens) return;
-      at = static_cast<int>(slot) & (p.cache.page_tokens - 1);
-      b0 = kv_block<FMT, D>(p.cache, slot >> (31 - __clz(p.cache.page_tokens)), 0, at / kKvBlockTokens);
-      step = static_cast<int64_t>(p.cache.page_tokens / kKvBlockTokens) * KvLayout<FMT, D>::kBlock;
+      on = slot >= 0 && slot < p.cache.n_pages * p.cache.page_tokens;
+      if (on) {
+        at = static_cast<int>(slot) & (p.cache.page_tokens - 1);
+        b0 = kv_block<FMT, D>(p.cache, slot >> (31 - __clz(p.cache.page_tokens)), 0, at / kKvBlockTokens);
+        step = static_cast<int64_t>(p.cache.page_tokens / kKvBlockTokens) * KvLayout<FMT, D>::kBlock;
+      }
     }
   }
   Raw<T> raw[kPasses];
+  if (on) {
+    const RowsIn& in = kind == 0 ? p.q : kind == 1 ? p.k : p.v;
+    const T* src = static_cast<const T*>(in.ptr) + token * in.token_stride + d0;
 #pragma unroll
-  for (int i = 0; i < kPasses; ++i) {
-    const int row = min(row0 + i * kAt + lane / kLanes, rows - 1);
-    const RowsIn& in = is_q ? p.q : row & 1 ? p.v : p.k;
-    raw[i].load_own(static_cast<const T*>(in.ptr) + token * in.token_stride + (is_q ? row : row >> 1) * in.head_stride + d0);
+    for (int i = 0; i < kPasses; ++i) raw[i].load_own(src + min(row0 + i * kAt + lane / kLanes, heads - 1) * in.head_stride);
   }
 
-  // ---- the angles of this lane's values
-  const int n = p.pairs;
-  int pos[4];
-#pragma unroll
-  for (int a = 0; a < 4; ++a) pos[a] = a < p.n_axes ? __ldg(p.positions + token * p.n_axes + a) : 0;
-  auto angle = [&](int j, float& c, float& s) {
-    const uint4 e = __ldg(p.plan + j);
-    const int x = e.z == 0 ? pos[0] : e.z == 1 ? pos[1] : e.z == 2 ? pos[2] : pos[3];
-    const uint64_t turns = static_cast<uint64_t>(e.y) << 32 | e.x;
-    const uint64_t t = turns * static_cast<uint64_t>(static_cast<int64_t>(x));
-    sincospif(static_cast<float>(static_cast<int32_t>(t >> 32)) * 0x1p-31f, &s, &c);
-  };
-  float c[8], s[8];
-#pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    const int i = d0 + e;
-    c[e] = 1.f, s[e] = 0.f;
-    if (p.neighbours) {
-      if (e & 1) c[e] = c[e - 1], s[e] = -s[e - 1];
-      else if (i < 2 * n) angle(i >> 1, c[e], s[e]), s[e] = -s[e];
-    } else if (i < 2 * n) {
-      angle(i < n ? i : i - n, c[e], s[e]);
-      if (i < n) s[e] = -s[e];
+  // ---- the angles of the block's tokens
+  const int tokens = static_cast<int>(min(div_small(w0 + kWarps - 1, per), p.n_tokens - 1) - t0) + 1;
+  for (int i = threadIdx.x; i < tokens * (D / 2); i += kThreads) {
+    const int t = i / (D / 2), j = i % (D / 2);
+    float c = 1.f, s = 0.f;
+    if (j < n) {
+      const uint4 e = __ldg(p.plan + j);
+      const int x = e.z < static_cast<unsigned>(p.n_axes) ? __ldg(p.positions + (t0 + t) * p.n_axes + e.z) : 0;
+      const uint64_t turns = static_cast<uint64_t>(e.y) << 32 | e.x;
+      const uint64_t turn = turns * static_cast<uint64_t>(static_cast<int64_t>(x));
+      sincospif(static_cast<float>(static_cast<int32_t>(turn >> 32)) * 0x1p-31f, &s, &c);
     }
+    const int quad = ((j >> 2) & 1) * (D / 16) + (j >> 3);
+    reinterpret_cast<float*>(&s_cos[t][quad])[j & 3] = c;
+    reinterpret_cast<float*>(&s_sin[t][quad])[j & 3] = s;
+  }
+  __syncthreads();
+  if (!on) return;
+
+  // this lane's: y = x c + other s, with -s for the first of a pair
+  const bool whole = (n & 7) == 0;
+  float c[8], s[8];
+  bool turned[8];
+  if (kind != 2) {
+    const int t = static_cast<int>(token - t0);
+    auto quad = [&](int q, float (&cc)[4], float (&ss)[4]) {
+      const float4 a = s_cos[t][(q & 1) * (D / 16) + (q >> 1)], b = s_sin[t][(q & 1) * (D / 16) + (q >> 1)];
+      cc[0] = a.x, cc[1] = a.y, cc[2] = a.z, cc[3] = a.w;
+      ss[0] = b.x, ss[1] = b.y, ss[2] = b.z, ss[3] = b.w;
+    };
+    float cc[4], ss[4];
+    if (p.neighbours) {
+      quad(d0 / 8, cc, ss);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) c[e] = cc[e / 2], s[e] = e & 1 ? ss[e / 2] : -ss[e / 2];
+    } else if (whole) {
+      const int j0 = d0 < n ? d0 : d0 < 2 * n ? d0 - n : 0;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        quad(j0 / 4 + h, cc, ss);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) c[4 * h + e] = cc[e], s[4 * h + e] = d0 < n ? -ss[e] : ss[e];
+      }
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const int i = d0 + e, j = i < n ? i : i < 2 * n ? i - n : 0, q = ((j >> 2) & 1) * (D / 16) + (j >> 3);
+        c[e] = reinterpret_cast<const float*>(&s_cos[t][q])[j & 3];
+        const float x = reinterpret_cast<const float*>(&s_sin[t][q])[j & 3];
+        s[e] = i < n ? -x : x;
+      }
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) turned[e] = d0 + e < 2 * n;
   }
 
 #pragma unroll
   for (int i = 0; i < kPasses; ++i) {
     const int row = row0 + i * kAt + lane / kLanes;
-    float x[8], y[8];
+    if (row0 + i * kAt >= heads) break;  // (the warp's)
+    float x[8];
     raw[i].values(x);
-    if (p.neighbours) {
+    if (kind != 2) {
+      float y[8];
+      if (p.neighbours) {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) y[e] = x[e ^ 1];
-    } else if ((n & 7) == 0) {
-      const int other = d0 < n ? lane + n / 8 : d0 < 2 * n ? lane - n / 8 : lane;
+        for (int e = 0; e < 8; ++e) y[e] = x[e ^ 1];
+      } else if (whole) {
+        const int other = d0 < n ? lane + n / 8 : d0 < 2 * n ? lane - n / 8 : lane;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) y[e] = __shfl_sync(full, x[e], other);
-    } else {
-      float* mine = s_row[threadIdx.x >> 5][lane / kLanes];
-      __syncwarp();
+        for (int e = 0; e < 8; ++e) y[e] = __shfl_sync(full, x[e], other);
+      } else {
+        float* mine = s_row[warp][lane / kLanes];
+        __syncwarp();
 #pragma unroll
-      for (int e = 0; e < 8; ++e) mine[d0 + e] = x[e];
-      __syncwarp();
+        for (int e = 0; e < 8; ++e) mine[d0 + e] = x[e];
+        __syncwarp();
 #pragma unroll
-      for (int e = 0; e < 8; ++e) y[e] = d0 + e < 2 * n ? mine[d0 + e < n ? d0 + e + n : d0 + e - n] : 0.f;
+        for (int e = 0; e < 8; ++e) y[e] = d0 + e < 2 * n ? mine[d0 + e < n ? d0 + e + n : d0 + e - n] : 0.f;
+      }
+#pragma unroll
+      for (int e = 0; e < 8; e += 2) {
+        float u, v;
+        unpack2(fma2(pack2(x[e], x[e + 1]), pack2(c[e], c[e + 1]), mul2(pack2(y[e], y[e + 1]), pack2(s[e], s[e + 1]))), u, v);
+        if (turned[e]) x[e] = u;
+        if (turned[e + 1]) x[e + 1] = v;
+      }
     }
-    const bool turn = is_q || !(row & 1);
-#pragma unroll
-    for (int e = 0; e < 8; ++e)
-      if (turn && d0 + e < 2 * n) x[e] = fmaf(x[e], c[e], y[e] * s[e]);
-    if (is_q) {
-      if (row < rows) {
+    if (kind == 0) {
+      if (row < heads) {
         const int64_t to = token * p.out.token_stride + row * p.out.head_stride + d0;
         if (p.out_dtype == QGEMV_DT_F16) store_values(static_cast<__half*>(p.out.ptr) + to, x);
         else if (p.out_dtype == QGEMV_DT_BF16) store_values(static_cast<__nv_bfloat16*>(p.out.ptr) + to, x);
         else store_values(static_cast<float*>(p.out.ptr) + to, x);
       }
     } else if constexpr (FMT != 0) {
-      encode<FMT, D>(b0 + (row >> 1) * step, row & 1, at % kKvBlockTokens, d0, x, row < rows);
+      encode<FMT, D>(b0 + row * step, kind == 2, at % kKvBlockTokens, d0, x, row < heads);
     }
   }
 }
@@ -131,8 +181,8 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const RopeParams p) {
 
 cudaError_t launch_rope(const RopeParams& p, int dtype, int head_dim, cudaStream_t s) {
   const int H = p.cache.pages ? p.cache.kv_heads : 0;
-  const int64_t warps = p.n_tokens * ((p.q_heads + kWarpRows - 1) / kWarpRows + (2 * H + kWarpRows - 1) / kWarpRows);
-  const int64_t grid = (warps + kThreads / 32 - 1) / (kThreads / 32);
+  const int64_t warps = p.n_tokens * (row_warps(p.q_heads) + 2 * row_warps(H));
+  const int64_t grid = (warps + kWarps - 1) / kWarps;
   if (grid > 0x7fffffff) return cudaErrorInvalidConfiguration;
   auto go = [&](auto kernel) {
     kernel<<<static_cast<unsigned>(grid), kThreads, 0, s>>>(p);

@@ -32,7 +32,7 @@ struct SelectParams {
   int32_t* out_lens;
 };
 
-// Pages of a sequence, at most: the scores lie in a cluster's shared memory.
+// Pages of a sequence, at most: the scores lie in a block's shared memory.
 int64_t select_most_pages();
 cudaError_t launch_summary(const SummaryParams& p, cudaStream_t s);
 cudaError_t launch_select(const SelectParams& p, cudaStream_t s);

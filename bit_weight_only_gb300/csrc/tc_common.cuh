@@ -252,13 +252,14 @@ __device__ __forceinline__ void allow_next_kernel() { asm volatile("griddepcontr
 __device__ __forceinline__ void wait_for_last_kernel() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 template <typename A>
-cudaError_t launch_after(void (*kernel)(const A), unsigned grid, const A& a, cudaStream_t s, int threads = 128) {
+cudaError_t launch_after(void (*kernel)(const A), unsigned grid, const A& a, cudaStream_t s, int threads = 128, int smem = 0) {
   cudaLaunchAttribute attr;
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr.val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(grid);
   cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = static_cast<size_t>(smem);
   cfg.stream = s;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;

@@ -576,7 +576,7 @@ int qgemv_beam_select(int dtype, const void* logits, int64_t row_stride, int64_t
  * are no page's number are passed over.  Free pages are given out lowest
  * first, in the order of the rows, so results depend on the inputs alone.
  * Where there are none left, the entry becomes -1 and *missing (device int32)
- * counts it.  At most 8192 rows of 2^20 entries a call; calls of one pool
+ * counts it.  At most 4096 rows of 2^20 entries a call; calls of one pool
  * one at a time.  All are asynchronous on `stream`, allocate nothing, can be
  * captured in a CUDA graph, and leave refs the only state.
  *
@@ -660,7 +660,7 @@ int qgemv_kv_summarize(const qgemv_kv_cache* cache, const int32_t* pages, int64_
  * then -1; lens (device int32 [n_seqs]) the context's length over them: a page
  * table for qgemv_attn_pages.  Sequences, q, cu_q and the table as for
  * qgemv_attn_tree; cache's pages are not read; table_stride is at most
- * 393216.  Asynchronous on `stream`, no allocation, can be captured in a CUDA
+ * 49152.  Asynchronous on `stream`, no allocation, can be captured in a CUDA
  * graph; the same inputs give the same choice.                               */
 int64_t qgemv_kv_select_width(int page_tokens, int64_t n_select);
 int qgemv_kv_select(const qgemv_kv_cache* cache, const int8_t* codes, const float* scales, const int32_t* table,

@@ -161,13 +161,13 @@ def test_reserve_edges():
 
 
 def test_most_rows():
-    rows = 8192
+    rows = 4096
     pool = qgemv.PagePool(2 * rows + 5, 16)
     t = torch.full((rows, 2), -1, dtype=torch.int32, device="cuda")
     zero = torch.zeros(rows, dtype=torch.int32, device="cuda")
     pool.reserve(t, zero, zero + 20)
     assert torch.equal(t.flatten(), torch.arange(2 * rows, dtype=torch.int32, device="cuda"))
-    # every row's first child is row 8191 - r, and nobody has a second one
+    # every row's first child is row 4095 - r, and nobody has a second one
     new, src, dst, tokens = pool.fork(t, torch.arange(rows - 1, -1, -1, dtype=torch.int32, device="cuda"), zero + 20)
     assert torch.equal(new, t.flip(0)) and bool((src == -1).all()) and bool((dst == -1).all())
     # row 0 has all of the children: its whole page is shared, the others' pages are free for the copies

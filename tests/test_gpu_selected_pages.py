@@ -255,13 +255,13 @@ def test_strides_tables_and_lengths():
 
 
 def test_the_longest_tables():
-    """A table of as many pages as a call takes, on a cluster of eight blocks, most of it used twice over."""
+    """A table of as many pages as a call takes, on a cluster of eight blocks, each page in it many times."""
     c, k, _ = cached("q4_0", 7, 3000, 16, 1, 64)
     s = qgemv.KeySummary(c)
     s.update(torch.arange(3000, dtype=torch.int32, device="cuda"))
-    table = np.arange(393216, dtype=np.int64) * 7 % 3000
+    table = np.arange(49152, dtype=np.int64) * 7 % 3000
     q = torch.randn(1, 1, 64, generator=torch.Generator(device="cuda").manual_seed(2), device="cuda").half()
-    ctx = 393216 * 16
+    ctx = 49152 * 16
     pages, l = c.select(q, i32(table)[None], i32([ctx]), i32([0, 1]), summary=s, n_select=5000)
     want, length = choice(q.cpu().numpy(), 1, list(table), ctx, 5000, 16, s.codes.cpu().numpy().astype(np.int64), s.scales.cpu().numpy())
     assert pages[0].tolist() == want and int(l[0]) == length == 5000 * 16

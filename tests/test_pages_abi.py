@@ -124,7 +124,7 @@ def test_beam_workspace_sizes(lib):
 
 
 BAD_POOL = [({"refs": None}, ARG), ({"refs": 258}, ALIGN), ({"n_pages": 0}, ARG), ({"n_pages": 1 << 31}, ARG), ({"rows": -1}, ARG),
-            ({"rows": 8193}, ARG), ({"stride": -1}, ARG), ({"stride": (1 << 20) + 1}, ARG), ({"table": None}, ARG)]
+            ({"rows": 4097}, ARG), ({"stride": -1}, ARG), ({"stride": (1 << 20) + 1}, ARG), ({"table": None}, ARG)]
 
 
 @pytest.mark.parametrize("kw, code", BAD_POOL)
@@ -139,7 +139,7 @@ def test_bad_pools_are_refused(lib, kw, code):
     ("reserve", {"need": 66}, ALIGN), ("reserve", {"rows": 0}, OK), ("reserve", {"stride": 0}, OK),
     ("fork", {"page": 512}, ARG), ("fork", {"parents": None}, ARG), ("fork", {"lens": None}, ARG), ("fork", {"new": None}, ARG),
     ("fork", {"src": None}, ARG), ("fork", {"dst": None}, ARG), ("fork", {"tokens": None}, ARG), ("fork", {"missing": None}, ARG),
-    ("fork", {"n": 8193}, ARG), ("fork", {"n": -1}, ARG), ("fork", {"src": 65}, ALIGN), ("fork", {"new": 1 << 20}, ARG),
+    ("fork", {"n": 4097}, ARG), ("fork", {"n": -1}, ARG), ("fork", {"src": 65}, ALIGN), ("fork", {"new": 1 << 20}, ARG),
     ("fork", {"new": (1 << 20) + 28}, ARG), ("fork", {"new": (1 << 20) - 44}, ARG), ("fork", {"rows": 0, "n": 0}, OK),
     ("release", {"page": 0}, ARG), ("release", {"lens": None}, ARG), ("release", {"keep": 3}, ALIGN), ("release", {"rows": 0}, OK),
     ("compact", {"new": None}, ARG), ("compact", {"src": None}, ARG), ("compact", {"n_moves": 49}, ARG), ("compact", {"n_moves": 101}, ARG),
@@ -171,7 +171,7 @@ def test_summary_refusals(lib, kw, code):
                                       ({"heads": 0}, ARG), ({"q": None}, ARG), ({"q": 264}, ALIGN), ({"qt": 1001}, ALIGN),
                                       ({"cu": None}, ARG), ({"ctx": None}, ARG), ({"table": None}, ARG), ({"pages": None}, ARG),
                                       ({"lens": None}, ARG), ({"lens": 66}, ALIGN), ({"select": -1}, ARG),
-                                      ({"select": (1 << 20) + 1}, ARG), ({"stride": 393217}, ARG), ({"stride": -1}, ARG),
+                                      ({"select": (1 << 20) + 1}, ARG), ({"stride": 49153}, ARG), ({"stride": -1}, ARG),
                                       ({"n": -1}, ARG), ({"seqs": -1}, ARG), ({"seqs": 0}, OK)])
 def test_select_refusals(lib, kw, code):
     assert call(lib.qgemv_kv_select, SELECT, {"cache": cache(), **kw}) == code
