@@ -12,8 +12,9 @@
 // largest of the threads' maxima when a tile would overflow the list (that
 // many keys at least reach it, and at most `width` threads' values do) and the
 // list's own `width`-th key once it was cut; after the first tile few values
-// pass.  A second kernel, a block a sequence, merges the parts' sorted lists
-// with the beams' scores in 64 bits: fp32 would make ties of scores that differ.
+// pass.  The last block of a sequence to end merges the parts' sorted lists, with
+// the beams' scores in 64 bits: fp32 would make ties of scores that differ.
+// (Which block that is changes nothing of the result.)
 //
 // Sums of exponentials are fp32, 17 additions a tile in a thread; the log sum,
 // whose whole powers of two are taken apart, and the scores are 64-bit.
@@ -33,6 +34,7 @@ constexpr int kThreads = 256;
 constexpr int kPer = 16;                       // values of a thread in a tile
 constexpr int kTile = kThreads * kPer;         // values of a tile
 constexpr int kListMax = 2048;                 // keys of the list
+constexpr int kSpare = 32;                     // of them beyond `width` before it is cut
 static_assert(kMaxWidth * kPer <= kListMax / 2, "a tile's candidates fit beside a list that was not cut yet");
 
 // Order of floats as unsigned numbers, +0 and -0 as one; 0 is below all.
@@ -167,11 +169,8 @@ __device__ uint64_t cut_list(int width, Lists& s) {
   for (int j = 0; j < 2; ++j) {
     const int i = threadIdx.x + j * kThreads;
     mine[j] = i < n ? s.list[i] : 0;
-  }
-  for (int i = 0; i < n; ++i) {
-    const uint64_t o = s.list[i];
-    rank[0] += o > mine[0];
-    rank[1] += o > mine[1];
+    if (i - (threadIdx.x & 31) >= n) continue;  // (the warp's)
+    for (int o = 0; o < n; ++o) rank[j] += s.list[o] > mine[j];
   }
   __syncthreads();
   if (threadIdx.x == 0) s.fill = min(n, width), s.threshold = 0;
@@ -187,11 +186,114 @@ __device__ uint64_t cut_list(int width, Lists& s) {
   return s.threshold;
 }
 
+__device__ __forceinline__ uint64_t ordered64(double x) {
+  const uint64_t b = static_cast<uint64_t>(__double_as_longlong(x + 0.0));
+  return b >> 63 ? ~b : b | 1ull << 63;
+}
+__device__ __forceinline__ double from_ordered64(uint64_t o) {
+  return __longlong_as_double(static_cast<long long>(o >> 63 ? o & ~(1ull << 63) : ~o));
+}
+
+constexpr int kMergeKeys = 2048;  // scores kept in shared memory
+constexpr int kMaxLists = kMaxBeams * kMaxParts;
+
+struct Merge {
+  double base[kMaxBeams];  // what a beam's candidates start from
+  uint64_t score[kMergeKeys];
+  uint32_t token[kMergeKeys];
+  unsigned char at[kMaxLists];
+};
+
+// A list is a part of a beam's row: list i is part i % parts of beam i / parts,
+// so that of equal scores the one from the lower list goes first.
+__device__ __forceinline__ void merge_beams(const BeamParams& p, int64_t seq, Merge& s) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const unsigned full = 0xffffffffu;
+  const int lists = p.beams * p.parts, first = min(p.width, kMergeKeys / lists);  // scores of a list that are kept
+  const unsigned long long* keys = p.keys + seq * lists * p.width;
+  for (int i = tid; i < lists; i += kThreads) s.at[i] = 0;
+  for (int b = warp; b < p.beams; b += kThreads / 32) {
+    const int64_t row = seq * p.beams + b;
+    const float2 ml = lane < p.parts ? __ldcg(p.sums + row * p.parts + lane) : make_float2(-INFINITY, 0.f);
+    const float score = __ldg(p.scores + row);
+    float top = ml.x;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(full, top, o));
+    float l = ml.x == -INFINITY && ml.y == 0.f ? 0.f : ml.y * ex2((ml.x - top) * kLog2e);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(full, l, o);
+    // log l = e log 2 + log m, 1 <= m < 2: the fp32 logarithm is small
+    const bool fine = l >= 0.5f && l < INFINITY && fabsf(top) < INFINITY && fabsf(score) < INFINITY;
+    const int e = static_cast<int>(__float_as_uint(l) >> 23) - 127;
+    const float m = __uint_as_float((__float_as_uint(l) & 0x007fffffu) | 0x3f800000u);
+    if (lane == 0)
+      s.base[b] = fine ? static_cast<double>(score) - static_cast<double>(top) - e * 0.69314718055994530942 - static_cast<double>(logf(m))
+                       : -INFINITY;
+  }
+  __syncthreads();
+  auto score_of = [&](int list, uint64_t key) -> uint64_t {
+    const double base = s.base[list / p.parts];
+    return key && base > -INFINITY ? ordered64(base + static_cast<double>(from_ordered(static_cast<uint32_t>(key >> 32)))) : 0;
+  };
+  for (int i = tid; i < lists * first; i += kThreads) {
+    const int list = i / first;
+    const uint64_t key = __ldcg(keys + static_cast<int64_t>(list) * p.width + i - list * first);
+    s.score[i] = score_of(list, key);
+    s.token[i] = 0xffffffffu - static_cast<uint32_t>(key);
+  }
+  __syncthreads();
+  if (warp != 0) return;
+  // rounds: each lane has the best of its lists (score, list, token)
+  uint64_t best = 0;
+  uint32_t token = 0;
+  int mine = 0;
+  auto look = [&] {
+    best = 0;
+    mine = 0x7fffffff;
+    for (int i = lane; i < lists; i += 32) {
+      const int at = s.at[i];
+      if (at >= p.width) continue;
+      uint64_t sc;
+      uint32_t tk;
+      if (at < first) {
+        sc = s.score[i * first + at], tk = s.token[i * first + at];
+      } else {
+        const uint64_t key = __ldcg(keys + static_cast<int64_t>(i) * p.width + at);
+        sc = score_of(i, key), tk = 0xffffffffu - static_cast<uint32_t>(key);
+      }
+      if (sc > best) best = sc, mine = i, token = tk;
+    }
+  };
+  look();
+  for (int i = 0; i < p.width; ++i) {
+    const uint32_t hi = static_cast<uint32_t>(best >> 32), top = __reduce_max_sync(full, hi);
+    const uint32_t lo = hi == top ? static_cast<uint32_t>(best) : 0, low = __reduce_max_sync(full, lo);
+    const bool have = hi == top && static_cast<uint32_t>(best) == low;
+    const int list = __reduce_min_sync(full, have ? mine : 0x7fffffff);
+    const int64_t to = seq * p.width + i;
+    if (top == 0) {  // (a score's pattern has high bits) no candidate is left
+      if (lane == 0) p.out_scores[to] = -INFINITY, p.out_beams[to] = -1, p.out_tokens[to] = -1;
+    } else if (have && mine == list) {
+      p.out_scores[to] = static_cast<float>(from_ordered64(best));
+      p.out_beams[to] = list / p.parts;
+      p.out_tokens[to] = static_cast<int32_t>(token);
+      ++s.at[list];
+      look();
+    }
+    __syncwarp();
+  }
+}
+
 template <typename T>
-__global__ void __launch_bounds__(kThreads) beam_row_kernel(const BeamParams p) {
-  __shared__ Lists s;
+__global__ void __launch_bounds__(kThreads, 4) beam_kernel(const BeamParams p) {
+  __shared__ union Shared {
+    Lists lists;
+    Merge merge;
+    __device__ Shared() {}
+  } shared;
   __shared__ float2 s_sum[kThreads / 32];
-  allow_next_kernel();
+  __shared__ bool s_last;
+  Lists& s = shared.lists;
   using Units = RowUnits<T>;
   constexpr int kVec = Units::kVec, kUnits = kPer / kVec;
   const int64_t row = blockIdx.x / p.parts;
@@ -217,25 +319,27 @@ __global__ void __launch_bounds__(kThreads) beam_row_kernel(const BeamParams p) 
     auto token = [&](int i) {
       return static_cast<uint32_t>(at + (static_cast<int64_t>(i / kVec) * kThreads + threadIdx.x) * kVec + i % kVec - units.lead);
     };
-    float top = x[0];
+    float top = fmaxf(x[0], x[1]);
 #pragma unroll
-    for (int i = 1; i < kPer; ++i) top = fmaxf(top, x[i]);
+    for (int i = 2; i < kPer; i += 2) top = fmaxf(top, fmaxf(x[i], x[i + 1]));
     const float mn = fmaxf(m, top), ref = mn == -INFINITY ? 0.f : mn;
-    float sum = 0.f;
+    const uint64_t less = pack2(-ref, -ref), scale = pack2(kLog2e, kLog2e);
+    uint64_t sum = pack2(0.f, 0.f);
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) sum += ex2((x[i] - ref) * kLog2e);
-    l = l * ex2((m - ref) * kLog2e) + sum;
+    for (int i = 0; i < kPer; i += 2) {
+      float u, v;
+      unpack2(mul2(add2(pack2(x[i], x[i + 1]), less), scale), u, v);
+      sum = add2(sum, pack2(ex2(u), ex2(v)));
+    }
+    float even, odd;
+    unpack2(sum, even, odd);
+    l = l * ex2((m - ref) * kLog2e) + (even + odd);
     m = mn;
 
     // candidates: values that the threshold's does not exceed
     const float low = threshold ? from_ordered(static_cast<uint32_t>(threshold >> 32)) : -INFINITY;
-    int mine = 0;
-    if (top >= low) {
-#pragma unroll
-      for (int i = 0; i < kPer; ++i) mine += key_of(x[i], token(i)) > threshold;
-    }
     const int fill = s.fill;  // read before any thread of this tile adds to it: the branches below are the block's
-    const int total = __syncthreads_count(mine > 0);
+    const int total = __syncthreads_count(top >= low);
     if (total == 0) continue;
     // (an upper bound: a thread has at most kPer)
     if (fill + total * kPer > kListMax) {
@@ -247,9 +351,10 @@ __global__ void __launch_bounds__(kThreads) beam_row_kernel(const BeamParams p) 
       if (th > threshold) threshold = th - 1;
       if (fill + p.width * kPer > kListMax) threshold = max(threshold, cut_list(p.width, s));
     }
-    if (mine) {
+    if (top >= low) {
 #pragma unroll
       for (int i = 0; i < kPer; ++i) {
+        if (!(x[i] >= low)) continue;
         const uint64_t k = key_of(x[i], token(i));
         if (k > threshold) {
           const int to = atomicAdd(&s.fill, 1);
@@ -258,10 +363,12 @@ __global__ void __launch_bounds__(kThreads) beam_row_kernel(const BeamParams p) 
       }
     }
     __syncthreads();
-    if (s.fill > 2 * kThreads) threshold = max(threshold, cut_list(p.width, s));
+    // A tight threshold keeps the tiles' candidates few, and a short list is cut
+    // quickly.
+    if (s.fill > p.width + kSpare) threshold = max(threshold, cut_list(p.width, s));
   }
   cut_list(p.width, s);
-  uint64_t* keys = p.keys + (row * p.parts + part) * p.width;
+  unsigned long long* keys = p.keys + (row * p.parts + part) * p.width;
   for (int i = threadIdx.x; i < p.width; i += kThreads) keys[i] = i < s.fill ? s.list[i] : 0;
 
   // the sums of the threads
@@ -281,104 +388,18 @@ __global__ void __launch_bounds__(kThreads) beam_row_kernel(const BeamParams p) 
     for (int w = 1; w < kThreads / 32; ++w) join(m, l, s_sum[w].x, s_sum[w].y);
     p.sums[row * p.parts + part] = make_float2(m, l);
   }
-}
-
-__device__ __forceinline__ uint64_t ordered64(double x) {
-  const uint64_t b = static_cast<uint64_t>(__double_as_longlong(x + 0.0));
-  return b >> 63 ? ~b : b | 1ull << 63;
-}
-__device__ __forceinline__ double from_ordered64(uint64_t o) {
-  return __longlong_as_double(static_cast<long long>(o >> 63 ? o & ~(1ull << 63) : ~o));
-}
-
-constexpr int kMergeThreads = 256;
-constexpr int kMergeKeys = 2048;                     // scores kept in shared memory
-constexpr int kMaxLists = kMaxBeams * kMaxParts;
-
-// A list is a part of a beam's row: list i is part i % parts of beam i / parts,
-// so that of equal scores the one from the lower list goes first.
-__global__ void __launch_bounds__(kMergeThreads) beam_merge_kernel(const BeamParams p) {
-  __shared__ double s_base[kMaxBeams];  // what a beam's candidates start from
-  __shared__ uint64_t s_score[kMergeKeys];
-  __shared__ uint32_t s_token[kMergeKeys];
-  __shared__ unsigned char s_at[kMaxLists];
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const unsigned full = 0xffffffffu;
-  const int64_t seq = blockIdx.x;
-  const int lists = p.beams * p.parts, first = min(p.width, kMergeKeys / lists);  // scores of a list that are kept
-  const uint64_t* keys = p.keys + seq * lists * p.width;
-  for (int i = tid; i < lists; i += kMergeThreads) s_at[i] = 0;
-  wait_for_last_kernel();
-  for (int b = warp; b < p.beams; b += kMergeThreads / 32) {
-    const int64_t row = seq * p.beams + b;
-    const float2 ml = lane < p.parts ? p.sums[row * p.parts + lane] : make_float2(-INFINITY, 0.f);
-    const float score = __ldg(p.scores + row);
-    float top = ml.x;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(full, top, o));
-    float l = ml.x == -INFINITY && ml.y == 0.f ? 0.f : ml.y * ex2((ml.x - top) * kLog2e);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(full, l, o);
-    // log l = e log 2 + log m, 1 <= m < 2: the fp32 logarithm is small
-    const bool fine = l >= 0.5f && l < INFINITY && fabsf(top) < INFINITY && fabsf(score) < INFINITY;
-    const int e = static_cast<int>(__float_as_uint(l) >> 23) - 127;
-    const float m = __uint_as_float((__float_as_uint(l) & 0x007fffffu) | 0x3f800000u);
-    if (lane == 0)
-      s_base[b] = fine ? static_cast<double>(score) - static_cast<double>(top) - e * 0.69314718055994530942 - static_cast<double>(logf(m))
-                       : -INFINITY;
+  // ---- the sequence's last block; the count is 0 again behind it
+  __threadfence();
+  __syncthreads();
+  const int64_t seq = row / p.beams;
+  if (threadIdx.x == 0) {
+    const unsigned blocks = static_cast<unsigned>(p.beams * p.parts);
+    s_last = atomicInc(p.arrived + seq, blocks - 1) == blocks - 1;
   }
   __syncthreads();
-  auto score_of = [&](int list, uint64_t key) -> uint64_t {
-    const double base = s_base[list / p.parts];
-    return key && base > -INFINITY ? ordered64(base + static_cast<double>(from_ordered(static_cast<uint32_t>(key >> 32)))) : 0;
-  };
-  for (int i = tid; i < lists * first; i += kMergeThreads) {
-    const int list = i / first;
-    const uint64_t key = keys[static_cast<int64_t>(list) * p.width + i - list * first];
-    s_score[i] = score_of(list, key);
-    s_token[i] = 0xffffffffu - static_cast<uint32_t>(key);
-  }
-  __syncthreads();
-  if (warp != 0) return;
-  // rounds: each lane has the best of its lists (score, list, token)
-  uint64_t best = 0;
-  uint32_t token = 0;
-  int mine = 0;
-  auto look = [&] {
-    best = 0;
-    mine = 0x7fffffff;
-    for (int i = lane; i < lists; i += 32) {
-      const int at = s_at[i];
-      if (at >= p.width) continue;
-      uint64_t sc;
-      uint32_t tk;
-      if (at < first) {
-        sc = s_score[i * first + at], tk = s_token[i * first + at];
-      } else {
-        const uint64_t key = keys[static_cast<int64_t>(i) * p.width + at];
-        sc = score_of(i, key), tk = 0xffffffffu - static_cast<uint32_t>(key);
-      }
-      if (sc > best) best = sc, mine = i, token = tk;
-    }
-  };
-  look();
-  for (int i = 0; i < p.width; ++i) {
-    const uint32_t hi = static_cast<uint32_t>(best >> 32), top = __reduce_max_sync(full, hi);
-    const uint32_t lo = hi == top ? static_cast<uint32_t>(best) : 0, low = __reduce_max_sync(full, lo);
-    const bool have = hi == top && static_cast<uint32_t>(best) == low;
-    const int list = __reduce_min_sync(full, have ? mine : 0x7fffffff);
-    const int64_t to = seq * p.width + i;
-    if (top == 0) {  // (a score's pattern has high bits) no candidate is left
-      if (lane == 0) p.out_scores[to] = -INFINITY, p.out_beams[to] = -1, p.out_tokens[to] = -1;
-    } else if (have && mine == list) {
-      p.out_scores[to] = static_cast<float>(from_ordered64(best));
-      p.out_beams[to] = list / p.parts;
-      p.out_tokens[to] = static_cast<int32_t>(token);
-      ++s_at[list];
-      look();
-    }
-    __syncwarp();
-  }
+  if (!s_last) return;
+  __threadfence();
+  merge_beams(p, seq, shared.merge);
 }
 
 }  // namespace
@@ -408,10 +429,11 @@ cudaError_t launch_beam(const BeamParams& given, int dtype, cudaStream_t s) {
     kernel<<<static_cast<unsigned>(grid), kThreads, 0, s>>>(p);
     return cudaGetLastError();
   };
-  const cudaError_t e = dtype == QGEMV_DT_F32 ? go(beam_row_kernel<float>)
-                        : dtype == QGEMV_DT_F16 ? go(beam_row_kernel<__half>) : go(beam_row_kernel<__nv_bfloat16>);
-  if (e != cudaSuccess) return e;
-  return launch_after(beam_merge_kernel, static_cast<unsigned>(p.n_seqs), p, s, kMergeThreads);
+  switch (dtype) {
+    case QGEMV_DT_F32: return go(beam_kernel<float>);
+    case QGEMV_DT_F16: return go(beam_kernel<__half>);
+    default: return go(beam_kernel<__nv_bfloat16>);
+  }
 }
 
 }  // namespace qgemv

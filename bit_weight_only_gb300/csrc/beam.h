@@ -11,8 +11,10 @@ namespace qgemv {
 constexpr int kMaxBeams = 64;   // of a sequence
 constexpr int kMaxWidth = 64;   // candidates kept of a sequence
 constexpr int kMaxParts = 32;   // parts of a row, each a block's
+constexpr int kMaxBeamSeqs = 4096;
 
-// Workspace: for each row and part the candidates' keys (uint64 [width],
+// Workspace: a count of arrivals for each of kMaxBeamSeqs sequences, 0 between
+// calls (in one place whatever the sizes of a call); for each row and part the candidates' keys (uint64 [width],
 // descending, 0: none), then the largest logit and the sum of exponentials.
 struct BeamParams {
   const void* logits;
@@ -23,8 +25,9 @@ struct BeamParams {
   float* out_scores;
   int32_t* out_beams;
   int32_t* out_tokens;
-  uint64_t* keys;   // [rows][parts][width]
-  float2* sums;     // [rows][parts]
+  unsigned* arrived;           // [kMaxBeamSeqs]
+  unsigned long long* keys;    // [rows][parts][width]
+  float2* sums;                // [rows][parts]
   int parts;
   int tiles;        // of a part, at most
 };

@@ -8,7 +8,7 @@ namespace {
 using namespace qgemv;
 
 bool beam_sizes_ok(int64_t n_seqs, int beams, int64_t vocab, int width) {
-  return n_seqs >= 0 && n_seqs <= (1 << 20) && beams >= 1 && beams <= kMaxBeams && vocab >= 1 &&
+  return n_seqs >= 0 && n_seqs <= kMaxBeamSeqs && beams >= 1 && beams <= kMaxBeams && vocab >= 1 &&
          vocab <= (int64_t(1) << 30) && width >= 1 && width <= kMaxWidth;
 }
 
@@ -19,7 +19,7 @@ extern "C" {
 int64_t qgemv_beam_ws_bytes(int64_t n_seqs, int beams, int64_t vocab, int width) {
   if (!beam_sizes_ok(n_seqs, beams, vocab, width)) return 0;
   const int64_t rows = (n_seqs > 0 ? n_seqs : 1) * beams;
-  return rows * beam_parts(1, vocab, 1 << 20) * (8 * static_cast<int64_t>(width) + 8);
+  return 4 * kMaxBeamSeqs + rows * beam_parts(1, vocab, 1 << 20) * (8 * static_cast<int64_t>(width) + 8);
 }
 
 int qgemv_beam_select(int dtype, const void* logits, int64_t row_stride, int64_t vocab, const float* scores, int64_t n_seqs,
@@ -28,8 +28,8 @@ int qgemv_beam_select(int dtype, const void* logits, int64_t row_stride, int64_t
   const int size = dtype_size(dtype);
   if (size == 0) return fail(QGEMV_ERR_ARG, "unknown dtype %d", dtype);
   if (!beam_sizes_ok(n_seqs, beams, vocab, width))
-    return fail(QGEMV_ERR_ARG, "%lld sequences of %d beams, %lld tokens, %d kept: at most 2^20 of %d, 2^30 and %d",
-                (long long)n_seqs, beams, (long long)vocab, width, kMaxBeams, kMaxWidth);
+    return fail(QGEMV_ERR_ARG, "%lld sequences of %d beams, %lld tokens, %d kept: at most %d of %d, 2^30 and %d",
+                (long long)n_seqs, beams, (long long)vocab, width, kMaxBeamSeqs, kMaxBeams, kMaxWidth);
   if (n_seqs == 0) return report_error(QGEMV_OK, "");
   if (row_stride < 0 || row_stride > (int64_t(1) << 38)) return fail(QGEMV_ERR_ARG, "row_stride outside [0, 2^38]");
   if (!logits || !scores || !out_scores || !out_beams || !out_tokens || !ws) return fail(QGEMV_ERR_ARG, "an argument is NULL");
@@ -52,7 +52,8 @@ int qgemv_beam_select(int dtype, const void* logits, int64_t row_stride, int64_t
   p.out_scores = out_scores;
   p.out_beams = out_beams;
   p.out_tokens = out_tokens;
-  p.keys = static_cast<uint64_t*>(ws);
+  p.arrived = static_cast<unsigned*>(ws);
+  p.keys = reinterpret_cast<unsigned long long*>(static_cast<uint8_t*>(ws) + 4 * kMaxBeamSeqs);
   return done(launch_beam(p, dtype, static_cast<cudaStream_t>(stream)), "launching the selection");
 }
 

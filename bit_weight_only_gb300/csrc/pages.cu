@@ -58,10 +58,10 @@ struct Counts {
   __device__ void load(const int32_t* refs, int64_t n_pages, int64_t at) {
     if (at + kPer <= n_pages && (reinterpret_cast<uintptr_t>(refs) & 15) == 0) {
 #pragma unroll
-      for (int i = 0; i < kPer; i += 4) *reinterpret_cast<int4*>(v + i) = *reinterpret_cast<const int4*>(refs + at + i);
+      for (int i = 0; i < kPer; i += 4) *reinterpret_cast<int4*>(v + i) = __ldcg(reinterpret_cast<const int4*>(refs + at + i));
     } else {
 #pragma unroll
-      for (int i = 0; i < kPer; ++i) v[i] = at + i < n_pages ? refs[at + i] : 1;
+      for (int i = 0; i < kPer; ++i) v[i] = at + i < n_pages ? __ldcg(refs + at + i) : 1;
     }
   }
 };
@@ -69,16 +69,16 @@ struct Counts {
 // The lowest free pages, `want` of them where there are as many: give(rank,
 // page), each by some thread of the block; `c` has the first step's counts.
 // Returns how many there were.
-template <typename F>
+template <int THREADS, typename F>
 __device__ int free_pages(const int32_t* refs, int64_t n_pages, int want, Counts<kGivePer>& c, int* s_warp, F give) {
   int got = 0;
-  for (int64_t p0 = 0; p0 < n_pages && got < want; p0 += kGive * kGivePer) {
+  for (int64_t p0 = 0; p0 < n_pages && got < want; p0 += THREADS * kGivePer) {
     const int64_t mine = p0 + static_cast<int64_t>(threadIdx.x) * kGivePer;
     if (p0 > 0) c.load(refs, n_pages, mine);
     int n = 0, total;
 #pragma unroll
     for (int i = 0; i < kGivePer; ++i) n += c.v[i] <= 0;
-    int rank = got + block_sum<kGive>(n, s_warp, total) - n;
+    int rank = got + block_sum<THREADS>(n, s_warp, total) - n;
 #pragma unroll
     for (int i = 0; i < kGivePer; ++i) {
       if (c.v[i] <= 0) {
@@ -126,30 +126,35 @@ __global__ void __launch_bounds__(kGive) reserve_kernel(const PoolParams p) {
     }
     return p.table + lo * p.table_stride + pages_for(p.from[lo], p.page_tokens) + rank - (lo > 0 ? s_upto[lo - 1] : 0);
   };
-  const int got = free_pages(p.refs, p.n_pages, static_cast<int>(want), counts, s_warp, [&](int rank, int32_t page) {
+  const int got = free_pages<kGive>(p.refs, p.n_pages, static_cast<int>(want), counts, s_warp, [&](int rank, int32_t page) {
     *place(rank) = page;
     p.refs[page] = 1;
   });
   for (int64_t r = got + static_cast<int64_t>(threadIdx.x); r < want; r += kGive) *place(static_cast<int>(r)) = -1;
-  if (threadIdx.x == 0 && got < want) *p.missing += static_cast<int>(want - got);
+  if (threadIdx.x == 0 && got < want) p.state[0] += static_cast<int>(want - got);
 }
 
 // ---- fork: a block for each old row (its pages' counts, its children's
-// copies) and each new one (its entries)
-__global__ void __launch_bounds__(kRowThreads) fork_rows_kernel(const PoolParams p) {
+// copies) and each new one (its entries); the last one to end gives the copies
+// their pages.
+constexpr int kForkThreads = 512;
+
+__global__ void __launch_bounds__(kForkThreads) fork_kernel(const PoolParams p) {
+  __shared__ int s_warp[32];
   __shared__ int s_kids, s_first;
-  allow_next_kernel();
+  __shared__ bool s_last;
+  extern __shared__ int2 s_rows[];  // (row, entry) of the rows that get a copy
   if (blockIdx.x < p.n_old) {
     const int64_t b = blockIdx.x;
     if (threadIdx.x == 0) s_kids = 0, s_first = 0x7fffffff;
     __syncthreads();
-    for (int64_t r = threadIdx.x; r < p.n_seqs; r += kRowThreads)
+    for (int64_t r = threadIdx.x; r < p.n_seqs; r += kForkThreads)
       if (p.parents[r] == b) atomicAdd(&s_kids, 1), atomicMin(&s_first, static_cast<int>(r));
     __syncthreads();
     const int kids = s_kids, len = max(p.from[b], 0), rest = len % p.page_tokens;
     const int64_t used = pages_for(len, p.page_tokens), here = min(used, p.old_stride);
     const int32_t* row = p.old_table + b * p.old_stride;
-    for (int64_t e = threadIdx.x; e < here; e += kRowThreads) {
+    for (int64_t e = threadIdx.x; e < here; e += kForkThreads) {
       const int32_t page = row[e];
       // the page that is filled in part stays with the first child alone
       const int change = (rest && e == used - 1 ? min(kids, 1) : kids) - 1;
@@ -157,11 +162,11 @@ __global__ void __launch_bounds__(kRowThreads) fork_rows_kernel(const PoolParams
     }
     const int32_t last = rest && used <= p.old_stride ? row[used - 1] : -1;
     const bool copies = last >= 0 && last < p.n_pages;
-    for (int64_t r = threadIdx.x; r < p.n_seqs; r += kRowThreads) {
+    for (int64_t r = threadIdx.x; r < p.n_seqs; r += kForkThreads) {
       if (p.parents[r] != b) continue;
       const bool copy = copies && r != s_first;
       p.src[r] = copy ? last : -1;
-      p.dst[r] = copy ? static_cast<int32_t>(used - 1) : -1;  // its entry, for the kernel that gives the page
+      p.dst[r] = copy ? static_cast<int32_t>(used - 1) : -1;  // its entry, for the block that gives the page
       p.tokens[r] = copy ? rest : 0;
     }
   } else {
@@ -170,24 +175,24 @@ __global__ void __launch_bounds__(kRowThreads) fork_rows_kernel(const PoolParams
     const bool there = b >= 0 && b < p.n_old;
     if (!there && threadIdx.x == 0) p.src[r] = p.dst[r] = -1, p.tokens[r] = 0;
     const int64_t used = there ? min(pages_for(p.from[b], p.page_tokens), p.old_stride) : 0;
-    for (int64_t e = threadIdx.x; e < p.table_stride; e += kRowThreads)
+    for (int64_t e = threadIdx.x; e < p.table_stride; e += kForkThreads)
       p.table[r * p.table_stride + e] = e < used ? p.old_table[b * p.old_stride + e] : -1;
   }
-}
-
-// The copies' pages: one block.
-__global__ void __launch_bounds__(kGive) fork_copies_kernel(const PoolParams p) {
-  __shared__ int s_warp[32];
-  extern __shared__ int2 s_rows[];  // (row, entry) of the rows that get a copy
-  wait_for_last_kernel();
+  // ---- the last block; the count of arrivals is 0 again behind it
+  __threadfence();
+  __syncthreads();
+  if (threadIdx.x == 0) s_last = atomicInc(reinterpret_cast<unsigned*>(p.state) + 1, gridDim.x - 1) == gridDim.x - 1;
+  __syncthreads();
+  if (!s_last) return;
+  __threadfence();
   Counts<kGivePer> counts;
   counts.load(p.refs, p.n_pages, static_cast<int64_t>(threadIdx.x) * kGivePer);
   int want = 0;
-  for (int64_t r0 = 0; r0 < p.n_seqs; r0 += kGive) {
+  for (int64_t r0 = 0; r0 < p.n_seqs; r0 += kForkThreads) {
     const int64_t r = r0 + threadIdx.x;
-    const int entry = r < p.n_seqs ? p.dst[r] : -1;
+    const int entry = r < p.n_seqs ? __ldcg(p.dst + r) : -1;
     int total;
-    const int at = want + block_sum<kGive>(entry >= 0, s_warp, total) - 1;
+    const int at = want + block_sum<kForkThreads>(entry >= 0, s_warp, total) - 1;
     if (entry >= 0) s_rows[at] = make_int2(static_cast<int>(r), entry);
     want += total;
   }
@@ -198,9 +203,9 @@ __global__ void __launch_bounds__(kGive) fork_copies_kernel(const PoolParams p) 
     p.table[r.x * p.table_stride + r.y] = page;
     if (page >= 0) p.refs[page] = 1;
   };
-  const int got = free_pages(p.refs, p.n_pages, want, counts, s_warp, give);
-  for (int i = got + threadIdx.x; i < want; i += kGive) give(i, -1);
-  if (threadIdx.x == 0 && got < want) *p.missing += want - got;
+  const int got = free_pages<kForkThreads>(p.refs, p.n_pages, want, counts, s_warp, give);
+  for (int i = got + threadIdx.x; i < want; i += kForkThreads) give(i, -1);
+  if (threadIdx.x == 0 && got < want) p.state[0] += want - got;
 }
 
 // ---- release: a block for each row
@@ -406,9 +411,8 @@ cudaError_t launch_pool_reserve(const PoolParams& p, cudaStream_t s) {
 }
 
 cudaError_t launch_pool_fork(const PoolParams& p, cudaStream_t s) {
-  fork_rows_kernel<<<static_cast<unsigned>(p.n_old + p.n_seqs), kRowThreads, 0, s>>>(p);
-  const cudaError_t e = cudaGetLastError();
-  return e != cudaSuccess ? e : launch_after(fork_copies_kernel, 1, p, s, kGive, static_cast<int>(p.n_seqs) * 8);
+  fork_kernel<<<static_cast<unsigned>(p.n_old + p.n_seqs), kForkThreads, static_cast<unsigned>(p.n_seqs) * 8, s>>>(p);
+  return cudaGetLastError();
 }
 
 cudaError_t launch_pool_release(const PoolParams& p, cudaStream_t s) {

@@ -20,7 +20,7 @@ struct PoolParams {
   int64_t table_stride, n_seqs;
   const int32_t* from;  // reserve: have; fork: lens; release: keep (may be NULL)
   const int32_t* to;    // reserve: need; release: lens
-  int32_t* missing;
+  int32_t* state;       // pages that were missing; arrivals, 0 between calls
   // fork
   const int32_t* old_table;
   int64_t old_stride, n_old;

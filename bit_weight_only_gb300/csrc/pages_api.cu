@@ -44,29 +44,29 @@ PoolParams pool(int32_t* refs, int64_t n_pages, int page_tokens, int32_t* table,
 extern "C" {
 
 int qgemv_pool_reserve(int32_t* refs, int64_t n_pages, int page_tokens, int32_t* table, int64_t table_stride, int64_t n_seqs,
-                       const int32_t* have, const int32_t* need, int32_t* missing, void* stream) {
+                       const int32_t* have, const int32_t* need, int32_t* state, void* stream) {
   QG_TRY(check_pool(refs, n_pages, page_tokens, table_stride, n_seqs));
   if (n_seqs == 0 || table_stride == 0) return report_error(QGEMV_OK, "");
-  if (!table || !have || !need || !missing) return fail(QGEMV_ERR_ARG, "table, have, need or missing is NULL");
-  if (!aligned4({table, have, need, missing})) return fail(QGEMV_ERR_ALIGN, "arrays must be 4-byte aligned");
+  if (!table || !have || !need || !state) return fail(QGEMV_ERR_ARG, "table, have, need or state is NULL");
+  if (!aligned4({table, have, need, state})) return fail(QGEMV_ERR_ALIGN, "arrays must be 4-byte aligned");
   PoolParams p = pool(refs, n_pages, page_tokens, table, table_stride, n_seqs);
   p.from = have;
   p.to = need;
-  p.missing = missing;
+  p.state = state;
   return done(launch_pool_reserve(p, static_cast<cudaStream_t>(stream)), "launching the reservation");
 }
 
 int qgemv_pool_fork(int32_t* refs, int64_t n_pages, int page_tokens, const int32_t* table, int64_t table_stride, int64_t n_rows,
                     const int32_t* parents, int64_t n_new, const int32_t* lens, int32_t* new_table, int32_t* src, int32_t* dst,
-                    int32_t* tokens, int32_t* missing, void* stream) {
+                    int32_t* tokens, int32_t* state, void* stream) {
   QG_TRY(check_pool(refs, n_pages, page_tokens, table_stride, n_rows));
   QG_TRY(check_pool(refs, n_pages, page_tokens, table_stride, n_new));
   if (n_rows == 0 && n_new == 0) return report_error(QGEMV_OK, "");
   if (n_rows > 0 && ((!table && table_stride > 0) || !lens)) return fail(QGEMV_ERR_ARG, "table or lens is NULL");
   if (n_new > 0 && (!parents || (!new_table && table_stride > 0) || !src || !dst || !tokens))
     return fail(QGEMV_ERR_ARG, "parents, new_table, src, dst or tokens is NULL");
-  if (!missing) return fail(QGEMV_ERR_ARG, "missing is NULL");
-  if (!aligned4({table, parents, lens, new_table, src, dst, tokens, missing})) return fail(QGEMV_ERR_ALIGN, "arrays must be 4-byte aligned");
+  if (!state) return fail(QGEMV_ERR_ARG, "state is NULL");
+  if (!aligned4({table, parents, lens, new_table, src, dst, tokens, state})) return fail(QGEMV_ERR_ALIGN, "arrays must be 4-byte aligned");
   if (new_table && new_table < table + n_rows * table_stride && table < new_table + n_new * table_stride)
     return fail(QGEMV_ERR_ARG, "the new table overlaps the old one");
   PoolParams p = pool(refs, n_pages, page_tokens, new_table, table_stride, n_new);
@@ -77,7 +77,7 @@ int qgemv_pool_fork(int32_t* refs, int64_t n_pages, int page_tokens, const int32
   p.src = src;
   p.dst = dst;
   p.tokens = tokens;
-  p.missing = missing;
+  p.state = state;
   return done(launch_pool_fork(p, static_cast<cudaStream_t>(stream)), "launching the fork");
 }
 

@@ -349,15 +349,15 @@ def qgemv_beam_select(dtype: int, logits: int, row_stride: int, vocab: int, scor
 
 
 def qgemv_pool_reserve(refs: int, n_pages: int, page_tokens: int, table: int, table_stride: int, n_seqs: int, have: int,
-                       need: int, missing: int, stream=None) -> int:
-    return _check(load().qgemv_pool_reserve(refs, n_pages, page_tokens, table, table_stride, n_seqs, have, need, missing,
+                       need: int, state: int, stream=None) -> int:
+    return _check(load().qgemv_pool_reserve(refs, n_pages, page_tokens, table, table_stride, n_seqs, have, need, state,
                                             _stream_ptr(stream)))
 
 
 def qgemv_pool_fork(refs: int, n_pages: int, page_tokens: int, table: int, table_stride: int, n_rows: int, parents: int,
-                    n_new: int, lens: int, new_table: int, src: int, dst: int, tokens: int, missing: int, stream=None) -> int:
+                    n_new: int, lens: int, new_table: int, src: int, dst: int, tokens: int, state: int, stream=None) -> int:
     return _check(load().qgemv_pool_fork(refs, n_pages, page_tokens, table, table_stride, n_rows, parents, n_new, lens,
-                                         new_table, src, dst, tokens, missing, _stream_ptr(stream)))
+                                         new_table, src, dst, tokens, state, _stream_ptr(stream)))
 
 
 def qgemv_pool_release(refs: int, n_pages: int, page_tokens: int, table: int, table_stride: int, n_seqs: int, lens: int,
@@ -990,24 +990,21 @@ class PagePool:
         _gpu("a pool", device)
         self.n_pages, self.page_tokens, self._nbytes = n_pages, page_tokens, nbytes
         self.refs = torch.zeros(n_pages, dtype=torch.int32, device=device)
-        self._missing = torch.zeros(1, dtype=torch.int32, device=device)
+        self._state = torch.zeros(2, dtype=torch.int32, device=device)  # pages that were missing; the calls' own
         self._ws = torch.empty(nbytes // 4, dtype=torch.int32, device=device)
-        self._dev = self.refs.get_device()
+        self._dev, self.device = self.refs.get_device(), self.refs.device
         torch.cuda.current_stream(self._dev).synchronize()  # any stream may use it first
 
-    def _table(self, table):
-        rows, stride = table.shape
-        return _index("table", table, _torch().int32, (rows, stride), self._dev), stride, rows
-
-    def _ints(self, name, t, n):
-        return _index(name, t, _torch().int32, (n,), self._dev)
+    def _ints(self, name, t, *shape):
+        return _index(name, t, _torch().int32, shape, self._dev)
 
     def reserve(self, table, have, need, stream=None):
         """Give row b, which holds have[b] tokens, the pages for need[b]; the
         table's entries are filled in place."""
-        ptr, stride, rows = self._table(table)
-        _call(self._dev, _lib.qgemv_pool_reserve, self.refs.data_ptr(), self.n_pages, self.page_tokens, ptr, stride, rows,
-              self._ints("have", have, rows), self._ints("need", need, rows), self._missing.data_ptr(), _on(stream, self._dev))
+        rows, stride = table.shape
+        _call(self._dev, _lib.qgemv_pool_reserve, self.refs.data_ptr(), self.n_pages, self.page_tokens,
+              self._ints("table", table, rows, stride), stride, rows, self._ints("have", have, rows),
+              self._ints("need", need, rows), self._state.data_ptr(), _on(stream, self._dev))
 
     def fork(self, table, parents, lens, stream=None):
         """Replace the rows of table (lens tokens each) by new ones, row r what
@@ -1016,48 +1013,51 @@ class PagePool:
         that a row has filled in part stays with its first child, the others
         get one each, and ``copy_pages(src, dst, tokens)`` of every cache
         copies its tokens."""
-        ptr, stride, rows = self._table(table)
         torch, dev = _torch(), self._dev
+        rows, stride = table.shape
         n, = parents.shape
         empty = torch.empty if stream is None else _empty_on(stream, dev)
-        new = empty((n, stride), dtype=torch.int32, device=table.device)
-        src, dst, tokens = (empty((n,), dtype=torch.int32, device=table.device) for _ in range(3))
-        _call(dev, _lib.qgemv_pool_fork, self.refs.data_ptr(), self.n_pages, self.page_tokens, ptr, stride, rows,
-              self._ints("parents", parents, n), n, self._ints("lens", lens, rows), new.data_ptr(), src.data_ptr(),
-              dst.data_ptr(), tokens.data_ptr(), self._missing.data_ptr(), _on(stream, dev))
+        new = empty((n, stride), dtype=torch.int32, device=self.device)
+        src, dst, tokens = (empty((n,), dtype=torch.int32, device=self.device) for _ in range(3))
+        _call(dev, _lib.qgemv_pool_fork, self.refs.data_ptr(), self.n_pages, self.page_tokens,
+              self._ints("table", table, rows, stride), stride, rows, self._ints("parents", parents, n), n,
+              self._ints("lens", lens, rows), new.data_ptr(), src.data_ptr(), dst.data_ptr(), tokens.data_ptr(),
+              self._state.data_ptr(), _on(stream, dev))
         return new, src, dst, tokens
 
     def release(self, table, lens, keep=None, stream=None):
         """Take back the pages of row b's tokens keep[b] .. lens[b] (all of
         them unless keep is given) that no kept token is in; their entries
-        become -1."""
-        ptr, stride, rows = self._table(table)
-        _call(self._dev, _lib.qgemv_pool_release, self.refs.data_ptr(), self.n_pages, self.page_tokens, ptr, stride, rows,
-              self._ints("lens", lens, rows), None if keep is None else self._ints("keep", keep, rows), _on(stream, self._dev))
+        become -1.  (A page that is kept in part is still shared with the rows
+        that hold it.)"""
+        rows, stride = table.shape
+        _call(self._dev, _lib.qgemv_pool_release, self.refs.data_ptr(), self.n_pages, self.page_tokens,
+              self._ints("table", table, rows, stride), stride, rows, self._ints("lens", lens, rows),
+              None if keep is None else self._ints("keep", keep, rows), _on(stream, self._dev))
 
     def compact(self, table, out=None, stream=None):
         """Move the pages in use to the lowest numbers.  Returns (new table,
         src, dst): the moves, for ``copy_pages`` of every cache, end with -1.
         The table holds every row that is in use; out may be table itself."""
-        ptr, stride, rows = self._table(table)
         torch, dev = _torch(), self._dev
+        rows, stride = table.shape
         empty = torch.empty if stream is None else _empty_on(stream, dev)
         n = self.n_pages // 2
         if out is None:
-            out = empty((rows, stride), dtype=torch.int32, device=table.device)
-        src, dst = (empty((n,), dtype=torch.int32, device=table.device) for _ in range(2))
-        _call(dev, _lib.qgemv_pool_compact, self.refs.data_ptr(), self.n_pages, ptr, stride, rows,
-              _index("out", out, torch.int32, (rows, stride), dev), src.data_ptr(), dst.data_ptr(), n, self._ws.data_ptr(),
-              self._nbytes, _on(stream, dev))
+            out = empty((rows, stride), dtype=torch.int32, device=self.device)
+        src, dst = empty((n,), dtype=torch.int32, device=self.device), empty((n,), dtype=torch.int32, device=self.device)
+        _call(dev, _lib.qgemv_pool_compact, self.refs.data_ptr(), self.n_pages, self._ints("table", table, rows, stride), stride,
+              rows, self._ints("out", out, rows, stride), src.data_ptr(), dst.data_ptr(), n, self._ws.data_ptr(), self._nbytes,
+              _on(stream, dev))
         return out, src, dst
 
     def status(self):
         """Synchronise; raises if pages ran out since the last call."""
         torch = _torch()
         torch.cuda.synchronize(self._dev)
-        n = int(self._missing.item())
+        n = int(self._state[0].item())
         if n:
-            self._missing.zero_()
+            self._state[0] = 0
             torch.cuda.synchronize(self._dev)
             raise QgemvError(QGEMV_ERR_NOMEM, f"{n} pages were not there to give")
 
@@ -1099,7 +1099,8 @@ def attn_prompt(q, k, v, cu_q, cu_k, *, max_q: int, workspace, scale=None, out=N
 
 class BeamWorkspace:
     """Workspace of ``beam_select`` for up to n_seqs sequences of these sizes,
-    reused by any number of calls, one at a time."""
+    reused by any number of calls, one at a time (calls that overlap on several
+    streams need one each)."""
 
     def __init__(self, n_seqs: int, beams: int, vocab: int, width: int, device="cuda"):
         import torch
@@ -1107,8 +1108,9 @@ class BeamWorkspace:
         if self.nbytes == 0:
             raise QgemvError(QGEMV_ERR_ARG, f"no workspace for {n_seqs} sequences of {beams} beams, {vocab} tokens, {width} kept")
         _gpu("a workspace", device)
-        self.buffer = torch.empty(self.nbytes, dtype=torch.uint8, device=device)
+        self.buffer = torch.zeros(self.nbytes, dtype=torch.uint8, device=device)
         self.ptr, self._dev = self.buffer.data_ptr(), self.buffer.get_device()
+        torch.cuda.current_stream(self._dev).synchronize()  # any stream may use it first
 
 
 def beam_select(logits, scores, width: int, *, workspace, out=None, stream=None):
@@ -1127,14 +1129,15 @@ def beam_select(logits, scores, width: int, *, workspace, out=None, stream=None)
                          f"strides {strides} on {logits.device}")
     if workspace._dev != dev:
         _elsewhere(workspace, dev)
-    got = n_seqs, width
     if out is None:
         empty = torch.empty if stream is None else _empty_on(stream, dev)
-        out = (empty(got, dtype=torch.float32, device=logits.device), empty(got, dtype=torch.int32, device=logits.device),
-               empty(got, dtype=torch.int32, device=logits.device))
-        to = out[0].data_ptr(), out[1].data_ptr(), out[2].data_ptr()
+        best = empty((n_seqs, width), dtype=torch.float32, device=logits.device)
+        parents = empty((n_seqs, width), dtype=torch.int32, device=logits.device)
+        tokens = empty((n_seqs, width), dtype=torch.int32, device=logits.device)
+        out, to = (best, parents, tokens), (best.data_ptr(), parents.data_ptr(), tokens.data_ptr())
     else:
-        to = tuple(_index(f"out[{i}]", t, kind, got, dev) for i, (t, kind) in enumerate(zip(out, (torch.float32, torch.int32, torch.int32))))
+        to = tuple(_index(f"out[{i}]", t, kind, (n_seqs, width), dev)
+                   for i, (t, kind) in enumerate(zip(out, (torch.float32, torch.int32, torch.int32))))
     _call(dev, _lib.qgemv_beam_select, _dtype_code(logits.dtype), logits.data_ptr(), strides[0] if shape[0] > 1 else shape[1],
           shape[1], _index("scores", scores, torch.float32, (n_seqs, beams), dev), n_seqs, beams, width, *to, workspace.ptr,
           workspace.nbytes, _on(stream, dev))

@@ -556,8 +556,10 @@ int qgemv_kv_write_rotated(const qgemv_kv_cache* cache, const void* plan, int pa
  * is not (a NaN or +infinity among its logits, or nothing but -infinity), has
  * no candidates, nor have tokens of -infinity; places for which there is no
  * candidate hold (-infinity, -1, -1).  The sums of exponentials are fp32, log sums and scores
- * are compared in 64 bits and rounded once.  beams and width are at most 64.
- * ws: qgemv_beam_ws_bytes bytes, 16-byte aligned, no setting up; calls that
+ * are compared in 64 bits and rounded once.  beams and width are at most 64,
+ * sequences 4096 a call.
+ * ws: qgemv_beam_ws_bytes bytes, 16-byte aligned, zeroed once by the caller and then
+ * reused by calls of any sizes that it is large enough for; calls that
  * overlap on the GPU need one each.  Asynchronous on `stream`, no allocation,
  * can be captured in a CUDA graph; bitwise reproducible.                     */
 int64_t qgemv_beam_ws_bytes(int64_t n_seqs, int beams, int64_t vocab, int width);
@@ -570,20 +572,21 @@ int qgemv_beam_select(int dtype, const void* logits, int64_t row_stride, int64_t
  * A pool's bookkeeping of pages, for any number of caches with the same
  * numbers of pages and tokens (a cache a layer, one page table): refs, device int32
  * [n_pages], counts the rows of page tables that hold a page; pages of count
- * 0 (or less) are free.  The caller zeroes it once.  Tables are device int32
+ * 0 (or less) are free.  state is device int32 [2].  The caller zeroes both
+ * once.  Tables are device int32
  * [rows][table_stride], lengths device int32 in tokens; a row of length n
  * holds the pages of its first ceil(n / page_tokens) entries.  Entries that
  * are no page's number are passed over.  Free pages are given out lowest
  * first, in the order of the rows, so results depend on the inputs alone.
- * Where there are none left, the entry becomes -1 and *missing (device int32)
- * counts it.  At most 4096 rows of 2^20 entries a call; calls of one pool
+ * Where there are none left, the entry becomes -1 and state[0] counts it
+ * (state[1] is the calls' own, 0 between them).  At most 4096 rows of 2^20 entries a call; calls of one pool
  * one at a time.  All are asynchronous on `stream`, allocate nothing, can be
- * captured in a CUDA graph, and leave refs the only state.
+ * captured in a CUDA graph.
  *
  * reserve: row b, which holds have[b] tokens, gets the pages that need[b]
  * tokens take beyond them.                                                   */
 int qgemv_pool_reserve(int32_t* refs, int64_t n_pages, int page_tokens, int32_t* table, int64_t table_stride, int64_t n_seqs,
-                       const int32_t* have, const int32_t* need, int32_t* missing, void* stream);
+                       const int32_t* have, const int32_t* need, int32_t* state, void* stream);
 
 /* fork (a step of beam search): the rows are replaced by n_new new ones, row
  * r of new_table (same table_stride; no overlap with table) what row
@@ -598,7 +601,7 @@ int qgemv_pool_reserve(int32_t* refs, int64_t n_pages, int page_tokens, int32_t*
  * length become -1 and are not counted.                                      */
 int qgemv_pool_fork(int32_t* refs, int64_t n_pages, int page_tokens, const int32_t* table, int64_t table_stride, int64_t n_rows,
                     const int32_t* parents, int64_t n_new, const int32_t* lens, int32_t* new_table, int32_t* src, int32_t* dst,
-                    int32_t* tokens, int32_t* missing, void* stream);
+                    int32_t* tokens, int32_t* state, void* stream);
 
 /* release: row b, of lens[b] tokens, keeps the pages of its first keep[b]
  * tokens (none where keep is NULL); the others' counts go down by one and

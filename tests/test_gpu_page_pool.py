@@ -91,7 +91,7 @@ class Plain:
 
 
 def same(pool, plain):
-    assert pool.refs.tolist() == plain.refs and int(pool._missing) == plain.missing
+    assert pool.refs.tolist() == plain.refs and int(pool._state[0]) == plain.missing
 
 
 @pytest.mark.parametrize("n_pages, page, rows, width, seed", [(40, 16, 3, 9, 0), (300, 64, 17, 12, 1), (5000, 16, 64, 40, 2),

@@ -33,7 +33,7 @@ def rotary(device="cuda:1", head_dim=64):
 def pool(device="cuda:1"):
     p = qgemv.PagePool.__new__(qgemv.PagePool)
     p.n_pages, p.page_tokens, p._nbytes, p._dev = 9, 16, 4096, torch.device(device).index
-    p.refs = p._missing = p._ws = Stand((9,), I32, device=device)
+    p.refs = p._state = p._ws = Stand((9,), I32, device=device)
     return p
 
 
