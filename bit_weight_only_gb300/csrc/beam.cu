@@ -8,10 +8,12 @@
 // of exponentials, and whatever passes the part's threshold goes to a list in
 // shared memory.  Of one row the order of the candidates is that of its logits
 // (ties: the lower token first), so a candidate is a 64-bit key, value above
-// inverted token, and no two are equal.  The threshold is the `width`-th
-// largest of the threads' maxima when a tile would overflow the list (that
-// many keys at least reach it, and at most `width` threads' values do) and the
-// list's own `width`-th key once it was cut; after the first tile few values
+// inverted token, and no two are equal.  The threshold is the list's
+// `width`-th key, taken anew when the list has grown a little; for the first
+// tile, a value that each warp has width / 8 threads at.  The block meets once
+// in four tiles.  Where their candidates overflow the list (values that rise
+// along the row) they are taken again tile by tile, behind the `width`-th
+// largest of the threads' maxima, which at most `width` threads' values
 // pass.  The last block of a sequence to end merges the parts' sorted lists, with
 // the beams' scores in 64 bits: fp32 would make ties of scores that differ.
 // (Which block that is changes nothing of the result.)
@@ -35,7 +37,8 @@ constexpr int kPer = 16;                       // values of a thread in a tile
 constexpr int kTile = kThreads * kPer;         // values of a tile
 constexpr int kListMax = 2048;                 // keys of the list
 constexpr int kSpare = 32;                     // of them beyond `width` before it is cut
-static_assert(kMaxWidth * kPer <= kListMax / 2, "a tile's candidates fit beside a list that was not cut yet");
+constexpr int kGroup = 4;                      // tiles between the block's meetings
+static_assert(kMaxWidth * kPer <= kListMax / 2, "a tile's candidates fit beside half a list");
 
 // Order of floats as unsigned numbers, +0 and -0 as one; 0 is below all.
 __device__ __forceinline__ uint32_t ordered(float x) {
@@ -102,6 +105,8 @@ struct Lists {
   uint64_t sorted[kThreads];  // the warps' maxima, each warp's in order
   uint64_t threshold;
   int fill;
+  int added[3];               // keys that a group of tiles added; two groups on, 0 again
+  float warp_low[kThreads / 32];
 };
 
 // The k-th largest (k <= 256) of the threads' keys, which differ or are 0; to
@@ -138,11 +143,11 @@ __device__ uint64_t kth_of_threads(uint64_t key, int k, Lists& s) {
   return s.threshold;
 }
 
-// Leaves the `width` largest keys of the list in it, in order, and the last of
-// them as the threshold (0 while there are fewer).
-__device__ uint64_t cut_list(int width, Lists& s) {
+// Leaves the `width` largest of the list's n keys in it, in order, and returns
+// the last of them as the threshold (0 while there are fewer); n becomes their
+// number.
+__device__ uint64_t cut_list(int width, int& n, Lists& s) {
   __syncthreads();
-  int n = min(s.fill, kListMax);
   if (n > 2 * kThreads) {  // first by the threads' maxima: at most `width` threads' keys stay
     uint64_t top = 0;
     for (int i = threadIdx.x; i < n; i += kThreads) top = max(top, s.list[i]);
@@ -153,7 +158,6 @@ __device__ uint64_t cut_list(int width, Lists& s) {
       const int i = threadIdx.x + j * kThreads;
       mine[j] = i < n ? s.list[i] : 0;
     }
-    __syncthreads();
     if (threadIdx.x == 0) s.fill = 0;
     __syncthreads();
 #pragma unroll
@@ -169,11 +173,10 @@ __device__ uint64_t cut_list(int width, Lists& s) {
   for (int j = 0; j < 2; ++j) {
     const int i = threadIdx.x + j * kThreads;
     mine[j] = i < n ? s.list[i] : 0;
-    if (i - (threadIdx.x & 31) >= n) continue;  // (the warp's)
+    if (i - static_cast<int>(threadIdx.x & 31) >= n) continue;  // (the warp's)
     for (int o = 0; o < n; ++o) rank[j] += s.list[o] > mine[j];
   }
-  __syncthreads();
-  if (threadIdx.x == 0) s.fill = min(n, width), s.threshold = 0;
+  if (threadIdx.x == 0) s.threshold = 0;
   __syncthreads();
 #pragma unroll
   for (int j = 0; j < 2; ++j) {
@@ -182,6 +185,7 @@ __device__ uint64_t cut_list(int width, Lists& s) {
       if (rank[j] == width - 1) s.threshold = mine[j];
     }
   }
+  n = min(n, width);
   __syncthreads();
   return s.threshold;
 }
@@ -212,6 +216,15 @@ __device__ __forceinline__ void merge_beams(const BeamParams& p, int64_t seq, Me
   const int lists = p.beams * p.parts, first = min(p.width, kMergeKeys / lists);  // scores of a list that are kept
   const unsigned long long* keys = p.keys + seq * lists * p.width;
   for (int i = tid; i < lists; i += kThreads) s.at[i] = 0;
+  // this thread's first keys, on their way while the log sums are worked out
+  constexpr int kAhead = 2;
+  unsigned long long ahead[kAhead];
+  auto key_at = [&](int i) {
+    const int list = i / first;
+    return __ldcg(keys + static_cast<int64_t>(list) * p.width + i - list * first);
+  };
+#pragma unroll
+  for (int j = 0; j < kAhead; ++j) ahead[j] = tid + j * kThreads < lists * first ? key_at(tid + j * kThreads) : 0;
   for (int b = warp; b < p.beams; b += kThreads / 32) {
     const int64_t row = seq * p.beams + b;
     const float2 ml = lane < p.parts ? __ldcg(p.sums + row * p.parts + lane) : make_float2(-INFINITY, 0.f);
@@ -235,12 +248,14 @@ __device__ __forceinline__ void merge_beams(const BeamParams& p, int64_t seq, Me
     const double base = s.base[list / p.parts];
     return key && base > -INFINITY ? ordered64(base + static_cast<double>(from_ordered(static_cast<uint32_t>(key >> 32)))) : 0;
   };
-  for (int i = tid; i < lists * first; i += kThreads) {
-    const int list = i / first;
-    const uint64_t key = __ldcg(keys + static_cast<int64_t>(list) * p.width + i - list * first);
-    s.score[i] = score_of(list, key);
+  auto keep = [&](int i, uint64_t key) {
+    s.score[i] = score_of(i / first, key);
     s.token[i] = 0xffffffffu - static_cast<uint32_t>(key);
-  }
+  };
+#pragma unroll
+  for (int j = 0; j < kAhead; ++j)
+    if (tid + j * kThreads < lists * first) keep(tid + j * kThreads, ahead[j]);
+  for (int i = tid + kAhead * kThreads; i < lists * first; i += kThreads) keep(i, key_at(i));
   __syncthreads();
   if (warp != 0) return;
   // rounds: each lane has the best of its lists (score, list, token)
@@ -300,76 +315,118 @@ __global__ void __launch_bounds__(kThreads, 4) beam_kernel(const BeamParams p) {
   const int part = static_cast<int>(blockIdx.x - row * p.parts);
   const Units units(static_cast<const T*>(p.logits) + row * p.row_stride, p.vocab);
   const int64_t first = static_cast<int64_t>(part) * p.tiles * kTile, last = min(units.end, first + static_cast<int64_t>(p.tiles) * kTile);
-  if (threadIdx.x == 0) s.fill = 0;
+  if (threadIdx.x < 3) s.added[threadIdx.x] = 0;
   __syncthreads();
 
   float m = -INFINITY, l = 0.f;
-  uint64_t threshold = 0;  // keys above it are candidates (and equal to it: it is in the list)
+  int n = 0;               // keys of the list
+  uint64_t threshold = 0;  // keys above it are candidates (what equals it is in the list)
+  float low = -INFINITY;   // their values are not below it
   uint4 ahead[kUnits];
-  auto fetch = [&](int64_t at) {
+  auto fetch = [&](int64_t at, uint4* w) {
 #pragma unroll
-    for (int i = 0; i < kUnits; ++i) ahead[i] = units.load(at / kVec + i * kThreads + threadIdx.x);
+    for (int i = 0; i < kUnits; ++i) w[i] = units.load(at / kVec + i * kThreads + threadIdx.x);
   };
-  if (first < last) fetch(first);
-  for (int64_t at = first; at < last; at += kTile) {
-    float x[kPer];
-#pragma unroll
-    for (int i = 0; i < kUnits; ++i) Units::values(ahead[i], x + i * kVec);
-    if (at + kTile < last) fetch(at + kTile);
-    auto token = [&](int i) {
-      return static_cast<uint32_t>(at + (static_cast<int64_t>(i / kVec) * kThreads + threadIdx.x) * kVec + i % kVec - units.lead);
-    };
+  auto token = [&](int64_t at, int i) {
+    return static_cast<uint32_t>(at + (static_cast<int64_t>(i / kVec) * kThreads + threadIdx.x) * kVec + i % kVec - units.lead);
+  };
+  auto top_of = [](const float (&x)[kPer]) {
     float top = fmaxf(x[0], x[1]);
 #pragma unroll
     for (int i = 2; i < kPer; i += 2) top = fmaxf(top, fmaxf(x[i], x[i + 1]));
-    const float mn = fmaxf(m, top), ref = mn == -INFINITY ? 0.f : mn;
-    const uint64_t less = pack2(-ref, -ref), scale = pack2(kLog2e, kLog2e);
-    uint64_t sum = pack2(0.f, 0.f);
+    return top;
+  };
+  // adds a tile's candidates to the list, its places counted by `count` from n0 on
+  auto add = [&](int64_t at, const float (&x)[kPer], int n0, int* count) {
 #pragma unroll
-    for (int i = 0; i < kPer; i += 2) {
-      float u, v;
-      unpack2(mul2(add2(pack2(x[i], x[i + 1]), less), scale), u, v);
-      sum = add2(sum, pack2(ex2(u), ex2(v)));
-    }
-    float even, odd;
-    unpack2(sum, even, odd);
-    l = l * ex2((m - ref) * kLog2e) + (even + odd);
-    m = mn;
-
-    // candidates: values that the threshold's does not exceed
-    const float low = threshold ? from_ordered(static_cast<uint32_t>(threshold >> 32)) : -INFINITY;
-    const int fill = s.fill;  // read before any thread of this tile adds to it: the branches below are the block's
-    const int total = __syncthreads_count(top >= low);
-    if (total == 0) continue;
-    // (an upper bound: a thread has at most kPer)
-    if (fill + total * kPer > kListMax) {
-      uint64_t best = 0;
-#pragma unroll
-      for (int i = 0; i < kPer; ++i) best = max(best, key_of(x[i], token(i)));
-      const uint64_t th = kth_of_threads(best, p.width, s);
-      // at least `width` of the tile reach it
-      if (th > threshold) threshold = th - 1;
-      if (fill + p.width * kPer > kListMax) threshold = max(threshold, cut_list(p.width, s));
-    }
-    if (top >= low) {
-#pragma unroll
-      for (int i = 0; i < kPer; ++i) {
-        if (!(x[i] >= low)) continue;
-        const uint64_t k = key_of(x[i], token(i));
-        if (k > threshold) {
-          const int to = atomicAdd(&s.fill, 1);
-          if (to < kListMax) s.list[to] = k;
-        }
+    for (int i = 0; i < kPer; ++i) {
+      if (!(x[i] >= low)) continue;
+      const uint64_t k = key_of(x[i], token(at, i));
+      if (k > threshold) {
+        const int to = n0 + atomicAdd(count, 1);
+        if (to < kListMax) s.list[to] = k;
       }
     }
+  };
+  if (first < last) fetch(first, ahead);
+  int turn = 0;
+  for (int64_t g0 = first; g0 < last; g0 += kGroup * kTile) {
+    int* count = s.added + turn;
+    turn = turn == 2 ? 0 : turn + 1;
+    if (threadIdx.x == 0) s.added[turn] = 0;  // (read last before the group before)
+    const int64_t g1 = min(last, g0 + kGroup * kTile);
+    for (int64_t at = g0; at < g1; at += kTile) {
+      float x[kPer];
+#pragma unroll
+      for (int i = 0; i < kUnits; ++i) Units::values(ahead[i], x + i * kVec);
+      if (at + kTile < last) fetch(at + kTile, ahead);
+      const float top = top_of(x), mn = fmaxf(m, top), ref = mn == -INFINITY ? 0.f : mn;
+      const uint64_t less = pack2(-ref, -ref), scale = pack2(kLog2e, kLog2e);
+      uint64_t sum = pack2(0.f, 0.f);
+#pragma unroll
+      for (int i = 0; i < kPer; i += 2) {
+        float u, v;
+        unpack2(mul2(add2(pack2(x[i], x[i + 1]), less), scale), u, v);
+        sum = add2(sum, pack2(ex2(u), ex2(v)));
+      }
+      float even, odd;
+      unpack2(sum, even, odd);
+      l = l * ex2((m - ref) * kLog2e) + (even + odd);
+      m = mn;
+      if (at == first) {
+        // the (width / 8)-th largest of each warp's threads: `width` values at
+        // least are not below the smallest of those
+        const int k = (p.width + kThreads / 32 - 1) / (kThreads / 32), lane = threadIdx.x & 31;
+        const uint32_t mine = top > -INFINITY ? ordered(top) : 0;
+        int above = 0;
+#pragma unroll
+        for (int o = 0; o < 32; ++o) {
+          const uint32_t other = __shfl_sync(0xffffffffu, mine, o);
+          above += other > mine || (other == mine && o < lane);
+        }
+        if (above == k - 1) s.warp_low[threadIdx.x >> 5] = mine ? top : -INFINITY;
+        __syncthreads();
+        low = s.warp_low[0];
+#pragma unroll
+        for (int w = 1; w < kThreads / 32; ++w) low = fminf(low, s.warp_low[w]);
+      }
+      if (top >= low) add(at, x, n, count);
+    }
     __syncthreads();
-    // A tight threshold keeps the tiles' candidates few, and a short list is cut
-    // quickly.
-    if (s.fill > p.width + kSpare) threshold = max(threshold, cut_list(p.width, s));
+    const int all = n + *count;
+    if (all <= kListMax) {
+      n = all;
+      // a tight threshold keeps the candidates few, and a short list is cut quickly
+      if (n > p.width + kSpare) threshold = max(threshold, cut_list(p.width, n, s));
+    } else {
+      // too many: this group again, tile by tile
+      if (n > kListMax / 2) threshold = max(threshold, cut_list(p.width, n, s));
+      for (int64_t at = g0; at < g1; at += kTile) {
+        uint4 w[kUnits];
+        float x[kPer];
+        fetch(at, w);
+#pragma unroll
+        for (int i = 0; i < kUnits; ++i) Units::values(w[i], x + i * kVec);
+        uint64_t best = 0;
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) best = max(best, key_of(x[i], token(at, i)));
+        // at least `width` of the tile reach it, of at most `width` threads
+        const uint64_t th = kth_of_threads(best, p.width, s);
+        if (th > threshold) threshold = th - 1;
+        low = threshold ? from_ordered(static_cast<uint32_t>(threshold >> 32)) : -INFINITY;
+        if (threadIdx.x == 0) s.fill = 0;
+        __syncthreads();
+        add(at, x, n, &s.fill);
+        __syncthreads();
+        n += s.fill;
+        threshold = max(threshold, cut_list(p.width, n, s));
+      }
+    }
+    if (threshold) low = from_ordered(static_cast<uint32_t>(threshold >> 32));
   }
-  cut_list(p.width, s);
+  cut_list(p.width, n, s);
   unsigned long long* keys = p.keys + (row * p.parts + part) * p.width;
-  for (int i = threadIdx.x; i < p.width; i += kThreads) keys[i] = i < s.fill ? s.list[i] : 0;
+  for (int i = threadIdx.x; i < p.width; i += kThreads) keys[i] = i < n ? s.list[i] : 0;
 
   // the sums of the threads
   auto join = [](float& m, float& l, float om, float ol) {

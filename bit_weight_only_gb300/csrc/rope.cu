@@ -33,9 +33,11 @@ constexpr int kWarpRows = 8;
 // Warps of a token: for its queries, keys and values.
 __host__ __device__ __forceinline__ int row_warps(int heads) { return (heads + kWarpRows - 1) / kWarpRows; }
 
+enum { kNone, kWhole, kAny, kNext };
+
 // FMT 0: rows only, no cache.
 template <int FMT, int D, typename T>
-__global__ void __launch_bounds__(kThreads) rope_kernel(const RopeParams p) {
+__global__ void __launch_bounds__(kThreads, 3) rope_kernel(const RopeParams p) {
   constexpr int kLanes = D / 8, kAt = 32 / kLanes;  // kAt rows at a time
   constexpr int kPasses = kWarpRows / kAt;
   // Cosines and sines of a token's D / 2 pairs, as quads of pairs 4 i .. 4 i + 3:
@@ -46,9 +48,11 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const RopeParams p) {
   const unsigned full = 0xffffffffu;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, n = p.pairs;
   const int H = FMT ? p.cache.kv_heads : 0, q_warps = row_warps(p.q_heads), k_warps = row_warps(H), per = q_warps + 2 * k_warps;
-  const int64_t w0 = static_cast<int64_t>(blockIdx.x) * kWarps, t0 = div_small(w0, per), w = w0 + warp;
-  const int64_t token = div_small(w, per);
-  const int part = static_cast<int>(w - token * per), kind = part < q_warps ? 0 : part < q_warps + k_warps ? 1 : 2;  // q, k, v
+  // the block's warps are w0 .. of all, the first of them warp `r0` of token t0
+  const int64_t w0 = static_cast<int64_t>(blockIdx.x) * kWarps, t0 = div_small(w0, per);
+  const unsigned r0 = static_cast<unsigned>(w0 - t0 * per), mine = (r0 + warp) / static_cast<unsigned>(per);
+  const int64_t token = t0 + mine;
+  const int part = static_cast<int>(r0 + warp - mine * per), kind = part < q_warps ? 0 : part < q_warps + k_warps ? 1 : 2;  // q, k, v
   const int heads = kind == 0 ? p.q_heads : H;
   const int row0 = (kind == 0 ? part : kind == 1 ? part - q_warps : part - q_warps - k_warps) * kWarpRows;
   const int d0 = (lane % kLanes) * 8;
@@ -77,7 +81,7 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const RopeParams p) {
   }
 
   // ---- the angles of the block's tokens
-  const int tokens = static_cast<int>(min(div_small(w0 + kWarps - 1, per), p.n_tokens - 1) - t0) + 1;
+  const int tokens = static_cast<int>(min(static_cast<int64_t>((r0 + kWarps - 1) / static_cast<unsigned>(per)), p.n_tokens - 1 - t0)) + 1;
   for (int i = threadIdx.x; i < tokens * (D / 2); i += kThreads) {
     const int t = i / (D / 2), j = i % (D / 2);
     float c = 1.f, s = 0.f;
@@ -95,86 +99,89 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const RopeParams p) {
   __syncthreads();
   if (!on) return;
 
-  // this lane's: y = x c + other s, with -s for the first of a pair
-  const bool whole = (n & 7) == 0;
-  float c[8], s[8];
-  bool turned[8];
-  if (kind != 2) {
-    const int t = static_cast<int>(token - t0);
-    auto quad = [&](int q, float (&cc)[4], float (&ss)[4]) {
-      const float4 a = s_cos[t][(q & 1) * (D / 16) + (q >> 1)], b = s_sin[t][(q & 1) * (D / 16) + (q >> 1)];
-      cc[0] = a.x, cc[1] = a.y, cc[2] = a.z, cc[3] = a.w;
-      ss[0] = b.x, ss[1] = b.y, ss[2] = b.z, ss[3] = b.w;
-    };
-    float cc[4], ss[4];
-    if (p.neighbours) {
-      quad(d0 / 8, cc, ss);
+  // ---- the rows, by the way in which a value meets the other one of its pair
+  auto rows = [&](auto how) {
+    constexpr int kHow = decltype(how)::value;  // kWhole, kAny, kNext: halves; neighbours; kNone: values
+    // y = x c + other s, with -s for the first of a pair
+    float c[8], s[8];
+    if constexpr (kHow != kNone) {
+      auto quad = [&](int q, float* cc, float* ss) {
+        const float4 a = s_cos[mine][(q & 1) * (D / 16) + (q >> 1)], b = s_sin[mine][(q & 1) * (D / 16) + (q >> 1)];
+        cc[0] = a.x, cc[1] = a.y, cc[2] = a.z, cc[3] = a.w;
+        ss[0] = b.x, ss[1] = b.y, ss[2] = b.z, ss[3] = b.w;
+      };
+      if constexpr (kHow == kNext) {
+        float cc[4], ss[4];
+        quad(d0 / 8, cc, ss);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) c[e] = cc[e / 2], s[e] = e & 1 ? ss[e / 2] : -ss[e / 2];
-    } else if (whole) {
-      const int j0 = d0 < n ? d0 : d0 < 2 * n ? d0 - n : 0;
+        for (int e = 0; e < 8; ++e) c[e] = cc[e / 2], s[e] = e & 1 ? ss[e / 2] : -ss[e / 2];
+      } else if constexpr (kHow == kWhole) {
+        const int j0 = d0 < n ? d0 : d0 < 2 * n ? d0 - n : 0;
+        quad(j0 / 4, c, s);
+        quad(j0 / 4 + 1, c + 4, s + 4);
+        if (d0 < n) {
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        quad(j0 / 4 + h, cc, ss);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) c[4 * h + e] = cc[e], s[4 * h + e] = d0 < n ? -ss[e] : ss[e];
-      }
-    } else {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const int i = d0 + e, j = i < n ? i : i < 2 * n ? i - n : 0, q = ((j >> 2) & 1) * (D / 16) + (j >> 3);
-        c[e] = reinterpret_cast<const float*>(&s_cos[t][q])[j & 3];
-        const float x = reinterpret_cast<const float*>(&s_sin[t][q])[j & 3];
-        s[e] = i < n ? -x : x;
-      }
-    }
-#pragma unroll
-    for (int e = 0; e < 8; ++e) turned[e] = d0 + e < 2 * n;
-  }
-
-#pragma unroll
-  for (int i = 0; i < kPasses; ++i) {
-    const int row = row0 + i * kAt + lane / kLanes;
-    if (row0 + i * kAt >= heads) break;  // (the warp's)
-    float x[8];
-    raw[i].values(x);
-    if (kind != 2) {
-      float y[8];
-      if (p.neighbours) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) y[e] = x[e ^ 1];
-      } else if (whole) {
-        const int other = d0 < n ? lane + n / 8 : d0 < 2 * n ? lane - n / 8 : lane;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) y[e] = __shfl_sync(full, x[e], other);
+          for (int e = 0; e < 8; ++e) s[e] = -s[e];
+        }
       } else {
-        float* mine = s_row[warp][lane / kLanes];
-        __syncwarp();
 #pragma unroll
-        for (int e = 0; e < 8; ++e) mine[d0 + e] = x[e];
-        __syncwarp();
-#pragma unroll
-        for (int e = 0; e < 8; ++e) y[e] = d0 + e < 2 * n ? mine[d0 + e < n ? d0 + e + n : d0 + e - n] : 0.f;
-      }
-#pragma unroll
-      for (int e = 0; e < 8; e += 2) {
-        float u, v;
-        unpack2(fma2(pack2(x[e], x[e + 1]), pack2(c[e], c[e + 1]), mul2(pack2(y[e], y[e + 1]), pack2(s[e], s[e + 1]))), u, v);
-        if (turned[e]) x[e] = u;
-        if (turned[e + 1]) x[e + 1] = v;
+        for (int e = 0; e < 8; ++e) {
+          const int i = d0 + e, j = i < n ? i : i < 2 * n ? i - n : 0, q = ((j >> 2) & 1) * (D / 16) + (j >> 3);
+          c[e] = reinterpret_cast<const float*>(&s_cos[mine][q])[j & 3];
+          const float x = reinterpret_cast<const float*>(&s_sin[mine][q])[j & 3];
+          s[e] = i < n ? -x : x;
+        }
       }
     }
-    if (kind == 0) {
-      if (row < heads) {
-        const int64_t to = token * p.out.token_stride + row * p.out.head_stride + d0;
-        if (p.out_dtype == QGEMV_DT_F16) store_values(static_cast<__half*>(p.out.ptr) + to, x);
-        else if (p.out_dtype == QGEMV_DT_BF16) store_values(static_cast<__nv_bfloat16*>(p.out.ptr) + to, x);
-        else store_values(static_cast<float*>(p.out.ptr) + to, x);
+#pragma unroll
+    for (int i = 0; i < kPasses; ++i) {
+      const int row = row0 + i * kAt + lane / kLanes;
+      if (row0 + i * kAt >= heads) break;  // (the warp's)
+      float x[8];
+      raw[i].values(x);
+      if constexpr (kHow != kNone) {
+        float y[8];
+        if constexpr (kHow == kNext) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) y[e] = x[e ^ 1];
+        } else if constexpr (kHow == kWhole) {
+          const int other = d0 < n ? lane + n / 8 : d0 < 2 * n ? lane - n / 8 : lane;
+#pragma unroll
+          for (int e = 0; e < 8; ++e) y[e] = __shfl_sync(full, x[e], other);
+        } else {
+          float* here = s_row[warp][lane / kLanes];
+          __syncwarp();
+#pragma unroll
+          for (int e = 0; e < 8; ++e) here[d0 + e] = x[e];
+          __syncwarp();
+#pragma unroll
+          for (int e = 0; e < 8; ++e) y[e] = d0 + e < 2 * n ? here[d0 + e < n ? d0 + e + n : d0 + e - n] : 0.f;
+        }
+#pragma unroll
+        for (int e = 0; e < 8; e += 2) {
+          float u, v;
+          unpack2(fma2(pack2(x[e], x[e + 1]), pack2(c[e], c[e + 1]), mul2(pack2(y[e], y[e + 1]), pack2(s[e], s[e + 1]))), u, v);
+          // (whole: a lane's eight values are turned or not together)
+          if (kHow == kWhole ? d0 < 2 * n : d0 + e < 2 * n) x[e] = u;
+          if (kHow == kWhole ? d0 < 2 * n : d0 + e + 1 < 2 * n) x[e + 1] = v;
+        }
       }
-    } else if constexpr (FMT != 0) {
-      encode<FMT, D>(b0 + row * step, kind == 2, at % kKvBlockTokens, d0, x, row < heads);
+      if (kind == 0) {
+        if (row < heads) {
+          const int64_t to = token * p.out.token_stride + row * p.out.head_stride + d0;
+          if (p.out_dtype == QGEMV_DT_F16) store_values(static_cast<__half*>(p.out.ptr) + to, x);
+          else if (p.out_dtype == QGEMV_DT_BF16) store_values(static_cast<__nv_bfloat16*>(p.out.ptr) + to, x);
+          else store_values(static_cast<float*>(p.out.ptr) + to, x);
+        }
+      } else if constexpr (FMT != 0) {
+        encode<FMT, D>(b0 + row * step, kind == 2, at % kKvBlockTokens, d0, x, row < heads);
+      }
     }
-  }
+  };
+  if (kind == 2) rows(std::integral_constant<int, kNone>());
+  else if (p.neighbours) rows(std::integral_constant<int, kNext>());
+  else if ((n & 7) == 0) rows(std::integral_constant<int, kWhole>());
+  else rows(std::integral_constant<int, kAny>());
 }
 
 }  // namespace

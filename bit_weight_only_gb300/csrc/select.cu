@@ -39,43 +39,47 @@ __device__ __forceinline__ int8_t code_of(float x, float a) {
   return static_cast<int8_t>(a > 0.f ? static_cast<int>(q) : 0);
 }
 
-constexpr int kSummaryWarps = 4;
+constexpr int kSummaryThreads = 128;
 
-// A block for a head of a page, its warps for runs of tokens.  Keys with an
-// infinity or NaN leave codes of 0 and a scale of NaN: such a page comes before
-// all others.
-template <int FMT, int D>
-__global__ void __launch_bounds__(32 * kSummaryWarps) summary_kernel(const SummaryParams p) {
+// W warps, one or the block's four, for a head of a page, each for a run of its
+// tokens.  Keys with an infinity or NaN leave codes of 0 and a scale of NaN: such
+// a page comes before all others.
+template <int FMT, int D, int W>
+__global__ void __launch_bounds__(kSummaryThreads) summary_kernel(const SummaryParams p) {
   constexpr int kLanes = D / 8, kAt = 32 / kLanes;  // kAt tokens at a time
-  constexpr int kAhead = 16 / kAt;                   // of 16 tokens
-  __shared__ float s_hi[kSummaryWarps][D], s_lo[kSummaryWarps][D];
-  __shared__ float s_max[kSummaryWarps];
+  constexpr int kAhead = 4;
+  __shared__ float s_edge[2][W][D];
+  __shared__ int s_bad[W];
   const unsigned full = 0xffffffffu;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, H = p.cache.kv_heads;
-  const int64_t i = div_small(blockIdx.x, H);
-  const int head = static_cast<int>(blockIdx.x - i * H);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, part = warp % W, H = p.cache.kv_heads;
+  const int64_t item = (static_cast<int64_t>(blockIdx.x) * (kSummaryThreads / 32) + warp) / W, i = div_small(item, H);
+  if (i >= p.n) return;  // (W > 1: the block's)
+  const int head = static_cast<int>(item - i * H);
   const int64_t page = __ldg(p.pages + i);
   if (page < 0 || page >= p.cache.n_pages) return;
-  const int d0 = (lane % kLanes) * 8;
+  const int d0 = (lane % kLanes) * 8, run = p.cache.page_tokens / W, t1 = (part + 1) * run;
   float hi[8], lo[8];
 #pragma unroll
   for (int e = 0; e < 8; ++e) hi[e] = -INFINITY, lo[e] = INFINITY;
   bool bad = false;
-  for (int blk = warp; blk < p.cache.page_tokens / kKvBlockTokens; blk += kSummaryWarps) {
-    const uint8_t* b = kv_block<FMT, D>(p.cache, page, head, blk);
+  for (int t0 = part * run + lane / kLanes; t0 < t1; t0 += kAt * kAhead) {
     Eight<FMT, D> x[kAhead];
 #pragma unroll
-    for (int k = 0; k < kAhead; ++k) x[k].load(b, false, k * kAt + lane / kLanes, d0);
+    for (int k = 0; k < kAhead; ++k) {
+      const int t = min(t0 + k * kAt, t1 - 1);  // (a token twice changes nothing)
+      x[k].load(kv_block<FMT, D>(p.cache, page, head, t / kKvBlockTokens), false, t % kKvBlockTokens, d0);
+    }
 #pragma unroll
     for (int k = 0; k < kAhead; ++k) {
-      float v[8];
+      float v[8], odd = 0.f;
       x[k].values(v);
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        bad |= !(fabsf(v[e]) < INFINITY);
+        odd = fmaf(v[e], 0.f, odd);  // NaN for an infinity or NaN
         hi[e] = fmaxf(hi[e], v[e]);
         lo[e] = fminf(lo[e], v[e]);
       }
+      bad |= odd != 0.f;
     }
   }
 #pragma unroll
@@ -86,31 +90,44 @@ __global__ void __launch_bounds__(32 * kSummaryWarps) summary_kernel(const Summa
       lo[e] = fminf(lo[e], __shfl_xor_sync(full, lo[e], o));
     }
   }
-  if (lane < kLanes) {
+  bad = __any_sync(full, bad);
+  // lanes of a token have eight channels each: those of the first hi, of the second lo
+  const bool low = lane / kLanes == 1;
+  float x[8];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) s_hi[warp][d0 + e] = hi[e], s_lo[warp][d0 + e] = lo[e];
+  for (int e = 0; e < 8; ++e) x[e] = low ? lo[e] : hi[e];
+  if constexpr (W > 1) {
+    if (lane < 2 * kLanes) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) s_edge[low][part][d0 + e] = x[e];
+    }
+    if (lane == 0) s_bad[part] = bad;
+    __syncthreads();
+    if (part != 0) return;
+#pragma unroll
+    for (int w = 1; w < W; ++w) {
+      bad |= s_bad[w] != 0;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float y = s_edge[low][w][d0 + e];
+        x[e] = low ? fminf(x[e], y) : fmaxf(x[e], y);
+      }
+    }
   }
-  bad = __syncthreads_or(bad);
-  // a thread for a channel from here
-  float h = -INFINITY, l = INFINITY;
-  if (tid < D) {
+  float m = 0.f;
 #pragma unroll
-    for (int w = 0; w < kSummaryWarps; ++w) h = fmaxf(h, s_hi[w][tid]), l = fminf(l, s_lo[w][tid]);
-  }
-  float m = tid < D ? fmaxf(fabsf(h), fabsf(l)) : 0.f;
+  for (int e = 0; e < 8; ++e) m = fmaxf(m, lane < 2 * kLanes ? fabsf(x[e]) : 0.f);
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(full, m, o));
-  if (lane == 0) s_max[warp] = m;
-  __syncthreads();
-#pragma unroll
-  for (int w = 0; w < kSummaryWarps; ++w) m = fmaxf(m, s_max[w]);
+  for (int o = 1; o < 32; o <<= 1) m = fmaxf(m, __shfl_xor_sync(full, m, o));
   const float a = bad ? __int_as_float(0x7fffffff) : __fdiv_rn(m, 127.f);
   const int64_t row = page * H + head;
-  if (tid < D) {
-    p.codes[row * 2 * D + tid] = code_of(h, a);
-    p.codes[row * 2 * D + D + tid] = code_of(l, a);
+  if (lane < 2 * kLanes) {
+    uint32_t w[2] = {0, 0};
+#pragma unroll
+    for (int e = 0; e < 8; ++e) w[e >> 2] |= (static_cast<uint32_t>(code_of(x[e], a)) & 0xffu) << (8 * (e & 3));
+    *reinterpret_cast<uint2*>(p.codes + row * 2 * D + low * D + d0) = make_uint2(w[0], w[1]);
   }
-  if (tid == 0) p.scales[row] = a;
+  if (lane == 0) p.scales[row] = a;
 }
 
 constexpr int kThreads = 512;
@@ -127,7 +144,7 @@ __device__ __forceinline__ uint32_t score_key(float x) {
 }
 
 template <int D>
-__global__ void __launch_bounds__(kThreads) select_kernel(const SelectParams p) {
+__global__ void __launch_bounds__(kThreads, 1) select_kernel(const SelectParams p) {
   constexpr int kLanes = 4;                    // lanes of a page
   constexpr int kUnits = 2 * D / 16 / kLanes;  // 16-byte units of a lane
   constexpr int kParts = kThreads / D;
@@ -155,7 +172,27 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const SelectParams p) 
     const int page = i < i1 ? __ldg(table + i) : -1;
     return page < p.cache.n_pages ? page : -1;
   };
-  int ahead = page_at(i0 + tid);
+  // 32 pages of a warp: lane l has the number and scale of page l, and of page 8 g
+  // + l / 4 the units l % 4, l % 4 + 4, ..
+  struct Pages {
+    int page;
+    float scale;
+    int4 c[4][kUnits];
+  } now;
+  auto fetch = [&](int page, Pages& x) {
+    x.page = page;
+    x.scale = page >= 0 ? __ldg(p.scales + static_cast<int64_t>(page) * H + head) : 0.f;
+#pragma unroll
+    for (int g = 0; g < 4; ++g) {
+      const int pg = __shfl_sync(full, page, 8 * g + lane / kLanes);
+      const int4* from = reinterpret_cast<const int4*>(p.codes + (static_cast<int64_t>(pg) * H + head) * 2 * D) + lane % kLanes;
+#pragma unroll
+      for (int u = 0; u < kUnits; ++u) x.c[g][u] = pg >= 0 ? __ldg(from + u * kLanes) : make_int4(0, 0, 0, 0);
+    }
+  };
+  // the first ones are on their way while the queries' codes are worked out
+  fetch(page_at(i0 + tid), now);
+  int ahead = page_at(i0 + tid + kThreads);
 
   // ---- the queries' codes
   int64_t q0 = __ldg(p.cu_q + seq);
@@ -202,32 +239,27 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const SelectParams p) 
 #pragma unroll
   for (int u = 0; u < kUnits; ++u) qc[u] = reinterpret_cast<const int4*>(s_q)[u * kLanes + lane % kLanes];
   for (int k0 = i0 + warp * 32; k0 < i1; k0 += kThreads) {
-    const int k = k0 + lane, page = ahead;
-    ahead = page_at(k + kThreads);
-    const float scale = page >= 0 ? __ldg(p.scales + static_cast<int64_t>(page) * H + head) : 0.f;
     int dot = 0;  // of this lane's page
 #pragma unroll
-    for (int g = 0; g < 4; ++g) {  // eight pages at a time
-      const int pg = __shfl_sync(full, page, 8 * g + lane / kLanes);
-      int4 c[kUnits];
-#pragma unroll
-      for (int u = 0; u < kUnits; ++u)
-        c[u] = pg >= 0 ? __ldg(reinterpret_cast<const int4*>(p.codes + (static_cast<int64_t>(pg) * H + head) * 2 * D) + u * kLanes + lane % kLanes)
-                       : make_int4(0, 0, 0, 0);
+    for (int g = 0; g < 4; ++g) {
       int sum = 0;
 #pragma unroll
       for (int u = 0; u < kUnits; ++u) {
-        sum = __dp4a(c[u].x, qc[u].x, sum);
-        sum = __dp4a(c[u].y, qc[u].y, sum);
-        sum = __dp4a(c[u].z, qc[u].z, sum);
-        sum = __dp4a(c[u].w, qc[u].w, sum);
+        sum = __dp4a(now.c[g][u].x, qc[u].x, sum);
+        sum = __dp4a(now.c[g][u].y, qc[u].y, sum);
+        sum = __dp4a(now.c[g][u].z, qc[u].z, sum);
+        sum = __dp4a(now.c[g][u].w, qc[u].w, sum);
       }
       sum += __shfl_xor_sync(full, sum, 1);
       sum += __shfl_xor_sync(full, sum, 2);
       const int got = __shfl_sync(full, sum, (lane & 7) * kLanes);
       if (lane / 8 == g) dot = got;
     }
-    if (k < i1) keys[k] = page >= 0 ? score_key(__fmul_rn(static_cast<float>(dot), scale)) : 0;
+    if (k0 + lane < i1) keys[k0 + lane] = now.page >= 0 ? score_key(__fmul_rn(static_cast<float>(dot), now.scale)) : 0;
+    if (k0 + kThreads < i1) {
+      fetch(ahead, now);
+      ahead = page_at(k0 + lane + 2 * kThreads);
+    }
   }
   cluster.sync();
   if (me != 0) return;
@@ -368,15 +400,22 @@ cudaError_t launch_select_of(const SelectParams& p, int cluster, int dev, int sm
 int64_t select_most_pages() { return kMaxKeys; }
 
 cudaError_t launch_summary(const SummaryParams& p, cudaStream_t s) {
-  const int64_t grid = p.n * p.cache.kv_heads;
+  int dev = 0, sms = 0;
+  const cudaError_t found = current_device(&dev, &sms);
+  if (found != cudaSuccess) return found;
+  const int64_t items = p.n * p.cache.kv_heads;
+  // Few heads of pages: a block each, for its latency.  Many: a warp each.
+  const bool few = items <= 4 * static_cast<int64_t>(sms);
+  const int64_t grid = few ? items : (items + kSummaryThreads / 32 - 1) / (kSummaryThreads / 32);
   if (grid > 0x7fffffff) return cudaErrorInvalidConfiguration;
   auto go = [&](auto kernel) {
-    kernel<<<static_cast<unsigned>(grid), 32 * kSummaryWarps, 0, s>>>(p);
+    kernel<<<static_cast<unsigned>(grid), kSummaryThreads, 0, s>>>(p);
     return cudaGetLastError();
   };
   auto by_dim = [&](auto fmt) {
     constexpr int F = decltype(fmt)::value;
-    return p.cache.head_dim == 64 ? go(summary_kernel<F, 64>) : go(summary_kernel<F, 128>);
+    if (few) return p.cache.head_dim == 64 ? go(summary_kernel<F, 64, 4>) : go(summary_kernel<F, 128, 4>);
+    return p.cache.head_dim == 64 ? go(summary_kernel<F, 64, 1>) : go(summary_kernel<F, 128, 1>);
   };
   switch (p.cache.format) {
     case QGEMV_KV_F16: return by_dim(std::integral_constant<int, QGEMV_KV_F16>());
