@@ -8,14 +8,14 @@
 
 namespace qgemv {
 
-constexpr int kMaxBeams = 64;   // of a sequence
-constexpr int kMaxWidth = 64;   // candidates kept of a sequence
-constexpr int kMaxParts = 32;   // parts of a row, each a block's
+constexpr int kMaxBeams = 64;      // of a sequence
+constexpr int kMaxWidth = 64;      // candidates kept of a sequence
 constexpr int kMaxBeamSeqs = 4096;
+constexpr int kBeamChunk = 512;    // values of a row that are summed up together
 
 // Workspace: a count of arrivals for each of kMaxBeamSeqs sequences, 0 between
-// calls (in one place whatever the sizes of a call); for each row and part the candidates' keys (uint64 [width],
-// descending, 0: none), then the largest logit and the sum of exponentials.
+// calls (in one place whatever the sizes of a call); for each chunk of each row
+// its largest logit and the sum of exp(x - that).
 struct BeamParams {
   const void* logits;
   int64_t row_stride, vocab;
@@ -25,14 +25,13 @@ struct BeamParams {
   float* out_scores;
   int32_t* out_beams;
   int32_t* out_tokens;
-  unsigned* arrived;           // [kMaxBeamSeqs]
-  unsigned long long* keys;    // [rows][parts][width]
-  float2* sums;                // [rows][parts]
-  int parts;
-  int tiles;        // of a part, at most
+  unsigned* arrived;  // [kMaxBeamSeqs]
+  float2* chunks;     // [rows][n_chunks]
+  int n_chunks;       // of a row
 };
 
-int beam_parts(int64_t rows, int64_t vocab, int sms);
+// (a row that starts inside a 16-byte unit is up to 7 values longer)
+inline int64_t beam_chunks(int64_t vocab) { return (vocab + 7 + kBeamChunk - 1) / kBeamChunk; }
 cudaError_t launch_beam(const BeamParams& p, int dtype, cudaStream_t s);
 
 }  // namespace qgemv

@@ -19,7 +19,7 @@ extern "C" {
 int64_t qgemv_beam_ws_bytes(int64_t n_seqs, int beams, int64_t vocab, int width) {
   if (!beam_sizes_ok(n_seqs, beams, vocab, width)) return 0;
   const int64_t rows = (n_seqs > 0 ? n_seqs : 1) * beams;
-  return 4 * kMaxBeamSeqs + rows * beam_parts(1, vocab, 1 << 20) * (8 * static_cast<int64_t>(width) + 8);
+  return 4 * kMaxBeamSeqs + rows * beam_chunks(vocab) * static_cast<int64_t>(sizeof(float2));
 }
 
 int qgemv_beam_select(int dtype, const void* logits, int64_t row_stride, int64_t vocab, const float* scores, int64_t n_seqs,
@@ -53,7 +53,8 @@ int qgemv_beam_select(int dtype, const void* logits, int64_t row_stride, int64_t
   p.out_beams = out_beams;
   p.out_tokens = out_tokens;
   p.arrived = static_cast<unsigned*>(ws);
-  p.keys = reinterpret_cast<unsigned long long*>(static_cast<uint8_t*>(ws) + 4 * kMaxBeamSeqs);
+  p.chunks = reinterpret_cast<float2*>(static_cast<uint8_t*>(ws) + 4 * kMaxBeamSeqs);
+  p.n_chunks = static_cast<int>(beam_chunks(vocab));
   return done(launch_beam(p, dtype, static_cast<cudaStream_t>(stream)), "launching the selection");
 }
 

@@ -182,12 +182,14 @@ __global__ void __launch_bounds__(kForkThreads) fork_kernel(const PoolParams p) 
       p.table[r * p.table_stride + e] = e < used ? p.old_table[b * p.old_stride + e] : -1;
   }
   // ---- the last block; the count of arrivals is 0 again behind it
-  __threadfence();
   __syncthreads();
-  if (threadIdx.x == 0) s_last = atomicInc(reinterpret_cast<unsigned*>(p.state) + 1, gridDim.x - 1) == gridDim.x - 1;
+  if (threadIdx.x == 0) {
+    __threadfence();
+    s_last = atomicInc(reinterpret_cast<unsigned*>(p.state) + 1, gridDim.x - 1) == gridDim.x - 1;
+    __threadfence();
+  }
   __syncthreads();
   if (!s_last) return;
-  __threadfence();
   Counts<kGivePer> counts;
   counts.load(p.refs, p.n_pages, static_cast<int64_t>(threadIdx.x) * kGivePer);
   int want = 0;

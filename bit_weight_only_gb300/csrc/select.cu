@@ -47,7 +47,7 @@ constexpr int kSummaryThreads = 128;
 template <int FMT, int D, int W>
 __global__ void __launch_bounds__(kSummaryThreads) summary_kernel(const SummaryParams p) {
   constexpr int kLanes = D / 8, kAt = 32 / kLanes;  // kAt tokens at a time
-  constexpr int kAhead = 4;
+  constexpr int kAhead = W > 1 ? 8 : 4;
   __shared__ float s_edge[2][W][D];
   __shared__ int s_bad[W];
   const unsigned full = 0xffffffffu;
@@ -133,6 +133,7 @@ __global__ void __launch_bounds__(kSummaryThreads) summary_kernel(const SummaryP
 constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
 constexpr int kBins = 2048;
+constexpr int kKeys = 16;  // keys of a thread at a time
 constexpr int kMaxCluster = 8;
 constexpr int kMaxKeys = 48 * 1024;  // pages of a sequence
 
@@ -163,10 +164,14 @@ __global__ void __launch_bounds__(kThreads, 1) select_kernel(const SelectParams 
   const int seq = item / H, head = item - seq * H, G = p.q_heads / H;
   const int shift = 31 - __clz(p.cache.page_tokens);
   const int ctx = max(0, __ldg(p.ctx_lens + seq));
+  int64_t q0 = __ldg(p.cu_q + seq);
+  int64_t T = static_cast<int64_t>(__ldg(p.cu_q + seq + 1)) - q0;
+  if (q0 < 0) T = 0;
+  T = max(static_cast<int64_t>(0), min(T, min(static_cast<int64_t>(kMaxDrafts), p.n_q - q0)));
   const int64_t whole = ctx >> shift;                              // pages that end before the context does
   const int pages = static_cast<int>(min(whole, p.table_stride));  // of them in the table
   const int32_t* table = p.table + static_cast<int64_t>(seq) * p.table_stride;
-  // this block's pages [i0, i1), 32 at a time for each warp
+  // this block's pages [i0, i1)
   const int per = (pages + C - 1) / C, i0 = min(me * per, pages), i1 = min(i0 + per, pages);
   auto page_at = [&](int i) {
     const int page = i < i1 ? __ldg(table + i) : -1;
@@ -191,14 +196,11 @@ __global__ void __launch_bounds__(kThreads, 1) select_kernel(const SelectParams 
     }
   };
   // the first ones are on their way while the queries' codes are worked out
-  fetch(page_at(i0 + tid), now);
-  int ahead = page_at(i0 + tid + kThreads);
+  const int first = i0 + tid;
+  fetch(page_at(first), now);
+  int ahead = page_at(first + kThreads);
 
   // ---- the queries' codes
-  int64_t q0 = __ldg(p.cu_q + seq);
-  int64_t T = static_cast<int64_t>(__ldg(p.cu_q + seq + 1)) - q0;
-  if (q0 < 0) T = 0;
-  T = max(static_cast<int64_t>(0), min(T, min(static_cast<int64_t>(kMaxDrafts), p.n_q - q0)));
   bool bad = false;
   {
     // exact sums: an fp16 value is a whole number of 2^-24
@@ -238,7 +240,7 @@ __global__ void __launch_bounds__(kThreads, 1) select_kernel(const SelectParams 
   int4 qc[kUnits];
 #pragma unroll
   for (int u = 0; u < kUnits; ++u) qc[u] = reinterpret_cast<const int4*>(s_q)[u * kLanes + lane % kLanes];
-  for (int k0 = i0 + warp * 32; k0 < i1; k0 += kThreads) {
+  for (int k = first; k - lane < i1; k += kThreads) {
     int dot = 0;  // of this lane's page
 #pragma unroll
     for (int g = 0; g < 4; ++g) {
@@ -255,22 +257,30 @@ __global__ void __launch_bounds__(kThreads, 1) select_kernel(const SelectParams 
       const int got = __shfl_sync(full, sum, (lane & 7) * kLanes);
       if (lane / 8 == g) dot = got;
     }
-    if (k0 + lane < i1) keys[k0 + lane] = now.page >= 0 ? score_key(__fmul_rn(static_cast<float>(dot), now.scale)) : 0;
-    if (k0 + kThreads < i1) {
+    if (k < i1) keys[k] = now.page >= 0 ? score_key(__fmul_rn(static_cast<float>(dot), now.scale)) : 0;
+    if (k - lane + kThreads < i1) {
       fetch(ahead, now);
-      ahead = page_at(k0 + lane + 2 * kThreads);
+      ahead = page_at(k + 2 * kThreads);
     }
   }
   cluster.sync();
   if (me != 0) return;
 
   // ---- the first block: candidates, and the range of their keys
+  auto every = [&](auto use) {  // use(key) of this thread's keys; 0 for those behind the end
+    for (int k0 = tid; k0 - tid < pages; k0 += kKeys * kThreads) {
+      uint32_t key[kKeys];
+#pragma unroll
+      for (int j = 0; j < kKeys; ++j) key[j] = k0 + j * kThreads < pages ? s_key[k0 + j * kThreads] : 0;
+#pragma unroll
+      for (int j = 0; j < kKeys; ++j) use(key[j]);
+    }
+  };
   uint32_t lo = 0xffffffffu, hi = 0;
   int n = 0;
-  for (int k = tid; k < pages; k += kThreads) {
-    const uint32_t key = s_key[k];
+  every([&](uint32_t key) {
     if (key) lo = min(lo, key), hi = max(hi, key), ++n;
-  }
+  });
   lo = __reduce_min_sync(full, lo), hi = __reduce_max_sync(full, hi), n = __reduce_add_sync(full, n);
   if (lane == 0) s_lo[warp] = lo, s_hi[warp] = hi, s_n[warp] = n;
   __syncthreads();
@@ -289,10 +299,10 @@ __global__ void __launch_bounds__(kThreads, 1) select_kernel(const SelectParams 
     for (;;) {
       for (int b = tid; b < kBins; b += kThreads) s_hist[b] = 0;
       __syncthreads();
-      for (int k = tid; k < pages; k += kThreads) {
-        const uint32_t key = s_key[k], from = key - base;
+      every([&](uint32_t key) {
+        const uint32_t from = key - base;
         if (key >= base && from <= span && key) atomicAdd(&s_hist[from >> low], 1);
-      }
+      });
       __syncthreads();
       // a thread for four neighbouring bins, the highest first
       const int b0 = kBins - 4 - 4 * tid;
@@ -306,7 +316,7 @@ __global__ void __launch_bounds__(kThreads, 1) select_kernel(const SelectParams 
       }
       if (lane == 31) s_eq[warp] = upto;
       __syncthreads();
-      for (int w = 0; w < warp; ++w) upto += s_eq[w];
+      upto += __reduce_add_sync(full, lane < warp ? s_eq[lane] : 0);
       const int above = upto - sum;  // keys in higher bins
       if (above < rest && upto >= rest) {
         int b = b0 + 3, left = rest - above, count = h.w;
@@ -335,33 +345,50 @@ __global__ void __launch_bounds__(kThreads, 1) select_kernel(const SelectParams 
     }
   }
 
-  // ---- the pages, in order: a warp for a run of keys
-  const int run = (pages + kThreads - 1) / kThreads * 32, k0 = warp * run, k1 = min(k0 + run, pages);
+  // ---- the pages, in order: a warp for a run of keys, kKeys / 2 of a lane at a time
+  constexpr int kAt = kKeys / 2;
+  const int run = (pages + kWarps * kAt * 32 - 1) / (kWarps * kAt * 32) * (kAt * 32), r0 = warp * run + lane, r1 = min(warp * run + run, pages);
   int above = 0, equal = 0;
-  for (int k = k0 + lane; k < k1; k += 32) {
-    above += s_key[k] > limit;
-    equal += s_key[k] == limit;
+  for (int k0 = r0; k0 - lane < r1; k0 += kAt * 32) {
+#pragma unroll
+    for (int j = 0; j < kAt; ++j) {
+      const int k = k0 + 32 * j;
+      const uint32_t key = k < r1 ? s_key[k] : 0;
+      above += key > limit;
+      equal += k < r1 && key == limit;
+    }
   }
   above = __reduce_add_sync(full, above), equal = __reduce_add_sync(full, equal);
   __syncthreads();
   if (lane == 0) s_n[warp] = above, s_eq[warp] = equal;
   __syncthreads();
-  int to = 0, before = 0;  // pages that lower warps write; keys at the limit that they have
-  for (int w = 0; w < warp; ++w) {
-    to += s_n[w] + max(0, min(s_eq[w], at_limit - before));
-    before += s_eq[w];
-  }
+  // keys at the limit that lower warps have, and pages that they write
+  int before = __reduce_add_sync(full, lane < warp ? s_eq[lane] : 0);
+  int to = __reduce_add_sync(full, lane < warp ? s_n[lane] : 0) + min(before, at_limit);
   int32_t* out = p.out + static_cast<int64_t>(item) * p.width;
   const unsigned lower = (1u << lane) - 1;
-  for (int k = k0 + lane; k < k0 + run; k += 32) {
-    const uint32_t key = k < k1 ? s_key[k] : 0;
-    const unsigned eqs = __ballot_sync(full, k < k1 && key == limit);
-    const bool take = k < k1 && (key > limit || (key == limit && before + __popc(eqs & lower) < at_limit));
-    const unsigned takes = __ballot_sync(full, take);
-    const int at = to + __popc(takes & lower);
-    if (take && at < want) out[at] = __ldg(table + k);
-    to += __popc(takes);
-    before += __popc(eqs);
+  if (above + equal > 0) {
+    for (int k0 = r0; k0 - lane < r1; k0 += kAt * 32) {
+      uint32_t key[kAt];
+      int32_t page[kAt];
+#pragma unroll
+      for (int j = 0; j < kAt; ++j) {
+        const int k = k0 + 32 * j;
+        key[j] = k < r1 ? s_key[k] : 0;
+        page[j] = k < r1 && key[j] >= limit ? __ldg(table + k) : -1;
+      }
+#pragma unroll
+      for (int j = 0; j < kAt; ++j) {
+        const bool in = k0 + 32 * j < r1;
+        const unsigned eqs = __ballot_sync(full, in && key[j] == limit);
+        const bool take = in && (key[j] > limit || (key[j] == limit && before + __popc(eqs & lower) < at_limit));
+        const unsigned takes = __ballot_sync(full, take);
+        const int at = to + __popc(takes & lower);
+        if (take && at < want) out[at] = page[j];
+        to += __popc(takes);
+        before += __popc(eqs);
+      }
+    }
   }
   // ---- the tail: the pages from the last whole one on
   for (int c = want + tid; c < p.width; c += kThreads) {
@@ -428,11 +455,11 @@ cudaError_t launch_select(const SelectParams& p, cudaStream_t s) {
   int dev = 0, sms = 0;
   const cudaError_t found = current_device(&dev, &sms);
   if (found != cudaSuccess) return found;
-  // Blocks of a cluster: while each has 256 pages at least, and the blocks are
-  // no more than the SMs twice over.
+  // Blocks of a cluster: while each has 256 pages at least, and there is an SM for
+  // each.
   const int64_t heads = static_cast<int64_t>(p.n_seqs) * p.cache.kv_heads;
   int cluster = 1;
-  while (cluster < kMaxCluster && p.table_stride > 256 * cluster && heads * cluster * 2 <= 2 * sms) cluster *= 2;
+  while (cluster < kMaxCluster && p.table_stride > 256 * cluster && heads * cluster * 2 <= sms) cluster *= 2;
   if (heads * cluster > 0x7fffffff) return cudaErrorInvalidConfiguration;
   const int smem = static_cast<int>(std::max<int64_t>(4 * p.table_stride, 16));
   return p.cache.head_dim == 64 ? launch_select_of<64>(p, cluster, dev, smem, s) : launch_select_of<128>(p, cluster, dev, smem, s);

@@ -233,5 +233,5 @@ def test_outputs_streams_and_graphs():
             g.replay()
             assert all(torch.equal(a, b) for a, b in zip(res, w))
     with pytest.raises(qgemv.QgemvError):
-        select(x, s, 16, workspace=ws)   # too small for that
+        select(torch.cat([x, x]), torch.cat([s, s]), 8, workspace=ws)   # too small for that
     assert all(t.shape == (0, 8) for t in select(x[:0], s[:0], 8, workspace=ws))
