@@ -20,6 +20,7 @@
 // the lanes; the log sum, whose whole powers of two are taken apart, and the
 // scores are 64-bit: fp32 would make ties of scores that differ.
 #include <algorithm>
+#include <cfloat>
 #include <type_traits>
 
 #include <cuda_bf16.h>
@@ -33,13 +34,13 @@
 namespace qgemv {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
 constexpr int kPer = kBeamChunk / 32;  // values of a lane
-constexpr int kCached = 2048;          // chunks' scores kept in shared memory
+constexpr int kWindow = 2048;          // chunks that are looked at together
 constexpr int kPicked = 512;           // chunks that are read again, at a time
 constexpr int kCands = 1024;           // candidates, at a time
-static_assert(kMaxWidth + kBeamChunk <= kCands, "a chunk's values fit beside those that stay");
+static_assert(kMaxWidth + kBeamChunk <= kCands && kWindow % kPicked == 0, "a chunk's values fit beside those that stay");
 
 // Order of floats as unsigned numbers, +0 and -0 as one; 0 is below all.
 __device__ __forceinline__ uint32_t ordered(float x) {
@@ -126,47 +127,39 @@ __device__ __forceinline__ bool better(uint64_t score, uint64_t place, uint64_t 
 
 struct Shared {
   double base[kMaxBeams];  // what a beam's candidates start from, or -infinity
-  uint64_t score[kCached]; // best scores of the first chunks
-  uint64_t sorted[kThreads];
   Candidate cand[kCands];
-  uint64_t picked_score[kPicked];
+  float about[kWindow];    // the chunks' best scores in fp32, of the first window
+  uint32_t bound[2 * kWarps];
+  int reach[2 * kWarps];
+  float picked_score[kPicked];
   int picked[kPicked], order[kPicked];
-  unsigned long long low;
-  int n_picked, n_cand, added;
+  uint32_t far;
+  int n_picked, n_cand;
 };
 
-// The k-th largest value (k <= 256) of the threads' keys, equal ones counted one
-// by one; 1 where fewer than k are above 0.  Each warp sorts its own, then a key
-// is counted in every warp's list by a binary search.
-__device__ __forceinline__ uint64_t kth_of_threads(uint64_t key, int k, Shared& s) {
-  const int lane = threadIdx.x & 31;
-#pragma unroll
-  for (int size = 2; size <= 32; size <<= 1) {
-#pragma unroll
-    for (int o = size >> 1; o > 0; o >>= 1) {
-      const uint64_t other = __shfl_xor_sync(0xffffffffu, key, o);
-      const bool descending = (lane & size) == 0 || size == 32, low = (lane & o) == 0;
-      if ((key < other) == (descending == low)) key = other;
-    }
+// A value that k of the threads' keys at least reach, and few more; 0 where fewer
+// than k are above 0.  Of the two keys of each warp about the (k / kWarps)-th
+// largest, the largest one that k reach.
+__device__ __forceinline__ uint32_t reached_by(uint32_t key, int k, Shared& s) {
+  const unsigned full = 0xffffffffu;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  static_assert(kWarps == 16, "two bounds of a warp are a lane's each");
+  if (threadIdx.x < 2 * kWarps) s.reach[threadIdx.x] = 0;
+  uint32_t left = key, top = 0;
+#pragma unroll 1
+  for (int j = (k + kWarps - 1) / kWarps; j >= 0; --j) {
+    top = __reduce_max_sync(full, left);
+    if (j < 2 && lane == 0) s.bound[2 * warp + j] = top;
+    if (lane == __ffs(__ballot_sync(full, left == top)) - 1) left = 0;
   }
-  s.sorted[threadIdx.x] = key;
-  if (threadIdx.x == 0) s.low = ~0ull;
-  if (__syncthreads_count(key != 0) < k) return 1;
-  int n[kWarps];  // keys of each warp above this one
-#pragma unroll
-  for (int w = 0; w < kWarps; ++w) n[w] = 0;
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w)
-      if (s.sorted[w * 32 + n[w] + o - 1] > key) n[w] += o;
-  }
-  int above = 0;
-#pragma unroll
-  for (int w = 0; w < kWarps; ++w) above += n[w] + (n[w] == 31 && s.sorted[w * 32 + 31] > key);
-  if (key && above < k) atomicMin(&s.low, static_cast<unsigned long long>(key));
   __syncthreads();
-  return s.low;
+  const uint32_t bound = s.bound[lane];
+  int reach = 0;  // keys of this warp that reach the lane's bound
+#pragma unroll 4
+  for (int o = 0; o < 32; ++o) reach += __shfl_sync(full, key, o) >= bound;
+  atomicAdd(&s.reach[lane], reach);
+  __syncthreads();
+  return __reduce_max_sync(full, s.reach[lane] >= k ? bound : 0);
 }
 
 // Leaves the `width` best of the n candidates, in order; returns their number.
@@ -210,6 +203,7 @@ __device__ __forceinline__ void choose(const BeamParams& p, int64_t seq) {
   for (int b = warp; b < p.beams; b += kWarps) {
     const float score = __ldg(p.scores + seq * p.beams + b);
     float m = -INFINITY, l = 0.f;
+#pragma unroll 1
     for (int c0 = 0; c0 < C; c0 += 32 * 8) {
       float2 ml[8];
 #pragma unroll
@@ -240,36 +234,49 @@ __device__ __forceinline__ void choose(const BeamParams& p, int64_t seq) {
       s.base[b] = fine ? static_cast<double>(score) - static_cast<double>(top) - e * 0.69314718055994530942 - static_cast<double>(logf(f))
                        : -INFINITY;
   }
-  if (tid == 0) s.n_cand = 0;
+  if (tid == 0) s.n_cand = 0, s.far = 0;
   __syncthreads();
-  // ---- the chunks' best scores
-  auto score_of = [&](int b, float x) -> uint64_t {
-    const double base = s.base[b];
-    return base > -INFINITY && x > -INFINITY ? ordered64(base + static_cast<double>(x)) : 0;
+  // ---- the chunks' best scores, in fp32: off by less than 2^-23 of the largest
+  // base and the score itself
+  auto score_of = [&](int b, float x) { return ordered64(s.base[b] + static_cast<double>(x)); };
+  auto about = [&](int i) -> float {  // -infinity: no candidates
+    const double base = s.base[i / C];
+    return base > -INFINITY ? static_cast<float>(base) + __ldcg(&chunks[i].x) : -INFINITY;
   };
-  uint64_t best = 0;
+  if (tid < p.beams && s.base[tid] > -INFINITY) atomicMax(&s.far, __float_as_uint(fabsf(static_cast<float>(s.base[tid]))));
+  float best = -INFINITY;
+#pragma unroll 4
   for (int i = tid; i < n_all; i += kThreads) {
-    const uint64_t mine = score_of(i / C, __ldcg(&chunks[i].x));
-    if (i < kCached) s.score[i] = mine;
-    best = max(best, mine);
+    const float mine = about(i);
+    if (i < kWindow) s.about[i] = mine;
+    best = fmaxf(best, mine);
   }
-  // candidates are not worse than (low, place): at first any place
-  uint64_t low = kth_of_threads(best, p.width, s), place = ~0ull;
+  const uint32_t bound = reached_by(best > -INFINITY ? ordered(best) : 0, p.width, s);
+  const float far = __uint_as_float(s.far);
+  auto less = [&](float x) { return x - 0x1p-20f * (far + fabsf(x)); };  // surely below what `x` stands for
+  // Chunks that have candidates are not below `from`; once there are `width`
+  // candidates (`filled`), others are not worse than (low, place).
+  float from = bound ? less(from_ordered(bound)) : -INFINITY;
+  uint64_t low = 0, place = 0;
+  bool filled = false;
   int n = 0;
-  // the place of a chunk's first token
-  auto place_of = [&](int i) {
+  // whether no value of chunk i, which reaches `from`, is a candidate
+  auto worse = [&](int i) {
     const int b = i / C, c = i - b * C;
-    return static_cast<uint64_t>(b) << 32 | static_cast<uint32_t>(max(0, c * kBeamChunk - 7));
+    const uint64_t at = static_cast<uint64_t>(b) << 32 | static_cast<uint32_t>(max(0, c * kBeamChunk - 7));  // its first token, or before
+    return filled && better(low, place, score_of(b, __ldcg(&chunks[i].x)), at);
   };
-  int step = kCached;
+  int step = kWindow;
+#pragma unroll 1
   for (int i0 = 0; i0 < n_all; i0 += step) {
     // ---- of `step` chunks those that reach it, the best first
     __syncthreads();
     if (tid == 0) s.n_picked = 0;
     __syncthreads();
+#pragma unroll 1
     for (int i = i0 + tid; i < min(i0 + step, n_all); i += kThreads) {
-      const uint64_t mine = i < kCached ? s.score[i] : score_of(i / C, __ldcg(&chunks[i].x));
-      if (mine && !better(low, place, mine, place_of(i))) {
+      const float mine = i < kWindow ? s.about[i] : about(i);
+      if (mine >= from && mine > -INFINITY && !worse(i)) {
         const int to = atomicAdd(&s.n_picked, 1);
         if (to < kPicked) s.picked_score[to] = mine, s.picked[to] = i;
       }
@@ -281,66 +288,90 @@ __device__ __forceinline__ void choose(const BeamParams& p, int64_t seq) {
       step = kPicked;
       continue;
     }
-    for (int i = tid; i < n_picked; i += kThreads) {
-      const uint64_t mine = s.picked_score[i];
-      const int at = s.picked[i];
+    if (tid < n_picked) {
+      static_assert(kPicked <= kThreads, "a thread for each");
+      const float mine = s.picked_score[tid];
+      const int at = s.picked[tid];
       int rank = 0;
 #pragma unroll 4
-      for (int j = 0; j < n_picked; ++j) rank += better(s.picked_score[j], s.picked[j], mine, at);
-      s.order[rank] = i;
+      for (int j = 0; j < n_picked; ++j) rank += s.picked_score[j] > mine || (s.picked_score[j] == mine && s.picked[j] < at);
+      s.order[rank] = tid;
     }
     __syncthreads();
-    // ---- a chunk for each warp at a time
-    for (int r0 = 0; r0 < n_picked; r0 += kWarps) {
-      const int first = s.order[r0];
-      if (better(low, place, s.picked_score[first], place_of(s.picked[first]))) break;  // nor do the others
-      const bool on = r0 + warp < n_picked;
-      const int i = on ? s.picked[s.order[r0 + warp]] : 0, b = i / C, c = i - b * C;
+    // ---- the r-th chunk of them, by a warp: its values that may be candidates
+    float x[kPer], least;  // values below that are worse
+    int b, c, lead;
+    auto look = [&](int r) {
+      const int i = s.picked[s.order[r]];
+      b = i / C, c = i - b * C;
       const Units units(static_cast<const T*>(p.logits) + (seq * p.beams + b) * p.row_stride, static_cast<int>(p.vocab));
-      float x[kPer];
-      float from = INFINITY;  // values below it are worse
-      if (on) {
-        if (units.inside(c)) {
-          uint4 w[Units::kUnits];
-          units.load(c, w);
-          Units::values(w, x);
-        } else {
-          units.edge(c, x);
-        }
-        const double base = s.base[b], d = low > 1 ? from_ordered64(low) - base : -INFINITY;
-        from = static_cast<float>(d - fabs(d) * 0x1p-20 - fabs(base) * 0x1p-40 - 1e-30);
-        if (low <= 1) from = -INFINITY;
+      lead = units.lead;
+      if (units.inside(c)) {
+        uint4 w[Units::kUnits];
+        units.load(c, w);
+        Units::values(w, x);
+      } else {
+        units.edge(c, x);
       }
-      auto add = [&] {
+      least = from > -INFINITY ? less(from - static_cast<float>(s.base[b])) : -FLT_MAX;
+    };
+    // to the candidates with their places and, for the time being, values
+    auto add = [&] {
 #pragma unroll
-        for (int k = 0; k < kPer; ++k) {
-          if (!(x[k] >= from) || !(x[k] > -INFINITY)) continue;
-          const uint64_t mine = score_of(b, x[k]), at = static_cast<uint64_t>(b) << 32 | units.token(c, k);
-          if (better(low, place, mine, at)) continue;
-          const int to = atomicAdd(&s.n_cand, 1);
-          if (to < kCands) s.cand[to] = {mine, at};
-        }
-      };
-      int mine = 0;
-      if (on) {
-#pragma unroll
-        for (int k = 0; k < kPer; ++k) mine += x[k] >= from;
+      for (int k = 0; k < kPer; ++k) {
+        if (!(x[k] >= least)) continue;
+        const int to = atomicAdd(&s.n_cand, 1);
+        if (to >= kCands) continue;
+        s.cand[to].place = static_cast<uint64_t>(b) << 32 | static_cast<uint32_t>(Units::place(c, k) - lead);
+        s.cand[to].score = __float_as_uint(x[k]);
       }
-      mine = __reduce_add_sync(full, mine);
-      if (tid == 0) s.added = 0;
+    };
+    auto score = [&](int n1) {  // of the candidates from n on
+      for (int j = n + tid; j < n1; j += kThreads)
+        s.cand[j].score = score_of(static_cast<int>(s.cand[j].place >> 32), __uint_as_float(static_cast<uint32_t>(s.cand[j].score)));
+      n = n1;
+    };
+    auto shorten = [&] {
+      n = cut(p.width, n, s);
+      if (tid == 0) s.n_cand = n;
+      if (n == p.width) {
+        low = s.cand[n - 1].score, place = s.cand[n - 1].place;
+        from = less(static_cast<float>(from_ordered64(low)));
+        filled = true;
+      }
       __syncthreads();
-      if (lane == 0) atomicAdd(&s.added, mine);
+    };
+    // Few: the warps go through them on their own.
+    bool done = n_picked <= 8 * kWarps;
+    if (done) {
+#pragma unroll 1
+      for (int r = warp; r < n_picked; r += kWarps) {
+        look(r);
+        add();
+      }
       __syncthreads();
-      const bool together = n + s.added <= kCands;
-      for (int turn = 0; turn < (together ? 1 : kWarps); ++turn) {
-        if (on && (together || turn == warp)) add();
+      const int n1 = s.n_cand;
+      __syncthreads();
+      done = n1 <= kCands;
+      if (done) score(n1);
+      else if (tid == 0) s.n_cand = n;
+    }
+    if (done && n > p.width) {
+      if (i0 + step < n_all) shorten();
+    } else if (!done) {
+      // Many, or with many candidates (values that rise, or are alike): one at a time.
+#pragma unroll 1
+      for (int r = 0; r < n_picked; ++r) {
         __syncthreads();
-        n = s.n_cand;
-        if (n <= p.width && together) break;  // (not full, or just)
-        n = cut(p.width, n, s);
-        if (tid == 0) s.n_cand = n;
-        if (n == p.width) low = s.cand[n - 1].score, place = s.cand[n - 1].place;
+        const int at = s.order[r];
+        if (s.picked_score[at] < from || worse(s.picked[at])) break;  // the others are, too
+        if (warp == 0) {
+          look(r);
+          add();
+        }
         __syncthreads();
+        score(s.n_cand);
+        if (n > p.width) shorten();
       }
     }
   }
@@ -385,7 +416,7 @@ __device__ __forceinline__ void sum_up(const BeamParams& p, int64_t chunk) {
 }
 
 template <typename T>
-__global__ void __launch_bounds__(kThreads, 6) beam_sums_kernel(const BeamParams p) {
+__global__ void __launch_bounds__(kThreads, 3) beam_sums_kernel(const BeamParams p) {
   const int64_t chunk = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
   if (chunk < p.n_seqs * p.beams * p.n_chunks) sum_up<T>(p, chunk);
 }
