@@ -229,66 +229,102 @@ __global__ void __launch_bounds__(kRowThreads) release_kernel(const PoolParams p
 __device__ __forceinline__ int64_t pool_tiles(int64_t n_pages) { return (n_pages + kPoolTile - 1) / kPoolTile; }
 
 constexpr int kTilePer = kPoolTile / kRowThreads;  // counts of a thread
+constexpr int kFewTiles = 16;
+
+// The moves: with U pages in use, the j-th one from number U on goes to the
+// j-th free one below.  map[page] = j for a page that moves, else -1.  `used`: U;
+// `upto`: pages in use before this thread's first one, page0, of which `on` has a
+// bit each; `below`: pages in use below number U.
+__device__ __forceinline__ void write_moves(const PoolParams& p, int64_t page0, uint32_t on, int upto, int used, int below) {
+  int32_t* map = p.scratch + pool_tiles(p.n_pages);
+#pragma unroll
+  for (int i = 0; i < kTilePer; ++i) {
+    const int64_t page = page0 + i;
+    if (page >= p.n_pages) break;
+    const bool here = on >> i & 1, moves = here && page >= used;
+    const int64_t j = moves ? upto - below : page - upto;
+    upto += here;
+    map[page] = moves ? static_cast<int32_t>(j) : -1;
+    if (j >= p.n_moves) continue;
+    if (moves) p.src[j] = static_cast<int32_t>(page);
+    else if (!here && page < used) p.dst[j] = static_cast<int32_t>(page);
+  }
+  // behind the moves: as many as there are pages in use from number `used` on
+  for (int64_t j = used - below + static_cast<int64_t>(blockIdx.x) * kRowThreads + threadIdx.x; j < p.n_moves; j += static_cast<int64_t>(gridDim.x) * kRowThreads)
+    p.src[j] = p.dst[j] = -1;
+}
+
+__device__ __forceinline__ uint32_t in_use(const PoolParams& p, int64_t page0) {
+  Counts<kTilePer> c;
+  c.load(p.refs, p.n_pages, page0);
+  uint32_t on = 0;
+#pragma unroll
+  for (int i = 0; i < kTilePer; ++i) on |= static_cast<uint32_t>(page0 + i < p.n_pages && c.v[i] > 0) << i;
+  return on;
+}
+// Bits of the pages below number `used`.
+__device__ __forceinline__ uint32_t bits_below(int64_t page0, int used) {
+  const int64_t n = used - page0;
+  return n <= 0 ? 0 : n >= kTilePer ? (1u << kTilePer) - 1 : (1u << n) - 1;
+}
+
+// Of few pages every block looks at all of them.
+__global__ void __launch_bounds__(kRowThreads) compact_few_kernel(const PoolParams p) {
+  __shared__ int s_warp[32], s_tile[32];
+  __shared__ unsigned short s_on[kFewTiles][kRowThreads];
+  allow_next_kernel();
+  const int tiles = static_cast<int>(pool_tiles(p.n_pages)), me = blockIdx.x, lane = threadIdx.x & 31;
+  if (threadIdx.x < 32) s_tile[threadIdx.x] = 0;
+  __syncthreads();
+#pragma unroll 2
+  for (int t = 0; t < tiles; ++t) {
+    const uint32_t on = in_use(p, static_cast<int64_t>(t) * kPoolTile + threadIdx.x * kTilePer);
+    s_on[t][threadIdx.x] = static_cast<unsigned short>(on);
+    const int n = __reduce_add_sync(0xffffffffu, __popc(on));
+    if (lane == 0) atomicAdd(&s_tile[t], n);
+  }
+  __syncthreads();
+  const int used = __reduce_add_sync(0xffffffffu, s_tile[lane]), before = __reduce_add_sync(0xffffffffu, lane < me ? s_tile[lane] : 0);
+  const int edge = used / kPoolTile;
+  int below = edge < tiles ? __popc(s_on[edge][threadIdx.x] & bits_below(static_cast<int64_t>(edge) * kPoolTile + threadIdx.x * kTilePer, used)) : 0;
+  block_sum<kRowThreads>(below, s_warp, below);
+  below += __reduce_add_sync(0xffffffffu, lane < edge ? s_tile[lane] : 0);
+  const uint32_t on = s_on[me][threadIdx.x];
+  int total;
+  const int upto = before + block_sum<kRowThreads>(__popc(on), s_warp, total) - __popc(on);
+  write_moves(p, static_cast<int64_t>(me) * kPoolTile + threadIdx.x * kTilePer, on, upto, used, below);
+}
 
 // Pages in use of a tile.
 __global__ void __launch_bounds__(kRowThreads) compact_count_kernel(const PoolParams p) {
   __shared__ int s_warp[32];
   allow_next_kernel();
-  Counts<kTilePer> c;
-  c.load(p.refs, p.n_pages, static_cast<int64_t>(blockIdx.x) * kPoolTile + threadIdx.x * kTilePer);
-  int n = 0, total;
-#pragma unroll
-  for (int i = 0; i < kTilePer; ++i)
-    n += static_cast<int64_t>(blockIdx.x) * kPoolTile + threadIdx.x * kTilePer + i < p.n_pages && c.v[i] > 0;
-  block_sum<kRowThreads>(n, s_warp, total);
+  int total;
+  block_sum<kRowThreads>(__popc(in_use(p, static_cast<int64_t>(blockIdx.x) * kPoolTile + threadIdx.x * kTilePer)), s_warp, total);
   if (threadIdx.x == 0) p.scratch[blockIdx.x] = total;
 }
 
-// The moves: with U pages in use, the j-th one from number U on goes to the
-// j-th free one below.  map[page] = j for a page that moves, else -1.
 __global__ void __launch_bounds__(kRowThreads) compact_moves_kernel(const PoolParams p) {
   __shared__ int s_warp[32];
   allow_next_kernel();
   const int64_t tiles = pool_tiles(p.n_pages), me = blockIdx.x, page0 = me * kPoolTile + threadIdx.x * kTilePer;
-  int32_t* map = p.scratch + tiles;
-  Counts<kTilePer> c;
-  c.load(p.refs, p.n_pages, page0);
+  const uint32_t on = in_use(p, page0);
   wait_for_last_kernel();
   // pages in use before this tile, and in all
-  int before = 0, all = 0, used, below;
+  int before = 0, all = 0, used, below = 0, total;
   for (int64_t t = threadIdx.x; t < tiles; t += kRowThreads) {
     all += p.scratch[t];
     if (t < me) before += p.scratch[t];
   }
   block_sum<kRowThreads>(before, s_warp, before);
   block_sum<kRowThreads>(all, s_warp, used);
-  // pages in use below number `used`
-  int n = 0;
   const int64_t edge = used / kPoolTile;
-  for (int64_t t = threadIdx.x; t < edge; t += kRowThreads) n += p.scratch[t];
-#pragma unroll 4
-  for (int64_t q = edge * kPoolTile + threadIdx.x; q < used; q += kRowThreads) n += p.refs[q] > 0;
-  block_sum<kRowThreads>(n, s_warp, below);
-
-  n = 0;
-#pragma unroll
-  for (int i = 0; i < kTilePer; ++i) n += page0 + i < p.n_pages && c.v[i] > 0;
-  int total;
-  int upto = before + block_sum<kRowThreads>(n, s_warp, total) - n;  // pages in use before this one
-#pragma unroll
-  for (int i = 0; i < kTilePer; ++i) {
-    const int64_t page = page0 + i;
-    if (page >= p.n_pages) break;
-    const bool on = c.v[i] > 0, moves = on && page >= used;
-    const int64_t j = moves ? upto - below : page - upto;
-    upto += on;
-    map[page] = moves ? static_cast<int32_t>(j) : -1;
-    if (j >= p.n_moves) continue;
-    if (moves) p.src[j] = static_cast<int32_t>(page);
-    else if (!on && page < used) p.dst[j] = static_cast<int32_t>(page);
-  }
-  // behind the moves: as many as there are pages in use from number `used` on
-  for (int64_t j = used - below + me * kRowThreads + threadIdx.x; j < p.n_moves; j += tiles * kRowThreads) p.src[j] = p.dst[j] = -1;
+  for (int64_t t = threadIdx.x; t < edge; t += kRowThreads) below += p.scratch[t];
+  const int64_t edge0 = edge * kPoolTile + threadIdx.x * kTilePer;
+  below += __popc(in_use(p, edge0) & bits_below(edge0, used));
+  block_sum<kRowThreads>(below, s_warp, below);
+  const int upto = before + block_sum<kRowThreads>(__popc(on), s_warp, total) - __popc(on);
+  write_moves(p, page0, on, upto, used, below);
 }
 
 // Tables and counts follow.
@@ -314,7 +350,7 @@ __global__ void __launch_bounds__(kRowThreads) compact_apply_kernel(const PoolPa
 constexpr int kCopyThreads = 256;
 constexpr int kCopyUnits = 4;  // 16-byte units of a thread
 constexpr int kCopyBytes = kCopyThreads * kCopyUnits * 16;
-constexpr int kCopyWindow = 1024;  // pairs that are looked at together
+constexpr int kCopyWindow = 512;  // pairs that are looked at together
 
 struct CopyPair {
   int from, to;
@@ -336,34 +372,31 @@ __device__ __forceinline__ int64_t copy_chunks(const CopyPagesParams& p, const C
   return (static_cast<int64_t>(c.run) * p.heads + kCopyBytes / 16 - 1) / (kCopyBytes / 16);
 }
 
-__device__ __forceinline__ void copy_chunk(const CopyPagesParams& p, const CopyPair& c, int64_t chunk) {
-  const uint32_t step = static_cast<uint32_t>(p.blocks) * p.block_bytes / 16;
-  const int64_t units = static_cast<int64_t>(c.run) * p.heads, u0 = chunk * (kCopyBytes / 16) + threadIdx.x;
+__device__ __forceinline__ void copy_chunk(const CopyPagesParams& p, const CopyPair& c, int chunk) {
+  const uint32_t gap = static_cast<uint32_t>(p.blocks) * p.block_bytes / 16 - c.run;  // units of a head that are not copied
+  const uint32_t units = c.run * p.heads, u0 = chunk * (kCopyBytes / 16) + threadIdx.x;
   const uint4* s = reinterpret_cast<const uint4*>(p.pages + c.from * p.page_bytes);
   uint4* d = reinterpret_cast<uint4*>(p.pages + c.to * p.page_bytes);
   uint4 x[kCopyUnits];
-  int64_t at[kCopyUnits];
+  uint32_t at[kCopyUnits];
 #pragma unroll
   for (int k = 0; k < kCopyUnits; ++k) {
-    const int64_t u = u0 + k * kCopyThreads;
-    at[k] = -1;
-    if (u < units) {
-      at[k] = u + static_cast<int64_t>(static_cast<uint64_t>(u) * c.per_run >> 40) * (step - c.run);
-      x[k] = s[at[k]];
-    }
+    const uint32_t u = u0 + k * kCopyThreads;
+    at[k] = u + static_cast<uint32_t>(u * c.per_run >> 40) * gap;
+    if (u < units) x[k] = s[at[k]];
   }
 #pragma unroll
   for (int k = 0; k < kCopyUnits; ++k)
-    if (at[k] >= 0) d[at[k]] = x[k];
+    if (u0 + k * kCopyThreads < units) d[at[k]] = x[k];
 }
 
 // Every chunk of every pair in turn.
 __global__ void __launch_bounds__(kCopyThreads) copy_all_kernel(const CopyPagesParams p) {
-  const int64_t chunks = (p.page_bytes + kCopyBytes - 1) / kCopyBytes;
-  for (int64_t item = blockIdx.x; item < p.n * chunks; item += gridDim.x) {
+  const int64_t chunks = (p.page_bytes + kCopyBytes - 1) / kCopyBytes, all = p.n * chunks;
+  for (int64_t item = blockIdx.x; item < all; item += gridDim.x) {
     const int64_t i = div_small(item, chunks);
     const CopyPair c = copy_pair(p, i);
-    if (c.run) copy_chunk(p, c, item - i * chunks);
+    if (c.run) copy_chunk(p, c, static_cast<int>(item - i * chunks));
   }
 }
 
@@ -385,7 +418,7 @@ __global__ void __launch_bounds__(kCopyThreads) copy_gathered_kernel(const CopyP
       mine[k] = copy_pair(p, w0 + threadIdx.x * kPer + k);
       if (mine[k].run) ++n, chunks += copy_chunks(p, mine[k]);
     }
-    // (a page has less than 2^14 chunks)
+    // (a page has at most 2^14 chunks)
     int at = block_sum<kCopyThreads>(n, s_warp, pairs) - n;
     int64_t upto = block_sum<kCopyThreads>(static_cast<int>(chunks), s_warp, total) - chunks;
 #pragma unroll
@@ -406,7 +439,7 @@ __global__ void __launch_bounds__(kCopyThreads) copy_gathered_kernel(const CopyP
         if (s_upto[mid] <= c) lo = mid + 1;
         else hi = mid;
       }
-      copy_chunk(p, s_pair[lo], c - (lo > 0 ? s_upto[lo - 1] : 0));
+      copy_chunk(p, s_pair[lo], static_cast<int>(c - (lo > 0 ? s_upto[lo - 1] : 0)));
     }
     done += total;
     __syncthreads();
@@ -432,10 +465,15 @@ cudaError_t launch_pool_release(const PoolParams& p, cudaStream_t s) {
 
 cudaError_t launch_pool_compact(const PoolParams& p, cudaStream_t s) {
   const unsigned tiles = static_cast<unsigned>((p.n_pages + kPoolTile - 1) / kPoolTile);
-  compact_count_kernel<<<tiles, kRowThreads, 0, s>>>(p);
-  cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
-  e = launch_after(compact_moves_kernel, tiles, p, s, kRowThreads);
+  cudaError_t e;
+  if (tiles <= kFewTiles) {
+    compact_few_kernel<<<tiles, kRowThreads, 0, s>>>(p);
+    e = cudaGetLastError();
+  } else {
+    compact_count_kernel<<<tiles, kRowThreads, 0, s>>>(p);
+    e = cudaGetLastError();
+    if (e == cudaSuccess) e = launch_after(compact_moves_kernel, tiles, p, s, kRowThreads);
+  }
   if (e != cudaSuccess) return e;
   const int64_t items = p.n_seqs * p.table_stride > p.n_moves ? p.n_seqs * p.table_stride : p.n_moves;
   const int64_t blocks = (items + kRowThreads - 1) / kRowThreads;

@@ -28,18 +28,20 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;  // and tokens of a block, at most
-constexpr int kWarpRows = 8;
+// Rows of a warp: what it has on its way is 2 kB of fp32, as of the 16-bit types.
+template <typename T>
+constexpr int kRowsOf = sizeof(T) == 4 ? 4 : 8;
 
-// Warps of a token: for its queries, keys and values.
-__host__ __device__ __forceinline__ int row_warps(int heads) { return (heads + kWarpRows - 1) / kWarpRows; }
+// Warps of a token's queries, keys or values.
+__host__ __device__ __forceinline__ int row_warps(int heads, int rows) { return (heads + rows - 1) / rows; }
 
 enum { kNone, kWhole, kAny, kNext };
 
 // FMT 0: rows only, no cache.
 template <int FMT, int D, typename T>
-__global__ void __launch_bounds__(kThreads, 3) rope_kernel(const RopeParams p) {
+__global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 4 : 3) rope_kernel(const RopeParams p) {
   constexpr int kLanes = D / 8, kAt = 32 / kLanes;  // kAt rows at a time
-  constexpr int kPasses = kWarpRows / kAt;
+  constexpr int kWarpRows = kRowsOf<T>, kPasses = kWarpRows / kAt;
   // Cosines and sines of a token's D / 2 pairs, as quads of pairs 4 i .. 4 i + 3:
   // the even quads first, so that neighbouring lanes, two quads each, read
   // neighbouring ones.
@@ -47,7 +49,7 @@ __global__ void __launch_bounds__(kThreads, 3) rope_kernel(const RopeParams p) {
   __shared__ float s_row[kWarps][kAt][D];
   const unsigned full = 0xffffffffu;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, n = p.pairs;
-  const int H = FMT ? p.cache.kv_heads : 0, q_warps = row_warps(p.q_heads), k_warps = row_warps(H), per = q_warps + 2 * k_warps;
+  const int H = FMT ? p.cache.kv_heads : 0, q_warps = row_warps(p.q_heads, kWarpRows), k_warps = row_warps(H, kWarpRows), per = q_warps + 2 * k_warps;
   // the block's warps are w0 .. of all, the first of them warp `r0` of token t0
   const int64_t w0 = static_cast<int64_t>(blockIdx.x) * kWarps, t0 = div_small(w0, per);
   const unsigned r0 = static_cast<unsigned>(w0 - t0 * per), mine = (r0 + warp) / static_cast<unsigned>(per);
@@ -188,7 +190,8 @@ __global__ void __launch_bounds__(kThreads, 3) rope_kernel(const RopeParams p) {
 
 cudaError_t launch_rope(const RopeParams& p, int dtype, int head_dim, cudaStream_t s) {
   const int H = p.cache.pages ? p.cache.kv_heads : 0;
-  const int64_t warps = p.n_tokens * (row_warps(p.q_heads) + 2 * row_warps(H));
+  const int rows = dtype == QGEMV_DT_F32 ? kRowsOf<float> : kRowsOf<__half>;
+  const int64_t warps = p.n_tokens * (row_warps(p.q_heads, rows) + 2 * row_warps(H, rows));
   const int64_t grid = (warps + kWarps - 1) / kWarps;
   if (grid > 0x7fffffff) return cudaErrorInvalidConfiguration;
   auto go = [&](auto kernel) {

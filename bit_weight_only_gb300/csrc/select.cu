@@ -39,6 +39,17 @@ __device__ __forceinline__ int8_t code_of(float x, float a) {
   return static_cast<int8_t>(a > 0.f ? static_cast<int>(q) : 0);
 }
 
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float min_nan(float a, float b) {
+  float r;
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
 constexpr int kSummaryThreads = 128;
 
 // W warps, one or the block's four, for a head of a page, each for a run of its
@@ -58,37 +69,59 @@ __global__ void __launch_bounds__(kSummaryThreads) summary_kernel(const SummaryP
   const int64_t page = __ldg(p.pages + i);
   if (page < 0 || page >= p.cache.n_pages) return;
   const int d0 = (lane % kLanes) * 8, run = p.cache.page_tokens / W, t1 = (part + 1) * run;
+  // NaN stays in the largest and smallest values, infinities show in them
   float hi[8], lo[8];
+  auto fetch = [&](Eight<FMT, D>& x, int t) {
+    x.load(kv_block<FMT, D>(p.cache, page, head, t / kKvBlockTokens), false, t % kKvBlockTokens, d0);
+  };
+  const int first = part * run + lane / kLanes;
+  if constexpr (FMT == QGEMV_KV_F16) {
+    __half2 h[4], l[4];
 #pragma unroll
-  for (int e = 0; e < 8; ++e) hi[e] = -INFINITY, lo[e] = INFINITY;
-  bool bad = false;
-  for (int t0 = part * run + lane / kLanes; t0 < t1; t0 += kAt * kAhead) {
-    Eight<FMT, D> x[kAhead];
+    for (int e = 0; e < 4; ++e) h[e] = __half2half2(__ushort_as_half(0xfc00)), l[e] = __half2half2(__ushort_as_half(0x7c00));
+    for (int t0 = first; t0 < t1; t0 += kAt * kAhead) {
+      Eight<FMT, D> x[kAhead];
 #pragma unroll
-    for (int k = 0; k < kAhead; ++k) {
-      const int t = min(t0 + k * kAt, t1 - 1);  // (a token twice changes nothing)
-      x[k].load(kv_block<FMT, D>(p.cache, page, head, t / kKvBlockTokens), false, t % kKvBlockTokens, d0);
+      for (int k = 0; k < kAhead; ++k) fetch(x[k], min(t0 + k * kAt, t1 - 1));  // (a token twice changes nothing)
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const __half2 v = *reinterpret_cast<const __half2*>(&(&x[k].w.x)[e]);
+          h[e] = __hmax2_nan(h[e], v), l[e] = __hmin2_nan(l[e], v);
+        }
+      }
     }
 #pragma unroll
-    for (int k = 0; k < kAhead; ++k) {
-      float v[8], odd = 0.f;
-      x[k].values(v);
+    for (int e = 0; e < 4; ++e) {
+      const float2 a = __half22float2(h[e]), b = __half22float2(l[e]);
+      hi[2 * e] = a.x, hi[2 * e + 1] = a.y, lo[2 * e] = b.x, lo[2 * e + 1] = b.y;
+    }
+  } else {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        odd = fmaf(v[e], 0.f, odd);  // NaN for an infinity or NaN
-        hi[e] = fmaxf(hi[e], v[e]);
-        lo[e] = fminf(lo[e], v[e]);
+    for (int e = 0; e < 8; ++e) hi[e] = -INFINITY, lo[e] = INFINITY;
+    for (int t0 = first; t0 < t1; t0 += kAt * kAhead) {
+      Eight<FMT, D> x[kAhead];
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k) fetch(x[k], min(t0 + k * kAt, t1 - 1));
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k) {
+        float v[8];
+        x[k].values(v);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) hi[e] = max_nan(hi[e], v[e]), lo[e] = min_nan(lo[e], v[e]);
       }
-      bad |= odd != 0.f;
     }
   }
+  bool bad = false;
 #pragma unroll
-  for (int o = kLanes; o < 32; o <<= 1) {
+  for (int e = 0; e < 8; ++e) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      hi[e] = fmaxf(hi[e], __shfl_xor_sync(full, hi[e], o));
-      lo[e] = fminf(lo[e], __shfl_xor_sync(full, lo[e], o));
+    for (int o = kLanes; o < 32; o <<= 1) {
+      hi[e] = max_nan(hi[e], __shfl_xor_sync(full, hi[e], o));
+      lo[e] = min_nan(lo[e], __shfl_xor_sync(full, lo[e], o));
     }
+    bad |= !(fabsf(hi[e]) < INFINITY) || !(fabsf(lo[e]) < INFINITY);
   }
   bad = __any_sync(full, bad);
   // lanes of a token have eight channels each: those of the first hi, of the second lo
@@ -122,10 +155,11 @@ __global__ void __launch_bounds__(kSummaryThreads) summary_kernel(const SummaryP
   const float a = bad ? __int_as_float(0x7fffffff) : __fdiv_rn(m, 127.f);
   const int64_t row = page * H + head;
   if (lane < 2 * kLanes) {
-    uint32_t w[2] = {0, 0};
-#pragma unroll
-    for (int e = 0; e < 8; ++e) w[e >> 2] |= (static_cast<uint32_t>(code_of(x[e], a)) & 0xffu) << (8 * (e & 3));
-    *reinterpret_cast<uint2*>(p.codes + row * 2 * D + low * D + d0) = make_uint2(w[0], w[1]);
+    uint32_t q[8];
+    round_quotients<false>(x, a, q);  // 0 where a is 0 or NaN
+    *reinterpret_cast<uint2*>(p.codes + row * 2 * D + low * D + d0) =
+        make_uint2(__byte_perm(__byte_perm(q[0], q[1], 0x0040), __byte_perm(q[2], q[3], 0x0040), 0x5410),
+                   __byte_perm(__byte_perm(q[4], q[5], 0x0040), __byte_perm(q[6], q[7], 0x0040), 0x5410));
   }
   if (lane == 0) p.scales[row] = a;
 }
@@ -345,9 +379,9 @@ __global__ void __launch_bounds__(kThreads, 1) select_kernel(const SelectParams 
     }
   }
 
-  // ---- the pages, in order: a warp for a run of keys, kKeys / 2 of a lane at a time
-  constexpr int kAt = kKeys / 2;
-  const int run = (pages + kWarps * kAt * 32 - 1) / (kWarps * kAt * 32) * (kAt * 32), r0 = warp * run + lane, r1 = min(warp * run + run, pages);
+  // ---- the pages, in order: a warp for a run of keys
+  constexpr int kAt = kKeys;
+  const int run = (pages + kThreads - 1) / kThreads * 32, r0 = warp * run + lane, r1 = min(warp * run + run, pages);
   int above = 0, equal = 0;
   for (int k0 = r0; k0 - lane < r1; k0 += kAt * 32) {
 #pragma unroll

@@ -898,9 +898,9 @@ class KVCache:
             raise QgemvError(QGEMV_ERR_ARG, f"n_select={n_select} is not in [0, 2^20]")
         if out is None:
             empty = torch.empty if stream is None else _empty_on(stream, dev)
-            out = (empty((n_seqs, self.kv_heads, width), dtype=torch.int32, device=self.device),
-                   empty((n_seqs,), dtype=torch.int32, device=self.device))
-            to = out[0].data_ptr(), out[1].data_ptr()
+            pages = empty((n_seqs, self.kv_heads, width), dtype=torch.int32, device=self.device)
+            lens = empty((n_seqs,), dtype=torch.int32, device=self.device)
+            out, to = (pages, lens), (pages.data_ptr(), lens.data_ptr())
         else:
             to = (_index("pages", out[0], torch.int32, (n_seqs, self.kv_heads, width), dev),
                   _index("lens", out[1], torch.int32, (n_seqs,), dev))
@@ -1014,15 +1014,21 @@ class PagePool:
         get one each, and ``copy_pages(src, dst, tokens)`` of every cache
         copies its tokens."""
         torch, dev = _torch(), self._dev
+        i32 = torch.int32
         rows, stride = table.shape
         n, = parents.shape
-        empty = torch.empty if stream is None else _empty_on(stream, dev)
-        new = empty((n, stride), dtype=torch.int32, device=self.device)
-        src, dst, tokens = (empty((n,), dtype=torch.int32, device=self.device) for _ in range(3))
-        _call(dev, _lib.qgemv_pool_fork, self.refs.data_ptr(), self.n_pages, self.page_tokens,
-              self._ints("table", table, rows, stride), stride, rows, self._ints("parents", parents, n), n,
-              self._ints("lens", lens, rows), new.data_ptr(), src.data_ptr(), dst.data_ptr(), tokens.data_ptr(),
-              self._state.data_ptr(), _on(stream, dev))
+        old = _index("table", table, i32, (rows, stride), dev)
+        ups, ls = _index("parents", parents, i32, (n,), dev), _index("lens", lens, i32, (rows,), dev)
+        if stream is None:
+            like = torch.empty_like
+            new = like(table) if n == rows else torch.empty((n, stride), dtype=i32, device=self.device)
+            src, dst, tokens = like(parents), like(parents), like(parents)
+        else:
+            empty = _empty_on(stream, dev)
+            new = empty((n, stride), dtype=i32, device=self.device)
+            src, dst, tokens = (empty((n,), dtype=i32, device=self.device) for _ in range(3))
+        _call(dev, _lib.qgemv_pool_fork, self.refs.data_ptr(), self.n_pages, self.page_tokens, old, stride, rows, ups, n, ls,
+              new.data_ptr(), src.data_ptr(), dst.data_ptr(), tokens.data_ptr(), self._state.data_ptr(), _on(stream, dev))
         return new, src, dst, tokens
 
     def release(self, table, lens, keep=None, stream=None):
