@@ -241,7 +241,8 @@ __device__ __forceinline__ void choose(const BeamParams& p, int64_t seq) {
   auto score_of = [&](int b, float x) { return ordered64(s.base[b] + static_cast<double>(x)); };
   auto about = [&](int i) -> float {  // -infinity: no candidates
     const double base = s.base[i / C];
-    return base > -INFINITY ? static_cast<float>(base) + __ldcg(&chunks[i].x) : -INFINITY;
+    const float x = __ldcg(&chunks[i].x);
+    return base > -INFINITY && x > -INFINITY ? fminf(fmaxf(static_cast<float>(base) + x, -FLT_MAX), FLT_MAX) : -INFINITY;
   };
   if (tid < p.beams && s.base[tid] > -INFINITY) atomicMax(&s.far, __float_as_uint(fabsf(static_cast<float>(s.base[tid]))));
   float best = -INFINITY;
@@ -313,7 +314,8 @@ __device__ __forceinline__ void choose(const BeamParams& p, int64_t seq) {
       } else {
         units.edge(c, x);
       }
-      least = from > -INFINITY ? less(from - static_cast<float>(s.base[b])) : -FLT_MAX;
+      least = less(from - static_cast<float>(s.base[b]));
+      if (!(least > -INFINITY && least < INFINITY)) least = -FLT_MAX;  // (also where fp32 ends)
     };
     // to the candidates with their places and, for the time being, values
     auto add = [&] {

@@ -647,6 +647,16 @@ def _gpu(what, device) -> None:
         raise ValueError(f"{what} must be on a CUDA device, not {device}")
 
 
+def _settle(dev: int) -> None:
+    """Wait for what the current stream sets up, so that any stream may use it first (while a graph is captured the
+    setting up is part of it)."""
+    torch = _torch()
+    stream = torch.cuda.current_stream(dev)
+    with torch.cuda.stream(stream):
+        if not torch.cuda.is_current_stream_capturing():
+            stream.synchronize()
+
+
 def _dtype_code(dtype) -> int:
     global _DTYPES
     if _DTYPES is None:
@@ -748,7 +758,7 @@ class Rotary:
         self.head_dim, self.pairs, self.axes, self.pairing = head_dim, n, len(sections), ROPE_PAIRINGS[pairs]
         self.plan = torch.from_numpy(plan).to(device)
         self.ptr, self._dev = self.plan.data_ptr(), self.plan.get_device()
-        torch.cuda.current_stream(self._dev).synchronize()  # any stream may use it first
+        _settle(self._dev)
 
     def rotate(self, x, positions, dtype=None, out=None, stream=None):
         """The rows x [n, heads, head_dim] turned to the positions (int32 [n,
@@ -961,7 +971,7 @@ class KeySummary:
         shape = cache.n_pages, cache.kv_heads
         self.codes = torch.zeros(*shape, 2, cache.head_dim, dtype=torch.int8, device=cache.device)
         self.scales = torch.zeros(shape, dtype=torch.float32, device=cache.device)
-        torch.cuda.current_stream(cache._dev).synchronize()  # any stream may use it first
+        _settle(cache._dev)
 
     def update(self, pages, stream=None):
         """Take the summaries of the pages (int32 [n]; numbers that are no page
@@ -993,7 +1003,7 @@ class PagePool:
         self._state = torch.zeros(2, dtype=torch.int32, device=device)  # pages that were missing; the calls' own
         self._ws = torch.empty(nbytes // 4, dtype=torch.int32, device=device)
         self._dev, self.device = self.refs.get_device(), self.refs.device
-        torch.cuda.current_stream(self._dev).synchronize()  # any stream may use it first
+        _settle(self._dev)
 
     def _ints(self, name, t, *shape):
         return _index(name, t, _torch().int32, shape, self._dev)
@@ -1116,7 +1126,7 @@ class BeamWorkspace:
         _gpu("a workspace", device)
         self.buffer = torch.zeros(self.nbytes, dtype=torch.uint8, device=device)
         self.ptr, self._dev = self.buffer.data_ptr(), self.buffer.get_device()
-        torch.cuda.current_stream(self._dev).synchronize()  # any stream may use it first
+        _settle(self._dev)
 
 
 def beam_select(logits, scores, width: int, *, workspace, out=None, stream=None):

@@ -192,6 +192,24 @@ def test_large_logits_and_scores():
     assert parents[0].tolist() == [1, 0] and tokens[0].tolist() == [5, 5] and float(out[0, 0]) == float(out[0, 1])
 
 
+@pytest.mark.parametrize("size", [1e20, 3e38])
+def test_scores_at_the_ends_of_fp32(size):
+    """Beams that far scores set apart; a sum past fp32 is infinite as a result, and in its order."""
+    x = draw(8, 6, 3000)
+    s = torch.tensor([[size, -size, size], [-size, 0.0, -1.0]], device="cuda")
+    out, parents, tokens = select(x, s, 12)
+    # of the first sequence beams 0 and 2 are alike up to their logits, which vanish beside the scores: ties go to beam 0 and
+    # the lower token
+    assert bool((parents[0] == 0).all()) and torch.equal(tokens[0], torch.arange(12, dtype=torch.int32, device="cuda"))
+    assert bool((out[0] == size).all())
+    assert set(parents[1].tolist()) <= {1, 2} and bool(torch.isfinite(out[1]).all())
+    check(x[4:6], s[1:, 1:], 12, (out[1:], parents[1:] - 1, tokens[1:]))
+    y = x * 0 + 3e38
+    y[0, 7] = 3.2e38
+    out, parents, tokens = select(y[:1], torch.tensor([[size]], device="cuda"), 2)
+    assert tokens[0, 0] == 7 and bool((parents == 0).all())
+
+
 def test_rows_past_32_bits():
     """Rows that start beyond 2^32 bytes and elements."""
     n = 1 << 22
