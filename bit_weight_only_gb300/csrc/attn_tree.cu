@@ -267,6 +267,7 @@ __global__ void __launch_bounds__(TreeShape<FMT, D, NT>::kThreads, kBlocksPerSm)
     const int R = sg.T * a.G, row0 = sg.tile * Sh::kRows;
     const int64_t q0 = p.cu_q[seq];
     const int ctx = sg.ctx, all = ctx + sg.T;
+    const int32_t* table = table_row(p, seq, head);
 
     // ---- this warp's units: u0 + warp + W * k
     const int n_mine = static_cast<int>((u1 - u0 - warp + W - 1) / W);
@@ -278,7 +279,7 @@ __global__ void __launch_bounds__(TreeShape<FMT, D, NT>::kThreads, kBlocksPerSm)
         const int64_t pi = (u * kKvBlockTokens) >> a.page_shift;
         src_of = 0;
         if (k + lane < n_mine && pi < p.table_stride) {
-          const int page = __ldg(table_row(p, seq, head) + pi);
+          const int page = __ldg(table + pi);
           if (page >= 0 && page < p.cache.n_pages)
             src_of = reinterpret_cast<unsigned long long>(
                 kv_block<FMT, D>(p.cache, page, head, static_cast<int>(u & ((p.cache.page_tokens >> 4) - 1))));

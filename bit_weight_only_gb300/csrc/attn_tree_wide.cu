@@ -585,12 +585,13 @@ __global__ void __launch_bounds__(kThreads, 1) tree_wide_kernel(const TreeArgs a
       while (ok && work.next(a, sg)) {
         const int n = static_cast<int>(sg.u1 - sg.u0);
         const int64_t n_pos = static_cast<int64_t>(sg.ctx) + sg.T;
+        const int32_t* table = table_row(p, sg.seq, sg.head);
         // lane b < 8: the page of block b of a unit, looked up a unit ahead
         auto page_of = [&](int j) -> int64_t {
           const int64_t pos = (sg.u0 + j) * kKeys + kKvBlockTokens * (lane & 7);
           const int64_t pi = pos >> a.page_shift;
           if (j >= n || pos >= n_pos || pi >= p.table_stride) return -1;
-          const int64_t pg = __ldg(table_row(p, sg.seq, sg.head) + pi);
+          const int64_t pg = __ldg(table + pi);
           return pg < p.cache.n_pages ? pg : -1;
         };
         int64_t ahead = page_of(0);
