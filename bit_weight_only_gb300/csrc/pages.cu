@@ -350,6 +350,7 @@ __global__ void __launch_bounds__(kRowThreads) compact_apply_kernel(const PoolPa
 constexpr int kCopyThreads = 256;
 constexpr int kCopyUnits = 4;  // 16-byte units of a thread
 constexpr int kCopyBytes = kCopyThreads * kCopyUnits * 16;
+constexpr int kCopyBlocks = 6;     // on an SM
 constexpr int kCopyWindow = 512;  // pairs that are looked at together
 
 struct CopyPair {
@@ -391,7 +392,7 @@ __device__ __forceinline__ void copy_chunk(const CopyPagesParams& p, const CopyP
 }
 
 // Every chunk of every pair in turn.
-__global__ void __launch_bounds__(kCopyThreads) copy_all_kernel(const CopyPagesParams p) {
+__global__ void __launch_bounds__(kCopyThreads, kCopyBlocks) copy_all_kernel(const CopyPagesParams p) {
   const int64_t chunks = (p.page_bytes + kCopyBytes - 1) / kCopyBytes, all = p.n * chunks;
   for (int64_t item = blockIdx.x; item < all; item += gridDim.x) {
     const int64_t i = div_small(item, chunks);
@@ -403,7 +404,7 @@ __global__ void __launch_bounds__(kCopyThreads) copy_all_kernel(const CopyPagesP
 // Blocks take the chunks of the pairs that are to be copied in turn: those pairs
 // are gathered first, kCopyWindow at a time, so that pairs without a page, or
 // with few tokens, leave no block without work.
-__global__ void __launch_bounds__(kCopyThreads) copy_gathered_kernel(const CopyPagesParams p) {
+__global__ void __launch_bounds__(kCopyThreads, kCopyBlocks) copy_gathered_kernel(const CopyPagesParams p) {
   __shared__ CopyPair s_pair[kCopyWindow];
   __shared__ int64_t s_upto[kCopyWindow];  // chunks of the pairs up to and with this one
   __shared__ int s_warp[32];
@@ -488,7 +489,7 @@ cudaError_t launch_copy_pages(const CopyPagesParams& p, cudaStream_t s) {
   // (128 beams, 57 pages of 1 MB in part: 11.9 us against 14.2), but for chunks
   // that run all at once.  Whole pages, as a packing has them, one behind the
   // other: as they come (2200 of 9001 Q4_0 pages of 74 kB: 55 us against 67).
-  const int64_t items = p.n * ((p.page_bytes + kCopyBytes - 1) / kCopyBytes), most = 8 * static_cast<int64_t>(sms);
+  const int64_t items = p.n * ((p.page_bytes + kCopyBytes - 1) / kCopyBytes), most = kCopyBlocks * static_cast<int64_t>(sms);
   const unsigned grid = static_cast<unsigned>(items < most ? items : most);
   if (items <= most || !p.tokens) copy_all_kernel<<<grid, kCopyThreads, 0, s>>>(p);
   else copy_gathered_kernel<<<grid, kCopyThreads, 0, s>>>(p);

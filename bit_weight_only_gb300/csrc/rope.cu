@@ -28,20 +28,23 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;  // and tokens of a block, at most
-// Rows of a warp: what it has on its way is 2 kB of fp32, as of the 16-bit types.
-template <typename T>
-constexpr int kRowsOf = sizeof(T) == 4 ? 4 : 8;
+constexpr int kWarpRows = 8;
 
 // Warps of a token's queries, keys or values.
-__host__ __device__ __forceinline__ int row_warps(int heads, int rows) { return (heads + rows - 1) / rows; }
+__host__ __device__ __forceinline__ int row_warps(int heads) { return (heads + kWarpRows - 1) / kWarpRows; }
+
+// Four floats of shared memory, read where it is written.
+__device__ __forceinline__ void lds_here(const float4* p, float* x) {
+  asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(x[0]), "=f"(x[1]), "=f"(x[2]), "=f"(x[3]) : "r"(smem_u32(p)));
+}
 
 enum { kNone, kWhole, kAny, kNext };
 
 // FMT 0: rows only, no cache.
 template <int FMT, int D, typename T>
-__global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 4 : 3) rope_kernel(const RopeParams p) {
+__global__ void __launch_bounds__(kThreads, 4) rope_kernel(const RopeParams p) {
   constexpr int kLanes = D / 8, kAt = 32 / kLanes;  // kAt rows at a time
-  constexpr int kWarpRows = kRowsOf<T>, kPasses = kWarpRows / kAt;
+  constexpr int kPasses = kWarpRows / kAt;
   // Cosines and sines of a token's D / 2 pairs, as quads of pairs 4 i .. 4 i + 3:
   // the even quads first, so that neighbouring lanes, two quads each, read
   // neighbouring ones.
@@ -49,7 +52,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 4 : 3) rope_kernel(
   __shared__ float s_row[kWarps][kAt][D];
   const unsigned full = 0xffffffffu;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, n = p.pairs;
-  const int H = FMT ? p.cache.kv_heads : 0, q_warps = row_warps(p.q_heads, kWarpRows), k_warps = row_warps(H, kWarpRows), per = q_warps + 2 * k_warps;
+  const int H = FMT ? p.cache.kv_heads : 0, q_warps = row_warps(p.q_heads), k_warps = row_warps(H), per = q_warps + 2 * k_warps;
   // the block's warps are w0 .. of all, the first of them warp `r0` of token t0
   const int64_t w0 = static_cast<int64_t>(blockIdx.x) * kWarps, t0 = div_small(w0, per);
   const unsigned r0 = static_cast<unsigned>(w0 - t0 * per), mine = (r0 + warp) / static_cast<unsigned>(per);
@@ -104,37 +107,6 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 4 : 3) rope_kernel(
   // ---- the rows, by the way in which a value meets the other one of its pair
   auto rows = [&](auto how) {
     constexpr int kHow = decltype(how)::value;  // kWhole, kAny, kNext: halves; neighbours; kNone: values
-    // y = x c + other s, with -s for the first of a pair
-    float c[8], s[8];
-    if constexpr (kHow != kNone) {
-      auto quad = [&](int q, float* cc, float* ss) {
-        const float4 a = s_cos[mine][(q & 1) * (D / 16) + (q >> 1)], b = s_sin[mine][(q & 1) * (D / 16) + (q >> 1)];
-        cc[0] = a.x, cc[1] = a.y, cc[2] = a.z, cc[3] = a.w;
-        ss[0] = b.x, ss[1] = b.y, ss[2] = b.z, ss[3] = b.w;
-      };
-      if constexpr (kHow == kNext) {
-        float cc[4], ss[4];
-        quad(d0 / 8, cc, ss);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) c[e] = cc[e / 2], s[e] = e & 1 ? ss[e / 2] : -ss[e / 2];
-      } else if constexpr (kHow == kWhole) {
-        const int j0 = d0 < n ? d0 : d0 < 2 * n ? d0 - n : 0;
-        quad(j0 / 4, c, s);
-        quad(j0 / 4 + 1, c + 4, s + 4);
-        if (d0 < n) {
-#pragma unroll
-          for (int e = 0; e < 8; ++e) s[e] = -s[e];
-        }
-      } else {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const int i = d0 + e, j = i < n ? i : i < 2 * n ? i - n : 0, q = ((j >> 2) & 1) * (D / 16) + (j >> 3);
-          c[e] = reinterpret_cast<const float*>(&s_cos[mine][q])[j & 3];
-          const float x = reinterpret_cast<const float*>(&s_sin[mine][q])[j & 3];
-          s[e] = i < n ? -x : x;
-        }
-      }
-    }
 #pragma unroll
     for (int i = 0; i < kPasses; ++i) {
       const int row = row0 + i * kAt + lane / kLanes;
@@ -158,6 +130,35 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 4 : 3) rope_kernel(
           __syncwarp();
 #pragma unroll
           for (int e = 0; e < 8; ++e) y[e] = d0 + e < 2 * n ? here[d0 + e < n ? d0 + e + n : d0 + e - n] : 0.f;
+        }
+        // y = x c + other s, with -s for the first of a pair: read for each pass (held
+        // for all of them they would take a quarter of the registers)
+        float c[8], s[8];
+        auto quad = [&](int q, float* cc, float* ss) {
+          lds_here(&s_cos[mine][(q & 1) * (D / 16) + (q >> 1)], cc);
+          lds_here(&s_sin[mine][(q & 1) * (D / 16) + (q >> 1)], ss);
+        };
+        if constexpr (kHow == kNext) {
+          float cc[4], ss[4];
+          quad(d0 / 8, cc, ss);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) c[e] = cc[e / 2], s[e] = e & 1 ? ss[e / 2] : -ss[e / 2];
+        } else if constexpr (kHow == kWhole) {
+          const int j0 = d0 < n ? d0 : d0 < 2 * n ? d0 - n : 0;
+          quad(j0 / 4, c, s);
+          quad(j0 / 4 + 1, c + 4, s + 4);
+          if (d0 < n) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) s[e] = -s[e];
+          }
+        } else {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const int i = d0 + e, j = i < n ? i : i < 2 * n ? i - n : 0, q = ((j >> 2) & 1) * (D / 16) + (j >> 3);
+            c[e] = reinterpret_cast<const float*>(&s_cos[mine][q])[j & 3];
+            const float v = reinterpret_cast<const float*>(&s_sin[mine][q])[j & 3];
+            s[e] = i < n ? -v : v;
+          }
         }
 #pragma unroll
         for (int e = 0; e < 8; e += 2) {
@@ -190,8 +191,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 4 : 3) rope_kernel(
 
 cudaError_t launch_rope(const RopeParams& p, int dtype, int head_dim, cudaStream_t s) {
   const int H = p.cache.pages ? p.cache.kv_heads : 0;
-  const int rows = dtype == QGEMV_DT_F32 ? kRowsOf<float> : kRowsOf<__half>;
-  const int64_t warps = p.n_tokens * (row_warps(p.q_heads, rows) + 2 * row_warps(H, rows));
+  const int64_t warps = p.n_tokens * (row_warps(p.q_heads) + 2 * row_warps(H));
   const int64_t grid = (warps + kWarps - 1) / kWarps;
   if (grid > 0x7fffffff) return cudaErrorInvalidConfiguration;
   auto go = [&](auto kernel) {

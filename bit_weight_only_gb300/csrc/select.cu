@@ -56,9 +56,9 @@ constexpr int kSummaryThreads = 128;
 // tokens.  Keys with an infinity or NaN leave codes of 0 and a scale of NaN: such
 // a page comes before all others.
 template <int FMT, int D, int W>
-__global__ void __launch_bounds__(kSummaryThreads) summary_kernel(const SummaryParams p) {
+__global__ void __launch_bounds__(kSummaryThreads, W > 1 ? 1 : 8) summary_kernel(const SummaryParams p) {
   constexpr int kLanes = D / 8, kAt = 32 / kLanes;  // kAt tokens at a time
-  constexpr int kAhead = W > 1 ? 8 : 4;
+  constexpr int kLoads = kKvBlockTokens / kAt;       // of a block of tokens
   __shared__ float s_edge[2][W][D];
   __shared__ int s_bad[W];
   const unsigned full = 0xffffffffu;
@@ -71,27 +71,40 @@ __global__ void __launch_bounds__(kSummaryThreads) summary_kernel(const SummaryP
   const int d0 = (lane % kLanes) * 8, run = p.cache.page_tokens / W, t1 = (part + 1) * run;
   // NaN stays in the largest and smallest values, infinities show in them
   float hi[8], lo[8];
-  auto fetch = [&](Eight<FMT, D>& x, int t) {
-    x.load(kv_block<FMT, D>(p.cache, page, head, t / kKvBlockTokens), false, t % kKvBlockTokens, d0);
+  // use(values) of this lane's eight of each token of the run, a block of tokens (or
+  // the run's part of one) at a time, all of it on its way together
+  auto every = [&](auto use) {
+    const int here = min(run, kKvBlockTokens);
+    for (int t0 = part * run; t0 < t1; t0 += kKvBlockTokens) {
+      const uint8_t* b = kv_block<FMT, D>(p.cache, page, head, t0 / kKvBlockTokens);
+      const int t = t0 % kKvBlockTokens + lane / kLanes;
+      Eight<FMT, D> x[kLoads];
+      if (here == kKvBlockTokens) {
+#pragma unroll
+        for (int k = 0; k < kLoads; ++k) x[k].load(b, false, t + k * kAt, d0);
+#pragma unroll
+        for (int k = 0; k < kLoads; ++k) use(x[k]);
+      } else {
+        for (int k = 0; k * kAt < here; k += 2) {  // four or eight tokens
+          x[0].load(b, false, t + k * kAt, d0);
+          x[1].load(b, false, t + min(k + 1, here / kAt - 1) * kAt, d0);  // (a token twice changes nothing)
+          use(x[0]);
+          use(x[1]);
+        }
+      }
+    }
   };
-  const int first = part * run + lane / kLanes;
   if constexpr (FMT == QGEMV_KV_F16) {
     __half2 h[4], l[4];
 #pragma unroll
     for (int e = 0; e < 4; ++e) h[e] = __half2half2(__ushort_as_half(0xfc00)), l[e] = __half2half2(__ushort_as_half(0x7c00));
-    for (int t0 = first; t0 < t1; t0 += kAt * kAhead) {
-      Eight<FMT, D> x[kAhead];
+    every([&](const Eight<FMT, D>& x) {
 #pragma unroll
-      for (int k = 0; k < kAhead; ++k) fetch(x[k], min(t0 + k * kAt, t1 - 1));  // (a token twice changes nothing)
-#pragma unroll
-      for (int k = 0; k < kAhead; ++k) {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const __half2 v = *reinterpret_cast<const __half2*>(&(&x[k].w.x)[e]);
-          h[e] = __hmax2_nan(h[e], v), l[e] = __hmin2_nan(l[e], v);
-        }
+      for (int e = 0; e < 4; ++e) {
+        const __half2 v = *reinterpret_cast<const __half2*>(&(&x.w.x)[e]);
+        h[e] = __hmax2_nan(h[e], v), l[e] = __hmin2_nan(l[e], v);
       }
-    }
+    });
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       const float2 a = __half22float2(h[e]), b = __half22float2(l[e]);
@@ -100,18 +113,12 @@ __global__ void __launch_bounds__(kSummaryThreads) summary_kernel(const SummaryP
   } else {
 #pragma unroll
     for (int e = 0; e < 8; ++e) hi[e] = -INFINITY, lo[e] = INFINITY;
-    for (int t0 = first; t0 < t1; t0 += kAt * kAhead) {
-      Eight<FMT, D> x[kAhead];
+    every([&](const Eight<FMT, D>& x) {
+      float v[8];
+      x.values(v);
 #pragma unroll
-      for (int k = 0; k < kAhead; ++k) fetch(x[k], min(t0 + k * kAt, t1 - 1));
-#pragma unroll
-      for (int k = 0; k < kAhead; ++k) {
-        float v[8];
-        x[k].values(v);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) hi[e] = max_nan(hi[e], v[e]), lo[e] = min_nan(lo[e], v[e]);
-      }
-    }
+      for (int e = 0; e < 8; ++e) hi[e] = max_nan(hi[e], v[e]), lo[e] = min_nan(lo[e], v[e]);
+    });
   }
   bool bad = false;
 #pragma unroll
