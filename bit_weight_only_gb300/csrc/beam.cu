@@ -7,14 +7,15 @@
 // each chunk of 512: its largest value m and the sum of exp(x - m).  A warp for a
 // chunk, with nothing to wait for but its loads: it takes many warps to have
 // enough bytes on their way (512 rows of 128000 tokens: 65 us with lists of
-// candidates kept during the pass, 96 with warps that take several chunks).  Then,
-// by a block for each sequence, the beams' log sums and each chunk's best score
-// are known; the `width`-th largest of its threads' best chunks bounds the result
-// from below, so that only the chunks that reach it, little more than `width`, are
-// read again, the best ones first, and their values ranked.
-//
-// Where all chunks are summed up at once, the block that has a sequence's last
-// one goes on with the choice; else the choice is a kernel of its own.
+// candidates kept during the pass, 96 with warps that take several chunks; 38 so,
+// 6.9 TB/s in bf16).  Then, by a block for each sequence, the beams' log sums and
+// each chunk's best score are known; the `width`-th largest of its threads' best
+// chunks bounds the result from below, so that only the chunks that reach it,
+// little more than `width`, are read again, the best ones first, and their values
+// ranked: latencies of 10 us, whatever the logits are.  (Fewer chunks with good
+// values than `width`, as in a first step of one beam, make a second, closer bound
+// of their lanes' best values: 4 beams of 32000 tokens, 64 kept, one beam alive: 24
+// us, against 180 with the chunks one after the other.)
 //
 // Sums of exponentials are fp32, six additions deep in a thread and five between
 // the lanes; the log sum, whose whole powers of two are taken apart, and the
@@ -40,6 +41,7 @@ constexpr int kPer = kBeamChunk / 32;  // values of a lane
 constexpr int kWindow = 2048;          // chunks that are looked at together
 constexpr int kPicked = 512;           // chunks that are read again, at a time
 constexpr int kCands = 1024;           // candidates, at a time
+constexpr int kFewCands = 256;         // candidates that are soon put in order
 static_assert(kMaxWidth + kBeamChunk <= kCands && kWindow % kPicked == 0, "a chunk's values fit beside those that stay");
 
 // Order of floats as unsigned numbers, +0 and -0 as one; 0 is below all.
@@ -131,6 +133,7 @@ struct Shared {
   float about[kWindow];    // the chunks' best scores in fp32, of the first window
   uint32_t bound[2 * kWarps];
   int reach[2 * kWarps];
+  uint32_t turned[kWarps * 33];
   float picked_score[kPicked];
   int picked[kPicked], order[kPicked];
   uint32_t far;
@@ -139,12 +142,17 @@ struct Shared {
 
 // A value that k of the threads' keys at least reach, and few more; 0 where fewer
 // than k are above 0.  Of the two keys of each warp about the (k / kWarps)-th
-// largest, the largest one that k reach.
+// largest, the largest one that k reach; the keys of neighbouring threads, which
+// are chunks of one beam, go to different warps first, so that it is a good one
+// where one beam has all of the best chunks.
 __device__ __forceinline__ uint32_t reached_by(uint32_t key, int k, Shared& s) {
   const unsigned full = 0xffffffffu;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   static_assert(kWarps == 16, "two bounds of a warp are a lane's each");
   if (threadIdx.x < 2 * kWarps) s.reach[threadIdx.x] = 0;
+  s.turned[warp * 33 + lane] = key;
+  __syncthreads();
+  key = s.turned[lane / 2 * 33 + (lane & 1) * 16 + warp];
   uint32_t left = key, top = 0;
 #pragma unroll 1
   for (int j = (k + kWarps - 1) / kWarps; j >= 0; --j) {
@@ -239,10 +247,11 @@ __device__ __forceinline__ void choose(const BeamParams& p, int64_t seq) {
   // ---- the chunks' best scores, in fp32: off by less than 2^-23 of the largest
   // base and the score itself
   auto score_of = [&](int b, float x) { return ordered64(s.base[b] + static_cast<double>(x)); };
-  auto about = [&](int i) -> float {  // -infinity: no candidates
-    const double base = s.base[i / C];
-    const float x = __ldcg(&chunks[i].x);
+  auto about_of = [](double base, float x) {  // -infinity: no candidate
     return base > -INFINITY && x > -INFINITY ? fminf(fmaxf(static_cast<float>(base) + x, -FLT_MAX), FLT_MAX) : -INFINITY;
+  };
+  auto about = [&](int i) {
+    return about_of(s.base[i / C], __ldcg(&chunks[i].x));
   };
   if (tid < p.beams && s.base[tid] > -INFINITY) atomicMax(&s.far, __float_as_uint(fabsf(static_cast<float>(s.base[tid]))));
   float best = -INFINITY;
@@ -317,16 +326,33 @@ __device__ __forceinline__ void choose(const BeamParams& p, int64_t seq) {
       least = less(from - static_cast<float>(s.base[b]));
       if (!(least > -INFINITY && least < INFINITY)) least = -FLT_MAX;  // (also where fp32 ends)
     };
-    // to the candidates with their places and, for the time being, values
+    // to the candidates with their places and, for the time being, values; returns
+    // whether there was room
     auto add = [&] {
+      uint32_t on = 0;
+#pragma unroll
+      for (int k = 0; k < kPer; ++k) on |= (x[k] >= least ? 1u : 0u) << k;
+      const int mine = __popc(on);
+      if (!__any_sync(full, mine > 0)) return true;
+      int upto = mine;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(full, upto, o);
+        if (lane >= o) upto += y;
+      }
+      int first = 0;
+      if (lane == 31) first = atomicAdd(&s.n_cand, upto);
+      first = __shfl_sync(full, first, 31);
+      if (first + __shfl_sync(full, upto, 31) > kCands) return false;
+      Candidate* to = s.cand + first + upto - mine;
 #pragma unroll
       for (int k = 0; k < kPer; ++k) {
-        if (!(x[k] >= least)) continue;
-        const int to = atomicAdd(&s.n_cand, 1);
-        if (to >= kCands) continue;
-        s.cand[to].place = static_cast<uint64_t>(b) << 32 | static_cast<uint32_t>(Units::place(c, k) - lead);
-        s.cand[to].score = __float_as_uint(x[k]);
+        if (!(on >> k & 1)) continue;
+        to->place = static_cast<uint64_t>(b) << 32 | static_cast<uint32_t>(Units::place(c, k) - lead);
+        to->score = __float_as_uint(x[k]);
+        ++to;
       }
+      return true;
     };
     auto score = [&](int n1) {  // of the candidates from n on
       for (int j = n + tid; j < n1; j += kThreads)
@@ -343,38 +369,71 @@ __device__ __forceinline__ void choose(const BeamParams& p, int64_t seq) {
       }
       __syncthreads();
     };
-    // Few: the warps go through them on their own.
-    bool done = n_picked <= 8 * kWarps;
-    if (done) {
+    // Few: the warps go through them on their own.  Many, or with many candidates
+    // (fewer chunks than `width` have the best ones): again, from a closer bound, of
+    // the lanes' best ones.  If it does not help (values that are alike): the best
+    // chunks one at a time, one, two, four and so on, until few are left that may
+    // have candidates.
+    int left = n_picked, alone = 1;
+    bool close = false;
 #pragma unroll 1
-      for (int r = warp; r < n_picked; r += kWarps) {
-        look(r);
-        add();
-      }
-      __syncthreads();
-      const int n1 = s.n_cand;
-      __syncthreads();
-      done = n1 <= kCands;
-      if (done) score(n1);
-      else if (tid == 0) s.n_cand = n;
-    }
-    if (done && n > p.width) {
-      if (i0 + step < n_all) shorten();
-    } else if (!done) {
-      // Many, or with many candidates (values that rise, or are alike): one at a time.
+    while (left > 0) {
+      if (left <= 8 * kWarps || close) {
 #pragma unroll 1
-      for (int r = 0; r < n_picked; ++r) {
-        __syncthreads();
-        const int at = s.order[r];
-        if (s.picked_score[at] < from || worse(s.picked[at])) break;  // the others are, too
-        if (warp == 0) {
+        for (int r = warp; r < left; r += kWarps) {
           look(r);
-          add();
+          if (!add()) break;
         }
         __syncthreads();
-        score(s.n_cand);
-        if (n > p.width) shorten();
+        const int n1 = s.n_cand;
+        __syncthreads();
+        if (n1 <= (close ? kCands : kFewCands)) {
+          score(n1);
+          if (n > p.width && i0 + step < n_all) shorten();
+          break;
+        }
+        if (tid == 0) s.n_cand = n;
       }
+      int batch = 0;
+      if (!close) {
+        close = true;
+        float mine = -INFINITY;
+#pragma unroll 1
+        for (int r = warp; r < left; r += kWarps) {
+          look(r);
+          mine = fmaxf(mine, about_of(s.base[b], largest(x)));
+        }
+        const uint32_t bound = reached_by(mine > -INFINITY ? ordered(mine) : 0, p.width, s);
+        if (bound) from = fmaxf(from, less(from_ordered(bound)));
+      } else {
+        batch = min(alone, left);
+        alone *= 2;
+#pragma unroll 1
+        for (int r = 0; r < batch; ++r) {
+          __syncthreads();
+          if (warp == 0) {
+            look(r);
+            add();
+          }
+          __syncthreads();
+          score(s.n_cand);
+          if (n > p.width) shorten();
+        }
+      }
+      // the others that are not worse, in their order
+      __syncthreads();
+      int at = -1;
+      if (tid >= batch && tid < left) {
+        at = s.order[tid];
+        if (s.picked_score[at] < from || worse(s.picked[at])) at = -1;
+      }
+      const unsigned on = __ballot_sync(full, at >= 0);
+      if (lane == 0) s.reach[warp] = __popc(on);
+      __syncthreads();
+      const int of_warp = lane < kWarps ? s.reach[lane] : 0, before = __reduce_add_sync(full, lane < warp ? of_warp : 0);
+      if (at >= 0) s.order[before + __popc(on & ((1u << lane) - 1))] = at;
+      left = __reduce_add_sync(full, of_warp);
+      __syncthreads();
     }
   }
   n = cut(p.width, n, s);
@@ -451,6 +510,12 @@ template <typename T>
 cudaError_t launch(const BeamParams& p, int dev, int sms, cudaStream_t s) {
   constexpr int kBytes = static_cast<int>(sizeof(Shared));
   const int64_t per_seq = static_cast<int64_t>(p.beams) * p.n_chunks, blocks = (per_seq + kWarps - 1) / kWarps;
+  // Few chunks are summed up all at once, and the block that has a sequence's last
+  // one goes on with the choice: a launch fewer (2 x 8 beams of 128000 tokens, fp16,
+  // 250 blocks: a call 14.5 us, 16.7 with two kernels).  More: the choice is a
+  // kernel of its own, and its registers and shared memory do not hold up the sums
+  // (500 blocks: 14.9 us on the device against 11.2, and calls alike; 64 x 8 beams of
+  // 128000 tokens in bf16: 82.7 against 48.2).
   if (blocks * p.n_seqs <= 2 * static_cast<int64_t>(sms)) {
     static std::atomic<uint64_t> set;
     const cudaError_t e = allow_shared_memory(set, dev, beam_kernel<T>, kBytes);

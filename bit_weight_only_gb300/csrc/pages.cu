@@ -229,7 +229,7 @@ __global__ void __launch_bounds__(kRowThreads) release_kernel(const PoolParams p
 __device__ __forceinline__ int64_t pool_tiles(int64_t n_pages) { return (n_pages + kPoolTile - 1) / kPoolTile; }
 
 constexpr int kTilePer = kPoolTile / kRowThreads;  // counts of a thread
-constexpr int kFewTiles = 16;
+constexpr int kFewTiles = 8;
 
 // The moves: with U pages in use, the j-th one from number U on goes to the
 // j-th free one below.  map[page] = j for a page that moves, else -1.  `used`: U;
@@ -467,6 +467,9 @@ cudaError_t launch_pool_release(const PoolParams& p, cudaStream_t s) {
 cudaError_t launch_pool_compact(const PoolParams& p, cudaStream_t s) {
   const unsigned tiles = static_cast<unsigned>((p.n_pages + kPoolTile - 1) / kPoolTile);
   cudaError_t e;
+  // Few pages: one kernel finds the moves (16000 pages: 7.5 us on the device, 8.1
+  // with two; a call 14.4 against 17.7; 32768 pages 9.5 against 8.6, a call 13.7
+  // against 16.8).  More: counts and moves apart (65536 pages: 8.8 us, 13.5 in one).
   if (tiles <= kFewTiles) {
     compact_few_kernel<<<tiles, kRowThreads, 0, s>>>(p);
     e = cudaGetLastError();
@@ -486,9 +489,11 @@ cudaError_t launch_copy_pages(const CopyPagesParams& p, cudaStream_t s) {
   const cudaError_t found = current_device(&dev, &sms);
   if (found != cudaSuccess) return found;
   // Pages in part, as a fork has them, with pairs that are none between: gathered
-  // (128 beams, 57 pages of 1 MB in part: 11.9 us against 14.2), but for chunks
+  // (128 beams, 57 pages of 1 MB in part: 10.1 us against 14.4), but for chunks
   // that run all at once.  Whole pages, as a packing has them, one behind the
-  // other: as they come (2200 of 9001 Q4_0 pages of 74 kB: 55 us against 67).
+  // other: as they come (2200 of 9001 Q4_0 pages of 74 kB: 58 us, 5.6 TB/s, against
+  // 63).  Six blocks an SM, with 16 kB of loads in flight
+  // each; a block for every chunk takes 74 us for the second.
   const int64_t items = p.n * ((p.page_bytes + kCopyBytes - 1) / kCopyBytes), most = kCopyBlocks * static_cast<int64_t>(sms);
   const unsigned grid = static_cast<unsigned>(items < most ? items : most);
   if (items <= most || !p.tokens) copy_all_kernel<<<grid, kCopyThreads, 0, s>>>(p);

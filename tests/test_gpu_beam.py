@@ -1,10 +1,11 @@
 """GPU tests of beam search's choice (qgemv_beam_select).
 
 Candidates of one beam are in the order of their logits, exactly, with ties to the lower token.  Scores of different beams are
-compared as sums in 64 bits that hold the beams' log sums, which are fp32 sums of exponentials: a thread adds at most 17 values a
-tile of 4096 (a rounding of 2^-24 each) and the rest of the block's and the parts' joins add fewer than 60; exponentials and
-rescalings are off by 2^-21 each, generously, twice nested.  So a log sum is off by at most (17 tiles + 60) 2^-24 + 2^-20; a score's rounding adds 2^-24 of
-it.
+compared as sums in 64 bits that hold the beams' log sums, which are fp32 sums of exponentials.  Chunks of 512 values: a lane adds
+16 of them and lanes are joined five times, fewer than 17 roundings of 2^-24 a chunk; a lane of the beam's warp adds every 32nd
+chunk, with a rescaling every eighth one, and five joins follow.  ``off_of`` allows 17 for every 4096 values and 60 more, which is
+not less for any vocabulary; exponentials and rescalings are off by 2^-21 each, generously, twice nested: 2^-20.  So a log sum is
+off by at most (17 (vocab / 4096 + 2) + 60) 2^-24 + 2^-20; a score's rounding adds 2^-24 of it.
 """
 import numpy as np
 import pytest
@@ -208,6 +209,29 @@ def test_scores_at_the_ends_of_fp32(size):
     y[0, 7] = 3.2e38
     out, parents, tokens = select(y[:1], torch.tensor([[size]], device="cuda"), 2)
     assert tokens[0, 0] == 7 and bool((parents == 0).all())
+
+
+@pytest.mark.parametrize("n, beams, vocab, width", [(16, 4, 32000, 8), (3, 8, 128000, 16), (2, 32, 32000, 64), (5, 3, 1500, 64),
+                                                    (2, 64, 4096, 33)])
+@pytest.mark.parametrize("kind", ["f32", "f16"])
+def test_beams_far_apart(kind, n, beams, vocab, width):
+    """One beam far ahead of the others, as scores drift apart, or the only one, as in a first step: all of the result, or all
+    of a beam's values, come from it."""
+    x = draw(width, n * beams, vocab, kind, 1.0)
+    for gap in (2.0, 5.0, 40.0, float("inf")):
+        s = beams_of(width, n, beams) - gap
+        s[torch.arange(n), (torch.arange(n) * 7 + beams - 1) % beams] = -0.25
+        check(x, s, width, select(x, s, width))
+
+
+@pytest.mark.parametrize("width", [1, 8, 64])
+@pytest.mark.parametrize("vocab", [20000, 400000])
+def test_scores_that_fp32_cannot_tell_apart(width, vocab):
+    """Far scores: many chunks' best candidates are alike in fp32 and in no order, and not in 64 bits."""
+    g = torch.Generator(device="cuda").manual_seed(width)
+    x = 1 + torch.stack([torch.randperm(vocab, generator=g, device="cuda") for _ in range(2)]).float() * 2.0 ** -23
+    s = torch.tensor([[-1000.0], [-70000.0]], device="cuda")
+    check(x, s, width, select(x, s, width))
 
 
 def test_rows_past_32_bits():
