@@ -11,13 +11,16 @@
 //
 // Bytes bound it, as the cache write (kv_cache.cu), whose layout it takes: a
 // lane for eight neighbouring values, a warp for eight rows of one token, all of
-// them queries, keys or values.  A block works out the angles of its eight
-// warps' tokens once, while their rows are on their way, and keeps cosines and
-// sines in shared memory; with an angle for each lane's values in every warp the
+// them queries, keys or values.  A block works out the angles of its four warps'
+// tokens once, while their rows are on their way, and keeps cosines and sines in
+// shared memory; with an angle for each lane's values in every warp the
 // instructions were the bound (27003 tokens of 32 + 32 + 32 heads, bf16 into an
-// fp16 cache: 408 us with the cache read again, 310 so, the kernel 198 of them at
-// 6.7 TB/s).  Four blocks an SM have enough loads in flight.  A single token is one
-// launch's latency, 3 us.
+// fp16 cache, and the cache read again: 408 us; so 293, of which the rotation is
+// 179, 7.4 TB/s with what L2 keeps).  Blocks of four warps wait for one another
+// less than those of eight (198 us) and of sixteen (208).  fp32 rows take more
+// registers and instructions a byte (2700 tokens of 80 heads into INT8: 29 us, 5.5
+// TB/s; with loads of 32 bytes no faster, nor with half the rows for a warp).  A
+// single token is one launch's latency, 3 us.
 #include <type_traits>
 
 #include "kv_codes.cuh"
@@ -26,7 +29,7 @@
 namespace qgemv {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;
 constexpr int kWarps = kThreads / 32;  // and tokens of a block, at most
 constexpr int kWarpRows = 8;
 
@@ -40,15 +43,17 @@ __device__ __forceinline__ void lds_here(const float4* p, float* x) {
 
 enum { kNone, kWhole, kAny, kNext };
 
-// FMT 0: rows only, no cache.
+// FMT 0: rows only, no cache.  Blocks on an SM: the most whose registers hold a
+// warp's rows (fp32: 29.3 us for the tokens above with seven, 30.6 with eight, 34.2
+// with nine; 16 bits: 179 with nine, 187 with eight).
 template <int FMT, int D, typename T>
-__global__ void __launch_bounds__(kThreads, 4) rope_kernel(const RopeParams p) {
+__global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 7 : 9) rope_kernel(const RopeParams p) {
   constexpr int kLanes = D / 8, kAt = 32 / kLanes;  // kAt rows at a time
   constexpr int kPasses = kWarpRows / kAt;
   // Cosines and sines of a token's D / 2 pairs, as quads of pairs 4 i .. 4 i + 3:
   // the even quads first, so that neighbouring lanes, two quads each, read
   // neighbouring ones.
-  __shared__ float4 s_cos[kWarps][D / 8], s_sin[kWarps][D / 8];
+  __shared__ float4 s_cos[kWarps][D / 8], s_sin[2][kWarps][D / 8];  // (sines, and their opposites)
   __shared__ float s_row[kWarps][kAt][D];
   const unsigned full = 0xffffffffu;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, n = p.pairs;
@@ -92,14 +97,20 @@ __global__ void __launch_bounds__(kThreads, 4) rope_kernel(const RopeParams p) {
     float c = 1.f, s = 0.f;
     if (j < n) {
       const uint4 e = __ldg(p.plan + j);
-      const int x = e.z < static_cast<unsigned>(p.n_axes) ? __ldg(p.positions + (t0 + t) * p.n_axes + e.z) : 0;
+      int x = 0;
+#pragma unroll
+      for (int a = 0; a < 4; ++a) {  // all of them, with nothing to wait for
+        const int at = a < p.n_axes ? __ldg(p.positions + (t0 + t) * p.n_axes + a) : 0;
+        if (e.z == a) x = at;
+      }
       const uint64_t turns = static_cast<uint64_t>(e.y) << 32 | e.x;
       const uint64_t turn = turns * static_cast<uint64_t>(static_cast<int64_t>(x));
       sincospif(static_cast<float>(static_cast<int32_t>(turn >> 32)) * 0x1p-31f, &s, &c);
     }
     const int quad = ((j >> 2) & 1) * (D / 16) + (j >> 3);
     reinterpret_cast<float*>(&s_cos[t][quad])[j & 3] = c;
-    reinterpret_cast<float*>(&s_sin[t][quad])[j & 3] = s;
+    reinterpret_cast<float*>(&s_sin[0][t][quad])[j & 3] = s;
+    reinterpret_cast<float*>(&s_sin[1][t][quad])[j & 3] = -s;
   }
   __syncthreads();
   if (!on) return;
@@ -131,42 +142,47 @@ __global__ void __launch_bounds__(kThreads, 4) rope_kernel(const RopeParams p) {
 #pragma unroll
           for (int e = 0; e < 8; ++e) y[e] = d0 + e < 2 * n ? here[d0 + e < n ? d0 + e + n : d0 + e - n] : 0.f;
         }
-        // y = x c + other s, with -s for the first of a pair: read for each pass (held
-        // for all of them they would take a quarter of the registers)
-        float c[8], s[8];
-        auto quad = [&](int q, float* cc, float* ss) {
-          lds_here(&s_cos[mine][(q & 1) * (D / 16) + (q >> 1)], cc);
-          lds_here(&s_sin[mine][(q & 1) * (D / 16) + (q >> 1)], ss);
+        // x = x c + y s, with -s for the first of a pair: read for each pass (held for
+        // all of them they would take a quarter of the registers)
+        auto turn = [&](int e, float c0, float c1, float s0, float s1, float& u, float& v) {
+          unpack2(fma2(pack2(x[e], x[e + 1]), pack2(c0, c1), mul2(pack2(y[e], y[e + 1]), pack2(s0, s1))), u, v);
         };
         if constexpr (kHow == kNext) {
-          float cc[4], ss[4];
-          quad(d0 / 8, cc, ss);
+          float c[4], s[4];
+          const int q = d0 / 8, at = (q & 1) * (D / 16) + (q >> 1);
+          lds_here(&s_cos[mine][at], c);
+          lds_here(&s_sin[0][mine][at], s);
 #pragma unroll
-          for (int e = 0; e < 8; ++e) c[e] = cc[e / 2], s[e] = e & 1 ? ss[e / 2] : -ss[e / 2];
+          for (int e = 0; e < 8; e += 2) {
+            float u, v;
+            turn(e, c[e / 2], c[e / 2], -s[e / 2], s[e / 2], u, v);
+            if (d0 + e < 2 * n) x[e] = u, x[e + 1] = v;
+          }
         } else if constexpr (kHow == kWhole) {
-          const int j0 = d0 < n ? d0 : d0 < 2 * n ? d0 - n : 0;
-          quad(j0 / 4, c, s);
-          quad(j0 / 4 + 1, c + 4, s + 4);
-          if (d0 < n) {
+          if (d0 < 2 * n) {  // a lane's eight values are turned or not together
+            const int j0 = d0 < n ? d0 : d0 - n, at = j0 >> 3;
+            float c[8], s[8];
+            lds_here(&s_cos[mine][at], c);
+            lds_here(&s_cos[mine][D / 16 + at], c + 4);
+            lds_here(&s_sin[d0 < n][mine][at], s);
+            lds_here(&s_sin[d0 < n][mine][D / 16 + at], s + 4);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) s[e] = -s[e];
+            for (int e = 0; e < 8; e += 2) turn(e, c[e], c[e + 1], s[e], s[e + 1], x[e], x[e + 1]);
           }
         } else {
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const int i = d0 + e, j = i < n ? i : i < 2 * n ? i - n : 0, q = ((j >> 2) & 1) * (D / 16) + (j >> 3);
-            c[e] = reinterpret_cast<const float*>(&s_cos[mine][q])[j & 3];
-            const float v = reinterpret_cast<const float*>(&s_sin[mine][q])[j & 3];
-            s[e] = i < n ? -v : v;
-          }
-        }
+          for (int e = 0; e < 8; e += 2) {
+            float c[2], s[2], u, v;
 #pragma unroll
-        for (int e = 0; e < 8; e += 2) {
-          float u, v;
-          unpack2(fma2(pack2(x[e], x[e + 1]), pack2(c[e], c[e + 1]), mul2(pack2(y[e], y[e + 1]), pack2(s[e], s[e + 1]))), u, v);
-          // (whole: a lane's eight values are turned or not together)
-          if (kHow == kWhole ? d0 < 2 * n : d0 + e < 2 * n) x[e] = u;
-          if (kHow == kWhole ? d0 < 2 * n : d0 + e + 1 < 2 * n) x[e + 1] = v;
+            for (int o = 0; o < 2; ++o) {
+              const int i = d0 + e + o, j = i < n ? i : i < 2 * n ? i - n : 0, q = ((j >> 2) & 1) * (D / 16) + (j >> 3);
+              c[o] = reinterpret_cast<const float*>(&s_cos[mine][q])[j & 3];
+              s[o] = reinterpret_cast<const float*>(&s_sin[i < n][mine][q])[j & 3];
+            }
+            turn(e, c[0], c[1], s[0], s[1], u, v);
+            if (d0 + e < 2 * n) x[e] = u;
+            if (d0 + e + 1 < 2 * n) x[e + 1] = v;
+          }
         }
       }
       if (kind == 0) {
