@@ -11,7 +11,7 @@
 // block in steps of 16384 counts, as many as are needed, the lowest first; the
 // compacting scan, which needs all counts, is spread over blocks of 4096 each,
 // whose sums every block adds up for itself.  Copies are bytes: a block takes
-// 16 kB of a page with all of its loads in flight.
+// 32 kB of a page with all of its loads in flight.
 #include "pages.h"
 #include "per_device.h"
 #include "kv_layout.cuh"
@@ -348,9 +348,9 @@ __global__ void __launch_bounds__(kRowThreads) compact_apply_kernel(const PoolPa
 
 // ---- copies: a block takes chunks of kCopyBytes of what is to be copied
 constexpr int kCopyThreads = 256;
-constexpr int kCopyUnits = 4;  // 16-byte units of a thread
+constexpr int kCopyUnits = 8;  // 16-byte units of a thread
 constexpr int kCopyBytes = kCopyThreads * kCopyUnits * 16;
-constexpr int kCopyBlocks = 6;     // on an SM
+constexpr int kCopyBlocks = 4;    // on an SM
 constexpr int kCopyWindow = 512;  // pairs that are looked at together
 
 struct CopyPair {
@@ -489,11 +489,11 @@ cudaError_t launch_copy_pages(const CopyPagesParams& p, cudaStream_t s) {
   const cudaError_t found = current_device(&dev, &sms);
   if (found != cudaSuccess) return found;
   // Pages in part, as a fork has them, with pairs that are none between: gathered
-  // (128 beams, 57 pages of 1 MB in part: 10.1 us against 14.4), but for chunks
-  // that run all at once.  Whole pages, as a packing has them, one behind the
-  // other: as they come (2200 of 9001 Q4_0 pages of 74 kB: 58 us, 5.6 TB/s, against
-  // 63).  Six blocks an SM, with 16 kB of loads in flight
-  // each; a block for every chunk takes 74 us for the second.
+  // (128 beams, 57 pages of 1 MB in part: 9.9 us against 12.4), but for chunks that
+  // run all at once.  Whole pages, as a packing has them, one behind the other: as
+  // they come (2200 of 9001 Q4_0 pages of 74 kB: 56 us, 5.8 TB/s read and written,
+  // against 60).  Four blocks an SM, with 32 kB of loads each; of the second's 16 kB
+  // chunks six blocks an SM take 58, a block for each 74.
   const int64_t items = p.n * ((p.page_bytes + kCopyBytes - 1) / kCopyBytes), most = kCopyBlocks * static_cast<int64_t>(sms);
   const unsigned grid = static_cast<unsigned>(items < most ? items : most);
   if (items <= most || !p.tokens) copy_all_kernel<<<grid, kCopyThreads, 0, s>>>(p);
