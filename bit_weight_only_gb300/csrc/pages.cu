@@ -10,12 +10,17 @@
 // latencies, of a launch and a scan, bounds it.  Free pages are found by one
 // block in steps of 16384 counts, as many as are needed, the lowest first; the
 // compacting scan, which needs all counts, is spread over blocks of 4096 each,
-// whose sums every block adds up for itself.  Copies are bytes: a block takes
+// whose sums every block adds up for itself (of few pages, a cluster does all of
+// it).  Copies are bytes: a block takes
 // 32 kB of a page with all of its loads in flight.
+#include <cooperative_groups.h>
+
 #include "pages.h"
 #include "per_device.h"
 #include "kv_layout.cuh"
 #include "tc_common.cuh"
+
+namespace cg = cooperative_groups;
 
 namespace qgemv {
 namespace {
@@ -229,7 +234,8 @@ __global__ void __launch_bounds__(kRowThreads) release_kernel(const PoolParams p
 __device__ __forceinline__ int64_t pool_tiles(int64_t n_pages) { return (n_pages + kPoolTile - 1) / kPoolTile; }
 
 constexpr int kTilePer = kPoolTile / kRowThreads;  // counts of a thread
-constexpr int kFewTiles = 8;
+constexpr int kFewTiles = 4, kFewBlocks = 8;
+constexpr int64_t kFewEntries = 1 << 15;
 
 // The moves: with U pages in use, the j-th one from number U on goes to the
 // j-th free one below.  map[page] = j for a page that moves, else -1.  `used`: U;
@@ -268,11 +274,37 @@ __device__ __forceinline__ uint32_t bits_below(int64_t page0, int used) {
   return n <= 0 ? 0 : n >= kTilePer ? (1u << kTilePer) - 1 : (1u << n) - 1;
 }
 
-// Of few pages every block looks at all of them.
-__global__ void __launch_bounds__(kRowThreads) compact_few_kernel(const PoolParams p) {
+// Tables and counts follow the moves: part `at` of `all`.
+__device__ __forceinline__ void follow_moves(const PoolParams& p, int64_t at, int64_t all) {
+  const int32_t* map = p.scratch + pool_tiles(p.n_pages);
+  const int64_t entries = p.n_seqs * p.table_stride;
+  constexpr int kAt = 4;
+  for (int64_t i0 = at; i0 < entries; i0 += kAt * all) {
+    int32_t page[kAt], j[kAt];
+#pragma unroll
+    for (int k = 0; k < kAt; ++k) page[k] = i0 + k * all < entries ? p.old_table[i0 + k * all] : -1;
+#pragma unroll
+    for (int k = 0; k < kAt; ++k) j[k] = page[k] >= 0 && page[k] < p.n_pages ? map[page[k]] : -1;
+#pragma unroll
+    for (int k = 0; k < kAt; ++k)
+      if (j[k] >= 0) page[k] = p.dst[j[k]];
+#pragma unroll
+    for (int k = 0; k < kAt; ++k)
+      if (i0 + k * all < entries) p.table[i0 + k * all] = page[k];
+  }
+  for (int64_t j = at; j < p.n_moves; j += all) {
+    const int32_t from = p.src[j], to = p.dst[j];
+    if (from < 0) break;
+    p.refs[to] = p.refs[from];
+    p.refs[from] = 0;
+  }
+}
+
+// Of few pages every block of a cluster looks at all of them; the last part is
+// the cluster's, too.
+__global__ void __cluster_dims__(kFewBlocks) __launch_bounds__(kRowThreads) compact_few_kernel(const PoolParams p) {
   __shared__ int s_warp[32], s_tile[32];
   __shared__ unsigned short s_on[kFewTiles][kRowThreads];
-  allow_next_kernel();
   const int tiles = static_cast<int>(pool_tiles(p.n_pages)), me = blockIdx.x, lane = threadIdx.x & 31;
   if (threadIdx.x < 32) s_tile[threadIdx.x] = 0;
   __syncthreads();
@@ -289,10 +321,12 @@ __global__ void __launch_bounds__(kRowThreads) compact_few_kernel(const PoolPara
   int below = edge < tiles ? __popc(s_on[edge][threadIdx.x] & bits_below(static_cast<int64_t>(edge) * kPoolTile + threadIdx.x * kTilePer, used)) : 0;
   block_sum<kRowThreads>(below, s_warp, below);
   below += __reduce_add_sync(0xffffffffu, lane < edge ? s_tile[lane] : 0);
-  const uint32_t on = s_on[me][threadIdx.x];
+  const uint32_t on = me < tiles ? s_on[me][threadIdx.x] : 0;
   int total;
   const int upto = before + block_sum<kRowThreads>(__popc(on), s_warp, total) - __popc(on);
   write_moves(p, static_cast<int64_t>(me) * kPoolTile + threadIdx.x * kTilePer, on, upto, used, below);
+  cg::this_cluster().sync();
+  follow_moves(p, me * kRowThreads + threadIdx.x, kFewBlocks * kRowThreads);
 }
 
 // Pages in use of a tile.
@@ -327,23 +361,9 @@ __global__ void __launch_bounds__(kRowThreads) compact_moves_kernel(const PoolPa
   write_moves(p, page0, on, upto, used, below);
 }
 
-// Tables and counts follow.
 __global__ void __launch_bounds__(kRowThreads) compact_apply_kernel(const PoolParams p) {
   wait_for_last_kernel();
-  const int32_t* map = p.scratch + pool_tiles(p.n_pages);
-  const int64_t at = static_cast<int64_t>(blockIdx.x) * kRowThreads + threadIdx.x, all = static_cast<int64_t>(gridDim.x) * kRowThreads;
-  for (int64_t i = at; i < p.n_seqs * p.table_stride; i += all) {
-    const int64_t b = i / p.table_stride, e = i - b * p.table_stride;
-    const int32_t page = p.old_table[b * p.old_stride + e];
-    const int j = page >= 0 && page < p.n_pages ? map[page] : -1;
-    p.table[i] = j >= 0 ? p.dst[j] : page;
-  }
-  for (int64_t j = at; j < p.n_moves; j += all) {
-    const int32_t from = p.src[j], to = p.dst[j];
-    if (from < 0) break;
-    p.refs[to] = p.refs[from];
-    p.refs[from] = 0;
-  }
+  follow_moves(p, static_cast<int64_t>(blockIdx.x) * kRowThreads + threadIdx.x, static_cast<int64_t>(gridDim.x) * kRowThreads);
 }
 
 // ---- copies: a block takes chunks of kCopyBytes of what is to be copied
@@ -466,20 +486,21 @@ cudaError_t launch_pool_release(const PoolParams& p, cudaStream_t s) {
 
 cudaError_t launch_pool_compact(const PoolParams& p, cudaStream_t s) {
   const unsigned tiles = static_cast<unsigned>((p.n_pages + kPoolTile - 1) / kPoolTile);
-  cudaError_t e;
-  // Few pages: one kernel finds the moves (16000 pages: 7.5 us on the device, 8.1
-  // with two; a call 14.4 against 17.7; 32768 pages 9.5 against 8.6, a call 13.7
-  // against 16.8).  More: counts and moves apart (65536 pages: 8.8 us, 13.5 in one).
-  if (tiles <= kFewTiles) {
-    compact_few_kernel<<<tiles, kRowThreads, 0, s>>>(p);
-    e = cudaGetLastError();
-  } else {
-    compact_count_kernel<<<tiles, kRowThreads, 0, s>>>(p);
-    e = cudaGetLastError();
-    if (e == cudaSuccess) e = launch_after(compact_moves_kernel, tiles, p, s, kRowThreads);
+  const int64_t entries = p.n_seqs * p.table_stride;
+  // Few pages and entries: all of it by a cluster of eight blocks, one launch (9001
+  // pages, 16384 entries: 7.7 us on the device, 8.0 with three kernels; a call 9.9
+  // against 15.7).  More: every tile has its block (32768 pages: 8.6 us, 10.2 in a
+  // cluster), and tables have more than eight (16000 pages, 262144 entries: 9.0
+  // against 20.5).
+  if (tiles <= kFewTiles && entries <= kFewEntries) {
+    compact_few_kernel<<<kFewBlocks, kRowThreads, 0, s>>>(p);
+    return cudaGetLastError();
   }
+  compact_count_kernel<<<tiles, kRowThreads, 0, s>>>(p);
+  cudaError_t e = cudaGetLastError();
+  if (e == cudaSuccess) e = launch_after(compact_moves_kernel, tiles, p, s, kRowThreads);
   if (e != cudaSuccess) return e;
-  const int64_t items = p.n_seqs * p.table_stride > p.n_moves ? p.n_seqs * p.table_stride : p.n_moves;
+  const int64_t items = entries > p.n_moves ? entries : p.n_moves;
   const int64_t blocks = (items + kRowThreads - 1) / kRowThreads;
   return launch_after(compact_apply_kernel, static_cast<unsigned>(blocks < 1 ? 1 : blocks < 1024 ? blocks : 1024), p, s, kRowThreads);
 }

@@ -18,7 +18,7 @@
 // fp16 cache, and the cache read again: 408 us; so 293, of which the rotation is
 // 179, 7.4 TB/s with what L2 keeps).  Blocks of four warps wait for one another
 // less than those of eight (198 us) and of sixteen (208).  fp32 rows take more
-// registers and instructions a byte (2700 tokens of 80 heads into INT8: 29 us, 5.5
+// registers and instructions a byte (2674 tokens of 80 heads into INT8: 29 us, 5.5
 // TB/s; with loads of 32 bytes no faster, nor with half the rows for a warp).  A
 // single token is one launch's latency, 3 us.
 #include <type_traits>

@@ -179,6 +179,25 @@ def test_most_rows():
         pool.reserve(torch.full((rows + 1, 1), -1, dtype=torch.int32, device="cuda"), i32([0] * (rows + 1)), i32([1] * (rows + 1)))
 
 
+@pytest.mark.parametrize("rows, width", [(1, 1), (3, 700), (64, 512), (64, 513), (2, 70001)])
+@pytest.mark.parametrize("n_pages", [1, 2, 4095, 4097, 16384, 16385])
+def test_packing_of_pools_and_tables_of_any_size(n_pages, rows, width):
+    """Counts of no, some and all pages, tables that name pages in any order and more than once, in place and not."""
+    g = np.random.default_rng(n_pages + width)
+    for used in (0.0, 0.02, 0.6, 1.0):
+        pool, plain = qgemv.PagePool(n_pages, 16), Plain(n_pages, 16)
+        refs = (g.random(n_pages) < used) * g.integers(1, 5, n_pages)
+        plain.refs = refs.tolist()
+        pool.refs.copy_(i32(plain.refs))
+        table = g.integers(-1, n_pages, (rows, width)).tolist()
+        dev = i32(table)
+        want, src, dst = plain.compact(table)
+        new, s, d = pool.compact(dev, out=dev if used == 0.6 else None)
+        assert new.tolist() == want and s[:len(src)].tolist() == src and d[:len(dst)].tolist() == dst
+        assert bool((s[len(src):] == -1).all()) and bool((d[len(dst):] == -1).all())
+        same(pool, plain)
+
+
 def test_tables_with_numbers_that_are_no_pages():
     """Entries outside the pool are passed over, and nothing outside the counts is touched."""
     bad = [[-7, 3, 1 << 30], [2, -2147483648, 99], [2147483647, 3, 5]]
