@@ -274,29 +274,42 @@ __device__ __forceinline__ uint32_t bits_below(int64_t page0, int used) {
   return n <= 0 ? 0 : n >= kTilePer ? (1u << kTilePer) - 1 : (1u << n) - 1;
 }
 
-// Tables and counts follow the moves: part `at` of `all`.
-__device__ __forceinline__ void follow_moves(const PoolParams& p, int64_t at, int64_t all) {
-  const int32_t* map = p.scratch + pool_tiles(p.n_pages);
-  const int64_t entries = p.n_seqs * p.table_stride;
-  constexpr int kAt = 4;
-  for (int64_t i0 = at; i0 < entries; i0 += kAt * all) {
-    int32_t page[kAt], j[kAt];
+// Entries of the tables, kAt of a thread, `all` apart.
+struct Entries {
+  static constexpr int kAt = 4;
+  int32_t page[kAt];
+  __device__ void load(const PoolParams& p, int64_t i0, int64_t all) {
 #pragma unroll
-    for (int k = 0; k < kAt; ++k) page[k] = i0 + k * all < entries ? p.old_table[i0 + k * all] : -1;
-#pragma unroll
-    for (int k = 0; k < kAt; ++k) j[k] = page[k] >= 0 && page[k] < p.n_pages ? map[page[k]] : -1;
-#pragma unroll
-    for (int k = 0; k < kAt; ++k)
-      if (j[k] >= 0) page[k] = p.dst[j[k]];
-#pragma unroll
-    for (int k = 0; k < kAt; ++k)
-      if (i0 + k * all < entries) p.table[i0 + k * all] = page[k];
+    for (int k = 0; k < kAt; ++k) page[k] = i0 + k * all < p.n_seqs * p.table_stride ? p.old_table[i0 + k * all] : -1;
   }
-  for (int64_t j = at; j < p.n_moves; j += all) {
-    const int32_t from = p.src[j], to = p.dst[j];
-    if (from < 0) break;
-    p.refs[to] = p.refs[from];
-    p.refs[from] = 0;
+};
+
+// Tables and counts follow the moves: part `at` of `all`, kAt entries and moves at
+// a time, each step's reads together; `now` has the first entries.
+__device__ __forceinline__ void follow_moves(const PoolParams& p, int64_t at, int64_t all, Entries& now) {
+  const int32_t* map = p.scratch + pool_tiles(p.n_pages);
+  const int64_t entries = p.n_seqs * p.table_stride, items = max(entries, p.n_moves);
+  constexpr int kAt = Entries::kAt;
+  for (int64_t i0 = at; i0 < items; i0 += kAt * all) {
+    if (i0 != at) now.load(p, i0, all);
+    int32_t j[kAt], from[kAt], to[kAt], refs[kAt];
+#pragma unroll
+    for (int k = 0; k < kAt; ++k) {
+      const int64_t i = i0 + k * all;
+      from[k] = i < p.n_moves ? p.src[i] : -1;
+      to[k] = i < p.n_moves ? p.dst[i] : -1;
+      j[k] = now.page[k] >= 0 && now.page[k] < p.n_pages ? map[now.page[k]] : -1;
+    }
+#pragma unroll
+    for (int k = 0; k < kAt; ++k) {
+      refs[k] = from[k] >= 0 ? p.refs[from[k]] : 0;
+      if (j[k] >= 0) now.page[k] = p.dst[j[k]];
+    }
+#pragma unroll
+    for (int k = 0; k < kAt; ++k) {
+      if (i0 + k * all < entries) p.table[i0 + k * all] = now.page[k];
+      if (from[k] >= 0) p.refs[to[k]] = refs[k], p.refs[from[k]] = 0;
+    }
   }
 }
 
@@ -306,6 +319,8 @@ __global__ void __cluster_dims__(kFewBlocks) __launch_bounds__(kRowThreads) comp
   __shared__ int s_warp[32], s_tile[32];
   __shared__ unsigned short s_on[kFewTiles][kRowThreads];
   const int tiles = static_cast<int>(pool_tiles(p.n_pages)), me = blockIdx.x, lane = threadIdx.x & 31;
+  Entries first;
+  first.load(p, me * kRowThreads + threadIdx.x, kFewBlocks * kRowThreads);
   if (threadIdx.x < 32) s_tile[threadIdx.x] = 0;
   __syncthreads();
 #pragma unroll 2
@@ -326,7 +341,7 @@ __global__ void __cluster_dims__(kFewBlocks) __launch_bounds__(kRowThreads) comp
   const int upto = before + block_sum<kRowThreads>(__popc(on), s_warp, total) - __popc(on);
   write_moves(p, static_cast<int64_t>(me) * kPoolTile + threadIdx.x * kTilePer, on, upto, used, below);
   cg::this_cluster().sync();
-  follow_moves(p, me * kRowThreads + threadIdx.x, kFewBlocks * kRowThreads);
+  follow_moves(p, me * kRowThreads + threadIdx.x, kFewBlocks * kRowThreads, first);
 }
 
 // Pages in use of a tile.
@@ -362,8 +377,11 @@ __global__ void __launch_bounds__(kRowThreads) compact_moves_kernel(const PoolPa
 }
 
 __global__ void __launch_bounds__(kRowThreads) compact_apply_kernel(const PoolParams p) {
+  const int64_t at = static_cast<int64_t>(blockIdx.x) * kRowThreads + threadIdx.x, all = static_cast<int64_t>(gridDim.x) * kRowThreads;
+  Entries first;
+  first.load(p, at, all);  // (nothing before in this call writes them)
   wait_for_last_kernel();
-  follow_moves(p, static_cast<int64_t>(blockIdx.x) * kRowThreads + threadIdx.x, static_cast<int64_t>(gridDim.x) * kRowThreads);
+  follow_moves(p, at, all, first);
 }
 
 // ---- copies: a block takes chunks of kCopyBytes of what is to be copied
@@ -488,10 +506,10 @@ cudaError_t launch_pool_compact(const PoolParams& p, cudaStream_t s) {
   const unsigned tiles = static_cast<unsigned>((p.n_pages + kPoolTile - 1) / kPoolTile);
   const int64_t entries = p.n_seqs * p.table_stride;
   // Few pages and entries: all of it by a cluster of eight blocks, one launch (9001
-  // pages, 16384 entries: 7.7 us on the device, 8.0 with three kernels; a call 9.9
-  // against 15.7).  More: every tile has its block (32768 pages: 8.6 us, 10.2 in a
-  // cluster), and tables have more than eight (16000 pages, 262144 entries: 9.0
-  // against 20.5).
+  // pages, 16384 entries: 7.7 us on the device as with three kernels, a call 11.5
+  // against 18.1; 200 pages, 4096 entries 4.6 against 6.8).  More: every tile has its
+  // block (32768 pages: 8.1 us, 10.5 in a cluster), and tables have more than eight
+  // (9001 pages, 262144 entries: 9.6 against 24.4).
   if (tiles <= kFewTiles && entries <= kFewEntries) {
     compact_few_kernel<<<kFewBlocks, kRowThreads, 0, s>>>(p);
     return cudaGetLastError();
