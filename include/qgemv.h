@@ -555,12 +555,12 @@ int qgemv_kv_write_rotated(const qgemv_kv_cache* cache, const void* plan, int pa
  * A beam whose score is not finite (-infinity: not in use), or whose log sum
  * is not (a NaN or +infinity among its logits, or nothing but -infinity), has
  * no candidates, nor have tokens of -infinity; places for which there is no
- * candidate hold (-infinity, -1, -1).  The sums of exponentials are fp32, log sums and scores
- * are compared in 64 bits and rounded once.  beams and width are at most 64,
- * sequences 4096 a call.
- * ws: qgemv_beam_ws_bytes bytes, 16-byte aligned, zeroed once by the caller and then
- * reused by calls of any sizes that it is large enough for; calls that
- * overlap on the GPU need one each.  Asynchronous on `stream`, no allocation,
+ * candidate hold (-infinity, -1, -1).  The sums of exponentials are fp32; log
+ * sums and scores are compared in 64 bits and rounded once.  beams and width
+ * are at most 64, sequences 4096 a call.
+ * ws: qgemv_beam_ws_bytes bytes, 16-byte aligned, zeroed once by the caller
+ * and then reused by calls of any sizes that it is large enough for; calls
+ * that overlap on the GPU need one each.  Asynchronous on `stream`, no allocation,
  * can be captured in a CUDA graph; bitwise reproducible.                     */
 int64_t qgemv_beam_ws_bytes(int64_t n_seqs, int beams, int64_t vocab, int width);
 int qgemv_beam_select(int dtype, const void* logits, int64_t row_stride, int64_t vocab, const float* scores, int64_t n_seqs,
@@ -570,18 +570,18 @@ int qgemv_beam_select(int dtype, const void* logits, int64_t row_stride, int64_t
 /* --------------------------------------------------------- pages of a cache ----
  *
  * A pool's bookkeeping of pages, for any number of caches with the same
- * numbers of pages and tokens (a cache a layer, one page table): refs, device int32
- * [n_pages], counts the rows of page tables that hold a page; pages of count
- * 0 (or less) are free.  state is device int32 [2].  The caller zeroes both
- * once.  Tables are device int32
- * [rows][table_stride], lengths device int32 in tokens; a row of length n
- * holds the pages of its first ceil(n / page_tokens) entries.  Entries that
- * are no page's number are passed over.  Free pages are given out lowest
- * first, in the order of the rows, so results depend on the inputs alone.
- * Where there are none left, the entry becomes -1 and state[0] counts it
- * (state[1] is the calls' own, 0 between them).  At most 4096 rows of 2^20 entries a call; calls of one pool
- * one at a time.  All are asynchronous on `stream`, allocate nothing, can be
- * captured in a CUDA graph.
+ * numbers of pages and tokens (a cache a layer, one page table): refs, device
+ * int32 [n_pages], counts the rows of page tables that hold a page; pages of
+ * count 0 (or less) are free.  state is device int32 [2].  The caller zeroes
+ * both once.  Tables are device int32 [rows][table_stride], lengths device
+ * int32 in tokens; a row of length n holds the pages of its first
+ * ceil(n / page_tokens) entries.  Entries that are no page's number are passed
+ * over.  Free pages are given out lowest first, in the order of the rows, so
+ * results depend on the inputs alone.  Where there are none left, the entry
+ * becomes -1 and state[0] counts it (state[1] is the calls' own, 0 between
+ * them).  At most 4096 rows of 2^20 entries a call; calls of one pool one at a
+ * time.  All are asynchronous on `stream`, allocate nothing, can be captured
+ * in a CUDA graph.
  *
  * reserve: row b, which holds have[b] tokens, gets the pages that need[b]
  * tokens take beyond them.                                                   */

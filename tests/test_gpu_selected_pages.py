@@ -93,6 +93,22 @@ def test_summaries(fmt, page, hkv, d):
 
 
 @pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("page, d", [(16, 128), (64, 64), (128, 128), (256, 64)])
+def test_summaries_of_many_pages(fmt, page, d):
+    """So many that a warp takes a page's head alone, and not a multiple of a block's; a page twice; one with a NaN."""
+    n_pages = 623
+    c, k, _ = cached(fmt, page + d, n_pages, page, 1, d)
+    bad = torch.full((1, 1, d), float("nan"), device="cuda")
+    c.write(bad, bad, torch.tensor([5 * page + page - 1], device="cuda"))
+    k = k.reshape(n_pages, page, 1, d)
+    k[5, -1] = np.nan
+    s = qgemv.KeySummary(c)
+    s.update(torch.cat([torch.randperm(n_pages, device="cuda").int(), i32([3, -1, n_pages])]))
+    q, a = summaries(k)
+    assert np.array_equal(s.codes.cpu().numpy(), q) and np.array_equal(s.scales.cpu().numpy(), a, equal_nan=True)
+
+
+@pytest.mark.parametrize("fmt", FMTS)
 def test_summaries_of_odd_pages(fmt):
     """Zeros, constants, the largest and smallest values, infinities and NaN."""
     page, d = 16, 64
