@@ -15,9 +15,9 @@
 // tokens once, while their rows are on their way, and keeps cosines and sines in
 // shared memory; with an angle for each lane's values in every warp the
 // instructions were the bound (27003 tokens of 32 + 32 + 32 heads, bf16 into an
-// fp16 cache, and the cache read again: 408 us; so 293, of which the rotation is
-// 179, 7.4 TB/s with what L2 keeps).  Blocks of four warps wait for one another
-// less than those of eight (198 us) and of sixteen (208).  fp32 rows take more
+// fp16 cache, and the cache read again: 408 us; so 284, of which the rotation is
+// 168, 7.9 TB/s with what L2 keeps).  Blocks of four warps wait for one another
+// less than those of eight (10% longer) and of sixteen (16%).  fp32 rows take more
 // registers and instructions a byte (2674 tokens of 80 heads into INT8: 29 us, 5.5
 // TB/s; with loads of 32 bytes no faster, nor with half the rows for a warp).  A
 // single token is one launch's latency, 3 us.
@@ -44,10 +44,10 @@ __device__ __forceinline__ void lds_here(const float4* p, float* x) {
 enum { kNone, kWhole, kAny, kNext };
 
 // FMT 0: rows only, no cache.  Blocks on an SM: the most whose registers hold a
-// warp's rows (fp32: 29.3 us for the tokens above with seven, 30.6 with eight, 34.2
-// with nine; 16 bits: 179 with nine, 187 with eight).
+// warp's rows (fp32: 30.1 us for the tokens above with seven, 28.6 with eight, 34.2
+// with nine; 16 bits: 171 with nine, 168 with ten, 181 with eleven).
 template <int FMT, int D, typename T>
-__global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 7 : 9) rope_kernel(const RopeParams p) {
+__global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 8 : 10) rope_kernel(const RopeParams p) {
   constexpr int kLanes = D / 8, kAt = 32 / kLanes;  // kAt rows at a time
   constexpr int kPasses = kWarpRows / kAt;
   // Cosines and sines of a token's D / 2 pairs, as quads of pairs 4 i .. 4 i + 3:
@@ -68,21 +68,9 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 7 : 9) rope_kernel(
   const int d0 = (lane % kLanes) * 8;
   bool on = token < p.n_tokens;
 
-  uint8_t* b0 = nullptr;
-  int at = 0;
-  int64_t step = 0;
-  if constexpr (FMT != 0) {
-    if (on && kind != 0) {
-      const int64_t slot = __ldg(p.slots + token);
-      on = slot >= 0 && slot < p.cache.n_pages * p.cache.page_tokens;
-      if (on) {
-        at = static_cast<int>(slot) & (p.cache.page_tokens - 1);
-        b0 = kv_block<FMT, D>(p.cache, slot >> (31 - __clz(p.cache.page_tokens)), 0, at / kKvBlockTokens);
-        step = static_cast<int64_t>(p.cache.page_tokens / kKvBlockTokens) * KvLayout<FMT, D>::kBlock;
-      }
-    }
-  }
-  Raw<T> raw[kPasses];
+  int64_t slot = 0;
+  if (FMT != 0 && on && kind != 0) slot = __ldg(p.slots + token);
+  Raw<T> raw[kPasses];  // (also of a token without a slot: its rows need not wait)
   if (on) {
     const RowsIn& in = kind == 0 ? p.q : kind == 1 ? p.k : p.v;
     const T* src = static_cast<const T*>(in.ptr) + token * in.token_stride + d0;
@@ -113,6 +101,17 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 7 : 9) rope_kernel(
     reinterpret_cast<float*>(&s_sin[1][t][quad])[j & 3] = -s;
   }
   __syncthreads();
+  uint8_t* b0 = nullptr;
+  int at = 0;
+  int64_t step = 0;
+  if constexpr (FMT != 0) {
+    on = on && slot >= 0 && slot < p.cache.n_pages * p.cache.page_tokens;
+    if (on && kind != 0) {
+      at = static_cast<int>(slot) & (p.cache.page_tokens - 1);
+      b0 = kv_block<FMT, D>(p.cache, slot >> (31 - __clz(p.cache.page_tokens)), 0, at / kKvBlockTokens);
+      step = static_cast<int64_t>(p.cache.page_tokens / kKvBlockTokens) * KvLayout<FMT, D>::kBlock;
+    }
+  }
   if (!on) return;
 
   // ---- the rows, by the way in which a value meets the other one of its pair
