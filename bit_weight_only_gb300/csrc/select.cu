@@ -15,7 +15,9 @@
 // first block's shared memory, which then finds the n_select-th of them by a
 // histogram over their range (and another over its bin, until the bin is taken
 // whole) and writes the pages in order.  One launch, nothing kept in global
-// memory, one synchronisation of the cluster: one token over 8187 pages of 8 heads
+// memory, and two barriers of the cluster: the first block has started before
+// others write to it (they arrive on entry and wait when their first score is due),
+// and has all of the scores before it goes on.  One token over 8187 pages of 8 heads
 // 12.4 us, over 1000 pages 9.0.  (With the scores left in their blocks' shared
 // memory and histograms read across, nine synchronisations: 24 us.)
 #include <cooperative_groups.h>
@@ -171,6 +173,11 @@ __global__ void __launch_bounds__(kSummaryThreads, W > 1 ? 1 : 8) summary_kernel
   if (lane == 0) p.scales[row] = a;
 }
 
+// Another block's shared memory may be touched once that block has started: all
+// arrive first, and wait before they touch it.  (Orders no memory.)
+__device__ __forceinline__ void cluster_started() { asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory"); }
+__device__ __forceinline__ void wait_for_cluster() { asm volatile("barrier.cluster.wait.aligned;" ::: "memory"); }
+
 constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
 constexpr int kBins = 2048;
@@ -197,6 +204,7 @@ __global__ void __launch_bounds__(kThreads, 1) select_kernel(const SelectParams 
   __shared__ int s_n[kWarps], s_eq[kWarps];
   __shared__ int s_digit, s_rest, s_count;
   extern __shared__ uint32_t s_key[];  // the first block's: of every page
+  cluster_started();
   cg::cluster_group cluster = cg::this_cluster();
   const unsigned full = 0xffffffffu;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -277,6 +285,7 @@ __global__ void __launch_bounds__(kThreads, 1) select_kernel(const SelectParams 
   __syncthreads();
 
   // ---- scores
+  wait_for_cluster();
   uint32_t* keys = cluster.map_shared_rank(s_key, 0);
   int4 qc[kUnits];
 #pragma unroll
