@@ -60,56 +60,79 @@ __device__ __forceinline__ double from_ordered64(uint64_t o) {
   return __longlong_as_double(static_cast<long long>(o >> 63 ? o & ~(1ull << 63) : ~o));
 }
 
-// 16-byte loads of a row that may start anywhere: the row's values are those of
-// 16-byte units from the unit that holds the first one.
+// A row's chunks of kBeamChunk tokens from its first one on, wherever the row
+// starts: which lane has which tokens, and so the order of all sums, does not
+// depend on where the row lies (equal rows have equal sums).  Rows that start
+// inside a lane's unit are read by words (64 x 8 of 128001 tokens in bf16 38.7 us,
+// of 128000 36.5; fp32 50.9 and 48.0; by two whole units each, whose words are
+// shifted, bf16 42.4; with the words exchanged between lanes 46).
 template <typename T>
 struct RowUnits {
-  static constexpr int kVec = 16 / sizeof(T), kUnits = kPer / kVec;
-  const uint4* base;  // unit 0 (its first values may lie before the row)
-  int lead, end;      // the row is values [lead, end) from there
-  __device__ RowUnits(const T* row, int n) {
-    const uintptr_t a = reinterpret_cast<uintptr_t>(row);
-    lead = static_cast<int>((a & 15) / sizeof(T));
-    base = reinterpret_cast<const uint4*>(a & ~static_cast<uintptr_t>(15));
-    end = lead + n;
-  }
-  // whether a chunk lies in the row whole
-  __device__ bool inside(int chunk) const { return chunk * kBeamChunk >= lead && (chunk + 1) * kBeamChunk <= end; }
-  // a lane's units of such a chunk
-  __device__ void load(int chunk, uint4 (&w)[kUnits]) const {
-    const uint4* from = base + chunk * (kBeamChunk / kVec) + (threadIdx.x & 31);
+  using Unit = typename std::conditional<sizeof(T) == 4, uint4, uint2>::type;
+  static constexpr int kVec = sizeof(Unit) / sizeof(T), kUnits = kPer / kVec, kWords = sizeof(Unit) / 4;
+  const T* row;
+  int n;
+  __device__ RowUnits(const T* first, int vocab) : row(first), n(vocab) {}
+  // whether a row of 16-bit values starts inside a word
+  __device__ bool odd() const { return sizeof(T) == 2 && (reinterpret_cast<uintptr_t>(row) & 2); }
+  __device__ bool aligned() const { return (reinterpret_cast<uintptr_t>(row) & (sizeof(Unit) - 1)) == 0; }
+  // whether what `load` reads of a chunk lies in the row whole (odd ones: half a word
+  // more at each end)
+  __device__ bool inside(int chunk) const { return (chunk + 1) * kBeamChunk + odd() <= n && chunk >= odd(); }
+  // a lane's values of such a chunk: by units, or by words, of which an odd row takes a
+  // half each
+  __device__ void load(int chunk, float (&x)[kPer]) const {
+    uint32_t w[kUnits][kWords];
+    const int lane = threadIdx.x & 31;
+    if (aligned()) {
+      const Unit* from = reinterpret_cast<const Unit*>(row) + chunk * (kBeamChunk / kVec) + lane;
 #pragma unroll
-    for (int i = 0; i < kUnits; ++i) w[i] = __ldg(from + 32 * i);
-  }
-  // a lane's values of another; what is outside the row is -infinity
-  __device__ void edge(int chunk, float (&x)[kPer]) const {
+      for (int i = 0; i < kUnits; ++i) *reinterpret_cast<Unit*>(w[i]) = __ldg(from + 32 * i);
+    } else {
+      const uint32_t* from = reinterpret_cast<const uint32_t*>(row - odd()) + (chunk * (kBeamChunk / kVec) + lane) * kWords;
+      uint32_t last[kUnits] = {};
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-      const int at = place(chunk, i);
-      x[i] = at >= lead && at < end ? static_cast<float>(reinterpret_cast<const T*>(base)[at]) : -INFINITY;
+      for (int i = 0; i < kUnits; ++i) {
+#pragma unroll
+        for (int k = 0; k < kWords; ++k) w[i][k] = __ldg(from + 32 * kWords * i + k);
+        if (odd()) last[i] = __ldg(from + 32 * kWords * i + kWords);
+      }
+      if (odd()) {
+#pragma unroll
+        for (int i = 0; i < kUnits; ++i) {
+#pragma unroll
+          for (int k = 0; k < kWords; ++k) w[i][k] = __funnelshift_r(w[i][k], k + 1 < kWords ? w[i][(k + 1) % kWords] : last[i], 16);
+        }
+      }
     }
-  }
-  __device__ static int place(int chunk, int i) {
-    return chunk * kBeamChunk + ((i / kVec) * 32 + static_cast<int>(threadIdx.x & 31)) * kVec + i % kVec;
-  }
-  // the token of a lane's value i of a chunk
-  __device__ uint32_t token(int chunk, int i) const {
-    return static_cast<uint32_t>(place(chunk, i) - lead);
-  }
-  __device__ static void values(const uint4 (&w)[kUnits], float (&x)[kPer]) {
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
-      const uint4& v = w[i / kVec];
       if constexpr (std::is_same<T, float>::value) {
-        x[i] = __uint_as_float((&v.x)[i % kVec]);
+        x[i] = __uint_as_float(w[i / kVec][i % kVec]);
       } else {
-        const uint32_t h = (&v.x)[(i % kVec) >> 1];
+        const uint32_t h = w[i / kVec][i % kVec >> 1];
         if constexpr (std::is_same<T, __half>::value)
           x[i] = __half2float(__ushort_as_half(static_cast<unsigned short>(i & 1 ? h >> 16 : h & 0xffffu)));
         else
           x[i] = __uint_as_float(i & 1 ? h & 0xffff0000u : h << 16);
       }
     }
+  }
+  // a lane's values of another; what is outside the row is -infinity
+  __device__ void edge(int chunk, float (&x)[kPer]) const {
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      const int at = place(chunk, i);
+      x[i] = at < n ? static_cast<float>(row[at]) : -INFINITY;
+    }
+  }
+  __device__ void get(int chunk, float (&x)[kPer]) const {
+    if (inside(chunk)) load(chunk, x);
+    else edge(chunk, x);
+  }
+  // the token of a lane's value i of a chunk
+  __device__ static int place(int chunk, int i) {
+    return chunk * kBeamChunk + ((i / kVec) * 32 + static_cast<int>(threadIdx.x & 31)) * kVec + i % kVec;
   }
 };
 
@@ -273,7 +296,7 @@ __device__ __forceinline__ void choose(const BeamParams& p, int64_t seq) {
   // whether no value of chunk i, which reaches `from`, is a candidate
   auto worse = [&](int i) {
     const int b = i / C, c = i - b * C;
-    const uint64_t at = static_cast<uint64_t>(b) << 32 | static_cast<uint32_t>(max(0, c * kBeamChunk - 7));  // its first token, or before
+    const uint64_t at = static_cast<uint64_t>(b) << 32 | static_cast<uint32_t>(c * kBeamChunk);  // its first token
     return filled && better(low, place, score_of(b, __ldcg(&chunks[i].x)), at);
   };
   int step = kWindow;
@@ -310,19 +333,11 @@ __device__ __forceinline__ void choose(const BeamParams& p, int64_t seq) {
     __syncthreads();
     // ---- the r-th chunk of them, by a warp: its values that may be candidates
     float x[kPer], least;  // values below that are worse
-    int b, c, lead;
+    int b, c;
     auto look = [&](int r) {
       const int i = s.picked[s.order[r]];
       b = i / C, c = i - b * C;
-      const Units units(static_cast<const T*>(p.logits) + (seq * p.beams + b) * p.row_stride, static_cast<int>(p.vocab));
-      lead = units.lead;
-      if (units.inside(c)) {
-        uint4 w[Units::kUnits];
-        units.load(c, w);
-        Units::values(w, x);
-      } else {
-        units.edge(c, x);
-      }
+      Units(static_cast<const T*>(p.logits) + (seq * p.beams + b) * p.row_stride, static_cast<int>(p.vocab)).get(c, x);
       least = less(from - static_cast<float>(s.base[b]));
       if (!(least > -INFINITY && least < INFINITY)) least = -FLT_MAX;  // (also where fp32 ends)
     };
@@ -348,7 +363,7 @@ __device__ __forceinline__ void choose(const BeamParams& p, int64_t seq) {
 #pragma unroll
       for (int k = 0; k < kPer; ++k) {
         if (!(on >> k & 1)) continue;
-        to->place = static_cast<uint64_t>(b) << 32 | static_cast<uint32_t>(Units::place(c, k) - lead);
+        to->place = static_cast<uint64_t>(b) << 32 | static_cast<uint32_t>(Units::place(c, k));
         to->score = __float_as_uint(x[k]);
         ++to;
       }
@@ -451,15 +466,8 @@ __device__ __forceinline__ void sum_up(const BeamParams& p, int64_t chunk) {
   using Units = RowUnits<T>;
   const int64_t row = div_small(chunk, p.n_chunks);
   const int c = static_cast<int>(chunk - row * p.n_chunks);
-  const Units units(static_cast<const T*>(p.logits) + row * p.row_stride, static_cast<int>(p.vocab));
   float x[kPer];
-  if (units.inside(c)) {
-    uint4 w[Units::kUnits];
-    units.load(c, w);
-    Units::values(w, x);
-  } else {
-    units.edge(c, x);
-  }
+  Units(static_cast<const T*>(p.logits) + row * p.row_stride, static_cast<int>(p.vocab)).get(c, x);
   const float m = from_ordered(__reduce_max_sync(0xffffffffu, ordered(largest(x)))), ref = m == -INFINITY ? 0.f : m;
   uint64_t sum[2] = {pack2(0.f, 0.f), pack2(0.f, 0.f)};
 #pragma unroll
@@ -490,7 +498,7 @@ __global__ void __launch_bounds__(kThreads) beam_choice_kernel(const BeamParams 
 
 // Both: a sequence's chunks are those of `blocks` blocks.
 template <typename T>
-__global__ void __launch_bounds__(kThreads) beam_kernel(const BeamParams p, int blocks) {
+__global__ void __launch_bounds__(kThreads, 2) beam_kernel(const BeamParams p, int blocks) {
   __shared__ bool s_last;
   const int per_seq = p.beams * p.n_chunks;
   const int64_t seq = blockIdx.x / blocks;

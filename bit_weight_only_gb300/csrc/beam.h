@@ -30,8 +30,7 @@ struct BeamParams {
   int n_chunks;       // of a row
 };
 
-// (a row that starts inside a 16-byte unit is up to 7 values longer)
-inline int64_t beam_chunks(int64_t vocab) { return (vocab + 7 + kBeamChunk - 1) / kBeamChunk; }
+inline int64_t beam_chunks(int64_t vocab) { return (vocab + kBeamChunk - 1) / kBeamChunk; }
 cudaError_t launch_beam(const BeamParams& p, int dtype, cudaStream_t s);
 
 }  // namespace qgemv
