@@ -555,10 +555,11 @@ int qgemv_kv_write_rotated(const qgemv_kv_cache* cache, const void* plan, int pa
  * A beam whose score is not finite (-infinity: not in use), or whose log sum
  * is not (a NaN or +infinity among its logits, or nothing but -infinity), has
  * no candidates, nor have tokens of -infinity; places for which there is no
- * candidate hold (-infinity, -1, -1).  The sums of exponentials are fp32; log
- * sums and scores are compared in 64 bits and rounded once.  Equal rows have
- * equal log sums, wherever they lie: beams of equal scores and rows tie.  beams
- * and width are at most 64, sequences 4096 a call.
+ * candidate hold (-infinity, -1, -1).  The sums of exponentials are fp32, off by
+ * less than 2^-17 of themselves however long a row is; log sums and scores are
+ * compared in 64 bits and rounded once.  Equal rows have equal log sums, wherever
+ * they lie: beams of equal scores and rows tie.  beams and width are at most 64,
+ * sequences 4096 a call.
  * ws: qgemv_beam_ws_bytes bytes, 16-byte aligned, zeroed once by the caller
  * and then reused by calls of any sizes that it is large enough for; calls
  * that overlap on the GPU need one each.  Asynchronous on `stream`, no allocation,
