@@ -6,8 +6,9 @@
 // a 64-bit fixed-point number of turns: turns(j) = round(2^64 freq(j) / 2 pi),
 // and position * turns(j) mod 2^64 is the angle without its whole turns, off by
 // at most |position| 2^-65 -- nothing is lost at far positions, and no 64-bit
-// floating point, which this GPU has little of, is needed.  Its upper 32 bits
-// become a float of at most 1 and sincospif's argument.
+// floating point, which this GPU has little of, is needed.  As a signed number it
+// is rounded once, to a float of at most 1 (half turns), sincospif's argument: small
+// angles keep their 24 bits, and -position gives the opposite angle exactly.
 //
 // Bytes bound it, as the cache write (kv_cache.cu), whose layout it takes: a
 // lane for eight neighbouring values, a warp for eight rows of one token, all of
@@ -93,7 +94,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 8 : 10) rope_kernel
       }
       const uint64_t turns = static_cast<uint64_t>(e.y) << 32 | e.x;
       const uint64_t turn = turns * static_cast<uint64_t>(static_cast<int64_t>(x));
-      sincospif(static_cast<float>(static_cast<int32_t>(turn >> 32)) * 0x1p-31f, &s, &c);
+      sincospif(__ll2float_rn(static_cast<int64_t>(turn)) * 0x1p-63f, &s, &c);
     }
     const int quad = ((j >> 2) & 1) * (D / 16) + (j >> 3);
     reinterpret_cast<float*>(&s_cos[t][quad])[j & 3] = c;
