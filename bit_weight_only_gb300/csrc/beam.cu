@@ -6,9 +6,10 @@
 // One pass over the logits, which are its bytes' floor, leaves two numbers of
 // each chunk of 512: its largest value m and the sum of exp(x - m).  A warp for a
 // chunk, with nothing to wait for but its loads: it takes many warps to have
-// enough bytes on their way (512 rows of 128000 tokens: 65 us with lists of
+// enough bytes on their way (512 rows of 128000 tokens in fp32: 65 us with lists of
 // candidates kept during the pass, 96 with warps that take several chunks; 38 so,
-// 6.9 TB/s in bf16).  Then, by a block for each sequence, the beams' log sums and
+// 6.9 TB/s; in bf16 27, 4.9 TB/s, with as many warps, exponentials and
+// instructions).  Then, by a block for each sequence, the beams' log sums and
 // each chunk's best score are known; the `width`-th largest of its threads' best
 // chunks bounds the result from below, so that only the chunks that reach it,
 // little more than `width`, are read again, the best ones first, and their values
@@ -17,7 +18,9 @@
 // of their lanes' best values: 4 beams of 32000 tokens, 64 kept, one beam alive: 24
 // us, against 180 with the chunks one after the other.)
 //
-// Sums of exponentials are fp32, and no longer chains of roundings for longer rows:
+// Sums of exponentials are fp32, and no longer chains of roundings for longer rows
+// (2^26 tokens in chunks that are alike: off by 2^-20.5, by 2^-14.6 if a lane's
+// chunks were added up one after the other):
 // a chunk's is six additions deep in a lane and five between the lanes, a beam's of
 // its chunks four, a sum whose rounding errors are added up beside it, and five.
 // The log sum, whose whole powers of two are taken apart, and the scores are
@@ -540,10 +543,10 @@ cudaError_t launch(const BeamParams& p, int dev, int sms, cudaStream_t s) {
   const int64_t per_seq = static_cast<int64_t>(p.beams) * p.n_chunks, blocks = (per_seq + kWarps - 1) / kWarps;
   // Few chunks are summed up all at once, and the block that has a sequence's last
   // one goes on with the choice: a launch fewer (2 x 8 beams of 128000 tokens, fp16,
-  // 250 blocks: a call 14.5 us, 16.7 with two kernels).  More: the choice is a
-  // kernel of its own, and its registers and shared memory do not hold up the sums
-  // (500 blocks: 14.9 us on the device against 11.2, and calls alike; 64 x 8 beams of
-  // 128000 tokens in bf16: 82.7 against 48.2).
+  // 250 blocks: a call 13.8 us, 16.7 with two kernels, which take 9.6 on the device
+  // against 10.4).  More: the choice is a kernel of its own, and its registers and
+  // shared memory do not hold up the sums (4 x 8, 500 blocks: 10.4 us on the device,
+  // 12.5 in one kernel; 64 x 8: bf16 36.7 against 77.9, fp32 48.6 against 80.7).
   if (blocks * p.n_seqs <= 2 * static_cast<int64_t>(sms)) {
     static std::atomic<uint64_t> set;
     const cudaError_t e = allow_shared_memory(set, dev, beam_kernel<T>, kBytes);

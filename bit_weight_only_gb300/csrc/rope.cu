@@ -44,9 +44,16 @@ __device__ __forceinline__ void lds_here(const float4* p, float* x) {
 
 enum { kNone, kWhole, kAny, kNext };
 
-// FMT 0: rows only, no cache.  Blocks on an SM: the most whose registers hold a
-// warp's rows (fp32: 30.1 us for the tokens above with seven, 28.6 with eight, 34.2
-// with nine; 16 bits: 171 with nine, 168 with ten, 181 with eleven).
+// FMT 0: rows only, no cache.  Blocks on an SM as measured (fp32: 30.1 us for the
+// tokens above with seven, 28.6 with eight, 34.2 with nine; 16 bits into fp16: 171
+// with nine, 168 with ten, 181 with eleven).  Their 64 and 48 registers hold a warp's
+// rows, but not all that the ways below and the quantisers want; at d = 128 a thread
+// stores and loads of what is spilled (bytes, over all of the kernel's code): 16 bits
+// into INT8 148 and 596, Q4_0 128 and 532, fp16 108 and 248, rows alone 96 and 168;
+// fp32 100 and 312, 104 and 320, 104 and 196, 48 and 60.  For 16 bits into INT8 and
+// Q4_0 nine blocks would be 2% better (27003 tokens of 96 heads in bf16, pairs in
+// halves, with eight, nine and ten: fp16 204, 196, 194 us; INT8 328, 322, 329; Q4_0
+// 521, 501, 513).
 template <int FMT, int D, typename T>
 __global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 8 : 10) rope_kernel(const RopeParams p) {
   constexpr int kLanes = D / 8, kAt = 32 / kLanes;  // kAt rows at a time
@@ -200,7 +207,9 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 8 : 10) rope_kernel
   if (kind == 2) rows(std::integral_constant<int, kNone>());
   else if (p.neighbours) rows(std::integral_constant<int, kNext>());
   // The other value of a pair comes by a shuffle where the pairs are a multiple of
-  // eight (4096 tokens of 32 heads: 11.7 us), else through shared memory (26.8).
+  // eight, else through shared memory, whose banks the stores and the single reads of
+  // cosines meet in (4096 tokens of 32 fp16 heads of 128: 64 pairs 12.4 us, 60 pairs
+  // 37.1; of 64: 32 pairs 8.5, 28 pairs 20.2).
   else if ((n & 7) == 0) rows(std::integral_constant<int, kWhole>());
   else rows(std::integral_constant<int, kAny>());
 }

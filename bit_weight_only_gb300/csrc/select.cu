@@ -510,7 +510,9 @@ cudaError_t launch_select(const SelectParams& p, cudaStream_t s) {
   // Blocks of a cluster: while each has 256 pages at least, and there is an SM for
   // each (us with 1, 2, 4 and 8 of them; 8 heads of one sequence of 512 pages: 10.1,
   // 9.0, 9.0, 8.9; of 8187: 30.8, 20.6, 15.4, 12.4; 32 heads of 1000: 11.8, 10.2,
-  // 9.2, 14.3; 12 sequences of 8 heads of 900: 12.7, 18.4, 20.3, 32.2).
+  // 9.2, 14.3; 12 sequences of 8 heads of 900: 12.7, 18.4, 20.3, 32.2).  The host knows
+  // the table's width and not the contexts' lengths: a table wider than its contexts
+  // takes the blocks and the shared memory of its width.
   const int64_t heads = static_cast<int64_t>(p.n_seqs) * p.cache.kv_heads;
   int cluster = 1;
   while (cluster < kMaxCluster && p.table_stride > 256 * cluster && heads * cluster * 2 <= sms) cluster *= 2;

@@ -762,7 +762,8 @@ class Rotary:
 
     def rotate(self, x, positions, dtype=None, out=None, stream=None):
         """The rows x [n, heads, head_dim] turned to the positions (int32 [n,
-        axes]), of x's type unless dtype is given; out may be x itself."""
+        axes]), of x's type unless dtype is given; out may be x itself, but no
+        other rows that overlap x."""
         n, heads, d = x.shape
         dev = self._dev
         rows = _rows("x", x, heads, self.head_dim, dev)
@@ -1010,7 +1011,8 @@ class PagePool:
 
     def reserve(self, table, have, need, stream=None):
         """Give row b, which holds have[b] tokens, the pages for need[b]; the
-        table's entries are filled in place."""
+        table's entries are filled in place.  (Tokens past the table's width
+        get none, and ``status`` does not tell.)"""
         rows, stride = table.shape
         _call(self._dev, _lib.qgemv_pool_reserve, self.refs.data_ptr(), self.n_pages, self.page_tokens,
               self._ints("table", table, rows, stride), stride, rows, self._ints("have", have, rows),
@@ -1044,8 +1046,9 @@ class PagePool:
     def release(self, table, lens, keep=None, stream=None):
         """Take back the pages of row b's tokens keep[b] .. lens[b] (all of
         them unless keep is given) that no kept token is in; their entries
-        become -1.  (A page that is kept in part is still shared with the rows
-        that hold it.)"""
+        become -1.  A page that is kept in part is still shared with the rows
+        that hold it, and no call makes it the row's alone: a row that goes on
+        from there writes into theirs."""
         rows, stride = table.shape
         _call(self._dev, _lib.qgemv_pool_release, self.refs.data_ptr(), self.n_pages, self.page_tokens,
               self._ints("table", table, rows, stride), stride, rows, self._ints("lens", lens, rows),

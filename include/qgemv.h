@@ -521,7 +521,7 @@ int qgemv_rope_plan(const double* freqs, const int32_t* axes, int pairs, void* p
 /* Rotate the rows x [n_tokens][heads][head_dim] of dtype into out (of
  * out_dtype; x itself, where pointer, strides and types are the same, but no
  * other rows that overlap x).  positions: device int32 [n_tokens][n_axes];
- * a pair of an axis past n_axes is not turned.  head_dim 64 or 128, at most
+ * a pair of an axis past n_axes takes position 0.  head_dim 64 or 128, at most
  * head_dim / 2 pairs.  Asynchronous on `stream`.                             */
 int qgemv_rope_rows(const void* plan, int pairs, int pairing, int n_axes, const int32_t* positions, int dtype, int heads,
                     int head_dim, const void* x, int64_t x_token_stride, int64_t x_head_stride, int64_t n_tokens,
@@ -551,7 +551,8 @@ int qgemv_kv_write_rotated(const qgemv_kv_cache* cache, const void* plan, int pa
  *     elements), of vocab tokens: an LM head's output.
  *   scores: device fp32 [n_seqs][beams], the beams' sums of log
  *     probabilities so far.
- *   out_scores, out_beams, out_tokens: device [n_seqs][width].
+ *   out_scores, out_beams, out_tokens: device [n_seqs][width], apart from the
+ *     inputs and from one another.
  * A beam whose score is not finite (-infinity: not in use), or whose log sum
  * is not (a NaN or +infinity among its logits, or nothing but -infinity), has
  * no candidates, nor have tokens of -infinity; places for which there is no
@@ -586,7 +587,8 @@ int qgemv_beam_select(int dtype, const void* logits, int64_t row_stride, int64_t
  * in a CUDA graph.
  *
  * reserve: row b, which holds have[b] tokens, gets the pages that need[b]
- * tokens take beyond them.                                                   */
+ * tokens take beyond them.  Entries past the table's width are not there: they
+ * are neither filled nor counted as missing.                                 */
 int qgemv_pool_reserve(int32_t* refs, int64_t n_pages, int page_tokens, int32_t* table, int64_t table_stride, int64_t n_seqs,
                        const int32_t* have, const int32_t* need, int32_t* state, void* stream);
 
@@ -607,7 +609,9 @@ int qgemv_pool_fork(int32_t* refs, int64_t n_pages, int page_tokens, const int32
 
 /* release: row b, of lens[b] tokens, keeps the pages of its first keep[b]
  * tokens (none where keep is NULL); the others' counts go down by one and
- * their entries become -1.                                                   */
+ * their entries become -1.  A page that is kept in part stays shared with the
+ * rows that hold it, and no call makes it this row's alone: a row that goes on
+ * from there writes into theirs.                                             */
 int qgemv_pool_release(int32_t* refs, int64_t n_pages, int page_tokens, int32_t* table, int64_t table_stride, int64_t n_seqs,
                        const int32_t* lens, const int32_t* keep, void* stream);
 
